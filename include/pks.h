@@ -413,6 +413,109 @@ pks_status pks_mla_sparse_attention(const pks_mla_args* args, pks_stream stream)
  * Synchronises the stream. */
 pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_stream stream);
 
+/* ------------------------------------------------------------------------
+ * Pages on the device ([PKV] "Paging", "Page sharing", "What this table does
+ * not say").  The host pool above hands pages out; these calls keep the
+ * sharing of a batch's pages on the GPU, so that a decode loop can fork, grow,
+ * truncate and compact its rows without a host round trip (every call is a
+ * few kernel launches and can be captured into a CUDA graph).  The state, one
+ * caller-owned device buffer (256-byte aligned), counts for every physical
+ * page the block-table entries that hold it; a page nobody holds is free.
+ * Layout (int32 unless noted):
+ *   [0..63]                header: num_pages, page_size, n_free (index 2),
+ *                          device error word, moves and grant (index 6) of
+ *                          the last call, magic, n_used of the last
+ *                          compaction (index 7), call counter
+ *   ref[num_pages]         holders of each page
+ *   free_map               bit p of the uint32 words: page p is free
+ *   scratch
+ * Each section starts on a 256-byte boundary; pks_pages_offsets gives ref and
+ * free_map.  Free pages are taken in ascending id order.
+ * ---------------------------------------------------------------------- */
+#define PKS_PAGES_MAX_POOLS 8
+
+/* One paged pool, [num_pages, page_size, token_bytes] bytes (K, V, indexer
+ * keys, latent rows, ...).  data and token_bytes: any alignment; multiples of
+ * 16 move 16 bytes at a time. */
+typedef struct pks_page_pool {
+  void* data;
+  int64_t token_bytes;
+} pks_page_pool;
+
+typedef struct pks_pages_args {
+  int32_t num_pages, page_size;
+  int32_t B, max_pages;     /* rows of the block table, 0..4096 */
+  void* state;              /* device, pks_pages_state_bytes, 256-byte aligned */
+  size_t state_bytes;
+  int32_t* seq_lens;        /* device int32 [B], updated */
+  int32_t* block_table;     /* device int32 [B, max_pages], updated; entries at
+                               p >= ceil(len_b / page_size) are ignored */
+  int32_t n_pools;          /* pools whose rows move with the pages, 0..8 */
+  int32_t reserved;         /* must be 0 */
+  pks_page_pool pools[PKS_PAGES_MAX_POOLS];
+} pks_pages_args;
+
+/* Bytes of the state.  INVALID: num_pages < 1 or more than 2^24, bytes NULL. */
+pks_status pks_pages_state_bytes(int32_t num_pages, size_t* bytes);
+
+/* Byte offsets of ref and free_map inside the state (nullable outputs). */
+pks_status pks_pages_offsets(int32_t num_pages, size_t* ref, size_t* free_map);
+
+/* Fill the state from the tables (e.g. those of pks_build_block_table): every
+ * entry p < ceil(len_b / page_size) holds its page.  An entry out of range or
+ * a bad length sets the device error word (the entry, or the row, counts for
+ * nothing). */
+pks_status pks_pages_init(const pks_pages_args* args, pks_stream stream);
+
+/* Fork: for every i < n, row dst_rows[i] becomes an alias of the first
+ * n_tokens[i] tokens of row src_rows[i] (n_tokens NULL or n_tokens[i] < 0:
+ * all of them).  Its ceil(n_tokens / page_size) entries are copied, their
+ * pages gain a holder and seq_lens[dst] is set; no K/V moves, a partly filled
+ * last page is shared until one of its holders grows (pks_pages_extend).
+ * dst rows must be empty (length 0) and no row may be both a source and a
+ * destination of one call; a fork that breaks this, a repeated destination
+ * after its first use, a row out of range, more tokens than the source holds
+ * or a bad page in the source leaves its row as it was and sets the error
+ * word.  src_rows, dst_rows, n_tokens: device int32 [n], n <= B.  One launch. */
+pks_status pks_pages_fork(const pks_pages_args* args, int32_t n, const int32_t* src_rows,
+                          const int32_t* dst_rows, const int32_t* n_tokens, pks_stream stream);
+
+/* Grow: seq_lens[b] += add[b] (device int32 [B], >= 0) with the pages that
+ * this takes.  A growing row whose last page is partly filled and held by
+ * others too gets a page of its own first, the page's filled rows copied in
+ * every pool (copy-on-write); when all holders of such a page grow in this
+ * call the highest row keeps it.  Pages are taken lowest id first, rows in
+ * ascending order, a row's copy before its new pages.  The new tokens' rows
+ * are the caller's to write.  All or nothing: when the free pages do not
+ * suffice, or a row would pass max_pages * page_size tokens, has a bad length
+ * or page, or add[b] < 0, nothing changes, the error word is set (6: out of
+ * pages) and the grant word (header index 6) is 0 instead of 1.  Two launches
+ * (one without pools). */
+pks_status pks_pages_extend(const pks_pages_args* args, const int32_t* add, pks_stream stream);
+
+/* Truncate row rows[i] to keep[i] tokens (keep NULL: 0, the whole row is given
+ * back): entries at p >= ceil(keep / page_size) become -1 and their pages lose
+ * a holder; pages without holders are free again.  A row out of range, a
+ * repeated row after its first use or keep[i] outside [0, len] changes nothing
+ * and sets the error word.  rows, keep: device int32 [n], n <= B.  One launch. */
+pks_status pks_pages_free(const pks_pages_args* args, int32_t n, const int32_t* rows,
+                          const int32_t* keep, pks_stream stream);
+
+/* Compact: with n_used pages held, the k-th held page at or above n_used (in
+ * ascending order) moves to the k-th free page below it in every pool, with
+ * its whole content, and the table follows; afterwards pages [0, n_used) are
+ * held and the rest are free.  page_map (device int32 [num_pages], nullable):
+ * the new id of every page that was held, -1 for the others.  Table entries
+ * at or beyond ceil(len_b / page_size) stay as they were.  Two launches. */
+pks_status pks_pages_compact(const pks_pages_args* args, int32_t* page_map, pks_stream stream);
+
+/* Copy the state's device error word to *code (host) and clear it;
+ * synchronises the stream.  0: none; 1 page id out of range; 3 length, token
+ * count or growth out of range; 4 a page lost more holders than it had;
+ * 6 out of pages; 7 row index out of range, repeated, not empty or both
+ * source and destination. */
+pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks_stream stream);
+
 /* ---- staging of a step's inputs and outputs --------------------------------
  * Not an operation of the pages: a serving convenience for moving a step's
  * small inputs (queries, lengths, block table) in and its outputs (attention

@@ -697,6 +697,105 @@ pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_str
   return PKS_OK;
 }
 
+// --------------------------------------------------------------- pages ---
+
+namespace {
+constexpr int32_t kMaxPages = int32_t(1) << 24;
+
+pks_status pages_check(const pks_pages_args* a) {
+  if (!a) return PKS_ERR_INVALID;
+  if (a->num_pages < 1 || a->page_size < 1 || a->B < 0 || a->max_pages < 1 || a->reserved != 0 ||
+      a->n_pools < 0 || a->n_pools > PKS_PAGES_MAX_POOLS)
+    return PKS_ERR_INVALID;
+  if (a->num_pages > kMaxPages || a->B > pks::kMaxB) return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)a->num_pages * a->page_size > INT32_MAX) return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)a->max_pages * a->page_size > pks::kMaxLen) return PKS_ERR_UNSUPPORTED;
+  if (a->B > 0 && (!a->seq_lens || !a->block_table)) return PKS_ERR_INVALID;
+  for (int i = 0; i < a->n_pools; ++i)
+    if (!a->pools[i].data || a->pools[i].token_bytes < 1 ||
+        a->pools[i].token_bytes > (int64_t(1) << 32))
+      return PKS_ERR_INVALID;
+  if (!a->state || (reinterpret_cast<uintptr_t>(a->state) & (pks::kAlign - 1)) != 0 ||
+      a->state_bytes < pks::pages_layout(a->num_pages).total)
+    return PKS_ERR_WORKSPACE;
+  return PKS_OK;
+}
+}  // namespace
+
+pks_status pks_pages_state_bytes(int32_t num_pages, size_t* bytes) {
+  if (!bytes || num_pages < 1 || num_pages > kMaxPages) return PKS_ERR_INVALID;
+  *bytes = pks::pages_layout(num_pages).total;
+  return PKS_OK;
+}
+
+pks_status pks_pages_offsets(int32_t num_pages, size_t* ref, size_t* free_map) {
+  if (num_pages < 1 || num_pages > kMaxPages) return PKS_ERR_INVALID;
+  const pks::PagesLayout L = pks::pages_layout(num_pages);
+  if (ref) *ref = L.ref;
+  if (free_map) *free_map = L.free_map;
+  return PKS_OK;
+}
+
+pks_status pks_pages_init(const pks_pages_args* args, pks_stream stream) {
+  const pks_status st = pages_check(args);
+  if (st != PKS_OK) return st;
+  return pks::from_cuda(pks::launch_pages_init(*args, pks::pages_layout(args->num_pages),
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_pages_fork(const pks_pages_args* args, int32_t n, const int32_t* src_rows,
+                          const int32_t* dst_rows, const int32_t* n_tokens, pks_stream stream) {
+  const pks_status st = pages_check(args);
+  if (st != PKS_OK) return st;
+  if (n < 0 || n > args->B || (n > 0 && (!src_rows || !dst_rows))) return PKS_ERR_INVALID;
+  if (n == 0) return PKS_OK;
+  return pks::from_cuda(pks::launch_pages_fork(*args, pks::pages_layout(args->num_pages), n,
+                                               src_rows, dst_rows, n_tokens,
+                                               reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_pages_extend(const pks_pages_args* args, const int32_t* add, pks_stream stream) {
+  const pks_status st = pages_check(args);
+  if (st != PKS_OK) return st;
+  if (args->B > 0 && !add) return PKS_ERR_INVALID;
+  if (args->B == 0) return PKS_OK;
+  return pks::from_cuda(pks::launch_pages_extend(*args, pks::pages_layout(args->num_pages), add,
+                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_pages_free(const pks_pages_args* args, int32_t n, const int32_t* rows,
+                          const int32_t* keep, pks_stream stream) {
+  const pks_status st = pages_check(args);
+  if (st != PKS_OK) return st;
+  if (n < 0 || n > args->B || (n > 0 && !rows)) return PKS_ERR_INVALID;
+  if (n == 0) return PKS_OK;
+  return pks::from_cuda(pks::launch_pages_free(*args, pks::pages_layout(args->num_pages), n, rows,
+                                               keep, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_pages_compact(const pks_pages_args* args, int32_t* page_map, pks_stream stream) {
+  const pks_status st = pages_check(args);
+  if (st != PKS_OK) return st;
+  return pks::from_cuda(pks::launch_pages_compact(*args, pks::pages_layout(args->num_pages),
+                                                  page_map,
+                                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks_stream stream) {
+  if (!code) return PKS_ERR_INVALID;
+  const pks_status st = pages_check(args);
+  if (st != PKS_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int32_t* dev = static_cast<int32_t*>(args->state) + 3;
+  int32_t host = 0;
+  cudaError_t e = cudaMemcpyAsync(&host, dev, sizeof(int32_t), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(dev, 0, sizeof(int32_t), s);
+  if (e != cudaSuccess) return PKS_ERR_CUDA;
+  *code = host;
+  return PKS_OK;
+}
+
 pks_status pks_stage_copy(const pks_copy_range* ranges, int32_t n, pks_stream stream) {
   if (!ranges || n < 1 || n > PKS_STAGE_MAX_RANGES) return PKS_ERR_INVALID;
   for (int i = 0; i < n; ++i)

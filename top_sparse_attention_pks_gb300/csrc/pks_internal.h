@@ -84,8 +84,12 @@ constexpr int kErrToken = 2;
 constexpr int kErrLen = 3;
 constexpr int kErrState = 4;
 constexpr int kErrTimeout = 5;
+constexpr int kErrNoPages = 6;
+constexpr int kErrRow = 7;
 // header word 5 of a residency state filled by pks_residency_init
 constexpr int32_t kResidencyMagic = 0x504b5352;
+// header word 5 of a page state filled by pks_pages_init
+constexpr int32_t kPagesMagic = 0x504b5047;
 
 struct TopkThreshold {
   int32_t bin;        // coarse threshold bin T1
@@ -167,6 +171,22 @@ cudaError_t launch_residency(int32_t* state, int32_t num_pages, int32_t capacity
                              size_t off_slot_page, size_t off_last_use, size_t off_lru,
                              size_t off_flag, size_t off_slot_flag, size_t off_vict,
                              cudaStream_t s);
+
+// ---- page table on the device (k_pages.cu): byte offsets inside the state
+struct PagesLayout {
+  size_t ref, free_map, cnt, last, stamp, zeroed, moves, taken, total;
+};
+PagesLayout pages_layout(int32_t num_pages);
+cudaError_t launch_pages_init(const pks_pages_args& a, const PagesLayout& L, cudaStream_t s);
+cudaError_t launch_pages_fork(const pks_pages_args& a, const PagesLayout& L, int n,
+                              const int32_t* src, const int32_t* dst, const int32_t* tokens,
+                              cudaStream_t s);
+cudaError_t launch_pages_free(const pks_pages_args& a, const PagesLayout& L, int n,
+                              const int32_t* rows, const int32_t* keep, cudaStream_t s);
+cudaError_t launch_pages_extend(const pks_pages_args& a, const PagesLayout& L, const int32_t* add,
+                                cudaStream_t s);
+cudaError_t launch_pages_compact(const pks_pages_args& a, const PagesLayout& L, int32_t* page_map,
+                                 cudaStream_t s);
 
 // Allocation-free attention (pks_sparse_attention_static): bytes of the
 // file-scope device scratch array, the least any call with these shapes

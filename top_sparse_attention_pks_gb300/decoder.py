@@ -248,3 +248,53 @@ class MlaDecodeStep:
         pks.pks_decode_select(self.select_args, stream)
         pks.pks_mla_sparse_attention(self.attention.args, stream)
         return self.out, self.topk_idx
+
+
+class PageTable:
+    """A block table whose page sharing is kept on the device (``pks_pages_*``):
+    holders of every page and the free pages.  ``seq_lens`` [B] and
+    ``block_table`` [B, max_pages] (int32, e.g. from ``Pool.build_block_table``)
+    stay the caller's tensors and are updated in place; ``pools`` are the paged
+    tensors [num_pages, page_size, ...] whose rows move with the pages.  All
+    calls run on ``stream`` (default: torch's current stream).
+
+    ``refs`` [num_pages], ``n_free`` and ``granted`` (0-dim) are views of the
+    state and ``page_map`` [num_pages] is what the last ``compact`` wrote."""
+
+    def __init__(self, seq_lens, block_table, num_pages: int, page_size: int, pools=(),
+                 state=None, stream=None):
+        dev = block_table.device
+        nbytes = pks.pks_pages_state_bytes(num_pages)
+        if state is None:
+            state = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        self.state = state
+        self.seq_lens, self.block_table, self.pools = seq_lens, block_table, list(pools)
+        self.args = pks.make_pages_args(seq_lens=seq_lens, block_table=block_table,
+                                        num_pages=num_pages, page_size=page_size, state=state,
+                                        pools=self.pools)
+        off = pks.pks_pages_offsets(num_pages)["ref"]
+        header = state[:256].view(torch.int32)
+        self.n_free, self.granted = header[2], header[6]
+        self.refs = state[off: off + 4 * int(num_pages)].view(torch.int32)
+        self.page_map = torch.empty(int(num_pages), dtype=torch.int32, device=dev)
+        pks.pks_pages_init(self.args, stream)
+
+    def fork(self, src_rows, dst_rows, n_tokens=None, stream=None):
+        """Rows ``dst_rows`` (empty) become aliases of ``src_rows``' first tokens."""
+        pks.pks_pages_fork(self.args, src_rows, dst_rows, n_tokens, stream)
+
+    def extend(self, add, stream=None):
+        """Every row grows by ``add`` [B] tokens, or none does (``granted`` is 0)."""
+        pks.pks_pages_extend(self.args, add, stream)
+
+    def free(self, rows, keep=None, stream=None):
+        """Truncate ``rows`` to ``keep`` tokens (default 0: give them back)."""
+        pks.pks_pages_free(self.args, rows, keep, stream)
+
+    def compact(self, stream=None):
+        """Move the held pages to the lowest ids; returns the map of page ids."""
+        pks.pks_pages_compact(self.args, self.page_map, stream)
+        return self.page_map
+
+    def device_error(self, stream=None) -> int:
+        return pks.pks_pages_device_error(self.args, stream)

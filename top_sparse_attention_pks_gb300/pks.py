@@ -66,6 +66,24 @@ class pks_mla_args(ctypes.Structure):
     ]
 
 
+PKS_PAGES_MAX_POOLS = 8
+
+
+class pks_page_pool(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_bytes", ctypes.c_int64)]
+
+
+class pks_pages_args(ctypes.Structure):
+    _fields_ = [
+        ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("B", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("state", ctypes.c_void_p), ("state_bytes", ctypes.c_size_t),
+        ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("n_pools", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("pools", pks_page_pool * PKS_PAGES_MAX_POOLS),
+    ]
+
+
 def library_path() -> Path:
     return _LIB_PATH
 
@@ -147,6 +165,23 @@ def _declare(L):
     L.pks_residency_update.argtypes = [_P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
                                        _P]
     L.pks_residency_update.restype = _ST
+    _PG = ctypes.POINTER(pks_pages_args)
+    L.pks_pages_state_bytes.argtypes = [_I32, ctypes.POINTER(ctypes.c_size_t)]
+    L.pks_pages_state_bytes.restype = _ST
+    L.pks_pages_offsets.argtypes = [_I32] + [ctypes.POINTER(ctypes.c_size_t)] * 2
+    L.pks_pages_offsets.restype = _ST
+    L.pks_pages_init.argtypes = [_PG, _P]
+    L.pks_pages_init.restype = _ST
+    L.pks_pages_fork.argtypes = [_PG, _I32, _P, _P, _P, _P]
+    L.pks_pages_fork.restype = _ST
+    L.pks_pages_extend.argtypes = [_PG, _P, _P]
+    L.pks_pages_extend.restype = _ST
+    L.pks_pages_free.argtypes = [_PG, _I32, _P, _P, _P]
+    L.pks_pages_free.restype = _ST
+    L.pks_pages_compact.argtypes = [_PG, _P, _P]
+    L.pks_pages_compact.restype = _ST
+    L.pks_pages_device_error.argtypes = [_PG, ctypes.POINTER(ctypes.c_int32), _P]
+    L.pks_pages_device_error.restype = _ST
     L.pks_stage_copy.argtypes = [ctypes.POINTER(pks_copy_range), _I32, _P]
     L.pks_stage_copy.restype = _ST
 
@@ -586,4 +621,86 @@ def pks_mla_device_error(args: pks_mla_args, stream=None) -> int:
     code = ctypes.c_int32()
     _check(lib().pks_mla_device_error(ctypes.byref(args), ctypes.byref(code), _stream(stream)),
            "pks_mla_device_error")
+    return code.value
+
+
+# ------------------------------------------------------- pages on the device
+
+def make_pages_args(*, seq_lens, block_table, num_pages: int, page_size: int, state,
+                    pools: Sequence = ()) -> pks_pages_args:
+    """Fill a ``pks_pages_args``: seq_lens [B], block_table [B, max_pages] (int32),
+    state (uint8), pools: tensors [num_pages, page_size, ...] of any type."""
+    a = pks_pages_args()
+    if len(pools) > PKS_PAGES_MAX_POOLS:
+        raise ValueError(f"at most {PKS_PAGES_MAX_POOLS} pools")
+    if block_table.dim() != 2 or tuple(seq_lens.shape) != tuple(block_table.shape[:1]):
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    a.num_pages, a.page_size = int(num_pages), int(page_size)
+    a.B, a.max_pages = int(block_table.shape[0]), int(block_table.shape[1])
+    a.seq_lens = _dptr(seq_lens, torch.int32, "seq_lens")
+    a.block_table = _dptr(block_table, torch.int32, "block_table")
+    a.state = _dptr(state, torch.uint8, "state")
+    a.state_bytes = state.numel()
+    a.n_pools = len(pools)
+    for i, p in enumerate(pools):
+        if p.dim() < 2 or tuple(p.shape[:2]) != (int(num_pages), int(page_size)):
+            raise ValueError(f"pool {i} must be [num_pages, page_size, ...]")
+        token = p[0, 0].numel() * p.element_size()
+        a.pools[i] = pks_page_pool(_dptr(p, p.dtype, f"pool {i}"), token)
+    return a
+
+
+def pks_pages_state_bytes(num_pages: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().pks_pages_state_bytes(int(num_pages), ctypes.byref(n)), "pks_pages_state_bytes")
+    return n.value
+
+
+def pks_pages_offsets(num_pages: int) -> dict:
+    v = [ctypes.c_size_t() for _ in range(2)]
+    _check(lib().pks_pages_offsets(int(num_pages), *map(ctypes.byref, v)), "pks_pages_offsets")
+    return dict(zip(("ref", "free_map"), (x.value for x in v)))
+
+
+def pks_pages_init(args: pks_pages_args, stream=None) -> None:
+    _check(lib().pks_pages_init(ctypes.byref(args), _stream(stream)), "pks_pages_init")
+
+
+def pks_pages_fork(args: pks_pages_args, src_rows, dst_rows, n_tokens=None, stream=None) -> None:
+    n = int(src_rows.shape[0])
+    if dst_rows.shape[0] != n or (n_tokens is not None and n_tokens.shape[0] != n):
+        raise ValueError("src_rows, dst_rows and n_tokens must have the same length")
+    _check(lib().pks_pages_fork(ctypes.byref(args), n, _dptr(src_rows, torch.int32, "src_rows"),
+                                _dptr(dst_rows, torch.int32, "dst_rows"),
+                                _dptr(n_tokens, torch.int32, "n_tokens"), _stream(stream)),
+           "pks_pages_fork")
+
+
+def pks_pages_extend(args: pks_pages_args, add, stream=None) -> None:
+    if add.numel() != args.B:
+        raise ValueError("add must be [B]")
+    _check(lib().pks_pages_extend(ctypes.byref(args), _dptr(add, torch.int32, "add"),
+                                  _stream(stream)), "pks_pages_extend")
+
+
+def pks_pages_free(args: pks_pages_args, rows, keep=None, stream=None) -> None:
+    n = int(rows.shape[0])
+    if keep is not None and keep.shape[0] != n:
+        raise ValueError("rows and keep must have the same length")
+    _check(lib().pks_pages_free(ctypes.byref(args), n, _dptr(rows, torch.int32, "rows"),
+                                _dptr(keep, torch.int32, "keep"), _stream(stream)),
+           "pks_pages_free")
+
+
+def pks_pages_compact(args: pks_pages_args, page_map=None, stream=None) -> None:
+    if page_map is not None and page_map.numel() != args.num_pages:
+        raise ValueError("page_map must be [num_pages]")
+    _check(lib().pks_pages_compact(ctypes.byref(args), _dptr(page_map, torch.int32, "page_map"),
+                                   _stream(stream)), "pks_pages_compact")
+
+
+def pks_pages_device_error(args: pks_pages_args, stream=None) -> int:
+    code = ctypes.c_int32()
+    _check(lib().pks_pages_device_error(ctypes.byref(args), ctypes.byref(code), _stream(stream)),
+           "pks_pages_device_error")
     return code.value
