@@ -414,6 +414,69 @@ pks_status pks_mla_sparse_attention(const pks_mla_args* args, pks_stream stream)
 pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_stream stream);
 
 /* ------------------------------------------------------------------------
+ * Dense attention over a batch with shared prefixes ([PKV] "Page sharing":
+ * identical prefixes point to the same pages; [SA] introduction: scaled
+ * dot-product attention).  For every request b, query token i and head h
+ *   out[b,i,h] = sum_t p_t V[t],  p = softmax over t of sm_scale * q[b,i,h] . K[t]
+ * over the tokens t < lim of request b found through its block-table row;
+ * lim = len_b, or with `causal` len_b - Nq + i + 1 (query token i stands at
+ * position len_b - Nq + i).  A query without tokens gets zeros.  The result
+ * is each request's own attention whatever the groups are: prefix_group only
+ * says between which requests aliased pages are looked for.  Within a group
+ * the leading table entries equal to the longest member's are the shared
+ * part; the group's common prefix (the least among the members that share at
+ * least half of what the second longest shares) takes part once for all of
+ * these members, the rest of each request on its own.  Rows of a tile beyond
+ * a causal query's limit count with weight zero, so their V rows have to be
+ * finite; rows at or beyond len_b are never read.
+ * ---------------------------------------------------------------------- */
+typedef struct pks_prefix_args {
+  int32_t B;              /* requests; B * Nq <= 4096 */
+  int32_t Hq, Hkv;        /* 1 <= Hq / Hkv <= 16 */
+  int32_t D;              /* 64 or 128 */
+  int32_t page_size, max_pages, num_pages;
+  int32_t n_queries;      /* Nq, 0 (one) to 64 */
+  int32_t causal;         /* 0 or 1 */
+  int32_t wait_limit;     /* as in pks_mla_args */
+  float sm_scale;         /* 0 = 1 / sqrt(D) */
+  int32_t reserved;       /* must be 0 */
+  const int32_t* seq_lens;      /* device int32 [B] */
+  const int32_t* block_table;   /* device int32 [B, max_pages] */
+  const int32_t* prefix_group;  /* NULL, or device int32 [B]: group id, negative = none */
+  const void* q;          /* device bf16 [B, Nq, Hq, D], 16-byte aligned */
+  const void* kv_k;       /* device bf16 [num_pages, page_size, Hkv, D], 16-byte aligned */
+  const void* kv_v;       /* likewise */
+  void* out;              /* device bf16 [B, Nq, Hq, D], 16-byte aligned (written) */
+  float* lse;             /* NULL, or device float [B, Nq, Hq] (written): ln of the sum of
+                             exp(sm_scale * q . K), -inf for a query without tokens */
+  void* workspace;        /* device scratch owned by the caller, 256-byte aligned; its first
+                             256 bytes zeroed once by the caller */
+  size_t workspace_bytes;
+} pks_prefix_args;
+
+/* Workspace bytes for these shapes (pointers may be NULL, but prefix_group
+ * NULL or not as in the calls). */
+pks_status pks_prefix_workspace_size(const pks_prefix_args* args, size_t* bytes);
+
+/* Find the shared prefixes and lay out the work, into the workspace: once
+ * whenever lengths, tables or groups have changed (one plan serves every layer
+ * of a step).  q, kv_k, kv_v, out and lse are not used.  One launch. */
+pks_status pks_prefix_plan(const pks_prefix_args* args, pks_stream stream);
+
+/* The attention by the plan in the workspace (lengths and groups as they were
+ * then; the table rows must still hold the same pages).  Two or three launches.  INVALID for
+ * NULL or misaligned pointers and shapes that are no shapes, UNSUPPORTED for
+ * shapes outside the ranges above, WORKSPACE for a missing, misaligned or too
+ * small workspace. */
+pks_status pks_prefix_attention(const pks_prefix_args* args, pks_stream stream);
+
+/* Copy the workspace's device error word to *code (host) and clear it;
+ * synchronises the stream (codes as for pks_decode_device_error; 5: a bounded
+ * wait inside the kernel gave up). */
+pks_status pks_prefix_device_error(const pks_prefix_args* args, int32_t* code,
+                                   pks_stream stream);
+
+/* ------------------------------------------------------------------------
  * Pages on the device ([PKV] "Paging", "Page sharing", "What this table does
  * not say").  The host pool above hands pages out; these calls keep the
  * sharing of a batch's pages on the GPU, so that a decode loop can fork, grow,

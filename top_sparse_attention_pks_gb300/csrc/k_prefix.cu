@@ -1,0 +1,1396 @@
+// Dense decode attention of a batch whose requests alias the pages of a shared
+// prefix: the prefix takes part once for all of them.
+//
+// "Paged KV cache, or why reserving for the maximum length is wasteful",
+// "Page sharing": requests with an identical prefix point at the same pages.
+// Attention splits over any partition of the tokens,
+//   out = sum_i w_i o_i / sum_i w_i l_i,  w_i = 2^(m_i - max m),
+// with (m_i, l_i, o_i) the maximum, sum and unnormalised output of part i, so
+// a request's attention is the shared prefix's part and its own tokens' part.
+// The prefix part of all members of a group is one dense product per KV head,
+// with (members x query tokens x heads of the group) rows: its K/V rows are
+// read once instead of once a member, and with enough rows it belongs on the
+// tensor cores with tensor-memory accumulators.
+//
+//   k_prefix_plan   which leading table entries each request shares with its
+//                   group's longest member, the groups' common prefix, and the
+//                   lists of work ("items") below
+//   k_prefix_wide   items of up to 256 query rows against a token range (the
+//                   prefixes; with more than 16 rows a request and KV head
+//                   also the requests' own tokens), tcgen05
+//   k_prefix_narrow own tokens of requests with up to 16 rows, streamed like
+//                   the sparse attention's rows
+//   k_prefix_merge  the parts' combination
+//
+// Both attention kernels are persistent and cut their work into equal ranges
+// (tiles of all items, head after head); a CTA writes a partial (m, l, o) for
+// each item that its range touches, in slots that the merge derives from the
+// plan again.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "pks_internal.h"
+#include "tcgen05.cuh"
+
+namespace pks {
+namespace {
+
+constexpr int kTile = 128;        // tokens of a wide tile (MMA N of S, K of P.V)
+constexpr int kRows = 128;        // query rows of one MMA
+constexpr int kItemRows = 256;    // query rows of an item: two MMAs
+constexpr int kNarrowRows = 16;   // most rows (Nq * G) of the narrow kernel
+constexpr int kNarrowTile = 16;
+constexpr int kNarrowStages = 3;
+constexpr int kNarrowRowCap = 2048;
+constexpr int kMaxB = 4096;
+// Shared tokens below which a group is not worth a prefix item: one wide tile.
+constexpr int kMinShared = kTile;
+
+struct Item {
+  int row0;     // prefix item: first row in group order; own item: first row of the request
+  int nrows;    // 1..256
+  int bt_row;   // block-table row its tokens are found through
+  int own;      // 1: rows of request bt_row against its own tokens
+  int t0, t1;   // token range
+  int unit0;    // units of the items before it (one head): tiles times MMAs a tile
+  int slot0;    // partial rows of the items before it (one head)
+};
+
+// plan header words
+constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTokens = 5;
+
+struct PlanPtrs {
+  int32_t* hdr;
+  int32_t *lens, *eq, *first, *lead;   // per request
+  int32_t *start;                      // first own token
+  int32_t *pitem, *prow;               // prefix: first item of the group, row in the group
+  int32_t *oitem;                      // first own item (wide)
+  int32_t *order;                      // members in group order
+  int32_t *npre;                       // [B + 1] own tokens before each request (narrow)
+  Item* items;                         // one more than there are
+};
+
+struct PrefixShape {
+  int B, Hq, Hkv, G, Nq, R;
+  int page_size, max_pages, num_pages;
+  int causal;
+  int narrow;      // own tokens by the narrow kernel
+  int wide_grid, narrow_grid;
+  int hg;          // KV heads of a narrow CTA
+};
+
+// 2^x with the hardware's approximate exponential (a few ulp in fp32)
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void flag_error(int32_t* err, int code) { atomicCAS(err, 0, code); }
+
+__device__ __forceinline__ int item_halves(int nrows) { return nrows <= kRows ? 2 : 1; }
+// MMAs a tile of an item costs: one, or two for two row blocks
+__device__ __forceinline__ int item_weight(int nrows) { return nrows <= kRows ? 1 : 2; }
+// partial rows of an item per CTA: with one row block each softmax group keeps its own
+__device__ __forceinline__ int item_slots(int nrows) { return nrows <= kRows ? 2 * nrows : nrows; }
+
+// CTAs that share `total` units: all, or one per `least` units
+__device__ __forceinline__ int used_grid(int64_t total, int grid, int least) {
+  const int64_t g = (total + least - 1) / least;
+  return g < 1 ? 1 : g < grid ? (int)g : grid;
+}
+constexpr int kWideLeast = 2;                    // tiles a CTA takes at least
+constexpr int kNarrowLeast = 2 * kNarrowTile;    // tokens a CTA takes at least
+
+__device__ __forceinline__ int64_t range_lo(int64_t total, int c, int n) { return c * total / n; }
+// the CTA whose range holds unit u
+__device__ __forceinline__ int range_owner(int64_t u, int64_t total, int n) {
+  return (int)(((u + 1) * n + total - 1) / total - 1);
+}
+
+// ------------------------------------------------------------------ plan ---
+
+constexpr int kPlanThreads = 256;
+
+template <typename T, typename F>
+__device__ __forceinline__ T block_reduce(T v, F op, T* s_red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
+  __syncthreads();
+  if (lane == 0) s_red[warp] = v;
+  __syncthreads();
+  v = s_red[0];
+#pragma unroll
+  for (int w = 1; w < kPlanThreads / 32; ++w) v = op(v, s_red[w]);
+  return v;
+}
+
+// exclusive scan over the block of one value a thread
+__device__ __forceinline__ int block_scan_ex(int v, int* s_red, int& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int x = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  __syncthreads();
+  if (lane == 31) s_red[warp] = x;
+  __syncthreads();
+  int before = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kPlanThreads / 32; ++w) {
+    if (w < warp) before += s_red[w];
+    total += s_red[w];
+  }
+  return before + x - v;
+}
+
+// tokens every query of the request sees
+__device__ __forceinline__ int seen_by_all(int len, int causal, int Nq) {
+  if (!causal) return len;
+  const int v = len - Nq + 1;
+  return v < 0 ? 0 : v;
+}
+
+// A block a request finds what it shares with its group's longest member; the
+// last block to finish makes the plan.
+__global__ void __launch_bounds__(kPlanThreads)
+k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
+              const int32_t* __restrict__ prefix_group, PlanPtrs pl, PrefixShape sh) {
+  extern __shared__ int s_dyn[];  // [4][B] in the last block
+  __shared__ long long s_red64[kPlanThreads / 32];
+  __shared__ int s_red[kPlanThreads / 32];
+  __shared__ int s_last;
+  const int tid = threadIdx.x, B = sh.B;
+  const int max_len = sh.max_pages * sh.page_size;
+  pdl_launch_dependents();
+  pdl_wait();
+  auto length = [&](int b) {
+    const int n = seq_lens[b];
+    return n < 0 || n > max_len ? 0 : n;
+  };
+  auto group = [&](int b) {
+    const int g = prefix_group ? prefix_group[b] : -1;
+    return g < 0 ? -1 : g;
+  };
+  auto pages = [&](int n) { return (n + sh.page_size - 1) / sh.page_size; };
+  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+    const int len = length(b), g = group(b);
+    if (tid == 0) {
+      if (len != seq_lens[b]) flag_error(pl.hdr + kErrWord, kErrLen);
+      pl.lens[b] = len;
+    }
+    int shared = 0, first = b, lead = b;
+    if (g >= 0) {
+      // longest member (the first of the longest) and first member of the group
+      long long best = -1;
+      int low = B;
+      for (int c = tid; c < B; c += kPlanThreads)
+        if (group(c) == g) {
+          const long long key = ((long long)length(c) << 12) | (kMaxB - 1 - c);
+          best = key > best ? key : best;
+          low = c < low ? c : low;
+        }
+      best = block_reduce(best, [](long long a, long long c) { return a > c ? a : c; }, s_red64);
+      first = block_reduce(low, [](int a, int c) { return a < c ? a : c; }, s_red);
+      lead = kMaxB - 1 - (int)(best & (kMaxB - 1));
+      // leading entries equal to the longest member's
+      const int np = pages(len);
+      const int32_t* mine = block_table + (int64_t)b * sh.max_pages;
+      const int32_t* its = block_table + (int64_t)lead * sh.max_pages;
+      int eq = np;
+      if (lead != b) {
+        constexpr int kStep = 4;
+        for (int p0 = 0; p0 < np; p0 += kPlanThreads * kStep) {
+          int differs = np;
+#pragma unroll
+          for (int u = 0; u < kStep; ++u) {
+            const int p = p0 + u * kPlanThreads + tid;
+            if (p < np && mine[p] != its[p]) differs = p < differs ? p : differs;
+          }
+          eq = block_reduce(differs, [](int a, int c) { return a < c ? a : c; }, s_red);
+          if (eq < np) break;
+        }
+      }
+      const int seen = seen_by_all(len, sh.causal, sh.Nq);
+      const int64_t tok = (int64_t)eq * sh.page_size;
+      shared = tok < seen ? (int)tok : seen;
+    }
+    if (tid == 0) {
+      pl.eq[b] = shared;
+      pl.first[b] = first;
+      pl.lead[b] = lead;
+    }
+  }
+  __threadfence();
+  __syncthreads();
+  if (tid == 0) s_last = atomicAdd(pl.hdr + kTicket, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (!s_last) return;
+  __threadfence();
+  if (tid == 0) pl.hdr[kTicket] = 0;
+
+  // ---- the last block: the groups' common prefixes.  The shared length of a
+  // group is the least among the members that share at least half of what the
+  // second longest shares; members with less stay on their own.
+  int* s_max = s_dyn;            // by first member: most shared tokens, the longest member aside
+  int* s_min = s_dyn + B;        // the group's prefix
+  int* s_cnt = s_dyn + 2 * B;    // members that take part
+  int* s_at = s_dyn + 3 * B;     // rows of the members before, in group order
+  for (int b = tid; b < B; b += kPlanThreads) {
+    s_max[b] = 0;
+    s_min[b] = 0x7fffffff;
+    s_cnt[b] = 0;
+  }
+  __syncthreads();
+  for (int b = tid; b < B; b += kPlanThreads)
+    if (__ldcg(pl.lead + b) != b) atomicMax(&s_max[__ldcg(pl.first + b)], __ldcg(pl.eq + b));
+  __syncthreads();
+  for (int b = tid; b < B; b += kPlanThreads) {
+    const int f = __ldcg(pl.first + b), e = __ldcg(pl.eq + b), most = s_max[f];
+    if (most >= kMinShared && e >= (most + 1) / 2) {
+      atomicMin(&s_min[f], e);
+      atomicAdd(&s_cnt[f], 1);
+    }
+  }
+  __syncthreads();
+  const int per = (B + kPlanThreads - 1) / kPlanThreads;
+  const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
+  // members and prefix items of the groups, by first member
+  int members = 0, items = 0, units = 0, slots = 0;
+  auto prefix_units = [&](int f, int& k, int& u, int& s) {
+    const int rows = s_cnt[f] * sh.R, nt = (s_min[f] + kTile - 1) / kTile;
+    k = (rows + kItemRows - 1) / kItemRows;
+    const int tail = rows - (k - 1) * kItemRows;
+    u = nt * (2 * (k - 1) + item_weight(tail));
+    s = (k - 1) * kItemRows + item_slots(tail);
+  };
+  for (int b = b_lo; b < b_hi; ++b)
+    if (s_cnt[b] >= 2) {
+      int k, u, s;
+      prefix_units(b, k, u, s);
+      members += s_cnt[b];
+      items += k;
+      units += u;
+      slots += s;
+    } else {
+      s_cnt[b] = 0;
+    }
+  int tm, ti, tu, ts;
+  int m0 = block_scan_ex(members, s_red, tm), i0 = block_scan_ex(items, s_red, ti);
+  int u0 = block_scan_ex(units, s_red, tu), sl0 = block_scan_ex(slots, s_red, ts);
+  for (int b = b_lo; b < b_hi; ++b) {
+    if (!s_cnt[b]) continue;
+    int k, u, s;
+    prefix_units(b, k, u, s);
+    const int T = s_min[b], rows = s_cnt[b] * sh.R, nt = (T + kTile - 1) / kTile;
+    const int lead = __ldcg(pl.lead + b);
+    s_at[b] = m0;
+    s_max[b] = i0;  // first item of the group from here on
+    int uu = u0, ss = sl0;
+    for (int i = 0; i < k; ++i) {
+      Item it;
+      it.row0 = m0 * sh.R + i * kItemRows;
+      it.nrows = min(kItemRows, rows - i * kItemRows);
+      it.bt_row = lead;
+      it.own = 0;
+      it.t0 = 0;
+      it.t1 = T;
+      it.unit0 = uu;
+      it.slot0 = ss;
+      pl.items[i0 + i] = it;
+      uu += nt * item_weight(it.nrows);
+      ss += item_slots(it.nrows);
+    }
+    m0 += s_cnt[b];
+    i0 += k;
+    u0 += u;
+    sl0 += s;
+  }
+  __syncthreads();
+  // members in group order, ascending within a group: one warp, 32 requests at
+  // a time (s_at counts up as members are placed)
+  if (tid < 32) {
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int b = b0 + tid;
+      int f = -1;
+      if (b < B) {
+        const int x = __ldcg(pl.first + b);
+        if (s_cnt[x] && __ldcg(pl.eq + b) >= s_min[x]) f = x;
+      }
+      const uint32_t peers = __match_any_sync(0xffffffffu, f);
+      int at = 0;
+      if (f >= 0) at = s_at[f] + __popc(peers & ((1u << tid) - 1));
+      __syncwarp();
+      if (f >= 0 && (peers >> tid) == 1u) s_at[f] = at + 1;  // the last of its group here
+      __syncwarp();
+      if (b < B) {
+        if (f >= 0) pl.order[at] = b;
+        pl.pitem[b] = f >= 0 ? s_max[f] : -1;
+        pl.prow[b] = at * sh.R;  // the group's first row is its first item's row0
+        pl.start[b] = f >= 0 ? s_min[f] : 0;
+      }
+    }
+  }
+  __syncthreads();
+  // own tokens: items of the wide kernel, or the narrow kernel's prefix sum
+  int own_i = 0, own_u = 0, own_s = 0, own_t = 0;
+  auto own_units = [&](int b, int& n, int& k, int& u, int& s) {
+    n = __ldcg(pl.lens + b) - pl.start[b];
+    k = u = s = 0;
+    if (n <= 0 || sh.narrow) return;
+    const int nt = (n + kTile - 1) / kTile;
+    k = (sh.R + kItemRows - 1) / kItemRows;
+    const int tail = sh.R - (k - 1) * kItemRows;
+    u = nt * (2 * (k - 1) + item_weight(tail));
+    s = (k - 1) * kItemRows + item_slots(tail);
+  };
+  for (int b = b_lo; b < b_hi; ++b) {
+    int n, k, u, s;
+    own_units(b, n, k, u, s);
+    own_i += k;
+    own_u += u;
+    own_s += s;
+    own_t += n;
+  }
+  int toi, tou, tos, tot;
+  int oi = ti + block_scan_ex(own_i, s_red, toi), ou = tu + block_scan_ex(own_u, s_red, tou);
+  int os = ts + block_scan_ex(own_s, s_red, tos), ot = block_scan_ex(own_t, s_red, tot);
+  for (int b = b_lo; b < b_hi; ++b) {
+    int n, k, u, s;
+    own_units(b, n, k, u, s);
+    pl.npre[b] = ot;
+    pl.oitem[b] = k ? oi : -1;
+    const int nt = (n + kTile - 1) / kTile;
+    int uu = ou, ss = os;
+    for (int i = 0; i < k; ++i) {
+      Item it;
+      it.row0 = i * kItemRows;
+      it.nrows = min(kItemRows, sh.R - i * kItemRows);
+      it.bt_row = b;
+      it.own = 1;
+      it.t0 = pl.start[b];
+      it.t1 = it.t0 + n;
+      it.unit0 = uu;
+      it.slot0 = ss;
+      pl.items[oi + i] = it;
+      uu += nt * item_weight(it.nrows);
+      ss += item_slots(it.nrows);
+    }
+    oi += k;
+    ou += u;
+    os += s;
+    ot += n;
+  }
+  if (tid == 0) {
+    pl.npre[B] = tot;
+    pl.hdr[kItems] = ti + toi;
+    pl.hdr[kUnits] = tu + tou;
+    pl.hdr[kSlots] = ts + tos;
+    pl.hdr[kTokens] = tot;
+    Item end = {};
+    end.unit0 = tu + tou;
+    end.slot0 = ts + tos;
+    pl.items[ti + toi] = end;
+  }
+}
+
+// ------------------------------------------------------------------ wide ---
+// One CTA an SM, 512 threads:
+//   warps 0-3, 4-7   softmax groups 0 and 1: a thread a query row
+//   warp 8           issues the MMAs
+//   warps 9-12       load Q and the K/V tiles
+// An item with more than 128 rows gives each softmax group a row block of its
+// own and every tile goes to both; with 128 or fewer both groups hold the same
+// rows and take the tiles in turn, so that one group's softmax always runs
+// beside the other's products.  Per (tile, group) "job":
+//   S[128 x 128] = Q K^T        tcgen05.mma, fp32 in tensor memory
+//   P            = 2^(S c - m)  a thread a row, bf16 into S's columns
+//   O[128 x D]  += P V          tcgen05.mma, P from tensor memory
+// issued as S(0), S(1), PV(0), S(2), PV(1), ...: the tensor pipe runs them in
+// this order, so S(j + 2) may overwrite the P of job j, and the completion of
+// S(j + 2) implies that of PV(j).  K and V tiles share a ring of 32 KB slots
+// (K, V, K, V, ...) in 128-byte swizzled rows.  The running maximum moves only
+// when a tile exceeds it by more than 8 (log2 units).
+
+constexpr int kWideThreads = 512;
+constexpr int kMmaWarp = 8, kLoadWarp = 9, kLoadThreads = 128;
+constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
+
+template <int D>
+struct Wide {
+  static constexpr int kBlk = D / 64;                          // 64-value column blocks
+  static constexpr uint32_t kBlkBytes = kTile * 128;
+  static constexpr uint32_t kTileBytes = kBlk * kBlkBytes;     // K, V or Q tile
+  static constexpr int kSlotsN = D == 128 ? 5 : 10;            // ring of K / V tiles
+  static constexpr uint32_t kSmem = (2 + kSlotsN) * kTileBytes + 1024;
+  // loads in flight beyond the newest; a piece has at least these (K and V of a tile)
+  static constexpr int kLag = 2;
+};
+constexpr uint32_t kTmemS = 256;  // columns: O of the groups at 0 and 128, S at 256 and 384
+
+template <int D>
+__global__ void __launch_bounds__(kWideThreads, 1)
+k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
+              const __nv_bfloat16* __restrict__ kv_k, const __nv_bfloat16* __restrict__ kv_v,
+              PlanPtrs pl, float2* __restrict__ part_ml, float* __restrict__ part_o,
+              PrefixShape sh, float scale_log2, long long budget) {
+  using W = Wide<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bar_full[W::kSlotsN], bar_free[W::kSlotsN], bar_q, bar_s[2],
+      bar_p[2], bar_o;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_abort, s_item;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sQ = base, sKV = base + 2 * W::kTileBytes;
+  const float kNegInf = __int_as_float(0xff800000);
+
+  if (warp == 0) tc::tmem_alloc(&s_tmem, 512);
+  if (tid == kMmaWarp * 32) {
+    for (int i = 0; i < W::kSlotsN; ++i) {
+      tc::mbar_init(&bar_full[i], kLoadThreads / 32);
+      tc::mbar_init(&bar_free[i], 1);
+    }
+    tc::mbar_init(&bar_q, kLoadThreads / 32);
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar_s[i], 1);
+      tc::mbar_init(&bar_p[i], 4);
+    }
+    tc::mbar_init(&bar_o, 1);
+    tc::mbar_init_fence();
+    s_abort = 0;
+  }
+  tc::fence_before();
+  __syncthreads();
+  tc::fence_after();
+  const uint32_t tmem = s_tmem;
+  pdl_wait();  // the plan
+  pdl_launch_dependents();
+
+  const int U = pl.hdr[kUnits], n_items = pl.hdr[kItems], slots_head = pl.hdr[kSlots];
+  const int64_t total = (int64_t)U * sh.Hkv;
+  const int grid = used_grid(total, gridDim.x, kWideLeast);
+  const int cta = blockIdx.x;
+  int64_t u = total > 0 && cta < grid ? range_lo(total, cta, grid) : 0;
+  const int64_t u_end = total > 0 && cta < grid ? range_lo(total, cta + 1, grid) : 0;
+
+  // counters of completed phases, the same in every role
+  uint32_t n_slot = 0, n_job[2] = {0, 0}, n_piece = 0;
+
+  while (u < u_end) {
+    // ---- the item of unit u and this CTA's tiles of it
+    const int head = (int)(u / U), ur = (int)(u - (int64_t)head * U);
+    for (int i = tid; i < n_items; i += kWideThreads)
+      if (pl.items[i].unit0 <= ur && ur < pl.items[i + 1].unit0) s_item = i;
+    __syncthreads();
+    const int item = s_item;
+    const Item it = pl.items[item];
+    const int next_unit = pl.items[item + 1].unit0;
+    const int w = item_weight(it.nrows);
+    const int64_t item_u0 = (int64_t)head * U + it.unit0;
+    const int64_t piece_end = u_end < (int64_t)head * U + next_unit ? u_end
+                                                                    : (int64_t)head * U + next_unit;
+    const int t_lo = (int)((u - item_u0 + w - 1) / w), t_hi = (int)((piece_end - item_u0 + w - 1) / w);
+    const int nt = t_hi - t_lo;
+    u = piece_end;
+    const int64_t slot = (int64_t)head * slots_head + it.slot0 + (int64_t)kItemRows * cta;
+    const bool pair = w == 2;
+    const int jobs = nt * w;
+    const int jobs1 = pair ? nt : nt / 2, jobs0 = jobs - jobs1;
+    auto job_group = [&](int j) { return j & 1; };
+    auto job_tile = [&](int j) { return pair ? j >> 1 : j; };
+    bool ok = true;
+
+    if (nt > 0 && warp == kMmaWarp) {
+      // ================= MMA issue =================
+      auto wait0 = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool r = lane == 0 ? tc::mbar_wait(bar, parity, &s_abort, budget) : true;
+        __syncwarp();
+        return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
+      };
+      auto issue_s = [&](int j) {
+        const int g = job_group(j), t = job_tile(j);
+        const uint32_t n = n_slot + 2 * t, s = n % W::kSlotsN;
+        const uint64_t dq = tc::desc_sw128(sQ + (pair ? g : 0) * W::kTileBytes, 16, 1024);
+        const uint64_t dk = tc::desc_sw128(sKV + s * W::kTileBytes, 16, 1024);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint64_t off = (uint64_t)(((kk >> 2) * W::kBlkBytes + (kk & 3) * 32) >> 4);
+          tc::mma_ss(tmem + kTmemS + g * kTile, dq + off, dk + off,
+                     tc::idesc_bf16(kRows, kTile, false), kk > 0 ? 1u : 0u);
+        }
+        tc::mma_commit(&bar_s[g]);
+        if (!pair || g == 1) tc::mma_commit(&bar_free[s]);
+      };
+      auto issue_pv = [&](int j) {
+        const int g = job_group(j), t = job_tile(j);
+        const uint32_t n = n_slot + 2 * t + 1, s = n % W::kSlotsN;
+        const uint64_t dv = tc::desc_sw128(sKV + s * W::kTileBytes, W::kBlkBytes, 1024);
+#pragma unroll
+        for (int kk = 0; kk < kTile / 16; ++kk)
+          tc::mma_ts(tmem + g * 128, tmem + kTmemS + g * kTile + kk * 8,
+                     dv + (uint64_t)((kk * 16 * 128) >> 4), tc::idesc_bf16(kRows, D, true),
+                     (j > 1 || kk > 0) ? 1u : 0u);
+        if (!pair || g == 1) tc::mma_commit(&bar_free[s]);
+      };
+      auto slot_full = [&](int j, int v) -> bool {
+        const uint32_t n = n_slot + 2 * job_tile(j) + v;
+        return wait0(&bar_full[n % W::kSlotsN], (n / W::kSlotsN) & 1);
+      };
+      ok = wait0(&bar_q, n_piece & 1);
+      int issued = 0;
+      if (ok && (ok = slot_full(0, 0))) {
+        if (lane == 0) {
+          tc::fence_after();
+          issue_s(0);
+        }
+        issued = 1;
+        __syncwarp();
+      }
+      for (int j = 0; j < jobs && ok; ++j) {
+        if (j + 1 < jobs) {
+          if (!(ok = slot_full(j + 1, 0))) break;
+          if (lane == 0) {
+            tc::fence_after();
+            issue_s(j + 1);
+          }
+          __syncwarp();
+        }
+        const int g = job_group(j);
+        if (!(ok = slot_full(j, 1))) break;
+        if (!(ok = wait0(&bar_p[g], (n_job[g] + (j >> 1)) & 1))) break;
+        if (lane == 0) {
+          tc::fence_after();
+          issue_pv(j);
+        }
+        __syncwarp();
+      }
+      // everything issued so far: O is complete, and nothing is in flight when
+      // the tensor memory is reused or freed
+      if (lane == 0) {
+        if (issued) tc::mma_commit(&bar_o);
+        if (!ok) {
+          flag_error(pl.hdr + kErrWord, kErrTimeout);
+          s_abort = 1;
+          if (issued) {
+            const long long t0 = clock64();
+            while (!tc::mbar_try_wait(&bar_o, n_piece & 1) && clock64() - t0 < kWaitCycles) {
+            }
+          }
+        }
+      }
+      __syncwarp();
+    } else if (nt > 0 && warp < kMmaWarp) {
+      // ================= softmax: a thread a query row =================
+      const int g = warp >> 2;
+      const int my_jobs = g ? jobs1 : jobs0;
+      const int x = (pair ? g * kRows : 0) + (tid & (kRows - 1));  // row of the item
+      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+      const uint32_t tS = tmem + lane_off + kTmemS + g * kTile, tO = tmem + lane_off + g * 128;
+      auto waitw = [&](uint64_t* bar, uint32_t parity) -> bool {
+        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, budget)) != 0;
+      };
+      // tokens this row sees
+      int limit = it.t1;
+      if (it.own && sh.causal && x < it.nrows) {
+        const int qi = (it.row0 + x) / sh.G;
+        limit = it.t1 - sh.Nq + qi + 1;
+      }
+      float m_run = kNegInf, l_run = 0.f;
+      for (int i = 0; i < my_jobs; ++i) {
+        const int t = pair ? i : 2 * i + g;
+        if (!waitw(&bar_s[g], (n_job[g] + i) & 1)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after();
+        const int nv = limit - (it.t0 + (t_lo + t) * kTile);  // valid columns
+        const bool masked = __any_sync(0xffffffffu, nv < kTile);
+        uint32_t sv[32];
+        float mx = kNegInf;
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 32) {
+          tc::tmem_ld32(tS + c, sv);
+          tc::tmem_ld_wait(sv);
+          if (masked) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (c + k < nv) mx = fmaxf(mx, __uint_as_float(sv[k]));
+          } else {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(sv[k]));
+          }
+        }
+        mx *= scale_log2;
+        const bool move = mx > m_run + 8.f;  // also true on the first valid tile
+        const float m_new = move ? mx : m_run;
+        const float alpha = move ? exp2f(m_run - m_new) : 1.f;
+        // O of the jobs before is complete: S of this job was issued after it
+        if (__any_sync(0xffffffffu, move && i > 0)) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            tc::tmem_ld32(tO + c, sv);
+            tc::tmem_ld_wait(sv);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sv[k] = __float_as_uint(__uint_as_float(sv[k]) * alpha);
+            tc::tmem_st32(tO + c, sv);
+          }
+          tc::tmem_st_wait();
+        }
+        l_run *= alpha;
+        m_run = m_new;
+        const float m_use = m_new == kNegInf ? 0.f : m_new;
+        // P takes the place of S columns that this warp has read already
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 64) {
+          uint32_t pk[32];
+          float sum = 0.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            tc::tmem_ld32(tS + c + 32 * h, sv);
+            tc::tmem_ld_wait(sv);
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              float p0 = ex2(fmaf(__uint_as_float(sv[k]), scale_log2, -m_use));
+              float p1 = ex2(fmaf(__uint_as_float(sv[k + 1]), scale_log2, -m_use));
+              if (masked) {
+                if (c + 32 * h + k >= nv) p0 = 0.f;
+                if (c + 32 * h + k + 1 >= nv) p1 = 0.f;
+              }
+              // P is rounded to bf16 for the second product (half a step, 2^-8 of
+              // each weight at most); the sum keeps the fp32 values, so that lse
+              // carries no such rounding
+              sum += p0 + p1;
+              const __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
+              pk[h * 16 + k / 2] = *reinterpret_cast<const uint32_t*>(&pp);
+            }
+          }
+          l_run += sum;
+          tc::tmem_st32(tS + c / 2, pk);
+        }
+        tc::tmem_st_wait();
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar_p[g]);
+      }
+      // ---- the piece's partial
+      if (ok && waitw(&bar_o, n_piece & 1)) {
+        tc::fence_after();
+        const bool mine = pair ? x < it.nrows : (tid & (kRows - 1)) < it.nrows;
+        const int64_t row = slot + (pair ? x : g * it.nrows + x);
+        if (mine) part_ml[row] = make_float2(m_run, l_run);
+        if (my_jobs > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t ov[32];
+            tc::tmem_ld32(tO + c, ov);
+            tc::tmem_ld_wait(ov);
+            if (mine) {
+              float* dst = part_o + row * D + c;
+#pragma unroll
+              for (int k = 0; k < 32; k += 4)
+                *reinterpret_cast<uint4*>(dst + k) =
+                    make_uint4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+            }
+          }
+        }
+      } else if (lane == 0) {
+        flag_error(pl.hdr + kErrWord, kErrTimeout);
+        s_abort = 1;
+      }
+    } else if (nt > 0 && warp >= kLoadWarp && warp < kLoadWarp + kLoadThreads / 32) {
+      // ================= loads =================
+      const int lt = tid - kLoadWarp * 32, lw = lt >> 5;
+      constexpr int kChunks = D / 8;              // 16-byte chunks of a row
+      constexpr int kRowsPer = 32 / kChunks;      // rows a warp instruction covers
+      const int sub = lane / kChunks, cc = lane % kChunks;
+      // warp lw fills rows 32 lw .. 32 lw + 31; chunk c of row r of column
+      // block j goes to chunk c ^ (r & 7)
+      auto dst_of = [&](uint32_t tile, int r) {
+        return tile + (cc >> 3) * W::kBlkBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
+      };
+#pragma unroll 1
+      for (int blk = 0; blk < (pair ? 2 : 1); ++blk) {
+        // query row of this lane: request, query token and head
+        const int x = blk * kRows + lw * 32 + lane;
+        int64_t off = -1;
+        if (x < it.nrows) {
+          const int gr = it.row0 + x;
+          const int b = it.own ? it.bt_row : pl.order[gr / sh.R];
+          const int r = it.own ? gr : gr % sh.R;
+          off = (((int64_t)b * sh.Nq + r / sh.G) * sh.Hq + head * sh.G + r % sh.G) * D;
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += kRowsPer) {
+          const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
+          tc::cp_async16(dst_of(sQ + blk * W::kTileBytes, lw * 32 + i + sub),
+                         q + (o >= 0 ? o + cc * 8 : 0), o >= 0 ? 16 : 0);
+        }
+      }
+      tc::cp_async_commit();
+      // physical row of this lane's token of tile t (-1: none)
+      const int32_t* bt = block_table + (int64_t)it.bt_row * sh.max_pages;
+      auto token_row = [&](int t) -> int {
+        const int tok = it.t0 + (t_lo + t) * kTile + lw * 32 + lane;
+        if (tok >= it.t1) return -1;
+        const int page = bt[tok / sh.page_size];
+        if ((unsigned)page >= (unsigned)sh.num_pages) {
+          flag_error(pl.hdr + kErrWord, kErrPage);
+          return -1;
+        }
+        return page * sh.page_size + tok % sh.page_size;
+      };
+      auto publish = [&](uint64_t* bar) {
+        tc::fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(bar);
+      };
+      const int total_loads = 2 * nt;
+      int row = token_row(0), next_row = -1;
+      int i = 0;
+      for (; i < total_loads; ++i) {
+        const uint32_t n = n_slot + i, s = n % W::kSlotsN;
+        if (n >= (uint32_t)W::kSlotsN) {
+          if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar_free[s], (n / W::kSlotsN - 1) & 1,
+                                                     &s_abort, budget))) {
+            ok = false;
+            break;
+          }
+        }
+        const bool is_v = i & 1;
+        const __nv_bfloat16* pool = is_v ? kv_v : kv_k;
+        const uint32_t tile = sKV + s * W::kTileBytes;
+#pragma unroll
+        for (int r = 0; r < 32; r += kRowsPer) {
+          const int pr = __shfl_sync(0xffffffffu, row, r + sub);
+          tc::cp_async16(dst_of(tile, lw * 32 + r + sub),
+                         pool + (pr >= 0 ? ((int64_t)pr * sh.Hkv + head) * D + cc * 8 : 0),
+                         pr >= 0 ? 16 : 0);
+        }
+        tc::cp_async_commit();
+        if (!is_v) next_row = (i >> 1) + 1 < nt ? token_row((i >> 1) + 1) : -1;
+        else row = next_row;
+        // publish what has landed: Q after the first kLag tiles, then the rest in order
+        tc::cp_async_wait<W::kLag>();
+        if (i == W::kLag - 1) publish(&bar_q);
+        if (i >= W::kLag) publish(&bar_full[(n - W::kLag) % W::kSlotsN]);
+      }
+      tc::cp_async_wait<0>();
+      if (ok) {
+        for (int k = total_loads - W::kLag; k < total_loads; ++k)
+          publish(&bar_full[(n_slot + k) % W::kSlotsN]);
+      } else if (lane == 0) {
+        flag_error(pl.hdr + kErrWord, kErrTimeout);
+        s_abort = 1;
+      }
+    }
+    // a share that rounds to no tile still has its place among the partials
+    if (nt == 0 && tid < item_slots(it.nrows)) part_ml[slot + tid] = make_float2(kNegInf, 0.f);
+    // ---- every role is done with the piece
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (nt > 0) {
+      n_slot += 2 * nt;
+      n_job[0] += jobs0;
+      n_job[1] += jobs1;
+      ++n_piece;
+    }
+    if (s_abort) break;
+  }
+  tc::fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc::fence_after();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- narrow ---
+// Own tokens of requests with at most 16 rows a KV head, streamed: a CTA takes
+// 16-token tiles of K and V rows of its HG heads (HG x D x 2 contiguous bytes a
+// token) through a 3-stage cp.async ring, a warp a KV head.  Both products run
+// transposed on mma.sync (tokens, then head dimension, as M; the rows as N), so
+// no MMA carries padding rows; the work is a few FLOP a byte and the ring's
+// rate is what bounds it.
+
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
+                                          uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+template <int D, int HG, int NT8>
+__global__ void __launch_bounds__(HG * 32, 1)
+k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
+                const __nv_bfloat16* __restrict__ kv_k, const __nv_bfloat16* __restrict__ kv_v,
+                PlanPtrs pl, float2* __restrict__ part_ml, float* __restrict__ part_o,
+                PrefixShape sh, float scale_log2, int wait_first) {
+  constexpr int NT = HG * 32, CH = D / 8, KS = D / 16, MT = D / 16, TILE = kNarrowTile;
+  constexpr int STAGE = TILE * HG * D;
+  const float kNegInf = __int_as_float(0xff800000);
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __nv_bfloat16* s_kv = reinterpret_cast<__nv_bfloat16*>(smem_raw);
+  int32_t* s_row = reinterpret_cast<int32_t*>(smem_raw + (size_t)kNarrowStages * 2 * STAGE * 2);
+  int32_t* s_pre = s_row + kNarrowRowCap;  // [B + 1]
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int B = sh.B, ngroups = sh.Hkv / HG;
+  // after the wide kernel the plan is complete (its CTAs waited for it before
+  // they let this grid start), and this grid only waits for it at its end
+  if (wait_first) pdl_wait();
+  pdl_launch_dependents();
+  const int Treq = pl.hdr[kTokens];
+  const int64_t T = (int64_t)Treq * ngroups;
+  const int grid = used_grid(T, gridDim.x, kNarrowLeast);
+  const int cta = blockIdx.x;
+  if (T == 0 || cta >= grid) {
+    if (!wait_first) pdl_wait();
+    return;
+  }
+  for (int i = tid; i <= B; i += NT) s_pre[i] = pl.npre[i];
+  __syncthreads();
+  const int64_t lo = range_lo(T, cta, grid), hi = range_lo(T, cta + 1, grid);
+
+  struct Cursor {
+    int g, b, p;
+    int64_t end;
+  };
+  auto locate = [&](int64_t f) {
+    Cursor c;
+    c.g = (int)(f / Treq);
+    const int fb = (int)(f - (int64_t)c.g * Treq);
+    int l = 0, h = B - 1;
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (s_pre[mid] <= fb) l = mid; else h = mid - 1;
+    }
+    c.b = l;
+    c.p = fb - s_pre[l];
+    c.end = (int64_t)c.g * Treq + s_pre[l + 1];
+    return c;
+  };
+  const int g8 = lane >> 2, t4 = lane & 3;
+  uint32_t qb[NT8][KS][2];
+  float o[NT8][MT][4], m_h[NT8][2], l_h[NT8][2];
+  int lim[NT8][2];  // own tokens that the thread's two rows see
+  auto begin = [&](const Cursor& c) {
+    const int head = c.g * HG + warp;
+    const int n = s_pre[c.b + 1] - s_pre[c.b];
+#pragma unroll
+    for (int nt = 0; nt < NT8; ++nt) {
+      const int j = nt * 8 + g8;
+      const __nv_bfloat16* src =
+          q + (((int64_t)c.b * sh.Nq + j / sh.G) * sh.Hq + (int64_t)head * sh.G + j % sh.G) * D + t4 * 2;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        qb[nt][ks][0] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+        qb[nt][ks][1] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m_h[nt][e] = kNegInf;
+        l_h[nt][e] = 0.f;
+        lim[nt][e] = sh.causal ? n - sh.Nq + (nt * 8 + 2 * t4 + e) / sh.G + 1 : n;
+      }
+    }
+  };
+  auto finish = [&](const Cursor& c) {
+    const int64_t base = (((int64_t)cta + (int64_t)c.g * B + c.b) * HG + warp) * sh.R;
+#pragma unroll
+    for (int nt = 0; nt < NT8; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float l = l_h[nt][e];
+        l += __shfl_xor_sync(0xffffffffu, l, 4);
+        l += __shfl_xor_sync(0xffffffffu, l, 8);
+        l += __shfl_xor_sync(0xffffffffu, l, 16);
+        const int j = nt * 8 + 2 * t4 + e;
+        if (j >= sh.R) continue;
+        float* po = part_o + (base + j) * D;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          po[mt * 16 + g8] = o[nt][mt][e];
+          po[mt * 16 + g8 + 8] = o[nt][mt][e + 2];
+        }
+        if (g8 == 0) part_ml[base + j] = make_float2(m_h[nt][e], l);
+      }
+  };
+
+  int64_t pos = lo;
+  Cursor cur{0, 0, 0, 0};
+  bool open = false;
+  for (int64_t chunk_lo = lo; chunk_lo < hi; chunk_lo += kNarrowRowCap) {
+    const int64_t chunk_hi = hi < chunk_lo + kNarrowRowCap ? hi : chunk_lo + kNarrowRowCap;
+    auto resolve = [&](int64_t f0, int64_t f1) {
+      for (int64_t f = f0 + tid; f < f1; f += NT) {
+        const Cursor c = locate(f);
+        const int t = pl.start[c.b] + c.p;
+        const int page = block_table[(int64_t)c.b * sh.max_pages + t / sh.page_size];
+        int row = -1;
+        if ((unsigned)page < (unsigned)sh.num_pages) row = page * sh.page_size + t % sh.page_size;
+        else flag_error(pl.hdr + kErrWord, kErrPage);
+        s_row[f - chunk_lo] = row;
+      }
+    };
+    constexpr int kFirst = NT > (kNarrowStages - 1) * TILE ? NT : (kNarrowStages - 1) * TILE;
+    const int64_t early = chunk_hi < chunk_lo + kFirst ? chunk_hi : chunk_lo + kFirst;
+    resolve(chunk_lo, early);
+    __syncthreads();
+    int64_t ld = chunk_lo, ld_end = locate(chunk_lo).end;
+    auto load_next = [&](int stage) {
+      if (ld >= chunk_hi) return;
+      if (ld >= ld_end) ld_end = locate(ld).end;
+      int64_t e = ld + TILE;
+      if (ld_end < e) e = ld_end;
+      if (chunk_hi < e) e = chunk_hi;
+      const int n = (int)(e - ld), g = (int)(ld / Treq), rbase = (int)(ld - chunk_lo);
+      __nv_bfloat16* sk = s_kv + (size_t)stage * 2 * STAGE;
+      __nv_bfloat16* sv = sk + STAGE;
+#pragma unroll 4
+      for (int idx = tid; idx < TILE * HG * CH; idx += NT) {
+        const int r = idx / (HG * CH), rem = idx % (HG * CH), hh = rem / CH, c = rem % CH;
+        const int row = r < n ? s_row[rbase + r] : -1;
+        const int off = (r * HG + hh) * D + ((c ^ (r & 7)) << 3);
+        const int64_t src = row >= 0 ? ((int64_t)row * sh.Hkv + g * HG + hh) * D + c * 8 : 0;
+        const int bytes = row >= 0 ? 16 : 0;
+        tc::cp_async16(tc::smem_u32(sk + off), kv_k + src, bytes);
+        tc::cp_async16(tc::smem_u32(sv + off), kv_v + src, bytes);
+      }
+      ld = e;
+    };
+    int n_tiles = 0;
+    for (int64_t f = chunk_lo, se = ld_end; f < chunk_hi; ++n_tiles) {
+      if (f >= se) se = locate(f).end;
+      int64_t e = f + TILE;
+      if (se < e) e = se;
+      f = chunk_hi < e ? chunk_hi : e;
+    }
+#pragma unroll
+    for (int st = 0; st < kNarrowStages - 1; ++st) {
+      if (st < n_tiles) load_next(st);
+      tc::cp_async_commit();
+    }
+    resolve(early, chunk_hi);
+    __syncthreads();
+    for (int tile = 0; tile < n_tiles; ++tile) {
+      if (tile + kNarrowStages - 1 < n_tiles) load_next((tile + kNarrowStages - 1) % kNarrowStages);
+      tc::cp_async_commit();
+      if (!open || pos >= cur.end) {
+        cur = locate(pos);
+        begin(cur);
+        open = true;
+      }
+      int64_t e64 = pos + TILE;
+      if (cur.end < e64) e64 = cur.end;
+      if (chunk_hi < e64) e64 = chunk_hi;
+      const int n = (int)(e64 - pos), rbase = (int)(pos - chunk_lo);
+      const int p0 = (int)(pos - (cur.end - (s_pre[cur.b + 1] - s_pre[cur.b])));  // own position
+      tc::cp_async_wait<kNarrowStages - 1>();
+      __syncthreads();
+      const __nv_bfloat16* sk = s_kv + (size_t)(tile % kNarrowStages) * 2 * STAGE;
+      const __nv_bfloat16* sv = sk + STAGE;
+      float sacc[2][NT8][4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int nt = 0; nt < NT8; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sacc[c][nt][i] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
+        const int chunk = 2 * ks + (lane >> 4);
+        uint32_t a[4];
+        ldsm_x4(tc::smem_u32(sk + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
+#pragma unroll
+        for (int nt = 0; nt < NT8; ++nt) mma_16816(sacc[ks & 1][nt], a, qb[nt][ks][0], qb[nt][ks][1]);
+      }
+      const bool v0 = g8 < n && s_row[rbase + g8] >= 0;
+      const bool v1 = g8 + 8 < n && s_row[rbase + g8 + 8] >= 0;
+      uint32_t pb[NT8][2];
+#pragma unroll
+      for (int nt = 0; nt < NT8; ++nt) {
+        float x[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const bool v = (i < 2 ? v0 : v1) && p0 + g8 + (i < 2 ? 0 : 8) < lim[nt][i & 1];
+          x[i] = v ? (sacc[0][nt][i] + sacc[1][nt][i]) * scale_log2 : kNegInf;
+        }
+        float al[2], p[4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float mx = fmaxf(x[e], x[e + 2]);
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          const float mn = fmaxf(m_h[nt][e], mx);
+          al[e] = mn == kNegInf ? 1.f : exp2f(m_h[nt][e] - mn);
+          p[e] = x[e] == kNegInf ? 0.f : ex2(x[e] - mn);
+          p[e + 2] = x[e + 2] == kNegInf ? 0.f : ex2(x[e + 2] - mn);
+          m_h[nt][e] = mn;
+        }
+        l_h[nt][0] = l_h[nt][0] * al[0] + (p[0] + p[2]);
+        l_h[nt][1] = l_h[nt][1] * al[1] + (p[1] + p[3]);
+        // rounded to bf16 for the second product only
+        const uint32_t lo2 = pack_bf16(p[0], p[1]), hi2 = pack_bf16(p[2], p[3]);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          o[nt][mt][0] *= al[0];
+          o[nt][mt][1] *= al[1];
+          o[nt][mt][2] *= al[0];
+          o[nt][mt][3] *= al[1];
+        }
+        pb[nt][0] = movmatrix_t(lo2);
+        pb[nt][1] = movmatrix_t(hi2);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        const int row = (lane & 7) + ((lane >> 4) << 3);
+        const int chunk = 2 * mt + ((lane >> 3) & 1);
+        uint32_t a[4];
+        ldsm_x4_t(tc::smem_u32(sv + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
+#pragma unroll
+        for (int nt = 0; nt < NT8; ++nt) mma_16816(o[nt][mt], a, pb[nt][0], pb[nt][1]);
+      }
+      __syncthreads();
+      pos += n;
+      if (pos == cur.end || pos == hi) {
+        finish(cur);
+        open = false;
+      }
+    }
+    tc::cp_async_wait<0>();
+    __syncthreads();
+  }
+  if (!wait_first) pdl_wait();
+}
+
+// ----------------------------------------------------------------- merge ---
+// A warp a (request, query token, head).  The parts: the prefix item's partials
+// (every CTA whose range touches the item; two softmax groups each when the
+// item has one row block), and the own tokens' partials of either kernel.
+template <int D>
+__global__ void __launch_bounds__(128)
+k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restrict__ wo,
+               const float2* __restrict__ nml, const float* __restrict__ no,
+               __nv_bfloat16* __restrict__ out, float* __restrict__ lse, PrefixShape sh) {
+  constexpr int V = D / 32;  // output values a lane
+  const float kNegInf = __int_as_float(0xff800000);
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  pdl_launch_dependents();
+  pdl_wait();
+  if (row >= (int64_t)sh.B * sh.Nq * sh.Hq) return;
+  const int h = (int)(row % sh.Hq), b = (int)(row / sh.Hq / sh.Nq), qi = (int)(row / sh.Hq % sh.Nq);
+  const int head = h / sh.G, r = qi * sh.G + h % sh.G;  // row of the request for this KV head
+
+  // up to three runs of partials: base row, stride a CTA, CTAs, groups a CTA
+  int64_t base[2] = {0, 0};
+  int count[2] = {0, 0}, halves[2] = {1, 1}, apart[2] = {0, 0};
+  const int U = pl.hdr[kUnits], slots_head = pl.hdr[kSlots];
+  const int64_t total = (int64_t)U * sh.Hkv;
+  const int wgrid = used_grid(total, sh.wide_grid, kWideLeast);
+  auto wide_run = [&](int k, int item, int x) {
+    const Item it = pl.items[item];
+    const int next = pl.items[item + 1].unit0;
+    const int64_t u0 = (int64_t)head * U + it.unit0, u1 = (int64_t)head * U + next;
+    if (u1 <= u0) return;
+    const int c0 = range_owner(u0, total, wgrid), c1 = range_owner(u1 - 1, total, wgrid);
+    base[k] = (int64_t)head * slots_head + it.slot0 + (int64_t)kItemRows * c0 + x;
+    count[k] = c1 - c0 + 1;
+    halves[k] = item_halves(it.nrows);
+    apart[k] = it.nrows;
+  };
+  const int pitem = pl.pitem[b];
+  if (pitem >= 0) {
+    const int x = pl.prow[b] + r - pl.items[pitem].row0;  // row within the group
+    wide_run(0, pitem + x / kItemRows, x % kItemRows);
+  }
+  const int n_own = pl.npre[b + 1] - pl.npre[b];
+  const float2* ml1 = wml;
+  const float* o1 = wo;
+  int stride1 = kItemRows;
+  if (n_own > 0) {
+    if (sh.narrow) {
+      const int Treq = pl.hdr[kTokens];
+      const int64_t T = (int64_t)Treq * (sh.Hkv / sh.hg);
+      const int ngrid = used_grid(T, sh.narrow_grid, kNarrowLeast);
+      const int g = head / sh.hg;
+      const int64_t f0 = (int64_t)g * Treq + pl.npre[b], f1 = f0 + n_own;
+      const int c0 = range_owner(f0, T, ngrid), c1 = range_owner(f1 - 1, T, ngrid);
+      base[1] = (((int64_t)c0 + (int64_t)g * sh.B + b) * sh.hg + head % sh.hg) * sh.R + r;
+      count[1] = c1 - c0 + 1;
+      stride1 = sh.hg * sh.R;
+      ml1 = nml;
+      o1 = no;
+    } else {
+      wide_run(1, pl.oitem[b] + r / kItemRows, r % kItemRows);
+    }
+  }
+  const int n0 = count[0] * halves[0], n1 = count[1] * halves[1], n = n0 + n1;
+  auto at = [&](int j) -> int64_t {
+    if (j < n0) return base[0] + (int64_t)(j / halves[0]) * kItemRows + (j % halves[0]) * apart[0];
+    j -= n0;
+    return base[1] + (int64_t)(j / halves[1]) * stride1 + (j % halves[1]) * apart[1];
+  };
+  float M = kNegInf;
+  for (int j = lane; j < n; j += 32) {
+    const float2 e = __ldcg((j < n0 ? wml : ml1) + at(j));
+    if (e.y != 0.f) M = fmaxf(M, e.x);
+  }
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+  float L = 0.f, acc[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) acc[v] = 0.f;
+  for (int j0 = 0; j0 < n; j0 += 32) {
+    float wgt = 0.f;
+    int64_t my = 0;
+    if (j0 + lane < n) {
+      my = at(j0 + lane);
+      const float2 e = __ldcg((j0 + lane < n0 ? wml : ml1) + my);
+      if (e.y != 0.f) {
+        wgt = exp2f(e.x - M);
+        L += wgt * e.y;
+      }
+    }
+    const int m = n - j0 < 32 ? n - j0 : 32;
+    for (int j = 0; j < m; ++j) {
+      const float f = __shfl_sync(0xffffffffu, wgt, j);
+      const int64_t p = __shfl_sync(0xffffffffu, my, j);
+      if (f == 0.f) continue;
+      const float* src = (j0 + j < n0 ? wo : o1) + p * D + lane * V;
+#pragma unroll
+      for (int v = 0; v < V; v += 2) {
+        const float2 x = __ldcg(reinterpret_cast<const float2*>(src + v));
+        acc[v] += f * x.x;
+        acc[v + 1] += f * x.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int s = 16; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  __nv_bfloat16* dst = out + row * D + lane * V;
+#pragma unroll
+  for (int v = 0; v < V; v += 2)
+    *reinterpret_cast<__nv_bfloat162*>(dst + v) =
+        __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+  if (lse && lane == 0)
+    lse[row] = L == 0.f ? kNegInf : (M + log2f(L)) * 0.6931471805599453f;
+}
+
+// ------------------------------------------------------------------ host ---
+
+PrefixShape prefix_shape(const pks_prefix_args& a) {
+  PrefixShape sh{};
+  sh.B = a.B;
+  sh.Hq = a.Hq;
+  sh.Hkv = a.Hkv;
+  sh.G = a.Hq / a.Hkv;
+  sh.Nq = a.n_queries > 1 ? a.n_queries : 1;
+  sh.R = sh.Nq * sh.G;
+  sh.page_size = a.page_size;
+  sh.max_pages = a.max_pages;
+  sh.num_pages = a.num_pages;
+  sh.causal = a.causal;
+  sh.narrow = sh.R <= kNarrowRows;
+  sh.hg = attn_heads_per_cta(a.Hkv);
+  sh.wide_grid = device_sm_count();
+  // shared memory holds one narrow CTA of eight heads an SM, more of fewer
+  const size_t stage = (size_t)2 * kNarrowTile * sh.hg * a.D * sizeof(__nv_bfloat16);
+  const size_t smem = kNarrowStages * stage + sizeof(int32_t) * (size_t)(kNarrowRowCap + a.B + 1);
+  int per_sm = (int)((size_t)(227 * 1024) / (smem + 1024));
+  if (per_sm > 4) per_sm = 4;
+  sh.narrow_grid = device_sm_count() * (per_sm < 1 ? 1 : per_sm);
+  return sh;
+}
+
+PlanPtrs plan_ptrs(void* ws, const PrefixLayout& L) {
+  uint8_t* p = static_cast<uint8_t*>(ws);
+  auto i32 = [&](size_t off) { return reinterpret_cast<int32_t*>(p + off); };
+  PlanPtrs pl;
+  pl.hdr = i32(L.hdr);
+  pl.lens = i32(L.per_request);
+  const size_t step = L.per_request_step / sizeof(int32_t);
+  pl.eq = pl.lens + step;
+  pl.first = pl.eq + step;
+  pl.lead = pl.first + step;
+  pl.start = pl.lead + step;
+  pl.pitem = pl.start + step;
+  pl.prow = pl.pitem + step;
+  pl.oitem = pl.prow + step;
+  pl.order = pl.oitem + step;
+  pl.npre = pl.order + step;
+  pl.items = reinterpret_cast<Item*>(p + L.items);
+  return pl;
+}
+
+// Dynamic shared memory limit of one kernel on the current device: raised once
+// to `bytes` (the same for every call), outside any stream.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, bool (&done)[64]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done[dev] = true;
+  return e;
+}
+
+template <int D>
+cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const PrefixShape& sh,
+                        float scale_log2, cudaStream_t s) {
+  static bool done[64] = {false};
+  cudaError_t e = allow_smem(k_prefix_wide<D>, Wide<D>::kSmem, done);
+  if (e != cudaSuccess) return e;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  return launch_ex(k_prefix_wide<D>, dim3(sh.wide_grid), dim3(kWideThreads), Wide<D>::kSmem, s,
+                   /*pdl=*/true, /*coop=*/false, a.block_table,
+                   static_cast<const __nv_bfloat16*>(a.q),
+                   static_cast<const __nv_bfloat16*>(a.kv_k),
+                   static_cast<const __nv_bfloat16*>(a.kv_v), plan_ptrs(ws, L),
+                   reinterpret_cast<float2*>(ws + L.wide_ml),
+                   reinterpret_cast<float*>(ws + L.wide_o), sh, scale_log2,
+                   a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles);
+}
+
+template <int D, int HG, int NT8>
+cudaError_t launch_narrow(const pks_prefix_args& a, const PrefixLayout& L, const PrefixShape& sh,
+                          float scale_log2, bool wait_first, cudaStream_t s) {
+  static bool done[64] = {false};
+  auto kern = k_prefix_narrow<D, HG, NT8>;
+  constexpr size_t kStages = (size_t)kNarrowStages * 2 * kNarrowTile * HG * D * sizeof(__nv_bfloat16);
+  cudaError_t e = allow_smem(kern, kStages + sizeof(int32_t) * (kNarrowRowCap + kMaxB + 1), done);
+  if (e != cudaSuccess) return e;
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const size_t smem = kStages + sizeof(int32_t) * (size_t)(kNarrowRowCap + a.B + 1);
+  return launch_ex(kern, dim3(sh.narrow_grid), dim3(HG * 32), smem, s, /*pdl=*/true,
+                   /*coop=*/false, a.block_table, static_cast<const __nv_bfloat16*>(a.q),
+                   static_cast<const __nv_bfloat16*>(a.kv_k),
+                   static_cast<const __nv_bfloat16*>(a.kv_v), plan_ptrs(ws, L),
+                   reinterpret_cast<float2*>(ws + L.narrow_ml),
+                   reinterpret_cast<float*>(ws + L.narrow_o), sh, scale_log2,
+                   wait_first ? 1 : 0);
+}
+
+template <int D>
+cudaError_t launch_parts(const pks_prefix_args& a, const PrefixLayout& L, const PrefixShape& sh,
+                         cudaStream_t s) {
+  const float scale = a.sm_scale > 0.f ? a.sm_scale : 1.f / sqrtf((float)D);
+  const float scale_log2 = scale * 1.4426950408889634f;
+  const bool wide = a.prefix_group || !sh.narrow;
+  cudaError_t e = cudaSuccess;
+  if (wide) e = launch_wide<D>(a, L, sh, scale_log2, s);
+  if (e != cudaSuccess) return e;
+  if (sh.narrow) {
+#define PKS_NARROW(HG_)                                                                    \
+  if (sh.hg == HG_)                                                                        \
+    e = sh.R <= 8 ? launch_narrow<D, HG_, 1>(a, L, sh, scale_log2, !wide, s)               \
+                  : launch_narrow<D, HG_, 2>(a, L, sh, scale_log2, !wide, s);
+    PKS_NARROW(1)
+    PKS_NARROW(2)
+    PKS_NARROW(4)
+    PKS_NARROW(8)
+#undef PKS_NARROW
+    if (e != cudaSuccess) return e;
+  }
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  const int64_t rows = (int64_t)sh.B * sh.Nq * sh.Hq;
+  return launch_ex(k_prefix_merge<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s,
+                   /*pdl=*/true, /*coop=*/false, plan_ptrs(ws, L),
+                   reinterpret_cast<const float2*>(ws + L.wide_ml),
+                   reinterpret_cast<const float*>(ws + L.wide_o),
+                   reinterpret_cast<const float2*>(ws + L.narrow_ml),
+                   reinterpret_cast<const float*>(ws + L.narrow_o),
+                   static_cast<__nv_bfloat16*>(a.out), a.lse, sh);
+}
+
+}  // namespace
+
+PrefixLayout prefix_layout(const pks_prefix_args& a) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  const PrefixShape sh = prefix_shape(a);
+  const int64_t B = sh.B, R = sh.R;
+  PrefixLayout L{};
+  size_t off = 0;
+  L.hdr = off;
+  off += 256;
+  L.per_request = off;
+  L.per_request_step = up(sizeof(int32_t) * (size_t)(B + 1));
+  off += 10 * L.per_request_step;
+  // items: prefix rows in blocks of 256, each group with a remainder (a group
+  // has two members at least); own tokens when the narrow kernel leaves them
+  const bool groups = a.prefix_group != nullptr;
+  const int64_t own_items = sh.narrow ? 0 : B * ((R + kItemRows - 1) / kItemRows);
+  L.items = off;
+  off = up(off + sizeof(Item) * (size_t)((groups ? B * R / kItemRows + B / 2 : 0) + own_items + 1));
+  // partial rows of one head: an item of up to 128 rows takes twice its rows
+  const int64_t pref = !groups ? 0 : B * R + (B * R < kRows * (B / 2) ? B * R : kRows * (B / 2));
+  const int64_t tail = R % kItemRows;
+  const int64_t own = sh.narrow ? 0 : B * (R - tail + (tail <= kRows ? 2 * tail : tail));
+  const size_t wide = groups || !sh.narrow
+                          ? (size_t)(sh.Hkv * (pref + own) + (int64_t)kItemRows * sh.wide_grid) : 0;
+  L.wide_ml = off;
+  off = up(off + sizeof(float2) * wide);
+  L.wide_o = off;
+  off = up(off + sizeof(float) * wide * (size_t)a.D);
+  const size_t narrow = sh.narrow ? (size_t)((sh.narrow_grid + (int64_t)(sh.Hkv / sh.hg) * B) *
+                                             sh.hg * R) : 0;
+  L.narrow_ml = off;
+  off = up(off + sizeof(float2) * narrow);
+  L.narrow_o = off;
+  off = up(off + sizeof(float) * narrow * (size_t)a.D);
+  L.total = off;
+  return L;
+}
+
+cudaError_t launch_prefix_plan(const pks_prefix_args& a, const PrefixLayout& L, cudaStream_t s) {
+  static bool done[64] = {false};
+  cudaError_t e = allow_smem(k_prefix_plan, 4 * sizeof(int32_t) * kMaxB, done);
+  if (e != cudaSuccess) return e;
+  const PrefixShape sh = prefix_shape(a);
+  return launch_ex(k_prefix_plan, dim3(a.prefix_group ? a.B : 1), dim3(kPlanThreads),
+                   4 * sizeof(int32_t) * (size_t)a.B, s, /*pdl=*/true, /*coop=*/false, a.seq_lens,
+                   a.block_table, a.prefix_group, plan_ptrs(a.workspace, L), sh);
+}
+
+cudaError_t launch_prefix_attention(const pks_prefix_args& a, const PrefixLayout& L,
+                                    cudaStream_t s) {
+  const PrefixShape sh = prefix_shape(a);
+  return a.D == 64 ? launch_parts<64>(a, L, sh, s) : launch_parts<128>(a, L, sh, s);
+}
+
+}  // namespace pks

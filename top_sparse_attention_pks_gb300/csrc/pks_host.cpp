@@ -697,6 +697,85 @@ pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_str
   return PKS_OK;
 }
 
+// ---------------------------------------------------- shared prefixes ---
+
+namespace {
+pks_status prefix_check(const pks_prefix_args* a) {
+  if (!a) return PKS_ERR_INVALID;
+  if (a->B < 0 || a->Hq < 1 || a->Hkv < 1 || a->D < 1 || a->page_size < 1 || a->max_pages < 1 ||
+      a->num_pages < 1 || a->n_queries < 0 || a->causal < 0 || a->causal > 1 ||
+      a->wait_limit < 0 || a->reserved != 0 || !(a->sm_scale >= 0.f) ||
+      std::isinf(a->sm_scale) || a->Hq % a->Hkv != 0)
+    return PKS_ERR_INVALID;
+  if (a->D != 64 && a->D != 128) return PKS_ERR_UNSUPPORTED;
+  if (a->Hq / a->Hkv > 16 || a->Hq > 4096 || a->n_queries > pks::kPrefixMaxQueries)
+    return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)a->B * std::max(1, a->n_queries) > pks::kMaxB) return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)a->num_pages * a->page_size > INT32_MAX) return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)a->max_pages * a->page_size > pks::kMaxLen) return PKS_ERR_UNSUPPORTED;
+  return PKS_OK;
+}
+pks_status prefix_check_workspace(const pks_prefix_args* a, const pks::PrefixLayout& L) {
+  if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & (pks::kAlign - 1)) != 0 ||
+      a->workspace_bytes < L.total)
+    return PKS_ERR_WORKSPACE;
+  return PKS_OK;
+}
+}  // namespace
+
+pks_status pks_prefix_workspace_size(const pks_prefix_args* args, size_t* bytes) {
+  if (!bytes) return PKS_ERR_INVALID;
+  const pks_status st = prefix_check(args);
+  if (st != PKS_OK) return st;
+  *bytes = pks::prefix_layout(*args).total;
+  return PKS_OK;
+}
+
+pks_status pks_prefix_plan(const pks_prefix_args* args, pks_stream stream) {
+  pks_status st = prefix_check(args);
+  if (st != PKS_OK) return st;
+  if (args->B > 0 && (!args->seq_lens || !args->block_table)) return PKS_ERR_INVALID;
+  const pks::PrefixLayout L = pks::prefix_layout(*args);
+  if ((st = prefix_check_workspace(args, L)) != PKS_OK) return st;
+  if (args->B == 0) return PKS_OK;
+  return pks::from_cuda(
+      pks::launch_prefix_plan(*args, L, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_prefix_attention(const pks_prefix_args* args, pks_stream stream) {
+  pks_status st = prefix_check(args);
+  if (st != PKS_OK) return st;
+  if (args->B > 0) {
+    if (!args->block_table || !args->q || !args->kv_k || !args->kv_v || !args->out)
+      return PKS_ERR_INVALID;
+    if (!pks::aligned16(args->q) || !pks::aligned16(args->kv_k) || !pks::aligned16(args->kv_v) ||
+        !pks::aligned16(args->out))
+      return PKS_ERR_INVALID;
+  }
+  const pks::PrefixLayout L = pks::prefix_layout(*args);
+  if ((st = prefix_check_workspace(args, L)) != PKS_OK) return st;
+  if (args->B == 0) return PKS_OK;
+  return pks::from_cuda(
+      pks::launch_prefix_attention(*args, L, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_prefix_device_error(const pks_prefix_args* args, int32_t* code,
+                                   pks_stream stream) {
+  if (!code) return PKS_ERR_INVALID;
+  pks_status st = prefix_check(args);
+  if (st != PKS_OK) return st;
+  if ((st = prefix_check_workspace(args, pks::prefix_layout(*args))) != PKS_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int32_t* dev = static_cast<int32_t*>(args->workspace);
+  int32_t host = 0;
+  cudaError_t e = cudaMemcpyAsync(&host, dev, sizeof(int32_t), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(dev, 0, sizeof(int32_t), s);
+  if (e != cudaSuccess) return PKS_ERR_CUDA;
+  *code = host;
+  return PKS_OK;
+}
+
 // --------------------------------------------------------------- pages ---
 
 namespace {

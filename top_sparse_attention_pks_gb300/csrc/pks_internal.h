@@ -172,6 +172,17 @@ cudaError_t launch_residency(int32_t* state, int32_t num_pages, int32_t capacity
                              size_t off_flag, size_t off_slot_flag, size_t off_vict,
                              cudaStream_t s);
 
+// ---- attention over shared prefixes (k_prefix.cu): byte offsets inside the
+// workspace; the header's first word is the device error word
+struct PrefixLayout {
+  size_t hdr, per_request, per_request_step, items, wide_ml, wide_o, narrow_ml, narrow_o, total;
+};
+constexpr int kPrefixMaxQueries = 64;
+PrefixLayout prefix_layout(const pks_prefix_args& a);
+cudaError_t launch_prefix_plan(const pks_prefix_args& a, const PrefixLayout& L, cudaStream_t s);
+cudaError_t launch_prefix_attention(const pks_prefix_args& a, const PrefixLayout& L,
+                                    cudaStream_t s);
+
 // ---- page table on the device (k_pages.cu): byte offsets inside the state
 struct PagesLayout {
   size_t ref, free_map, cnt, last, stamp, zeroed, moves, taken, total;

@@ -250,6 +250,57 @@ class MlaDecodeStep:
         return self.out, self.topk_idx
 
 
+class PrefixAttention:
+    """Dense decode attention of a batch whose requests alias the pages of shared
+    prefixes (``pks_prefix_plan`` and ``pks_prefix_attention``): a prefix's K/V
+    take part once for all requests of its group.  q [B, Hq, D] or
+    [B, Nq, Hq, D] (query tokens at the end of each request, ``causal`` among
+    themselves), kv_k / kv_v [num_pages, P, Hkv, D] (bf16), prefix_group [B]
+    (int32, negative: none) or None.  Owns ``out``, ``lse`` (when asked for) and
+    the workspace.
+
+    Calling the object plans and attends.  ``plan`` alone is needed whenever
+    lengths, table or groups have changed; ``attend`` serves further layers,
+    ``attend(q, kv_k, kv_v)`` with tensors of the same shapes."""
+
+    def __init__(self, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
+                 causal: bool = False, sm_scale: float = 0.0, lse: bool = False,
+                 wait_limit: int = 0):
+        dev = q.device
+        self.out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+        self.lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
+        kw = dict(seq_lens=seq_lens, block_table=block_table, q=q, kv_k=kv_k, kv_v=kv_v,
+                  prefix_group=prefix_group, causal=causal, sm_scale=sm_scale, out=self.out,
+                  lse=self.lse, wait_limit=wait_limit)
+        nbytes = pks.pks_prefix_workspace_size(pks.make_prefix_args(**kw))
+        self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+        self.workspace[:256].zero_()
+        self.args = pks.make_prefix_args(workspace=self.workspace, **kw)
+        self._keep = (seq_lens, block_table, prefix_group, q, kv_k, kv_v)
+
+    def plan(self, stream=None):
+        pks.pks_prefix_plan(self.args, stream)
+
+    def attend(self, q=None, kv_k=None, kv_v=None, stream=None):
+        for name, t in (("q", q), ("kv_k", kv_k), ("kv_v", kv_v)):
+            if t is None:
+                continue
+            was = self._keep[("q", "kv_k", "kv_v").index(name) + 3]
+            if tuple(t.shape) != tuple(was.shape) or t.device != was.device:
+                raise ValueError(f"{name} must have the shape and device it was planned with")
+            setattr(self.args, name, pks._dptr(t, torch.bfloat16, name))
+        pks.pks_prefix_attention(self.args, stream)
+        return self.out
+
+    def __call__(self, stream=None):
+        pks.pks_prefix_plan(self.args, stream)
+        pks.pks_prefix_attention(self.args, stream)
+        return self.out
+
+    def device_error(self, stream=None) -> int:
+        return pks.pks_prefix_device_error(self.args, stream)
+
+
 class PageTable:
     """A block table whose page sharing is kept on the device (``pks_pages_*``):
     holders of every page and the free pages.  ``seq_lens`` [B] and

@@ -66,6 +66,20 @@ class pks_mla_args(ctypes.Structure):
     ]
 
 
+class pks_prefix_args(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("n_queries", ctypes.c_int32),
+        ("causal", ctypes.c_int32), ("wait_limit", ctypes.c_int32),
+        ("sm_scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+        ("seq_lens", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+        ("prefix_group", ctypes.c_void_p), ("q", ctypes.c_void_p), ("kv_k", ctypes.c_void_p),
+        ("kv_v", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 PKS_PAGES_MAX_POOLS = 8
 
 
@@ -165,6 +179,15 @@ def _declare(L):
     L.pks_residency_update.argtypes = [_P, _I32, _I32, _I32, _I32, _I32, _I32, _P, _P, _P, _P,
                                        _P]
     L.pks_residency_update.restype = _ST
+    _PX = ctypes.POINTER(pks_prefix_args)
+    L.pks_prefix_workspace_size.argtypes = [_PX, ctypes.POINTER(ctypes.c_size_t)]
+    L.pks_prefix_workspace_size.restype = _ST
+    L.pks_prefix_plan.argtypes = [_PX, _P]
+    L.pks_prefix_plan.restype = _ST
+    L.pks_prefix_attention.argtypes = [_PX, _P]
+    L.pks_prefix_attention.restype = _ST
+    L.pks_prefix_device_error.argtypes = [_PX, ctypes.POINTER(ctypes.c_int32), _P]
+    L.pks_prefix_device_error.restype = _ST
     _PG = ctypes.POINTER(pks_pages_args)
     L.pks_pages_state_bytes.argtypes = [_I32, ctypes.POINTER(ctypes.c_size_t)]
     L.pks_pages_state_bytes.restype = _ST
@@ -621,6 +644,77 @@ def pks_mla_device_error(args: pks_mla_args, stream=None) -> int:
     code = ctypes.c_int32()
     _check(lib().pks_mla_device_error(ctypes.byref(args), ctypes.byref(code), _stream(stream)),
            "pks_mla_device_error")
+    return code.value
+
+
+# ------------------------------------------------------- shared prefixes
+
+def make_prefix_args(*, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
+                     causal: bool = False, sm_scale: float = 0.0, out=None, lse=None,
+                     workspace=None, num_pages: Optional[int] = None,
+                     wait_limit: int = 0) -> pks_prefix_args:
+    """Fill a ``pks_prefix_args``: q [B, Hq, D] or [B, Nq, Hq, D] (``out`` alike,
+    ``lse`` without the last dimension), kv_k / kv_v [num_pages, page_size, Hkv, D],
+    prefix_group [B] or None."""
+    a = pks_prefix_args()
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, D] or [B, Nq, Hq, D]")
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    if q.dim() == 4:
+        if q.shape[1] < 1:
+            raise ValueError("q needs at least one query token")
+        a.n_queries = int(q.shape[1])
+    npages, P, Hkv, D2 = kv_k.shape
+    if D2 != D or tuple(kv_v.shape) != tuple(kv_k.shape):
+        raise ValueError("kv_k / kv_v / q shapes disagree")
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    if prefix_group is not None and tuple(prefix_group.shape) != (B,):
+        raise ValueError("prefix_group must be [B]")
+    if out is not None and tuple(out.shape) != tuple(q.shape):
+        raise ValueError("out must have q's shape")
+    if lse is not None and tuple(lse.shape) != tuple(q.shape[:-1]):
+        raise ValueError("lse must have q's shape without the last dimension")
+    a.B, a.Hq, a.Hkv, a.D = int(B), int(Hq), int(Hkv), int(D)
+    a.page_size, a.max_pages = int(P), int(block_table.shape[1])
+    a.num_pages = int(npages if num_pages is None else num_pages)
+    a.causal = 1 if causal else 0
+    a.sm_scale = float(sm_scale)
+    a.wait_limit = int(wait_limit)
+    a.seq_lens = _dptr(seq_lens, torch.int32, "seq_lens")
+    a.block_table = _dptr(block_table, torch.int32, "block_table")
+    a.prefix_group = _dptr(prefix_group, torch.int32, "prefix_group")
+    a.q = _dptr(q, torch.bfloat16, "q")
+    a.kv_k = _dptr(kv_k, torch.bfloat16, "kv_k")
+    a.kv_v = _dptr(kv_v, torch.bfloat16, "kv_v")
+    a.out = _dptr(out, torch.bfloat16, "out")
+    a.lse = _dptr(lse, torch.float32, "lse")
+    if workspace is not None:
+        a.workspace = _dptr(workspace, torch.uint8, "workspace")
+        a.workspace_bytes = workspace.numel()
+    return a
+
+
+def pks_prefix_workspace_size(args: pks_prefix_args) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().pks_prefix_workspace_size(ctypes.byref(args), ctypes.byref(n)),
+           "pks_prefix_workspace_size")
+    return n.value
+
+
+def pks_prefix_plan(args: pks_prefix_args, stream=None) -> None:
+    _check(lib().pks_prefix_plan(ctypes.byref(args), _stream(stream)), "pks_prefix_plan")
+
+
+def pks_prefix_attention(args: pks_prefix_args, stream=None) -> None:
+    _check(lib().pks_prefix_attention(ctypes.byref(args), _stream(stream)),
+           "pks_prefix_attention")
+
+
+def pks_prefix_device_error(args: pks_prefix_args, stream=None) -> int:
+    code = ctypes.c_int32()
+    _check(lib().pks_prefix_device_error(ctypes.byref(args), ctypes.byref(code),
+                                         _stream(stream)), "pks_prefix_device_error")
     return code.value
 
 
