@@ -110,6 +110,7 @@ def test_workspace_size():
     a.B, a.Hq, a.Hkv, a.D = 4096, 128, 8, 128
     rows = 4096 * 128
     assert pks.pks_prefix_workspace_size(a) < 5 * rows * (128 + 2) * 4
-    a.B = 0
+    a = args()
+    a.B = 0  # an empty batch is no error and launches nothing
     pks.pks_prefix_plan(a)
     pks.pks_prefix_attention(a)
