@@ -27,6 +27,8 @@
 // each item that its range touches, in slots that the merge derives from the
 // plan again.
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -78,6 +80,7 @@ struct PrefixShape {
   int causal;
   int narrow;      // own tokens by the narrow kernel
   int wide_grid, narrow_grid;
+  int box;         // rows of a TMA box (0: the page size has none)
   int hg;          // KV heads of a narrow CTA
 };
 
@@ -403,23 +406,29 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 // ------------------------------------------------------------------ wide ---
 // One CTA an SM, 512 threads:
 //   warps 0-3, 4-7   softmax groups 0 and 1: a thread a query row
-//   warp 8           issues the MMAs
-//   warps 9-12       load Q and the K/V tiles
-// An item with more than 128 rows gives each softmax group a row block of its
-// own and every tile goes to both; with 128 or fewer both groups hold the same
-// rows and take the tiles in turn, so that one group's softmax always runs
-// beside the other's products.  Per (tile, group) "job":
+//   warps 8, 9       issue the MMAs of groups 0 and 1
+//   warps 10-13      load Q and the K/V tiles
+// An item with more than 128 rows gives each group a row block of its own and
+// every tile goes to both; with 128 or fewer both groups hold the same rows and
+// take the tiles in turn, so that one group's softmax always runs beside the
+// other's products.  Per job (a tile of a group):
 //   S[128 x 128] = Q K^T        tcgen05.mma, fp32 in tensor memory
 //   P            = 2^(S c - m)  a thread a row, bf16 into S's columns
-//   O[128 x D]  += P V          tcgen05.mma, P from tensor memory
-// issued as S(0), S(1), PV(0), S(2), PV(1), ...: the tensor pipe runs them in
-// this order, so S(j + 2) may overwrite the P of job j, and the completion of
-// S(j + 2) implies that of PV(j).  K and V tiles share a ring of 32 KB slots
-// (K, V, K, V, ...) in 128-byte swizzled rows.  The running maximum moves only
-// when a tile exceeds it by more than 8 (log2 units).
+//   O[128 x D]  += P V          tcgen05.mma, P from tensor memory, in two halves
+//                               as the softmax delivers them
+// An issuing thread's products run in its order, so the next S may overwrite the
+// P before it, and the completion of S implies that of the P.V before it.  (One
+// thread for both groups left the tensor pipe idle through its waits: 40% active;
+// an issuer a group hides them behind the other's products.)
+// K and V tiles share a ring of slots (K, V, K, V, ...) of 128-byte swizzled
+// rows.  A tile of whole boxes (sh.box: the largest power of two up to 128 that
+// divides the page size, from 8, the swizzle's period) comes by TMA, the last
+// tile of a range and tiles of odd pages row by row with cp.async, which fills
+// what lies beyond the range with zeros.  The running maximum moves only when a
+// tile exceeds it by more than 8 (log2 units).
 
 constexpr int kWideThreads = 512;
-constexpr int kMmaWarp = 8, kLoadWarp = 9, kLoadThreads = 128;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadThreads = 128;
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
 
 template <int D>
@@ -434,18 +443,65 @@ struct Wide {
 };
 constexpr uint32_t kTmemS = 256;  // columns: O of the groups at 0 and 128, S at 256 and 384
 
+// One CTA's share of one item.
+struct Piece {
+  Item it;
+  int head, t_lo, nt;   // first tile and tiles
+  bool pair;            // two row blocks
+  int jobs0, jobs1;     // jobs of the softmax groups
+  int64_t slot;         // its first partial row
+  int64_t next;         // unit after it
+};
+// The piece that starts at unit u (a whole warp).
+__device__ __forceinline__ Piece piece_at(const PlanPtrs& pl, int64_t u, int64_t u_end, int U,
+                                          int n_items, int slots_head, int cta) {
+  Piece p;
+  p.head = (int)(u / U);
+  const int ur = (int)(u - (int64_t)p.head * U), lane = threadIdx.x & 31;
+  int item = 0;
+  for (int i0 = 0; i0 < n_items; i0 += 32) {  // the last item that starts at or before ur
+    const bool le = i0 + lane < n_items && pl.items[i0 + lane].unit0 <= ur;
+    const uint32_t m = __ballot_sync(0xffffffffu, le);
+    if (m) item = i0 + 31 - __clz(m);
+    if (m != 0xffffffffu) break;
+  }
+  p.it = pl.items[item];
+  const int w = item_weight(p.it.nrows);
+  const int64_t u0 = (int64_t)p.head * U + p.it.unit0;
+  const int64_t end = (int64_t)p.head * U + pl.items[item + 1].unit0;
+  p.next = u_end < end ? u_end : end;
+  p.t_lo = (int)((u - u0 + w - 1) / w);
+  p.nt = (int)((p.next - u0 + w - 1) / w) - p.t_lo;
+  p.pair = w == 2;
+  p.jobs1 = p.pair ? p.nt : p.nt / 2;
+  p.jobs0 = p.nt * w - p.jobs1;
+  p.slot = (int64_t)p.head * slots_head + p.it.slot0 + (int64_t)kItemRows * cta;
+  return p;
+}
+
+// registers of the softmax warpgroups and of the others: the launch's 512 x 128
+constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "the launch's registers");
+
 template <int D>
 __global__ void __launch_bounds__(kWideThreads, 1)
 k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
               const __nv_bfloat16* __restrict__ kv_k, const __nv_bfloat16* __restrict__ kv_v,
               PlanPtrs pl, float2* __restrict__ part_ml, float* __restrict__ part_o,
-              PrefixShape sh, float scale_log2, long long budget) {
+              PrefixShape sh, float scale_log2, long long budget,
+              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
   using W = Wide<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bar_full[W::kSlotsN], bar_free[W::kSlotsN], bar_q, bar_s[2],
-      bar_p[2], bar_o;
+  // bar_tma / bar_cp: a ring slot has landed, by either way of loading; bar_go: it
+  // may be filled by the second; bar_free:
+  // its products are done (both issuers'); bar_q / bar_qfree: the same for Q;
+  // bar_s[g]: S of group g's job; bar_p[g][h]: half h of its P is written;
+  // bar_turn[g]: the other issuer has issued its job's P.V and next S; bar_o[g]:
+  // every product of the group's piece; bar_drain[g]: on giving up
+  __shared__ __align__(8) uint64_t bar_tma[W::kSlotsN], bar_cp[W::kSlotsN], bar_go[W::kSlotsN],
+      bar_free[W::kSlotsN],      bar_q, bar_qfree, bar_s[2], bar_p[2][2], bar_turn[2], bar_o[2], bar_drain[2];
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort, s_item;
+  __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + 2 * W::kTileBytes;
@@ -454,15 +510,21 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   if (warp == 0) tc::tmem_alloc(&s_tmem, 512);
   if (tid == kMmaWarp * 32) {
     for (int i = 0; i < W::kSlotsN; ++i) {
-      tc::mbar_init(&bar_full[i], kLoadThreads / 32);
-      tc::mbar_init(&bar_free[i], 1);
+      tc::mbar_init(&bar_tma[i], 1);
+      tc::mbar_init(&bar_cp[i], kLoadThreads / 32);
+      tc::mbar_init(&bar_go[i], 1);
+      tc::mbar_init(&bar_free[i], 2);
     }
     tc::mbar_init(&bar_q, kLoadThreads / 32);
+    tc::mbar_init(&bar_qfree, 2);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar_s[i], 1);
-      tc::mbar_init(&bar_p[i], 4);
+      tc::mbar_init(&bar_p[i][0], 4);
+      tc::mbar_init(&bar_p[i][1], 4);
+      tc::mbar_init(&bar_turn[i], 1);
+      tc::mbar_init(&bar_o[i], 1);
+      tc::mbar_init(&bar_drain[i], 1);
     }
-    tc::mbar_init(&bar_o, 1);
     tc::mbar_init_fence();
     s_abort = 0;
   }
@@ -477,332 +539,453 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   const int64_t total = (int64_t)U * sh.Hkv;
   const int grid = used_grid(total, gridDim.x, kWideLeast);
   const int cta = blockIdx.x;
-  int64_t u = total > 0 && cta < grid ? range_lo(total, cta, grid) : 0;
-  const int64_t u_end = total > 0 && cta < grid ? range_lo(total, cta + 1, grid) : 0;
+  const bool part = total > 0 && cta < grid;
+  const int64_t u_begin = part ? range_lo(total, cta, grid) : 0;
+  const int64_t u_end = part ? range_lo(total, cta + 1, grid) : 0;
+  bool ok = true;
+  // a wait of the whole warp
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, budget)) != 0;
+  };
+  // tiles of a piece that come by TMA: those before the range's end, in pages of
+  // whole boxes, from a start that keeps every box in one page
+  auto tma_tiles = [&](const Piece& pc) -> int {
+    if (sh.box == 0 || pc.it.t0 % sh.box != 0) return 0;
+    const int full = (pc.it.t1 - pc.it.t0) / kTile - pc.t_lo;
+    return full < pc.nt ? full : pc.nt;
+  };
 
-  // counters of completed phases, the same in every role
-  uint32_t n_slot = 0, n_job[2] = {0, 0}, n_piece = 0;
-
-  while (u < u_end) {
-    // ---- the item of unit u and this CTA's tiles of it
-    const int head = (int)(u / U), ur = (int)(u - (int64_t)head * U);
-    for (int i = tid; i < n_items; i += kWideThreads)
-      if (pl.items[i].unit0 <= ur && ur < pl.items[i + 1].unit0) s_item = i;
-    __syncthreads();
-    const int item = s_item;
-    const Item it = pl.items[item];
-    const int next_unit = pl.items[item + 1].unit0;
-    const int w = item_weight(it.nrows);
-    const int64_t item_u0 = (int64_t)head * U + it.unit0;
-    const int64_t piece_end = u_end < (int64_t)head * U + next_unit ? u_end
-                                                                    : (int64_t)head * U + next_unit;
-    const int t_lo = (int)((u - item_u0 + w - 1) / w), t_hi = (int)((piece_end - item_u0 + w - 1) / w);
-    const int nt = t_hi - t_lo;
-    u = piece_end;
-    const int64_t slot = (int64_t)head * slots_head + it.slot0 + (int64_t)kItemRows * cta;
-    const bool pair = w == 2;
-    const int jobs = nt * w;
-    const int jobs1 = pair ? nt : nt / 2, jobs0 = jobs - jobs1;
-    auto job_group = [&](int j) { return j & 1; };
-    auto job_tile = [&](int j) { return pair ? j >> 1 : j; };
-    bool ok = true;
-
-    if (nt > 0 && warp == kMmaWarp) {
-      // ================= MMA issue =================
-      auto wait0 = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool r = lane == 0 ? tc::mbar_wait(bar, parity, &s_abort, budget) : true;
-        __syncwarp();
-        return __shfl_sync(0xffffffffu, r ? 1 : 0, 0) != 0;
-      };
-      auto issue_s = [&](int j) {
-        const int g = job_group(j), t = job_tile(j);
-        const uint32_t n = n_slot + 2 * t, s = n % W::kSlotsN;
-        const uint64_t dq = tc::desc_sw128(sQ + (pair ? g : 0) * W::kTileBytes, 16, 1024);
-        const uint64_t dk = tc::desc_sw128(sKV + s * W::kTileBytes, 16, 1024);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          const uint64_t off = (uint64_t)(((kk >> 2) * W::kBlkBytes + (kk & 3) * 32) >> 4);
-          tc::mma_ss(tmem + kTmemS + g * kTile, dq + off, dk + off,
-                     tc::idesc_bf16(kRows, kTile, false), kk > 0 ? 1u : 0u);
-        }
-        tc::mma_commit(&bar_s[g]);
-        if (!pair || g == 1) tc::mma_commit(&bar_free[s]);
-      };
-      auto issue_pv = [&](int j) {
-        const int g = job_group(j), t = job_tile(j);
-        const uint32_t n = n_slot + 2 * t + 1, s = n % W::kSlotsN;
-        const uint64_t dv = tc::desc_sw128(sKV + s * W::kTileBytes, W::kBlkBytes, 1024);
-#pragma unroll
-        for (int kk = 0; kk < kTile / 16; ++kk)
-          tc::mma_ts(tmem + g * 128, tmem + kTmemS + g * kTile + kk * 8,
-                     dv + (uint64_t)((kk * 16 * 128) >> 4), tc::idesc_bf16(kRows, D, true),
-                     (j > 1 || kk > 0) ? 1u : 0u);
-        if (!pair || g == 1) tc::mma_commit(&bar_free[s]);
-      };
-      auto slot_full = [&](int j, int v) -> bool {
-        const uint32_t n = n_slot + 2 * job_tile(j) + v;
-        return wait0(&bar_full[n % W::kSlotsN], (n / W::kSlotsN) & 1);
-      };
-      ok = wait0(&bar_q, n_piece & 1);
-      int issued = 0;
-      if (ok && (ok = slot_full(0, 0))) {
-        if (lane == 0) {
-          tc::fence_after();
-          issue_s(0);
-        }
-        issued = 1;
-        __syncwarp();
+  // Every role walks the same pieces and keeps its own count of the phases.
+  if (warp < kMmaWarp) {
+    // ================= softmax: a thread a query row =================
+    tc::setmaxnreg_inc<kSoftmaxRegs>();
+    const int g = warp >> 2;
+    const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lane_off + kTmemS + g * kTile, tO = tmem + lane_off + g * 128;
+    const uint64_t scale2 = tc::pack2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
+    uint32_t n_job = 0, n_piece = 0;
+    for (int64_t u = u_begin; u < u_end && ok;) {
+      const Piece pc = piece_at(pl, u, u_end, U, n_items, slots_head, cta);
+      u = pc.next;
+      const int x = (pc.pair ? g * kRows : 0) + (tid & (kRows - 1));  // row of the item
+      const int64_t row = pc.slot + (pc.pair ? x : g * pc.it.nrows + x);
+      const bool mine = x < pc.it.nrows;
+      if (pc.nt == 0) {
+        // a share that rounds to no tile still has its place among the partials
+        if (mine) part_ml[row] = make_float2(kNegInf, 0.f);
+        continue;
       }
-      for (int j = 0; j < jobs && ok; ++j) {
-        if (j + 1 < jobs) {
-          if (!(ok = slot_full(j + 1, 0))) break;
-          if (lane == 0) {
-            tc::fence_after();
-            issue_s(j + 1);
-          }
-          __syncwarp();
-        }
-        const int g = job_group(j);
-        if (!(ok = slot_full(j, 1))) break;
-        if (!(ok = wait0(&bar_p[g], (n_job[g] + (j >> 1)) & 1))) break;
-        if (lane == 0) {
-          tc::fence_after();
-          issue_pv(j);
-        }
-        __syncwarp();
-      }
-      // everything issued so far: O is complete, and nothing is in flight when
-      // the tensor memory is reused or freed
-      if (lane == 0) {
-        if (issued) tc::mma_commit(&bar_o);
-        if (!ok) {
-          flag_error(pl.hdr + kErrWord, kErrTimeout);
-          s_abort = 1;
-          if (issued) {
-            const long long t0 = clock64();
-            while (!tc::mbar_try_wait(&bar_o, n_piece & 1) && clock64() - t0 < kWaitCycles) {
+      const int my_jobs = g ? pc.jobs1 : pc.jobs0;
+      const bool idle = !__any_sync(0xffffffffu, mine);  // no row of this warp counts
+      // tokens this row sees
+      int limit = pc.it.t1;
+      if (pc.it.own && sh.causal && mine) limit = pc.it.t1 - sh.Nq + (pc.it.row0 + x) / sh.G + 1;
+      limit -= pc.it.t0 + pc.t_lo * kTile;
+      float m_run = kNegInf, l_run = 0.f;
+      for (int i = 0; i < my_jobs; ++i) {
+        if (!(ok = wait(&bar_s[g], n_job & 1))) break;
+        ++n_job;
+        tc::fence_after();
+        if (!idle) {
+          const int nv = limit - (pc.pair ? i : 2 * i + g) * kTile;  // valid columns
+          uint32_t s0[32], s1[32], s2[32], s3[32];
+          tc::tmem_ld32(tS, s0);
+          tc::tmem_ld32(tS + 32, s1);
+          tc::tmem_ld32(tS + 64, s2);
+          tc::tmem_ld32(tS + 96, s3);
+          tc::tmem_ld_wait(s0);
+          tc::tmem_ld_pin(s1);
+          tc::tmem_ld_pin(s2);
+          tc::tmem_ld_pin(s3);
+          if (__any_sync(0xffffffffu, nv < kTile)) {
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              if (k >= nv) s0[k] = 0xff800000u;
+              if (32 + k >= nv) s1[k] = 0xff800000u;
+              if (64 + k >= nv) s2[k] = 0xff800000u;
+              if (96 + k >= nv) s3[k] = 0xff800000u;
             }
           }
+          float mx0 = kNegInf, mx1 = kNegInf, mx2 = kNegInf, mx3 = kNegInf;
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            mx0 = tc::max3(mx0, __uint_as_float(s0[k]), __uint_as_float(s0[k + 1]));
+            mx1 = tc::max3(mx1, __uint_as_float(s1[k]), __uint_as_float(s1[k + 1]));
+            mx2 = tc::max3(mx2, __uint_as_float(s2[k]), __uint_as_float(s2[k + 1]));
+            mx3 = tc::max3(mx3, __uint_as_float(s3[k]), __uint_as_float(s3[k + 1]));
+          }
+          const float mx = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * scale_log2;
+          const bool move = mx > m_run + 8.f;  // also true on the first valid tile
+          const float m_new = move ? mx : m_run;
+          const float alpha = move ? exp2f(m_run - m_new) : 1.f;
+          m_run = m_new;
+          // the weights; P is rounded to bf16 for the second product (each by
+          // half a step, 2^-8 of itself, at most) while the sum keeps the fp32
+          // values, so that lse carries no such rounding
+          const float neg = m_new == kNegInf ? 0.f : -m_new;
+          const uint64_t neg2 = tc::pack2(__float_as_uint(neg), __float_as_uint(neg));
+          uint64_t sum_a = 0, sum_b = 0;
+          auto weights = [&](uint32_t (&sv)[32], uint32_t* pk) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              float a0, a1, b0, b1;
+              tc::unpack2(tc::fma2(tc::pack2(sv[k], sv[k + 1]), scale2, neg2), a0, a1);
+              tc::unpack2(tc::fma2(tc::pack2(sv[k + 2], sv[k + 3]), scale2, neg2), b0, b1);
+              a0 = ex2(a0);
+              a1 = ex2(a1);
+              b0 = ex2(b0);
+              b1 = ex2(b1);
+              sum_a = tc::add2(sum_a, tc::pack2(__float_as_uint(a0), __float_as_uint(a1)));
+              sum_b = tc::add2(sum_b, tc::pack2(__float_as_uint(b0), __float_as_uint(b1)));
+              const __nv_bfloat162 pa = __floats2bfloat162_rn(a0, a1);
+              const __nv_bfloat162 pb = __floats2bfloat162_rn(b0, b1);
+              pk[k / 2] = *reinterpret_cast<const uint32_t*>(&pa);
+              pk[k / 2 + 1] = *reinterpret_cast<const uint32_t*>(&pb);
+            }
+          };
+          // O of the jobs before is complete: S of this job was issued after it
+          if (__any_sync(0xffffffffu, move && i > 0)) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+              uint32_t ov[16];
+              tc::tmem_ld16(tO + c, ov);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) ov[k] = __float_as_uint(__uint_as_float(ov[k]) * alpha);
+              tc::tmem_st16(tO + c, ov);
+            }
+          }
+          // P takes the place of S columns, all of which are in registers
+          uint32_t pk[32];
+          weights(s0, pk);
+          weights(s1, pk + 16);
+          tc::tmem_st32(tS, pk);
+          tc::tmem_st_wait();
+          tc::fence_before();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar_p[g][0]);
+          weights(s2, pk);
+          weights(s3, pk + 16);
+          tc::tmem_st32(tS + 32, pk);
+          float la, lb, lc, ld;
+          tc::unpack2(sum_a, la, lb);
+          tc::unpack2(sum_b, lc, ld);
+          l_run = l_run * alpha + ((la + lb) + (lc + ld));
+          tc::tmem_st_wait();
+        } else {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bar_p[g][0]);
+        }
+        tc::fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bar_p[g][1]);
+      }
+      // ---- the piece's partial
+      if (my_jobs == 0) {
+        if (mine) part_ml[row] = make_float2(kNegInf, 0.f);
+        continue;
+      }
+      if (!ok || !(ok = wait(&bar_o[g], n_piece & 1))) break;
+      ++n_piece;
+      tc::fence_after();
+      if (idle) continue;
+      if (mine) part_ml[row] = make_float2(m_run, l_run);
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        uint32_t ov[32];
+        tc::tmem_ld32(tO + c, ov);
+        tc::tmem_ld_wait(ov);
+        if (mine) {
+          float* dst = part_o + row * D + c;
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<uint4*>(dst + k) = make_uint4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+        }
+      }
+      tc::fence_before();  // the reads of O come before the P that lets it be overwritten
+    }
+    if (!ok && lane == 0) {
+      flag_error(pl.hdr + kErrWord, kErrTimeout);
+      s_abort = 1;
+    }
+  } else {
+    tc::setmaxnreg_dec<kOtherRegs>();
+    if (warp < kLoadWarp) {
+      // ================= MMA issue of one group =================
+      const int g = warp - kMmaWarp;
+      const uint32_t tS = tmem + kTmemS + g * kTile, tO = tmem + g * 128;
+      uint32_t n_slot = 0, n_job = 0, n_piece = 0, n_turn = 0, ph_tma = 0, ph_cp = 0;
+      bool owed = false;
+      for (int64_t u = u_begin; u < u_end && ok;) {
+        const Piece pc = piece_at(pl, u, u_end, U, n_items, slots_head, cta);
+        u = pc.next;
+        if (pc.nt == 0) continue;
+        const int by_tma = tma_tiles(pc);
+        const int my_jobs = g ? pc.jobs1 : pc.jobs0;
+        // K of tile t has landed already (no wait, no phase taken)
+        auto ready = [&](int t, int tma) -> bool {
+          const uint32_t sl = (n_slot + 2 * t) % W::kSlotsN;
+          const bool r = t < tma ? tc::mbar_test_wait(&bar_tma[sl], (ph_tma >> sl) & 1)
+                                 : tc::mbar_test_wait(&bar_cp[sl], (ph_cp >> sl) & 1);
+          return __all_sync(0xffffffffu, r) != 0;
+        };
+        // a tile's K (v = 0) or V has landed
+        auto landed = [&](int t, int v) -> bool {
+          const uint32_t sl = (n_slot + 2 * t + v) % W::kSlotsN;
+          const bool tma = t < by_tma;
+          uint32_t& ph = tma ? ph_tma : ph_cp;
+          const bool r = wait(tma ? &bar_tma[sl] : &bar_cp[sl], (ph >> sl) & 1);
+          ph ^= 1u << sl;
+          return r;
+        };
+        // (the turn passes with four of S's steps to go: the other issuer's first
+        // product then queues behind them without a gap)
+        auto issue_s = [&](int t, bool last, uint64_t* pass) {
+          tc::fence_after();
+          if (tc::elect_one()) {
+            const uint32_t sl = (n_slot + 2 * t) % W::kSlotsN;
+            const uint64_t dq = tc::desc_sw128(sQ + (pc.pair ? g : 0) * W::kTileBytes, 16, 1024);
+            const uint64_t dk = tc::desc_sw128(sKV + sl * W::kTileBytes, 16, 1024);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint64_t off = (uint64_t)(((kk >> 2) * W::kBlkBytes + (kk & 3) * 32) >> 4);
+              tc::mma_ss(tS, dq + off, dk + off, tc::idesc_bf16(kRows, kTile, false),
+                         kk > 0 ? 1u : 0u);
+              if (kk == D / 16 - 4 && pass) tc::mbar_arrive(pass);
+            }
+            tc::mma_commit(&bar_s[g]);
+            tc::mma_commit(&bar_free[sl]);
+            if (last) tc::mma_commit(&bar_qfree);
+          }
+          __syncwarp();
+        };
+        // the other group's tile: waited for and released like an own one, so that
+        // no barrier completes two phases between two waits of a warp
+        auto skip = [&](int t) -> bool {
+          for (int v = 0; v < 2; ++v) {
+            if (!landed(t, v)) return false;
+            if (tc::elect_one()) tc::mbar_arrive(&bar_free[(n_slot + 2 * t + v) % W::kSlotsN]);
+            __syncwarp();
+          }
+          return true;
+        };
+        const int step = pc.pair ? 1 : 2, t0 = pc.pair ? 0 : g;
+        ok = wait(&bar_q, n_piece & 1);
+        if (my_jobs > 0 && ok) {
+          if (t0 == 1) ok = skip(0);
+          if (ok && (ok = landed(t0, 0))) issue_s(t0, my_jobs == 1, nullptr);
+        } else if (ok) {  // the one tile is the other group's
+          ok = skip(0);
+        }
+        for (int i = 0; i < my_jobs && ok; ++i, ++n_job) {
+          const int t = t0 + i * step, job = 2 * i + g;
+          if (!(ok = landed(t, 1))) break;
+          const uint32_t sl = (n_slot + 2 * t + 1) % W::kSlotsN;
+          const uint64_t dv = tc::desc_sw128(sKV + sl * W::kTileBytes, W::kBlkBytes, 1024);
+          if (!(ok = wait(&bar_p[g][0], n_job & 1))) break;
+          // after the other group's products of the job before (at the start of a
+          // piece: of the piece before, when its last job was group 1's)
+          if (job > 0 || (owed && n_piece > 0)) {
+            if (!(ok = wait(&bar_turn[g], n_turn & 1))) break;
+            ++n_turn;
+          }
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            if (h == 1 && !(ok = wait(&bar_p[g][1], n_job & 1))) break;
+            tc::fence_after();
+            if (tc::elect_one()) {
+#pragma unroll
+              for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                tc::mma_ts(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4),
+                           tc::idesc_bf16(kRows, D, true), (i > 0 || kk > 0) ? 1u : 0u);
+              if (h == 1) {
+                tc::mma_commit(&bar_free[sl]);
+                if (i == my_jobs - 1) tc::mma_commit(&bar_o[g]);
+              }
+            }
+            __syncwarp();
+          }
+          if (!ok) break;
+          // then the next S, and the turn: early when S would have to wait for K
+          const bool more = i + 1 < my_jobs;
+          bool pass = g == 1 || job + 1 < pc.jobs0 + pc.jobs1;
+          const int tn = t + step;
+          if (pass && (!more || !ready(tn, by_tma))) {
+            if (tc::elect_one()) tc::mbar_arrive(&bar_turn[1 - g]);
+            __syncwarp();
+            pass = false;
+          }
+          if (more) {
+            if (step == 2) ok = skip(t + 1);
+            if (!ok || !(ok = landed(tn, 0))) break;
+            issue_s(tn, i + 2 == my_jobs, pass ? &bar_turn[1 - g] : nullptr);
+          }
+        }
+        // tiles behind the group's last one
+        if (ok && my_jobs > 0 && t0 + my_jobs * step - step + 1 < pc.nt)
+          ok = skip(pc.nt - 1);
+        owed = (pc.jobs0 + pc.jobs1) % 2 == 0;
+        if (my_jobs == 0 && ok && tc::elect_one()) tc::mbar_arrive(&bar_qfree);
+        __syncwarp();
+        n_slot += 2 * pc.nt;
+        ++n_piece;
+      }
+      if (!ok && tc::elect_one()) {
+        flag_error(pl.hdr + kErrWord, kErrTimeout);
+        s_abort = 1;
+        // nothing may be in flight when the tensor memory is freed
+        tc::mma_commit(&bar_drain[g]);
+        const long long t0 = clock64();
+        while (!tc::mbar_try_wait(&bar_drain[g], 0) && clock64() - t0 < kWaitCycles) {
         }
       }
       __syncwarp();
-    } else if (nt > 0 && warp < kMmaWarp) {
-      // ================= softmax: a thread a query row =================
-      const int g = warp >> 2;
-      const int my_jobs = g ? jobs1 : jobs0;
-      const int x = (pair ? g * kRows : 0) + (tid & (kRows - 1));  // row of the item
-      const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
-      const uint32_t tS = tmem + lane_off + kTmemS + g * kTile, tO = tmem + lane_off + g * 128;
-      auto waitw = [&](uint64_t* bar, uint32_t parity) -> bool {
-        return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, budget)) != 0;
-      };
-      // tokens this row sees
-      int limit = it.t1;
-      if (it.own && sh.causal && x < it.nrows) {
-        const int qi = (it.row0 + x) / sh.G;
-        limit = it.t1 - sh.Nq + qi + 1;
-      }
-      float m_run = kNegInf, l_run = 0.f;
-      for (int i = 0; i < my_jobs; ++i) {
-        const int t = pair ? i : 2 * i + g;
-        if (!waitw(&bar_s[g], (n_job[g] + i) & 1)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after();
-        const int nv = limit - (it.t0 + (t_lo + t) * kTile);  // valid columns
-        const bool masked = __any_sync(0xffffffffu, nv < kTile);
-        uint32_t sv[32];
-        float mx = kNegInf;
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 32) {
-          tc::tmem_ld32(tS + c, sv);
-          tc::tmem_ld_wait(sv);
-          if (masked) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-              if (c + k < nv) mx = fmaxf(mx, __uint_as_float(sv[k]));
-          } else {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) mx = fmaxf(mx, __uint_as_float(sv[k]));
-          }
-        }
-        mx *= scale_log2;
-        const bool move = mx > m_run + 8.f;  // also true on the first valid tile
-        const float m_new = move ? mx : m_run;
-        const float alpha = move ? exp2f(m_run - m_new) : 1.f;
-        // O of the jobs before is complete: S of this job was issued after it
-        if (__any_sync(0xffffffffu, move && i > 0)) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            tc::tmem_ld32(tO + c, sv);
-            tc::tmem_ld_wait(sv);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) sv[k] = __float_as_uint(__uint_as_float(sv[k]) * alpha);
-            tc::tmem_st32(tO + c, sv);
-          }
-          tc::tmem_st_wait();
-        }
-        l_run *= alpha;
-        m_run = m_new;
-        const float m_use = m_new == kNegInf ? 0.f : m_new;
-        // P takes the place of S columns that this warp has read already
-#pragma unroll 1
-        for (int c = 0; c < kTile; c += 64) {
-          uint32_t pk[32];
-          float sum = 0.f;
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            tc::tmem_ld32(tS + c + 32 * h, sv);
-            tc::tmem_ld_wait(sv);
-#pragma unroll
-            for (int k = 0; k < 32; k += 2) {
-              float p0 = ex2(fmaf(__uint_as_float(sv[k]), scale_log2, -m_use));
-              float p1 = ex2(fmaf(__uint_as_float(sv[k + 1]), scale_log2, -m_use));
-              if (masked) {
-                if (c + 32 * h + k >= nv) p0 = 0.f;
-                if (c + 32 * h + k + 1 >= nv) p1 = 0.f;
-              }
-              // P is rounded to bf16 for the second product (half a step, 2^-8 of
-              // each weight at most); the sum keeps the fp32 values, so that lse
-              // carries no such rounding
-              sum += p0 + p1;
-              const __nv_bfloat162 pp = __floats2bfloat162_rn(p0, p1);
-              pk[h * 16 + k / 2] = *reinterpret_cast<const uint32_t*>(&pp);
-            }
-          }
-          l_run += sum;
-          tc::tmem_st32(tS + c / 2, pk);
-        }
-        tc::tmem_st_wait();
-        tc::fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar_p[g]);
-      }
-      // ---- the piece's partial
-      if (ok && waitw(&bar_o, n_piece & 1)) {
-        tc::fence_after();
-        const bool mine = pair ? x < it.nrows : (tid & (kRows - 1)) < it.nrows;
-        const int64_t row = slot + (pair ? x : g * it.nrows + x);
-        if (mine) part_ml[row] = make_float2(m_run, l_run);
-        if (my_jobs > 0) {
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t ov[32];
-            tc::tmem_ld32(tO + c, ov);
-            tc::tmem_ld_wait(ov);
-            if (mine) {
-              float* dst = part_o + row * D + c;
-#pragma unroll
-              for (int k = 0; k < 32; k += 4)
-                *reinterpret_cast<uint4*>(dst + k) =
-                    make_uint4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
-            }
-          }
-        }
-      } else if (lane == 0) {
-        flag_error(pl.hdr + kErrWord, kErrTimeout);
-        s_abort = 1;
-      }
-    } else if (nt > 0 && warp >= kLoadWarp && warp < kLoadWarp + kLoadThreads / 32) {
+    } else if (warp < kLoadWarp + kLoadThreads / 32) {
       // ================= loads =================
-      const int lt = tid - kLoadWarp * 32, lw = lt >> 5;
-      constexpr int kChunks = D / 8;              // 16-byte chunks of a row
-      constexpr int kRowsPer = 32 / kChunks;      // rows a warp instruction covers
+      const int lw = warp - kLoadWarp;
+      constexpr int kChunks = D / 8;          // 16-byte chunks of a row
+      constexpr int kRowsPer = 32 / kChunks;  // rows a warp instruction covers
       const int sub = lane / kChunks, cc = lane % kChunks;
       // warp lw fills rows 32 lw .. 32 lw + 31; chunk c of row r of column
       // block j goes to chunk c ^ (r & 7)
       auto dst_of = [&](uint32_t tile, int r) {
         return tile + (cc >> 3) * W::kBlkBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
       };
-#pragma unroll 1
-      for (int blk = 0; blk < (pair ? 2 : 1); ++blk) {
-        // query row of this lane: request, query token and head
-        const int x = blk * kRows + lw * 32 + lane;
-        int64_t off = -1;
-        if (x < it.nrows) {
-          const int gr = it.row0 + x;
-          const int b = it.own ? it.bt_row : pl.order[gr / sh.R];
-          const int r = it.own ? gr : gr % sh.R;
-          off = (((int64_t)b * sh.Nq + r / sh.G) * sh.Hq + head * sh.G + r % sh.G) * D;
-        }
-#pragma unroll
-        for (int i = 0; i < 32; i += kRowsPer) {
-          const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
-          tc::cp_async16(dst_of(sQ + blk * W::kTileBytes, lw * 32 + i + sub),
-                         q + (o >= 0 ? o + cc * 8 : 0), o >= 0 ? 16 : 0);
-        }
-      }
-      tc::cp_async_commit();
-      // physical row of this lane's token of tile t (-1: none)
-      const int32_t* bt = block_table + (int64_t)it.bt_row * sh.max_pages;
-      auto token_row = [&](int t) -> int {
-        const int tok = it.t0 + (t_lo + t) * kTile + lw * 32 + lane;
-        if (tok >= it.t1) return -1;
-        const int page = bt[tok / sh.page_size];
-        if ((unsigned)page >= (unsigned)sh.num_pages) {
-          flag_error(pl.hdr + kErrWord, kErrPage);
-          return -1;
-        }
-        return page * sh.page_size + tok % sh.page_size;
-      };
       auto publish = [&](uint64_t* bar) {
         tc::fence_async_smem();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
       };
-      const int total_loads = 2 * nt;
-      int row = token_row(0), next_row = -1;
-      int i = 0;
-      for (; i < total_loads; ++i) {
-        const uint32_t n = n_slot + i, s = n % W::kSlotsN;
-        if (n >= (uint32_t)W::kSlotsN) {
-          if (!__all_sync(0xffffffffu, tc::mbar_wait(&bar_free[s], (n / W::kSlotsN - 1) & 1,
-                                                     &s_abort, budget))) {
-            ok = false;
-            break;
+      uint32_t n_slot = 0, n_piece = 0;
+      uint32_t ph_go = 0;
+      uint32_t tma_used = 0, tma_count = 0;  // by slot: any TMA copy, their number modulo two
+      for (int64_t u = u_begin; u < u_end && ok;) {
+        const Piece pc = piece_at(pl, u, u_end, U, n_items, slots_head, cta);
+        u = pc.next;
+        if (pc.nt == 0) continue;
+        // physical row of this lane's token of tile t (-1: none)
+        const int32_t* bt = block_table + (int64_t)pc.it.bt_row * sh.max_pages;
+        auto token_row = [&](int t) -> int {
+          const int tok = pc.it.t0 + (pc.t_lo + t) * kTile + lw * 32 + lane;
+          if (tok >= pc.it.t1) return -1;
+          const int page = bt[tok / sh.page_size];
+          if ((unsigned)page >= (unsigned)sh.num_pages) {
+            flag_error(pl.hdr + kErrWord, kErrPage);
+            return -1;
+          }
+          return page * sh.page_size + tok % sh.page_size;
+        };
+        const int by_tma = tma_tiles(pc);
+        // first row of this lane's box of tile t (warp 0; lane b * kBlk + j copies
+        // column block j of box b; a bad page gives zeros, from beyond the pool)
+        const int n_box = sh.box ? kTile / sh.box : 0, my_box = lane / W::kBlk;
+        auto box_row = [&](int t) -> int {
+          if (t >= by_tma || my_box >= n_box) return 0;
+          const int tok = pc.it.t0 + (pc.t_lo + t) * kTile + my_box * sh.box;
+          const int page = bt[tok / sh.page_size];
+          if ((unsigned)page >= (unsigned)sh.num_pages) {
+            flag_error(pl.hdr + kErrWord, kErrPage);
+            return sh.num_pages * sh.page_size;
+          }
+          return page * sh.page_size + tok % sh.page_size;
+        };
+        int row = lw == 0 ? box_row(0) : 0;
+        if (n_piece > 0 && !(ok = wait(&bar_qfree, (n_piece - 1) & 1))) break;
+#pragma unroll 1
+        for (int blk = 0; blk < (pc.pair ? 2 : 1); ++blk) {
+          // query row of this lane: request, query token and head
+          const int x = blk * kRows + lw * 32 + lane;
+          int64_t off = -1;
+          if (x < pc.it.nrows) {
+            const int gr = pc.it.row0 + x;
+            const int b = pc.it.own ? pc.it.bt_row : pl.order[gr / sh.R];
+            const int r = pc.it.own ? gr : gr % sh.R;
+            off = (((int64_t)b * sh.Nq + r / sh.G) * sh.Hq + pc.head * sh.G + r % sh.G) * D;
+          }
+#pragma unroll 4
+          for (int i = 0; i < 32; i += kRowsPer) {
+            const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
+            tc::cp_async16(dst_of(sQ + blk * W::kTileBytes, lw * 32 + i + sub),
+                           q + (o >= 0 ? o + cc * 8 : 0), o >= 0 ? 16 : 0);
           }
         }
-        const bool is_v = i & 1;
-        const __nv_bfloat16* pool = is_v ? kv_v : kv_k;
-        const uint32_t tile = sKV + s * W::kTileBytes;
-#pragma unroll
-        for (int r = 0; r < 32; r += kRowsPer) {
-          const int pr = __shfl_sync(0xffffffffu, row, r + sub);
-          tc::cp_async16(dst_of(tile, lw * 32 + r + sub),
-                         pool + (pr >= 0 ? ((int64_t)pr * sh.Hkv + head) * D + cc * 8 : 0),
-                         pr >= 0 ? 16 : 0);
-        }
         tc::cp_async_commit();
-        if (!is_v) next_row = (i >> 1) + 1 < nt ? token_row((i >> 1) + 1) : -1;
-        else row = next_row;
-        // publish what has landed: Q after the first kLag tiles, then the rest in order
-        tc::cp_async_wait<W::kLag>();
-        if (i == W::kLag - 1) publish(&bar_q);
-        if (i >= W::kLag) publish(&bar_full[(n - W::kLag) % W::kSlotsN]);
+        int waiting = 0;  // tiles copied by cp.async and not published yet
+        int done = 0;
+        for (int t = 0; t < pc.nt && ok; ++t) {
+          if (t >= by_tma) row = token_row(t);
+          const int next_row = lw == 0 ? box_row(t + 1) : 0;
+#pragma unroll
+          for (int v = 0; v < 2; ++v, ++done) {
+            const uint32_t n = n_slot + done, s = n % W::kSlotsN;
+            // warp 0 waits for room; the others copy only where it has let them
+            if (lw == 0 && n >= (uint32_t)W::kSlotsN &&
+                !(ok = wait(&bar_free[s], (n / W::kSlotsN - 1) & 1)))
+              break;
+            if (t >= by_tma) {
+              if (lw == 0) {
+                if (lane == 0) tc::mbar_arrive(&bar_go[s]);
+              } else if (!(ok = wait(&bar_go[s], (ph_go >> s) & 1))) {
+                break;
+              }
+              ph_go ^= 1u << s;
+            }
+            const uint32_t tile = sKV + s * W::kTileBytes;
+            if (t < by_tma) {
+              if (lw == 0) {
+                tma_used |= 1u << s;
+                tma_count ^= 1u << s;
+                if (lane == 0) tc::mbar_arrive_expect(&bar_tma[s], W::kTileBytes);
+                __syncwarp();
+                if (my_box < n_box) {
+                  const int j = lane % W::kBlk;
+                  tc::tma_load_3d(tile + j * W::kBlkBytes + my_box * sh.box * 128,
+                                  v ? &map_v : &map_k, j * 64, pc.head, row, &bar_tma[s]);
+                }
+              }
+            } else {
+              const __nv_bfloat16* pool = (v ? kv_v : kv_k) + pc.head * D + cc * 8;
+#pragma unroll 8
+              for (int r = 0; r < 32; r += kRowsPer) {
+                const int pr = __shfl_sync(0xffffffffu, row, r + sub);
+                tc::cp_async16(dst_of(tile, lw * 32 + r + sub),
+                               pool + (pr >= 0 ? (int64_t)pr * sh.Hkv * D : 0), pr >= 0 ? 16 : 0);
+              }
+              tc::cp_async_commit();
+              ++waiting;
+            }
+            if (done == 1) {  // Q, behind the first K and V tile
+              if (waiting == 0) tc::cp_async_wait<0>();
+              else tc::cp_async_wait<2>();
+              publish(&bar_q);
+            }
+            if (waiting > W::kLag) {
+              tc::cp_async_wait<W::kLag>();
+              publish(&bar_cp[(n - W::kLag) % W::kSlotsN]);
+              --waiting;
+            }
+          }
+          row = next_row;
+        }
+        tc::cp_async_wait<0>();
+        for (; waiting; --waiting) publish(&bar_cp[(n_slot + done - waiting) % W::kSlotsN]);
+        n_slot += done;
+        ++n_piece;
       }
-      tc::cp_async_wait<0>();
-      if (ok) {
-        for (int k = total_loads - W::kLag; k < total_loads; ++k)
-          publish(&bar_full[(n_slot + k) % W::kSlotsN]);
-      } else if (lane == 0) {
+      if (!ok && lane == 0) {
         flag_error(pl.hdr + kErrWord, kErrTimeout);
         s_abort = 1;
       }
+      // the TMA copies in flight land before the shared memory is given up (in
+      // the normal course every one has been waited for)
+      if (!ok && lw == 0 && lane == 0) {
+        const long long t0 = clock64();
+        for (int i = 0; i < W::kSlotsN; ++i)
+          while (((tma_used >> i) & 1) && !tc::mbar_try_wait(&bar_tma[i], (~tma_count >> i) & 1) &&
+                 clock64() - t0 < kWaitCycles) {
+          }
+      }
+      __syncwarp();
     }
-    // a share that rounds to no tile still has its place among the partials
-    if (nt == 0 && tid < item_slots(it.nrows)) part_ml[slot + tid] = make_float2(kNegInf, 0.f);
-    // ---- every role is done with the piece
-    tc::fence_before();
-    __syncthreads();
-    tc::fence_after();
-    if (nt > 0) {
-      n_slot += 2 * nt;
-      n_job[0] += jobs0;
-      n_job[1] += jobs1;
-      ++n_piece;
-    }
-    if (s_abort) break;
   }
   tc::fence_before();
   __syncthreads();
@@ -1227,6 +1410,9 @@ PrefixShape prefix_shape(const pks_prefix_args& a) {
   sh.narrow = sh.R <= kNarrowRows;
   sh.hg = attn_heads_per_cta(a.Hkv);
   sh.wide_grid = device_sm_count();
+  sh.box = a.page_size & -a.page_size;
+  if (sh.box > kTile) sh.box = kTile;
+  if (sh.box < 8) sh.box = 0;
   // shared memory holds one narrow CTA of eight heads an SM, more of fewer
   const size_t stage = (size_t)2 * kNarrowTile * sh.hg * a.D * sizeof(__nv_bfloat16);
   const size_t smem = kNarrowStages * stage + sizeof(int32_t) * (size_t)(kNarrowRowCap + a.B + 1);
@@ -1270,6 +1456,30 @@ cudaError_t allow_smem(K kern, size_t bytes, bool (&done)[64]) {
   return e;
 }
 
+// Tensor map of a K or V pool as rows x heads x D, a box being `rows` tokens of
+// one head and 64 of its values, 128-byte swizzled.
+cudaError_t pool_map(CUtensorMap* map, const void* pool, const pks_prefix_args& a, int rows) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv,
+                              (cuuint64_t)a.num_pages * (cuuint64_t)a.page_size};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.Hkv * a.D * 2};
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, ones[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims,
+                            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 template <int D>
 cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const PrefixShape& sh,
                         float scale_log2, cudaStream_t s) {
@@ -1277,6 +1487,11 @@ cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const P
   cudaError_t e = allow_smem(k_prefix_wide<D>, Wide<D>::kSmem, done);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  CUtensorMap map_k{}, map_v{};
+  if (sh.box > 0) {
+    if ((e = pool_map(&map_k, a.kv_k, a, sh.box)) != cudaSuccess) return e;
+    if ((e = pool_map(&map_v, a.kv_v, a, sh.box)) != cudaSuccess) return e;
+  }
   return launch_ex(k_prefix_wide<D>, dim3(sh.wide_grid), dim3(kWideThreads), Wide<D>::kSmem, s,
                    /*pdl=*/true, /*coop=*/false, a.block_table,
                    static_cast<const __nv_bfloat16*>(a.q),
@@ -1284,7 +1499,7 @@ cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const P
                    static_cast<const __nv_bfloat16*>(a.kv_v), plan_ptrs(ws, L),
                    reinterpret_cast<float2*>(ws + L.wide_ml),
                    reinterpret_cast<float*>(ws + L.wide_o), sh, scale_log2,
-                   a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles);
+                   a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles, map_k, map_v);
 }
 
 template <int D, int HG, int NT8>

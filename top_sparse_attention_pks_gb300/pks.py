@@ -224,8 +224,9 @@ def _check(code: int, where: str):
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        if torch.cuda.is_available() and torch.cuda.is_initialized():
-            return torch.cuda.current_stream().cuda_stream
+        if torch.cuda.is_initialized():
+            # the raw handle: a Stream object costs microseconds a call
+            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
         return None
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
