@@ -22,10 +22,11 @@
 //                   the sparse attention's rows
 //   k_prefix_merge  the parts' combination
 //
-// Both attention kernels are persistent and cut their work into equal ranges
-// (tiles of all items, head after head); a CTA writes a partial (m, l, o) for
-// each item that its range touches, in slots that the merge derives from the
-// plan again.
+// Both attention kernels are persistent; each has part of the SMs, as their
+// estimated times are, and cuts its work into equal ranges (tiles of all items,
+// or own tokens, head after head); a CTA writes a partial (m, l, o) for each
+// item or request that its range touches, in slots that the merge derives from
+// the plan again.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -54,28 +55,41 @@ struct Item {
   int row0;     // prefix item: first row in group order; own item: first row of the request
   int nrows;    // 1..256
   int bt_row;   // block-table row its tokens are found through
-  int own;      // 1: rows of request bt_row against its own tokens
+  int own;      // rows of request bt_row against its own tokens: its length; else 0
   int t0, t1;   // token range
-  int unit0;    // units of the items before it (one head): tiles times MMAs a tile
+  int unit0;    // tiles of the items before it (one head)
   int slot0;    // partial rows of the items before it (one head)
+};
+// Where a wide CTA starts.
+struct Start {
+  int head, item;
+  int pad[2];
+};
+// What the merge needs of a request.
+struct Request {
+  int gunit, gslot, grows, gtiles;  // its group's prefix items: tiles 0 when it has none
+  int row;                          // its first row in the group
+  int ounit, oslot;                 // its own items (wide)
+  int own;                          // own tokens
 };
 
 // plan header words
-constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTokens = 5;
+constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTokens = 5,
+              kShare = 6, kWideCtas = 7, kNarrowCtas = 8;
 
 struct PlanPtrs {
   int32_t* hdr;
   int32_t *lens, *eq, *first, *lead;   // per request
   int32_t *start;                      // first own token
-  int32_t *pitem, *prow;               // prefix: first item of the group, row in the group
-  int32_t *oitem;                      // first own item (wide)
   int32_t *order;                      // members in group order
-  int32_t *npre;                       // [B + 1] own tokens before each request (narrow)
-  Item* items;                         // one more than there are
+  int32_t *npre;                       // [B + 1] own tokens before each request
+  Request* req;
+  Start* starts;                       // per wide CTA
+  Item* items;
 };
 
 struct PrefixShape {
-  int B, Hq, Hkv, G, Nq, R;
+  int B, Hq, Hkv, G, Nq, R, D;
   int page_size, max_pages, num_pages;
   int causal;
   int narrow;      // own tokens by the narrow kernel
@@ -93,19 +107,12 @@ __device__ __forceinline__ float ex2(float x) {
 
 __device__ __forceinline__ void flag_error(int32_t* err, int code) { atomicCAS(err, 0, code); }
 
-__device__ __forceinline__ int item_halves(int nrows) { return nrows <= kRows ? 2 : 1; }
-// MMAs a tile of an item costs: one, or two for two row blocks
-__device__ __forceinline__ int item_weight(int nrows) { return nrows <= kRows ? 1 : 2; }
-// partial rows of an item per CTA: with one row block each softmax group keeps its own
-__device__ __forceinline__ int item_slots(int nrows) { return nrows <= kRows ? 2 * nrows : nrows; }
-
-// CTAs that share `total` units: all, or one per `least` units
-__device__ __forceinline__ int used_grid(int64_t total, int grid, int least) {
-  const int64_t g = (total + least - 1) / least;
-  return g < 1 ? 1 : g < grid ? (int)g : grid;
-}
-constexpr int kWideLeast = 2;                    // tiles a CTA takes at least
-constexpr int kNarrowLeast = 2 * kNarrowTile;    // tokens a CTA takes at least
+constexpr int kWideLeast = 2;                  // tiles a wide CTA takes at least
+constexpr int kNarrowLeast = 2 * kNarrowTile;  // tokens a narrow CTA takes at least
+// Estimated nanoseconds an SM spends: on a wide tile with two row blocks (the
+// products of 256 rows, D = 128; half of that at least with D = 64), and on a
+// kilobyte that all SMs stream together (6.8 TB/s over 152 of them).
+constexpr int kPairNs = 1500, kStreamNsPerKb = 23;
 
 __device__ __forceinline__ int64_t range_lo(int64_t total, int c, int n) { return c * total / n; }
 // the CTA whose range holds unit u
@@ -116,6 +123,7 @@ __device__ __forceinline__ int range_owner(int64_t u, int64_t total, int n) {
 // ------------------------------------------------------------------ plan ---
 
 constexpr int kPlanThreads = 256;
+constexpr int kPlanArrays = 13;
 
 template <typename T, typename F>
 __device__ __forceinline__ T block_reduce(T v, F op, T* s_red) {
@@ -131,26 +139,28 @@ __device__ __forceinline__ T block_reduce(T v, F op, T* s_red) {
   return v;
 }
 
-// exclusive scan over the block of one value a thread
-__device__ __forceinline__ int block_scan_ex(int v, int* s_red, int& total) {
+// exclusive scan over the block of four values a thread
+__device__ __forceinline__ int4 block_scan_ex(int4 v, int4* s_red, int4& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int x = v;
+  auto add = [](int4 a, int4 c) { return make_int4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w); };
+  int4 x = v;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const int4 y = make_int4(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o),
+                             __shfl_up_sync(0xffffffffu, x.z, o), __shfl_up_sync(0xffffffffu, x.w, o));
+    if (lane >= o) x = add(x, y);
   }
   __syncthreads();
   if (lane == 31) s_red[warp] = x;
   __syncthreads();
-  int before = 0;
-  total = 0;
+  int4 before = make_int4(-v.x, -v.y, -v.z, -v.w);
+  total = make_int4(0, 0, 0, 0);
 #pragma unroll
   for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before += s_red[w];
-    total += s_red[w];
+    if (w < warp) before = add(before, s_red[w]);
+    total = add(total, s_red[w]);
   }
-  return before + x - v;
+  return add(before, x);
 }
 
 // tokens every query of the request sees
@@ -165,7 +175,8 @@ __device__ __forceinline__ int seen_by_all(int len, int causal, int Nq) {
 __global__ void __launch_bounds__(kPlanThreads)
 k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
               const int32_t* __restrict__ prefix_group, PlanPtrs pl, PrefixShape sh) {
-  extern __shared__ int s_dyn[];  // [4][B] in the last block
+  extern __shared__ int s_dyn[];  // [kPlanArrays][B] in the last block
+  __shared__ int4 s_red4[kPlanThreads / 32];
   __shared__ long long s_red64[kPlanThreads / 32];
   __shared__ int s_red[kPlanThreads / 32];
   __shared__ int s_last;
@@ -238,168 +249,210 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   __threadfence();
   if (tid == 0) pl.hdr[kTicket] = 0;
 
-  // ---- the last block: the groups' common prefixes.  The shared length of a
-  // group is the least among the members that share at least half of what the
-  // second longest shares; members with less stay on their own.
-  int* s_max = s_dyn;            // by first member: most shared tokens, the longest member aside
-  int* s_min = s_dyn + B;        // the group's prefix
-  int* s_cnt = s_dyn + 2 * B;    // members that take part
-  int* s_at = s_dyn + 3 * B;     // rows of the members before, in group order
+  // ---- the last block.  The requests' findings, all in one round trip
+  int* s_first = s_dyn;           // by request
+  int* s_lead = s_first + B;
+  int* s_eq = s_lead + B;
+  int* s_len = s_eq + B;
+  int* s_pre = s_len + B;         // by first member: the group's prefix
+  int* s_cnt = s_pre + B;         // ... members that take part
+  int* s_at = s_cnt + B;          // ... the most shared; then members placed so far
+  int* s_item = s_at + B;         // ... first prefix item, unit and slot
+  int* s_unit = s_item + B;
+  int* s_slot = s_unit + B;
+  int* s_oitem = s_slot + B;      // by request: first own item, unit and slot
+  int* s_ounit = s_oitem + B;
+  int* s_oslot = s_ounit + B;
   for (int b = tid; b < B; b += kPlanThreads) {
-    s_max[b] = 0;
-    s_min[b] = 0x7fffffff;
-    s_cnt[b] = 0;
+    s_first[b] = __ldcg(pl.first + b);
+    s_lead[b] = __ldcg(pl.lead + b);
+    s_eq[b] = __ldcg(pl.eq + b);
+    s_len[b] = __ldcg(pl.lens + b);
+    s_pre[b] = 0x7fffffff;
+    s_cnt[b] = s_at[b] = 0;
   }
   __syncthreads();
+  // The groups' common prefixes: the least shared length among the members that
+  // share at least half of what the second longest shares; members with less
+  // stay on their own.
   for (int b = tid; b < B; b += kPlanThreads)
-    if (__ldcg(pl.lead + b) != b) atomicMax(&s_max[__ldcg(pl.first + b)], __ldcg(pl.eq + b));
+    if (s_lead[b] != b) atomicMax(&s_at[s_first[b]], s_eq[b]);
   __syncthreads();
   for (int b = tid; b < B; b += kPlanThreads) {
-    const int f = __ldcg(pl.first + b), e = __ldcg(pl.eq + b), most = s_max[f];
+    const int f = s_first[b], e = s_eq[b], most = s_at[f];
     if (most >= kMinShared && e >= (most + 1) / 2) {
-      atomicMin(&s_min[f], e);
+      atomicMin(&s_pre[f], e);
       atomicAdd(&s_cnt[f], 1);
     }
   }
   __syncthreads();
+  auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
+  auto blocks = [](int rows) { return (rows + kItemRows - 1) / kItemRows; };
+  // the group (by its first member) that request b takes part in, or -1
+  auto joined = [&](int b) {
+    const int f = s_first[b];
+    return s_cnt[f] >= 2 && s_eq[b] >= s_pre[f] ? f : -1;
+  };
   const int per = (B + kPlanThreads - 1) / kPlanThreads;
   const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
-  // members and prefix items of the groups, by first member
-  int members = 0, items = 0, units = 0, slots = 0;
-  auto prefix_units = [&](int f, int& k, int& u, int& s) {
-    const int rows = s_cnt[f] * sh.R, nt = (s_min[f] + kTile - 1) / kTile;
-    k = (rows + kItemRows - 1) / kItemRows;
-    const int tail = rows - (k - 1) * kItemRows;
-    u = nt * (2 * (k - 1) + item_weight(tail));
-    s = (k - 1) * kItemRows + item_slots(tail);
-  };
-  for (int b = b_lo; b < b_hi; ++b)
-    if (s_cnt[b] >= 2) {
-      int k, u, s;
-      prefix_units(b, k, u, s);
-      members += s_cnt[b];
-      items += k;
-      units += u;
-      slots += s;
-    } else {
-      s_cnt[b] = 0;
-    }
-  int tm, ti, tu, ts;
-  int m0 = block_scan_ex(members, s_red, tm), i0 = block_scan_ex(items, s_red, ti);
-  int u0 = block_scan_ex(units, s_red, tu), sl0 = block_scan_ex(slots, s_red, ts);
+  const int own_blocks = sh.narrow ? 0 : blocks(sh.R);
+  // members, tiles of both kinds, own tokens
+  int4 sum = make_int4(0, 0, 0, 0), all;
   for (int b = b_lo; b < b_hi; ++b) {
-    if (!s_cnt[b]) continue;
-    int k, u, s;
-    prefix_units(b, k, u, s);
-    const int T = s_min[b], rows = s_cnt[b] * sh.R, nt = (T + kTile - 1) / kTile;
-    const int lead = __ldcg(pl.lead + b);
-    s_at[b] = m0;
-    s_max[b] = i0;  // first item of the group from here on
-    int uu = u0, ss = sl0;
-    for (int i = 0; i < k; ++i) {
-      Item it;
-      it.row0 = m0 * sh.R + i * kItemRows;
-      it.nrows = min(kItemRows, rows - i * kItemRows);
-      it.bt_row = lead;
-      it.own = 0;
-      it.t0 = 0;
-      it.t1 = T;
-      it.unit0 = uu;
-      it.slot0 = ss;
-      pl.items[i0 + i] = it;
-      uu += nt * item_weight(it.nrows);
-      ss += item_slots(it.nrows);
+    if (s_cnt[b] >= 2) {
+      sum.x += s_cnt[b];
+      sum.y += blocks(s_cnt[b] * sh.R) * tiles(s_pre[b]);
     }
-    m0 += s_cnt[b];
-    i0 += k;
-    u0 += u;
-    sl0 += s;
+    const int f = joined(b), own = s_len[b] - (f >= 0 ? s_pre[f] : 0);
+    sum.z += own_blocks * tiles(own);
+    sum.w += own;
+  }
+  int4 ex = block_scan_ex(sum, s_red4, all);
+  const int U = all.y + all.z;
+  // SMs for either kernel by the time they will need, and the tiles a wide CTA
+  // takes (all of the same number, so that items cut at multiples of it run in
+  // step; see the wide kernel)
+  const int64_t total = (int64_t)U * sh.Hkv;
+  const int64_t wide_ns = total * (kPairNs * (sh.D / 64) / 2);
+  const int64_t narrow_ns =
+      sh.narrow ? (int64_t)all.w * sh.Hkv * sh.D * 4 * kStreamNsPerKb / 1024 : 0;
+  int W = sh.wide_grid;
+  if (narrow_ns > 0 && total > 0) {
+    W = (int)((wide_ns * sh.wide_grid + (wide_ns + narrow_ns) / 2) / (wide_ns + narrow_ns));
+    W = max(1, min(sh.wide_grid - 1, W));
+  }
+  const int sms_left = total > 0 ? sh.wide_grid - W : sh.wide_grid;
+  W = (int)min((int64_t)W, (total + kWideLeast - 1) / kWideLeast);
+  const int S = total > 0 ? (int)((total + W - 1) / W) : 1;
+  W = (int)((total + S - 1) / S);
+  if (tid == 0) {
+    const int64_t T = (int64_t)all.w * (sh.Hkv / sh.hg);
+    const int64_t n = min((int64_t)sms_left * (sh.narrow_grid / sh.wide_grid),
+                          (T + kNarrowLeast - 1) / kNarrowLeast);
+    pl.hdr[kUnits] = U;
+    pl.hdr[kTokens] = all.w;
+    pl.hdr[kShare] = S;
+    pl.hdr[kWideCtas] = W;
+    pl.hdr[kNarrowCtas] = sh.narrow ? (int)n : 0;
+    pl.npre[B] = all.w;
+  }
+  // items: a token range in cuts of S tiles, every row block of a cut in turn
+  int members = ex.x, ot = ex.w;
+  auto cuts = [&](int n) { return (n + S - 1) / S; };
+  sum = make_int4(0, 0, 0, 0);
+  int4 osum = make_int4(0, 0, 0, 0), oall;
+  for (int b = b_lo; b < b_hi; ++b) {
+    if (s_cnt[b] >= 2) {
+      const int rows = s_cnt[b] * sh.R, nt = tiles(s_pre[b]);
+      s_at[b] = members;
+      members += s_cnt[b];
+      sum.x += blocks(rows) * cuts(nt);
+      sum.y += blocks(rows) * nt;
+      sum.z += rows * cuts(nt);
+    }
+    const int f = joined(b), own = s_len[b] - (f >= 0 ? s_pre[f] : 0), nt = tiles(own);
+    pl.npre[b] = ot;
+    pl.start[b] = f >= 0 ? s_pre[f] : 0;
+    ot += own;
+    osum.x += own_blocks * cuts(nt);
+    osum.y += own_blocks * nt;
+    osum.z += own_blocks ? sh.R * cuts(nt) : 0;
+  }
+  ex = block_scan_ex(sum, s_red4, all);
+  int4 oex = block_scan_ex(osum, s_red4, oall);
+  for (int b = b_lo; b < b_hi; ++b) {
+    s_item[b] = ex.x;
+    s_unit[b] = ex.y;
+    s_slot[b] = ex.z;
+    s_oitem[b] = all.x + oex.x;
+    s_ounit[b] = all.y + oex.y;
+    s_oslot[b] = all.z + oex.z;
+    if (s_cnt[b] >= 2) {
+      const int rows = s_cnt[b] * sh.R, nt = tiles(s_pre[b]);
+      ex.x += blocks(rows) * cuts(nt);
+      ex.y += blocks(rows) * nt;
+      ex.z += rows * cuts(nt);
+    }
+    const int f = joined(b), nt = tiles(s_len[b] - (f >= 0 ? s_pre[f] : 0));
+    oex.x += own_blocks * cuts(nt);
+    oex.y += own_blocks * nt;
+    oex.z += own_blocks ? sh.R * cuts(nt) : 0;
+  }
+  const int n_items = all.x + oall.x;
+  if (tid == 0) {
+    pl.hdr[kItems] = n_items;
+    pl.hdr[kSlots] = all.z + oall.z;
   }
   __syncthreads();
+  // the items, and the CTAs that start in them
+  for (int i = tid; i < n_items; i += kPlanThreads) {
+    const bool own = i >= all.x;
+    const int* first_item = own ? s_oitem : s_item;
+    int lo = 0, hi = B - 1;  // the last request whose first item is at or before i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (first_item[mid] <= i) lo = mid; else hi = mid - 1;
+    }
+    const int j = i - first_item[lo];
+    const int rows = own ? sh.R : s_cnt[lo] * sh.R, k = blocks(rows);
+    const int f = joined(lo), begin = own && f >= 0 ? s_pre[f] : 0;
+    const int end = own ? s_len[lo] : s_pre[lo];
+    const int cut = j / k, blk = j % k, left = tiles(end - begin) - cut * S, nt = min(S, left);
+    Item it;
+    it.row0 = (own ? 0 : s_at[lo] * sh.R) + blk * kItemRows;
+    it.nrows = min(kItemRows, rows - blk * kItemRows);
+    it.bt_row = own ? lo : s_lead[lo];
+    it.own = own ? s_len[lo] : 0;
+    it.t0 = begin + cut * S * kTile;
+    it.t1 = left > S ? it.t0 + S * kTile : end;
+    it.unit0 = (own ? s_ounit[lo] : s_unit[lo]) + cut * S * k + blk * nt;
+    it.slot0 = (own ? s_oslot[lo] : s_slot[lo]) + cut * rows + blk * kItemRows;
+    pl.items[i] = it;
+    for (int h = 0; h < sh.Hkv; ++h) {
+      const int64_t u0 = (int64_t)h * U + it.unit0, c = (u0 + S - 1) / S;
+      if (c * S < u0 + nt) {
+        Start st = {};
+        st.head = h;
+        st.item = i;
+        pl.starts[c] = st;
+      }
+    }
+  }
+  __syncthreads();  // s_at counts members from here on
   // members in group order, ascending within a group: one warp, 32 requests at
-  // a time (s_at counts up as members are placed)
+  // a time; and what the merge needs of each request
   if (tid < 32) {
     for (int b0 = 0; b0 < B; b0 += 32) {
       const int b = b0 + tid;
-      int f = -1;
-      if (b < B) {
-        const int x = __ldcg(pl.first + b);
-        if (s_cnt[x] && __ldcg(pl.eq + b) >= s_min[x]) f = x;
-      }
+      const int f = b < B ? joined(b) : -1;
       const uint32_t peers = __match_any_sync(0xffffffffu, f);
       int at = 0;
       if (f >= 0) at = s_at[f] + __popc(peers & ((1u << tid) - 1));
       __syncwarp();
       if (f >= 0 && (peers >> tid) == 1u) s_at[f] = at + 1;  // the last of its group here
       __syncwarp();
-      if (b < B) {
-        if (f >= 0) pl.order[at] = b;
-        pl.pitem[b] = f >= 0 ? s_max[f] : -1;
-        pl.prow[b] = at * sh.R;  // the group's first row is its first item's row0
-        pl.start[b] = f >= 0 ? s_min[f] : 0;
+      if (f >= 0) {
+        pl.order[at] = b;
+        s_lead[b] = at;
       }
     }
   }
   __syncthreads();
-  // own tokens: items of the wide kernel, or the narrow kernel's prefix sum
-  int own_i = 0, own_u = 0, own_s = 0, own_t = 0;
-  auto own_units = [&](int b, int& n, int& k, int& u, int& s) {
-    n = __ldcg(pl.lens + b) - pl.start[b];
-    k = u = s = 0;
-    if (n <= 0 || sh.narrow) return;
-    const int nt = (n + kTile - 1) / kTile;
-    k = (sh.R + kItemRows - 1) / kItemRows;
-    const int tail = sh.R - (k - 1) * kItemRows;
-    u = nt * (2 * (k - 1) + item_weight(tail));
-    s = (k - 1) * kItemRows + item_slots(tail);
-  };
-  for (int b = b_lo; b < b_hi; ++b) {
-    int n, k, u, s;
-    own_units(b, n, k, u, s);
-    own_i += k;
-    own_u += u;
-    own_s += s;
-    own_t += n;
-  }
-  int toi, tou, tos, tot;
-  int oi = ti + block_scan_ex(own_i, s_red, toi), ou = tu + block_scan_ex(own_u, s_red, tou);
-  int os = ts + block_scan_ex(own_s, s_red, tos), ot = block_scan_ex(own_t, s_red, tot);
-  for (int b = b_lo; b < b_hi; ++b) {
-    int n, k, u, s;
-    own_units(b, n, k, u, s);
-    pl.npre[b] = ot;
-    pl.oitem[b] = k ? oi : -1;
-    const int nt = (n + kTile - 1) / kTile;
-    int uu = ou, ss = os;
-    for (int i = 0; i < k; ++i) {
-      Item it;
-      it.row0 = i * kItemRows;
-      it.nrows = min(kItemRows, sh.R - i * kItemRows);
-      it.bt_row = b;
-      it.own = 1;
-      it.t0 = pl.start[b];
-      it.t1 = it.t0 + n;
-      it.unit0 = uu;
-      it.slot0 = ss;
-      pl.items[oi + i] = it;
-      uu += nt * item_weight(it.nrows);
-      ss += item_slots(it.nrows);
+  // (s_at now ends each group: its first member stands s_cnt places before)
+  for (int b = tid; b < B; b += kPlanThreads) {
+    const int f = joined(b);
+    Request q = {};
+    if (f >= 0) {
+      q.gunit = s_unit[f];
+      q.gslot = s_slot[f];
+      q.grows = s_cnt[f] * sh.R;
+      q.gtiles = tiles(s_pre[f]);
+      q.row = (s_lead[b] - (s_at[f] - s_cnt[f])) * sh.R;
     }
-    oi += k;
-    ou += u;
-    os += s;
-    ot += n;
-  }
-  if (tid == 0) {
-    pl.npre[B] = tot;
-    pl.hdr[kItems] = ti + toi;
-    pl.hdr[kUnits] = tu + tou;
-    pl.hdr[kSlots] = ts + tos;
-    pl.hdr[kTokens] = tot;
-    Item end = {};
-    end.unit0 = tu + tou;
-    end.slot0 = ts + tos;
-    pl.items[ti + toi] = end;
+    q.ounit = s_ounit[b];
+    q.oslot = s_oslot[b];
+    q.own = s_len[b] - (f >= 0 ? s_pre[f] : 0);
+    pl.req[b] = q;
   }
 }
 
@@ -424,7 +477,10 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 // rows.  A tile of whole boxes (sh.box: the largest power of two up to 128 that
 // divides the page size, from 8, the swizzle's period) comes by TMA, the last
 // tile of a range and tiles of odd pages row by row with cp.async, which fills
-// what lies beyond the range with zeros.  The running maximum moves only when a
+// what lies beyond the range with zeros.  All CTAs take the same number of tiles
+// and a prefix is cut into items of just as many, row blocks within a cut next to
+// each other: CTAs that read the same tiles for different rows then do so in
+// step, from L2.  The running maximum moves only when a
 // tile exceeds it by more than 8 (log2 units).
 
 constexpr int kWideThreads = 512;
@@ -450,33 +506,39 @@ struct Piece {
   bool pair;            // two row blocks
   int jobs0, jobs1;     // jobs of the softmax groups
   int64_t slot;         // its first partial row
-  int64_t next;         // unit after it
 };
-// The piece that starts at unit u (a whole warp).
-__device__ __forceinline__ Piece piece_at(const PlanPtrs& pl, int64_t u, int64_t u_end, int U,
-                                          int n_items, int slots_head, int cta) {
-  Piece p;
-  p.head = (int)(u / U);
-  const int ur = (int)(u - (int64_t)p.head * U), lane = threadIdx.x & 31;
-  int item = 0;
-  for (int i0 = 0; i0 < n_items; i0 += 32) {  // the last item that starts at or before ur
-    const bool le = i0 + lane < n_items && pl.items[i0 + lane].unit0 <= ur;
-    const uint32_t m = __ballot_sync(0xffffffffu, le);
-    if (m) item = i0 + 31 - __clz(m);
-    if (m != 0xffffffffu) break;
+// A CTA's walk over its tiles; every role walks the same pieces.
+struct Walk {
+  const Item* items;
+  int64_t u, end;       // next tile and the CTA's last + 1, over all heads
+  int head, item;       // the item of u
+  int U, n_items, slots_head, cta;
+  __device__ __forceinline__ bool more() const { return u < end; }
+  __device__ __forceinline__ Piece next() {
+    Piece p;
+    p.it = items[item];
+    p.head = head;
+    const int nt = (p.it.t1 - p.it.t0 + kTile - 1) / kTile;
+    p.t_lo = (int)(u - ((int64_t)head * U + p.it.unit0));
+    p.nt = (int)(end - u < nt - p.t_lo ? end - u : nt - p.t_lo);
+    p.pair = p.it.nrows > kRows;
+    p.jobs1 = p.pair ? p.nt : p.nt / 2;
+    p.jobs0 = p.pair ? p.nt : p.nt - p.jobs1;
+    p.slot = (int64_t)head * slots_head + p.it.slot0 + (int64_t)kItemRows * cta;
+    u += p.nt;
+    if (++item == n_items) {
+      item = 0;
+      ++head;
+    }
+    return p;
   }
-  p.it = pl.items[item];
-  const int w = item_weight(p.it.nrows);
-  const int64_t u0 = (int64_t)p.head * U + p.it.unit0;
-  const int64_t end = (int64_t)p.head * U + pl.items[item + 1].unit0;
-  p.next = u_end < end ? u_end : end;
-  p.t_lo = (int)((u - u0 + w - 1) / w);
-  p.nt = (int)((p.next - u0 + w - 1) / w) - p.t_lo;
-  p.pair = w == 2;
-  p.jobs1 = p.pair ? p.nt : p.nt / 2;
-  p.jobs0 = p.nt * w - p.jobs1;
-  p.slot = (int64_t)p.head * slots_head + p.it.slot0 + (int64_t)kItemRows * cta;
-  return p;
+};
+
+// eight fp32 values, 32 bytes aligned: a whole sector a thread
+__device__ __forceinline__ void store8(float* dst, const float (&v)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(dst), "f"(v[0]),
+               "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7])
+               : "memory");
 }
 
 // registers of the softmax warpgroups and of the others: the launch's 512 x 128
@@ -497,9 +559,11 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   // its products are done (both issuers'); bar_q / bar_qfree: the same for Q;
   // bar_s[g]: S of group g's job; bar_p[g][h]: half h of its P is written;
   // bar_turn[g]: the other issuer has issued its job's P.V and next S; bar_o[g]:
-  // every product of the group's piece; bar_drain[g]: on giving up
+  // every product of the group's piece; bar_x[g] / bar_y[g]: the group's maxima
+  // are posted / it has read the other's O; bar_drain[g]: on giving up
   __shared__ __align__(8) uint64_t bar_tma[W::kSlotsN], bar_cp[W::kSlotsN], bar_go[W::kSlotsN],
-      bar_free[W::kSlotsN],      bar_q, bar_qfree, bar_s[2], bar_p[2][2], bar_turn[2], bar_o[2], bar_drain[2];
+      bar_free[W::kSlotsN],      bar_q, bar_qfree, bar_s[2], bar_p[2][2], bar_turn[2], bar_o[2], bar_x[2], bar_y[2], bar_drain[2];
+  __shared__ float2 s_ml[kRows];  // a row's maximum and sum, group 1's and then group 0's
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -523,6 +587,8 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       tc::mbar_init(&bar_p[i][1], 4);
       tc::mbar_init(&bar_turn[i], 1);
       tc::mbar_init(&bar_o[i], 1);
+      tc::mbar_init(&bar_x[i], 4);
+      tc::mbar_init(&bar_y[i], 4);
       tc::mbar_init(&bar_drain[i], 1);
     }
     tc::mbar_init_fence();
@@ -535,13 +601,22 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   pdl_wait();  // the plan
   pdl_launch_dependents();
 
-  const int U = pl.hdr[kUnits], n_items = pl.hdr[kItems], slots_head = pl.hdr[kSlots];
-  const int64_t total = (int64_t)U * sh.Hkv;
-  const int grid = used_grid(total, gridDim.x, kWideLeast);
   const int cta = blockIdx.x;
-  const bool part = total > 0 && cta < grid;
-  const int64_t u_begin = part ? range_lo(total, cta, grid) : 0;
-  const int64_t u_end = part ? range_lo(total, cta + 1, grid) : 0;
+  Walk walk;
+  {
+    const Start st = pl.starts[cta];  // (one round trip with the header)
+    const int S = pl.hdr[kShare], W = pl.hdr[kWideCtas];
+    walk.items = pl.items;
+    walk.U = pl.hdr[kUnits];
+    walk.n_items = pl.hdr[kItems];
+    walk.slots_head = pl.hdr[kSlots];
+    walk.cta = cta;
+    walk.head = st.head;
+    walk.item = st.item;
+    const int64_t total = (int64_t)walk.U * sh.Hkv;
+    walk.u = (int64_t)cta * S;
+    walk.end = cta >= W ? walk.u : walk.u + S < total ? walk.u + S : total;
+  }
   bool ok = true;
   // a wait of the whole warp
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -563,23 +638,17 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + kTmemS + g * kTile, tO = tmem + lane_off + g * 128;
     const uint64_t scale2 = tc::pack2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
-    uint32_t n_job = 0, n_piece = 0;
-    for (int64_t u = u_begin; u < u_end && ok;) {
-      const Piece pc = piece_at(pl, u, u_end, U, n_items, slots_head, cta);
-      u = pc.next;
+    uint32_t n_job = 0, n_piece = 0, n_split = 0;
+    while (walk.more() && ok) {
+      const Piece pc = walk.next();
       const int x = (pc.pair ? g * kRows : 0) + (tid & (kRows - 1));  // row of the item
-      const int64_t row = pc.slot + (pc.pair ? x : g * pc.it.nrows + x);
+      const int64_t row = pc.slot + x;
       const bool mine = x < pc.it.nrows;
-      if (pc.nt == 0) {
-        // a share that rounds to no tile still has its place among the partials
-        if (mine) part_ml[row] = make_float2(kNegInf, 0.f);
-        continue;
-      }
       const int my_jobs = g ? pc.jobs1 : pc.jobs0;
       const bool idle = !__any_sync(0xffffffffu, mine);  // no row of this warp counts
       // tokens this row sees
       int limit = pc.it.t1;
-      if (pc.it.own && sh.causal && mine) limit = pc.it.t1 - sh.Nq + (pc.it.row0 + x) / sh.G + 1;
+      if (pc.it.own && sh.causal && mine) limit = pc.it.own - sh.Nq + (pc.it.row0 + x) / sh.G + 1;
       limit -= pc.it.t0 + pc.t_lo * kTile;
       float m_run = kNegInf, l_run = 0.f;
       for (int i = 0; i < my_jobs; ++i) {
@@ -680,28 +749,88 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         if (lane == 0) tc::mbar_arrive(&bar_p[g][1]);
       }
       // ---- the piece's partial
-      if (my_jobs == 0) {
-        if (mine) part_ml[row] = make_float2(kNegInf, 0.f);
-        continue;
-      }
-      if (!ok || !(ok = wait(&bar_o[g], n_piece & 1))) break;
+      if (!ok) break;
+      if (my_jobs == 0) continue;  // (one tile: it was the other group's)
+      if (!(ok = wait(&bar_o[g], n_piece & 1))) break;
       ++n_piece;
       tc::fence_after();
-      if (idle) continue;
-      if (mine) part_ml[row] = make_float2(m_run, l_run);
+      float* dst = part_o + row * D;
+      if (pc.pair || pc.jobs1 == 0) {
+        if (mine) part_ml[row] = make_float2(m_run, l_run);
+        if (!idle) {
 #pragma unroll 1
-      for (int c = 0; c < D; c += 32) {
-        uint32_t ov[32];
-        tc::tmem_ld32(tO + c, ov);
-        tc::tmem_ld_wait(ov);
-        if (mine) {
-          float* dst = part_o + row * D + c;
+          for (int c = 0; c < D; c += 32) {
+            uint32_t ov[32];
+            tc::tmem_ld32(tO + c, ov);
+            tc::tmem_ld_wait(ov);
+            if (mine) {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4)
-            *reinterpret_cast<uint4*>(dst + k) = make_uint4(ov[k], ov[k + 1], ov[k + 2], ov[k + 3]);
+              for (int k = 0; k < 32; k += 8) {
+                float v[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(ov[k + e]);
+                store8(dst + c + k, v);
+              }
+            }
+          }
+        }
+        tc::fence_before();  // the reads of O come before the P that lets it be overwritten
+        continue;
+      }
+      // both groups hold the same rows: they exchange maxima and sums, and each
+      // combines half of the columns (its warps read the other group's O, which
+      // lies in the same lanes of the tensor memory)
+      const int xr = tid & (kRows - 1);
+      float2 e0 = make_float2(m_run, l_run), e1 = e0;
+      if (g == 0) {
+        if (!(ok = wait(&bar_x[1], n_split & 1))) break;
+        e1 = s_ml[xr];
+        s_ml[xr] = e0;
+      } else {
+        s_ml[xr] = e1;
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar_x[g]);
+      if (g == 1) {
+        if (!(ok = wait(&bar_x[0], n_split & 1))) break;
+        e0 = s_ml[xr];
+      }
+      tc::fence_after();
+      if (!idle) {
+        const float M = e0.y == 0.f ? e1.x : e1.y == 0.f ? e0.x : fmaxf(e0.x, e1.x);
+        const float w0 = e0.y == 0.f ? 0.f : exp2f(e0.x - M);
+        const float w1 = e1.y == 0.f ? 0.f : exp2f(e1.x - M);
+        if (mine && g == 0) part_ml[row] = make_float2(M, e0.y * w0 + e1.y * w1);
+        const uint32_t tA = tmem + lane_off, tB = tA + 128;
+#pragma unroll 1
+        for (int c = g * (D / 2); c < (g + 1) * (D / 2); c += 32) {
+          uint32_t a[32], b[32];
+          tc::tmem_ld32(tA + c, a);
+          tc::tmem_ld32(tB + c, b);
+          tc::tmem_ld_wait(a);
+          tc::tmem_ld_pin(b);
+          if (mine) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              float v[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                // (a part without tokens may hold 0 times infinity)
+                const float va = w0 == 0.f ? 0.f : w0 * __uint_as_float(a[k + e]);
+                const float vb = w1 == 0.f ? 0.f : w1 * __uint_as_float(b[k + e]);
+                v[e] = va + vb;
+              }
+              store8(dst + c + k, v);
+            }
+          }
         }
       }
-      tc::fence_before();  // the reads of O come before the P that lets it be overwritten
+      // neither group goes on before the other has read its O and maxima
+      tc::fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar_y[g]);
+      if (!(ok = wait(&bar_y[1 - g], n_split & 1))) break;
+      ++n_split;
     }
     if (!ok && lane == 0) {
       flag_error(pl.hdr + kErrWord, kErrTimeout);
@@ -715,10 +844,8 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       const uint32_t tS = tmem + kTmemS + g * kTile, tO = tmem + g * 128;
       uint32_t n_slot = 0, n_job = 0, n_piece = 0, n_turn = 0, ph_tma = 0, ph_cp = 0;
       bool owed = false;
-      for (int64_t u = u_begin; u < u_end && ok;) {
-        const Piece pc = piece_at(pl, u, u_end, U, n_items, slots_head, cta);
-        u = pc.next;
-        if (pc.nt == 0) continue;
+      while (walk.more() && ok) {
+        const Piece pc = walk.next();
         const int by_tma = tma_tiles(pc);
         const int my_jobs = g ? pc.jobs1 : pc.jobs0;
         // K of tile t has landed already (no wait, no phase taken)
@@ -858,10 +985,8 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       uint32_t n_slot = 0, n_piece = 0;
       uint32_t ph_go = 0;
       uint32_t tma_used = 0, tma_count = 0;  // by slot: any TMA copy, their number modulo two
-      for (int64_t u = u_begin; u < u_end && ok;) {
-        const Piece pc = piece_at(pl, u, u_end, U, n_items, slots_head, cta);
-        u = pc.next;
-        if (pc.nt == 0) continue;
+      while (walk.more() && ok) {
+        const Piece pc = walk.next();
         // physical row of this lane's token of tile t (-1: none)
         const int32_t* bt = block_table + (int64_t)pc.it.bt_row * sh.max_pages;
         auto token_row = [&](int t) -> int {
@@ -1043,22 +1168,21 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __nv_bfloat16* s_kv = reinterpret_cast<__nv_bfloat16*>(smem_raw);
   int32_t* s_row = reinterpret_cast<int32_t*>(smem_raw + (size_t)kNarrowStages * 2 * STAGE * 2);
-  int32_t* s_pre = s_row + kNarrowRowCap;  // [B + 1]
+  int32_t* s_pre = s_row + kNarrowRowCap;  // [B + 1] own tokens before each request
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = sh.B, ngroups = sh.Hkv / HG;
   // after the wide kernel the plan is complete (its CTAs waited for it before
   // they let this grid start), and this grid only waits for it at its end
   if (wait_first) pdl_wait();
   pdl_launch_dependents();
-  const int Treq = pl.hdr[kTokens];
+  const int Treq = pl.hdr[kTokens], grid = pl.hdr[kNarrowCtas];
   const int64_t T = (int64_t)Treq * ngroups;
-  const int grid = used_grid(T, gridDim.x, kNarrowLeast);
   const int cta = blockIdx.x;
-  if (T == 0 || cta >= grid) {
+  for (int i = tid; i <= B; i += NT) s_pre[i] = pl.npre[i];
+  if (cta >= grid) {
     if (!wait_first) pdl_wait();
     return;
   }
-  for (int i = tid; i <= B; i += NT) s_pre[i] = pl.npre[i];
   __syncthreads();
   const int64_t lo = range_lo(T, cta, grid), hi = range_lo(T, cta + 1, grid);
 
@@ -1279,112 +1403,123 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
 }
 
 // ----------------------------------------------------------------- merge ---
-// A warp a (request, query token, head).  The parts: the prefix item's partials
-// (every CTA whose range touches the item; two softmax groups each when the
-// item has one row block), and the own tokens' partials of either kernel.
+// A warp a (request, query token, head).  The parts: the group's prefix items
+// and the request's own (each cut of a token range lies in the ranges of one or
+// two CTAs), or the narrow CTAs that its own tokens are spread over.
 template <int D>
 __global__ void __launch_bounds__(128)
 k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restrict__ wo,
                const float2* __restrict__ nml, const float* __restrict__ no,
                __nv_bfloat16* __restrict__ out, float* __restrict__ lse, PrefixShape sh) {
   constexpr int V = D / 32;  // output values a lane
+  constexpr int kBatch = 8;  // partial rows in flight
   const float kNegInf = __int_as_float(0xff800000);
   const int lane = threadIdx.x & 31;
-  const int64_t row = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
   pdl_launch_dependents();
-  pdl_wait();
-  if (row >= (int64_t)sh.B * sh.Nq * sh.Hq) return;
-  const int h = (int)(row % sh.Hq), b = (int)(row / sh.Hq / sh.Nq), qi = (int)(row / sh.Hq % sh.Nq);
+  const int h = row % sh.Hq, bq = row / sh.Hq, b = bq / sh.Nq, qi = bq % sh.Nq;
   const int head = h / sh.G, r = qi * sh.G + h % sh.G;  // row of the request for this KV head
+  pdl_wait();
+  if (b >= sh.B) return;
+  const Request rq = pl.req[b];
+  const int pre = pl.npre[b];
+  const int U = pl.hdr[kUnits], S = pl.hdr[kShare], slots_head = pl.hdr[kSlots];
+  const int Treq = pl.hdr[kTokens], ngrid = pl.hdr[kNarrowCtas];
 
-  // up to three runs of partials: base row, stride a CTA, CTAs, groups a CTA
-  int64_t base[2] = {0, 0};
-  int count[2] = {0, 0}, halves[2] = {1, 1}, apart[2] = {0, 0};
-  const int U = pl.hdr[kUnits], slots_head = pl.hdr[kSlots];
-  const int64_t total = (int64_t)U * sh.Hkv;
-  const int wgrid = used_grid(total, sh.wide_grid, kWideLeast);
-  auto wide_run = [&](int k, int item, int x) {
-    const Item it = pl.items[item];
-    const int next = pl.items[item + 1].unit0;
-    const int64_t u0 = (int64_t)head * U + it.unit0, u1 = (int64_t)head * U + next;
-    if (u1 <= u0) return;
-    const int c0 = range_owner(u0, total, wgrid), c1 = range_owner(u1 - 1, total, wgrid);
-    base[k] = (int64_t)head * slots_head + it.slot0 + (int64_t)kItemRows * c0 + x;
-    count[k] = c1 - c0 + 1;
-    halves[k] = item_halves(it.nrows);
-    apart[k] = it.nrows;
+  // candidate j of a run of wide items: CTA j % 2 of cut j / 2 (-1: there is none)
+  auto wide_at = [&](int j, int unit, int slot, int rows, int nt, int x) -> int64_t {
+    const int cut = j >> 1, len = min(S, nt - cut * S), k = (rows + kItemRows - 1) / kItemRows;
+    const int blk = x / kItemRows;
+    const int64_t u0 = (int64_t)head * U + unit + (int64_t)cut * S * k + blk * len;
+    const int64_t c0 = u0 / S, c = c0 + (j & 1);
+    if (c > (u0 + len - 1) / S) return -1;
+    return (int64_t)head * slots_head + slot + (int64_t)cut * rows + x + kItemRows * c;
   };
-  const int pitem = pl.pitem[b];
-  if (pitem >= 0) {
-    const int x = pl.prow[b] + r - pl.items[pitem].row0;  // row within the group
-    wide_run(0, pitem + x / kItemRows, x % kItemRows);
-  }
-  const int n_own = pl.npre[b + 1] - pl.npre[b];
-  const float2* ml1 = wml;
-  const float* o1 = wo;
-  int stride1 = kItemRows;
-  if (n_own > 0) {
+  const int n0 = 2 * ((rq.gtiles + S - 1) / S);
+  int n1 = 0, c0 = 0;
+  const int g = sh.narrow ? head / sh.hg : 0;
+  if (rq.own > 0) {
     if (sh.narrow) {
-      const int Treq = pl.hdr[kTokens];
-      const int64_t T = (int64_t)Treq * (sh.Hkv / sh.hg);
-      const int ngrid = used_grid(T, sh.narrow_grid, kNarrowLeast);
-      const int g = head / sh.hg;
-      const int64_t f0 = (int64_t)g * Treq + pl.npre[b], f1 = f0 + n_own;
-      const int c0 = range_owner(f0, T, ngrid), c1 = range_owner(f1 - 1, T, ngrid);
-      base[1] = (((int64_t)c0 + (int64_t)g * sh.B + b) * sh.hg + head % sh.hg) * sh.R + r;
-      count[1] = c1 - c0 + 1;
-      stride1 = sh.hg * sh.R;
-      ml1 = nml;
-      o1 = no;
+      const int64_t T = (int64_t)Treq * (sh.Hkv / sh.hg), f0 = (int64_t)g * Treq + pre;
+      c0 = range_owner(f0, T, ngrid);
+      n1 = range_owner(f0 + rq.own - 1, T, ngrid) - c0 + 1;
     } else {
-      wide_run(1, pl.oitem[b] + r / kItemRows, r % kItemRows);
+      n1 = 2 * (((rq.own + kTile - 1) / kTile + S - 1) / S);
     }
   }
-  const int n0 = count[0] * halves[0], n1 = count[1] * halves[1], n = n0 + n1;
+  const int n = n0 + n1;
   auto at = [&](int j) -> int64_t {
-    if (j < n0) return base[0] + (int64_t)(j / halves[0]) * kItemRows + (j % halves[0]) * apart[0];
+    if (j < n0) return wide_at(j, rq.gunit, rq.gslot, rq.grows, rq.gtiles, rq.row + r);
     j -= n0;
-    return base[1] + (int64_t)(j / halves[1]) * stride1 + (j % halves[1]) * apart[1];
+    if (!sh.narrow) return wide_at(j, rq.ounit, rq.oslot, sh.R, (rq.own + kTile - 1) / kTile, r);
+    return (((int64_t)c0 + j + (int64_t)g * sh.B + b) * sh.hg + head % sh.hg) * sh.R + r;
   };
-  float M = kNegInf;
-  for (int j = lane; j < n; j += 32) {
-    const float2 e = __ldcg((j < n0 ? wml : ml1) + at(j));
-    if (e.y != 0.f) M = fmaxf(M, e.x);
-  }
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-  float L = 0.f, acc[V];
+  const float2* ml1 = sh.narrow ? nml : wml;
+  const float* o1 = sh.narrow ? no : wo;
+  // (up to 32 parts at a time; nearly always all of them: the running maximum
+  // rescales what came before)
+  float M = kNegInf, L = 0.f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
   for (int j0 = 0; j0 < n; j0 += 32) {
-    float wgt = 0.f;
-    int64_t my = 0;
-    if (j0 + lane < n) {
-      my = at(j0 + lane);
-      const float2 e = __ldcg((j0 + lane < n0 ? wml : ml1) + my);
-      if (e.y != 0.f) {
-        wgt = exp2f(e.x - M);
-        L += wgt * e.y;
-      }
-    }
-    const int m = n - j0 < 32 ? n - j0 : 32;
-    for (int j = 0; j < m; ++j) {
-      const float f = __shfl_sync(0xffffffffu, wgt, j);
-      const int64_t p = __shfl_sync(0xffffffffu, my, j);
-      if (f == 0.f) continue;
-      const float* src = (j0 + j < n0 ? wo : o1) + p * D + lane * V;
+    const int j = j0 + lane;
+    const int64_t my = j < n ? at(j) : -1;
+    float2 e = make_float2(kNegInf, 0.f);
+    if (my >= 0) e = __ldcg((j < n0 ? wml : ml1) + my);
+    const float* src = (j < n0 ? wo : o1) + (my >= 0 ? my : 0) * D;
+    float m = e.y == 0.f ? kNegInf : e.x;
 #pragma unroll
-      for (int v = 0; v < V; v += 2) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(src + v));
-        acc[v] += f * x.x;
-        acc[v + 1] += f * x.y;
+    for (int s = 16; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    const float m_new = fmaxf(M, m);
+    const float keep = L == 0.f ? 0.f : exp2f(M - m_new);
+    const float wgt = e.y == 0.f ? 0.f : exp2f(e.x - m_new);
+    float l = wgt * e.y;
+#pragma unroll
+    for (int s = 16; s >= 1; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+    if (j0 > 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] *= keep;
+    }
+    L = (L == 0.f ? 0.f : L * keep) + l;
+    M = m_new;
+    // the rows that count, kBatch loads in flight
+    uint32_t left = __ballot_sync(0xffffffffu, wgt != 0.f);
+    while (left) {
+      float x[kBatch][V], f[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        f[u] = 0.f;
+        const int k = left ? __ffs(left) - 1 : 0;
+        const float fk = __shfl_sync(0xffffffffu, wgt, k);
+        const float* p = reinterpret_cast<const float*>(
+            __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(src), k));
+        if (left) {
+          f[u] = fk;
+          if (V == 4) {
+            const float4 t = __ldcg(reinterpret_cast<const float4*>(p) + lane);
+            x[u][0] = t.x;
+            x[u][1] = t.y;
+            x[u][V - 2] = t.z;
+            x[u][V - 1] = t.w;
+          } else {
+            const float2 t = __ldcg(reinterpret_cast<const float2*>(p) + lane);
+            x[u][0] = t.x;
+            x[u][1] = t.y;
+          }
+          left &= left - 1;
+        } else {
+#pragma unroll
+          for (int v = 0; v < V; ++v) x[u][v] = 0.f;
+        }
       }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u)
+#pragma unroll
+        for (int v = 0; v < V; ++v) acc[v] += f[u] * x[u][v];
     }
   }
-#pragma unroll
-  for (int s = 16; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  __nv_bfloat16* dst = out + row * D + lane * V;
+  __nv_bfloat16* dst = out + (int64_t)row * D + lane * V;
 #pragma unroll
   for (int v = 0; v < V; v += 2)
     *reinterpret_cast<__nv_bfloat162*>(dst + v) =
@@ -1403,6 +1538,7 @@ PrefixShape prefix_shape(const pks_prefix_args& a) {
   sh.G = a.Hq / a.Hkv;
   sh.Nq = a.n_queries > 1 ? a.n_queries : 1;
   sh.R = sh.Nq * sh.G;
+  sh.D = a.D;
   sh.page_size = a.page_size;
   sh.max_pages = a.max_pages;
   sh.num_pages = a.num_pages;
@@ -1433,11 +1569,10 @@ PlanPtrs plan_ptrs(void* ws, const PrefixLayout& L) {
   pl.first = pl.eq + step;
   pl.lead = pl.first + step;
   pl.start = pl.lead + step;
-  pl.pitem = pl.start + step;
-  pl.prow = pl.pitem + step;
-  pl.oitem = pl.prow + step;
-  pl.order = pl.oitem + step;
+  pl.order = pl.start + step;
   pl.npre = pl.order + step;
+  pl.req = reinterpret_cast<Request*>(p + L.requests);
+  pl.starts = reinterpret_cast<Start*>(p + L.starts);
   pl.items = reinterpret_cast<Item*>(p + L.items);
   return pl;
 }
@@ -1565,19 +1700,23 @@ PrefixLayout prefix_layout(const pks_prefix_args& a) {
   off += 256;
   L.per_request = off;
   L.per_request_step = up(sizeof(int32_t) * (size_t)(B + 1));
-  off += 10 * L.per_request_step;
-  // items: prefix rows in blocks of 256, each group with a remainder (a group
-  // has two members at least); own tokens when the narrow kernel leaves them
+  off += 7 * L.per_request_step;
+  L.requests = off;
+  off = up(off + sizeof(Request) * (size_t)B);
+  L.starts = off;
+  off = up(off + sizeof(Start) * (size_t)sh.wide_grid);
+  // items of one head: prefix rows in blocks of 256, each group with a remainder
+  // (a group has two members at least), own rows likewise when the narrow kernel
+  // leaves them, and the cuts (at most the CTAs' number)
   const bool groups = a.prefix_group != nullptr;
   const int64_t own_items = sh.narrow ? 0 : B * ((R + kItemRows - 1) / kItemRows);
   L.items = off;
-  off = up(off + sizeof(Item) * (size_t)((groups ? B * R / kItemRows + B / 2 : 0) + own_items + 1));
-  // partial rows of one head: an item of up to 128 rows takes twice its rows
-  const int64_t pref = !groups ? 0 : B * R + (B * R < kRows * (B / 2) ? B * R : kRows * (B / 2));
-  const int64_t tail = R % kItemRows;
-  const int64_t own = sh.narrow ? 0 : B * (R - tail + (tail <= kRows ? 2 * tail : tail));
-  const size_t wide = groups || !sh.narrow
-                          ? (size_t)(sh.Hkv * (pref + own) + (int64_t)kItemRows * sh.wide_grid) : 0;
+  off = up(off + sizeof(Item) * (size_t)((groups ? B * R / kItemRows + B / 2 : 0) + own_items +
+                                         sh.wide_grid + 1));
+  // partial rows: each row once a head for its first cut; the further cuts, at
+  // most one a CTA over all heads; and the places of the CTAs apart
+  const int64_t once = (groups ? B * R : 0) + (sh.narrow ? 0 : B * R);
+  const size_t wide = once ? (size_t)(sh.Hkv * once + 2 * (int64_t)kItemRows * sh.wide_grid) : 0;
   L.wide_ml = off;
   off = up(off + sizeof(float2) * wide);
   L.wide_o = off;
@@ -1594,11 +1733,12 @@ PrefixLayout prefix_layout(const pks_prefix_args& a) {
 
 cudaError_t launch_prefix_plan(const pks_prefix_args& a, const PrefixLayout& L, cudaStream_t s) {
   static bool done[64] = {false};
-  cudaError_t e = allow_smem(k_prefix_plan, 4 * sizeof(int32_t) * kMaxB, done);
+  cudaError_t e = allow_smem(k_prefix_plan, kPlanArrays * sizeof(int32_t) * kMaxB, done);
   if (e != cudaSuccess) return e;
   const PrefixShape sh = prefix_shape(a);
-  return launch_ex(k_prefix_plan, dim3(a.prefix_group ? a.B : 1), dim3(kPlanThreads),
-                   4 * sizeof(int32_t) * (size_t)a.B, s, /*pdl=*/true, /*coop=*/false, a.seq_lens,
+  const int grid = a.B < 2 * sh.wide_grid ? a.B : 2 * sh.wide_grid;
+  return launch_ex(k_prefix_plan, dim3(a.prefix_group ? grid : 1), dim3(kPlanThreads),
+                   kPlanArrays * sizeof(int32_t) * (size_t)a.B, s, /*pdl=*/true, /*coop=*/false, a.seq_lens,
                    a.block_table, a.prefix_group, plan_ptrs(a.workspace, L), sh);
 }
 

@@ -175,7 +175,8 @@ cudaError_t launch_residency(int32_t* state, int32_t num_pages, int32_t capacity
 // ---- attention over shared prefixes (k_prefix.cu): byte offsets inside the
 // workspace; the header's first word is the device error word
 struct PrefixLayout {
-  size_t hdr, per_request, per_request_step, items, wide_ml, wide_o, narrow_ml, narrow_o, total;
+  size_t hdr, per_request, per_request_step, requests, starts, items, wide_ml, wide_o, narrow_ml,
+      narrow_o, total;
 };
 constexpr int kPrefixMaxQueries = 64;
 PrefixLayout prefix_layout(const pks_prefix_args& a);
