@@ -46,7 +46,6 @@ constexpr int kItemRows = 256;    // query rows of an item: two MMAs
 constexpr int kNarrowRows = 16;   // most rows (Nq * G) of the narrow kernel
 constexpr int kNarrowTile = 16;
 constexpr int kNarrowStages = 3;
-constexpr int kNarrowRowCap = 2048;
 constexpr int kMaxB = 4096;
 // Shared tokens below which a group is not worth a prefix item: one wide tile.
 constexpr int kMinShared = kTile;
@@ -62,6 +61,7 @@ struct Item {
 };
 // Where a wide CTA starts.
 struct Start {
+  Item it;
   int head, item;
   int pad[2];
 };
@@ -75,7 +75,8 @@ struct Request {
 
 // plan header words
 constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTokens = 5,
-              kShare = 6, kWideCtas = 7, kNarrowCtas = 8;
+              kShare = 6, kWideCtas = 7, kBig = 8, kPieces = 9, kSmall = 10, kClaim = 11,
+              kBigTokens = 12;  // (64 bits)
 
 struct PlanPtrs {
   int32_t* hdr;
@@ -109,16 +110,40 @@ __device__ __forceinline__ void flag_error(int32_t* err, int code) { atomicCAS(e
 
 constexpr int kWideLeast = 2;                  // tiles a wide CTA takes at least
 constexpr int kNarrowLeast = 2 * kNarrowTile;  // tokens a narrow CTA takes at least
+constexpr int kSmallLeast = 96;                // tokens of a small narrow piece at least
+constexpr int kSmallPerSm = 8;                 // small pieces an SM at most
+// Share of its tokens that the narrow kernel deals out beforehand when the wide
+// kernel runs beside it (in 1/16); the rest goes to whichever SM is free.
+constexpr int kDealt = 11;
 // Estimated nanoseconds an SM spends: on a wide tile with two row blocks (the
 // products of 256 rows, D = 128; half of that at least with D = 64), and on a
 // kilobyte that all SMs stream together (6.8 TB/s over 152 of them).
 constexpr int kPairNs = 1500, kStreamNsPerKb = 23;
 
-__device__ __forceinline__ int64_t range_lo(int64_t total, int c, int n) { return c * total / n; }
-// the CTA whose range holds unit u
-__device__ __forceinline__ int range_owner(int64_t u, int64_t total, int n) {
-  return (int)(((u + 1) * n + total - 1) / total - 1);
-}
+// The narrow kernel's pieces: `big` equal ones that cover the first big_tokens of
+// the T tokens (all heads), one for each CTA that starts at once, and small ones
+// for whichever CTA is free.  A piece has its place among the partials whoever
+// computes it, so that results do not depend on who does.
+struct Pieces {
+  int64_t T, big_tokens;
+  int big, n, small;
+  __device__ __forceinline__ Pieces(const int32_t* hdr, int ngroups)
+      : T((int64_t)hdr[kTokens] * ngroups),
+        big_tokens(*reinterpret_cast<const int64_t*>(hdr + kBigTokens)),
+        big(hdr[kBig]),
+        n(hdr[kPieces]),
+        small(hdr[kSmall]) {}
+  __device__ __forceinline__ int64_t lo(int p) const {
+    if (p < big) return p * big_tokens / big;
+    const int64_t x = big_tokens + (int64_t)(p - big) * small;
+    return x < T ? x : T;
+  }
+  // the piece that holds token f
+  __device__ __forceinline__ int of(int64_t f) const {
+    if (f < big_tokens) return (int)(((f + 1) * big + big_tokens - 1) / big_tokens - 1);
+    return big + (int)((f - big_tokens) / small);
+  }
+};
 
 // ------------------------------------------------------------------ plan ---
 
@@ -321,19 +346,27 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     W = (int)((wide_ns * sh.wide_grid + (wide_ns + narrow_ns) / 2) / (wide_ns + narrow_ns));
     W = max(1, min(sh.wide_grid - 1, W));
   }
-  const int sms_left = total > 0 ? sh.wide_grid - W : sh.wide_grid;
+  const bool beside = narrow_ns > 0 && total > 0;
+  const int sms_left = beside ? sh.wide_grid - W : sh.wide_grid;
   W = (int)min((int64_t)W, (total + kWideLeast - 1) / kWideLeast);
   const int S = total > 0 ? (int)((total + W - 1) / W) : 1;
   W = (int)((total + S - 1) / S);
   if (tid == 0) {
-    const int64_t T = (int64_t)all.w * (sh.Hkv / sh.hg);
-    const int64_t n = min((int64_t)sms_left * (sh.narrow_grid / sh.wide_grid),
-                          (T + kNarrowLeast - 1) / kNarrowLeast);
+    const int64_t T = sh.narrow ? (int64_t)all.w * (sh.Hkv / sh.hg) : 0;
+    const int64_t big_tokens = beside ? T * kDealt / 16 : T;
+    const int64_t big = min((int64_t)sms_left * (sh.narrow_grid / sh.wide_grid),
+                            (big_tokens + kNarrowLeast - 1) / kNarrowLeast);
     pl.hdr[kUnits] = U;
     pl.hdr[kTokens] = all.w;
     pl.hdr[kShare] = S;
     pl.hdr[kWideCtas] = W;
-    pl.hdr[kNarrowCtas] = sh.narrow ? (int)n : 0;
+    pl.hdr[kBig] = (int)big;
+    const int64_t rest = T - big_tokens, most = (int64_t)kSmallPerSm * sh.wide_grid;
+    const int64_t small = max((int64_t)kSmallLeast, (rest + most - 1) / most);
+    *reinterpret_cast<int64_t*>(pl.hdr + kBigTokens) = big_tokens;
+    pl.hdr[kSmall] = (int)small;
+    pl.hdr[kPieces] = (int)(big + (rest + small - 1) / small);
+    pl.hdr[kClaim] = 0;
     pl.npre[B] = all.w;
   }
   // items: a token range in cuts of S tiles, every row block of a cut in turn
@@ -412,6 +445,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
       const int64_t u0 = (int64_t)h * U + it.unit0, c = (u0 + S - 1) / S;
       if (c * S < u0 + nt) {
         Start st = {};
+        st.it = it;
         st.head = h;
         st.item = i;
         pl.starts[c] = st;
@@ -510,13 +544,14 @@ struct Piece {
 // A CTA's walk over its tiles; every role walks the same pieces.
 struct Walk {
   const Item* items;
+  Item it;              // of u (loaded a piece ahead)
   int64_t u, end;       // next tile and the CTA's last + 1, over all heads
-  int head, item;       // the item of u
+  int head, item;
   int U, n_items, slots_head, cta;
   __device__ __forceinline__ bool more() const { return u < end; }
   __device__ __forceinline__ Piece next() {
     Piece p;
-    p.it = items[item];
+    p.it = it;
     p.head = head;
     const int nt = (p.it.t1 - p.it.t0 + kTile - 1) / kTile;
     p.t_lo = (int)(u - ((int64_t)head * U + p.it.unit0));
@@ -530,6 +565,7 @@ struct Walk {
       item = 0;
       ++head;
     }
+    if (more()) it = items[item];
     return p;
   }
 };
@@ -579,7 +615,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       tc::mbar_init(&bar_go[i], 1);
       tc::mbar_init(&bar_free[i], 2);
     }
-    tc::mbar_init(&bar_q, kLoadThreads / 32);
+    tc::mbar_init(&bar_q, kLoadThreads / 32 - 1);
     tc::mbar_init(&bar_qfree, 2);
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&bar_s[i], 1);
@@ -611,6 +647,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     walk.n_items = pl.hdr[kItems];
     walk.slots_head = pl.hdr[kSlots];
     walk.cta = cta;
+    walk.it = st.it;
     walk.head = st.head;
     walk.item = st.item;
     const int64_t total = (int64_t)walk.U * sh.Hkv;
@@ -982,13 +1019,30 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
       };
+      // first row of this lane's box of an item's tile, when it comes by TMA (warp
+      // 0; lane b * kBlk + j copies column block j of box b; a bad page gives
+      // zeros, from beyond the pool)
+      const int n_box = sh.box ? kTile / sh.box : 0, my_box = lane / W::kBlk;
+      auto box_row = [&](const Item& it, int tile) -> int {
+        if (my_box >= n_box || it.t0 % sh.box != 0 || it.t0 + (tile + 1) * kTile > it.t1) return 0;
+        const int tok = it.t0 + tile * kTile + my_box * sh.box;
+        const int page = block_table[(int64_t)it.bt_row * sh.max_pages + tok / sh.page_size];
+        if ((unsigned)page >= (unsigned)sh.num_pages) {
+          flag_error(pl.hdr + kErrWord, kErrPage);
+          return sh.num_pages * sh.page_size;
+        }
+        return page * sh.page_size + tok % sh.page_size;
+      };
       uint32_t n_slot = 0, n_piece = 0;
       uint32_t ph_go = 0;
       uint32_t tma_used = 0, tma_count = 0;  // by slot: any TMA copy, their number modulo two
+      int row = lw == 0 && walk.more()
+                    ? box_row(walk.it, (int)(walk.u - ((int64_t)walk.head * walk.U + walk.it.unit0)))
+                    : 0;
       while (walk.more() && ok) {
         const Piece pc = walk.next();
-        // physical row of this lane's token of tile t (-1: none)
         const int32_t* bt = block_table + (int64_t)pc.it.bt_row * sh.max_pages;
+        // physical row of this lane's token of tile t (-1: none)
         auto token_row = [&](int t) -> int {
           const int tok = pc.it.t0 + (pc.t_lo + t) * kTile + lw * 32 + lane;
           if (tok >= pc.it.t1) return -1;
@@ -1000,45 +1054,38 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           return page * sh.page_size + tok % sh.page_size;
         };
         const int by_tma = tma_tiles(pc);
-        // first row of this lane's box of tile t (warp 0; lane b * kBlk + j copies
-        // column block j of box b; a bad page gives zeros, from beyond the pool)
-        const int n_box = sh.box ? kTile / sh.box : 0, my_box = lane / W::kBlk;
-        auto box_row = [&](int t) -> int {
-          if (t >= by_tma || my_box >= n_box) return 0;
-          const int tok = pc.it.t0 + (pc.t_lo + t) * kTile + my_box * sh.box;
-          const int page = bt[tok / sh.page_size];
-          if ((unsigned)page >= (unsigned)sh.num_pages) {
-            flag_error(pl.hdr + kErrWord, kErrPage);
-            return sh.num_pages * sh.page_size;
-          }
-          return page * sh.page_size + tok % sh.page_size;
-        };
-        int row = lw == 0 ? box_row(0) : 0;
-        if (n_piece > 0 && !(ok = wait(&bar_qfree, (n_piece - 1) & 1))) break;
+        if (lw > 0) {  // Q: warps 1-3 (warp 0 sends the first tiles meanwhile)
+          if (n_piece > 0 && !(ok = wait(&bar_qfree, (n_piece - 1) & 1))) break;
 #pragma unroll 1
-        for (int blk = 0; blk < (pc.pair ? 2 : 1); ++blk) {
-          // query row of this lane: request, query token and head
-          const int x = blk * kRows + lw * 32 + lane;
-          int64_t off = -1;
-          if (x < pc.it.nrows) {
-            const int gr = pc.it.row0 + x;
-            const int b = pc.it.own ? pc.it.bt_row : pl.order[gr / sh.R];
-            const int r = pc.it.own ? gr : gr % sh.R;
-            off = (((int64_t)b * sh.Nq + r / sh.G) * sh.Hq + pc.head * sh.G + r % sh.G) * D;
-          }
+          for (int c = lw - 1; c < (pc.pair ? 8 : 4); c += 3) {
+            // query row of this lane: request, query token and head
+            const int x = c * 32 + lane;
+            int64_t off = -1;
+            if (x < pc.it.nrows) {
+              const int gr = pc.it.row0 + x;
+              const int b = pc.it.own ? pc.it.bt_row : pl.order[gr / sh.R];
+              const int r = pc.it.own ? gr : gr % sh.R;
+              off = (((int64_t)b * sh.Nq + r / sh.G) * sh.Hq + pc.head * sh.G + r % sh.G) * D;
+            }
 #pragma unroll 4
-          for (int i = 0; i < 32; i += kRowsPer) {
-            const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
-            tc::cp_async16(dst_of(sQ + blk * W::kTileBytes, lw * 32 + i + sub),
-                           q + (o >= 0 ? o + cc * 8 : 0), o >= 0 ? 16 : 0);
+            for (int i = 0; i < 32; i += kRowsPer) {
+              const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
+              tc::cp_async16(dst_of(sQ + (c >> 2) * W::kTileBytes, (c & 3) * 32 + i + sub),
+                             q + (o >= 0 ? o + cc * 8 : 0), o >= 0 ? 16 : 0);
+            }
           }
+          tc::cp_async_commit();
+          tc::cp_async_wait<0>();
+          publish(&bar_q);
         }
-        tc::cp_async_commit();
         int waiting = 0;  // tiles copied by cp.async and not published yet
         int done = 0;
         for (int t = 0; t < pc.nt && ok; ++t) {
           if (t >= by_tma) row = token_row(t);
-          const int next_row = lw == 0 ? box_row(t + 1) : 0;
+          // the row of the tile after this one, in the next piece if need be
+          int next_row = 0;
+          if (lw == 0 && (t + 1 < pc.nt || walk.more()))
+            next_row = t + 1 < pc.nt ? box_row(pc.it, pc.t_lo + t + 1) : box_row(walk.it, 0);
 #pragma unroll
           for (int v = 0; v < 2; ++v, ++done) {
             const uint32_t n = n_slot + done, s = n % W::kSlotsN;
@@ -1077,11 +1124,6 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
               }
               tc::cp_async_commit();
               ++waiting;
-            }
-            if (done == 1) {  // Q, behind the first K and V tile
-              if (waiting == 0) tc::cp_async_wait<0>();
-              else tc::cp_async_wait<2>();
-              publish(&bar_q);
             }
             if (waiting > W::kLag) {
               tc::cp_async_wait<W::kLag>();
@@ -1156,6 +1198,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+constexpr int kTileRing = 8;  // tiles described ahead of or behind their use
+
 template <int D, int HG, int NT8>
 __global__ void __launch_bounds__(HG * 32, 1)
 k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
@@ -1167,55 +1211,134 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
   const float kNegInf = __int_as_float(0xff800000);
   extern __shared__ __align__(128) uint8_t smem_raw[];
   __nv_bfloat16* s_kv = reinterpret_cast<__nv_bfloat16*>(smem_raw);
-  int32_t* s_row = reinterpret_cast<int32_t*>(smem_raw + (size_t)kNarrowStages * 2 * STAGE * 2);
-  int32_t* s_pre = s_row + kNarrowRowCap;  // [B + 1] own tokens before each request
+  // [B + 1] own tokens before each request
+  int32_t* s_pre = reinterpret_cast<int32_t*>(smem_raw + (size_t)kNarrowStages * 2 * STAGE * 2);
+  // a tile: n tokens (0: no more) from own position p0 of request b for the
+  // heads of group g, in a piece; kFirst / kLast of its request in the piece
+  struct Tile {
+    int n, b, g, p0, own, piece, flags, pad;
+  };
+  constexpr int kFirst = 1, kLast = 2;
+  __shared__ Tile s_tile[kTileRing];
+  __shared__ int32_t s_row[kTileRing][TILE];  // physical rows (-1: none)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int B = sh.B, ngroups = sh.Hkv / HG;
   // after the wide kernel the plan is complete (its CTAs waited for it before
   // they let this grid start), and this grid only waits for it at its end
   if (wait_first) pdl_wait();
   pdl_launch_dependents();
-  const int Treq = pl.hdr[kTokens], grid = pl.hdr[kNarrowCtas];
-  const int64_t T = (int64_t)Treq * ngroups;
+  const Pieces pieces(pl.hdr, ngroups);
+  const int Treq = pl.hdr[kTokens];
   const int cta = blockIdx.x;
   for (int i = tid; i <= B; i += NT) s_pre[i] = pl.npre[i];
-  if (cta >= grid) {
+  if (cta >= pieces.big && pieces.n == pieces.big) {
     if (!wait_first) pdl_wait();
     return;
   }
   __syncthreads();
-  const int64_t lo = range_lo(T, cta, grid), hi = range_lo(T, cta + 1, grid);
 
-  struct Cursor {
-    int g, b, p;
-    int64_t end;
+  // ---- the tiles in order, described by warp 0: its cursor, the same in all lanes
+  int piece = -1, claimed = 0;
+  int64_t f = 0, f_end = 0, seg_end = 0;  // flattened position, end of the piece and request
+  int cb = 0, cg = 0, cstart = 0;
+  auto claim = [&]() {  // (used a piece later, so that its latency is hidden)
+    if (lane == 0) claimed = pieces.big + atomicAdd(pl.hdr + kClaim, 1);
   };
-  auto locate = [&](int64_t f) {
-    Cursor c;
-    c.g = (int)(f / Treq);
-    const int fb = (int)(f - (int64_t)c.g * Treq);
+  auto open_piece = [&](int p) {
+    piece = p;
+    if (p >= pieces.n) return;
+    f = pieces.lo(p);
+    f_end = pieces.lo(p + 1);
+    cg = (int)(f / Treq);
+    const int fb = (int)(f - (int64_t)cg * Treq);
     int l = 0, h = B - 1;
     while (l < h) {
       const int mid = (l + h + 1) >> 1;
       if (s_pre[mid] <= fb) l = mid; else h = mid - 1;
     }
-    c.b = l;
-    c.p = fb - s_pre[l];
-    c.end = (int64_t)c.g * Treq + s_pre[l + 1];
-    return c;
+    cb = l;
+    seg_end = (int64_t)cg * Treq + s_pre[cb + 1];
+    cstart = pl.start[cb];
+    claim();
   };
+  // describe tile k; returns its lane's page, still to come, and the row in it
+  auto describe = [&](int k, int& page, int& in_page) {
+    page = -1;
+    in_page = 0;
+    if (piece < pieces.n && f == f_end) open_piece(__shfl_sync(0xffffffffu, claimed, 0));
+    Tile t = {};
+    if (piece < pieces.n) {
+      bool first = f == pieces.lo(piece);
+      while (f == seg_end) {  // the next request with own tokens
+        if (++cb == B) {
+          cb = 0;
+          ++cg;
+        }
+        seg_end = (int64_t)cg * Treq + s_pre[cb + 1];
+        cstart = pl.start[cb];
+      }
+      const int64_t seg_lo = (int64_t)cg * Treq + s_pre[cb];
+      first |= f == seg_lo;
+      int64_t e = f + TILE;
+      if (seg_end < e) e = seg_end;
+      if (f_end < e) e = f_end;
+      t.n = (int)(e - f);
+      t.b = cb;
+      t.g = cg;
+      t.p0 = (int)(f - seg_lo);
+      t.own = s_pre[cb + 1] - s_pre[cb];
+      t.piece = piece;
+      t.flags = (first ? kFirst : 0) | (e == seg_end || e == f_end ? kLast : 0);
+      if (lane < t.n) {
+        const int tok = cstart + t.p0 + lane;
+        page = block_table[(int64_t)cb * sh.max_pages + tok / sh.page_size];
+        in_page = tok % sh.page_size;
+      }
+      f = e;
+    }
+    if (lane == 0) s_tile[k % kTileRing] = t;
+    if (lane >= t.n) in_page = -1;
+  };
+  auto place = [&](int k, int page, int in_page) {
+    if (lane >= TILE) return;
+    int row = -1;
+    if (in_page >= 0) {
+      if ((unsigned)page < (unsigned)sh.num_pages) row = page * sh.page_size + in_page;
+      else flag_error(pl.hdr + kErrWord, kErrPage);
+    }
+    s_row[k % kTileRing][lane] = row;
+  };
+  auto load = [&](int k) {
+    const Tile& t = s_tile[k % kTileRing];
+    if (t.n > 0) {
+      __nv_bfloat16* sk = s_kv + (size_t)(k % kNarrowStages) * 2 * STAGE;
+      __nv_bfloat16* sv = sk + STAGE;
+      const int g = t.g;
+#pragma unroll 4
+      for (int idx = tid; idx < TILE * HG * CH; idx += NT) {
+        const int r = idx / (HG * CH), rem = idx % (HG * CH), hh = rem / CH, c = rem % CH;
+        const int row = s_row[k % kTileRing][r];
+        const int off = (r * HG + hh) * D + ((c ^ (r & 7)) << 3);
+        const int64_t src = row >= 0 ? ((int64_t)row * sh.Hkv + g * HG + hh) * D + c * 8 : 0;
+        const int bytes = row >= 0 ? 16 : 0;
+        tc::cp_async16(tc::smem_u32(sk + off), kv_k + src, bytes);
+        tc::cp_async16(tc::smem_u32(sv + off), kv_v + src, bytes);
+      }
+    }
+    tc::cp_async_commit();
+  };
+
   const int g8 = lane >> 2, t4 = lane & 3;
   uint32_t qb[NT8][KS][2];
   float o[NT8][MT][4], m_h[NT8][2], l_h[NT8][2];
   int lim[NT8][2];  // own tokens that the thread's two rows see
-  auto begin = [&](const Cursor& c) {
-    const int head = c.g * HG + warp;
-    const int n = s_pre[c.b + 1] - s_pre[c.b];
+  auto begin = [&](const Tile& t) {
+    const int head = t.g * HG + warp;
 #pragma unroll
     for (int nt = 0; nt < NT8; ++nt) {
       const int j = nt * 8 + g8;
       const __nv_bfloat16* src =
-          q + (((int64_t)c.b * sh.Nq + j / sh.G) * sh.Hq + (int64_t)head * sh.G + j % sh.G) * D + t4 * 2;
+          q + (((int64_t)t.b * sh.Nq + j / sh.G) * sh.Hq + (int64_t)head * sh.G + j % sh.G) * D + t4 * 2;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         qb[nt][ks][0] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
@@ -1227,12 +1350,12 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
       for (int e = 0; e < 2; ++e) {
         m_h[nt][e] = kNegInf;
         l_h[nt][e] = 0.f;
-        lim[nt][e] = sh.causal ? n - sh.Nq + (nt * 8 + 2 * t4 + e) / sh.G + 1 : n;
+        lim[nt][e] = sh.causal ? t.own - sh.Nq + (nt * 8 + 2 * t4 + e) / sh.G + 1 : t.own;
       }
     }
   };
-  auto finish = [&](const Cursor& c) {
-    const int64_t base = (((int64_t)cta + (int64_t)c.g * B + c.b) * HG + warp) * sh.R;
+  auto finish = [&](const Tile& t) {
+    const int64_t base = (((int64_t)t.piece + (int64_t)t.g * B + t.b) * HG + warp) * sh.R;
 #pragma unroll
     for (int nt = 0; nt < NT8; ++nt)
 #pragma unroll
@@ -1253,152 +1376,106 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
       }
   };
 
-  int64_t pos = lo;
-  Cursor cur{0, 0, 0, 0};
-  bool open = false;
-  for (int64_t chunk_lo = lo; chunk_lo < hi; chunk_lo += kNarrowRowCap) {
-    const int64_t chunk_hi = hi < chunk_lo + kNarrowRowCap ? hi : chunk_lo + kNarrowRowCap;
-    auto resolve = [&](int64_t f0, int64_t f1) {
-      for (int64_t f = f0 + tid; f < f1; f += NT) {
-        const Cursor c = locate(f);
-        const int t = pl.start[c.b] + c.p;
-        const int page = block_table[(int64_t)c.b * sh.max_pages + t / sh.page_size];
-        int row = -1;
-        if ((unsigned)page < (unsigned)sh.num_pages) row = page * sh.page_size + t % sh.page_size;
-        else flag_error(pl.hdr + kErrWord, kErrPage);
-        s_row[f - chunk_lo] = row;
-      }
-    };
-    constexpr int kFirst = NT > (kNarrowStages - 1) * TILE ? NT : (kNarrowStages - 1) * TILE;
-    const int64_t early = chunk_hi < chunk_lo + kFirst ? chunk_hi : chunk_lo + kFirst;
-    resolve(chunk_lo, early);
-    __syncthreads();
-    int64_t ld = chunk_lo, ld_end = locate(chunk_lo).end;
-    auto load_next = [&](int stage) {
-      if (ld >= chunk_hi) return;
-      if (ld >= ld_end) ld_end = locate(ld).end;
-      int64_t e = ld + TILE;
-      if (ld_end < e) e = ld_end;
-      if (chunk_hi < e) e = chunk_hi;
-      const int n = (int)(e - ld), g = (int)(ld / Treq), rbase = (int)(ld - chunk_lo);
-      __nv_bfloat16* sk = s_kv + (size_t)stage * 2 * STAGE;
-      __nv_bfloat16* sv = sk + STAGE;
-#pragma unroll 4
-      for (int idx = tid; idx < TILE * HG * CH; idx += NT) {
-        const int r = idx / (HG * CH), rem = idx % (HG * CH), hh = rem / CH, c = rem % CH;
-        const int row = r < n ? s_row[rbase + r] : -1;
-        const int off = (r * HG + hh) * D + ((c ^ (r & 7)) << 3);
-        const int64_t src = row >= 0 ? ((int64_t)row * sh.Hkv + g * HG + hh) * D + c * 8 : 0;
-        const int bytes = row >= 0 ? 16 : 0;
-        tc::cp_async16(tc::smem_u32(sk + off), kv_k + src, bytes);
-        tc::cp_async16(tc::smem_u32(sv + off), kv_v + src, bytes);
-      }
-      ld = e;
-    };
-    int n_tiles = 0;
-    for (int64_t f = chunk_lo, se = ld_end; f < chunk_hi; ++n_tiles) {
-      if (f >= se) se = locate(f).end;
-      int64_t e = f + TILE;
-      if (se < e) e = se;
-      f = chunk_hi < e ? chunk_hi : e;
+  // ---- tile k is described (its table entry requested) while tile k - 4 is
+  // computed, its rows are placed one tile later and its copies sent two before
+  // its use
+  int page = -1, in_page = -1;
+  if (warp == 0) {
+    if (cta < pieces.big) {
+      open_piece(cta);
+    } else {
+      claim();
+      open_piece(__shfl_sync(0xffffffffu, claimed, 0));
     }
+    int pg[3], ip[3];
 #pragma unroll
-    for (int st = 0; st < kNarrowStages - 1; ++st) {
-      if (st < n_tiles) load_next(st);
-      tc::cp_async_commit();
+    for (int k = 0; k < 3; ++k) describe(k, pg[k], ip[k]);
+    describe(3, page, in_page);
+#pragma unroll
+    for (int k = 0; k < 3; ++k) place(k, pg[k], ip[k]);
+  }
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kNarrowStages - 1; ++k) load(k);
+  for (int k = 0;; ++k) {
+    const Tile t = s_tile[k % kTileRing];
+    if (t.n == 0) break;
+    load(k + kNarrowStages - 1);
+    if (warp == 0) {
+      place(k + 3, page, in_page);
+      describe(k + 4, page, in_page);
     }
-    resolve(early, chunk_hi);
+    if (t.flags & kFirst) begin(t);
+    tc::cp_async_wait<kNarrowStages - 1>();
     __syncthreads();
-    for (int tile = 0; tile < n_tiles; ++tile) {
-      if (tile + kNarrowStages - 1 < n_tiles) load_next((tile + kNarrowStages - 1) % kNarrowStages);
-      tc::cp_async_commit();
-      if (!open || pos >= cur.end) {
-        cur = locate(pos);
-        begin(cur);
-        open = true;
+    const __nv_bfloat16* sk = s_kv + (size_t)(k % kNarrowStages) * 2 * STAGE;
+    const __nv_bfloat16* sv = sk + STAGE;
+    float sacc[2][NT8][4];
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+      for (int nt = 0; nt < NT8; ++nt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) sacc[c][nt][i] = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
+      const int chunk = 2 * ks + (lane >> 4);
+      uint32_t a[4];
+      ldsm_x4(tc::smem_u32(sk + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
+#pragma unroll
+      for (int nt = 0; nt < NT8; ++nt) mma_16816(sacc[ks & 1][nt], a, qb[nt][ks][0], qb[nt][ks][1]);
+    }
+    const bool v0 = s_row[k % kTileRing][g8] >= 0, v1 = s_row[k % kTileRing][g8 + 8] >= 0;
+    uint32_t pb[NT8][2];
+#pragma unroll
+    for (int nt = 0; nt < NT8; ++nt) {
+      float x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool v = (i < 2 ? v0 : v1) && t.p0 + g8 + (i < 2 ? 0 : 8) < lim[nt][i & 1];
+        x[i] = v ? (sacc[0][nt][i] + sacc[1][nt][i]) * scale_log2 : kNegInf;
       }
-      int64_t e64 = pos + TILE;
-      if (cur.end < e64) e64 = cur.end;
-      if (chunk_hi < e64) e64 = chunk_hi;
-      const int n = (int)(e64 - pos), rbase = (int)(pos - chunk_lo);
-      const int p0 = (int)(pos - (cur.end - (s_pre[cur.b + 1] - s_pre[cur.b])));  // own position
-      tc::cp_async_wait<kNarrowStages - 1>();
-      __syncthreads();
-      const __nv_bfloat16* sk = s_kv + (size_t)(tile % kNarrowStages) * 2 * STAGE;
-      const __nv_bfloat16* sv = sk + STAGE;
-      float sacc[2][NT8][4];
+      float al[2], p[4];
 #pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int nt = 0; nt < NT8; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) sacc[c][nt][i] = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
-        const int chunk = 2 * ks + (lane >> 4);
-        uint32_t a[4];
-        ldsm_x4(tc::smem_u32(sk + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
-#pragma unroll
-        for (int nt = 0; nt < NT8; ++nt) mma_16816(sacc[ks & 1][nt], a, qb[nt][ks][0], qb[nt][ks][1]);
+      for (int e = 0; e < 2; ++e) {
+        float mx = fmaxf(x[e], x[e + 2]);
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+        const float mn = fmaxf(m_h[nt][e], mx);
+        al[e] = mn == kNegInf ? 1.f : exp2f(m_h[nt][e] - mn);
+        p[e] = x[e] == kNegInf ? 0.f : ex2(x[e] - mn);
+        p[e + 2] = x[e + 2] == kNegInf ? 0.f : ex2(x[e + 2] - mn);
+        m_h[nt][e] = mn;
       }
-      const bool v0 = g8 < n && s_row[rbase + g8] >= 0;
-      const bool v1 = g8 + 8 < n && s_row[rbase + g8 + 8] >= 0;
-      uint32_t pb[NT8][2];
-#pragma unroll
-      for (int nt = 0; nt < NT8; ++nt) {
-        float x[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const bool v = (i < 2 ? v0 : v1) && p0 + g8 + (i < 2 ? 0 : 8) < lim[nt][i & 1];
-          x[i] = v ? (sacc[0][nt][i] + sacc[1][nt][i]) * scale_log2 : kNegInf;
-        }
-        float al[2], p[4];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float mx = fmaxf(x[e], x[e + 2]);
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float mn = fmaxf(m_h[nt][e], mx);
-          al[e] = mn == kNegInf ? 1.f : exp2f(m_h[nt][e] - mn);
-          p[e] = x[e] == kNegInf ? 0.f : ex2(x[e] - mn);
-          p[e + 2] = x[e + 2] == kNegInf ? 0.f : ex2(x[e + 2] - mn);
-          m_h[nt][e] = mn;
-        }
-        l_h[nt][0] = l_h[nt][0] * al[0] + (p[0] + p[2]);
-        l_h[nt][1] = l_h[nt][1] * al[1] + (p[1] + p[3]);
-        // rounded to bf16 for the second product only
-        const uint32_t lo2 = pack_bf16(p[0], p[1]), hi2 = pack_bf16(p[2], p[3]);
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          o[nt][mt][0] *= al[0];
-          o[nt][mt][1] *= al[1];
-          o[nt][mt][2] *= al[0];
-          o[nt][mt][3] *= al[1];
-        }
-        pb[nt][0] = movmatrix_t(lo2);
-        pb[nt][1] = movmatrix_t(hi2);
-      }
+      l_h[nt][0] = l_h[nt][0] * al[0] + (p[0] + p[2]);
+      l_h[nt][1] = l_h[nt][1] * al[1] + (p[1] + p[3]);
+      // rounded to bf16 for the second product only
+      const uint32_t lo2 = pack_bf16(p[0], p[1]), hi2 = pack_bf16(p[2], p[3]);
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        const int row = (lane & 7) + ((lane >> 4) << 3);
-        const int chunk = 2 * mt + ((lane >> 3) & 1);
-        uint32_t a[4];
-        ldsm_x4_t(tc::smem_u32(sv + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
-#pragma unroll
-        for (int nt = 0; nt < NT8; ++nt) mma_16816(o[nt][mt], a, pb[nt][0], pb[nt][1]);
+        o[nt][mt][0] *= al[0];
+        o[nt][mt][1] *= al[1];
+        o[nt][mt][2] *= al[0];
+        o[nt][mt][3] *= al[1];
       }
-      __syncthreads();
-      pos += n;
-      if (pos == cur.end || pos == hi) {
-        finish(cur);
-        open = false;
-      }
+      pb[nt][0] = movmatrix_t(lo2);
+      pb[nt][1] = movmatrix_t(hi2);
     }
-    tc::cp_async_wait<0>();
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int row = (lane & 7) + ((lane >> 4) << 3);
+      const int chunk = 2 * mt + ((lane >> 3) & 1);
+      uint32_t a[4];
+      ldsm_x4_t(tc::smem_u32(sv + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
+#pragma unroll
+      for (int nt = 0; nt < NT8; ++nt) mma_16816(o[nt][mt], a, pb[nt][0], pb[nt][1]);
+    }
+    if (t.flags & kLast) finish(t);
     __syncthreads();
   }
+  tc::cp_async_wait<0>();
   if (!wait_first) pdl_wait();
 }
 
@@ -1424,7 +1501,9 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   const Request rq = pl.req[b];
   const int pre = pl.npre[b];
   const int U = pl.hdr[kUnits], S = pl.hdr[kShare], slots_head = pl.hdr[kSlots];
-  const int Treq = pl.hdr[kTokens], ngrid = pl.hdr[kNarrowCtas];
+  const int Treq = pl.hdr[kTokens];
+  const Pieces pieces(pl.hdr, sh.Hkv / sh.hg);
+  if (row == 0 && lane == 0) pl.hdr[kClaim] = 0;  // for the next call by this plan
 
   // candidate j of a run of wide items: CTA j % 2 of cut j / 2 (-1: there is none)
   auto wide_at = [&](int j, int unit, int slot, int rows, int nt, int x) -> int64_t {
@@ -1440,9 +1519,9 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   const int g = sh.narrow ? head / sh.hg : 0;
   if (rq.own > 0) {
     if (sh.narrow) {
-      const int64_t T = (int64_t)Treq * (sh.Hkv / sh.hg), f0 = (int64_t)g * Treq + pre;
-      c0 = range_owner(f0, T, ngrid);
-      n1 = range_owner(f0 + rq.own - 1, T, ngrid) - c0 + 1;
+      const int64_t f0 = (int64_t)g * Treq + pre;
+      c0 = pieces.of(f0);
+      n1 = pieces.of(f0 + rq.own - 1) - c0 + 1;
     } else {
       n1 = 2 * (((rq.own + kTile - 1) / kTile + S - 1) / S);
     }
@@ -1551,8 +1630,8 @@ PrefixShape prefix_shape(const pks_prefix_args& a) {
   if (sh.box < 8) sh.box = 0;
   // shared memory holds one narrow CTA of eight heads an SM, more of fewer
   const size_t stage = (size_t)2 * kNarrowTile * sh.hg * a.D * sizeof(__nv_bfloat16);
-  const size_t smem = kNarrowStages * stage + sizeof(int32_t) * (size_t)(kNarrowRowCap + a.B + 1);
-  int per_sm = (int)((size_t)(227 * 1024) / (smem + 1024));
+  const size_t smem = kNarrowStages * stage + sizeof(int32_t) * (size_t)(a.B + 1);
+  int per_sm = (int)((size_t)(227 * 1024) / (smem + 2048));
   if (per_sm > 4) per_sm = 4;
   sh.narrow_grid = device_sm_count() * (per_sm < 1 ? 1 : per_sm);
   return sh;
@@ -1643,10 +1722,10 @@ cudaError_t launch_narrow(const pks_prefix_args& a, const PrefixLayout& L, const
   static bool done[64] = {false};
   auto kern = k_prefix_narrow<D, HG, NT8>;
   constexpr size_t kStages = (size_t)kNarrowStages * 2 * kNarrowTile * HG * D * sizeof(__nv_bfloat16);
-  cudaError_t e = allow_smem(kern, kStages + sizeof(int32_t) * (kNarrowRowCap + kMaxB + 1), done);
+  cudaError_t e = allow_smem(kern, kStages + sizeof(int32_t) * (kMaxB + 1), done);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  const size_t smem = kStages + sizeof(int32_t) * (size_t)(kNarrowRowCap + a.B + 1);
+  const size_t smem = kStages + sizeof(int32_t) * (size_t)(a.B + 1);
   return launch_ex(kern, dim3(sh.narrow_grid), dim3(HG * 32), smem, s, /*pdl=*/true,
                    /*coop=*/false, a.block_table, static_cast<const __nv_bfloat16*>(a.q),
                    static_cast<const __nv_bfloat16*>(a.kv_k),
@@ -1721,8 +1800,9 @@ PrefixLayout prefix_layout(const pks_prefix_args& a) {
   off = up(off + sizeof(float2) * wide);
   L.wide_o = off;
   off = up(off + sizeof(float) * wide * (size_t)a.D);
-  const size_t narrow = sh.narrow ? (size_t)((sh.narrow_grid + (int64_t)(sh.Hkv / sh.hg) * B) *
-                                             sh.hg * R) : 0;
+  const int64_t small = groups ? (int64_t)kSmallPerSm * sh.wide_grid : 0;
+  const size_t narrow = sh.narrow ? (size_t)((sh.narrow_grid + small +
+                                              (int64_t)(sh.Hkv / sh.hg) * B) * sh.hg * R) : 0;
   L.narrow_ml = off;
   off = up(off + sizeof(float2) * narrow);
   L.narrow_o = off;
