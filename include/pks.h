@@ -431,7 +431,7 @@ pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_str
  * finite; rows at or beyond len_b are never read.
  * ---------------------------------------------------------------------- */
 typedef struct pks_prefix_args {
-  int32_t B;              /* requests; B * Nq <= 4096 */
+  int32_t B;              /* requests; B * Nq <= 4096, B * max_pages * page_size <= 2^34 */
   int32_t Hq, Hkv;        /* 1 <= Hq / Hkv <= 16 */
   int32_t D;              /* 64 or 128 */
   int32_t page_size, max_pages, num_pages;

@@ -45,7 +45,6 @@ constexpr int kRows = 128;        // query rows of one MMA
 constexpr int kItemRows = 256;    // query rows of an item: two MMAs
 constexpr int kNarrowRows = 16;   // most rows (Nq * G) of the narrow kernel
 constexpr int kNarrowTile = 16;
-constexpr int kNarrowStages = 3;
 constexpr int kMaxB = 4096;
 // Shared tokens below which a group is not worth a prefix item: one wide tile.
 constexpr int kMinShared = kTile;
@@ -74,16 +73,16 @@ struct Request {
 };
 
 // plan header words
-constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTokens = 5,
+constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTiles = 5,
               kShare = 6, kWideCtas = 7, kBig = 8, kPieces = 9, kSmall = 10, kClaim = 11,
-              kBigTokens = 12;  // (64 bits)
+              kBigTiles = 12;  // (64 bits)
 
 struct PlanPtrs {
   int32_t* hdr;
   int32_t *lens, *eq, *first, *lead;   // per request
   int32_t *start;                      // first own token
   int32_t *order;                      // members in group order
-  int32_t *npre;                       // [B + 1] own tokens before each request
+  int32_t *npre;                       // [B + 1] narrow tiles before each request
   Request* req;
   Start* starts;                       // per wide CTA
   Item* items;
@@ -109,39 +108,41 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ void flag_error(int32_t* err, int code) { atomicCAS(err, 0, code); }
 
 constexpr int kWideLeast = 2;                  // tiles a wide CTA takes at least
-constexpr int kNarrowLeast = 2 * kNarrowTile;  // tokens a narrow CTA takes at least
-constexpr int kSmallLeast = 96;                // tokens of a small narrow piece at least
+constexpr int kNarrowLeast = 2;                // tiles a narrow CTA takes at least
+constexpr int kSmallLeast = 6;                 // tiles of a small narrow piece at least
 constexpr int kSmallPerSm = 8;                 // small pieces an SM at most
-// Share of its tokens that the narrow kernel deals out beforehand when the wide
-// kernel runs beside it (in 1/16); the rest goes to whichever SM is free.
-constexpr int kDealt = 11;
-// Estimated nanoseconds an SM spends: on a wide tile with two row blocks (the
-// products of 256 rows, D = 128; half of that at least with D = 64), and on a
-// kilobyte that all SMs stream together (6.8 TB/s over 152 of them).
-constexpr int kPairNs = 1500, kStreamNsPerKb = 23;
+// Beside the wide kernel, a narrow CTA is dealt this share (in 1/16) of what it
+// could stream in the time estimated for all; the rest goes to whichever SM is
+// free.
+constexpr int kDealt = 10;
+// Estimated nanoseconds an SM spends with D = 128 (half with D = 64): on a wide
+// tile with two row blocks (its products), on one with a single block (its bytes,
+// while the narrow kernel loads the memory too), and on a kilobyte streamed by the
+// narrow kernel.
+constexpr int kPairNs = 1750, kSingleNs = 2600, kStreamNsPerKb = 24;
 
-// The narrow kernel's pieces: `big` equal ones that cover the first big_tokens of
-// the T tokens (all heads), one for each CTA that starts at once, and small ones
+// The narrow kernel's pieces: `big` equal ones that cover the first big_tiles of
+// the T tiles (all heads), one for each CTA that starts at once, and small ones
 // for whichever CTA is free.  A piece has its place among the partials whoever
 // computes it, so that results do not depend on who does.
 struct Pieces {
-  int64_t T, big_tokens;
+  int64_t T, big_tiles;
   int big, n, small;
   __device__ __forceinline__ Pieces(const int32_t* hdr, int ngroups)
-      : T((int64_t)hdr[kTokens] * ngroups),
-        big_tokens(*reinterpret_cast<const int64_t*>(hdr + kBigTokens)),
+      : T((int64_t)hdr[kTiles] * ngroups),
+        big_tiles(*reinterpret_cast<const int64_t*>(hdr + kBigTiles)),
         big(hdr[kBig]),
         n(hdr[kPieces]),
         small(hdr[kSmall]) {}
   __device__ __forceinline__ int64_t lo(int p) const {
-    if (p < big) return p * big_tokens / big;
-    const int64_t x = big_tokens + (int64_t)(p - big) * small;
+    if (p < big) return p * big_tiles / big;
+    const int64_t x = big_tiles + (int64_t)(p - big) * small;
     return x < T ? x : T;
   }
-  // the piece that holds token f
+  // the piece that holds tile f
   __device__ __forceinline__ int of(int64_t f) const {
-    if (f < big_tokens) return (int)(((f + 1) * big + big_tokens - 1) / big_tokens - 1);
-    return big + (int)((f - big_tokens) / small);
+    if (f < big_tiles) return (int)(((f + 1) * big + big_tiles - 1) / big_tiles - 1);
+    return big + (int)((f - big_tiles) / small);
   }
 };
 
@@ -313,6 +314,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   __syncthreads();
   auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
   auto blocks = [](int rows) { return (rows + kItemRows - 1) / kItemRows; };
+  auto single = [](int rows) { return (rows - 1) % kItemRows < kRows ? 1 : 0; };
   // the group (by its first member) that request b takes part in, or -1
   auto joined = [&](int b) {
     const int f = s_first[b];
@@ -321,26 +323,31 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   const int per = (B + kPlanThreads - 1) / kPlanThreads;
   const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
   const int own_blocks = sh.narrow ? 0 : blocks(sh.R);
-  // members, tiles of both kinds, own tokens
+  auto own_tiles = [&](int n) { return sh.narrow ? (n + kNarrowTile - 1) / kNarrowTile : 0; };
+  // members, wide tiles, those with a single row block among them, narrow tiles
   int4 sum = make_int4(0, 0, 0, 0), all;
   for (int b = b_lo; b < b_hi; ++b) {
     if (s_cnt[b] >= 2) {
+      const int rows = s_cnt[b] * sh.R;
       sum.x += s_cnt[b];
-      sum.y += blocks(s_cnt[b] * sh.R) * tiles(s_pre[b]);
+      sum.y += blocks(rows) * tiles(s_pre[b]);
+      sum.z += single(rows) * tiles(s_pre[b]);
     }
     const int f = joined(b), own = s_len[b] - (f >= 0 ? s_pre[f] : 0);
-    sum.z += own_blocks * tiles(own);
-    sum.w += own;
+    sum.y += own_blocks * tiles(own);
+    sum.z += own_blocks ? single(sh.R) * tiles(own) : 0;
+    sum.w += own_tiles(own);
   }
   int4 ex = block_scan_ex(sum, s_red4, all);
-  const int U = all.y + all.z;
+  const int U = all.y;
   // SMs for either kernel by the time they will need, and the tiles a wide CTA
   // takes (all of the same number, so that items cut at multiples of it run in
   // step; see the wide kernel)
   const int64_t total = (int64_t)U * sh.Hkv;
-  const int64_t wide_ns = total * (kPairNs * (sh.D / 64) / 2);
-  const int64_t narrow_ns =
-      sh.narrow ? (int64_t)all.w * sh.Hkv * sh.D * 4 * kStreamNsPerKb / 1024 : 0;
+  const int64_t singles = (int64_t)all.z * sh.Hkv;
+  const int64_t wide_ns = ((total - singles) * kPairNs + singles * kSingleNs) * sh.D / 128;
+  const int64_t tile_bytes = (int64_t)kNarrowTile * sh.D * 4;  // K and V, one head
+  const int64_t narrow_ns = all.w * sh.Hkv * tile_bytes / 1024 * kStreamNsPerKb;
   int W = sh.wide_grid;
   if (narrow_ns > 0 && total > 0) {
     W = (int)((wide_ns * sh.wide_grid + (wide_ns + narrow_ns) / 2) / (wide_ns + narrow_ns));
@@ -352,18 +359,23 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   const int S = total > 0 ? (int)((total + W - 1) / W) : 1;
   W = (int)((total + S - 1) / S);
   if (tid == 0) {
-    const int64_t T = sh.narrow ? (int64_t)all.w * (sh.Hkv / sh.hg) : 0;
-    const int64_t big_tokens = beside ? T * kDealt / 16 : T;
-    const int64_t big = min((int64_t)sms_left * (sh.narrow_grid / sh.wide_grid),
-                            (big_tokens + kNarrowLeast - 1) / kNarrowLeast);
+    const int64_t T = (int64_t)all.w * (sh.Hkv / sh.hg);
+    const int per_sm = sh.narrow_grid / sh.wide_grid;
+    int64_t big = (int64_t)sms_left * per_sm, big_tiles = T;
+    if (beside) {
+      const int64_t all_ns = (wide_ns + narrow_ns) / sh.wide_grid;
+      const int64_t tile_ns = sh.hg * tile_bytes / 1024 * kStreamNsPerKb * per_sm;
+      big_tiles = min(T, big * (all_ns * kDealt / 16 / tile_ns));
+    }
+    big = min(big, (big_tiles + kNarrowLeast - 1) / kNarrowLeast);
     pl.hdr[kUnits] = U;
-    pl.hdr[kTokens] = all.w;
+    pl.hdr[kTiles] = all.w;
     pl.hdr[kShare] = S;
     pl.hdr[kWideCtas] = W;
     pl.hdr[kBig] = (int)big;
-    const int64_t rest = T - big_tokens, most = (int64_t)kSmallPerSm * sh.wide_grid;
+    const int64_t rest = T - big_tiles, most = (int64_t)kSmallPerSm * sh.wide_grid;
     const int64_t small = max((int64_t)kSmallLeast, (rest + most - 1) / most);
-    *reinterpret_cast<int64_t*>(pl.hdr + kBigTokens) = big_tokens;
+    *reinterpret_cast<int64_t*>(pl.hdr + kBigTiles) = big_tiles;
     pl.hdr[kSmall] = (int)small;
     pl.hdr[kPieces] = (int)(big + (rest + small - 1) / small);
     pl.hdr[kClaim] = 0;
@@ -386,7 +398,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     const int f = joined(b), own = s_len[b] - (f >= 0 ? s_pre[f] : 0), nt = tiles(own);
     pl.npre[b] = ot;
     pl.start[b] = f >= 0 ? s_pre[f] : 0;
-    ot += own;
+    ot += own_tiles(own);
     osum.x += own_blocks * cuts(nt);
     osum.y += own_blocks * nt;
     osum.z += own_blocks ? sh.R * cuts(nt) : 0;
@@ -1111,7 +1123,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
                 if (my_box < n_box) {
                   const int j = lane % W::kBlk;
                   tc::tma_load_3d(tile + j * W::kBlkBytes + my_box * sh.box * 128,
-                                  v ? &map_v : &map_k, j * 64, pc.head, row, &bar_tma[s]);
+                                  v ? &map_v : &map_k, j * 64, row, pc.head, &bar_tma[s]);
                 }
               }
             } else {
@@ -1164,11 +1176,16 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
 
 // ---------------------------------------------------------------- narrow ---
 // Own tokens of requests with at most 16 rows a KV head, streamed: a CTA takes
-// 16-token tiles of K and V rows of its HG heads (HG x D x 2 contiguous bytes a
-// token) through a 3-stage cp.async ring, a warp a KV head.  Both products run
-// transposed on mma.sync (tokens, then head dimension, as M; the rows as N), so
-// no MMA carries padding rows; the work is a few FLOP a byte and the ring's
-// rate is what bounds it.
+// 16-token tiles of K and V rows of its HG heads through a ring in shared memory.
+// A warp has one KV head and up to eight rows (two warps a head for more, on the
+// same tiles); both products run transposed on mma.sync (tokens, then head
+// dimension, as M; the rows as N), so no MMA carries padding rows.  The work is a
+// few FLOP a byte and memory is what bounds it, as long as the work between a
+// tile's arrival and its release is short: so a warp of its own finds the tiles'
+// rows and fills the ring, by TMA where 16 tokens lie in whole 8-row boxes of
+// pages, else row by row with cp.async, which fills what is missing with zeros.
+// A ring stage holds K, then V, each as [64-value block][8 tokens of 16][head]
+// [token][128 bytes, swizzled].
 
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];\n"
@@ -1198,37 +1215,67 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
-constexpr int kTileRing = 8;  // tiles described ahead of or behind their use
+template <int D, int HG>
+struct Narrow {
+  static constexpr int kBlk = D / 64;
+  static constexpr uint32_t kBoxBytes = HG * 8 * 128;          // 64 values of 8 tokens, all heads
+  static constexpr uint32_t kHalfBytes = kBlk * 2 * kBoxBytes;  // K or V of a tile
+  static constexpr uint32_t kTileBytes = 2 * kHalfBytes;
+  static constexpr int kPerSm = HG >= 8 ? 1 : HG == 4 ? 2 : 4;  // CTAs an SM
+  static constexpr int kFit = (int)(192 * 1024 / kPerSm / kTileBytes);
+  static constexpr int kStages = kFit > 6 ? 6 : kFit;
+  static constexpr size_t smem(int B) {
+    return kStages * (size_t)kTileBytes + 1024 + sizeof(int32_t) * (size_t)(B + 1);
+  }
+};
+constexpr int kTileRing = 8;  // descriptions of tiles, more than stages
 
-template <int D, int HG, int NT8>
-__global__ void __launch_bounds__(HG * 32, 1)
+template <int D, int HG, int WPH>
+__global__ void __launch_bounds__((HG * WPH + 1) * 32, Narrow<D, HG>::kPerSm)
 k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
                 const __nv_bfloat16* __restrict__ kv_k, const __nv_bfloat16* __restrict__ kv_v,
                 PlanPtrs pl, float2* __restrict__ part_ml, float* __restrict__ part_o,
-                PrefixShape sh, float scale_log2, int wait_first) {
-  constexpr int NT = HG * 32, CH = D / 8, KS = D / 16, MT = D / 16, TILE = kNarrowTile;
-  constexpr int STAGE = TILE * HG * D;
+                PrefixShape sh, float scale_log2, int wait_first, long long budget,
+                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+  using N = Narrow<D, HG>;
+  constexpr int NT = (HG * WPH + 1) * 32, KS = D / 16, MT = D / 16, TILE = kNarrowTile;
+  static_assert(N::kStages < kTileRing, "a description outlives its stage");
   const float kNegInf = __int_as_float(0xff800000);
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  __nv_bfloat16* s_kv = reinterpret_cast<__nv_bfloat16*>(smem_raw);
-  // [B + 1] own tokens before each request
-  int32_t* s_pre = reinterpret_cast<int32_t*>(smem_raw + (size_t)kNarrowStages * 2 * STAGE * 2);
-  // a tile: n tokens (0: no more) from own position p0 of request b for the
-  // heads of group g, in a piece; kFirst / kLast of its request in the piece
+  extern __shared__ uint8_t smem_raw[];
+  // a tile: tokens from own position p0 of request b (own: all of them) for the
+  // heads of group g, in a piece; mask: its tokens; kFirst / kLast of its request
+  // in the piece, kEnd: no more tiles
   struct Tile {
-    int n, b, g, p0, own, piece, flags, pad;
+    int b, g, p0, own, piece, flags;
+    uint32_t mask;
+    int pad;
   };
-  constexpr int kFirst = 1, kLast = 2;
+  constexpr int kFirst = 1, kLast = 2, kEnd = 4;
   __shared__ Tile s_tile[kTileRing];
-  __shared__ int32_t s_row[kTileRing][TILE];  // physical rows (-1: none)
+  // bar_full: the producer's 32 lanes and its one announcement; bar_empty: the
+  // consumer warps
+  __shared__ __align__(8) uint64_t bar_full[N::kStages], bar_empty[N::kStages];
+  __shared__ int s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  // [B + 1] narrow tiles before each request
+  int32_t* s_pre = reinterpret_cast<int32_t*>(smem_raw + (base - tc::smem_u32(smem_raw)) +
+                                              N::kStages * (size_t)N::kTileBytes);
   const int B = sh.B, ngroups = sh.Hkv / HG;
+  if (tid == 0) {
+    for (int i = 0; i < N::kStages; ++i) {
+      tc::mbar_init(&bar_full[i], 33);
+      tc::mbar_init(&bar_empty[i], HG * WPH);
+    }
+    tc::mbar_init_fence();
+    s_abort = 0;
+  }
   // after the wide kernel the plan is complete (its CTAs waited for it before
   // they let this grid start), and this grid only waits for it at its end
   if (wait_first) pdl_wait();
   pdl_launch_dependents();
   const Pieces pieces(pl.hdr, ngroups);
-  const int Treq = pl.hdr[kTokens];
+  const int Treq = pl.hdr[kTiles];
   const int cta = blockIdx.x;
   for (int i = tid; i <= B; i += NT) s_pre[i] = pl.npre[i];
   if (cta >= pieces.big && pieces.n == pieces.big) {
@@ -1236,246 +1283,268 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     return;
   }
   __syncthreads();
+  bool ok = true;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, budget)) != 0;
+  };
 
-  // ---- the tiles in order, described by warp 0: its cursor, the same in all lanes
-  int piece = -1, claimed = 0;
-  int64_t f = 0, f_end = 0, seg_end = 0;  // flattened position, end of the piece and request
-  int cb = 0, cg = 0, cstart = 0;
-  auto claim = [&]() {  // (used a piece later, so that its latency is hidden)
-    if (lane == 0) claimed = pieces.big + atomicAdd(pl.hdr + kClaim, 1);
-  };
-  auto open_piece = [&](int p) {
-    piece = p;
-    if (p >= pieces.n) return;
-    f = pieces.lo(p);
-    f_end = pieces.lo(p + 1);
-    cg = (int)(f / Treq);
-    const int fb = (int)(f - (int64_t)cg * Treq);
-    int l = 0, h = B - 1;
-    while (l < h) {
-      const int mid = (l + h + 1) >> 1;
-      if (s_pre[mid] <= fb) l = mid; else h = mid - 1;
-    }
-    cb = l;
-    seg_end = (int64_t)cg * Treq + s_pre[cb + 1];
-    cstart = pl.start[cb];
-    claim();
-  };
-  // describe tile k; returns its lane's page, still to come, and the row in it
-  auto describe = [&](int k, int& page, int& in_page) {
-    page = -1;
-    in_page = 0;
-    if (piece < pieces.n && f == f_end) open_piece(__shfl_sync(0xffffffffu, claimed, 0));
-    Tile t = {};
-    if (piece < pieces.n) {
-      bool first = f == pieces.lo(piece);
-      while (f == seg_end) {  // the next request with own tokens
+  if (warp == HG * WPH) {
+    // ================= producer: the tiles in order =================
+    int piece = -1, claimed = 0;
+    int64_t f = 0, f_end = 0, seg_end = 0;  // next tile, end of the piece and of the request
+    int cb = 0, cg = 0, cstart = 0, clen = 0;
+    bool opened = false;
+    auto request = [&]() {
+      seg_end = (int64_t)cg * Treq + s_pre[cb + 1];
+      cstart = pl.start[cb];
+      clen = pl.lens[cb] - cstart;
+    };
+    auto claim = [&]() {  // (used a piece later, so that its latency is hidden)
+      if (lane == 0) claimed = pieces.big + atomicAdd(pl.hdr + kClaim, 1);
+    };
+    auto open_piece = [&](int p) {
+      piece = p;
+      if (p >= pieces.n) return;
+      f = pieces.lo(p);
+      f_end = pieces.lo(p + 1);
+      cg = (int)(f / Treq);
+      const int fb = (int)(f - (int64_t)cg * Treq);
+      int l = 0, h = B - 1;
+      while (l < h) {
+        const int mid = (l + h + 1) >> 1;
+        if (s_pre[mid] <= fb) l = mid; else h = mid - 1;
+      }
+      cb = l;
+      request();
+      opened = true;
+      claim();
+    };
+    // the next tile: its description, and its lane's (token's) page, still to
+    // come, with the row in it (-1: no token)
+    auto describe = [&](Tile& t, int& page, int& in_page) {
+      t = Tile{};
+      t.flags = kEnd;
+      page = in_page = -1;
+      if (piece < pieces.n && f == f_end) open_piece(__shfl_sync(0xffffffffu, claimed, 0));
+      if (piece >= pieces.n) return;
+      while (f == seg_end) {  // the next request with tiles
         if (++cb == B) {
           cb = 0;
           ++cg;
         }
-        seg_end = (int64_t)cg * Treq + s_pre[cb + 1];
-        cstart = pl.start[cb];
+        request();
+        opened = true;
       }
-      const int64_t seg_lo = (int64_t)cg * Treq + s_pre[cb];
-      first |= f == seg_lo;
-      int64_t e = f + TILE;
-      if (seg_end < e) e = seg_end;
-      if (f_end < e) e = f_end;
-      t.n = (int)(e - f);
       t.b = cb;
       t.g = cg;
-      t.p0 = (int)(f - seg_lo);
-      t.own = s_pre[cb + 1] - s_pre[cb];
+      t.p0 = (int)(f - ((int64_t)cg * Treq + s_pre[cb])) * TILE;
+      t.own = clen;
       t.piece = piece;
-      t.flags = (first ? kFirst : 0) | (e == seg_end || e == f_end ? kLast : 0);
-      if (lane < t.n) {
+      t.flags = (opened ? kFirst : 0) | (f + 1 == seg_end || f + 1 == f_end ? kLast : 0);
+      opened = false;
+      const int n = clen - t.p0;
+      if (lane < n && lane < TILE) {
         const int tok = cstart + t.p0 + lane;
         page = block_table[(int64_t)cb * sh.max_pages + tok / sh.page_size];
         in_page = tok % sh.page_size;
       }
-      f = e;
-    }
-    if (lane == 0) s_tile[k % kTileRing] = t;
-    if (lane >= t.n) in_page = -1;
-  };
-  auto place = [&](int k, int page, int in_page) {
-    if (lane >= TILE) return;
-    int row = -1;
-    if (in_page >= 0) {
-      if ((unsigned)page < (unsigned)sh.num_pages) row = page * sh.page_size + in_page;
-      else flag_error(pl.hdr + kErrWord, kErrPage);
-    }
-    s_row[k % kTileRing][lane] = row;
-  };
-  auto load = [&](int k) {
-    const Tile& t = s_tile[k % kTileRing];
-    if (t.n > 0) {
-      __nv_bfloat16* sk = s_kv + (size_t)(k % kNarrowStages) * 2 * STAGE;
-      __nv_bfloat16* sv = sk + STAGE;
-      const int g = t.g;
-#pragma unroll 4
-      for (int idx = tid; idx < TILE * HG * CH; idx += NT) {
-        const int r = idx / (HG * CH), rem = idx % (HG * CH), hh = rem / CH, c = rem % CH;
-        const int row = s_row[k % kTileRing][r];
-        const int off = (r * HG + hh) * D + ((c ^ (r & 7)) << 3);
-        const int64_t src = row >= 0 ? ((int64_t)row * sh.Hkv + g * HG + hh) * D + c * 8 : 0;
-        const int bytes = row >= 0 ? 16 : 0;
-        tc::cp_async16(tc::smem_u32(sk + off), kv_k + src, bytes);
-        tc::cp_async16(tc::smem_u32(sv + off), kv_v + src, bytes);
-      }
-    }
-    tc::cp_async_commit();
-  };
-
-  const int g8 = lane >> 2, t4 = lane & 3;
-  uint32_t qb[NT8][KS][2];
-  float o[NT8][MT][4], m_h[NT8][2], l_h[NT8][2];
-  int lim[NT8][2];  // own tokens that the thread's two rows see
-  auto begin = [&](const Tile& t) {
-    const int head = t.g * HG + warp;
-#pragma unroll
-    for (int nt = 0; nt < NT8; ++nt) {
-      const int j = nt * 8 + g8;
-      const __nv_bfloat16* src =
-          q + (((int64_t)t.b * sh.Nq + j / sh.G) * sh.Hq + (int64_t)head * sh.G + j % sh.G) * D + t4 * 2;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        qb[nt][ks][0] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
-        qb[nt][ks][1] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
-      }
-#pragma unroll
-      for (int i = 0; i < MT; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m_h[nt][e] = kNegInf;
-        l_h[nt][e] = 0.f;
-        lim[nt][e] = sh.causal ? t.own - sh.Nq + (nt * 8 + 2 * t4 + e) / sh.G + 1 : t.own;
-      }
-    }
-  };
-  auto finish = [&](const Tile& t) {
-    const int64_t base = (((int64_t)t.piece + (int64_t)t.g * B + t.b) * HG + warp) * sh.R;
-#pragma unroll
-    for (int nt = 0; nt < NT8; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float l = l_h[nt][e];
-        l += __shfl_xor_sync(0xffffffffu, l, 4);
-        l += __shfl_xor_sync(0xffffffffu, l, 8);
-        l += __shfl_xor_sync(0xffffffffu, l, 16);
-        const int j = nt * 8 + 2 * t4 + e;
-        if (j >= sh.R) continue;
-        float* po = part_o + (base + j) * D;
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          po[mt * 16 + g8] = o[nt][mt][e];
-          po[mt * 16 + g8 + 8] = o[nt][mt][e + 2];
-        }
-        if (g8 == 0) part_ml[base + j] = make_float2(m_h[nt][e], l);
-      }
-  };
-
-  // ---- tile k is described (its table entry requested) while tile k - 4 is
-  // computed, its rows are placed one tile later and its copies sent two before
-  // its use
-  int page = -1, in_page = -1;
-  if (warp == 0) {
+      ++f;
+    };
     if (cta < pieces.big) {
       open_piece(cta);
     } else {
       claim();
       open_piece(__shfl_sync(0xffffffffu, claimed, 0));
     }
-    int pg[3], ip[3];
-#pragma unroll
-    for (int k = 0; k < 3; ++k) describe(k, pg[k], ip[k]);
-    describe(3, page, in_page);
-#pragma unroll
-    for (int k = 0; k < 3; ++k) place(k, pg[k], ip[k]);
-  }
-  __syncthreads();
-#pragma unroll
-  for (int k = 0; k < kNarrowStages - 1; ++k) load(k);
-  for (int k = 0;; ++k) {
-    const Tile t = s_tile[k % kTileRing];
-    if (t.n == 0) break;
-    load(k + kNarrowStages - 1);
-    if (warp == 0) {
-      place(k + 3, page, in_page);
-      describe(k + 4, page, in_page);
+    // two tiles described ahead: their table entries are on the way
+    Tile t0, t1, t2;
+    int pg0, pg1, pg2, ip0, ip1, ip2;
+    describe(t0, pg0, ip0);
+    describe(t1, pg1, ip1);
+    uint32_t k = 0;
+    uint32_t used = 0;  // stages with a TMA copy in flight at some time
+    for (;; ++k) {
+      describe(t2, pg2, ip2);
+      const uint32_t s = k % N::kStages;
+      if (k >= (uint32_t)N::kStages && !(ok = wait(&bar_empty[s], (k / N::kStages - 1) & 1))) break;
+      int row = -1;
+      if (ip0 >= 0) {
+        if ((unsigned)pg0 < (unsigned)sh.num_pages) row = pg0 * sh.page_size + ip0;
+        else flag_error(pl.hdr + kErrWord, kErrPage);
+      }
+      t0.mask = __ballot_sync(0xffffffffu, row >= 0);
+      if (lane == 0) s_tile[k % kTileRing] = t0;
+      const uint32_t tile = base + s * N::kTileBytes;
+      if (t0.flags & kEnd) {
+        tc::mbar_arrive(&bar_full[s]);
+        if (lane == 0) tc::mbar_arrive(&bar_full[s]);
+        ++k;
+        break;
+      }
+      // whole boxes: all 16 tokens, in steps of eight from a box's first row
+      const bool whole = sh.box > 0 && t0.mask == 0xffffu &&
+                         __shfl_sync(0xffffffffu, ip0, 0) % 8 == 0;
+      if (whole) {
+        if (lane == 0) tc::mbar_arrive_expect(&bar_full[s], N::kTileBytes);
+        __syncwarp();
+        used |= 1u << s;
+        // lane 4 v + 2 j + h: K or V, block j, half h of the tokens
+        const int v = lane >> 2, j = (lane >> 1) & 1, h = lane & 1;
+        const int pr = __shfl_sync(0xffffffffu, row, (h * 8) & 31);
+        if (v < 2 && j < N::kBlk)
+          tc::tma_load_3d(tile + v * N::kHalfBytes + (j * 2 + h) * N::kBoxBytes,
+                          v ? &map_v : &map_k, j * 64, pr, t0.g * HG, &bar_full[s]);
+        tc::mbar_arrive(&bar_full[s]);
+      } else {
+        constexpr int kChunks = D / 8;
+#pragma unroll 4
+        for (int i = lane; i < TILE * HG * kChunks; i += 32) {
+          const int r = i / (HG * kChunks), hh = i / kChunks % HG, c = i % kChunks;
+          const int pr = __shfl_sync(0xffffffffu, row, r);
+          const uint32_t dst = tile + ((c >> 3) * 2 + (r >> 3)) * N::kBoxBytes +
+                               (hh * 8 + (r & 7)) * 128 + (((c & 7) ^ (r & 7)) << 4);
+          const int64_t src = pr >= 0 ? ((int64_t)pr * sh.Hkv + t0.g * HG + hh) * D + c * 8 : 0;
+          tc::cp_async16(dst, kv_k + src, pr >= 0 ? 16 : 0);
+          tc::cp_async16(dst + N::kHalfBytes, kv_v + src, pr >= 0 ? 16 : 0);
+        }
+        tc::cp_async_arrive(&bar_full[s]);
+        if (lane == 0) tc::mbar_arrive(&bar_full[s]);
+      }
+      t0 = t1;
+      pg0 = pg1;
+      ip0 = ip1;
+      t1 = t2;
+      pg1 = pg2;
+      ip1 = ip2;
     }
-    if (t.flags & kFirst) begin(t);
-    tc::cp_async_wait<kNarrowStages - 1>();
-    __syncthreads();
-    const __nv_bfloat16* sk = s_kv + (size_t)(k % kNarrowStages) * 2 * STAGE;
-    const __nv_bfloat16* sv = sk + STAGE;
-    float sacc[2][NT8][4];
-#pragma unroll
-    for (int c = 0; c < 2; ++c)
-#pragma unroll
-      for (int nt = 0; nt < NT8; ++nt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) sacc[c][nt][i] = 0.f;
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int row = (lane & 7) + (((lane >> 3) & 1) << 3);
-      const int chunk = 2 * ks + (lane >> 4);
-      uint32_t a[4];
-      ldsm_x4(tc::smem_u32(sk + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
-#pragma unroll
-      for (int nt = 0; nt < NT8; ++nt) mma_16816(sacc[ks & 1][nt], a, qb[nt][ks][0], qb[nt][ks][1]);
+    tc::cp_async_wait<0>();
+    if (!ok) {
+      if (lane == 0) {
+        flag_error(pl.hdr + kErrWord, kErrTimeout);
+        s_abort = 1;
+      }
+      // the copies in flight land before the shared memory is given up
+      const long long t0c = clock64();
+      for (uint32_t n = k > (uint32_t)N::kStages ? k - N::kStages : 0; n < k; ++n)
+        while (((used >> (n % N::kStages)) & 1) &&
+               !tc::mbar_try_wait(&bar_full[n % N::kStages], (n / N::kStages) & 1) &&
+               clock64() - t0c < kWaitCycles) {
+        }
     }
-    const bool v0 = s_row[k % kTileRing][g8] >= 0, v1 = s_row[k % kTileRing][g8 + 8] >= 0;
-    uint32_t pb[NT8][2];
+    __syncwarp();
+  } else {
+    // ================= consumers =================
+    const int hh = warp % HG, c0 = (warp / HG) * 8;  // KV head of the group, first row
+    const int g8 = lane >> 2, t4 = lane & 3;
+    uint32_t qb[KS][2];
+    float o[MT][4], m_h[2] = {kNegInf, kNegInf}, l_h[2] = {0.f, 0.f};
+    int lim[2] = {0, 0};  // own tokens that the thread's two rows see
+    for (uint32_t k = 0;; ++k) {
+      const uint32_t s = k % N::kStages;
+      if (!(ok = wait(&bar_full[s], (k / N::kStages) & 1))) break;
+      const Tile t = s_tile[k % kTileRing];
+      if (t.flags & kEnd) break;
+      if (t.flags & kFirst) {
+        const int head = t.g * HG + hh, j = c0 + g8;
+        const __nv_bfloat16* src =
+            q + (((int64_t)t.b * sh.Nq + j / sh.G) * sh.Hq + (int64_t)head * sh.G + j % sh.G) * D +
+            t4 * 2;
 #pragma unroll
-    for (int nt = 0; nt < NT8; ++nt) {
+        for (int ks = 0; ks < KS; ++ks) {
+          qb[ks][0] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+          qb[ks][1] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          m_h[e] = kNegInf;
+          l_h[e] = 0.f;
+          lim[e] = sh.causal ? t.own - sh.Nq + (c0 + 2 * t4 + e) / sh.G + 1 : t.own;
+        }
+      }
+      const uint32_t sk = base + s * N::kTileBytes + hh * 1024, sv = sk + N::kHalfBytes;
+      float sacc[2][4];
+#pragma unroll
+      for (int c = 0; c < 2; ++c) sacc[c][0] = sacc[c][1] = sacc[c][2] = sacc[c][3] = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int r = lane & 7, h = (lane >> 3) & 1, c = 2 * ks + (lane >> 4);
+        uint32_t a[4];
+        ldsm_x4(sk + ((c >> 3) * 2 + h) * N::kBoxBytes + r * 128 + (((c & 7) ^ r) << 4), a);
+        mma_16816(sacc[ks & 1], a, qb[ks][0], qb[ks][1]);
+      }
+      const bool v0 = (t.mask >> g8) & 1, v1 = (t.mask >> (g8 + 8)) & 1;
       float x[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const bool v = (i < 2 ? v0 : v1) && t.p0 + g8 + (i < 2 ? 0 : 8) < lim[nt][i & 1];
-        x[i] = v ? (sacc[0][nt][i] + sacc[1][nt][i]) * scale_log2 : kNegInf;
+        const bool v = (i < 2 ? v0 : v1) && t.p0 + g8 + (i < 2 ? 0 : 8) < lim[i & 1];
+        x[i] = v ? (sacc[0][i] + sacc[1][i]) * scale_log2 : kNegInf;
       }
       float al[2], p[4];
+      bool moved = false;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float mx = fmaxf(x[e], x[e + 2]);
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        const float mn = fmaxf(m_h[nt][e], mx);
-        al[e] = mn == kNegInf ? 1.f : exp2f(m_h[nt][e] - mn);
+        // the running maximum moves when the tile exceeds it by more than 8
+        const bool mv = mx > m_h[e] + 8.f;
+        const float mn = mv ? mx : m_h[e];
+        al[e] = mv ? exp2f(m_h[e] - mn) : 1.f;
+        moved |= mv;
         p[e] = x[e] == kNegInf ? 0.f : ex2(x[e] - mn);
         p[e + 2] = x[e + 2] == kNegInf ? 0.f : ex2(x[e + 2] - mn);
-        m_h[nt][e] = mn;
+        l_h[e] = l_h[e] * al[e] + (p[e] + p[e + 2]);
+        m_h[e] = mn;
       }
-      l_h[nt][0] = l_h[nt][0] * al[0] + (p[0] + p[2]);
-      l_h[nt][1] = l_h[nt][1] * al[1] + (p[1] + p[3]);
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          o[mt][0] *= al[0];
+          o[mt][1] *= al[1];
+          o[mt][2] *= al[0];
+          o[mt][3] *= al[1];
+        }
+      }
       // rounded to bf16 for the second product only
-      const uint32_t lo2 = pack_bf16(p[0], p[1]), hi2 = pack_bf16(p[2], p[3]);
+      const uint32_t pb0 = movmatrix_t(pack_bf16(p[0], p[1])), pb1 = movmatrix_t(pack_bf16(p[2], p[3]));
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
-        o[nt][mt][0] *= al[0];
-        o[nt][mt][1] *= al[1];
-        o[nt][mt][2] *= al[0];
-        o[nt][mt][3] *= al[1];
+        const int r = lane & 7, h = lane >> 4, c = 2 * mt + ((lane >> 3) & 1);
+        uint32_t a[4];
+        ldsm_x4_t(sv + ((c >> 3) * 2 + h) * N::kBoxBytes + r * 128 + (((c & 7) ^ r) << 4), a);
+        mma_16816(o[mt], a, pb0, pb1);
       }
-      pb[nt][0] = movmatrix_t(lo2);
-      pb[nt][1] = movmatrix_t(hi2);
-    }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar_empty[s]);
+      if (t.flags & kLast) {
+        const int64_t at = (((int64_t)t.piece + (int64_t)t.g * B + t.b) * HG + hh) * sh.R;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      const int row = (lane & 7) + ((lane >> 4) << 3);
-      const int chunk = 2 * mt + ((lane >> 3) & 1);
-      uint32_t a[4];
-      ldsm_x4_t(tc::smem_u32(sv + (row * HG + warp) * D + ((chunk ^ (row & 7)) << 3)), a);
+        for (int e = 0; e < 2; ++e) {
+          float l = l_h[e];
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          const int j = c0 + 2 * t4 + e;
+          if (j >= sh.R) continue;
+          float* po = part_o + (at + j) * D;
 #pragma unroll
-      for (int nt = 0; nt < NT8; ++nt) mma_16816(o[nt][mt], a, pb[nt][0], pb[nt][1]);
+          for (int mt = 0; mt < MT; ++mt) {
+            po[mt * 16 + g8] = o[mt][e];
+            po[mt * 16 + g8 + 8] = o[mt][e + 2];
+          }
+          if (g8 == 0) part_ml[at + j] = make_float2(m_h[e], l);
+        }
+      }
     }
-    if (t.flags & kLast) finish(t);
-    __syncthreads();
+    if (!ok && lane == 0) {
+      flag_error(pl.hdr + kErrWord, kErrTimeout);
+      s_abort = 1;
+    }
   }
-  tc::cp_async_wait<0>();
+  __syncthreads();  // no warp leaves while copies may still land
   if (!wait_first) pdl_wait();
 }
 
@@ -1501,7 +1570,7 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   const Request rq = pl.req[b];
   const int pre = pl.npre[b];
   const int U = pl.hdr[kUnits], S = pl.hdr[kShare], slots_head = pl.hdr[kSlots];
-  const int Treq = pl.hdr[kTokens];
+  const int Treq = pl.hdr[kTiles];
   const Pieces pieces(pl.hdr, sh.Hkv / sh.hg);
   if (row == 0 && lane == 0) pl.hdr[kClaim] = 0;  // for the next call by this plan
 
@@ -1521,7 +1590,7 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
     if (sh.narrow) {
       const int64_t f0 = (int64_t)g * Treq + pre;
       c0 = pieces.of(f0);
-      n1 = pieces.of(f0 + rq.own - 1) - c0 + 1;
+      n1 = pieces.of(f0 + (rq.own + kNarrowTile - 1) / kNarrowTile - 1) - c0 + 1;
     } else {
       n1 = 2 * (((rq.own + kTile - 1) / kTile + S - 1) / S);
     }
@@ -1628,12 +1697,7 @@ PrefixShape prefix_shape(const pks_prefix_args& a) {
   sh.box = a.page_size & -a.page_size;
   if (sh.box > kTile) sh.box = kTile;
   if (sh.box < 8) sh.box = 0;
-  // shared memory holds one narrow CTA of eight heads an SM, more of fewer
-  const size_t stage = (size_t)2 * kNarrowTile * sh.hg * a.D * sizeof(__nv_bfloat16);
-  const size_t smem = kNarrowStages * stage + sizeof(int32_t) * (size_t)(a.B + 1);
-  int per_sm = (int)((size_t)(227 * 1024) / (smem + 2048));
-  if (per_sm > 4) per_sm = 4;
-  sh.narrow_grid = device_sm_count() * (per_sm < 1 ? 1 : per_sm);
+  sh.narrow_grid = device_sm_count() * (sh.hg >= 8 ? 1 : sh.hg == 4 ? 2 : 4);
   return sh;
 }
 
@@ -1670,9 +1734,10 @@ cudaError_t allow_smem(K kern, size_t bytes, bool (&done)[64]) {
   return e;
 }
 
-// Tensor map of a K or V pool as rows x heads x D, a box being `rows` tokens of
-// one head and 64 of its values, 128-byte swizzled.
-cudaError_t pool_map(CUtensorMap* map, const void* pool, const pks_prefix_args& a, int rows) {
+// Tensor map of a K or V pool as heads x rows x D, a box being `rows` tokens of
+// `heads` heads and 64 of their values, 128-byte swizzled.
+cudaError_t pool_map(CUtensorMap* map, const void* pool, const pks_prefix_args& a, int rows,
+                     int heads) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;
@@ -1683,10 +1748,10 @@ cudaError_t pool_map(CUtensorMap* map, const void* pool, const pks_prefix_args& 
     if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
-  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.Hkv,
-                              (cuuint64_t)a.num_pages * (cuuint64_t)a.page_size};
-  const cuuint64_t strides[2] = {(cuuint64_t)a.D * 2, (cuuint64_t)a.Hkv * a.D * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows}, ones[3] = {1, 1, 1};
+  const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.num_pages * (cuuint64_t)a.page_size,
+                              (cuuint64_t)a.Hkv};
+  const cuuint64_t strides[2] = {(cuuint64_t)a.Hkv * a.D * 2, (cuuint64_t)a.D * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)heads}, ones[3] = {1, 1, 1};
   const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims,
                             strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
                             CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1703,8 +1768,8 @@ cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const P
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap map_k{}, map_v{};
   if (sh.box > 0) {
-    if ((e = pool_map(&map_k, a.kv_k, a, sh.box)) != cudaSuccess) return e;
-    if ((e = pool_map(&map_v, a.kv_v, a, sh.box)) != cudaSuccess) return e;
+    if ((e = pool_map(&map_k, a.kv_k, a, sh.box, 1)) != cudaSuccess) return e;
+    if ((e = pool_map(&map_v, a.kv_v, a, sh.box, 1)) != cudaSuccess) return e;
   }
   return launch_ex(k_prefix_wide<D>, dim3(sh.wide_grid), dim3(kWideThreads), Wide<D>::kSmem, s,
                    /*pdl=*/true, /*coop=*/false, a.block_table,
@@ -1716,23 +1781,28 @@ cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const P
                    a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles, map_k, map_v);
 }
 
-template <int D, int HG, int NT8>
+template <int D, int HG, int WPH>
 cudaError_t launch_narrow(const pks_prefix_args& a, const PrefixLayout& L, const PrefixShape& sh,
                           float scale_log2, bool wait_first, cudaStream_t s) {
   static bool done[64] = {false};
-  auto kern = k_prefix_narrow<D, HG, NT8>;
-  constexpr size_t kStages = (size_t)kNarrowStages * 2 * kNarrowTile * HG * D * sizeof(__nv_bfloat16);
-  cudaError_t e = allow_smem(kern, kStages + sizeof(int32_t) * (kMaxB + 1), done);
+  using N = Narrow<D, HG>;
+  auto kern = k_prefix_narrow<D, HG, WPH>;
+  cudaError_t e = allow_smem(kern, N::smem(kMaxB), done);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  const size_t smem = kStages + sizeof(int32_t) * (size_t)(a.B + 1);
-  return launch_ex(kern, dim3(sh.narrow_grid), dim3(HG * 32), smem, s, /*pdl=*/true,
-                   /*coop=*/false, a.block_table, static_cast<const __nv_bfloat16*>(a.q),
+  CUtensorMap map_k{}, map_v{};
+  if (sh.box > 0) {
+    if ((e = pool_map(&map_k, a.kv_k, a, 8, HG)) != cudaSuccess) return e;
+    if ((e = pool_map(&map_v, a.kv_v, a, 8, HG)) != cudaSuccess) return e;
+  }
+  return launch_ex(kern, dim3(sh.narrow_grid), dim3((HG * WPH + 1) * 32), N::smem(a.B), s,
+                   /*pdl=*/true, /*coop=*/false, a.block_table,
+                   static_cast<const __nv_bfloat16*>(a.q),
                    static_cast<const __nv_bfloat16*>(a.kv_k),
                    static_cast<const __nv_bfloat16*>(a.kv_v), plan_ptrs(ws, L),
                    reinterpret_cast<float2*>(ws + L.narrow_ml),
-                   reinterpret_cast<float*>(ws + L.narrow_o), sh, scale_log2,
-                   wait_first ? 1 : 0);
+                   reinterpret_cast<float*>(ws + L.narrow_o), sh, scale_log2, wait_first ? 1 : 0,
+                   a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles, map_k, map_v);
 }
 
 template <int D>

@@ -711,6 +711,8 @@ pks_status prefix_check(const pks_prefix_args* a) {
   if (a->Hq / a->Hkv > 16 || a->Hq > 4096 || a->n_queries > pks::kPrefixMaxQueries)
     return PKS_ERR_UNSUPPORTED;
   if ((int64_t)a->B * std::max(1, a->n_queries) > pks::kMaxB) return PKS_ERR_UNSUPPORTED;
+  // the plan counts 16-token tiles of the whole batch in 32 bits
+  if ((int64_t)a->B * a->max_pages * a->page_size > (int64_t(1) << 34)) return PKS_ERR_UNSUPPORTED;
   if ((int64_t)a->num_pages * a->page_size > INT32_MAX) return PKS_ERR_UNSUPPORTED;
   if ((int64_t)a->max_pages * a->page_size > pks::kMaxLen) return PKS_ERR_UNSUPPORTED;
   return PKS_OK;
