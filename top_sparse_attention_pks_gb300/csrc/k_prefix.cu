@@ -114,12 +114,12 @@ constexpr int kSmallPerSm = 8;                 // small pieces an SM at most
 // Beside the wide kernel, a narrow CTA is dealt this share (in 1/16) of what it
 // could stream in the time estimated for all; the rest goes to whichever SM is
 // free.
-constexpr int kDealt = 10;
+constexpr int kDealt = 8;
 // Estimated nanoseconds an SM spends with D = 128 (half with D = 64): on a wide
 // tile with two row blocks (its products), on one with a single block (its bytes,
 // while the narrow kernel loads the memory too), and on a kilobyte streamed by the
 // narrow kernel.
-constexpr int kPairNs = 1750, kSingleNs = 2600, kStreamNsPerKb = 24;
+constexpr int kPairNs = 1950, kSingleNs = 4000, kStreamNsPerKb = 24;
 
 // The narrow kernel's pieces: `big` equal ones that cover the first big_tiles of
 // the T tiles (all heads), one for each CTA that starts at once, and small ones
@@ -345,7 +345,8 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   // step; see the wide kernel)
   const int64_t total = (int64_t)U * sh.Hkv;
   const int64_t singles = (int64_t)all.z * sh.Hkv;
-  const int64_t wide_ns = ((total - singles) * kPairNs + singles * kSingleNs) * sh.D / 128;
+  const int64_t pairs_ns = (total - singles) * kPairNs * sh.D / 128;
+  const int64_t wide_ns = pairs_ns + singles * kSingleNs * sh.D / 128;
   const int64_t tile_bytes = (int64_t)kNarrowTile * sh.D * 4;  // K and V, one head
   const int64_t narrow_ns = all.w * sh.Hkv * tile_bytes / 1024 * kStreamNsPerKb;
   int W = sh.wide_grid;
@@ -363,7 +364,8 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     const int per_sm = sh.narrow_grid / sh.wide_grid;
     int64_t big = (int64_t)sms_left * per_sm, big_tiles = T;
     if (beside) {
-      const int64_t all_ns = (wide_ns + narrow_ns) / sh.wide_grid;
+      const int64_t singles_kb = singles * kTile * sh.D * 4 / 1024;
+      const int64_t all_ns = (pairs_ns + singles_kb * kStreamNsPerKb + narrow_ns) / sh.wide_grid;
       const int64_t tile_ns = sh.hg * tile_bytes / 1024 * kStreamNsPerKb * per_sm;
       big_tiles = min(T, big * (all_ns * kDealt / 16 / tile_ns));
     }
