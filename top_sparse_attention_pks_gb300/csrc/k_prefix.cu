@@ -558,14 +558,13 @@ struct Piece {
 // A CTA's walk over its tiles; every role walks the same pieces.
 struct Walk {
   const Item* items;
-  Item it;              // of u (loaded a piece ahead)
   int64_t u, end;       // next tile and the CTA's last + 1, over all heads
   int head, item;
   int U, n_items, slots_head, cta;
   __device__ __forceinline__ bool more() const { return u < end; }
   __device__ __forceinline__ Piece next() {
     Piece p;
-    p.it = it;
+    p.it = items[item];
     p.head = head;
     const int nt = (p.it.t1 - p.it.t0 + kTile - 1) / kTile;
     p.t_lo = (int)(u - ((int64_t)head * U + p.it.unit0));
@@ -579,7 +578,6 @@ struct Walk {
       item = 0;
       ++head;
     }
-    if (more()) it = items[item];
     return p;
   }
 };
@@ -661,7 +659,6 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     walk.n_items = pl.hdr[kItems];
     walk.slots_head = pl.hdr[kSlots];
     walk.cta = cta;
-    walk.it = st.it;
     walk.head = st.head;
     walk.item = st.item;
     const int64_t total = (int64_t)walk.U * sh.Hkv;
@@ -959,13 +956,18 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           if (!(ok = landed(t, 1))) break;
           const uint32_t sl = (n_slot + 2 * t + 1) % W::kSlotsN;
           const uint64_t dv = tc::desc_sw128(sKV + sl * W::kTileBytes, W::kBlkBytes, 1024);
-          if (!(ok = wait(&bar_p[g][0], n_job & 1))) break;
+          // K of the next tile, if it is there: S then follows P.V without a wait
+          const bool more = i + 1 < my_jobs;
+          const int tn = t + step;
+          const bool early = more && step == 1 && ready(tn, by_tma);
+          if (early && !(ok = landed(tn, 0))) break;
           // after the other group's products of the job before (at the start of a
           // piece: of the piece before, when its last job was group 1's)
-          if (job > 0 || (owed && n_piece > 0)) {
+          if (job > 0 || owed) {
             if (!(ok = wait(&bar_turn[g], n_turn & 1))) break;
             ++n_turn;
           }
+          if (!(ok = wait(&bar_p[g][0], n_job & 1))) break;
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             if (h == 1 && !(ok = wait(&bar_p[g][1], n_job & 1))) break;
@@ -983,19 +985,18 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
             __syncwarp();
           }
           if (!ok) break;
-          // then the next S, and the turn: early when S would have to wait for K
-          const bool more = i + 1 < my_jobs;
-          bool pass = g == 1 || job + 1 < pc.jobs0 + pc.jobs1;
-          const int tn = t + step;
-          if (pass && (!more || !ready(tn, by_tma))) {
-            if (tc::elect_one()) tc::mbar_arrive(&bar_turn[1 - g]);
-            __syncwarp();
-            pass = false;
-          }
-          if (more) {
-            if (step == 2) ok = skip(t + 1);
-            if (!ok || !(ok = landed(tn, 0))) break;
+          // then the next S, and the turn: before S when that has to wait for K
+          const bool pass = g == 1 || job + 1 < pc.jobs0 + pc.jobs1;
+          if (early) {
             issue_s(tn, i + 2 == my_jobs, pass ? &bar_turn[1 - g] : nullptr);
+          } else {
+            if (pass && tc::elect_one()) tc::mbar_arrive(&bar_turn[1 - g]);
+            __syncwarp();
+            if (more) {
+              if (step == 2) ok = skip(t + 1);
+              if (!ok || !(ok = landed(tn, 0))) break;
+              issue_s(tn, i + 2 == my_jobs, nullptr);
+            }
           }
         }
         // tiles behind the group's last one
@@ -1050,11 +1051,15 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       uint32_t n_slot = 0, n_piece = 0;
       uint32_t ph_go = 0;
       uint32_t tma_used = 0, tma_count = 0;  // by slot: any TMA copy, their number modulo two
-      int row = lw == 0 && walk.more()
-                    ? box_row(walk.it, (int)(walk.u - ((int64_t)walk.head * walk.U + walk.it.unit0)))
-                    : 0;
+      int row = 0;
+      if (lw == 0 && walk.more()) {
+        const Item first = pl.starts[cta].it;
+        row = box_row(first, (int)(walk.u - ((int64_t)walk.head * walk.U + first.unit0)));
+      }
       while (walk.more() && ok) {
         const Piece pc = walk.next();
+        Item then = {};  // the next piece's item, for its first row
+        if (lw == 0 && walk.more()) then = walk.items[walk.item];
         const int32_t* bt = block_table + (int64_t)pc.it.bt_row * sh.max_pages;
         // physical row of this lane's token of tile t (-1: none)
         auto token_row = [&](int t) -> int {
@@ -1099,7 +1104,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           // the row of the tile after this one, in the next piece if need be
           int next_row = 0;
           if (lw == 0 && (t + 1 < pc.nt || walk.more()))
-            next_row = t + 1 < pc.nt ? box_row(pc.it, pc.t_lo + t + 1) : box_row(walk.it, 0);
+            next_row = t + 1 < pc.nt ? box_row(pc.it, pc.t_lo + t + 1) : box_row(then, 0);
 #pragma unroll
           for (int v = 0; v < 2; ++v, ++done) {
             const uint32_t n = n_slot + done, s = n % W::kSlotsN;
