@@ -28,8 +28,10 @@ constexpr int kHdrPages = 0, kHdrPageSize = 1, kHdrFree = 2, kHdrErr = 3, kHdrMo
               kHdrMagic = 5, kHdrGrant = 6, kHdrUsed = 7, kHdrCalls = 8;
 
 constexpr int kRowThreads = 256;    // fork, free: a block a row
+constexpr int kRowUnroll = 8;       // entries of a row a thread has in flight
 constexpr int kPlanThreads = 1024;  // extend and compact: the one planning block
 constexpr int kMaxRows = 4096;
+constexpr int kTakenShared = 1024;  // taken pages that extend keeps in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;  // units a thread has in flight
 
@@ -134,6 +136,8 @@ k_pages_fork(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
              int B, int max_pages, int n, const int32_t* __restrict__ src_rows,
              const int32_t* __restrict__ dst_rows, const int32_t* __restrict__ n_tokens) {
   const int i = blockIdx.x, tid = threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   const int src = src_rows[i], dst = dst_rows[i];
   bool bad = (unsigned)src >= (unsigned)B || (unsigned)dst >= (unsigned)B || src == dst;
   for (int j = tid; j < n; j += kRowThreads) {
@@ -160,16 +164,33 @@ k_pages_fork(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
   const int32_t* from = block_table + (int64_t)src * max_pages;
   int32_t* to = block_table + (int64_t)dst * max_pages;
   bool bad_page = false;
-  for (int p = tid; p < np; p += kRowThreads)
-    bad_page |= (unsigned)from[p] >= (unsigned)num_pages;
+  for (int p0 = tid; p0 < np; p0 += kRowThreads * kRowUnroll) {
+    int page[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const int p = p0 + u * kRowThreads;
+      page[u] = p < np ? from[p] : 0;
+    }
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) bad_page |= (unsigned)page[u] >= (unsigned)num_pages;
+  }
   if (__syncthreads_or(bad_page)) {  // also: every thread has read the destination's length
     if (tid == 0) flag_error(st.hdr, kErrPage);
     return;
   }
-  for (int p = tid; p < np; p += kRowThreads) {
-    const int page = from[p];
-    to[p] = page;
-    atomicAdd(&st.ref[page], 1);
+  for (int p0 = tid; p0 < np; p0 += kRowThreads * kRowUnroll) {
+    int page[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const int p = p0 + u * kRowThreads;
+      page[u] = p < np ? from[p] : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u)
+      if (page[u] >= 0) {
+        to[p0 + u * kRowThreads] = page[u];
+        atomicAdd(&st.ref[page[u]], 1);
+      }
   }
   if (tid == 0) seq_lens[dst] = tok;
 }
@@ -180,6 +201,8 @@ k_pages_free(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
              int B, int max_pages, int n, const int32_t* __restrict__ rows,
              const int32_t* __restrict__ keep) {
   const int i = blockIdx.x, tid = threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   const int row = rows[i];
   bool bad = (unsigned)row >= (unsigned)B;
   for (int j = tid; j < i; j += kRowThreads) bad |= rows[j] == row;
@@ -196,20 +219,30 @@ k_pages_free(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
   const int p1 = pages_of(len, page_size);
   int32_t* row_t = block_table + (int64_t)row * max_pages;
   int freed = 0;
-  for (int p = pages_of(tok, page_size) + tid; p < p1; p += kRowThreads) {
-    const int page = row_t[p];
-    row_t[p] = -1;
-    if ((unsigned)page >= (unsigned)num_pages) {
-      flag_error(st.hdr, kErrPage);
-      continue;
+  for (int p0 = pages_of(tok, page_size) + tid; p0 < p1; p0 += kRowThreads * kRowUnroll) {
+    int page[kRowUnroll], had[kRowUnroll];
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      const int p = p0 + u * kRowThreads;
+      page[u] = p < p1 ? row_t[p] : -2;
     }
-    const int had = atomicSub(&st.ref[page], 1);
-    if (had <= 0) {  // the tables hold it more often than its count says
-      atomicAdd(&st.ref[page], 1);
-      flag_error(st.hdr, kErrState);
-    } else if (had == 1) {
-      atomicOr(&st.free_map[page >> 5], 1u << (page & 31));
-      ++freed;
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      if (page[u] == -2) continue;
+      row_t[p0 + u * kRowThreads] = -1;
+      if ((unsigned)page[u] < (unsigned)num_pages) had[u] = atomicSub(&st.ref[page[u]], 1);
+      else flag_error(st.hdr, kErrPage);
+    }
+#pragma unroll
+    for (int u = 0; u < kRowUnroll; ++u) {
+      if ((unsigned)page[u] >= (unsigned)num_pages) continue;
+      if (had[u] <= 0) {  // the tables hold it more often than its count says
+        atomicAdd(&st.ref[page[u]], 1);
+        flag_error(st.hdr, kErrState);
+      } else if (had[u] == 1) {
+        atomicOr(&st.free_map[page[u] >> 5], 1u << (page[u] & 31));
+        ++freed;
+      }
     }
   }
   freed = __reduce_add_sync(0xffffffffu, freed);
@@ -226,19 +259,33 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   __shared__ int s_warp[32];
   __shared__ int s_start[kMaxRows + 1];  // first taken page of each row
   __shared__ int s_had[kMaxRows];        // the row's pages before
+  __shared__ int s_taken[kTakenShared];  // the first taken pages (the rest: st.taken)
   const int tid = threadIdx.x;
   const int max_len = max_pages * page_size;
+  pdl_launch_dependents();  // the copies' blocks may come in and wait
+  pdl_wait();
   const int n_free = st.hdr[kHdrFree];
-  int len[kPer], inc[kPer], tail[kPer];
+  const int words = (num_pages + 31) / 32;
+  // the bitmap's first words, on their way while the rows are looked at
+  uint4 first_words = make_uint4(0, 0, 0, 0);
+  if (tid * 4 < words) first_words = *reinterpret_cast<const uint4*>(st.free_map + tid * 4);
+  int len[kPer], inc[kPer], tail[kPer], holders[kPer];
   bool bad_len = false, bad_page = false;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int b = tid * kPer + u;
+    const int b = tid + u * kPlanThreads;
     len[u] = inc[u] = 0;
+    if (b < B) {
+      len[u] = seq_lens[b];
+      inc[u] = add[b];
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    const int b = tid + u * kPlanThreads;
     tail[u] = -1;  // the partly filled last page of a growing row
+    holders[u] = 0;
     if (b >= B) continue;
-    len[u] = seq_lens[b];
-    inc[u] = add[b];
     if (len[u] < 0 || len[u] > max_len || inc[u] < 0 || inc[u] > max_len - len[u]) {
       bad_len = true;
       inc[u] = 0;
@@ -250,40 +297,47 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
       } else {
         atomicAdd(&st.cnt[tail[u]], 1);
         atomicMax(&st.last[tail[u]], b + 1);
+        holders[u] = st.ref[tail[u]];
       }
     }
   }
   const bool any_len = __syncthreads_or(bad_len), any_page = __syncthreads_or(bad_page);
-  int need[kPer], sum = 0;
+  int need[kPer];
   bool copy[kPer];
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int b = tid * kPer + u;
+    const int b = tid + u * kPlanThreads;
     copy[u] = false;
     need[u] = 0;
     if (inc[u] > 0) {
-      if (tail[u] >= 0) {
-        const int holders = st.ref[tail[u]];
-        // the last growing holder keeps the page when every holder grows
-        copy[u] = holders > 1 &&
-                  !(__ldcg(&st.cnt[tail[u]]) == holders && __ldcg(&st.last[tail[u]]) == b + 1);
-      }
+      // the last growing holder keeps the page when every holder grows
+      if (tail[u] >= 0)
+        copy[u] = holders[u] > 1 && !(__ldcg(&st.cnt[tail[u]]) == holders[u] &&
+                                      __ldcg(&st.last[tail[u]]) == b + 1);
       need[u] = pages_of(len[u] + inc[u], page_size) - pages_of(len[u], page_size) + copy[u];
     }
-    sum += need[u];
   }
-  int total;
-  int at = block_scan<kPlanThreads>(sum, s_warp, total) - sum;
+  // prefix sums of needs and copies over the rows, 1024 rows at a time
+  int at[kPer], c_at[kPer], total = 0, copies = 0;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) {
+    at[u] = c_at[u] = 0;
+    if (u * kPlanThreads >= B) continue;  // (the whole block)
+    int t0, t1;
+    at[u] = total + block_scan<kPlanThreads>(need[u], s_warp, t0) - need[u];
+    c_at[u] = copies + block_scan<kPlanThreads>(copy[u], s_warp, t1) - copy[u];
+    total += t0;
+    copies += t1;
+  }
   const bool granted = !any_len && !any_page && total <= n_free;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {  // (all threads have read the counts)
     if (tail[u] >= 0) st.cnt[tail[u]] = st.last[tail[u]] = 0;
-    const int b = tid * kPer + u;
+    const int b = tid + u * kPlanThreads;
     if (b < B) {
-      s_start[b] = at;
+      s_start[b] = at[u];
       s_had[b] = pages_of(len[u], page_size) - copy[u];
     }
-    at += need[u];
   }
   if (tid == 0) {
     s_start[B] = total;
@@ -295,12 +349,12 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   }
   if (!granted) return;
   // the lowest `total` free pages: rank every thread's words of the bitmap
-  const int words = (num_pages + 31) / 32;
   int rank0 = 0;
   for (int w0 = 0; rank0 < total && w0 < words; w0 += kPlanThreads * 4) {
-    uint4 m = make_uint4(0, 0, 0, 0);
+    uint4 m = first_words;
     const int w = w0 + tid * 4;  // the map is padded to whole uint4s
-    if (w < words) m = *reinterpret_cast<const uint4*>(st.free_map + w);
+    if (w0 > 0) m = make_uint4(0, 0, 0, 0);
+    if (w0 > 0 && w < words) m = *reinterpret_cast<const uint4*>(st.free_map + w);
     const int mine = __popc(m.x) + __popc(m.y) + __popc(m.z) + __popc(m.w);
     int in_pass;
     int r = rank0 + block_scan<kPlanThreads>(mine, s_warp, in_pass) - mine;
@@ -311,24 +365,23 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
         while (x[j] && r < total) {
           const int bit = __ffs(x[j]) - 1;
           x[j] &= x[j] - 1;
-          st.taken[r++] = (w + j) * 32 + bit;
+          const int page = (w + j) * 32 + bit;
+          if (r < kTakenShared) s_taken[r] = page;
+          else st.taken[r] = page;
+          ++r;
         }
       *reinterpret_cast<uint4*>(st.free_map + w) = make_uint4(x[0], x[1], x[2], x[3]);
     }
     rank0 += in_pass;
   }
-  // copies: numbered in row order
-  int ncopy = 0;
-#pragma unroll
-  for (int u = 0; u < kPer; ++u) ncopy += copy[u];
-  int copies;
-  int c = block_scan<kPlanThreads>(ncopy, s_warp, copies) - ncopy;
+  __syncthreads();
+  auto taken = [&](int r) { return r < kTakenShared ? s_taken[r] : st.taken[r]; };
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
-    const int b = tid * kPer + u;
+    const int b = tid + u * kPlanThreads;
     if (b >= B) continue;
-    if (copy[u]) {
-      st.moves[c++] = make_int4(tail[u], st.taken[s_start[b]], len[u] % page_size, 0);
+    if (copy[u]) {  // numbered in row order
+      st.moves[c_at[u]] = make_int4(tail[u], taken(at[u]), len[u] % page_size, 0);
       atomicSub(&st.ref[tail[u]], 1);
     }
     if (inc[u] > 0) seq_lens[b] = len[u] + inc[u];
@@ -341,7 +394,7 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
       const int mid = (lo + hi + 1) >> 1;
       if (s_start[mid] <= r) lo = mid; else hi = mid - 1;
     }
-    const int page = st.taken[r];
+    const int page = taken(r);
     block_table[(int64_t)lo * max_pages + s_had[lo] + (r - s_start[lo])] = page;
     st.ref[page] = 1;
   }
@@ -357,6 +410,8 @@ __global__ void __launch_bounds__(kPlanThreads)
 k_pages_pair(PageState st, int num_pages) {
   __shared__ int s_warp[32];
   const int tid = threadIdx.x;
+  pdl_launch_dependents();  // the moving blocks may come in and wait
+  pdl_wait();
   const int n_used = num_pages - st.hdr[kHdrFree];
   const int words = (num_pages + 31) / 32;
   const uint32_t call = (uint32_t)st.hdr[kHdrCalls] + 1;
@@ -438,6 +493,7 @@ __device__ __forceinline__ void move_units(const PageState& st, const MovePools&
 template <typename V>
 __global__ void __launch_bounds__(kMoveThreads)
 k_pages_copy_tails(PageState st, MovePools pools, int page_size, int64_t jobs_per_pool) {
+  pdl_launch_dependents();
   pdl_wait();
   move_units<V>(st, pools, page_size, false, jobs_per_pool);
 }
@@ -447,6 +503,7 @@ __global__ void __launch_bounds__(kMoveThreads)
 k_pages_move(PageState st, MovePools pools, const int32_t* __restrict__ seq_lens,
              int32_t* __restrict__ block_table, int32_t* __restrict__ page_map, int num_pages,
              int page_size, int B, int max_pages, int64_t jobs_per_pool) {
+  pdl_launch_dependents();
   pdl_wait();
   const int n_used = st.hdr[kHdrUsed];
   const uint32_t call = (uint32_t)st.hdr[kHdrCalls];
@@ -562,26 +619,24 @@ cudaError_t launch_pages_init(const pks_pages_args& a, const PagesLayout& L, cud
 cudaError_t launch_pages_fork(const pks_pages_args& a, const PagesLayout& L, int n,
                               const int32_t* src, const int32_t* dst, const int32_t* tokens,
                               cudaStream_t s) {
-  k_pages_fork<<<n, kRowThreads, 0, s>>>(page_state(a.state, L), a.seq_lens, a.block_table,
-                                         a.num_pages, a.page_size, a.B, a.max_pages, n, src, dst,
-                                         tokens);
-  return cudaGetLastError();
+  return launch_ex(k_pages_fork, dim3(n), dim3(kRowThreads), 0, s, /*pdl=*/true, /*coop=*/false,
+                   page_state(a.state, L), a.seq_lens, a.block_table, a.num_pages, a.page_size, a.B,
+                   a.max_pages, n, src, dst, tokens);
 }
 
 cudaError_t launch_pages_free(const pks_pages_args& a, const PagesLayout& L, int n,
                               const int32_t* rows, const int32_t* keep, cudaStream_t s) {
-  k_pages_free<<<n, kRowThreads, 0, s>>>(page_state(a.state, L), a.seq_lens, a.block_table,
-                                         a.num_pages, a.page_size, a.B, a.max_pages, n, rows,
-                                         keep);
-  return cudaGetLastError();
+  return launch_ex(k_pages_free, dim3(n), dim3(kRowThreads), 0, s, /*pdl=*/true, /*coop=*/false,
+                   page_state(a.state, L), a.seq_lens, a.block_table, a.num_pages, a.page_size, a.B,
+                   a.max_pages, n, rows, keep);
 }
 
 cudaError_t launch_pages_extend(const pks_pages_args& a, const PagesLayout& L, const int32_t* add,
                                 cudaStream_t s) {
   const PageState st = page_state(a.state, L);
-  k_pages_extend<<<1, kPlanThreads, 0, s>>>(st, a.seq_lens, a.block_table, a.num_pages,
-                                            a.page_size, a.B, a.max_pages, add);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_ex(k_pages_extend, dim3(1), dim3(kPlanThreads), 0, s, /*pdl=*/true,
+                            /*coop=*/false, st, a.seq_lens, a.block_table, a.num_pages, a.page_size,
+                            a.B, a.max_pages, add);
   if (e != cudaSuccess || a.n_pools == 0) return e;
   const int w = move_width(a);
   const int64_t jobs = move_jobs_per_pool(a, w);
@@ -596,8 +651,8 @@ cudaError_t launch_pages_extend(const pks_pages_args& a, const PagesLayout& L, c
 cudaError_t launch_pages_compact(const pks_pages_args& a, const PagesLayout& L, int32_t* page_map,
                                  cudaStream_t s) {
   const PageState st = page_state(a.state, L);
-  k_pages_pair<<<1, kPlanThreads, 0, s>>>(st, a.num_pages);
-  cudaError_t e = cudaGetLastError();
+  cudaError_t e = launch_ex(k_pages_pair, dim3(1), dim3(kPlanThreads), 0, s, /*pdl=*/true,
+                            /*coop=*/false, st, a.num_pages);
   if (e != cudaSuccess) return e;
   const int w = move_width(a);
   const int64_t jobs = move_jobs_per_pool(a, w);
