@@ -75,7 +75,7 @@ struct Request {
 // plan header words
 constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTiles = 5,
               kShare = 6, kWideCtas = 7, kBig = 8, kPieces = 9, kSmall = 10, kClaim = 11,
-              kBigTiles = 12;  // (64 bits)
+              kBigTiles = 12 /* 64 bits */, kDealtTiles = 14;
 
 struct PlanPtrs {
   int32_t* hdr;
@@ -127,21 +127,22 @@ constexpr int kPairNs = 1950, kSingleNs = 4000, kStreamNsPerKb = 24;
 // computes it, so that results do not depend on who does.
 struct Pieces {
   int64_t T, big_tiles;
-  int big, n, small;
+  int big, n, small, share;
   __device__ __forceinline__ Pieces(const int32_t* hdr, int ngroups)
       : T((int64_t)hdr[kTiles] * ngroups),
         big_tiles(*reinterpret_cast<const int64_t*>(hdr + kBigTiles)),
         big(hdr[kBig]),
         n(hdr[kPieces]),
-        small(hdr[kSmall]) {}
+        small(hdr[kSmall]),
+        share(hdr[kDealtTiles]) {}
   __device__ __forceinline__ int64_t lo(int p) const {
-    if (p < big) return p * big_tiles / big;
+    if (p < big) return (int64_t)p * share;
     const int64_t x = big_tiles + (int64_t)(p - big) * small;
     return x < T ? x : T;
   }
   // the piece that holds tile f
   __device__ __forceinline__ int of(int64_t f) const {
-    if (f < big_tiles) return (int)(((f + 1) * big + big_tiles - 1) / big_tiles - 1);
+    if (f < big_tiles) return (int)(f / share);
     return big + (int)((f - big_tiles) / small);
   }
 };
@@ -370,6 +371,10 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
       big_tiles = min(T, big * (all_ns * kDealt / 16 / tile_ns));
     }
     big = min(big, (big_tiles + kNarrowLeast - 1) / kNarrowLeast);
+    const int64_t share = big > 0 ? (big_tiles + big - 1) / big : 1;
+    big = (big_tiles + share - 1) / share;
+    big_tiles = min(T, big * share);
+    pl.hdr[kDealtTiles] = (int)share;
     pl.hdr[kUnits] = U;
     pl.hdr[kTiles] = all.w;
     pl.hdr[kShare] = S;
@@ -687,21 +692,28 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     const uint32_t tS = tmem + lane_off + kTmemS + g * kTile, tO = tmem + lane_off + g * 128;
     const uint64_t scale2 = tc::pack2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     uint32_t n_job = 0, n_piece = 0, n_split = 0;
-    while (walk.more() && ok) {
-      const Piece pc = walk.next();
+    // (the first round is a job on whatever the tensor memory holds: it brings
+    // the code into the instruction cache while the first tiles are on their way,
+    // 2 us that the first job took longer otherwise)
+    for (bool dry = walk.more(); (dry || walk.more()) && ok; dry = false) {
+      Piece pc = {};
+      pc.jobs0 = pc.jobs1 = 1;
+      if (!dry) pc = walk.next();
       const int x = (pc.pair ? g * kRows : 0) + (tid & (kRows - 1));  // row of the item
       const int64_t row = pc.slot + x;
       const bool mine = x < pc.it.nrows;
       const int my_jobs = g ? pc.jobs1 : pc.jobs0;
-      const bool idle = !__any_sync(0xffffffffu, mine);  // no row of this warp counts
+      const bool idle = !dry && !__any_sync(0xffffffffu, mine);  // no row of this warp counts
       // tokens this row sees
       int limit = pc.it.t1;
       if (pc.it.own && sh.causal && mine) limit = pc.it.own - sh.Nq + (pc.it.row0 + x) / sh.G + 1;
       limit -= pc.it.t0 + pc.t_lo * kTile;
       float m_run = kNegInf, l_run = 0.f;
       for (int i = 0; i < my_jobs; ++i) {
-        if (!(ok = wait(&bar_s[g], n_job & 1))) break;
-        ++n_job;
+        if (!dry) {
+          if (!(ok = wait(&bar_s[g], n_job & 1))) break;
+          ++n_job;
+        }
         tc::fence_after();
         if (!idle) {
           const int nv = limit - (pc.pair ? i : 2 * i + g) * kTile;  // valid columns
@@ -775,14 +787,14 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           uint32_t pk[32];
           weights(s0, pk);
           weights(s1, pk + 16);
-          tc::tmem_st32(tS, pk);
+          if (!dry) tc::tmem_st32(tS, pk);  // (the first S may be there already)
           tc::tmem_st_wait();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive(&bar_p[g][0]);
+          if (lane == 0 && !dry) tc::mbar_arrive(&bar_p[g][0]);
           weights(s2, pk);
           weights(s3, pk + 16);
-          tc::tmem_st32(tS + 32, pk);
+          if (!dry) tc::tmem_st32(tS + 32, pk);
           float la, lb, lc, ld;
           tc::unpack2(sum_a, la, lb);
           tc::unpack2(sum_b, lc, ld);
@@ -794,8 +806,9 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bar_p[g][1]);
+        if (lane == 0 && !dry) tc::mbar_arrive(&bar_p[g][1]);
       }
+      if (dry) continue;
       // ---- the piece's partial
       if (!ok) break;
       if (my_jobs == 0) continue;  // (one tile: it was the other group's)
@@ -1314,8 +1327,13 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
       if (p >= pieces.n) return;
       f = pieces.lo(p);
       f_end = pieces.lo(p + 1);
-      cg = (int)(f / Treq);
-      const int fb = (int)(f - (int64_t)cg * Treq);
+      cg = 0;
+      int64_t rest = f;
+      while (rest >= Treq) {
+        rest -= Treq;
+        ++cg;
+      }
+      const int fb = (int)rest;
       int l = 0, h = B - 1;
       while (l < h) {
         const int mid = (l + h + 1) >> 1;
@@ -1446,11 +1464,19 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     uint32_t qb[KS][2];
     float o[MT][4], m_h[2] = {kNegInf, kNegInf}, l_h[2] = {0.f, 0.f};
     int lim[2] = {0, 0};  // own tokens that the thread's two rows see
-    for (uint32_t k = 0;; ++k) {
-      const uint32_t s = k % N::kStages;
-      if (!(ok = wait(&bar_full[s], (k / N::kStages) & 1))) break;
-      const Tile t = s_tile[k % kTileRing];
-      if (t.flags & kEnd) break;
+    // (the first round is on a tile of no tokens: it brings the loop's code into
+    // the instruction cache while the first copies are on their way, 2 us that
+    // the first tile took longer otherwise)
+    for (uint32_t k = ~0u;; ++k) {
+      const bool dry = k == ~0u;
+      const uint32_t s = dry ? 0 : k % N::kStages;
+      Tile t = {};
+      t.flags = kFirst;
+      if (!dry) {
+        if (!(ok = wait(&bar_full[s], (k / N::kStages) & 1))) break;
+        t = s_tile[k % kTileRing];
+        if (t.flags & kEnd) break;
+      }
       if (t.flags & kFirst) {
         const int head = t.g * HG + hh, j = c0 + g8;
         const __nv_bfloat16* src =
@@ -1525,7 +1551,7 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
         mma_16816(o[mt], a, pb0, pb1);
       }
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&bar_empty[s]);
+      if (lane == 0 && !dry) tc::mbar_arrive(&bar_empty[s]);
       if (t.flags & kLast) {
         const int64_t at = (((int64_t)t.piece + (int64_t)t.g * B + t.b) * HG + hh) * sh.R;
 #pragma unroll
