@@ -62,7 +62,8 @@ struct Item {
 struct Start {
   Item it;
   int head, item;
-  int pad[2];
+  int tile;       // of the item
+  int pad;
 };
 // What the merge needs of a request.
 struct Request {
@@ -467,6 +468,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
         st.it = it;
         st.head = h;
         st.item = i;
+        st.tile = (int)(c * S - u0);
         pl.starts[c] = st;
       }
     }
@@ -563,23 +565,23 @@ struct Piece {
 // A CTA's walk over its tiles; every role walks the same pieces.
 struct Walk {
   const Item* items;
-  int64_t u, end;       // next tile and the CTA's last + 1, over all heads
-  int head, item;
-  int U, n_items, slots_head, cta;
-  __device__ __forceinline__ bool more() const { return u < end; }
+  int left;             // tiles to come
+  int head, item, tile; // the next one
+  const int* sizes;     // items and partial rows of a head (shared memory)
+  __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ Piece next() {
     Piece p;
     p.it = items[item];
     p.head = head;
-    const int nt = (p.it.t1 - p.it.t0 + kTile - 1) / kTile;
-    p.t_lo = (int)(u - ((int64_t)head * U + p.it.unit0));
-    p.nt = (int)(end - u < nt - p.t_lo ? end - u : nt - p.t_lo);
+    p.t_lo = tile;
+    p.nt = min(left, (p.it.t1 - p.it.t0 + kTile - 1) / kTile - tile);
     p.pair = p.it.nrows > kRows;
     p.jobs1 = p.pair ? p.nt : p.nt / 2;
     p.jobs0 = p.pair ? p.nt : p.nt - p.jobs1;
-    p.slot = (int64_t)head * slots_head + p.it.slot0 + (int64_t)kItemRows * cta;
-    u += p.nt;
-    if (++item == n_items) {
+    p.slot = (int64_t)head * sizes[1] + p.it.slot0 + (int64_t)kItemRows * blockIdx.x;
+    left -= p.nt;
+    tile = 0;
+    if (++item == sizes[0]) {
       item = 0;
       ++head;
     }
@@ -595,7 +597,7 @@ __device__ __forceinline__ void store8(float* dst, const float (&v)[8]) {
 }
 
 // registers of the softmax warpgroups and of the others: the launch's 512 x 128
-constexpr int kSoftmaxRegs = 184, kOtherRegs = 72;
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "the launch's registers");
 
 template <int D>
@@ -618,7 +620,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       bar_free[W::kSlotsN],      bar_q, bar_qfree, bar_s[2], bar_p[2][2], bar_turn[2], bar_o[2], bar_x[2], bar_y[2], bar_drain[2];
   __shared__ float2 s_ml[kRows];  // a row's maximum and sum, group 1's and then group 0's
   __shared__ uint32_t s_tmem;
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_sizes[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t base = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t sQ = base, sKV = base + 2 * W::kTileBytes;
@@ -659,16 +661,18 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   {
     const Start st = pl.starts[cta];  // (one round trip with the header)
     const int S = pl.hdr[kShare], W = pl.hdr[kWideCtas];
+    const int64_t total = (int64_t)pl.hdr[kUnits] * sh.Hkv - (int64_t)cta * S;
+    if (lane == 0) {  // (all warps write the same)
+      s_sizes[0] = pl.hdr[kItems];
+      s_sizes[1] = pl.hdr[kSlots];
+    }
+    __syncwarp();
     walk.items = pl.items;
-    walk.U = pl.hdr[kUnits];
-    walk.n_items = pl.hdr[kItems];
-    walk.slots_head = pl.hdr[kSlots];
-    walk.cta = cta;
+    walk.sizes = s_sizes;
     walk.head = st.head;
     walk.item = st.item;
-    const int64_t total = (int64_t)walk.U * sh.Hkv;
-    walk.u = (int64_t)cta * S;
-    walk.end = cta >= W ? walk.u : walk.u + S < total ? walk.u + S : total;
+    walk.tile = st.tile;
+    walk.left = cta >= W ? 0 : (int)min((int64_t)S, total);
   }
   bool ok = true;
   // a wait of the whole warp
@@ -784,17 +788,19 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
             }
           }
           // P takes the place of S columns, all of which are in registers
-          uint32_t pk[32];
+          uint32_t pk[16];
           weights(s0, pk);
-          weights(s1, pk + 16);
-          if (!dry) tc::tmem_st32(tS, pk);  // (the first S may be there already)
+          if (!dry) tc::tmem_st16(tS, pk);  // (the first S may be there already)
+          weights(s1, pk);
+          if (!dry) tc::tmem_st16(tS + 16, pk);
           tc::tmem_st_wait();
           tc::fence_before();
           __syncwarp();
           if (lane == 0 && !dry) tc::mbar_arrive(&bar_p[g][0]);
           weights(s2, pk);
-          weights(s3, pk + 16);
-          if (!dry) tc::tmem_st32(tS + 32, pk);
+          if (!dry) tc::tmem_st16(tS + 32, pk);
+          weights(s3, pk);
+          if (!dry) tc::tmem_st16(tS + 48, pk);
           float la, lb, lc, ld;
           tc::unpack2(sum_a, la, lb);
           tc::unpack2(sum_b, lc, ld);
@@ -920,9 +926,10 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         auto landed = [&](int t, int v) -> bool {
           const uint32_t sl = (n_slot + 2 * t + v) % W::kSlotsN;
           const bool tma = t < by_tma;
-          uint32_t& ph = tma ? ph_tma : ph_cp;
-          const bool r = wait(tma ? &bar_tma[sl] : &bar_cp[sl], (ph >> sl) & 1);
-          ph ^= 1u << sl;
+          const bool r = wait(tma ? &bar_tma[sl] : &bar_cp[sl],
+                              ((tma ? ph_tma : ph_cp) >> sl) & 1);
+          ph_tma ^= (uint32_t)tma << sl;
+          ph_cp ^= (uint32_t)!tma << sl;
           return r;
         };
         // (the turn passes with four of S's steps to go: the other issuer's first
@@ -1067,7 +1074,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       int row = 0;
       if (lw == 0 && walk.more()) {
         const Item first = pl.starts[cta].it;
-        row = box_row(first, (int)(walk.u - ((int64_t)walk.head * walk.U + first.unit0)));
+        row = box_row(first, walk.tile);
       }
       while (walk.more() && ok) {
         const Piece pc = walk.next();
