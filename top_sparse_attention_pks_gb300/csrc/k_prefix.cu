@@ -110,17 +110,17 @@ __device__ __forceinline__ void flag_error(int32_t* err, int code) { atomicCAS(e
 
 constexpr int kWideLeast = 2;                  // tiles a wide CTA takes at least
 constexpr int kNarrowLeast = 2;                // tiles a narrow CTA takes at least
-constexpr int kSmallLeast = 6;                 // tiles of a small narrow piece at least
+constexpr int kSmallLeast = 12;                // tiles of a small narrow piece at least
 constexpr int kSmallPerSm = 8;                 // small pieces an SM at most
 // Beside the wide kernel, a narrow CTA is dealt this share (in 1/16) of what it
 // could stream in the time estimated for all; the rest goes to whichever SM is
 // free.
-constexpr int kDealt = 8;
+constexpr int kDealt = 13;
 // Estimated nanoseconds an SM spends with D = 128 (half with D = 64): on a wide
 // tile with two row blocks (its products), on one with a single block (its bytes,
 // while the narrow kernel loads the memory too), and on a kilobyte streamed by the
 // narrow kernel.
-constexpr int kPairNs = 1950, kSingleNs = 4000, kStreamNsPerKb = 24;
+constexpr int kPairNs = 1950, kSingleNs = 2000, kStreamNsPerKb = 24;
 
 // The narrow kernel's pieces: `big` equal ones that cover the first big_tiles of
 // the T tiles (all heads), one for each CTA that starts at once, and small ones
@@ -150,22 +150,9 @@ struct Pieces {
 
 // ------------------------------------------------------------------ plan ---
 
-constexpr int kPlanThreads = 256;
-constexpr int kPlanArrays = 13;
-
-template <typename T, typename F>
-__device__ __forceinline__ T block_reduce(T v, F op, T* s_red) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) v = op(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if (lane == 0) s_red[warp] = v;
-  __syncthreads();
-  v = s_red[0];
-#pragma unroll
-  for (int w = 1; w < kPlanThreads / 32; ++w) v = op(v, s_red[w]);
-  return v;
-}
+constexpr int kPlanThreads = 512;
+constexpr int kPlanArrays = 14;
+constexpr int kPlanOneBlock = 32;  // requests up to which one block does it all
 
 // exclusive scan over the block of four values a thread
 __device__ __forceinline__ int4 block_scan_ex(int4 v, int4* s_red, int4& total) {
@@ -198,64 +185,76 @@ __device__ __forceinline__ int seen_by_all(int len, int causal, int Nq) {
   return v < 0 ? 0 : v;
 }
 
-// A block a request finds what it shares with its group's longest member; the
-// last block to finish makes the plan.
+// A warp a request finds what it shares with its group's longest member; then one
+// block, the only one or the last to finish, makes the plan.
 __global__ void __launch_bounds__(kPlanThreads)
 k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
               const int32_t* __restrict__ prefix_group, PlanPtrs pl, PrefixShape sh) {
-  extern __shared__ int s_dyn[];  // [kPlanArrays][B] in the last block
+  extern __shared__ int s_dyn[];  // [kPlanArrays][B]
   __shared__ int4 s_red4[kPlanThreads / 32];
-  __shared__ long long s_red64[kPlanThreads / 32];
-  __shared__ int s_red[kPlanThreads / 32];
   __shared__ int s_last;
-  const int tid = threadIdx.x, B = sh.B;
+  const int tid = threadIdx.x, lane = tid & 31, B = sh.B;
   const int max_len = sh.max_pages * sh.page_size;
+  const bool alone = gridDim.x == 1;
+  int* s_first = s_dyn;           // by request
+  int* s_lead = s_first + B;
+  int* s_eq = s_lead + B;
+  int* s_len = s_eq + B;
+  int* s_group = s_len + B;
   pdl_launch_dependents();
   pdl_wait();
-  auto length = [&](int b) {
-    const int n = seq_lens[b];
-    return n < 0 || n > max_len ? 0 : n;
-  };
-  auto group = [&](int b) {
+  for (int b = tid; b < B; b += kPlanThreads) {
+    int n = seq_lens[b];
     const int g = prefix_group ? prefix_group[b] : -1;
-    return g < 0 ? -1 : g;
-  };
-  auto pages = [&](int n) { return (n + sh.page_size - 1) / sh.page_size; };
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
-    const int len = length(b), g = group(b);
-    if (tid == 0) {
-      if (len != seq_lens[b]) flag_error(pl.hdr + kErrWord, kErrLen);
-      pl.lens[b] = len;
+    if (n < 0 || n > max_len) {
+      flag_error(pl.hdr + kErrWord, kErrLen);
+      n = 0;
     }
+    s_len[b] = n;
+    s_group[b] = g < 0 ? -1 : g;
+    if (blockIdx.x == 0) pl.lens[b] = n;
+  }
+  __syncthreads();
+  for (int b = blockIdx.x * (kPlanThreads / 32) + (tid >> 5); b < B;
+       b += gridDim.x * (kPlanThreads / 32)) {
+    const int len = s_len[b], g = s_group[b];
     int shared = 0, first = b, lead = b;
     if (g >= 0) {
       // longest member (the first of the longest) and first member of the group
       long long best = -1;
       int low = B;
-      for (int c = tid; c < B; c += kPlanThreads)
-        if (group(c) == g) {
-          const long long key = ((long long)length(c) << 12) | (kMaxB - 1 - c);
+      for (int c = lane; c < B; c += 32)
+        if (s_group[c] == g) {
+          const long long key = ((long long)s_len[c] << 12) | (kMaxB - 1 - c);
           best = key > best ? key : best;
           low = c < low ? c : low;
         }
-      best = block_reduce(best, [](long long a, long long c) { return a > c ? a : c; }, s_red64);
-      first = block_reduce(low, [](int a, int c) { return a < c ? a : c; }, s_red);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) {
+        const long long other = __shfl_xor_sync(0xffffffffu, best, o);
+        best = other > best ? other : best;
+      }
+      first = __reduce_min_sync(0xffffffffu, low);
       lead = kMaxB - 1 - (int)(best & (kMaxB - 1));
       // leading entries equal to the longest member's
-      const int np = pages(len);
+      const int np = (len + sh.page_size - 1) / sh.page_size;
       const int32_t* mine = block_table + (int64_t)b * sh.max_pages;
       const int32_t* its = block_table + (int64_t)lead * sh.max_pages;
       int eq = np;
       if (lead != b) {
-        constexpr int kStep = 4;
-        for (int p0 = 0; p0 < np; p0 += kPlanThreads * kStep) {
-          int differs = np;
+        constexpr int kStep = 16;
+        for (int p0 = 0; p0 < np; p0 += 32 * kStep) {
+          int differs = np, x[kStep], y[kStep];
 #pragma unroll
           for (int u = 0; u < kStep; ++u) {
-            const int p = p0 + u * kPlanThreads + tid;
-            if (p < np && mine[p] != its[p]) differs = p < differs ? p : differs;
+            const int p = p0 + u * 32 + lane;
+            x[u] = p < np ? mine[p] : 0;
+            y[u] = p < np ? its[p] : 0;
           }
-          eq = block_reduce(differs, [](int a, int c) { return a < c ? a : c; }, s_red);
+#pragma unroll
+          for (int u = kStep - 1; u >= 0; --u)
+            if (x[u] != y[u]) differs = p0 + u * 32 + lane;
+          eq = __reduce_min_sync(0xffffffffu, differs);
           if (eq < np) break;
         }
       }
@@ -263,26 +262,28 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
       const int64_t tok = (int64_t)eq * sh.page_size;
       shared = tok < seen ? (int)tok : seen;
     }
-    if (tid == 0) {
-      pl.eq[b] = shared;
-      pl.first[b] = first;
-      pl.lead[b] = lead;
+    if (lane == 0) {
+      (alone ? s_eq : pl.eq)[b] = shared;
+      (alone ? s_first : pl.first)[b] = first;
+      (alone ? s_lead : pl.lead)[b] = lead;
     }
   }
-  __threadfence();
-  __syncthreads();
-  if (tid == 0) s_last = atomicAdd(pl.hdr + kTicket, 1) == (int)gridDim.x - 1;
-  __syncthreads();
-  if (!s_last) return;
-  __threadfence();
-  if (tid == 0) pl.hdr[kTicket] = 0;
+  if (!alone) {
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) s_last = atomicAdd(pl.hdr + kTicket, 1) == (int)gridDim.x - 1;
+    __syncthreads();
+    if (!s_last) return;
+    __threadfence();
+    if (tid == 0) pl.hdr[kTicket] = 0;
+    for (int b = tid; b < B; b += kPlanThreads) {
+      s_first[b] = __ldcg(pl.first + b);
+      s_lead[b] = __ldcg(pl.lead + b);
+      s_eq[b] = __ldcg(pl.eq + b);
+    }
+  }
 
-  // ---- the last block.  The requests' findings, all in one round trip
-  int* s_first = s_dyn;           // by request
-  int* s_lead = s_first + B;
-  int* s_eq = s_lead + B;
-  int* s_len = s_eq + B;
-  int* s_pre = s_len + B;         // by first member: the group's prefix
+  int* s_pre = s_group + B;       // by first member: the group's prefix
   int* s_cnt = s_pre + B;         // ... members that take part
   int* s_at = s_cnt + B;          // ... the most shared; then members placed so far
   int* s_item = s_at + B;         // ... first prefix item, unit and slot
@@ -292,10 +293,6 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   int* s_ounit = s_oitem + B;
   int* s_oslot = s_ounit + B;
   for (int b = tid; b < B; b += kPlanThreads) {
-    s_first[b] = __ldcg(pl.first + b);
-    s_lead[b] = __ldcg(pl.lead + b);
-    s_eq[b] = __ldcg(pl.eq + b);
-    s_len[b] = __ldcg(pl.lens + b);
     s_pre[b] = 0x7fffffff;
     s_cnt[b] = s_at[b] = 0;
   }
@@ -350,13 +347,19 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   const int64_t pairs_ns = (total - singles) * kPairNs * sh.D / 128;
   const int64_t wide_ns = pairs_ns + singles * kSingleNs * sh.D / 128;
   const int64_t tile_bytes = (int64_t)kNarrowTile * sh.D * 4;  // K and V, one head
-  const int64_t narrow_ns = all.w * sh.Hkv * tile_bytes / 1024 * kStreamNsPerKb;
+  const int64_t narrow_ns = (int64_t)all.w * sh.Hkv * tile_bytes / 1024 * kStreamNsPerKb;
   int W = sh.wide_grid;
   if (narrow_ns > 0 && total > 0) {
     W = (int)((wide_ns * sh.wide_grid + (wide_ns + narrow_ns) / 2) / (wide_ns + narrow_ns));
     W = max(1, min(sh.wide_grid - 1, W));
   }
-  const bool beside = narrow_ns > 0 && total > 0;
+  // side by side only when the wide kernel needs three quarters of the narrow
+  // one's time at least: its CTAs get less than their share of a memory that the
+  // narrow kernel loads (with 2% of the bytes wide, 64 requests of up to 32k
+  // tokens: 588 us side by side on 9 SMs, 950 on 3, 578 one after the other; with
+  // half of them, 32 requests with four drafts: 88 against 97)
+  const bool beside = narrow_ns > 0 && total > 0 && 4 * wide_ns >= 3 * narrow_ns;
+  if (!beside) W = sh.wide_grid;
   const int sms_left = beside ? sh.wide_grid - W : sh.wide_grid;
   W = (int)min((int64_t)W, (total + kWideLeast - 1) / kWideLeast);
   const int S = total > 0 ? (int)((total + W - 1) / W) : 1;
@@ -1926,8 +1929,9 @@ cudaError_t launch_prefix_plan(const pks_prefix_args& a, const PrefixLayout& L, 
   cudaError_t e = allow_smem(k_prefix_plan, kPlanArrays * sizeof(int32_t) * kMaxB, done);
   if (e != cudaSuccess) return e;
   const PrefixShape sh = prefix_shape(a);
-  const int grid = a.B < 2 * sh.wide_grid ? a.B : 2 * sh.wide_grid;
-  return launch_ex(k_prefix_plan, dim3(a.prefix_group ? grid : 1), dim3(kPlanThreads),
+  const int warps = kPlanThreads / 32, blocks = (a.B + warps - 1) / warps;
+  const int grid = !a.prefix_group || a.B <= kPlanOneBlock ? 1 : blocks;
+  return launch_ex(k_prefix_plan, dim3(grid), dim3(kPlanThreads),
                    kPlanArrays * sizeof(int32_t) * (size_t)a.B, s, /*pdl=*/true, /*coop=*/false, a.seq_lens,
                    a.block_table, a.prefix_group, plan_ptrs(a.workspace, L), sh);
 }
