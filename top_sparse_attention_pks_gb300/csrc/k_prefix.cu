@@ -106,6 +106,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// quotient of two non-negative numbers that nearly always fit in 32 bits, where
+// the division takes a fraction of the time
+__device__ __forceinline__ int64_t quot(int64_t a, int64_t b) {
+  if (((uint64_t)a | (uint64_t)b) >> 32) return a / b;
+  return (int64_t)((uint32_t)a / (uint32_t)b);
+}
+
 __device__ __forceinline__ void flag_error(int32_t* err, int code) { atomicCAS(err, 0, code); }
 
 constexpr int kWideLeast = 2;                  // tiles a wide CTA takes at least
@@ -143,8 +150,8 @@ struct Pieces {
   }
   // the piece that holds tile f
   __device__ __forceinline__ int of(int64_t f) const {
-    if (f < big_tiles) return (int)(f / share);
-    return big + (int)((f - big_tiles) / small);
+    if (f < big_tiles) return (int)quot(f, share);
+    return big + (int)quot(f - big_tiles, small);
   }
 };
 
@@ -152,31 +159,8 @@ struct Pieces {
 
 constexpr int kPlanThreads = 512;
 constexpr int kPlanArrays = 14;
+constexpr int kPlanWarps = 4;      // warps a request otherwise
 constexpr int kPlanOneBlock = 32;  // requests up to which one block does it all
-
-// exclusive scan over the block of four values a thread
-__device__ __forceinline__ int4 block_scan_ex(int4 v, int4* s_red, int4& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  auto add = [](int4 a, int4 c) { return make_int4(a.x + c.x, a.y + c.y, a.z + c.z, a.w + c.w); };
-  int4 x = v;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int4 y = make_int4(__shfl_up_sync(0xffffffffu, x.x, o), __shfl_up_sync(0xffffffffu, x.y, o),
-                             __shfl_up_sync(0xffffffffu, x.z, o), __shfl_up_sync(0xffffffffu, x.w, o));
-    if (lane >= o) x = add(x, y);
-  }
-  __syncthreads();
-  if (lane == 31) s_red[warp] = x;
-  __syncthreads();
-  int4 before = make_int4(-v.x, -v.y, -v.z, -v.w);
-  total = make_int4(0, 0, 0, 0);
-#pragma unroll
-  for (int w = 0; w < kPlanThreads / 32; ++w) {
-    if (w < warp) before = add(before, s_red[w]);
-    total = add(total, s_red[w]);
-  }
-  return add(before, x);
-}
 
 // tokens every query of the request sees
 __device__ __forceinline__ int seen_by_all(int len, int causal, int Nq) {
@@ -185,14 +169,14 @@ __device__ __forceinline__ int seen_by_all(int len, int causal, int Nq) {
   return v < 0 ? 0 : v;
 }
 
-// A warp a request finds what it shares with its group's longest member; then one
+// Warps find what each request shares with its group's longest member; then one
 // block, the only one or the last to finish, makes the plan.
 __global__ void __launch_bounds__(kPlanThreads)
 k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
               const int32_t* __restrict__ prefix_group, PlanPtrs pl, PrefixShape sh) {
   extern __shared__ int s_dyn[];  // [kPlanArrays][B]
-  __shared__ int4 s_red4[kPlanThreads / 32];
-  __shared__ int s_last;
+  __shared__ int s_total[3 + 8];  // tiles, those with one row block, narrow tiles; the scans'
+  __shared__ int s_last, s_equal[kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, B = sh.B;
   const int max_len = sh.max_pages * sh.page_size;
   const bool alone = gridDim.x == 1;
@@ -200,7 +184,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   int* s_lead = s_first + B;
   int* s_eq = s_lead + B;
   int* s_len = s_eq + B;
-  int* s_group = s_len + B;
+  int* s_group = s_dyn + (kPlanArrays - 1) * B;  // (the last of the quantities, later)
   pdl_launch_dependents();
   pdl_wait();
   for (int b = tid; b < B; b += kPlanThreads) {
@@ -215,10 +199,16 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     if (blockIdx.x == 0) pl.lens[b] = n;
   }
   __syncthreads();
-  for (int b = blockIdx.x * (kPlanThreads / 32) + (tid >> 5); b < B;
-       b += gridDim.x * (kPlanThreads / 32)) {
-    const int len = s_len[b], g = s_group[b];
-    int shared = 0, first = b, lead = b;
+  // (four warps a request when there are more blocks than one)
+  const int wpr = alone ? 1 : kPlanWarps, at_once = kPlanThreads / 32 / wpr;
+  const int slot = (tid >> 5) / wpr, sub = (tid >> 5) % wpr;
+  for (int b0 = blockIdx.x * at_once; b0 < B; b0 += gridDim.x * at_once) {
+    const int b = b0 + slot;
+    const int len = b < B ? s_len[b] : 0, g = b < B ? s_group[b] : -1;
+    const int np = (len + sh.page_size - 1) / sh.page_size;
+    int first = b, lead = b;
+    if (tid < at_once) s_equal[tid] = 0x7fffffff;
+    __syncthreads();
     if (g >= 0) {
       // longest member (the first of the longest) and first member of the group
       long long best = -1;
@@ -237,36 +227,36 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
       first = __reduce_min_sync(0xffffffffu, low);
       lead = kMaxB - 1 - (int)(best & (kMaxB - 1));
       // leading entries equal to the longest member's
-      const int np = (len + sh.page_size - 1) / sh.page_size;
       const int32_t* mine = block_table + (int64_t)b * sh.max_pages;
       const int32_t* its = block_table + (int64_t)lead * sh.max_pages;
-      int eq = np;
-      if (lead != b) {
-        constexpr int kStep = 16;
-        for (int p0 = 0; p0 < np; p0 += 32 * kStep) {
-          int differs = np, x[kStep], y[kStep];
+      constexpr int kStep = 16;
+      for (int p0 = sub * 32 * kStep; lead != b && p0 < np; p0 += wpr * 32 * kStep) {
+        int differs = 0x7fffffff, x[kStep], y[kStep];
 #pragma unroll
-          for (int u = 0; u < kStep; ++u) {
-            const int p = p0 + u * 32 + lane;
-            x[u] = p < np ? mine[p] : 0;
-            y[u] = p < np ? its[p] : 0;
-          }
+        for (int u = 0; u < kStep; ++u) {
+          const int p = p0 + u * 32 + lane;
+          x[u] = p < np ? mine[p] : 0;
+          y[u] = p < np ? its[p] : 0;
+        }
 #pragma unroll
-          for (int u = kStep - 1; u >= 0; --u)
-            if (x[u] != y[u]) differs = p0 + u * 32 + lane;
-          eq = __reduce_min_sync(0xffffffffu, differs);
-          if (eq < np) break;
+        for (int u = kStep - 1; u >= 0; --u)
+          if (x[u] != y[u]) differs = p0 + u * 32 + lane;
+        differs = __reduce_min_sync(0xffffffffu, differs);
+        if (differs != 0x7fffffff) {
+          if (lane == 0) atomicMin(&s_equal[slot], differs);
+          break;
         }
       }
-      const int seen = seen_by_all(len, sh.causal, sh.Nq);
-      const int64_t tok = (int64_t)eq * sh.page_size;
-      shared = tok < seen ? (int)tok : seen;
     }
-    if (lane == 0) {
-      (alone ? s_eq : pl.eq)[b] = shared;
+    __syncthreads();
+    if (lane == 0 && sub == 0 && b < B) {
+      const int seen = seen_by_all(len, sh.causal, sh.Nq);
+      const int64_t tok = (int64_t)min(np, s_equal[slot]) * sh.page_size;
+      (alone ? s_eq : pl.eq)[b] = g < 0 ? 0 : tok < seen ? (int)tok : seen;
       (alone ? s_first : pl.first)[b] = first;
       (alone ? s_lead : pl.lead)[b] = lead;
     }
+    __syncthreads();
   }
   if (!alone) {
     __threadfence();
@@ -283,28 +273,37 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     }
   }
 
-  int* s_pre = s_group + B;       // by first member: the group's prefix
-  int* s_cnt = s_pre + B;         // ... members that take part
-  int* s_at = s_cnt + B;          // ... the most shared; then members placed so far
-  int* s_item = s_at + B;         // ... first prefix item, unit and slot
+  // eight quantities by request (those of a group by its first member), summed up
+  // over the requests before: members; prefix items, tiles and partial rows; narrow
+  // tiles; own items, tiles and partial rows
+  int* s_pre = s_len + B;    // by first member: the group's prefix
+  int* s_cnt = s_pre + B;    // ... members that take part
+  int* s_at = s_cnt + B;
+  int* s_item = s_at + B;
   int* s_unit = s_item + B;
   int* s_slot = s_unit + B;
-  int* s_oitem = s_slot + B;      // by request: first own item, unit and slot
+  int* s_otile = s_slot + B;
+  int* s_oitem = s_otile + B;
   int* s_ounit = s_oitem + B;
   int* s_oslot = s_ounit + B;
+  int* s_most = s_at;        // first: the most shared, the longest member aside
+#pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads) {
     s_pre[b] = 0x7fffffff;
-    s_cnt[b] = s_at[b] = 0;
+    s_cnt[b] = s_most[b] = 0;
   }
+  if (tid < 3) s_total[tid] = 0;
   __syncthreads();
   // The groups' common prefixes: the least shared length among the members that
   // share at least half of what the second longest shares; members with less
   // stay on their own.
+#pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads)
-    if (s_lead[b] != b) atomicMax(&s_at[s_first[b]], s_eq[b]);
+    if (s_lead[b] != b) atomicMax(&s_most[s_first[b]], s_eq[b]);
   __syncthreads();
+#pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads) {
-    const int f = s_first[b], e = s_eq[b], most = s_at[f];
+    const int f = s_first[b], e = s_eq[b], most = s_most[f];
     if (most >= kMinShared && e >= (most + 1) / 2) {
       atomicMin(&s_pre[f], e);
       atomicAdd(&s_cnt[f], 1);
@@ -319,141 +318,133 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     const int f = s_first[b];
     return s_cnt[f] >= 2 && s_eq[b] >= s_pre[f] ? f : -1;
   };
-  const int per = (B + kPlanThreads - 1) / kPlanThreads;
-  const int b_lo = min(B, tid * per), b_hi = min(B, b_lo + per);
   const int own_blocks = sh.narrow ? 0 : blocks(sh.R);
-  auto own_tiles = [&](int n) { return sh.narrow ? (n + kNarrowTile - 1) / kNarrowTile : 0; };
-  // members, wide tiles, those with a single row block among them, narrow tiles
-  int4 sum = make_int4(0, 0, 0, 0), all;
-  for (int b = b_lo; b < b_hi; ++b) {
-    if (s_cnt[b] >= 2) {
-      const int rows = s_cnt[b] * sh.R;
-      sum.x += s_cnt[b];
-      sum.y += blocks(rows) * tiles(s_pre[b]);
-      sum.z += single(rows) * tiles(s_pre[b]);
-    }
-    const int f = joined(b), own = s_len[b] - (f >= 0 ? s_pre[f] : 0);
-    sum.y += own_blocks * tiles(own);
-    sum.z += own_blocks ? single(sh.R) * tiles(own) : 0;
-    sum.w += own_tiles(own);
+#pragma unroll 1
+  for (int b = tid; b < B; b += kPlanThreads) {
+    const bool has = s_cnt[b] >= 2;
+    const int rows = s_cnt[b] * sh.R, nt = has ? tiles(s_pre[b]) : 0;
+    const int f = joined(b), begin = f >= 0 ? s_pre[f] : 0, own = s_len[b] - begin;
+    s_at[b] = has ? s_cnt[b] : 0;
+    s_unit[b] = has ? blocks(rows) * nt : 0;
+    s_otile[b] = sh.narrow ? (own + kNarrowTile - 1) / kNarrowTile : 0;
+    s_ounit[b] = own_blocks * tiles(own);
+    pl.start[b] = begin;
+    const int u = s_unit[b] + s_ounit[b];
+    if (u) atomicAdd(&s_total[0], u);
+    const int ones = (has ? single(rows) * nt : 0) + (own_blocks ? single(sh.R) * tiles(own) : 0);
+    if (ones) atomicAdd(&s_total[1], ones);
+    if (s_otile[b]) atomicAdd(&s_total[2], s_otile[b]);
   }
-  int4 ex = block_scan_ex(sum, s_red4, all);
-  const int U = all.y;
+  __syncthreads();
+  const int U = s_total[0], own_tiles = s_total[2];
   // SMs for either kernel by the time they will need, and the tiles a wide CTA
   // takes (all of the same number, so that items cut at multiples of it run in
   // step; see the wide kernel)
-  const int64_t total = (int64_t)U * sh.Hkv;
-  const int64_t singles = (int64_t)all.z * sh.Hkv;
-  const int64_t pairs_ns = (total - singles) * kPairNs * sh.D / 128;
-  const int64_t wide_ns = pairs_ns + singles * kSingleNs * sh.D / 128;
-  const int64_t tile_bytes = (int64_t)kNarrowTile * sh.D * 4;  // K and V, one head
-  const int64_t narrow_ns = (int64_t)all.w * sh.Hkv * tile_bytes / 1024 * kStreamNsPerKb;
+  const int64_t total = (int64_t)U * sh.Hkv, singles = (int64_t)s_total[1] * sh.Hkv;
+  const float pairs_ns = (float)(total - singles) * kPairNs * sh.D / 128;
+  const float wide_ns = pairs_ns + (float)singles * kSingleNs * sh.D / 128;
+  const float stage_kb = (float)kNarrowTile * sh.D * 4 / 1024;  // K and V of a tile, one head
+  const float narrow_ns = (float)own_tiles * sh.Hkv * stage_kb * kStreamNsPerKb;
   int W = sh.wide_grid;
-  if (narrow_ns > 0 && total > 0) {
-    W = (int)((wide_ns * sh.wide_grid + (wide_ns + narrow_ns) / 2) / (wide_ns + narrow_ns));
-    W = max(1, min(sh.wide_grid - 1, W));
-  }
   // side by side only when the wide kernel needs three quarters of the narrow
   // one's time at least: its CTAs get less than their share of a memory that the
   // narrow kernel loads (with 2% of the bytes wide, 64 requests of up to 32k
   // tokens: 588 us side by side on 9 SMs, 950 on 3, 578 one after the other; with
   // half of them, 32 requests with four drafts: 88 against 97)
-  const bool beside = narrow_ns > 0 && total > 0 && 4 * wide_ns >= 3 * narrow_ns;
-  if (!beside) W = sh.wide_grid;
+  const bool beside = own_tiles > 0 && total > 0 && 4 * wide_ns >= 3 * narrow_ns;
+  if (beside) {
+    W = (int)(wide_ns / (wide_ns + narrow_ns) * sh.wide_grid + 0.5f);
+    W = max(1, min(sh.wide_grid - 1, W));
+  }
   const int sms_left = beside ? sh.wide_grid - W : sh.wide_grid;
   W = (int)min((int64_t)W, (total + kWideLeast - 1) / kWideLeast);
-  const int S = total > 0 ? (int)((total + W - 1) / W) : 1;
-  W = (int)((total + S - 1) / S);
-  if (tid == 0) {
-    const int64_t T = (int64_t)all.w * (sh.Hkv / sh.hg);
+  const int S = total > 0 ? (int)quot(total + W - 1, W) : 1;
+  // items: a token range in cuts of S tiles, every row block of a cut in turn
+  auto cuts = [&](int nt) { return (int)((unsigned)(nt + S - 1) / (unsigned)S); };
+#pragma unroll 1
+  for (int b = tid; b < B; b += kPlanThreads) {
+    const bool has = s_cnt[b] >= 2;
+    const int rows = s_cnt[b] * sh.R, c = has ? cuts(tiles(s_pre[b])) : 0;
+    const int f = joined(b), oc = own_blocks ? cuts(tiles(s_len[b] - (f >= 0 ? s_pre[f] : 0))) : 0;
+    s_item[b] = c * blocks(rows);
+    s_slot[b] = c * rows;
+    s_oitem[b] = oc * own_blocks;
+    s_oslot[b] = oc * sh.R;
+  }
+  __syncthreads();
+  const int warp = tid >> 5;
+  if (warp < 8) {  // a warp a quantity
+    int* v = s_at + warp * B;
+    int sum = 0;
+#pragma unroll 1
+    for (int b0 = 0; b0 < B; b0 += 32) {
+      const int b = b0 + lane, mine = b < B ? v[b] : 0;
+      int x = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+      }
+      if (b < B) v[b] = sum + x - mine;
+      sum += __shfl_sync(0xffffffffu, x, 31);
+    }
+    if (lane == 0) s_total[3 + warp] = sum;
+  } else if (tid == 8 * 32) {  // the narrow kernel's pieces
+    const int64_t T = (int64_t)own_tiles * (sh.Hkv / sh.hg);
     const int per_sm = sh.narrow_grid / sh.wide_grid;
     int64_t big = (int64_t)sms_left * per_sm, big_tiles = T;
     if (beside) {
-      const int64_t singles_kb = singles * kTile * sh.D * 4 / 1024;
-      const int64_t all_ns = (pairs_ns + singles_kb * kStreamNsPerKb + narrow_ns) / sh.wide_grid;
-      const int64_t tile_ns = sh.hg * tile_bytes / 1024 * kStreamNsPerKb * per_sm;
-      big_tiles = min(T, big * (all_ns * kDealt / 16 / tile_ns));
+      const float all_ns = pairs_ns + narrow_ns + (float)singles * (stage_kb * kTile / kNarrowTile) *
+                                                      kStreamNsPerKb;
+      const float tile_ns = sh.hg * stage_kb * kStreamNsPerKb * per_sm;
+      big_tiles = min(T, big * (int64_t)(all_ns / sh.wide_grid * (kDealt / 16.f) / tile_ns));
     }
     big = min(big, (big_tiles + kNarrowLeast - 1) / kNarrowLeast);
-    const int64_t share = big > 0 ? (big_tiles + big - 1) / big : 1;
-    big = (big_tiles + share - 1) / share;
+    const int64_t share = big_tiles > 0 ? quot(big_tiles + big - 1, big) : 1;
+    big = quot(big_tiles + share - 1, share);
     big_tiles = min(T, big * share);
-    pl.hdr[kDealtTiles] = (int)share;
-    pl.hdr[kUnits] = U;
-    pl.hdr[kTiles] = all.w;
-    pl.hdr[kShare] = S;
-    pl.hdr[kWideCtas] = W;
-    pl.hdr[kBig] = (int)big;
     const int64_t rest = T - big_tiles, most = (int64_t)kSmallPerSm * sh.wide_grid;
-    const int64_t small = max((int64_t)kSmallLeast, (rest + most - 1) / most);
+    const int64_t small = max((int64_t)kSmallLeast, quot(rest + most - 1, most));
+    pl.hdr[kTiles] = own_tiles;
+    pl.hdr[kDealtTiles] = (int)share;
+    pl.hdr[kBig] = (int)big;
     *reinterpret_cast<int64_t*>(pl.hdr + kBigTiles) = big_tiles;
     pl.hdr[kSmall] = (int)small;
-    pl.hdr[kPieces] = (int)(big + (rest + small - 1) / small);
+    pl.hdr[kPieces] = (int)(big + quot(rest + small - 1, small));
     pl.hdr[kClaim] = 0;
-    pl.npre[B] = all.w;
-  }
-  // items: a token range in cuts of S tiles, every row block of a cut in turn
-  int members = ex.x, ot = ex.w;
-  auto cuts = [&](int n) { return (n + S - 1) / S; };
-  sum = make_int4(0, 0, 0, 0);
-  int4 osum = make_int4(0, 0, 0, 0), oall;
-  for (int b = b_lo; b < b_hi; ++b) {
-    if (s_cnt[b] >= 2) {
-      const int rows = s_cnt[b] * sh.R, nt = tiles(s_pre[b]);
-      s_at[b] = members;
-      members += s_cnt[b];
-      sum.x += blocks(rows) * cuts(nt);
-      sum.y += blocks(rows) * nt;
-      sum.z += rows * cuts(nt);
-    }
-    const int f = joined(b), own = s_len[b] - (f >= 0 ? s_pre[f] : 0), nt = tiles(own);
-    pl.npre[b] = ot;
-    pl.start[b] = f >= 0 ? s_pre[f] : 0;
-    ot += own_tiles(own);
-    osum.x += own_blocks * cuts(nt);
-    osum.y += own_blocks * nt;
-    osum.z += own_blocks ? sh.R * cuts(nt) : 0;
-  }
-  ex = block_scan_ex(sum, s_red4, all);
-  int4 oex = block_scan_ex(osum, s_red4, oall);
-  for (int b = b_lo; b < b_hi; ++b) {
-    s_item[b] = ex.x;
-    s_unit[b] = ex.y;
-    s_slot[b] = ex.z;
-    s_oitem[b] = all.x + oex.x;
-    s_ounit[b] = all.y + oex.y;
-    s_oslot[b] = all.z + oex.z;
-    if (s_cnt[b] >= 2) {
-      const int rows = s_cnt[b] * sh.R, nt = tiles(s_pre[b]);
-      ex.x += blocks(rows) * cuts(nt);
-      ex.y += blocks(rows) * nt;
-      ex.z += rows * cuts(nt);
-    }
-    const int f = joined(b), nt = tiles(s_len[b] - (f >= 0 ? s_pre[f] : 0));
-    oex.x += own_blocks * cuts(nt);
-    oex.y += own_blocks * nt;
-    oex.z += own_blocks ? sh.R * cuts(nt) : 0;
-  }
-  const int n_items = all.x + oall.x;
-  if (tid == 0) {
-    pl.hdr[kItems] = n_items;
-    pl.hdr[kSlots] = all.z + oall.z;
+  } else if (tid == 9 * 32) {
+    pl.hdr[kUnits] = U;
+    pl.hdr[kShare] = S;
+    pl.hdr[kWideCtas] = (int)quot(total + S - 1, S);
   }
   __syncthreads();
+  // (own items, tiles and partial rows come behind the prefixes')
+  const int p_items = s_total[4], p_units = s_total[5], p_slots = s_total[6];
+  const int n_items = p_items + s_total[8];
+  if (tid == 0) {
+    pl.hdr[kItems] = n_items;
+    pl.hdr[kSlots] = p_slots + s_total[10];
+    pl.npre[B] = own_tiles;
+  }
+#pragma unroll 1
+  for (int b = tid; b < B; b += kPlanThreads) pl.npre[b] = s_otile[b];
   // the items, and the CTAs that start in them
+#pragma unroll 1
   for (int i = tid; i < n_items; i += kPlanThreads) {
-    const bool own = i >= all.x;
+    const bool own = i >= p_items;
+    const int at = own ? i - p_items : i;
     const int* first_item = own ? s_oitem : s_item;
-    int lo = 0, hi = B - 1;  // the last request whose first item is at or before i
+    int lo = 0, hi = B - 1;  // the last request whose first item is at or before it
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if (first_item[mid] <= i) lo = mid; else hi = mid - 1;
+      if (first_item[mid] <= at) lo = mid; else hi = mid - 1;
     }
-    const int j = i - first_item[lo];
+    const int j = at - first_item[lo];
     const int rows = own ? sh.R : s_cnt[lo] * sh.R, k = blocks(rows);
     const int f = joined(lo), begin = own && f >= 0 ? s_pre[f] : 0;
     const int end = own ? s_len[lo] : s_pre[lo];
-    const int cut = j / k, blk = j % k, left = tiles(end - begin) - cut * S, nt = min(S, left);
+    const int cut = (int)((unsigned)j / (unsigned)k), blk = j - cut * k;
+    const int left = tiles(end - begin) - cut * S, nt = min(S, left);
     Item it;
     it.row0 = (own ? 0 : s_at[lo] * sh.R) + blk * kItemRows;
     it.nrows = min(kItemRows, rows - blk * kItemRows);
@@ -461,11 +452,12 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     it.own = own ? s_len[lo] : 0;
     it.t0 = begin + cut * S * kTile;
     it.t1 = left > S ? it.t0 + S * kTile : end;
-    it.unit0 = (own ? s_ounit[lo] : s_unit[lo]) + cut * S * k + blk * nt;
-    it.slot0 = (own ? s_oslot[lo] : s_slot[lo]) + cut * rows + blk * kItemRows;
+    it.unit0 = (own ? p_units + s_ounit[lo] : s_unit[lo]) + cut * S * k + blk * nt;
+    it.slot0 = (own ? p_slots + s_oslot[lo] : s_slot[lo]) + cut * rows + blk * kItemRows;
     pl.items[i] = it;
+#pragma unroll 1
     for (int h = 0; h < sh.Hkv; ++h) {
-      const int64_t u0 = (int64_t)h * U + it.unit0, c = (u0 + S - 1) / S;
+      const int64_t u0 = (int64_t)h * U + it.unit0, c = quot(u0 + S - 1, S);
       if (c * S < u0 + nt) {
         Start st = {};
         st.it = it;
@@ -480,6 +472,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   // members in group order, ascending within a group: one warp, 32 requests at
   // a time; and what the merge needs of each request
   if (tid < 32) {
+#pragma unroll 1
     for (int b0 = 0; b0 < B; b0 += 32) {
       const int b = b0 + tid;
       const int f = b < B ? joined(b) : -1;
@@ -497,6 +490,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   }
   __syncthreads();
   // (s_at now ends each group: its first member stands s_cnt places before)
+#pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads) {
     const int f = joined(b);
     Request q = {};
@@ -507,8 +501,8 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
       q.gtiles = tiles(s_pre[f]);
       q.row = (s_lead[b] - (s_at[f] - s_cnt[f])) * sh.R;
     }
-    q.ounit = s_ounit[b];
-    q.oslot = s_oslot[b];
+    q.ounit = p_units + s_ounit[b];
+    q.oslot = p_slots + s_oslot[b];
     q.own = s_len[b] - (f >= 0 ? s_pre[f] : 0);
     pl.req[b] = q;
   }
@@ -1622,8 +1616,8 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
     const int cut = j >> 1, len = min(S, nt - cut * S), k = (rows + kItemRows - 1) / kItemRows;
     const int blk = x / kItemRows;
     const int64_t u0 = (int64_t)head * U + unit + (int64_t)cut * S * k + blk * len;
-    const int64_t c0 = u0 / S, c = c0 + (j & 1);
-    if (c > (u0 + len - 1) / S) return -1;
+    const int64_t c0 = quot(u0, S), c = c0 + (j & 1);
+    if (u0 + len <= c * S) return -1;  // (the item ends before CTA c begins)
     return (int64_t)head * slots_head + slot + (int64_t)cut * rows + x + kItemRows * c;
   };
   const int n0 = 2 * ((rq.gtiles + S - 1) / S);
@@ -1929,8 +1923,9 @@ cudaError_t launch_prefix_plan(const pks_prefix_args& a, const PrefixLayout& L, 
   cudaError_t e = allow_smem(k_prefix_plan, kPlanArrays * sizeof(int32_t) * kMaxB, done);
   if (e != cudaSuccess) return e;
   const PrefixShape sh = prefix_shape(a);
-  const int warps = kPlanThreads / 32, blocks = (a.B + warps - 1) / warps;
-  const int grid = !a.prefix_group || a.B <= kPlanOneBlock ? 1 : blocks;
+  const int at_once = kPlanThreads / 32 / kPlanWarps, most = 2 * sh.wide_grid;
+  const int blocks = (a.B + at_once - 1) / at_once;
+  const int grid = !a.prefix_group || a.B <= kPlanOneBlock ? 1 : blocks < most ? blocks : most;
   return launch_ex(k_prefix_plan, dim3(grid), dim3(kPlanThreads),
                    kPlanArrays * sizeof(int32_t) * (size_t)a.B, s, /*pdl=*/true, /*coop=*/false, a.seq_lens,
                    a.block_table, a.prefix_group, plan_ptrs(a.workspace, L), sh);
