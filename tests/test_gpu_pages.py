@@ -225,6 +225,28 @@ def test_large_table_many_rows():
     t.compact()  # nothing left to move
 
 
+def test_needs_past_32_bits_are_refused():
+    """2100 rows that ask for 2^20 pages each: 2.2e9 pages, more than an int holds."""
+    rows, width = 2100, 1 << 20
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    table = torch.empty((rows, width), dtype=torch.int32, device="cuda")
+    pg = PageTable(lens, table, 1000, 1)
+    pg.extend(torch.full((rows,), width, dtype=torch.int32, device="cuda"))
+    assert pg.device_error() == 6
+    assert int(pg.granted) == 0 and int(pg.n_free) == 1000 and not lens.any()
+    assert not pg.refs.any()
+    pg.extend(dev(np.arange(rows) < 1000))
+    assert pg.device_error() == 0 and int(pg.n_free) == 0
+
+
+def test_tensors_elsewhere_are_refused():
+    lens, table = torch.zeros(2, dtype=torch.int32), torch.zeros((2, 3), dtype=torch.int32)
+    with pytest.raises(ValueError):
+        PageTable(lens, table.cuda(), 4, 2)
+    with pytest.raises(ValueError):
+        PageTable(lens.cuda(), table.cuda(), 4, 2, pools=[torch.zeros(4, 2, 8)])
+
+
 def test_empty_calls_and_full_pool():
     t = start(np.random.default_rng(3), 4, 16, 64, 8, 1.0)
     t.fork([], [])

@@ -208,6 +208,51 @@ def test_many_requests():
         rows=[0, 1, 5, 63, 64, 2000, 4000, 4095])
 
 
+def test_offsets_past_32_bits():
+    """Pools of 4.6 GB each, the requests' pages at their far end: element offsets
+    beyond 2^31 on every path (whole boxes, odd starts, drafts)."""
+    P, Hkv, D, N = 16, 8, 128, 140_000
+    k = torch.empty((N, P, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty((N, P, Hkv, D), dtype=torch.bfloat16, device="cuda")
+    for Nq, lens in ((1, [700, 650, 90]), (5, [700, 650, 90])):
+        b = Batch(lens, [0, 0, -1], [512, 512, 0], page=P, Hkv=Hkv, G=4, D=D, Nq=Nq, seed=20 + Nq)
+        n = b.k.shape[0]
+        k[N - n:], v[N - n:] = b.k, b.v
+        b.k, b.v = k, v
+        b.table = torch.where(b.table >= 0, b.table + (N - n), b.table)
+        b.run(causal=True)
+
+
+def test_batches_without_tokens():
+    for lens, group in (([0, 0, 0], [0, 0, -1]), ([0], [-1])):
+        for Nq in (1, 7):
+            b = Batch(lens, group, [0] * len(lens), Hkv=2, G=8, D=128, Nq=Nq, seed=23)
+            b.run(causal=True)
+    q = torch.empty((0, 8, 64), dtype=torch.bfloat16, device="cuda")
+    pool = torch.empty((1, 16, 2, 64), dtype=torch.bfloat16, device="cuda")
+    att = PrefixAttention(dev(np.zeros(0)), dev(np.zeros((0, 1))), q, pool, pool)
+    assert att().shape == (0, 8, 64)
+    torch.cuda.synchronize()
+    with pytest.raises(ValueError):
+        PrefixAttention(torch.zeros(1, dtype=torch.int32), dev([[0]]),
+                        torch.empty((1, 8, 64), dtype=torch.bfloat16, device="cuda"), pool, pool)
+
+
+def test_results_do_not_depend_on_who_computes_them():
+    """Both kernels side by side with pieces claimed by whichever CTA is free: every
+    run gives the same bits."""
+    rng = np.random.default_rng(24)
+    lens = (4000 + rng.integers(1, 900, 32)).tolist()
+    b = Batch(lens, (np.arange(32) // 8).tolist(), [4000] * 32, page=16, Hkv=8, G=4, D=128, Nq=4,
+              seed=24)
+    att = b.run(causal=True, rows=[0, 9, 31])
+    want = att.out.clone(), att.lse.clone()
+    for _ in range(30):
+        att.out.fill_(float("nan"))
+        att.attend()
+        assert torch.equal(att.out, want[0]) and torch.equal(att.lse, want[1])
+
+
 def test_infinite_values_in_rows_of_others():
     """A request's own infinities and NaN stay its own, also beside a prefix."""
     b = Batch([600, 610, 620], [0] * 3, [512] * 3, page=16, D=128, Hkv=1, G=8, seed=13)

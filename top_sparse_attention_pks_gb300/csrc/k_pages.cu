@@ -263,6 +263,7 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   __shared__ int s_start[kMaxRows + 1];  // first taken page of each row
   __shared__ int s_had[kMaxRows];        // the row's pages before
   __shared__ int s_taken[kTakenShared];  // the first taken pages (the rest: st.taken)
+  __shared__ unsigned long long s_need;
   const int tid = threadIdx.x;
   const int max_len = max_pages * page_size;
   pdl_launch_dependents();  // the copies' blocks may come in and wait
@@ -272,6 +273,7 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   // the bitmap's first words, on their way while the rows are looked at
   uint4 first_words = make_uint4(0, 0, 0, 0);
   if (tid * 4 < words) first_words = *reinterpret_cast<const uint4*>(st.free_map + tid * 4);
+  if (tid == 0) s_need = 0;
   int len[kPer], inc[kPer], tail[kPer], holders[kPer];
   bool bad_len = false, bad_page = false;
 #pragma unroll
@@ -320,19 +322,26 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
       need[u] = pages_of(len[u] + inc[u], page_size) - pages_of(len[u], page_size) + copy[u];
     }
   }
+  // the rows' needs may sum up past 32 bits before they are refused
+  long long mine = 0;
+#pragma unroll
+  for (int u = 0; u < kPer; ++u) mine += need[u];
+  if (mine) atomicAdd(&s_need, (unsigned long long)mine);
+  __syncthreads();
+  const bool enough = s_need <= (unsigned long long)n_free;
   // prefix sums of needs and copies over the rows, 1024 rows at a time
   int at[kPer], c_at[kPer], total = 0, copies = 0;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     at[u] = c_at[u] = 0;
-    if (u * kPlanThreads >= B) continue;  // (the whole block)
+    if (u * kPlanThreads >= B || !enough) continue;  // (the whole block)
     int t0, t1;
     at[u] = total + block_scan<kPlanThreads>(need[u], s_warp, t0) - need[u];
     c_at[u] = copies + block_scan<kPlanThreads>(copy[u], s_warp, t1) - copy[u];
     total += t0;
     copies += t1;
   }
-  const bool granted = !any_len && !any_page && total <= n_free;
+  const bool granted = !any_len && !any_page && enough;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {  // (all threads have read the counts)
     if (tail[u] >= 0) st.cnt[tail[u]] = st.last[tail[u]] = 0;

@@ -266,6 +266,7 @@ class PrefixAttention:
     def __init__(self, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
                  causal: bool = False, sm_scale: float = 0.0, lse: bool = False,
                  wait_limit: int = 0):
+        pks._on_current_device(seq_lens, block_table, q, kv_k, kv_v, prefix_group)
         dev = q.device
         self.out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
@@ -314,6 +315,7 @@ class PageTable:
 
     def __init__(self, seq_lens, block_table, num_pages: int, page_size: int, pools=(),
                  state=None, stream=None):
+        pks._on_current_device(seq_lens, block_table, state, *pools)
         dev = block_table.device
         nbytes = pks.pks_pages_state_bytes(num_pages)
         if state is None:

@@ -245,6 +245,14 @@ def _dptr(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
     return t.data_ptr()
 
 
+def _on_current_device(*tensors) -> None:
+    """The library launches on the current device: its tensors have to be there."""
+    here = torch.device("cuda", torch.cuda.current_device())
+    for t in tensors:
+        if t is not None and t.device != here:
+            raise ValueError(f"tensor on {t.device}, but the current device is {here}")
+
+
 def _host_i32(x) -> np.ndarray:
     if isinstance(x, torch.Tensor):
         x = x.detach().cpu().numpy()
