@@ -136,13 +136,17 @@ constexpr int kPairNs = 1950, kSingleNs = 2000, kStreamNsPerKb = 24;
 struct Pieces {
   int64_t T, big_tiles;
   int big, n, small, share;
-  __device__ __forceinline__ Pieces(const int32_t* hdr, int ngroups)
-      : T((int64_t)__ldcg(hdr + kTiles) * ngroups),
-        big_tiles(__ldcg(reinterpret_cast<const long long*>(hdr + kBigTiles))),
-        big(__ldcg(hdr + kBig)),
-        n(__ldcg(hdr + kPieces)),
-        small(__ldcg(hdr + kSmall)),
-        share(__ldcg(hdr + kDealtTiles)) {}
+  __device__ __forceinline__ Pieces(const int32_t* hdr, int ngroups) {
+    const int4 a = __ldcg(reinterpret_cast<const int4*>(hdr + kTiles - 1));
+    const int4 b = __ldcg(reinterpret_cast<const int4*>(hdr + kBig));
+    const int4 c = __ldcg(reinterpret_cast<const int4*>(hdr + kBigTiles));
+    T = (int64_t)a.y * ngroups;
+    big = b.x;
+    n = b.y;
+    small = b.z;
+    big_tiles = (int64_t)(uint32_t)c.x | (int64_t)c.y << 32;
+    share = c.z;
+  }
   __device__ __forceinline__ int64_t lo(int p) const {
     if (p < big) return (int64_t)p * share;
     const int64_t x = big_tiles + (int64_t)(p - big) * small;
@@ -1295,9 +1299,11 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     s_abort = 0;
   }
   // after the wide kernel the plan is complete (its CTAs waited for it before
-  // they let this grid start), and this grid only waits for it at its end; what
-  // it reads before comes from L2, where the kernels before the wide one left it
+  // they let this grid start), and this grid only waits for it at its end: the
+  // fence drops what the SM's L1 may hold from before (what is read ahead of it
+  // comes from L2, where the kernels before the wide one left it)
   if (wait_first) pdl_wait();
+  else if (warp == HG * WPH) __threadfence();  // (for all, by the barrier below)
   pdl_launch_dependents();
   const Pieces pieces(pl.hdr, ngroups);
   const int Treq = __ldcg(pl.hdr + kTiles);
@@ -1321,8 +1327,8 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     bool opened = false;
     auto request = [&]() {
       seg_end = (int64_t)cg * Treq + s_pre[cb + 1];
-      cstart = __ldcg(pl.start + cb);
-      clen = __ldcg(pl.lens + cb) - cstart;
+      cstart = pl.start[cb];
+      clen = pl.lens[cb] - cstart;
     };
     auto claim = [&]() {  // (used a piece later, so that its latency is hidden)
       if (lane == 0) claimed = pieces.big + atomicAdd(pl.hdr + kClaim, 1);
@@ -1375,7 +1381,7 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
       const int n = clen - t.p0;
       if (lane < n && lane < TILE) {
         const int tok = cstart + t.p0 + lane;
-        page = __ldcg(block_table + (int64_t)cb * sh.max_pages + tok / sh.page_size);
+        page = block_table[(int64_t)cb * sh.max_pages + tok / sh.page_size];
         in_page = tok % sh.page_size;
       }
       ++f;
@@ -1489,8 +1495,8 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
             t4 * 2;
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          qb[ks][0] = j < sh.R ? __ldcg(reinterpret_cast<const uint32_t*>(src + ks * 16)) : 0u;
-          qb[ks][1] = j < sh.R ? __ldcg(reinterpret_cast<const uint32_t*>(src + ks * 16 + 8)) : 0u;
+          qb[ks][0] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16) : 0u;
+          qb[ks][1] = j < sh.R ? *reinterpret_cast<const uint32_t*>(src + ks * 16 + 8) : 0u;
         }
 #pragma unroll
         for (int i = 0; i < MT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
