@@ -34,8 +34,10 @@ constexpr int kMaxRows = 4096;
 constexpr int kTakenShared = 1024;  // taken pages that extend keeps in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;  // units a thread has in flight
-// blocks an SM of the moving kernels (of compact, 367 MB moved: 134 us with 4,
-// 128 with 8, 123 with 16)
+// blocks an SM of the moving kernels: more in flight for whole pages (compact, 367
+// MB moved: 134 us with 4 a SM, 128 with 8, 123 with 16), fewer to launch for the
+// tails (256 rows that copy 34 MB: 24 us with 4, 34 with 16)
+constexpr int kTailBlocks = 4;
 constexpr int kMoveBlocks = 16;
 
 struct PageState {
@@ -652,7 +654,7 @@ cudaError_t launch_pages_extend(const pks_pages_args& a, const PagesLayout& L, c
   if (e != cudaSuccess || a.n_pools == 0) return e;
   const int w = move_width(a);
   const int64_t jobs = move_jobs_per_pool(a, w);
-  const dim3 grid(device_sm_count() * kMoveBlocks);
+  const dim3 grid(device_sm_count() * kTailBlocks);
   const MovePools pools = move_pools(a);
   auto kern = w == 16 ? k_pages_copy_tails<int4>
                       : w == 4 ? k_pages_copy_tails<int32_t> : k_pages_copy_tails<uint8_t>;

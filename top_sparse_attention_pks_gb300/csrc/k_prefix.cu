@@ -536,8 +536,15 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 // what lies beyond the range with zeros.  All CTAs take the same number of tiles
 // and a prefix is cut into items of just as many, row blocks within a cut next to
 // each other: CTAs that read the same tiles for different rows then do so in
-// step, from L2.  The running maximum moves only when a
-// tile exceeds it by more than 8 (log2 units).
+// step, from L2 (1024 rows on 131,072 tokens: 0.64 GB read from memory instead of
+// 2.15).  The running maximum moves only when a tile exceeds it by more than 8
+// (log2 units).
+//
+// Measured on that product (K/V of 8 heads, 550 GFLOP): 1.3 PFLOP/s on the SMs it
+// has, the tensor pipe 67% active.  Softmax arithmetic is not what bounds it
+// (without the exponentials it takes as long); the pipe takes about 76 cycles for
+// a product of 64 when one issuer feeds it and idles where the turns change.  With
+// a single row block and 64 KB a tile it is bound by memory.
 
 constexpr int kWideThreads = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadThreads = 128;
@@ -611,14 +618,15 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   using W = Wide<D>;
   extern __shared__ uint8_t smem_raw[];
   // bar_tma / bar_cp: a ring slot has landed, by either way of loading; bar_go: it
-  // may be filled by the second; bar_free:
-  // its products are done (both issuers'); bar_q / bar_qfree: the same for Q;
+  // may be filled by the second; bar_free: its products are done (both issuers');
+  // bar_q / bar_qfree: Q is there / its last product is done;
   // bar_s[g]: S of group g's job; bar_p[g][h]: half h of its P is written;
   // bar_turn[g]: the other issuer has issued its job's P.V and next S; bar_o[g]:
   // every product of the group's piece; bar_x[g] / bar_y[g]: the group's maxima
   // are posted / it has read the other's O; bar_drain[g]: on giving up
   __shared__ __align__(8) uint64_t bar_tma[W::kSlotsN], bar_cp[W::kSlotsN], bar_go[W::kSlotsN],
-      bar_free[W::kSlotsN],      bar_q, bar_qfree, bar_s[2], bar_p[2][2], bar_turn[2], bar_o[2], bar_x[2], bar_y[2], bar_drain[2];
+      bar_free[W::kSlotsN], bar_q, bar_qfree, bar_s[2], bar_p[2][2], bar_turn[2], bar_o[2],
+      bar_x[2], bar_y[2], bar_drain[2];
   __shared__ float2 s_ml[kRows];  // a row's maximum and sum, group 1's and then group 0's
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_sizes[2];
@@ -697,28 +705,21 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     const uint32_t tS = tmem + lane_off + kTmemS + g * kTile, tO = tmem + lane_off + g * 128;
     const uint64_t scale2 = tc::pack2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
     uint32_t n_job = 0, n_piece = 0, n_split = 0;
-    // (the first round is a job on whatever the tensor memory holds: it brings
-    // the code into the instruction cache while the first tiles are on their way,
-    // 2 us that the first job took longer otherwise)
-    for (bool dry = walk.more(); (dry || walk.more()) && ok; dry = false) {
-      Piece pc = {};
-      pc.jobs0 = pc.jobs1 = 1;
-      if (!dry) pc = walk.next();
+    while (walk.more() && ok) {
+      const Piece pc = walk.next();
       const int x = (pc.pair ? g * kRows : 0) + (tid & (kRows - 1));  // row of the item
       const int64_t row = pc.slot + x;
       const bool mine = x < pc.it.nrows;
       const int my_jobs = g ? pc.jobs1 : pc.jobs0;
-      const bool idle = !dry && !__any_sync(0xffffffffu, mine);  // no row of this warp counts
+      const bool idle = !__any_sync(0xffffffffu, mine);  // no row of this warp counts
       // tokens this row sees
       int limit = pc.it.t1;
       if (pc.it.own && sh.causal && mine) limit = pc.it.own - sh.Nq + (pc.it.row0 + x) / sh.G + 1;
       limit -= pc.it.t0 + pc.t_lo * kTile;
       float m_run = kNegInf, l_run = 0.f;
       for (int i = 0; i < my_jobs; ++i) {
-        if (!dry) {
-          if (!(ok = wait(&bar_s[g], n_job & 1))) break;
-          ++n_job;
-        }
+        if (!(ok = wait(&bar_s[g], n_job & 1))) break;
+        ++n_job;
         tc::fence_after();
         if (!idle) {
           const int nv = limit - (pc.pair ? i : 2 * i + g) * kTile;  // valid columns
@@ -791,17 +792,17 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           // P takes the place of S columns, all of which are in registers
           uint32_t pk[16];
           weights(s0, pk);
-          if (!dry) tc::tmem_st16(tS, pk);  // (the first S may be there already)
+          tc::tmem_st16(tS, pk);
           weights(s1, pk);
-          if (!dry) tc::tmem_st16(tS + 16, pk);
+          tc::tmem_st16(tS + 16, pk);
           tc::tmem_st_wait();
           tc::fence_before();
           __syncwarp();
-          if (lane == 0 && !dry) tc::mbar_arrive(&bar_p[g][0]);
+          if (lane == 0) tc::mbar_arrive(&bar_p[g][0]);
           weights(s2, pk);
-          if (!dry) tc::tmem_st16(tS + 32, pk);
+          tc::tmem_st16(tS + 32, pk);
           weights(s3, pk);
-          if (!dry) tc::tmem_st16(tS + 48, pk);
+          tc::tmem_st16(tS + 48, pk);
           float la, lb, lc, ld;
           tc::unpack2(sum_a, la, lb);
           tc::unpack2(sum_b, lc, ld);
@@ -813,9 +814,8 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         }
         tc::fence_before();
         __syncwarp();
-        if (lane == 0 && !dry) tc::mbar_arrive(&bar_p[g][1]);
+        if (lane == 0) tc::mbar_arrive(&bar_p[g][1]);
       }
-      if (dry) continue;
       // ---- the piece's partial
       if (!ok) break;
       if (my_jobs == 0) continue;  // (one tile: it was the other group's)
@@ -1475,19 +1475,11 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     uint32_t qb[KS][2];
     float o[MT][4], m_h[2] = {kNegInf, kNegInf}, l_h[2] = {0.f, 0.f};
     int lim[2] = {0, 0};  // own tokens that the thread's two rows see
-    // (the first round is on a tile of no tokens: it brings the loop's code into
-    // the instruction cache while the first copies are on their way, 2 us that
-    // the first tile took longer otherwise)
-    for (uint32_t k = ~0u;; ++k) {
-      const bool dry = k == ~0u;
-      const uint32_t s = dry ? 0 : k % N::kStages;
-      Tile t = {};
-      t.flags = kFirst;
-      if (!dry) {
-        if (!(ok = wait(&bar_full[s], (k / N::kStages) & 1))) break;
-        t = s_tile[k % kTileRing];
-        if (t.flags & kEnd) break;
-      }
+    for (uint32_t k = 0;; ++k) {
+      const uint32_t s = k % N::kStages;
+      if (!(ok = wait(&bar_full[s], (k / N::kStages) & 1))) break;
+      const Tile t = s_tile[k % kTileRing];
+      if (t.flags & kEnd) break;
       if (t.flags & kFirst) {
         const int head = t.g * HG + hh, j = c0 + g8;
         const __nv_bfloat16* src =
@@ -1562,7 +1554,7 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
         mma_16816(o[mt], a, pb0, pb1);
       }
       __syncwarp();
-      if (lane == 0 && !dry) tc::mbar_arrive(&bar_empty[s]);
+      if (lane == 0) tc::mbar_arrive(&bar_empty[s]);
       if (t.flags & kLast) {
         const int64_t at = (((int64_t)t.piece + (int64_t)t.g * B + t.b) * HG + hh) * sh.R;
 #pragma unroll
