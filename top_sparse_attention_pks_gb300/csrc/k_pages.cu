@@ -34,10 +34,8 @@ constexpr int kMaxRows = 4096;
 constexpr int kTakenShared = 1024;  // taken pages that extend keeps in shared memory
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnroll = 4;  // units a thread has in flight
-// blocks an SM of the moving kernels: more in flight for whole pages (compact, 367
-// MB moved: 134 us with 4 a SM, 128 with 8, 123 with 16), fewer to launch for the
-// tails (256 rows that copy 34 MB: 24 us with 4, 34 with 16)
-constexpr int kTailBlocks = 4;
+// blocks an SM of the moving kernels (compact, 367 MB moved: 134 us with 4, 128 with
+// 8, 123 with 16; tails take the same from 4 on)
 constexpr int kMoveBlocks = 16;
 
 struct PageState {
@@ -265,7 +263,7 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   __shared__ int s_start[kMaxRows + 1];  // first taken page of each row
   __shared__ int s_had[kMaxRows];        // the row's pages before
   __shared__ int s_taken[kTakenShared];  // the first taken pages (the rest: st.taken)
-  __shared__ unsigned long long s_need;
+  __shared__ unsigned s_need[kPlanThreads / 32];
   const int tid = threadIdx.x;
   const int max_len = max_pages * page_size;
   pdl_launch_dependents();  // the copies' blocks may come in and wait
@@ -275,7 +273,6 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   // the bitmap's first words, on their way while the rows are looked at
   uint4 first_words = make_uint4(0, 0, 0, 0);
   if (tid * 4 < words) first_words = *reinterpret_cast<const uint4*>(st.free_map + tid * 4);
-  if (tid == 0) s_need = 0;
   int len[kPer], inc[kPer], tail[kPer], holders[kPer];
   bool bad_len = false, bad_page = false;
 #pragma unroll
@@ -324,13 +321,18 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
       need[u] = pages_of(len[u] + inc[u], page_size) - pages_of(len[u], page_size) + copy[u];
     }
   }
-  // the rows' needs may sum up past 32 bits before they are refused
-  long long mine = 0;
+  // the rows' needs may sum up past 32 bits before they are refused (a warp's do
+  // not: 128 rows of up to 2^24 pages)
+  unsigned mine = 0;
 #pragma unroll
   for (int u = 0; u < kPer; ++u) mine += need[u];
-  if (mine) atomicAdd(&s_need, (unsigned long long)mine);
+  mine = __reduce_add_sync(0xffffffffu, mine);
+  if ((tid & 31) == 0) s_need[tid >> 5] = mine;
   __syncthreads();
-  const bool enough = s_need <= (unsigned long long)n_free;
+  unsigned long long all = s_need[tid & 31];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
+  const bool enough = all <= (unsigned long long)n_free;
   // prefix sums of needs and copies over the rows, 1024 rows at a time
   int at[kPer], c_at[kPer], total = 0, copies = 0;
 #pragma unroll
@@ -654,7 +656,7 @@ cudaError_t launch_pages_extend(const pks_pages_args& a, const PagesLayout& L, c
   if (e != cudaSuccess || a.n_pools == 0) return e;
   const int w = move_width(a);
   const int64_t jobs = move_jobs_per_pool(a, w);
-  const dim3 grid(device_sm_count() * kTailBlocks);
+  const dim3 grid(device_sm_count() * kMoveBlocks);
   const MovePools pools = move_pools(a);
   auto kern = w == 16 ? k_pages_copy_tails<int4>
                       : w == 4 ? k_pages_copy_tails<int32_t> : k_pages_copy_tails<uint8_t>;
