@@ -1585,24 +1585,33 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
 }
 
 // ----------------------------------------------------------------- merge ---
-// A warp a (request, query token, head).  The parts: the group's prefix items
+// LPR lanes a (request, query token, head).  The parts: the group's prefix items
 // and the request's own (each cut of a token range lies in the ranges of one or
-// two CTAs), or the narrow CTAs that its own tokens are spread over.
-template <int D>
+// two CTAs), or the narrow CTAs that its own tokens are spread over.  A few loads
+// that wait for one another and little else, so few rows take a warp each, which
+// has all parts in flight at once, and many take eight lanes, where finding the
+// parts is shared by four rows.  Measured (a whole pass, us, by a warp / by eight
+// lanes): 88,320 rows of one or two parts 98 / 57, 15,360 34.9 / 26.7, 7,680
+// 31.0 / 26.7; of about ten parts 16,384 rows 224 / 221, 6,144 equal, 4,096
+// 86 / 89, 512 35 / 39.
+constexpr int kManyRowsPerSm = 40;
+template <int D, int LPR>
 __global__ void __launch_bounds__(128)
 k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restrict__ wo,
                const float2* __restrict__ nml, const float* __restrict__ no,
                __nv_bfloat16* __restrict__ out, float* __restrict__ lse, PrefixShape sh) {
-  constexpr int V = D / 32;  // output values a lane
-  constexpr int kBatch = 8;  // partial rows in flight
+  constexpr int V = D / LPR;               // output values a lane
+  constexpr int C = V < 4 ? V : 4;         // of them next to each other
+  constexpr int kBatch = V > 8 ? 4 : 8;  // partial rows in flight
   const float kNegInf = __int_as_float(0xff800000);
-  const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & (LPR - 1), first = threadIdx.x & 31 & ~(LPR - 1);
+  const int64_t row = ((int64_t)blockIdx.x * 128 + threadIdx.x) / LPR;
   pdl_launch_dependents();
-  const int h = row % sh.Hq, bq = row / sh.Hq, b = bq / sh.Nq, qi = bq % sh.Nq;
+  const int64_t rows = (int64_t)sh.B * sh.Nq * sh.Hq;
+  const int at_row = (int)min(row, rows - 1);  // (a warp's lanes stay together)
+  const int h = at_row % sh.Hq, bq = at_row / sh.Hq, b = bq / sh.Nq, qi = bq % sh.Nq;
   const int head = h / sh.G, r = qi * sh.G + h % sh.G;  // row of the request for this KV head
   pdl_wait();
-  if (b >= sh.B) return;
   const Request rq = pl.req[b];
   const int pre = pl.npre[b];
   const int U = pl.hdr[kUnits], S = pl.hdr[kShare], slots_head = pl.hdr[kSlots];
@@ -1640,12 +1649,13 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   };
   const float2* ml1 = sh.narrow ? nml : wml;
   const float* o1 = sh.narrow ? no : wo;
-  // (up to 32 parts at a time; nearly always all of them: the running maximum
+  // (up to LPR parts at a time; nearly always all of them: the running maximum
   // rescales what came before)
   float M = kNegInf, L = 0.f, acc[V];
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
-  for (int j0 = 0; j0 < n; j0 += 32) {
+  const int n_warp = LPR == 32 ? n : __reduce_max_sync(0xffffffffu, n);
+  for (int j0 = 0; j0 < n_warp; j0 += LPR) {
     const int j = j0 + lane;
     const int64_t my = j < n ? at(j) : -1;
     float2 e = make_float2(kNegInf, 0.f);
@@ -1653,13 +1663,13 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
     const float* src = (j < n0 ? wo : o1) + (my >= 0 ? my : 0) * D;
     float m = e.y == 0.f ? kNegInf : e.x;
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    for (int s = LPR / 2; s >= 1; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
     const float m_new = fmaxf(M, m);
     const float keep = L == 0.f ? 0.f : exp2f(M - m_new);
     const float wgt = e.y == 0.f ? 0.f : exp2f(e.x - m_new);
     float l = wgt * e.y;
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+    for (int s = LPR / 2; s >= 1; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
     if (j0 > 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) acc[v] *= keep;
@@ -1668,27 +1678,32 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
     M = m_new;
     // the rows that count, kBatch loads in flight
     uint32_t left = __ballot_sync(0xffffffffu, wgt != 0.f);
-    while (left) {
+    if (LPR < 32) left = (left >> first) & ((1u << (LPR & 31)) - 1);
+    while (LPR == 32 ? left : __any_sync(0xffffffffu, left)) {
       float x[kBatch][V], f[kBatch];
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
         f[u] = 0.f;
         const int k = left ? __ffs(left) - 1 : 0;
-        const float fk = __shfl_sync(0xffffffffu, wgt, k);
+        const float fk = __shfl_sync(0xffffffffu, wgt, k, LPR);
         const float* p = reinterpret_cast<const float*>(
-            __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(src), k));
+            __shfl_sync(0xffffffffu, reinterpret_cast<uintptr_t>(src), k, LPR));
         if (left) {
           f[u] = fk;
-          if (V == 4) {
-            const float4 t = __ldcg(reinterpret_cast<const float4*>(p) + lane);
-            x[u][0] = t.x;
-            x[u][1] = t.y;
-            x[u][V - 2] = t.z;
-            x[u][V - 1] = t.w;
-          } else {
-            const float2 t = __ldcg(reinterpret_cast<const float2*>(p) + lane);
-            x[u][0] = t.x;
-            x[u][1] = t.y;
+#pragma unroll
+          for (int v = 0; v < V; v += C) {
+            const float* at = p + v * LPR + lane * C;
+            if (C == 4) {
+              const float4 t = __ldcg(reinterpret_cast<const float4*>(at));
+              x[u][v] = t.x;
+              x[u][v + 1] = t.y;
+              x[u][v + C - 2] = t.z;
+              x[u][v + C - 1] = t.w;
+            } else {
+              const float2 t = __ldcg(reinterpret_cast<const float2*>(at));
+              x[u][v] = t.x;
+              x[u][v + 1] = t.y;
+            }
           }
           left &= left - 1;
         } else {
@@ -1703,11 +1718,18 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  __nv_bfloat16* dst = out + (int64_t)row * D + lane * V;
+  if (row >= rows) return;
+  __nv_bfloat16* dst = out + row * D + lane * C;
 #pragma unroll
-  for (int v = 0; v < V; v += 2)
-    *reinterpret_cast<__nv_bfloat162*>(dst + v) =
-        __floats2bfloat162_rn(acc[v] * inv, acc[v + 1] * inv);
+  for (int v = 0; v < V; v += C) {
+    uint32_t w[C / 2];
+#pragma unroll
+    for (int e = 0; e < C; e += 2) w[e / 2] = pack_bf16(acc[v + e] * inv, acc[v + e + 1] * inv);
+    if (C == 4)
+      *reinterpret_cast<uint2*>(dst + v * LPR) = make_uint2(w[0], w[C / 2 - 1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst + v * LPR) = w[0];
+  }
   if (lse && lane == 0)
     lse[row] = L == 0.f ? kNegInf : (M + log2f(L)) * 0.6931471805599453f;
 }
@@ -1864,7 +1886,10 @@ cudaError_t launch_parts(const pks_prefix_args& a, const PrefixLayout& L, const 
   }
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int64_t rows = (int64_t)sh.B * sh.Nq * sh.Hq;
-  return launch_ex(k_prefix_merge<D>, dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, s,
+  const bool many = rows >= (int64_t)kManyRowsPerSm * sh.wide_grid;
+  const int per_block = many ? 16 : 4;
+  return launch_ex(many ? k_prefix_merge<D, 8> : k_prefix_merge<D, 32>,
+                   dim3((unsigned)((rows + per_block - 1) / per_block)), dim3(128), 0, s,
                    /*pdl=*/true, /*coop=*/false, plan_ptrs(ws, L),
                    reinterpret_cast<const float2*>(ws + L.wide_ml),
                    reinterpret_cast<const float*>(ws + L.wide_o),
