@@ -117,7 +117,10 @@ __device__ __forceinline__ void flag_error(int32_t* err, int code) { atomicCAS(e
 
 constexpr int kWideLeast = 2;                  // tiles a wide CTA takes at least
 constexpr int kNarrowLeast = 2;                // tiles a narrow CTA takes at least
-constexpr int kSmallLeast = 12;                // tiles of a small narrow piece at least
+// Tiles of a small narrow piece at least, when there are as many for every CTA
+// (2,000 tiles on 152 CTAs: 83.4 us a pass, with pieces of their share of the rest
+// 85.6; 100 tiles in pieces of 12 39 us, of 2 29 us).
+constexpr int kSmallLeast = 12;
 constexpr int kSmallPerSm = 8;                 // small pieces an SM at most
 // Beside the wide kernel, a narrow CTA is dealt this share (in 1/16) of what it
 // could stream in the time estimated for all; the rest goes to whichever SM is
@@ -408,7 +411,9 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     big = quot(big_tiles + share - 1, share);
     big_tiles = min(T, big * share);
     const int64_t rest = T - big_tiles, most = (int64_t)kSmallPerSm * sh.wide_grid;
-    const int64_t small = max((int64_t)kSmallLeast, quot(rest + most - 1, most));
+    const int64_t even = quot(T + sh.narrow_grid - 1, sh.narrow_grid);
+    const int64_t least = min((int64_t)kSmallLeast, max((int64_t)kNarrowLeast, even));
+    const int64_t small = max(least, quot(rest + most - 1, most));
     pl.hdr[kTiles] = own_tiles;
     pl.hdr[kDealtTiles] = (int)share;
     pl.hdr[kBig] = (int)big;
@@ -1432,16 +1437,24 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
                           v ? &map_v : &map_k, j * 64, pr, t0.g * HG, &bar_full[s]);
         tc::mbar_arrive(&bar_full[s]);
       } else {
-        constexpr int kChunks = D / 8;
-#pragma unroll 4
-        for (int i = lane; i < TILE * HG * kChunks; i += 32) {
-          const int r = i / (HG * kChunks), hh = i / kChunks % HG, c = i % kChunks;
-          const int pr = __shfl_sync(0xffffffffu, row, r);
-          const uint32_t dst = tile + ((c >> 3) * 2 + (r >> 3)) * N::kBoxBytes +
-                               (hh * 8 + (r & 7)) * 128 + (((c & 7) ^ (r & 7)) << 4);
-          const int64_t src = pr >= 0 ? ((int64_t)pr * sh.Hkv + t0.g * HG + hh) * D + c * 8 : 0;
-          tc::cp_async16(dst, kv_k + src, pr >= 0 ? 16 : 0);
-          tc::cp_async16(dst + N::kHalfBytes, kv_v + src, pr >= 0 ? 16 : 0);
+        // a lane's 16-byte chunk c of the rows of every kStep-th head, from h0, of
+        // every kTok-th token, from r0
+        constexpr int kChunks = D / 8, kPer = HG * kChunks;
+        constexpr int kTok = kPer < 32 ? 32 / kPer : 1, kStep = 32 / kChunks;
+        const int c = lane % kChunks, h0 = lane / kChunks % HG, r0 = kPer < 32 ? lane / kPer : 0;
+        const uint32_t dst0 = tile + (c >> 3) * 2 * N::kBoxBytes + h0 * 1024;
+        const int64_t src0 = (t0.g * HG + h0) * D + c * 8, row_step = (int64_t)sh.Hkv * D;
+#pragma unroll 8
+        for (int i = 0; i < TILE; i += kTok) {
+          const int r = i + r0, pr = __shfl_sync(0xffffffffu, row, r);
+          const uint32_t dst = dst0 + (r >> 3) * N::kBoxBytes + (r & 7) * 128 +
+                               (((c & 7) ^ (r & 7)) << 4);
+          const int64_t src = src0 + (pr >= 0 ? pr * row_step : 0);
+#pragma unroll
+          for (int h = 0; h < HG; h += kStep) {
+            tc::cp_async16(dst + h * 1024, kv_k + src + h * D, pr >= 0 ? 16 : 0);
+            tc::cp_async16(dst + h * 1024 + N::kHalfBytes, kv_v + src + h * D, pr >= 0 ? 16 : 0);
+          }
         }
         tc::cp_async_arrive(&bar_full[s]);
         if (lane == 0) tc::mbar_arrive(&bar_full[s]);
@@ -1590,13 +1603,16 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
 // two CTAs), or the narrow CTAs that its own tokens are spread over.  A few loads
 // that wait for one another and little else, so few rows take a warp each, which
 // has all parts in flight at once, and many take eight lanes, where finding the
-// parts is shared by four rows.  Measured (a whole pass, us, by a warp / by eight
+// parts is shared by four rows.  Very few rows, which may have hundreds of parts
+// each, take a block each.  Measured (a whole pass, us, by a warp / by eight
 // lanes): 88,320 rows of one or two parts 98 / 57, 15,360 34.9 / 26.7, 7,680
 // 31.0 / 26.7; of about ten parts 16,384 rows 224 / 221, 6,144 equal, 4,096
-// 86 / 89, 512 35 / 39.
-constexpr int kManyRowsPerSm = 40;
-template <int D, int LPR>
-__global__ void __launch_bounds__(128)
+// 86 / 89, 512 35 / 39; by a warp / by a block of four: 42 rows of up to 400 parts
+// 51 / 33, 256 of 150 41 / 31, 380 to 1,000 of ten or fewer between 8% less and 7%
+// more, 2,560 50 / 55.
+constexpr int kManyRowsPerSm = 40, kFewRowsPerSm = 7, kFewWarps = 4;
+template <int D, int LPR, int WPR>
+__global__ void __launch_bounds__(WPR > 1 ? WPR * 32 : 128)
 k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restrict__ wo,
                const float2* __restrict__ nml, const float* __restrict__ no,
                __nv_bfloat16* __restrict__ out, float* __restrict__ lse, PrefixShape sh) {
@@ -1605,7 +1621,8 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   constexpr int kBatch = V > 8 ? 4 : 8;  // partial rows in flight
   const float kNegInf = __int_as_float(0xff800000);
   const int lane = threadIdx.x & (LPR - 1), first = threadIdx.x & 31 & ~(LPR - 1);
-  const int64_t row = ((int64_t)blockIdx.x * 128 + threadIdx.x) / LPR;
+  const int64_t row = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) / (LPR * WPR);
+  const int warp = WPR > 1 ? threadIdx.x >> 5 : 0;  // of the row
   pdl_launch_dependents();
   const int64_t rows = (int64_t)sh.B * sh.Nq * sh.Hq;
   const int at_row = (int)min(row, rows - 1);  // (a warp's lanes stay together)
@@ -1617,7 +1634,7 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   const int U = pl.hdr[kUnits], S = pl.hdr[kShare], slots_head = pl.hdr[kSlots];
   const int Treq = pl.hdr[kTiles];
   const Pieces pieces(pl.hdr, sh.Hkv / sh.hg);
-  if (row == 0 && lane == 0) pl.hdr[kClaim] = 0;  // for the next call by this plan
+  if (row == 0 && lane == 0 && warp == 0) pl.hdr[kClaim] = 0;  // for the next call by this plan
 
   // candidate j of a run of wide items: CTA j % 2 of cut j / 2 (-1: there is none)
   auto wide_at = [&](int j, int unit, int slot, int rows, int nt, int x) -> int64_t {
@@ -1655,8 +1672,8 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
 #pragma unroll
   for (int v = 0; v < V; ++v) acc[v] = 0.f;
   const int n_warp = LPR == 32 ? n : __reduce_max_sync(0xffffffffu, n);
-  for (int j0 = 0; j0 < n_warp; j0 += LPR) {
-    const int j = j0 + lane;
+  for (int j0 = 0; j0 < n_warp; j0 += LPR * WPR) {
+    const int j = j0 + lane * WPR + warp;
     const int64_t my = j < n ? at(j) : -1;
     float2 e = make_float2(kNegInf, 0.f);
     if (my >= 0) e = __ldcg((j < n0 ? wml : ml1) + my);
@@ -1715,6 +1732,37 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
       for (int u = 0; u < kBatch; ++u)
 #pragma unroll
         for (int v = 0; v < V; ++v) acc[v] += f[u] * x[u][v];
+    }
+  }
+  if (WPR > 1) {  // the warps' sums
+    __shared__ float s_m[WPR], s_l[WPR], s_o[WPR][D];
+#pragma unroll
+    for (int v = 0; v < V; ++v) s_o[warp][(v / C * LPR + lane) * C + v % C] = acc[v];
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = L;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+    const float l = lane < WPR ? s_l[lane & (WPR - 1)] : 0.f;
+    const float m = l == 0.f ? kNegInf : s_m[lane & (WPR - 1)];
+    M = m;
+#pragma unroll
+    for (int s = WPR / 2; s >= 1; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    const float f = l == 0.f ? 0.f : exp2f(m - M);
+    L = f * l;
+#pragma unroll
+    for (int s = WPR / 2; s >= 1; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+    L = __shfl_sync(0xffffffffu, L, 0);
+    M = __shfl_sync(0xffffffffu, M, 0);
+#pragma unroll
+    for (int v = 0; v < V; ++v) acc[v] = 0.f;
+#pragma unroll
+    for (int k = 0; k < WPR; ++k) {
+      const float fk = __shfl_sync(0xffffffffu, f, k);
+      if (fk == 0.f) continue;
+#pragma unroll
+      for (int v = 0; v < V; ++v) acc[v] += fk * s_o[k][(v / C * LPR + lane) * C + v % C];
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
@@ -1887,9 +1935,13 @@ cudaError_t launch_parts(const pks_prefix_args& a, const PrefixLayout& L, const 
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   const int64_t rows = (int64_t)sh.B * sh.Nq * sh.Hq;
   const bool many = rows >= (int64_t)kManyRowsPerSm * sh.wide_grid;
-  const int per_block = many ? 16 : 4;
-  return launch_ex(many ? k_prefix_merge<D, 8> : k_prefix_merge<D, 32>,
-                   dim3((unsigned)((rows + per_block - 1) / per_block)), dim3(128), 0, s,
+  const bool few = rows <= (int64_t)kFewRowsPerSm * sh.wide_grid;
+  const int per_block = many ? 16 : few ? 1 : 4;
+  return launch_ex(many  ? k_prefix_merge<D, 8, 1>
+                   : few ? k_prefix_merge<D, 32, kFewWarps>
+                         : k_prefix_merge<D, 32, 1>,
+                   dim3((unsigned)((rows + per_block - 1) / per_block)),
+                   dim3(few ? 32 * kFewWarps : 128), 0, s,
                    /*pdl=*/true, /*coop=*/false, plan_ptrs(ws, L),
                    reinterpret_cast<const float2*>(ws + L.wide_ml),
                    reinterpret_cast<const float*>(ws + L.wide_o),
