@@ -558,8 +558,8 @@ constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless w
 template <int D>
 struct Wide {
   static constexpr int kBlk = D / 64;                          // 64-value column blocks
-  static constexpr uint32_t kBlkBytes = kTile * 128;
-  static constexpr uint32_t kTileBytes = kBlk * kBlkBytes;     // K, V or Q tile
+  static constexpr uint32_t kGroupBytes = kBlk * 1024;         // eight rows: a block's, then the next's
+  static constexpr uint32_t kTileBytes = kTile / 8 * kGroupBytes;  // K, V or Q tile
   static constexpr int kSlotsN = D == 128 ? 5 : 10;            // ring of K / V tiles
   static constexpr uint32_t kSmem = (2 + kSlotsN) * kTileBytes + 1024;
   // loads in flight beyond the newest; a piece has at least these (K and V of a tile)
@@ -944,11 +944,11 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           tc::fence_after();
           if (tc::elect_one()) {
             const uint32_t sl = (n_slot + 2 * t) % W::kSlotsN;
-            const uint64_t dq = tc::desc_sw128(sQ + (pc.pair ? g : 0) * W::kTileBytes, 16, 1024);
-            const uint64_t dk = tc::desc_sw128(sKV + sl * W::kTileBytes, 16, 1024);
+            const uint64_t dq = tc::desc_sw128(sQ + (pc.pair ? g : 0) * W::kTileBytes, 16, W::kGroupBytes);
+            const uint64_t dk = tc::desc_sw128(sKV + sl * W::kTileBytes, 16, W::kGroupBytes);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)(((kk >> 2) * W::kBlkBytes + (kk & 3) * 32) >> 4);
+              const uint64_t off = (uint64_t)(((kk >> 2) * 1024 + (kk & 3) * 32) >> 4);
               tc::mma_ss(tS, dq + off, dk + off, tc::idesc_bf16(kRows, kTile, false),
                          kk > 0 ? 1u : 0u);
               if (kk == D / 16 - 4 && pass) tc::mbar_arrive(pass);
@@ -981,7 +981,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           const int t = t0 + i * step, job = 2 * i + g;
           if (!(ok = landed(t, 1))) break;
           const uint32_t sl = (n_slot + 2 * t + 1) % W::kSlotsN;
-          const uint64_t dv = tc::desc_sw128(sKV + sl * W::kTileBytes, W::kBlkBytes, 1024);
+          const uint64_t dv = tc::desc_sw128(sKV + sl * W::kTileBytes, 1024, W::kGroupBytes);
           // K of the next tile, if it is there: S then follows P.V without a wait
           const bool more = i + 1 < my_jobs;
           const int tn = t + step;
@@ -1001,7 +1001,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
             if (tc::elect_one()) {
 #pragma unroll
               for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
-                tc::mma_ts(tO, tS + kk * 8, dv + (uint64_t)((kk * 16 * 128) >> 4),
+                tc::mma_ts(tO, tS + kk * 8, dv + (uint64_t)((kk * 2 * W::kGroupBytes) >> 4),
                            tc::idesc_bf16(kRows, D, true), (i > 0 || kk > 0) ? 1u : 0u);
               if (h == 1) {
                 tc::mma_commit(&bar_free[sl]);
@@ -1050,10 +1050,12 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       constexpr int kChunks = D / 8;          // 16-byte chunks of a row
       constexpr int kRowsPer = 32 / kChunks;  // rows a warp instruction covers
       const int sub = lane / kChunks, cc = lane % kChunks;
-      // warp lw fills rows 32 lw .. 32 lw + 31; chunk c of row r of column
-      // block j goes to chunk c ^ (r & 7)
+      // warp lw fills rows 32 lw .. 32 lw + 31, this lane rows r + sub; chunk c of
+      // row r of a 64-value block goes to chunk c ^ (r & 7)
       auto dst_of = [&](uint32_t tile, int r) {
-        return tile + (cc >> 3) * W::kBlkBytes + r * 128 + (((cc & 7) ^ (r & 7)) << 4);
+        const int r8 = (r & 7) + sub;
+        return tile + (r >> 3) * W::kGroupBytes + (cc >> 3) * 1024 + r8 * 128 +
+               (((cc & 7) ^ r8) << 4);
       };
       auto publish = [&](uint64_t* bar) {
         tc::fence_async_smem();
@@ -1061,9 +1063,8 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         if (lane == 0) tc::mbar_arrive(bar);
       };
       // first row of this lane's box of an item's tile, when it comes by TMA (warp
-      // 0; lane b * kBlk + j copies column block j of box b; a bad page gives
-      // zeros, from beyond the pool)
-      const int n_box = sh.box ? kTile / sh.box : 0, my_box = lane / W::kBlk;
+      // 0, a lane a box; a bad page gives zeros, from beyond the pool)
+      const int n_box = sh.box ? kTile / sh.box : 0, my_box = lane;
       auto box_row = [&](const Item& it, int tile) -> int {
         if (my_box >= n_box || it.t0 % sh.box != 0 || it.t0 + (tile + 1) * kTile > it.t1) return 0;
         const int tok = it.t0 + tile * kTile + my_box * sh.box;
@@ -1115,7 +1116,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
 #pragma unroll 4
             for (int i = 0; i < 32; i += kRowsPer) {
               const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
-              tc::cp_async16(dst_of(sQ + (c >> 2) * W::kTileBytes, (c & 3) * 32 + i + sub),
+              tc::cp_async16(dst_of(sQ + (c >> 2) * W::kTileBytes, (c & 3) * 32 + i),
                              q + (o >= 0 ? o + cc * 8 : 0), o >= 0 ? 16 : 0);
             }
           }
@@ -1153,18 +1154,16 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
                 tma_count ^= 1u << s;
                 if (lane == 0) tc::mbar_arrive_expect(&bar_tma[s], W::kTileBytes);
                 __syncwarp();
-                if (my_box < n_box) {
-                  const int j = lane % W::kBlk;
-                  tc::tma_load_3d(tile + j * W::kBlkBytes + my_box * sh.box * 128,
-                                  v ? &map_v : &map_k, j * 64, row, pc.head, &bar_tma[s]);
-                }
+                if (my_box < n_box)
+                  tc::tma_load_5d(tile + my_box * (sh.box / 8) * W::kGroupBytes,
+                                  v ? &map_v : &map_k, 0, 0, 0, row / 8, pc.head, &bar_tma[s]);
               }
             } else {
               const __nv_bfloat16* pool = (v ? kv_v : kv_k) + pc.head * D + cc * 8;
 #pragma unroll 8
               for (int r = 0; r < 32; r += kRowsPer) {
                 const int pr = __shfl_sync(0xffffffffu, row, r + sub);
-                tc::cp_async16(dst_of(tile, lw * 32 + r + sub),
+                tc::cp_async16(dst_of(tile, lw * 32 + r),
                                pool + (pr >= 0 ? (int64_t)pr * sh.Hkv * D : 0), pr >= 0 ? 16 : 0);
               }
               tc::cp_async_commit();
@@ -1840,10 +1839,8 @@ cudaError_t allow_smem(K kern, size_t bytes, bool (&done)[64]) {
   return e;
 }
 
-// Tensor map of a K or V pool as heads x rows x D, a box being `rows` tokens of
-// `heads` heads and 64 of their values, 128-byte swizzled.
-cudaError_t pool_map(CUtensorMap* map, const void* pool, const pks_prefix_args& a, int rows,
-                     int heads) {
+cudaError_t encode_map(CUtensorMap* map, const void* pool, int rank, const cuuint64_t* dims,
+                       const cuuint64_t* strides, const cuuint32_t* box) {
   static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
   if (!encode) {
     void* fn = nullptr;
@@ -1854,15 +1851,34 @@ cudaError_t pool_map(CUtensorMap* map, const void* pool, const pks_prefix_args& 
     if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
     encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
   }
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+                            const_cast<void*>(pool), dims, strides, box, ones,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Tensor map of a K or V pool as heads x rows x D for the narrow kernel, a box
+// being eight tokens of `heads` heads and 64 of their values, 128-byte swizzled.
+cudaError_t narrow_map(CUtensorMap* map, const void* pool, const pks_prefix_args& a, int heads) {
   const cuuint64_t dims[3] = {(cuuint64_t)a.D, (cuuint64_t)a.num_pages * (cuuint64_t)a.page_size,
                               (cuuint64_t)a.Hkv};
   const cuuint64_t strides[2] = {(cuuint64_t)a.Hkv * a.D * 2, (cuuint64_t)a.D * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)rows, (cuuint32_t)heads}, ones[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims,
-                            strides, box, ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+  const cuuint32_t box[3] = {64, 8, (cuuint32_t)heads};
+  return encode_map(map, pool, 3, dims, strides, box);
+}
+
+// The wide kernel's: heads x groups of eight rows x 64-value blocks x rows x
+// values, a box being all blocks of `rows` tokens of a head, in the tile's layout.
+cudaError_t wide_map(CUtensorMap* map, const void* pool, const pks_prefix_args& a, int rows) {
+  const cuuint64_t row = (cuuint64_t)a.Hkv * a.D * 2;
+  const cuuint64_t dims[5] = {64, 8, (cuuint64_t)a.D / 64,
+                              (cuuint64_t)a.num_pages * (cuuint64_t)a.page_size / 8,
+                              (cuuint64_t)a.Hkv};
+  const cuuint64_t strides[4] = {row, 128, 8 * row, (cuuint64_t)a.D * 2};
+  const cuuint32_t box[5] = {64, 8, (cuuint32_t)a.D / 64, (cuuint32_t)rows / 8, 1};
+  return encode_map(map, pool, 5, dims, strides, box);
 }
 
 template <int D>
@@ -1874,8 +1890,8 @@ cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const P
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap map_k{}, map_v{};
   if (sh.box > 0) {
-    if ((e = pool_map(&map_k, a.kv_k, a, sh.box, 1)) != cudaSuccess) return e;
-    if ((e = pool_map(&map_v, a.kv_v, a, sh.box, 1)) != cudaSuccess) return e;
+    if ((e = wide_map(&map_k, a.kv_k, a, sh.box)) != cudaSuccess) return e;
+    if ((e = wide_map(&map_v, a.kv_v, a, sh.box)) != cudaSuccess) return e;
   }
   return launch_ex(k_prefix_wide<D>, dim3(sh.wide_grid), dim3(kWideThreads), Wide<D>::kSmem, s,
                    /*pdl=*/true, /*coop=*/false, a.block_table,
@@ -1898,8 +1914,8 @@ cudaError_t launch_narrow(const pks_prefix_args& a, const PrefixLayout& L, const
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap map_k{}, map_v{};
   if (sh.box > 0) {
-    if ((e = pool_map(&map_k, a.kv_k, a, 8, HG)) != cudaSuccess) return e;
-    if ((e = pool_map(&map_v, a.kv_v, a, 8, HG)) != cudaSuccess) return e;
+    if ((e = narrow_map(&map_k, a.kv_k, a, HG)) != cudaSuccess) return e;
+    if ((e = narrow_map(&map_v, a.kv_v, a, HG)) != cudaSuccess) return e;
   }
   return launch_ex(kern, dim3(sh.narrow_grid), dim3((HG * WPH + 1) * 32), N::smem(a.B), s,
                    /*pdl=*/true, /*coop=*/false, a.block_table,
