@@ -521,7 +521,8 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 // One CTA an SM, 512 threads:
 //   warps 0-3, 4-7   softmax groups 0 and 1: a thread a query row
 //   warps 8, 9       issue the MMAs of groups 0 and 1
-//   warps 10-13      load Q and the K/V tiles
+//   warps 10-13      load the K/V tiles (TMA_WARPS of them those that come by TMA)
+//   warps 14, 15     load Q, a piece ahead where it fits, and tell the others
 // An item with more than 128 rows gives each group a row block of its own and
 // every tile goes to both; with 128 or fewer both groups hold the same rows and
 // take the tiles in turn, so that one group's softmax always runs beside the
@@ -552,13 +553,15 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 // a single row block and 64 KB a tile it is bound by memory.
 
 constexpr int kWideThreads = 512;
-constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadThreads = 128;
+constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadWarps = 4, kQWarp = 14;
+constexpr int kNotes = 4;  // pieces announced at a time, at most
+constexpr long long kDrainCycles = 20000000LL;   // about 10 ms
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
 
 template <int D>
 struct Wide {
   static constexpr int kBlk = D / 64;                          // 64-value column blocks
-  static constexpr uint32_t kGroupBytes = kBlk * 1024;         // eight rows: a block's, then the next's
+  static constexpr uint32_t kGroupBytes = kBlk * 1024;         // eight rows, block by block
   static constexpr uint32_t kTileBytes = kTile / 8 * kGroupBytes;  // K, V or Q tile
   static constexpr int kSlotsN = D == 128 ? 5 : 10;            // ring of K / V tiles
   static constexpr uint32_t kSmem = (2 + kSlotsN) * kTileBytes + 1024;
@@ -575,7 +578,16 @@ struct Piece {
   int jobs0, jobs1;     // jobs of the softmax groups
   int64_t slot;         // its first partial row
 };
-// A CTA's walk over its tiles; every role walks the same pieces.
+// What the issuers and the softmax need of a piece.
+struct Note {
+  int nt, by_tma, jobs0, jobs1;
+  int nrows, row0, own;  // of its item
+  int tok0, tok1;        // its first token, the item's last + 1
+  int q_block;           // ring block of Q (of group 0 when there are two)
+  int pair, last;
+  int64_t slot;
+};
+// A CTA's walk over its tiles, by the loads' warps.
 struct Walk {
   const Item* items;
   int left;             // tiles to come
@@ -613,7 +625,7 @@ __device__ __forceinline__ void store8(float* dst, const float (&v)[8]) {
 constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
 static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "the launch's registers");
 
-template <int D>
+template <int D, int TMA_WARPS>
 __global__ void __launch_bounds__(kWideThreads, 1)
 k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
               const __nv_bfloat16* __restrict__ kv_k, const __nv_bfloat16* __restrict__ kv_v,
@@ -624,15 +636,17 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   extern __shared__ uint8_t smem_raw[];
   // bar_tma / bar_cp: a ring slot has landed, by either way of loading; bar_go: it
   // may be filled by the second; bar_free: its products are done (both issuers');
-  // bar_q / bar_qfree: Q is there / its last product is done;
+  // bar_note[i]: piece note i and its Q are there; bar_noted: they have been read;
+  // bar_qfree[i]: the last product with Q block i is done (both issuers');
   // bar_s[g]: S of group g's job; bar_p[g][h]: half h of its P is written;
   // bar_turn[g]: the other issuer has issued its job's P.V and next S; bar_o[g]:
   // every product of the group's piece; bar_x[g] / bar_y[g]: the group's maxima
   // are posted / it has read the other's O; bar_drain[g]: on giving up
   __shared__ __align__(8) uint64_t bar_tma[W::kSlotsN], bar_cp[W::kSlotsN], bar_go[W::kSlotsN],
-      bar_free[W::kSlotsN], bar_q, bar_qfree, bar_s[2], bar_p[2][2], bar_turn[2], bar_o[2],
-      bar_x[2], bar_y[2], bar_drain[2];
+      bar_free[W::kSlotsN], bar_note[kNotes], bar_noted[kNotes], bar_qfree[2], bar_s[2],
+      bar_p[2][2], bar_turn[2], bar_o[2], bar_x[2], bar_y[2], bar_drain[2];
   __shared__ float2 s_ml[kRows];  // a row's maximum and sum, group 1's and then group 0's
+  __shared__ Note s_note[kNotes];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_sizes[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -643,14 +657,17 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   if (warp == 0) tc::tmem_alloc(&s_tmem, 512);
   if (tid == kMmaWarp * 32) {
     for (int i = 0; i < W::kSlotsN; ++i) {
-      tc::mbar_init(&bar_tma[i], 1);
-      tc::mbar_init(&bar_cp[i], kLoadThreads / 32);
+      tc::mbar_init(&bar_tma[i], TMA_WARPS);
+      tc::mbar_init(&bar_cp[i], kQWarp - kLoadWarp);
       tc::mbar_init(&bar_go[i], 1);
       tc::mbar_init(&bar_free[i], 2);
     }
-    tc::mbar_init(&bar_q, kLoadThreads / 32 - 1);
-    tc::mbar_init(&bar_qfree, 2);
+    for (int i = 0; i < kNotes; ++i) {
+      tc::mbar_init(&bar_note[i], 2);
+      tc::mbar_init(&bar_noted[i], kLoadWarp);
+    }
     for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&bar_qfree[i], 2);
       tc::mbar_init(&bar_s[i], 1);
       tc::mbar_init(&bar_p[i][0], 4);
       tc::mbar_init(&bar_p[i][1], 4);
@@ -701,7 +718,16 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     return full < pc.nt ? full : pc.nt;
   };
 
-  // Every role walks the same pieces and keeps its own count of the phases.
+  // the next piece's note, read and released
+  auto read_note = [&](uint32_t n, Note& note) -> bool {
+    if (!wait(&bar_note[n % kNotes], (n / kNotes) & 1)) return false;
+    note = s_note[n % kNotes];
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bar_noted[n % kNotes]);
+    return true;
+  };
+
+  // Every role keeps its own count of the phases.
   if (warp < kMmaWarp) {
     // ================= softmax: a thread a query row =================
     tc::setmaxnreg_inc<kSoftmaxRegs>();
@@ -709,18 +735,20 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     const uint32_t lane_off = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t tS = tmem + lane_off + kTmemS + g * kTile, tO = tmem + lane_off + g * 128;
     const uint64_t scale2 = tc::pack2(__float_as_uint(scale_log2), __float_as_uint(scale_log2));
-    uint32_t n_job = 0, n_piece = 0, n_split = 0;
-    while (walk.more() && ok) {
-      const Piece pc = walk.next();
+    uint32_t n_job = 0, n_note = 0, n_piece = 0, n_split = 0;
+    for (bool more = walk.more(); more;) {
+      Note pc;
+      if (!(ok = read_note(n_note++, pc))) break;
+      more = !pc.last;
       const int x = (pc.pair ? g * kRows : 0) + (tid & (kRows - 1));  // row of the item
       const int64_t row = pc.slot + x;
-      const bool mine = x < pc.it.nrows;
+      const bool mine = x < pc.nrows;
       const int my_jobs = g ? pc.jobs1 : pc.jobs0;
       const bool idle = !__any_sync(0xffffffffu, mine);  // no row of this warp counts
       // tokens this row sees
-      int limit = pc.it.t1;
-      if (pc.it.own && sh.causal && mine) limit = pc.it.own - sh.Nq + (pc.it.row0 + x) / sh.G + 1;
-      limit -= pc.it.t0 + pc.t_lo * kTile;
+      int limit = pc.tok1;
+      if (pc.own && sh.causal && mine) limit = pc.own - sh.Nq + (pc.row0 + x) / sh.G + 1;
+      limit -= pc.tok0;
       float m_run = kNegInf, l_run = 0.f;
       for (int i = 0; i < my_jobs; ++i) {
         if (!(ok = wait(&bar_s[g], n_job & 1))) break;
@@ -915,12 +943,19 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       // ================= MMA issue of one group =================
       const int g = warp - kMmaWarp;
       const uint32_t tS = tmem + kTmemS + g * kTile, tO = tmem + g * 128;
-      uint32_t n_slot = 0, n_job = 0, n_piece = 0, n_turn = 0, ph_tma = 0, ph_cp = 0;
+      uint32_t n_slot = 0, n_job = 0, n_note = 0, n_turn = 0, ph_tma = 0, ph_cp = 0;
       bool owed = false;
-      while (walk.more() && ok) {
-        const Piece pc = walk.next();
-        const int by_tma = tma_tiles(pc);
+      for (bool more_pieces = walk.more(); more_pieces && ok;) {
+        Note pc;
+        if (!(ok = read_note(n_note++, pc))) break;
+        more_pieces = !pc.last;
+        const int by_tma = pc.by_tma;
         const int my_jobs = g ? pc.jobs1 : pc.jobs0;
+        const int q_block = pc.pair ? (pc.q_block + g) & 1 : pc.q_block;
+        // a Q block that this issuer has no product with
+        if ((pc.pair || my_jobs == 0) && tc::elect_one())
+          tc::mbar_arrive(&bar_qfree[pc.pair ? q_block ^ 1 : q_block]);
+        __syncwarp();
         // K of tile t has landed already (no wait, no phase taken)
         auto ready = [&](int t, int tma) -> bool {
           const uint32_t sl = (n_slot + 2 * t) % W::kSlotsN;
@@ -944,7 +979,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           tc::fence_after();
           if (tc::elect_one()) {
             const uint32_t sl = (n_slot + 2 * t) % W::kSlotsN;
-            const uint64_t dq = tc::desc_sw128(sQ + (pc.pair ? g : 0) * W::kTileBytes, 16, W::kGroupBytes);
+            const uint64_t dq = tc::desc_sw128(sQ + q_block * W::kTileBytes, 16, W::kGroupBytes);
             const uint64_t dk = tc::desc_sw128(sKV + sl * W::kTileBytes, 16, W::kGroupBytes);
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
@@ -955,7 +990,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
             }
             tc::mma_commit(&bar_s[g]);
             tc::mma_commit(&bar_free[sl]);
-            if (last) tc::mma_commit(&bar_qfree);
+            if (last) tc::mma_commit(&bar_qfree[q_block]);
           }
           __syncwarp();
         };
@@ -970,11 +1005,10 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           return true;
         };
         const int step = pc.pair ? 1 : 2, t0 = pc.pair ? 0 : g;
-        ok = wait(&bar_q, n_piece & 1);
-        if (my_jobs > 0 && ok) {
+        if (my_jobs > 0) {
           if (t0 == 1) ok = skip(0);
           if (ok && (ok = landed(t0, 0))) issue_s(t0, my_jobs == 1, nullptr);
-        } else if (ok) {  // the one tile is the other group's
+        } else {  // the one tile is the other group's
           ok = skip(0);
         }
         for (int i = 0; i < my_jobs && ok; ++i, ++n_job) {
@@ -1029,10 +1063,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         if (ok && my_jobs > 0 && t0 + my_jobs * step - step + 1 < pc.nt)
           ok = skip(pc.nt - 1);
         owed = (pc.jobs0 + pc.jobs1) % 2 == 0;
-        if (my_jobs == 0 && ok && tc::elect_one()) tc::mbar_arrive(&bar_qfree);
-        __syncwarp();
         n_slot += 2 * pc.nt;
-        ++n_piece;
       }
       if (!ok && tc::elect_one()) {
         flag_error(pl.hdr + kErrWord, kErrTimeout);
@@ -1044,7 +1075,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         }
       }
       __syncwarp();
-    } else if (warp < kLoadWarp + kLoadThreads / 32) {
+    } else {
       // ================= loads =================
       const int lw = warp - kLoadWarp;
       constexpr int kChunks = D / 8;          // 16-byte chunks of a row
@@ -1062,48 +1093,29 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(bar);
       };
-      // first row of this lane's box of an item's tile, when it comes by TMA (warp
-      // 0, a lane a box; a bad page gives zeros, from beyond the pool)
-      const int n_box = sh.box ? kTile / sh.box : 0, my_box = lane;
-      auto box_row = [&](const Item& it, int tile) -> int {
-        if (my_box >= n_box || it.t0 % sh.box != 0 || it.t0 + (tile + 1) * kTile > it.t1) return 0;
-        const int tok = it.t0 + tile * kTile + my_box * sh.box;
-        const int page = block_table[(int64_t)it.bt_row * sh.max_pages + tok / sh.page_size];
-        if ((unsigned)page >= (unsigned)sh.num_pages) {
-          flag_error(pl.hdr + kErrWord, kErrPage);
-          return sh.num_pages * sh.page_size;
-        }
-        return page * sh.page_size + tok % sh.page_size;
-      };
-      uint32_t n_slot = 0, n_piece = 0;
-      uint32_t ph_go = 0;
-      uint32_t tma_used = 0, tma_count = 0;  // by slot: any TMA copy, their number modulo two
-      int row = 0;
-      if (lw == 0 && walk.more()) {
-        const Item first = pl.starts[cta].it;
-        row = box_row(first, walk.tile);
-      }
-      while (walk.more() && ok) {
-        const Piece pc = walk.next();
-        Item then = {};  // the next piece's item, for its first row
-        if (lw == 0 && walk.more()) then = walk.items[walk.item];
-        const int32_t* bt = block_table + (int64_t)pc.it.bt_row * sh.max_pages;
-        // physical row of this lane's token of tile t (-1: none)
-        auto token_row = [&](int t) -> int {
-          const int tok = pc.it.t0 + (pc.t_lo + t) * kTile + lw * 32 + lane;
-          if (tok >= pc.it.t1) return -1;
-          const int page = bt[tok / sh.page_size];
-          if ((unsigned)page >= (unsigned)sh.num_pages) {
-            flag_error(pl.hdr + kErrWord, kErrPage);
-            return -1;
-          }
-          return page * sh.page_size + tok % sh.page_size;
-        };
-        const int by_tma = tma_tiles(pc);
-        if (lw > 0) {  // Q: warps 1-3 (warp 0 sends the first tiles meanwhile)
-          if (n_piece > 0 && !(ok = wait(&bar_qfree, (n_piece - 1) & 1))) break;
+      if (warp >= kQWarp) {
+        // ---- Q blocks, 32 rows of a block and the next 32 by turns, and the notes
+        const int qw = warp - kQWarp;
+        uint32_t n_note = 0, n_block = 0, uses0 = 0, uses1 = 0;
+        while (walk.more() && ok) {
+          const Piece pc = walk.next();
+          const uint32_t nn = n_note % kNotes;
+          if (n_note >= (uint32_t)kNotes &&
+              !(ok = wait(&bar_noted[nn], (n_note / kNotes - 1) & 1)))
+            break;
+          const int q_block = n_block & 1;
+          // room: the blocks' products before are done
+          if ((pc.pair || q_block == 0) && uses0 > 0 &&
+              !(ok = wait(&bar_qfree[0], (uses0 - 1) & 1)))
+            break;
+          if ((pc.pair || q_block == 1) && uses1 > 0 &&
+              !(ok = wait(&bar_qfree[1], (uses1 - 1) & 1)))
+            break;
+          uses0 += pc.pair || q_block == 0;
+          uses1 += pc.pair || q_block == 1;
+          n_block += pc.pair ? 2 : 1;
 #pragma unroll 1
-          for (int c = lw - 1; c < (pc.pair ? 8 : 4); c += 3) {
+          for (int c = qw; c < (pc.pair ? 8 : 4); c += 2) {
             // query row of this lane: request, query token and head
             const int x = c * 32 + lane;
             int64_t off = -1;
@@ -1113,89 +1125,153 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
               const int r = pc.it.own ? gr : gr % sh.R;
               off = (((int64_t)b * sh.Nq + r / sh.G) * sh.Hq + pc.head * sh.G + r % sh.G) * D;
             }
+            const uint32_t tile = sQ + ((q_block + (c >> 2)) & 1) * W::kTileBytes;
 #pragma unroll 4
             for (int i = 0; i < 32; i += kRowsPer) {
               const int64_t o = __shfl_sync(0xffffffffu, off, i + sub);
-              tc::cp_async16(dst_of(sQ + (c >> 2) * W::kTileBytes, (c & 3) * 32 + i),
-                             q + (o >= 0 ? o + cc * 8 : 0), o >= 0 ? 16 : 0);
+              tc::cp_async16(dst_of(tile, (c & 3) * 32 + i), q + (o >= 0 ? o + cc * 8 : 0),
+                             o >= 0 ? 16 : 0);
             }
           }
           tc::cp_async_commit();
-          tc::cp_async_wait<0>();
-          publish(&bar_q);
-        }
-        int waiting = 0;  // tiles copied by cp.async and not published yet
-        int done = 0;
-        for (int t = 0; t < pc.nt && ok; ++t) {
-          if (t >= by_tma) row = token_row(t);
-          // the row of the tile after this one, in the next piece if need be
-          int next_row = 0;
-          if (lw == 0 && (t + 1 < pc.nt || walk.more()))
-            next_row = t + 1 < pc.nt ? box_row(pc.it, pc.t_lo + t + 1) : box_row(then, 0);
-#pragma unroll
-          for (int v = 0; v < 2; ++v, ++done) {
-            const uint32_t n = n_slot + done, s = n % W::kSlotsN;
-            // warp 0 waits for room; the others copy only where it has let them
-            if (lw == 0 && n >= (uint32_t)W::kSlotsN &&
-                !(ok = wait(&bar_free[s], (n / W::kSlotsN - 1) & 1)))
-              break;
-            if (t >= by_tma) {
-              if (lw == 0) {
-                if (lane == 0) tc::mbar_arrive(&bar_go[s]);
-              } else if (!(ok = wait(&bar_go[s], (ph_go >> s) & 1))) {
-                break;
-              }
-              ph_go ^= 1u << s;
-            }
-            const uint32_t tile = sKV + s * W::kTileBytes;
-            if (t < by_tma) {
-              if (lw == 0) {
-                tma_used |= 1u << s;
-                tma_count ^= 1u << s;
-                if (lane == 0) tc::mbar_arrive_expect(&bar_tma[s], W::kTileBytes);
-                __syncwarp();
-                if (my_box < n_box)
-                  tc::tma_load_5d(tile + my_box * (sh.box / 8) * W::kGroupBytes,
-                                  v ? &map_v : &map_k, 0, 0, 0, row / 8, pc.head, &bar_tma[s]);
-              }
-            } else {
-              const __nv_bfloat16* pool = (v ? kv_v : kv_k) + pc.head * D + cc * 8;
-#pragma unroll 8
-              for (int r = 0; r < 32; r += kRowsPer) {
-                const int pr = __shfl_sync(0xffffffffu, row, r + sub);
-                tc::cp_async16(dst_of(tile, lw * 32 + r),
-                               pool + (pr >= 0 ? (int64_t)pr * sh.Hkv * D : 0), pr >= 0 ? 16 : 0);
-              }
-              tc::cp_async_commit();
-              ++waiting;
-            }
-            if (waiting > W::kLag) {
-              tc::cp_async_wait<W::kLag>();
-              publish(&bar_cp[(n - W::kLag) % W::kSlotsN]);
-              --waiting;
-            }
+          if (qw == 0 && lane == 0) {
+            Note note;
+            note.nt = pc.nt;
+            note.by_tma = tma_tiles(pc);
+            note.jobs0 = pc.jobs0;
+            note.jobs1 = pc.jobs1;
+            note.nrows = pc.it.nrows;
+            note.row0 = pc.it.row0;
+            note.own = pc.it.own;
+            note.tok0 = pc.it.t0 + pc.t_lo * kTile;
+            note.tok1 = pc.it.t1;
+            note.q_block = q_block;
+            note.pair = pc.pair;
+            note.last = !walk.more();
+            note.slot = pc.slot;
+            s_note[nn] = note;
           }
-          row = next_row;
+          tc::cp_async_wait<0>();
+          publish(&bar_note[nn]);
+          ++n_note;
+        }
+        if (!ok && lane == 0) {
+          flag_error(pl.hdr + kErrWord, kErrTimeout);
+          s_abort = 1;
         }
         tc::cp_async_wait<0>();
-        for (; waiting; --waiting) publish(&bar_cp[(n_slot + done - waiting) % W::kSlotsN]);
-        n_slot += done;
-        ++n_piece;
-      }
-      if (!ok && lane == 0) {
-        flag_error(pl.hdr + kErrWord, kErrTimeout);
-        s_abort = 1;
-      }
-      // the TMA copies in flight land before the shared memory is given up (in
-      // the normal course every one has been waited for)
-      if (!ok && lw == 0 && lane == 0) {
-        const long long t0 = clock64();
-        for (int i = 0; i < W::kSlotsN; ++i)
-          while (((tma_used >> i) & 1) && !tc::mbar_try_wait(&bar_tma[i], (~tma_count >> i) & 1) &&
-                 clock64() - t0 < kWaitCycles) {
+      } else {
+        // first row of this lane's box of an item's tile, when it comes by TMA (a bad
+        // page gives zeros, from beyond the pool)
+        const int n_box = sh.box && lw < TMA_WARPS ? kTile / sh.box / TMA_WARPS : 0;
+        const int my_box = lw * n_box + lane;
+        auto box_row = [&](const Item& it, int tile) -> int {
+          if (lane >= n_box || it.t0 % sh.box != 0 || it.t0 + (tile + 1) * kTile > it.t1) return 0;
+          const int tok = it.t0 + tile * kTile + my_box * sh.box;
+          const int page = block_table[(int64_t)it.bt_row * sh.max_pages + tok / sh.page_size];
+          if ((unsigned)page >= (unsigned)sh.num_pages) {
+            flag_error(pl.hdr + kErrWord, kErrPage);
+            return sh.num_pages * sh.page_size;
           }
+          return page * sh.page_size + tok % sh.page_size;
+        };
+        uint32_t n_slot = 0;
+        uint32_t ph_go = 0;
+        uint32_t tma_used = 0, tma_count = 0;  // by slot: any TMA copy, their number modulo two
+        int row = 0;
+        if (walk.more()) {
+          const Item first = pl.starts[cta].it;
+          row = box_row(first, walk.tile);
+        }
+        while (walk.more() && ok) {
+          const Piece pc = walk.next();
+          Item then = {};  // the next piece's item, for its first row
+          if (walk.more()) then = walk.items[walk.item];
+          const int32_t* bt = block_table + (int64_t)pc.it.bt_row * sh.max_pages;
+          // physical row of this lane's token of tile t (-1: none)
+          auto token_row = [&](int t) -> int {
+            const int tok = pc.it.t0 + (pc.t_lo + t) * kTile + lw * 32 + lane;
+            if (tok >= pc.it.t1) return -1;
+            const int page = bt[tok / sh.page_size];
+            if ((unsigned)page >= (unsigned)sh.num_pages) {
+              flag_error(pl.hdr + kErrWord, kErrPage);
+              return -1;
+            }
+            return page * sh.page_size + tok % sh.page_size;
+          };
+          const int by_tma = tma_tiles(pc);
+          int waiting = 0;  // tiles copied by cp.async and not published yet
+          int done = 0;
+          for (int t = 0; t < pc.nt && ok; ++t) {
+            if (t >= by_tma) row = token_row(t);
+            // the row of the tile after this one, in the next piece if need be
+            int next_row = 0;
+            if (t + 1 < pc.nt || walk.more())
+              next_row = t + 1 < pc.nt ? box_row(pc.it, pc.t_lo + t + 1) : box_row(then, 0);
+  #pragma unroll
+            for (int v = 0; v < 2; ++v, ++done) {
+              const uint32_t n = n_slot + done, s = n % W::kSlotsN;
+              // a warp that takes part in every fill waits for room; the others copy
+              // only where warp 0 has let them
+              if (lw < TMA_WARPS) {
+                if (n >= (uint32_t)W::kSlotsN &&
+                    !(ok = wait(&bar_free[s], (n / W::kSlotsN - 1) & 1)))
+                  break;
+                if (TMA_WARPS < kLoadWarps && t >= by_tma && lane == 0) tc::mbar_arrive(&bar_go[s]);
+              } else if (t >= by_tma) {
+                if (!(ok = wait(&bar_go[s], (ph_go >> s) & 1))) break;
+                ph_go ^= 1u << s;
+              }
+              const uint32_t tile = sKV + s * W::kTileBytes;
+              if (t < by_tma) {
+                if (lw >= TMA_WARPS) continue;
+                tma_used |= 1u << s;
+                tma_count ^= 1u << s;
+                if (lane == 0) tc::mbar_arrive_expect(&bar_tma[s], W::kTileBytes / TMA_WARPS);
+                __syncwarp();
+                if (lane < n_box)
+                  tc::tma_load_5d(tile + my_box * (sh.box / 8) * W::kGroupBytes,
+                                  v ? &map_v : &map_k, 0, 0, 0, row / 8, pc.head, &bar_tma[s]);
+              } else {
+                const __nv_bfloat16* pool = (v ? kv_v : kv_k) + pc.head * D + cc * 8;
+  #pragma unroll 8
+                for (int r = 0; r < 32; r += kRowsPer) {
+                  const int pr = __shfl_sync(0xffffffffu, row, r + sub);
+                  tc::cp_async16(dst_of(tile, lw * 32 + r),
+                                 pool + (pr >= 0 ? (int64_t)pr * sh.Hkv * D : 0), pr >= 0 ? 16 : 0);
+                }
+                tc::cp_async_commit();
+                ++waiting;
+              }
+              if (waiting > W::kLag) {
+                tc::cp_async_wait<W::kLag>();
+                publish(&bar_cp[(n - W::kLag) % W::kSlotsN]);
+                --waiting;
+              }
+            }
+            row = next_row;
+          }
+          tc::cp_async_wait<0>();
+          for (; waiting; --waiting) publish(&bar_cp[(n_slot + done - waiting) % W::kSlotsN]);
+          n_slot += done;
+        }
+        if (!ok && lane == 0) {
+          flag_error(pl.hdr + kErrWord, kErrTimeout);
+          s_abort = 1;
+        }
+        // the TMA copies in flight land before the shared memory is given up (in
+        // the normal course every one has been waited for; a slot that not all of
+        // the warps filled stays open, so its copies get a limited time)
+        if (!ok && lane == 0) {
+          const long long t0 = clock64();
+          for (int i = 0; i < W::kSlotsN; ++i)
+            while (((tma_used >> i) & 1) &&
+                   !tc::mbar_try_wait(&bar_tma[i], (~tma_count >> i) & 1) &&
+                   clock64() - t0 < kDrainCycles) {
+            }
+        }
+        __syncwarp();
       }
-      __syncwarp();
     }
   }
   tc::fence_before();
@@ -1884,8 +1960,14 @@ cudaError_t wide_map(CUtensorMap* map, const void* pool, const pks_prefix_args& 
 template <int D>
 cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const PrefixShape& sh,
                         float scale_log2, cudaStream_t s) {
-  static bool done[64] = {false};
-  cudaError_t e = allow_smem(k_prefix_wide<D>, Wide<D>::kSmem, done);
+  static bool done[2][64] = {};
+  // Boxes of 64 rows or more are issued by one warp; smaller ones, which would take
+  // it too long, by four, and so are the other pages' rows (1024 rows on 131,072
+  // tokens, us, by one / four: D = 128, pages of 8 568 / 383, of 16 453 / 383, of 64
+  // with the narrow kernel beside it 415 / 425; D = 64, pages of 16 449 / 329).
+  const bool spread = sh.box <= kTile / kLoadWarps;
+  auto kern = spread ? k_prefix_wide<D, kLoadWarps> : k_prefix_wide<D, 1>;
+  cudaError_t e = allow_smem(kern, Wide<D>::kSmem, done[spread]);
   if (e != cudaSuccess) return e;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   CUtensorMap map_k{}, map_v{};
@@ -1893,7 +1975,7 @@ cudaError_t launch_wide(const pks_prefix_args& a, const PrefixLayout& L, const P
     if ((e = wide_map(&map_k, a.kv_k, a, sh.box)) != cudaSuccess) return e;
     if ((e = wide_map(&map_v, a.kv_v, a, sh.box)) != cudaSuccess) return e;
   }
-  return launch_ex(k_prefix_wide<D>, dim3(sh.wide_grid), dim3(kWideThreads), Wide<D>::kSmem, s,
+  return launch_ex(kern, dim3(sh.wide_grid), dim3(kWideThreads), Wide<D>::kSmem, s,
                    /*pdl=*/true, /*coop=*/false, a.block_table,
                    static_cast<const __nv_bfloat16*>(a.q),
                    static_cast<const __nv_bfloat16*>(a.kv_k),
@@ -2019,7 +2101,8 @@ cudaError_t launch_prefix_plan(const pks_prefix_args& a, const PrefixLayout& L, 
   const int blocks = (a.B + at_once - 1) / at_once;
   const int grid = !a.prefix_group || a.B <= kPlanOneBlock ? 1 : blocks < most ? blocks : most;
   return launch_ex(k_prefix_plan, dim3(grid), dim3(kPlanThreads),
-                   kPlanArrays * sizeof(int32_t) * (size_t)a.B, s, /*pdl=*/true, /*coop=*/false, a.seq_lens,
+                   kPlanArrays * sizeof(int32_t) * (size_t)a.B, s, /*pdl=*/true,
+                   /*coop=*/false, a.seq_lens,
                    a.block_table, a.prefix_group, plan_ptrs(a.workspace, L), sh);
 }
 
