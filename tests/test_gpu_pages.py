@@ -341,3 +341,27 @@ def test_table_feeds_the_decode_step():
     out0, idx0 = SparseDecodeStep(before, wl.k)()
     assert torch.equal(out, out0) and torch.equal(idx, idx0)
     assert step.device_error() == 0 and pages.device_error() == 0
+
+
+def test_tensors_elsewhere_are_refused(monkeypatch):
+    """Arguments on the host, and calls while another device is the current one."""
+    lens, table = dev([20, 0, 0]), dev([[0, 1, -1], [-1] * 3, [-1] * 3])
+    pages = PageTable(lens, table, 6, 16)
+    rows = torch.tensor([1], dtype=torch.int32)
+    calls = [lambda r: pages.fork(dev([0]), r), lambda r: pages.fork(r, dev([1])),
+             lambda r: pages.fork(dev([0]), dev([1]), r), lambda r: pages.free(r),
+             lambda r: pages.free(dev([0]), r),
+             lambda r: pages.extend(torch.cat([r, r, r]))]
+    for call in calls:
+        with pytest.raises(ValueError):
+            call(rows)
+    with pytest.raises(ValueError):
+        PageTable(lens.cpu(), table, 6, 16)
+    here = rows.cuda()
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: 1)
+        for call in [lambda: pages.free(here), lambda: pages.fork(here, here), pages.compact,
+                     lambda: pages.extend(lens)]:
+            with pytest.raises(ValueError):
+                call()
+    assert pages.device_error() == 0 and int(pages.n_free) == 4

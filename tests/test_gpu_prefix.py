@@ -402,3 +402,75 @@ def test_fork_extend_attend_free_compact():
     pages.compact()
     assert int(table[[1, 2, 4, 6, 8]].max()) == held - 1
     steps(3)
+
+
+@pytest.mark.parametrize("page", [8, 24, 32, 40, 192])
+@pytest.mark.parametrize("D,G", [(64, 8), (128, 16)])
+def test_boxes(page, D, G):
+    """Boxes of 8, 16, 32 and 64 rows, whole tiles and ends, one block of rows and
+    two; several pieces a CTA."""
+    members = 20 if page < 40 else 6
+    pre = -(-1000 // page) * page
+    lens = [pre + 7 * i for i in range(members)] + [3 * page + 5]
+    Batch(lens, [1] * members + [-1], [pre] * members + [0], page=page, D=D, Hkv=2, G=G,
+          seed=page + D).run()
+    Batch(lens, [1] * members + [-1], [pre] * members + [0], page=page, D=D, Hkv=2, G=G, Nq=3,
+          seed=page + D + 1).run(causal=True, rows=[0, 5, members])
+
+
+@pytest.mark.parametrize("Hkv", [1, 2, 4, 8])
+@pytest.mark.parametrize("page", [1, 3])
+@pytest.mark.parametrize("D", [64, 128])
+def test_own_tokens_row_by_row(Hkv, page, D):
+    """Pages without whole boxes: every number of heads that a CTA takes."""
+    Batch([100, 33, 16, 15, 1], [-1] * 5, [0] * 5, page=page, D=D, Hkv=Hkv, G=2, Nq=3,
+          seed=Hkv + page + D).run(causal=True)
+
+
+@pytest.mark.parametrize("B,Hkv,G,Nq", [
+    (1, 1, 4, 2),      # hundreds of parts a row
+    (3, 8, 8, 1),
+    (40, 8, 16, 1),    # a warp a row
+    (6, 8, 8, 17),     # the most rows of that kind (152 SMs: 6,080), and one more
+    (190, 8, 4, 1),    # request
+    (191, 8, 4, 1),
+    (16, 8, 16, 8),    # eight lanes a row, some rows of many parts
+])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_and_parts(B, Hkv, G, Nq, D):
+    """Few and many rows to merge, the first request's of many parts, some of none."""
+    lens = [9000] + [0, 70, 300, 17][: B - 1] * (B // 4 + 1)
+    lens = lens[:B]
+    Batch(lens, [-1] * B, [0] * B, D=D, Hkv=Hkv, G=G, Nq=Nq, seed=B).run(
+        rows=sorted({0, min(1, B - 1), min(3, B - 1), B - 1}))
+
+
+def test_little_own_work_beside_the_prefix():
+    """Pieces of a few tiles, and of twelve."""
+    for own in (20, 200, 900):
+        Batch([320 + own] * 13, [0] * 8 + [1] * 5, [320] * 13, page=5, D=128, Hkv=8, G=4,
+              seed=own).run(rows=[0, 7, 8, 12])
+
+
+def test_later_calls_keep_to_a_layers_tensors():
+    b = Batch([900, 1200], [0, 0], [768] * 2, seed=21)
+    att = b.attention()
+    q = (b.q.float() * 0.5).to(torch.bfloat16)
+    b.q = q.clone()
+    att.plan()
+    att.attend(q)
+    del q
+    trash = [torch.full_like(b.q, float("nan")) for _ in range(8)]
+    out = att()
+    torch.cuda.synchronize()
+    b.check(out, att.lse)
+    del trash
+
+
+def test_another_current_device_is_refused(monkeypatch):
+    b = Batch([900, 1200], [0, 0], [768] * 2, seed=22)
+    att = b.attention()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (att, att.plan, att.attend, b.attention):
+        with pytest.raises(ValueError):
+            call()

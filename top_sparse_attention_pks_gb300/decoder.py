@@ -261,7 +261,8 @@ class PrefixAttention:
 
     Calling the object plans and attends.  ``plan`` alone is needed whenever
     lengths, table or groups have changed; ``attend`` serves further layers,
-    ``attend(q, kv_k, kv_v)`` with tensors of the same shapes."""
+    ``attend(q, kv_k, kv_v)`` with tensors of the same shapes, which later calls
+    keep to.  One object's calls run one after another: their workspace is one."""
 
     def __init__(self, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
                  causal: bool = False, sm_scale: float = 0.0, lse: bool = False,
@@ -277,23 +278,28 @@ class PrefixAttention:
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         self.workspace[:256].zero_()
         self.args = pks.make_prefix_args(workspace=self.workspace, **kw)
-        self._keep = (seq_lens, block_table, prefix_group, q, kv_k, kv_v)
+        self._keep = [seq_lens, block_table, prefix_group, q, kv_k, kv_v]
 
     def plan(self, stream=None):
+        pks._on_current_device(self.out)
         pks.pks_prefix_plan(self.args, stream)
 
     def attend(self, q=None, kv_k=None, kv_v=None, stream=None):
         for name, t in (("q", q), ("kv_k", kv_k), ("kv_v", kv_v)):
             if t is None:
                 continue
-            was = self._keep[("q", "kv_k", "kv_v").index(name) + 3]
-            if tuple(t.shape) != tuple(was.shape) or t.device != was.device:
+            at = ("q", "kv_k", "kv_v").index(name) + 3
+            was = self._keep[at]
+            if t.shape != was.shape or t.device != was.device:
                 raise ValueError(f"{name} must have the shape and device it was planned with")
             setattr(self.args, name, pks._dptr(t, torch.bfloat16, name))
+            self._keep[at] = t
+        pks._on_current_device(self.out)
         pks.pks_prefix_attention(self.args, stream)
         return self.out
 
     def __call__(self, stream=None):
+        pks._on_current_device(self.out)
         pks.pks_prefix_plan(self.args, stream)
         pks.pks_prefix_attention(self.args, stream)
         return self.out
@@ -308,7 +314,7 @@ class PageTable:
     ``block_table`` [B, max_pages] (int32, e.g. from ``Pool.build_block_table``)
     stay the caller's tensors and are updated in place; ``pools`` are the paged
     tensors [num_pages, page_size, ...] whose rows move with the pages.  All
-    calls run on ``stream`` (default: torch's current stream).
+    calls run on ``stream`` (default: torch's current stream), one after another.
 
     ``refs`` [num_pages], ``n_free`` and ``granted`` (0-dim) are views of the
     state and ``page_map`` [num_pages] is what the last ``compact`` wrote."""
@@ -334,18 +340,22 @@ class PageTable:
 
     def fork(self, src_rows, dst_rows, n_tokens=None, stream=None):
         """Rows ``dst_rows`` (empty) become aliases of ``src_rows``' first tokens."""
+        pks._on_current_device(self.state, src_rows, dst_rows, n_tokens)
         pks.pks_pages_fork(self.args, src_rows, dst_rows, n_tokens, stream)
 
     def extend(self, add, stream=None):
         """Every row grows by ``add`` [B] tokens, or none does (``granted`` is 0)."""
+        pks._on_current_device(self.state, add)
         pks.pks_pages_extend(self.args, add, stream)
 
     def free(self, rows, keep=None, stream=None):
         """Truncate ``rows`` to ``keep`` tokens (default 0: give them back)."""
+        pks._on_current_device(self.state, rows, keep)
         pks.pks_pages_free(self.args, rows, keep, stream)
 
     def compact(self, stream=None):
         """Move the held pages to the lowest ids; returns the map of page ids."""
+        pks._on_current_device(self.state)
         pks.pks_pages_compact(self.args, self.page_map, stream)
         return self.page_map
 

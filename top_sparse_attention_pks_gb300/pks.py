@@ -247,10 +247,10 @@ def _dptr(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
 
 def _on_current_device(*tensors) -> None:
     """The library launches on the current device: its tensors have to be there."""
-    here = torch.device("cuda", torch.cuda.current_device())
-    for t in tensors:
-        if t is not None and t.device != here:
-            raise ValueError(f"tensor on {t.device}, but the current device is {here}")
+    here = torch.cuda.current_device()
+    for t in tensors:  # (get_device is -1 on the host)
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensor on {t.device}, but the current device is cuda:{here}")
 
 
 def _host_i32(x) -> np.ndarray:
@@ -770,8 +770,8 @@ def pks_pages_init(args: pks_pages_args, stream=None) -> None:
 
 
 def pks_pages_fork(args: pks_pages_args, src_rows, dst_rows, n_tokens=None, stream=None) -> None:
-    n = int(src_rows.shape[0])
-    if dst_rows.shape[0] != n or (n_tokens is not None and n_tokens.shape[0] != n):
+    n = src_rows.numel()
+    if dst_rows.numel() != n or (n_tokens is not None and n_tokens.numel() != n):
         raise ValueError("src_rows, dst_rows and n_tokens must have the same length")
     _check(lib().pks_pages_fork(ctypes.byref(args), n, _dptr(src_rows, torch.int32, "src_rows"),
                                 _dptr(dst_rows, torch.int32, "dst_rows"),
@@ -787,8 +787,8 @@ def pks_pages_extend(args: pks_pages_args, add, stream=None) -> None:
 
 
 def pks_pages_free(args: pks_pages_args, rows, keep=None, stream=None) -> None:
-    n = int(rows.shape[0])
-    if keep is not None and keep.shape[0] != n:
+    n = rows.numel()
+    if keep is not None and keep.numel() != n:
         raise ValueError("rows and keep must have the same length")
     _check(lib().pks_pages_free(ctypes.byref(args), n, _dptr(rows, torch.int32, "rows"),
                                 _dptr(keep, torch.int32, "keep"), _stream(stream)),
