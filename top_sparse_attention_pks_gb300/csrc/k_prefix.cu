@@ -1208,7 +1208,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
             int next_row = 0;
             if (t + 1 < pc.nt || walk.more())
               next_row = t + 1 < pc.nt ? box_row(pc.it, pc.t_lo + t + 1) : box_row(then, 0);
-  #pragma unroll
+#pragma unroll
             for (int v = 0; v < 2; ++v, ++done) {
               const uint32_t n = n_slot + done, s = n % W::kSlotsN;
               // a warp that takes part in every fill waits for room; the others copy
@@ -1234,7 +1234,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
                                   v ? &map_v : &map_k, 0, 0, 0, row / 8, pc.head, &bar_tma[s]);
               } else {
                 const __nv_bfloat16* pool = (v ? kv_v : kv_k) + pc.head * D + cc * 8;
-  #pragma unroll 8
+#pragma unroll 8
                 for (int r = 0; r < 32; r += kRowsPer) {
                   const int pr = __shfl_sync(0xffffffffu, row, r + sub);
                   tc::cp_async16(dst_of(tile, lw * 32 + r),
