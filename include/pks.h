@@ -428,7 +428,8 @@ pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_str
  * least half of what the second longest shares) takes part once for all of
  * these members, the rest of each request on its own.  Rows of a tile beyond
  * a causal query's limit count with weight zero, so their V rows have to be
- * finite; rows at or beyond len_b are never read.
+ * finite; rows at or beyond len_b are never read.  Calls that share a workspace
+ * run one after another.
  * ---------------------------------------------------------------------- */
 typedef struct pks_prefix_args {
   int32_t B;              /* requests; B * Nq <= 4096, B * max_pages * page_size <= 2^34 */
@@ -493,7 +494,8 @@ pks_status pks_prefix_device_error(const pks_prefix_args* args, int32_t* code,
  *   free_map               bit p of the uint32 words: page p is free
  *   scratch
  * Each section starts on a 256-byte boundary; pks_pages_offsets gives ref and
- * free_map.  Free pages are taken in ascending id order.
+ * free_map.  Free pages are taken in ascending id order.  Calls on one state run
+ * one after another.
  * ---------------------------------------------------------------------- */
 #define PKS_PAGES_MAX_POOLS 8
 

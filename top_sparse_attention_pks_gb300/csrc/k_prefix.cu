@@ -43,10 +43,15 @@ namespace {
 constexpr int kTile = 128;        // tokens of a wide tile (MMA N of S, K of P.V)
 constexpr int kRows = 128;        // query rows of one MMA
 constexpr int kItemRows = 256;    // query rows of an item: two MMAs
-constexpr int kNarrowRows = 16;   // most rows (Nq * G) of the narrow kernel
+// Most rows (Nq * G) of the narrow kernel.  With 16 rows, four drafts, us a pass:
+// 64 requests 126, by the wide kernel (16 of its 128 rows in use) 136; 32 requests
+// 83 and 82, 16 requests 60 and 57.
+constexpr int kNarrowRows = 16;
 constexpr int kNarrowTile = 16;
 constexpr int kMaxB = 4096;
-// Shared tokens below which a group is not worth a prefix item: one wide tile.
+// Shared tokens below which a group is not worth a prefix item: one wide tile (64
+// tokens shared by three of five short requests: 22.7 us with the item, 18.6
+// without; 200 to 1500 by eight cost up to 12 us of 57 to 67, 6000 save 11 of 50).
 constexpr int kMinShared = kTile;
 
 struct Item {
@@ -167,7 +172,9 @@ struct Pieces {
 constexpr int kPlanThreads = 512;
 constexpr int kPlanArrays = 14;
 constexpr int kPlanWarps = 4;      // warps a request otherwise
-constexpr int kPlanOneBlock = 32;  // requests up to which one block does it all
+// Requests up to which one block does it all (a pass of 5: 18.6 us by one block,
+// 20.0 by several; of 107: 64.7 and 55.4; of 128 with long tables 460 and 418).
+constexpr int kPlanOneBlock = 32;
 
 // tokens every query of the request sees
 __device__ __forceinline__ int seen_by_all(int len, int causal, int Nq) {
@@ -546,11 +553,13 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 // 2.15).  The running maximum moves only when a tile exceeds it by more than 8
 // (log2 units).
 //
-// Measured on that product (K/V of 8 heads, 550 GFLOP): 1.3 PFLOP/s on the SMs it
-// has, the tensor pipe 67% active.  Softmax arithmetic is not what bounds it
+// Measured on that product (K/V of 8 heads, 550 GFLOP): 1.45 PFLOP/s, the tensor
+// pipe 72% active on the SMs it has.  Softmax arithmetic is not what bounds it
 // (without the exponentials it takes as long); the pipe takes about 76 cycles for
-// a product of 64 when one issuer feeds it and idles where the turns change.  With
-// a single row block and 64 KB a tile it is bound by memory.
+// a product of 64 when one issuer feeds it, both operands coming from shared
+// memory, and idles where the turns change.  With D = 64 half the products take
+// 325 of 379 us: a group's next S waits for its P.V.  With a single row block and
+// 64 KB a tile it is bound by memory.
 
 constexpr int kWideThreads = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadWarps = 4, kQWarp = 14;
