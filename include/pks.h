@@ -472,8 +472,9 @@ pks_status pks_prefix_plan(const pks_prefix_args* args, pks_stream stream);
 pks_status pks_prefix_attention(const pks_prefix_args* args, pks_stream stream);
 
 /* Copy the workspace's device error word to *code (host) and clear it;
- * synchronises the stream (codes as for pks_decode_device_error; 5: a bounded
- * wait inside the kernel gave up). */
+ * synchronises the stream (codes as for pks_decode_device_error; 4: no plan for
+ * these shapes in the workspace, nothing written; 5: a bounded wait inside the
+ * kernel gave up). */
 pks_status pks_prefix_device_error(const pks_prefix_args* args, int32_t* code,
                                    pks_stream stream);
 
@@ -577,7 +578,8 @@ pks_status pks_pages_compact(const pks_pages_args* args, int32_t* page_map, pks_
 /* Copy the state's device error word to *code (host) and clear it;
  * synchronises the stream.  0: none; 1 page id out of range; 3 length, token
  * count or growth out of range; 4 a page lost more holders than it had;
- * 6 out of pages; 7 row index out of range, repeated, not empty or both
+ * or the state is not one that pks_pages_init filled for these pages (then the
+ * call changed nothing); 6 out of pages; 7 row index out of range, repeated, not empty or both
  * source and destination. */
 pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks_stream stream);
 

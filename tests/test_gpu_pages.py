@@ -365,3 +365,48 @@ def test_tensors_elsewhere_are_refused(monkeypatch):
             with pytest.raises(ValueError):
                 call()
     assert pages.device_error() == 0 and int(pages.n_free) == 4
+
+
+def test_states_of_other_pages_are_refused():
+    """A state that was not filled, or for other pages, changes nothing."""
+    lens, table = dev([20, 0, 5]), dev([[0, 1, -1], [-1] * 3, [2, -1, -1]])
+    pool = torch.arange(8 * 16, dtype=torch.int32, device="cuda").view(8, 16, 1)
+    size = pks.pks_pages_state_bytes(8)
+    for fill in (0, 7):
+        state = torch.zeros(size, dtype=torch.uint8, device="cuda")
+        full = pks.make_pages_args(seq_lens=lens, block_table=table, num_pages=8, page_size=16,
+                                   state=state, pools=[pool])
+        if fill:  # for seven pages
+            pks.pks_pages_init(pks.make_pages_args(seq_lens=lens, block_table=table, num_pages=7,
+                                                   page_size=16, state=state))
+        before = [x.clone() for x in (lens, table, pool)]
+        calls = [lambda: pks.pks_pages_fork(full, dev([0]), dev([1])),
+                 lambda: pks.pks_pages_free(full, dev([0])),
+                 lambda: pks.pks_pages_extend(full, dev([1, 1, 30])),
+                 lambda: pks.pks_pages_compact(full)]
+        for call in calls:
+            call()
+            assert pks.pks_pages_device_error(full) == 4
+        for was, x in zip(before, (lens, table, pool)):
+            assert torch.equal(was, x)
+
+
+def test_fewer_free_pages_than_counted():
+    lens, table = dev([20, 0, 5]), dev([[0, 1, -1], [-1] * 3, [2, -1, -1]])
+    pages = PageTable(lens, table, 8, 16)
+    pages.n_free.fill_(7)  # five are free
+    pages.extend(dev([28, 48, 43]))  # six pages
+    assert int(pages.granted) == 0 and pages.device_error() == 4
+    assert lens.tolist() == [20, 0, 5]
+    assert table.tolist() == [[0, 1, -1], [-1] * 3, [2, -1, -1]]
+
+
+@pytest.mark.parametrize("entry", [-1, -2, 6, 2 ** 31 - 1])
+def test_free_flags_any_bad_entry(entry):
+    lens, table = dev([40, 0]), dev([[0, 1, 2], [-1] * 3])
+    pages = PageTable(lens, table, 6, 16)
+    table[0, 1] = entry
+    pages.free(dev([0]))
+    assert pages.device_error() == 1
+    assert lens.tolist() == [0, 0] and int(table.max()) == -1
+    assert pages.refs.tolist() == [0, 1, 0, 0, 0, 0] and int(pages.n_free) == 5

@@ -67,6 +67,12 @@ __device__ __forceinline__ void flag_error(int32_t* hdr, int code) {
   atomicCAS(hdr + kHdrErr, 0, code);
 }
 
+// the state is one that pks_pages_init filled for these pages
+__device__ __forceinline__ bool state_ok(const PageState& st, int num_pages, int page_size) {
+  const int2 of = *reinterpret_cast<const int2*>(st.hdr + kHdrPages);
+  return (st.hdr[kHdrMagic] == kPagesMagic) & (of.x == num_pages) & (of.y == page_size);
+}
+
 __device__ __forceinline__ int pages_of(int tokens, int page_size) {
   return (int)(((int64_t)tokens + page_size - 1) / page_size);
 }
@@ -141,6 +147,7 @@ k_pages_fork(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
   const int i = blockIdx.x, tid = threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
+  const bool known = state_ok(st, num_pages, page_size);
   const int src = src_rows[i], dst = dst_rows[i];
   bool bad = (unsigned)src >= (unsigned)B || (unsigned)dst >= (unsigned)B || src == dst;
   for (int j = tid; j < n; j += kRowThreads) {
@@ -148,8 +155,8 @@ k_pages_fork(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
     // an earlier fork has this destination; a row on both sides
     bad |= (j < i && d == dst) || d == src || s == dst;
   }
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) flag_error(st.hdr, kErrRow);
+  if (__syncthreads_or(bad) || !known) {
+    if (tid == 0) flag_error(st.hdr, known ? kErrRow : kErrState);
     return;
   }
   if (seq_lens[dst] != 0) {
@@ -206,11 +213,12 @@ k_pages_free(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
   const int i = blockIdx.x, tid = threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
+  const bool known = state_ok(st, num_pages, page_size);
   const int row = rows[i];
   bool bad = (unsigned)row >= (unsigned)B;
   for (int j = tid; j < i; j += kRowThreads) bad |= rows[j] == row;
-  if (__syncthreads_or(bad)) {
-    if (tid == 0) flag_error(st.hdr, kErrRow);
+  if (__syncthreads_or(bad) || !known) {
+    if (tid == 0) flag_error(st.hdr, known ? kErrRow : kErrState);
     return;
   }
   const int len = seq_lens[row];
@@ -227,11 +235,11 @@ k_pages_free(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
       const int p = p0 + u * kRowThreads;
-      page[u] = p < p1 ? row_t[p] : -2;
+      page[u] = p < p1 ? row_t[p] : -1;
     }
 #pragma unroll
     for (int u = 0; u < kRowUnroll; ++u) {
-      if (page[u] == -2) continue;
+      if (p0 + u * kRowThreads >= p1) continue;
       row_t[p0 + u * kRowThreads] = -1;
       if ((unsigned)page[u] < (unsigned)num_pages) had[u] = atomicSub(&st.ref[page[u]], 1);
       else flag_error(st.hdr, kErrPage);
@@ -269,6 +277,7 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   pdl_launch_dependents();  // the copies' blocks may come in and wait
   pdl_wait();
   const int n_free = st.hdr[kHdrFree];
+  const bool known = state_ok(st, num_pages, page_size);
   const int words = (num_pages + 31) / 32;
   // the bitmap's first words, on their way while the rows are looked at
   uint4 first_words = make_uint4(0, 0, 0, 0);
@@ -283,6 +292,13 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
       len[u] = seq_lens[b];
       inc[u] = add[b];
     }
+  }
+  if (!known) {
+    if (tid == 0) {
+      flag_error(st.hdr, kErrState);
+      st.hdr[kHdrGrant] = st.hdr[kHdrMoves] = 0;
+    }
+    return;
   }
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
@@ -390,6 +406,13 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
     }
     rank0 += in_pass;
   }
+  if (rank0 < total) {  // the bitmap has fewer pages than the count of free ones
+    if (tid == 0) {
+      flag_error(st.hdr, kErrState);
+      st.hdr[kHdrGrant] = st.hdr[kHdrMoves] = 0;
+    }
+    return;
+  }
   __syncthreads();
   auto taken = [&](int r) { return r < kTakenShared ? s_taken[r] : st.taken[r]; };
 #pragma unroll
@@ -423,11 +446,15 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
 // ---- compact: one block pairs the held pages at or above n_used with the free
 // pages below it, both in ascending order
 __global__ void __launch_bounds__(kPlanThreads)
-k_pages_pair(PageState st, int num_pages) {
+k_pages_pair(PageState st, int num_pages, int page_size) {
   __shared__ int s_warp[32];
   const int tid = threadIdx.x;
   pdl_launch_dependents();  // the moving blocks may come in and wait
   pdl_wait();
+  if (!state_ok(st, num_pages, page_size)) {
+    if (tid == 0) flag_error(st.hdr, kErrState);
+    return;
+  }
   const int n_used = num_pages - st.hdr[kHdrFree];
   const int words = (num_pages + 31) / 32;
   const uint32_t call = (uint32_t)st.hdr[kHdrCalls] + 1;
@@ -508,9 +535,11 @@ __device__ __forceinline__ void move_units(const PageState& st, const MovePools&
 
 template <typename V>
 __global__ void __launch_bounds__(kMoveThreads)
-k_pages_copy_tails(PageState st, MovePools pools, int page_size, int64_t jobs_per_pool) {
+k_pages_copy_tails(PageState st, MovePools pools, int num_pages, int page_size,
+                   int64_t jobs_per_pool) {
   pdl_launch_dependents();
   pdl_wait();
+  if (!state_ok(st, num_pages, page_size)) return;
   move_units<V>(st, pools, page_size, false, jobs_per_pool);
 }
 
@@ -521,6 +550,7 @@ k_pages_move(PageState st, MovePools pools, const int32_t* __restrict__ seq_lens
              int page_size, int B, int max_pages, int64_t jobs_per_pool) {
   pdl_launch_dependents();
   pdl_wait();
+  if (!state_ok(st, num_pages, page_size)) return;
   const int n_used = st.hdr[kHdrUsed];
   const uint32_t call = (uint32_t)st.hdr[kHdrCalls];
   const int t0 = blockIdx.x * kMoveThreads + threadIdx.x, step = gridDim.x * kMoveThreads;
@@ -661,14 +691,14 @@ cudaError_t launch_pages_extend(const pks_pages_args& a, const PagesLayout& L, c
   auto kern = w == 16 ? k_pages_copy_tails<int4>
                       : w == 4 ? k_pages_copy_tails<int32_t> : k_pages_copy_tails<uint8_t>;
   return launch_ex(kern, grid, dim3(kMoveThreads), 0, s, /*pdl=*/true, /*coop=*/false, st, pools,
-                   a.page_size, jobs);
+                   a.num_pages, a.page_size, jobs);
 }
 
 cudaError_t launch_pages_compact(const pks_pages_args& a, const PagesLayout& L, int32_t* page_map,
                                  cudaStream_t s) {
   const PageState st = page_state(a.state, L);
   cudaError_t e = launch_ex(k_pages_pair, dim3(1), dim3(kPlanThreads), 0, s, /*pdl=*/true,
-                            /*coop=*/false, st, a.num_pages);
+                            /*coop=*/false, st, a.num_pages, a.page_size);
   if (e != cudaSuccess) return e;
   const int w = move_width(a);
   const int64_t jobs = move_jobs_per_pool(a, w);
