@@ -474,3 +474,25 @@ def test_another_current_device_is_refused(monkeypatch):
     for call in (att, att.plan, att.attend, b.attention):
         with pytest.raises(ValueError):
             call()
+
+
+@pytest.mark.parametrize("Nq,groups", [(1, True), (1, False), (5, True)])
+def test_attention_needs_a_plan_of_its_shapes(Nq, groups):
+    b = Batch([900, 1200], [0, 0], [768] * 2, Nq=Nq, seed=23, groups_passed=groups)
+    att = b.attention()
+    att.out.fill_(3.0)
+    att.attend()
+    torch.cuda.synchronize()
+    assert att.device_error() == 4 and bool((att.out == 3.0).all())
+    att.plan()
+    # a plan of the same buffers for other shapes
+    other = b.attention(causal=True)
+    other.args.workspace, other.args.workspace_bytes = (att.args.workspace,
+                                                        att.args.workspace_bytes)
+    other.out.fill_(3.0)
+    other.attend()
+    assert other.device_error() == 4 and bool((other.out == 3.0).all())
+    out = att.attend()
+    torch.cuda.synchronize()
+    assert att.device_error() == 0
+    b.check(out, att.lse)

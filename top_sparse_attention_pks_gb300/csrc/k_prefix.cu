@@ -81,7 +81,7 @@ struct Request {
 // plan header words
 constexpr int kErrWord = 0, kTicket = 1, kItems = 2, kUnits = 3, kSlots = 4, kTiles = 5,
               kShare = 6, kWideCtas = 7, kBig = 8, kPieces = 9, kSmall = 10, kClaim = 11,
-              kBigTiles = 12 /* 64 bits */, kDealtTiles = 14;
+              kBigTiles = 12 /* 64 bits */, kDealtTiles = 14, kTag = 15;
 
 struct PlanPtrs {
   int32_t* hdr;
@@ -102,6 +102,7 @@ struct PrefixShape {
   int wide_grid, narrow_grid;
   int box;         // rows of a TMA box (0: the page size has none)
   int hg;          // KV heads of a narrow CTA
+  int tag;         // of the shapes: a plan serves calls of the same shapes only
 };
 
 // 2^x with the hardware's approximate exponential (a few ulp in fp32)
@@ -143,7 +144,7 @@ constexpr int kPairNs = 1950, kSingleNs = 2000, kStreamNsPerKb = 24;
 // computes it, so that results do not depend on who does.
 struct Pieces {
   int64_t T, big_tiles;
-  int big, n, small, share;
+  int big, n, small, share, tag;
   __device__ __forceinline__ Pieces(const int32_t* hdr, int ngroups) {
     const int4 a = __ldcg(reinterpret_cast<const int4*>(hdr + kTiles - 1));
     const int4 b = __ldcg(reinterpret_cast<const int4*>(hdr + kBig));
@@ -153,7 +154,8 @@ struct Pieces {
     n = b.y;
     small = b.z;
     big_tiles = (int64_t)(uint32_t)c.x | (int64_t)c.y << 32;
-    share = c.z;
+    share = c.z;  // (kDealtTiles)
+    tag = c.w;    // (kTag)
   }
   __device__ __forceinline__ int64_t lo(int p) const {
     if (p < big) return (int64_t)p * share;
@@ -441,6 +443,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     pl.hdr[kItems] = n_items;
     pl.hdr[kSlots] = p_slots + s_total[10];
     pl.npre[B] = own_tiles;
+    pl.hdr[kTag] = sh.tag;
   }
 #pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads) pl.npre[b] = s_otile[b];
@@ -700,7 +703,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   Walk walk;
   {
     const Start st = pl.starts[cta];  // (one round trip with the header)
-    const int S = pl.hdr[kShare], W = pl.hdr[kWideCtas];
+    const int S = pl.hdr[kShare], W = pl.hdr[kWideCtas], tag = pl.hdr[kTag];
     const int64_t total = (int64_t)pl.hdr[kUnits] * sh.Hkv - (int64_t)cta * S;
     if (lane == 0) {  // (all warps write the same)
       s_sizes[0] = pl.hdr[kItems];
@@ -712,7 +715,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     walk.head = st.head;
     walk.item = st.item;
     walk.tile = st.tile;
-    walk.left = cta >= W ? 0 : (int)min((int64_t)S, total);
+    walk.left = cta >= W || tag != sh.tag ? 0 : (int)min((int64_t)S, total);
   }
   bool ok = true;
   // a wait of the whole warp
@@ -1398,7 +1401,7 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
   const int Treq = __ldcg(pl.hdr + kTiles);
   const int cta = blockIdx.x;
   for (int i = tid; i <= B; i += NT) s_pre[i] = __ldcg(pl.npre + i);
-  if (cta >= pieces.big && pieces.n == pieces.big) {
+  if (pieces.tag != sh.tag || (cta >= pieces.big && pieces.n == pieces.big)) {
     if (!wait_first) pdl_wait();
     return;
   }
@@ -1718,7 +1721,11 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   const int U = pl.hdr[kUnits], S = pl.hdr[kShare], slots_head = pl.hdr[kSlots];
   const int Treq = pl.hdr[kTiles];
   const Pieces pieces(pl.hdr, sh.Hkv / sh.hg);
-  if (row == 0 && lane == 0 && warp == 0) pl.hdr[kClaim] = 0;  // for the next call by this plan
+  const bool planned = pieces.tag == sh.tag;
+  if (row == 0 && lane == 0 && warp == 0) {
+    pl.hdr[kClaim] = 0;  // for the next call by this plan
+    if (!planned) flag_error(pl.hdr + kErrWord, kErrState);
+  }
 
   // candidate j of a run of wide items: CTA j % 2 of cut j / 2 (-1: there is none)
   auto wide_at = [&](int j, int unit, int slot, int rows, int nt, int x) -> int64_t {
@@ -1741,7 +1748,7 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
       n1 = 2 * (((rq.own + kTile - 1) / kTile + S - 1) / S);
     }
   }
-  const int n = n0 + n1;
+  const int n = planned ? n0 + n1 : 0;  // (a return above would hold the loads back)
   auto at = [&](int j) -> int64_t {
     if (j < n0) return wide_at(j, rq.gunit, rq.gslot, rq.grows, rq.gtiles, rq.row + r);
     j -= n0;
@@ -1850,7 +1857,7 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
     }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  if (row >= rows) return;
+  if (row >= rows || !planned) return;
   __nv_bfloat16* dst = out + row * D + lane * C;
 #pragma unroll
   for (int v = 0; v < V; v += C) {
@@ -1888,6 +1895,11 @@ PrefixShape prefix_shape(const pks_prefix_args& a) {
   if (sh.box > kTile) sh.box = kTile;
   if (sh.box < 8) sh.box = 0;
   sh.narrow_grid = device_sm_count() * (sh.hg >= 8 ? 1 : sh.hg == 4 ? 2 : 4);
+  uint32_t tag = 2166136261u;  // (FNV-1a, a word at a time)
+  for (int x : {sh.B, sh.Hq, sh.Hkv, sh.Nq, sh.D, sh.page_size, sh.max_pages, sh.num_pages,
+                sh.causal, a.prefix_group != nullptr ? 1 : 0})
+    tag = (tag ^ (uint32_t)x) * 16777619u;
+  sh.tag = (int)(tag | 1u);  // (never the zeroed workspace's)
   return sh;
 }
 
