@@ -426,7 +426,8 @@ pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_str
  * the leading table entries equal to the longest member's are the shared
  * part; the group's common prefix (the least among the members that share at
  * least half of what the second longest shares) takes part once for all of
- * these members, the rest of each request on its own.  Rows of a tile beyond
+ * these members when that is worth it (min_shared), the rest of each request on
+ * its own.  Rows of a tile beyond
  * a causal query's limit count with weight zero, so their V rows have to be
  * finite; rows at or beyond len_b are never read.  Calls that share a workspace
  * run one after another.
@@ -453,6 +454,9 @@ typedef struct pks_prefix_args {
   void* workspace;        /* device scratch owned by the caller, 256-byte aligned; its first
                              256 bytes zeroed once by the caller */
   size_t workspace_bytes;
+  int32_t min_shared;     /* take a prefix once when at least this many tokens are shared; 0:
+                             when it is expected to be faster than reading them as own */
+  int32_t reserved2;      /* must be 0 */
 } pks_prefix_args;
 
 /* Workspace bytes for these shapes (pointers may be NULL, but prefix_group
@@ -579,8 +583,8 @@ pks_status pks_pages_compact(const pks_pages_args* args, int32_t* page_map, pks_
  * synchronises the stream.  0: none; 1 page id out of range; 3 length, token
  * count or growth out of range; 4 a page lost more holders than it had;
  * or the state is not one that pks_pages_init filled for these pages (then the
- * call changed nothing); 6 out of pages; 7 row index out of range, repeated, not empty or both
- * source and destination. */
+ * call changed nothing); 6 out of pages; 7 row index out of range, repeated,
+ * not empty or both source and destination. */
 pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks_stream stream);
 
 /* ---- staging of a step's inputs and outputs --------------------------------

@@ -114,3 +114,12 @@ def test_workspace_size():
     a.B = 0  # an empty batch is no error and launches nothing
     pks.pks_prefix_plan(a)
     pks.pks_prefix_attention(a)
+
+
+def test_min_shared():
+    for change in (dict(min_shared=-1), dict(reserved2=1)):
+        a = args()
+        for k, v in change.items():
+            setattr(a, k, v)
+        for call in (pks.pks_prefix_workspace_size, pks.pks_prefix_plan, pks.pks_prefix_attention):
+            refused(-1, call, a)

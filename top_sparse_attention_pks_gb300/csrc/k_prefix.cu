@@ -49,10 +49,6 @@ constexpr int kItemRows = 256;    // query rows of an item: two MMAs
 constexpr int kNarrowRows = 16;
 constexpr int kNarrowTile = 16;
 constexpr int kMaxB = 4096;
-// Shared tokens below which a group is not worth a prefix item: one wide tile (64
-// tokens shared by three of five short requests: 22.7 us with the item, 18.6
-// without; 200 to 1500 by eight cost up to 12 us of 57 to 67, 6000 save 11 of 50).
-constexpr int kMinShared = kTile;
 
 struct Item {
   int row0;     // prefix item: first row in group order; own item: first row of the request
@@ -102,8 +98,26 @@ struct PrefixShape {
   int wide_grid, narrow_grid;
   int box;         // rows of a TMA box (0: the page size has none)
   int hg;          // KV heads of a narrow CTA
+  int min_shared;  // the caller's, or 0
   int tag;         // of the shapes: a plan serves calls of the same shapes only
 };
+
+// Unless the caller says from how many shared tokens on (min_shared): shared tokens
+// below which a group is not worth a prefix item, one wide tile; and, where the
+// narrow kernel would read them as own tokens, the bytes of K and V that all groups
+// have to save together, for the wide kernel beside it, its partials and the split
+// of the SMs cost as much as reading those, the more the more requests there are.
+// Rows that come one by one cost three times as much.  Measured (us a pass, shared /
+// each its own, and the megabytes saved): 32 requests in groups of eight with 600
+// tokens 67 / 57, 69; with 1000 73 / 64, 115; with 1500 69 / 67, 172; 64 in one with
+// 500 90 / 80, 129; 8 in one with 3000 43.5 / 42, 86, with 6000 38 / 50, 172; 4 with
+// 6000 35 / 38, 74; pages of 17, 4 in pairs 76 / 84, 61, 40 in groups of 25 33 / 39,
+// 78.
+constexpr int kMinShared = kTile;
+__device__ __forceinline__ int64_t least_saved(const PrefixShape& sh) {
+  const int64_t boxes = min(200000000, 40000000 + 3500000 * min(sh.B, 100));
+  return sh.box ? boxes : boxes / 3;
+}
 
 // 2^x with the hardware's approximate exponential (a few ulp in fp32)
 __device__ __forceinline__ float ex2(float x) {
@@ -192,7 +206,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
               const int32_t* __restrict__ prefix_group, PlanPtrs pl, PrefixShape sh) {
   extern __shared__ int s_dyn[];  // [kPlanArrays][B]
   __shared__ int s_total[3 + 8];  // tiles, those with one row block, narrow tiles; the scans'
-  __shared__ int s_last, s_equal[kPlanThreads / 32];
+  __shared__ int s_last, s_saved, s_equal[kPlanThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, B = sh.B;
   const int max_len = sh.max_pages * sh.page_size;
   const bool alone = gridDim.x == 1;
@@ -309,6 +323,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     s_cnt[b] = s_most[b] = 0;
   }
   if (tid < 3) s_total[tid] = 0;
+  if (tid == 0) s_saved = 0;
   __syncthreads();
   // The groups' common prefixes: the least shared length among the members that
   // share at least half of what the second longest shares; members with less
@@ -320,7 +335,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 #pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads) {
     const int f = s_first[b], e = s_eq[b], most = s_most[f];
-    if (most >= kMinShared && e >= (most + 1) / 2) {
+    if (most >= (sh.min_shared ? sh.min_shared : kMinShared) && e >= (most + 1) / 2) {
       atomicMin(&s_pre[f], e);
       atomicAdd(&s_cnt[f], 1);
     }
@@ -329,15 +344,23 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   auto tiles = [](int n) { return (n + kTile - 1) / kTile; };
   auto blocks = [](int rows) { return (rows + kItemRows - 1) / kItemRows; };
   auto single = [](int rows) { return (rows - 1) % kItemRows < kRows ? 1 : 0; };
+  bool share = true;
+  if (sh.narrow && !sh.min_shared) {
+#pragma unroll 1
+    for (int b = tid; b < B; b += kPlanThreads)  // (in tiles: 2^27 at most)
+      if (s_cnt[b] >= 2) atomicAdd(&s_saved, (s_cnt[b] - 1) * tiles(s_pre[b]));
+    __syncthreads();
+    share = (int64_t)s_saved * sh.Hkv * (kTile * 4 * sh.D) >= least_saved(sh);
+  }
   // the group (by its first member) that request b takes part in, or -1
   auto joined = [&](int b) {
     const int f = s_first[b];
-    return s_cnt[f] >= 2 && s_eq[b] >= s_pre[f] ? f : -1;
+    return share && s_cnt[f] >= 2 && s_eq[b] >= s_pre[f] ? f : -1;
   };
   const int own_blocks = sh.narrow ? 0 : blocks(sh.R);
 #pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads) {
-    const bool has = s_cnt[b] >= 2;
+    const bool has = share && s_cnt[b] >= 2;
     const int rows = s_cnt[b] * sh.R, nt = has ? tiles(s_pre[b]) : 0;
     const int f = joined(b), begin = f >= 0 ? s_pre[f] : 0, own = s_len[b] - begin;
     s_at[b] = has ? s_cnt[b] : 0;
@@ -379,7 +402,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   auto cuts = [&](int nt) { return (int)((unsigned)(nt + S - 1) / (unsigned)S); };
 #pragma unroll 1
   for (int b = tid; b < B; b += kPlanThreads) {
-    const bool has = s_cnt[b] >= 2;
+    const bool has = share && s_cnt[b] >= 2;
     const int rows = s_cnt[b] * sh.R, c = has ? cuts(tiles(s_pre[b])) : 0;
     const int f = joined(b), oc = own_blocks ? cuts(tiles(s_len[b] - (f >= 0 ? s_pre[f] : 0))) : 0;
     s_item[b] = c * blocks(rows);
@@ -1888,6 +1911,7 @@ PrefixShape prefix_shape(const pks_prefix_args& a) {
   sh.max_pages = a.max_pages;
   sh.num_pages = a.num_pages;
   sh.causal = a.causal;
+  sh.min_shared = a.min_shared;
   sh.narrow = sh.R <= kNarrowRows;
   sh.hg = attn_heads_per_cta(a.Hkv);
   sh.wide_grid = device_sm_count();

@@ -704,8 +704,8 @@ pks_status prefix_check(const pks_prefix_args* a) {
   if (!a) return PKS_ERR_INVALID;
   if (a->B < 0 || a->Hq < 1 || a->Hkv < 1 || a->D < 1 || a->page_size < 1 || a->max_pages < 1 ||
       a->num_pages < 1 || a->n_queries < 0 || a->causal < 0 || a->causal > 1 ||
-      a->wait_limit < 0 || a->reserved != 0 || !(a->sm_scale >= 0.f) ||
-      std::isinf(a->sm_scale) || a->Hq % a->Hkv != 0)
+      a->wait_limit < 0 || a->reserved != 0 || a->min_shared < 0 || a->reserved2 != 0 ||
+      !(a->sm_scale >= 0.f) || std::isinf(a->sm_scale) || a->Hq % a->Hkv != 0)
     return PKS_ERR_INVALID;
   if (a->D != 64 && a->D != 128) return PKS_ERR_UNSUPPORTED;
   if (a->Hq / a->Hkv > 16 || a->Hq > 4096 || a->n_queries > pks::kPrefixMaxQueries)

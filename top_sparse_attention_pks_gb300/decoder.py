@@ -256,7 +256,8 @@ class PrefixAttention:
     take part once for all requests of its group.  q [B, Hq, D] or
     [B, Nq, Hq, D] (query tokens at the end of each request, ``causal`` among
     themselves), kv_k / kv_v [num_pages, P, Hkv, D] (bf16), prefix_group [B]
-    (int32, negative: none) or None.  Owns ``out``, ``lse`` (when asked for) and
+    (int32, negative: none) or None, min_shared: tokens from which on a prefix is
+    taken once (0: when that is expected to be faster).  Owns ``out``, ``lse`` (when asked for) and
     the workspace.
 
     Calling the object plans and attends.  ``plan`` alone is needed whenever
@@ -266,14 +267,14 @@ class PrefixAttention:
 
     def __init__(self, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
                  causal: bool = False, sm_scale: float = 0.0, lse: bool = False,
-                 wait_limit: int = 0):
+                 wait_limit: int = 0, min_shared: int = 0):
         pks._on_current_device(seq_lens, block_table, q, kv_k, kv_v, prefix_group)
         dev = q.device
         self.out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
         kw = dict(seq_lens=seq_lens, block_table=block_table, q=q, kv_k=kv_k, kv_v=kv_v,
                   prefix_group=prefix_group, causal=causal, sm_scale=sm_scale, out=self.out,
-                  lse=self.lse, wait_limit=wait_limit)
+                  lse=self.lse, wait_limit=wait_limit, min_shared=min_shared)
         nbytes = pks.pks_prefix_workspace_size(pks.make_prefix_args(**kw))
         self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
         self.workspace[:256].zero_()

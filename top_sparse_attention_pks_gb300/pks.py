@@ -77,6 +77,7 @@ class pks_prefix_args(ctypes.Structure):
         ("prefix_group", ctypes.c_void_p), ("q", ctypes.c_void_p), ("kv_k", ctypes.c_void_p),
         ("kv_v", ctypes.c_void_p), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
         ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("min_shared", ctypes.c_int32), ("reserved2", ctypes.c_int32),
     ]
 
 
@@ -661,7 +662,7 @@ def pks_mla_device_error(args: pks_mla_args, stream=None) -> int:
 def make_prefix_args(*, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
                      causal: bool = False, sm_scale: float = 0.0, out=None, lse=None,
                      workspace=None, num_pages: Optional[int] = None,
-                     wait_limit: int = 0) -> pks_prefix_args:
+                     wait_limit: int = 0, min_shared: int = 0) -> pks_prefix_args:
     """Fill a ``pks_prefix_args``: q [B, Hq, D] or [B, Nq, Hq, D] (``out`` alike,
     ``lse`` without the last dimension), kv_k / kv_v [num_pages, page_size, Hkv, D],
     prefix_group [B] or None."""
@@ -690,6 +691,7 @@ def make_prefix_args(*, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
     a.causal = 1 if causal else 0
     a.sm_scale = float(sm_scale)
     a.wait_limit = int(wait_limit)
+    a.min_shared = int(min_shared)
     a.seq_lens = _dptr(seq_lens, torch.int32, "seq_lens")
     a.block_table = _dptr(block_table, torch.int32, "block_table")
     a.prefix_group = _dptr(prefix_group, torch.int32, "prefix_group")
