@@ -433,8 +433,8 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
     const int per_sm = sh.narrow_grid / sh.wide_grid;
     int64_t big = (int64_t)sms_left * per_sm, big_tiles = T;
     if (beside) {
-      const float all_ns = pairs_ns + narrow_ns + (float)singles * (stage_kb * kTile / kNarrowTile) *
-                                                      kStreamNsPerKb;
+      const float all_ns = pairs_ns + narrow_ns +
+                           (float)singles * (stage_kb * kTile / kNarrowTile) * kStreamNsPerKb;
       const float tile_ns = sh.hg * stage_kb * kStreamNsPerKb * per_sm;
       big_tiles = min(T, big * (int64_t)(all_ns / sh.wide_grid * (kDealt / 16.f) / tile_ns));
     }
@@ -558,8 +558,9 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 //   warps 14, 15     load Q, a piece ahead where it fits, and tell the others
 // An item with more than 128 rows gives each group a row block of its own and
 // every tile goes to both; with 128 or fewer both groups hold the same rows and
-// take the tiles in turn, so that one group's softmax always runs beside the
-// other's products.  Per job (a tile of a group):
+// take the tiles in turn, through all pieces (6 requests over prefixes of 7,000
+// tokens: 33 us, 37 when group 0 began every piece), so that one group's softmax
+// always runs beside the other's products.  Per job (a tile of a group):
 //   S[128 x 128] = Q K^T        tcgen05.mma, fp32 in tensor memory
 //   P            = 2^(S c - m)  a thread a row, bf16 into S's columns
 //   O[128 x D]  += P V          tcgen05.mma, P from tensor memory, in two halves
@@ -611,6 +612,7 @@ struct Piece {
   int head, t_lo, nt;   // first tile and tiles
   bool pair;            // two row blocks
   int jobs0, jobs1;     // jobs of the softmax groups
+  int turn;             // the group that begins
   int64_t slot;         // its first partial row
 };
 // What the issuers and the softmax need of a piece.
@@ -619,7 +621,7 @@ struct Note {
   int nrows, row0, own;  // of its item
   int tok0, tok1;        // its first token, the item's last + 1
   int q_block;           // ring block of Q (of group 0 when there are two)
-  int pair, last;
+  int pair, turn, last;
   int64_t slot;
 };
 // A CTA's walk over its tiles, by the loads' warps.
@@ -627,6 +629,7 @@ struct Walk {
   const Item* items;
   int left;             // tiles to come
   int head, item, tile; // the next one
+  int turn;             // the group whose job comes next
   const int* sizes;     // items and partial rows of a head (shared memory)
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ Piece next() {
@@ -636,8 +639,10 @@ struct Walk {
     p.t_lo = tile;
     p.nt = min(left, (p.it.t1 - p.it.t0 + kTile - 1) / kTile - tile);
     p.pair = p.it.nrows > kRows;
-    p.jobs1 = p.pair ? p.nt : p.nt / 2;
-    p.jobs0 = p.pair ? p.nt : p.nt - p.jobs1;
+    p.turn = turn;
+    p.jobs0 = p.pair ? p.nt : (p.nt + 1 - turn) / 2;
+    p.jobs1 = p.pair ? p.nt : (p.nt + turn) / 2;
+    if (!p.pair) turn ^= p.nt & 1;
     p.slot = (int64_t)head * sizes[1] + p.it.slot0 + (int64_t)kItemRows * blockIdx.x;
     left -= p.nt;
     tile = 0;
@@ -738,6 +743,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     walk.head = st.head;
     walk.item = st.item;
     walk.tile = st.tile;
+    walk.turn = 0;
     walk.left = cta >= W || tag != sh.tag ? 0 : (int)min((int64_t)S, total);
   }
   bool ok = true;
@@ -790,7 +796,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         ++n_job;
         tc::fence_after();
         if (!idle) {
-          const int nv = limit - (pc.pair ? i : 2 * i + g) * kTile;  // valid columns
+          const int nv = limit - (pc.pair ? i : 2 * i + (g ^ pc.turn)) * kTile;  // valid columns
           uint32_t s0[32], s1[32], s2[32], s3[32];
           tc::tmem_ld32(tS, s0);
           tc::tmem_ld32(tS + 32, s1);
@@ -891,7 +897,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       ++n_piece;
       tc::fence_after();
       float* dst = part_o + row * D;
-      if (pc.pair || pc.jobs1 == 0) {
+      if (pc.pair || pc.nt == 1) {
         if (mine) part_ml[row] = make_float2(m_run, l_run);
         if (!idle) {
 #pragma unroll 1
@@ -979,7 +985,6 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       const int g = warp - kMmaWarp;
       const uint32_t tS = tmem + kTmemS + g * kTile, tO = tmem + g * 128;
       uint32_t n_slot = 0, n_job = 0, n_note = 0, n_turn = 0, ph_tma = 0, ph_cp = 0;
-      bool owed = false;
       for (bool more_pieces = walk.more(); more_pieces && ok;) {
         Note pc;
         if (!(ok = read_note(n_note++, pc))) break;
@@ -1039,7 +1044,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           }
           return true;
         };
-        const int step = pc.pair ? 1 : 2, t0 = pc.pair ? 0 : g;
+        const int step = pc.pair ? 1 : 2, t0 = pc.pair ? 0 : g ^ pc.turn;
         if (my_jobs > 0) {
           if (t0 == 1) ok = skip(0);
           if (ok && (ok = landed(t0, 0))) issue_s(t0, my_jobs == 1, nullptr);
@@ -1047,7 +1052,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           ok = skip(0);
         }
         for (int i = 0; i < my_jobs && ok; ++i, ++n_job) {
-          const int t = t0 + i * step, job = 2 * i + g;
+          const int t = t0 + i * step;
           if (!(ok = landed(t, 1))) break;
           const uint32_t sl = (n_slot + 2 * t + 1) % W::kSlotsN;
           const uint64_t dv = tc::desc_sw128(sKV + sl * W::kTileBytes, 1024, W::kGroupBytes);
@@ -1056,9 +1061,9 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           const int tn = t + step;
           const bool early = more && step == 1 && ready(tn, by_tma);
           if (early && !(ok = landed(tn, 0))) break;
-          // after the other group's products of the job before (at the start of a
-          // piece: of the piece before, when its last job was group 1's)
-          if (job > 0 || owed) {
+          // after the other group's products of the job before: the groups take
+          // turns through all pieces, group 0 begins
+          if (g == 1 || n_job > 0) {
             if (!(ok = wait(&bar_turn[g], n_turn & 1))) break;
             ++n_turn;
           }
@@ -1081,11 +1086,10 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           }
           if (!ok) break;
           // then the next S, and the turn: before S when that has to wait for K
-          const bool pass = g == 1 || job + 1 < pc.jobs0 + pc.jobs1;
           if (early) {
-            issue_s(tn, i + 2 == my_jobs, pass ? &bar_turn[1 - g] : nullptr);
+            issue_s(tn, i + 2 == my_jobs, &bar_turn[1 - g]);
           } else {
-            if (pass && tc::elect_one()) tc::mbar_arrive(&bar_turn[1 - g]);
+            if (tc::elect_one()) tc::mbar_arrive(&bar_turn[1 - g]);
             __syncwarp();
             if (more) {
               if (step == 2) ok = skip(t + 1);
@@ -1097,7 +1101,6 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         // tiles behind the group's last one
         if (ok && my_jobs > 0 && t0 + my_jobs * step - step + 1 < pc.nt)
           ok = skip(pc.nt - 1);
-        owed = (pc.jobs0 + pc.jobs1) % 2 == 0;
         n_slot += 2 * pc.nt;
       }
       if (!ok && tc::elect_one()) {
@@ -1182,6 +1185,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
             note.tok1 = pc.it.t1;
             note.q_block = q_block;
             note.pair = pc.pair;
+            note.turn = pc.turn;
             note.last = !walk.more();
             note.slot = pc.slot;
             s_note[nn] = note;
