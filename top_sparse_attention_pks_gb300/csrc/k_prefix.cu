@@ -670,8 +670,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
 k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
               const __nv_bfloat16* __restrict__ kv_k, const __nv_bfloat16* __restrict__ kv_v,
               PlanPtrs pl, float2* __restrict__ part_ml, float* __restrict__ part_o,
-              PrefixShape sh, float scale_log2, long long budget,
-              const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+              PrefixShape sh, float scale_log2, long long wait_cycles,
+              const __grid_constant__ CUtensorMap map_k,
+              const __grid_constant__ CUtensorMap map_v) {
   using W = Wide<D>;
   extern __shared__ uint8_t smem_raw[];
   // bar_tma / bar_cp: a ring slot has landed, by either way of loading; bar_go: it
@@ -749,7 +750,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   bool ok = true;
   // a wait of the whole warp
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, budget)) != 0;
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, wait_cycles)) != 0;
   };
   // tiles of a piece that come by TMA: those before the range's end, in pages of
   // whole boxes, from a start that keeps every box in one page
@@ -1382,8 +1383,9 @@ __global__ void __launch_bounds__((HG * WPH + 1) * 32, Narrow<D, HG>::kPerSm)
 k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __restrict__ q,
                 const __nv_bfloat16* __restrict__ kv_k, const __nv_bfloat16* __restrict__ kv_v,
                 PlanPtrs pl, float2* __restrict__ part_ml, float* __restrict__ part_o,
-                PrefixShape sh, float scale_log2, int wait_first, long long budget,
-                const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v) {
+                PrefixShape sh, float scale_log2, int wait_first, long long wait_cycles,
+                const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v) {
   using N = Narrow<D, HG>;
   constexpr int NT = (HG * WPH + 1) * 32, KS = D / 16, MT = D / 16, TILE = kNarrowTile;
   static_assert(N::kStages < kTileRing, "a description outlives its stage");
@@ -1435,7 +1437,7 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
   __syncthreads();
   bool ok = true;
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, budget)) != 0;
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, wait_cycles)) != 0;
   };
 
   if (warp == HG * WPH) {
@@ -1672,7 +1674,8 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
         }
       }
       // rounded to bf16 for the second product only
-      const uint32_t pb0 = movmatrix_t(pack_bf16(p[0], p[1])), pb1 = movmatrix_t(pack_bf16(p[2], p[3]));
+      const uint32_t pb0 = movmatrix_t(pack_bf16(p[0], p[1]));
+      const uint32_t pb1 = movmatrix_t(pack_bf16(p[2], p[3]));
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         const int r = lane & 7, h = lane >> 4, c = 2 * mt + ((lane >> 3) & 1);

@@ -94,13 +94,13 @@ __device__ __forceinline__ bool mbar_test_wait(uint64_t* bar, uint32_t parity) {
 }
 // bounded wait for the phase with the given parity; false when it gave up or
 // when another warp of the CTA has given up (*abort set).  The first test does
-// not block, so that a tiny budget gives up on anything not ready yet.
+// not block, so that a tiny limit gives up on anything not ready yet.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity,
-                                          const volatile int* abort, long long budget) {
+                                          const volatile int* abort, long long wait_cycles) {
   if (mbar_test_wait(bar, parity)) return true;
   const long long t0 = clock64();
   do {
-    if (*abort || clock64() - t0 > budget) return false;
+    if (*abort || clock64() - t0 > wait_cycles) return false;
   } while (!mbar_try_wait(bar, parity));
   return true;
 }
