@@ -584,7 +584,8 @@ pks_status pks_pages_compact(const pks_pages_args* args, int32_t* page_map, pks_
  * count or growth out of range; 4 a page lost more holders than it had;
  * or the state is not one that pks_pages_init filled for these pages (then the
  * call changed nothing); 6 out of pages; 7 row index out of range, repeated,
- * not empty or both source and destination. */
+ * not empty or both source and destination.  Of several errors since the word
+ * was last read one is kept. */
 pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks_stream stream);
 
 /* ---- staging of a step's inputs and outputs --------------------------------

@@ -343,7 +343,7 @@ def test_table_feeds_the_decode_step():
     assert step.device_error() == 0 and pages.device_error() == 0
 
 
-def test_tensors_elsewhere_are_refused(monkeypatch):
+def test_arguments_elsewhere_are_refused(monkeypatch):
     """Arguments on the host, and calls while another device is the current one."""
     lens, table = dev([20, 0, 0]), dev([[0, 1, -1], [-1] * 3, [-1] * 3])
     pages = PageTable(lens, table, 6, 16)
