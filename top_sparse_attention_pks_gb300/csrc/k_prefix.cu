@@ -591,7 +591,6 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
 constexpr int kWideThreads = 512;
 constexpr int kMmaWarp = 8, kLoadWarp = 10, kLoadWarps = 4, kQWarp = 14;
 constexpr int kNotes = 4;  // pieces announced at a time, at most
-constexpr long long kDrainCycles = 20000000LL;   // about 10 ms
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
 
 template <int D>
@@ -623,6 +622,12 @@ struct Note {
   int q_block;           // ring block of Q (of group 0 when there are two)
   int pair, turn, last;
   int64_t slot;
+};
+// What a loading warp has put into the ring's slots: the number of its half tiles
+// (K or V; slot by slot in turn), and by slot whether the last came by TMA, whether
+// any did, and the number of those modulo two.
+struct Fills {
+  uint32_t n, by_tma, used, count;
 };
 // A CTA's walk over its tiles, by the loads' warps.
 struct Walk {
@@ -682,11 +687,13 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   // bar_s[g]: S of group g's job; bar_p[g][h]: half h of its P is written;
   // bar_turn[g]: the other issuer has issued its job's P.V and next S; bar_o[g]:
   // every product of the group's piece; bar_x[g] / bar_y[g]: the group's maxima
-  // are posted / it has read the other's O; bar_drain[g]: on giving up
+  // are posted / it has read the other's O; bar_drain[g]: every product of the
+  // group, at its issuer's end
   __shared__ __align__(8) uint64_t bar_tma[W::kSlotsN], bar_cp[W::kSlotsN], bar_go[W::kSlotsN],
       bar_free[W::kSlotsN], bar_note[kNotes], bar_noted[kNotes], bar_qfree[2], bar_s[2],
       bar_p[2][2], bar_turn[2], bar_o[2], bar_x[2], bar_y[2], bar_drain[2];
   __shared__ float2 s_ml[kRows];  // a row's maximum and sum, group 1's and then group 0's
+  __shared__ Fills s_fills[TMA_WARPS];
   __shared__ Note s_note[kNotes];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort, s_sizes[2];
@@ -986,6 +993,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       const int g = warp - kMmaWarp;
       const uint32_t tS = tmem + kTmemS + g * kTile, tO = tmem + g * 128;
       uint32_t n_slot = 0, n_job = 0, n_note = 0, n_turn = 0, ph_tma = 0, ph_cp = 0;
+      bool issued = false;  // any product (every one comes behind an S)
       for (bool more_pieces = walk.more(); more_pieces && ok;) {
         Note pc;
         if (!(ok = read_note(n_note++, pc))) break;
@@ -1017,6 +1025,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         // (the turn passes with four of S's steps to go: the other issuer's first
         // product then queues behind them without a gap)
         auto issue_s = [&](int t, bool last, uint64_t* pass) {
+          issued = true;
           tc::fence_after();
           if (tc::elect_one()) {
             const uint32_t sl = (n_slot + 2 * t) % W::kSlotsN;
@@ -1104,13 +1113,18 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           ok = skip(pc.nt - 1);
         n_slot += 2 * pc.nt;
       }
-      if (!ok && tc::elect_one()) {
-        flag_error(pl.hdr + kErrWord, kErrTimeout);
-        s_abort = 1;
-        // nothing may be in flight when the tensor memory is freed
-        tc::mma_commit(&bar_drain[g]);
-        const long long t0 = clock64();
-        while (!tc::mbar_try_wait(&bar_drain[g], 0) && clock64() - t0 < kWaitCycles) {
+      if (tc::elect_one()) {
+        if (!ok) {
+          flag_error(pl.hdr + kErrWord, kErrTimeout);
+          s_abort = 1;
+        }
+        // every product that this thread issued is done before the tensor memory is
+        // freed, also when another warp gave up (else they are done already)
+        if (issued) {
+          tc::mma_commit(&bar_drain[g]);
+          const long long t0 = clock64();
+          while (!tc::mbar_try_wait(&bar_drain[g], 0) && clock64() - t0 < kWaitCycles) {
+          }
         }
       }
       __syncwarp();
@@ -1217,7 +1231,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
         };
         uint32_t n_slot = 0;
         uint32_t ph_go = 0;
-        uint32_t tma_used = 0, tma_count = 0;  // by slot: any TMA copy, their number modulo two
+        Fills fills = {};  // (its number of half tiles: n_slot, until the end)
         int row = 0;
         if (walk.more()) {
           const Item first = pl.starts[cta].it;
@@ -1265,14 +1279,16 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
               const uint32_t tile = sKV + s * W::kTileBytes;
               if (t < by_tma) {
                 if (lw >= TMA_WARPS) continue;
-                tma_used |= 1u << s;
-                tma_count ^= 1u << s;
+                fills.by_tma |= 1u << s;
+                fills.used |= 1u << s;
+                fills.count ^= 1u << s;
                 if (lane == 0) tc::mbar_arrive_expect(&bar_tma[s], W::kTileBytes / TMA_WARPS);
                 __syncwarp();
                 if (lane < n_box)
                   tc::tma_load_5d(tile + my_box * (sh.box / 8) * W::kGroupBytes,
                                   v ? &map_v : &map_k, 0, 0, 0, row / 8, pc.head, &bar_tma[s]);
               } else {
+                fills.by_tma &= ~(1u << s);
                 const __nv_bfloat16* pool = (v ? kv_v : kv_k) + pc.head * D + cc * 8;
 #pragma unroll 8
                 for (int r = 0; r < 32; r += kRowsPer) {
@@ -1299,15 +1315,29 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           flag_error(pl.hdr + kErrWord, kErrTimeout);
           s_abort = 1;
         }
-        // the TMA copies in flight land before the shared memory is given up (in
-        // the normal course every one has been waited for; a slot that not all of
-        // the warps filled stays open, so its copies get a limited time)
-        if (!ok && lane == 0) {
+        // The TMA copies land before the shared memory is given up, whoever gave up
+        // (else they have landed already).  A slot's barrier counts an arrival of
+        // every warp: what the furthest has filled and this one has not (less than
+        // once around the ring, as a slot is filled again only behind products with
+        // its last contents) gets this warp's arrival without any copy.
+        if (lw < TMA_WARPS) {
+          fills.n = n_slot;
+          if (TMA_WARPS > 1) {
+            if (lane == 0) s_fills[lw] = fills;
+            asm volatile("bar.sync 1, %0;\n" ::"n"(TMA_WARPS * 32) : "memory");
+            const uint32_t mine = fills.n;
+#pragma unroll
+            for (int w = 0; w < TMA_WARPS; ++w)
+              if (s_fills[w].n > fills.n) fills = s_fills[w];
+            for (uint32_t n = mine; n < fills.n; ++n)
+              if (lane == 0 && ((fills.by_tma >> (n % W::kSlotsN)) & 1))
+                tc::mbar_arrive(&bar_tma[n % W::kSlotsN]);
+          }
           const long long t0 = clock64();
           for (int i = 0; i < W::kSlotsN; ++i)
-            while (((tma_used >> i) & 1) &&
-                   !tc::mbar_try_wait(&bar_tma[i], (~tma_count >> i) & 1) &&
-                   clock64() - t0 < kDrainCycles) {
+            while (((fills.used >> i) & 1) &&
+                   !tc::mbar_try_wait(&bar_tma[i], (~fills.count >> i) & 1) &&
+                   clock64() - t0 < kWaitCycles) {
             }
         }
         __syncwarp();
