@@ -688,7 +688,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   // bar_turn[g]: the other issuer has issued its job's P.V and next S; bar_o[g]:
   // every product of the group's piece; bar_x[g] / bar_y[g]: the group's maxima
   // are posted / it has read the other's O; bar_drain[g]: every product of the
-  // group, at its issuer's end
+  // group, when a warp has given up
   __shared__ __align__(8) uint64_t bar_tma[W::kSlotsN], bar_cp[W::kSlotsN], bar_go[W::kSlotsN],
       bar_free[W::kSlotsN], bar_note[kNotes], bar_noted[kNotes], bar_qfree[2], bar_s[2],
       bar_p[2][2], bar_turn[2], bar_o[2], bar_x[2], bar_y[2], bar_drain[2];
@@ -774,6 +774,20 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&bar_noted[n % kNotes]);
     return true;
+  };
+
+  // The end of a warp's role: whether any warp has given up.  In the normal course
+  // every copy and product has been waited for by then; else those that a warp has
+  // left in flight end before the memory that they write is given up.
+  auto gave_up = [&]() -> bool {
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;\n" ::"n"(kWideThreads) : "memory");
+    return s_abort != 0;
+  };
+  auto land = [&](uint64_t* bar, uint32_t parity) {
+    const long long t0 = clock64();
+    while (!tc::mbar_try_wait(bar, parity) && clock64() - t0 < kWaitCycles) {
+    }
   };
 
   // Every role keeps its own count of the phases.
@@ -986,6 +1000,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
       flag_error(pl.hdr + kErrWord, kErrTimeout);
       s_abort = 1;
     }
+    gave_up();
   } else {
     tc::setmaxnreg_dec<kOtherRegs>();
     if (warp < kLoadWarp) {
@@ -1113,19 +1128,13 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           ok = skip(pc.nt - 1);
         n_slot += 2 * pc.nt;
       }
-      if (tc::elect_one()) {
-        if (!ok) {
-          flag_error(pl.hdr + kErrWord, kErrTimeout);
-          s_abort = 1;
-        }
-        // every product that this thread issued is done before the tensor memory is
-        // freed, also when another warp gave up (else they are done already)
-        if (issued) {
-          tc::mma_commit(&bar_drain[g]);
-          const long long t0 = clock64();
-          while (!tc::mbar_try_wait(&bar_drain[g], 0) && clock64() - t0 < kWaitCycles) {
-          }
-        }
+      if (!ok && tc::elect_one()) {
+        flag_error(pl.hdr + kErrWord, kErrTimeout);
+        s_abort = 1;
+      }
+      if (gave_up() && issued && tc::elect_one()) {
+        tc::mma_commit(&bar_drain[g]);
+        land(&bar_drain[g], 0);
       }
       __syncwarp();
     } else {
@@ -1214,6 +1223,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           s_abort = 1;
         }
         tc::cp_async_wait<0>();
+        gave_up();
       } else {
         // first row of this lane's box of an item's tile, when it comes by TMA (a bad
         // page gives zeros, from beyond the pool)
@@ -1315,30 +1325,22 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
           flag_error(pl.hdr + kErrWord, kErrTimeout);
           s_abort = 1;
         }
-        // The TMA copies land before the shared memory is given up, whoever gave up
-        // (else they have landed already).  A slot's barrier counts an arrival of
-        // every warp: what the furthest has filled and this one has not (less than
-        // once around the ring, as a slot is filled again only behind products with
-        // its last contents) gets this warp's arrival without any copy.
-        if (lw < TMA_WARPS) {
+        if (gave_up() && lw < TMA_WARPS) {
+          // A slot's barrier counts an arrival of every warp: what the furthest has
+          // filled and this one has not (once around the ring at most, as a slot is
+          // filled again only behind products with its last contents) gets this
+          // warp's arrival without any copy.
           fills.n = n_slot;
-          if (TMA_WARPS > 1) {
-            if (lane == 0) s_fills[lw] = fills;
-            asm volatile("bar.sync 1, %0;\n" ::"n"(TMA_WARPS * 32) : "memory");
-            const uint32_t mine = fills.n;
+          if (lane == 0) s_fills[lw] = fills;
+          asm volatile("bar.sync 2, %0;\n" ::"n"(TMA_WARPS * 32) : "memory");
 #pragma unroll
-            for (int w = 0; w < TMA_WARPS; ++w)
-              if (s_fills[w].n > fills.n) fills = s_fills[w];
-            for (uint32_t n = mine; n < fills.n; ++n)
-              if (lane == 0 && ((fills.by_tma >> (n % W::kSlotsN)) & 1))
-                tc::mbar_arrive(&bar_tma[n % W::kSlotsN]);
-          }
-          const long long t0 = clock64();
+          for (int w = 0; w < TMA_WARPS; ++w)
+            if (s_fills[w].n > fills.n) fills = s_fills[w];
+          for (uint32_t n = n_slot; n < fills.n; ++n)
+            if (lane == 0 && ((fills.by_tma >> (n % W::kSlotsN)) & 1))
+              tc::mbar_arrive(&bar_tma[n % W::kSlotsN]);
           for (int i = 0; i < W::kSlotsN; ++i)
-            while (((fills.used >> i) & 1) &&
-                   !tc::mbar_try_wait(&bar_tma[i], (~fills.count >> i) & 1) &&
-                   clock64() - t0 < kWaitCycles) {
-            }
+            if ((fills.used >> i) & 1) land(&bar_tma[i], (~fills.count >> i) & 1);
         }
         __syncwarp();
       }
