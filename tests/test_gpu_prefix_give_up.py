@@ -50,3 +50,23 @@ def test_wide(page, D, Nq, tokens):
     b = Batch(lens, [0] * len(lens), [tokens] * len(lens), page=page, Hkv=2, G=8, D=D, Nq=Nq,
               seed=page + D + tokens)
     give_up(b, causal=True, min_shared=128)
+
+
+@pytest.mark.parametrize("page", [1, 16, 64])  # row by row, by boxes
+@pytest.mark.parametrize("D,Hkv,G,Nq",
+                         [(64, 1, 4, 1), (128, 8, 4, 3), (128, 4, 8, 1), (64, 3, 5, 2)])
+@pytest.mark.parametrize("tokens", [32, 30000])  # two tiles a CTA: its ring is never full; more
+def test_narrow(page, D, Hkv, G, Nq, tokens):
+    """Own tokens of up to 16 rows, no groups: the narrow kernel alone."""
+    lens = [tokens, tokens - 7, 1, 0, 90]
+    b = Batch(lens, [-1] * 5, [0] * 5, page=page, Hkv=Hkv, G=G, D=D, Nq=Nq, seed=page + Hkv,
+              groups_passed=False)
+    give_up(b, causal=Nq > 1)
+
+
+@pytest.mark.parametrize("page", [5, 16, 128])
+def test_both(page):
+    """Prefixes by the wide kernel and own tokens by the narrow one beside it."""
+    lens = [2000 + 150 * i for i in range(8)]
+    b = Batch(lens, [0] * 8, [1920] * 8, page=page, Hkv=4, G=4, D=128, Nq=2, seed=page)
+    give_up(b, causal=True, min_shared=128)

@@ -1472,6 +1472,7 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, wait_cycles)) != 0;
   };
 
+  uint32_t n_fills = 0;  // the producer's
   if (warp == HG * WPH) {
     // ================= producer: the tiles in order =================
     int piece = -1, claimed = 0;
@@ -1551,7 +1552,6 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     describe(t0, pg0, ip0);
     describe(t1, pg1, ip1);
     uint32_t k = 0;
-    uint32_t used = 0;  // stages with a TMA copy in flight at some time
     for (;; ++k) {
       describe(t2, pg2, ip2);
       const uint32_t s = k % N::kStages;
@@ -1576,7 +1576,6 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
       if (whole) {
         if (lane == 0) tc::mbar_arrive_expect(&bar_full[s], N::kTileBytes);
         __syncwarp();
-        used |= 1u << s;
         // lane 4 v + 2 j + h: K or V, block j, half h of the tokens
         const int v = lane >> 2, j = (lane >> 1) & 1, h = lane & 1;
         const int pr = __shfl_sync(0xffffffffu, row, (h * 8) & 31);
@@ -1614,20 +1613,12 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
       pg1 = pg2;
       ip1 = ip2;
     }
-    tc::cp_async_wait<0>();
-    if (!ok) {
-      if (lane == 0) {
-        flag_error(pl.hdr + kErrWord, kErrTimeout);
-        s_abort = 1;
-      }
-      // the copies in flight land before the shared memory is given up
-      const long long t0c = clock64();
-      for (uint32_t n = k > (uint32_t)N::kStages ? k - N::kStages : 0; n < k; ++n)
-        while (((used >> (n % N::kStages)) & 1) &&
-               !tc::mbar_try_wait(&bar_full[n % N::kStages], (n / N::kStages) & 1) &&
-               clock64() - t0c < kWaitCycles) {
-        }
+    if (!ok && lane == 0) {
+      flag_error(pl.hdr + kErrWord, kErrTimeout);
+      s_abort = 1;
     }
+    tc::cp_async_wait<0>();
+    n_fills = k;
     __syncwarp();
   } else {
     // ================= consumers =================
@@ -1742,7 +1733,17 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
       s_abort = 1;
     }
   }
-  __syncthreads();  // no warp leaves while copies may still land
+  __syncthreads();
+  // In the normal course every copy has been waited for by now.  When a consumer gave
+  // up, the last fill of any stage may still be on its way: it lands before the
+  // shared memory is given up.
+  if (s_abort && warp == HG * WPH) {
+    const long long t0 = clock64();
+    for (uint32_t n = n_fills > (uint32_t)N::kStages ? n_fills - N::kStages : 0; n < n_fills; ++n)
+      while (!tc::mbar_try_wait(&bar_full[n % N::kStages], (n / N::kStages) & 1) &&
+             clock64() - t0 < kWaitCycles) {
+      }
+  }
   if (!wait_first) pdl_wait();
 }
 
