@@ -648,8 +648,8 @@ def time_mla_oracle(wl, t, budget_s, steps=None, warmup=0):
 
 
 def mla_bench(wl, args, dev, rank, world, dist):
-    """The DSA decode step with sparse MLA: pks_decode_select (scan + top-k)
-    and pks_mla_sparse_attention, captured in one CUDA graph."""
+    """The DSA decode step with sparse MLA (pks_mla_decode_step: scan, top-k,
+    MLA), captured in one CUDA graph."""
     if args.requests:
         wl = shrink(wl, args.requests)
     if args.topk:
@@ -781,8 +781,7 @@ def mla_bench(wl, args, dev, rank, world, dist):
 
     def call():  # the calls a user makes for one step
         pks.pks_stage_copy([(t[nm], host_in[nm]) for nm in names], s)
-        pks.pks_decode_select(step.select_args, s)
-        pks.pks_mla_sparse_attention(step.attention.args, s)
+        pks.pks_mla_decode_step(step.select_args, step.attention.args, s)
         pks.pks_stage_copy([(out_h, step.out), (idx_h, step.topk_idx)], s)
 
     with torch.cuda.stream(s):

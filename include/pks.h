@@ -408,6 +408,14 @@ pks_status pks_mla_workspace_size(const pks_mla_args* args, size_t* bytes);
  * zeroes the error word once (pks_mla_device_error clears it). */
 pks_status pks_mla_sparse_attention(const pks_mla_args* args, pks_stream stream);
 
+/* The DSA step in one call: pks_decode_select(select), then
+ * pks_mla_sparse_attention(mla) over its selection, whose set-up then overlaps
+ * the top-k's end (the same results as the two calls).  INVALID also when B, k
+ * or topk_idx of the two differ, or with more than one query token; nothing is
+ * launched unless both are valid. */
+pks_status pks_mla_decode_step(const pks_decode_args* select, const pks_mla_args* mla,
+                               pks_stream stream);
+
 /* Copy the MLA workspace's device error word to *code and clear it (codes as
  * for pks_decode_device_error; 5: a bounded wait inside the kernel gave up).
  * Synchronises the stream. */

@@ -201,7 +201,7 @@ k_sparse_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restri
   }
   // the merge grid may take the SM slots this grid leaves free
   pdl_launch_dependents();
-  pdl_wait();  // the selection comes from the top-k kernel
+  pdl_wait();  // the selection comes from the top-k kernel (its addresses: from s_prefix)
   const int64_t Treq = s_prefix[B];
   const int64_t T = Treq * ngroups;
   // with fewer positions than CTAs only the first T CTAs take part, so every
@@ -541,7 +541,7 @@ k_attention_merge(const int32_t* __restrict__ prefix, const float2* __restrict__
   const int qh = blockIdx.x * 4 + (threadIdx.x >> 5);  // query head
   const int b = blockIdx.y;
   pdl_launch_dependents();  // a following kernel may launch and wait for this grid
-  pdl_wait();  // prefix and partials come from the attention kernel
+  pdl_wait(prefix);  // prefix and partials come from the attention kernel
   if (qh >= Hq) return;
   const int h = qh / G, gg = qh % G;  // KV head and row within its group
   const int g = h / HG, hh = h % HG;
@@ -668,8 +668,10 @@ cudaError_t launch_attn_t(const pks_decode_args& a, const WorkspaceLayout& L, ui
   const int G = a.Hq / a.Hkv;
   const int min_per_cta = a.attn_splits > 0 ? 0 : kAttnMinPositions;
   const float scale_log2 = 1.4426950408889634f / sqrtf((float)a.D);
+  // behind the step's own top-k (trim) the kernel starts early and reads the lengths
+  // before it waits; what is before a call that stands alone may still write them
   cudaError_t e = launch_ex(
-      kern, dim3(grid), dim3(HG * 32), smem, s, /*pdl=*/true, /*coop=*/false, a.seq_lens,
+      kern, dim3(grid), dim3(HG * 32), smem, s, /*pdl=*/trim, /*coop=*/false, a.seq_lens,
       a.block_table, reinterpret_cast<const __nv_bfloat16*>(a.q),
       reinterpret_cast<const __nv_bfloat16*>(a.kv_k), reinterpret_cast<const __nv_bfloat16*>(a.kv_v),
       (const int32_t*)a.topk_idx, reinterpret_cast<int32_t*>(ws + L.attn_prefix),

@@ -143,11 +143,13 @@ k_indexer_scan_mma(const int32_t* __restrict__ seq_lens, const int32_t* __restri
   constexpr int NLD = 2 * 2 * HALVES;  // loads per lane per 32-token round
 
   extern __shared__ int smem_i[];
-  // the top-k grid may take SM slots as soon as this grid's CTAs retire
-  pdl_launch_dependents();
-  // launched with programmatic serialization: inputs staged by the kernel
+  // launched with programmatic serialization: inputs written by the kernel
   // before this one (if any) are visible after the wait
-  pdl_wait();
+  int tid = threadIdx.x;
+  pdl_wait(tid);  // (every address below depends on it)
+  // the top-k grid may take SM slots as soon as this grid's CTAs retire; from
+  // here on the step's inputs are ready, which its later kernels count on
+  pdl_launch_dependents();
   int* s_hist = smem_i;                      // [NQ][kScoreBins]
   int* s_prefix = smem_i + NQ * kScoreBins;  // [B + 1]
   // NQ > 1 or FW: (weighted) ReLU of each (token, query head) of a warp's round
@@ -155,7 +157,7 @@ k_indexer_scan_mma(const int32_t* __restrict__ seq_lens, const int32_t* __restri
   __shared__ int s_ep[kTile ? NT / 32 : 1][32][8];
   __shared__ int s_warp[NT / 32];
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int lane = tid & 31, warp = tid >> 5;
   const int gq = lane >> 2, tq = lane & 3;  // MMA group and thread-in-group
   const int max_len = max_pages * page_size;
 

@@ -146,7 +146,7 @@ k_pages_fork(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
              const int32_t* __restrict__ dst_rows, const int32_t* __restrict__ n_tokens) {
   const int i = blockIdx.x, tid = threadIdx.x;
   pdl_launch_dependents();
-  pdl_wait();
+  pdl_wait(src_rows, dst_rows, n_tokens);
   const bool known = state_ok(st, num_pages, page_size);
   const int src = src_rows[i], dst = dst_rows[i];
   bool bad = (unsigned)src >= (unsigned)B || (unsigned)dst >= (unsigned)B || src == dst;
@@ -212,7 +212,7 @@ k_pages_free(PageState st, int32_t* seq_lens, int32_t* block_table, int num_page
              const int32_t* __restrict__ keep) {
   const int i = blockIdx.x, tid = threadIdx.x;
   pdl_launch_dependents();
-  pdl_wait();
+  pdl_wait(rows, keep);
   const bool known = state_ok(st, num_pages, page_size);
   const int row = rows[i];
   bool bad = (unsigned)row >= (unsigned)B;
@@ -275,7 +275,7 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   const int tid = threadIdx.x;
   const int max_len = max_pages * page_size;
   pdl_launch_dependents();  // the copies' blocks may come in and wait
-  pdl_wait();
+  pdl_wait(add);
   const int n_free = st.hdr[kHdrFree];
   const bool known = state_ok(st, num_pages, page_size);
   const int words = (num_pages + 31) / 32;
@@ -549,7 +549,7 @@ k_pages_move(PageState st, MovePools pools, const int32_t* __restrict__ seq_lens
              int32_t* __restrict__ block_table, int32_t* __restrict__ page_map, int num_pages,
              int page_size, int B, int max_pages, int64_t jobs_per_pool) {
   pdl_launch_dependents();
-  pdl_wait();
+  pdl_wait(seq_lens);
   if (!state_ok(st, num_pages, page_size)) return;
   const int n_used = st.hdr[kHdrUsed];
   const uint32_t call = (uint32_t)st.hdr[kHdrCalls];

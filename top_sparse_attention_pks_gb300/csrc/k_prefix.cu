@@ -216,7 +216,7 @@ k_prefix_plan(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   int* s_len = s_eq + B;
   int* s_group = s_dyn + (kPlanArrays - 1) * B;  // (the last of the quantities, later)
   pdl_launch_dependents();
-  pdl_wait();
+  pdl_wait(seq_lens, block_table, prefix_group);
   for (int b = tid; b < B; b += kPlanThreads) {
     int n = seq_lens[b];
     const int g = prefix_group ? prefix_group[b] : -1;
@@ -732,7 +732,7 @@ k_prefix_wide(const int32_t* __restrict__ block_table, const __nv_bfloat16* __re
   __syncthreads();
   tc::fence_after();
   const uint32_t tmem = s_tmem;
-  pdl_wait();  // the plan
+  pdl_wait(pl.hdr, pl.starts);  // the plan
   pdl_launch_dependents();
 
   const int cta = blockIdx.x;
@@ -1778,7 +1778,7 @@ k_prefix_merge(PlanPtrs pl, const float2* __restrict__ wml, const float* __restr
   const int at_row = (int)min(row, rows - 1);  // (a warp's lanes stay together)
   const int h = at_row % sh.Hq, bq = at_row / sh.Hq, b = bq / sh.Nq, qi = bq % sh.Nq;
   const int head = h / sh.G, r = qi * sh.G + h % sh.G;  // row of the request for this KV head
-  pdl_wait();
+  pdl_wait(pl.req, pl.npre, pl.hdr);
   const Request rq = pl.req[b];
   const int pre = pl.npre[b];
   const int U = pl.hdr[kUnits], S = pl.hdr[kShare], slots_head = pl.hdr[kSlots];

@@ -39,10 +39,10 @@ k_stage_copy(const StageRanges r) {
   // launched with programmatic serialization: the next kernel may launch now
   // and wait for this one; this one waits for the kernel before it
   pdl_launch_dependents();
-  pdl_wait();
+  int64_t u0 = (int64_t)blockIdx.x * kStageThreads + threadIdx.x;
+  pdl_wait(u0);  // (all addresses depend on it)
   const int64_t stride = (int64_t)gridDim.x * kStageThreads;
-  for (int64_t u0 = (int64_t)blockIdx.x * kStageThreads + threadIdx.x; u0 < r.total;
-       u0 += stride * kStageUnroll) {
+  for (; u0 < r.total; u0 += stride * kStageUnroll) {
     int4 v[kStageUnroll];
     int which[kStageUnroll];
 #pragma unroll

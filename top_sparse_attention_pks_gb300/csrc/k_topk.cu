@@ -453,7 +453,7 @@ k_topk_select(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ 
   const int b = blockIdx.y, c = blockIdx.x, tid = threadIdx.x;
   const int start = c * kTopkChunk;
   const int len = clamp_len(seq_lens[b / nq], max_len);  // b: virtual request
-  pdl_wait();  // scores and histogram come from the scan
+  pdl_wait(scores, w.hist);  // scores and histogram come from the scan
 
   // all loads of the chunk phase at once: this thread's 16 scores (rows
   // padded to whole chunks, so always in bounds) and 8 histogram bins
@@ -723,7 +723,7 @@ k_topk_threshold(const int32_t* __restrict__ seq_lens, const int32_t* __restrict
 
   const int b = blockIdx.y, c = blockIdx.x, tid = threadIdx.x;
   const int len = clamp_len(seq_lens[b / nq], max_len);  // b: virtual request
-  pdl_wait();  // scores and histogram come from the scan
+  pdl_wait(scores, w.hist);  // scores and histogram come from the scan
   pdl_launch_dependents();
   int32_t* row = topk + (int64_t)b * k;
   if (len <= k) {
@@ -858,7 +858,7 @@ k_topk_emit(const int32_t* __restrict__ seq_lens, const uint32_t* __restrict__ b
   constexpr int kWords = kTopkChunk / 32;  // 128 words per chunk
   const int b = blockIdx.y, c = blockIdx.x, tid = threadIdx.x;
   const int len = clamp_len(seq_lens[b / nq], max_len);  // b: virtual request
-  pdl_wait();  // bitmap and offsets come from k_topk_threshold
+  pdl_wait(bits, chunk_off);  // bitmap and offsets come from k_topk_threshold
   pdl_launch_dependents();
   if (len <= k || len <= kBitmapTokens) return;  // written by the threshold kernel
   const int nch = (len + kTopkChunk - 1) / kTopkChunk;

@@ -664,20 +664,40 @@ pks_status pks_mla_workspace_size(const pks_mla_args* args, size_t* bytes) {
   return PKS_OK;
 }
 
-pks_status pks_mla_sparse_attention(const pks_mla_args* args, pks_stream stream) {
-  pks_status st = mla_check(args);
+namespace {
+pks_status mla_check_call(const pks_mla_args* a) {
+  pks_status st = mla_check(a);
   if (st != PKS_OK) return st;
-  if (args->B > 0) {
-    if (!args->seq_lens || !args->block_table || !args->topk_idx || !args->q || !args->kv ||
-        !args->out)
+  if (a->B > 0) {
+    if (!a->seq_lens || !a->block_table || !a->topk_idx || !a->q || !a->kv || !a->out)
       return PKS_ERR_INVALID;
-    if (!pks::aligned16(args->q) || !pks::aligned16(args->kv) || !pks::aligned16(args->out))
+    if (!pks::aligned16(a->q) || !pks::aligned16(a->kv) || !pks::aligned16(a->out))
       return PKS_ERR_INVALID;
   }
-  const pks::MlaLayout L = pks::mla_layout(*args);
-  if ((st = mla_check_workspace(args, L)) != PKS_OK) return st;
+  return mla_check_workspace(a, pks::mla_layout(*a));
+}
+}  // namespace
+
+pks_status pks_mla_sparse_attention(const pks_mla_args* args, pks_stream stream) {
+  const pks_status st = mla_check_call(args);
+  if (st != PKS_OK) return st;
   if (args->B == 0) return PKS_OK;
-  return pks::from_cuda(pks::launch_mla(*args, L, reinterpret_cast<cudaStream_t>(stream)));
+  return pks::from_cuda(pks::launch_mla(*args, pks::mla_layout(*args), /*behind_topk=*/false,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status pks_mla_decode_step(const pks_decode_args* select, const pks_mla_args* mla,
+                               pks_stream stream) {
+  if (!select) return PKS_ERR_INVALID;
+  pks_status st = mla_check_call(mla);
+  if (st != PKS_OK) return st;
+  if (select->B != mla->B || select->k != mla->k || select->n_queries > 1 ||
+      select->topk_idx != mla->topk_idx)
+    return PKS_ERR_INVALID;
+  st = decode_impl(select, stream, nullptr, /*attention=*/false);
+  if (st != PKS_OK || mla->B == 0) return st;
+  return pks::from_cuda(pks::launch_mla(*mla, pks::mla_layout(*mla), /*behind_topk=*/true,
+                                        reinterpret_cast<cudaStream_t>(stream)));
 }
 
 pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_stream stream) {

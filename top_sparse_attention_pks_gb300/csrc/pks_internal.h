@@ -18,9 +18,35 @@ namespace pks {
 // kernel drains, run what does not depend on it, and wait in pdl_wait()
 // until it has completed and its writes are visible.  A kernel calls
 // pdl_launch_dependents() once the next kernel's CTAs may take SM slots.
+// The kernel before a call's first one may be any of the library's (a staging
+// copy, a page call) and still be writing what the call reads, so a call's first
+// kernel reads nothing before pdl_wait(), or is launched without the attribute.
+// Where later ones read the call's inputs before their own wait (top-k, attention
+// and MLA behind the scan), every kernel before them waits before it calls
+// pdl_launch_dependents(): the inputs are then complete before they can start.
 // Both are no-ops for a kernel launched without the attribute.
 #ifdef __CUDACC__
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+// A pointer to read through behind the wait, or an index that its addresses are
+// made of, is named in it, unless they come from loads that stand behind the wait
+// themselves: nothing in these kernels writes through a const __restrict__
+// pointer, so a memory clobber does not keep the compiler from moving a load
+// through one up past the wait (it does: a fork in front of the MLA kernel gave
+// old lengths).  What is named gets a new value behind the wait.
+template <typename... P>
+__device__ __forceinline__ void behind(P&... p) {
+  auto renew = [](auto& x) {
+    if constexpr (sizeof(x) == 8) asm volatile("" : "+l"(x) : : "memory");
+    else asm volatile("" : "+r"(x) : : "memory");
+    return 0;
+  };
+  int done[] = {0, renew(p)...};
+  (void)done;
+}
+template <typename... P>
+__device__ __forceinline__ void pdl_wait(P&... p) {
+  asm volatile("griddepcontrol.wait;\n" ::: "memory");
+  behind(p...);
+}
 __device__ __forceinline__ void pdl_launch_dependents() {
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
 }
@@ -163,7 +189,9 @@ struct MlaLayout {
 };
 int mla_splits(const pks_mla_args& a);
 MlaLayout mla_layout(const pks_mla_args& a);
-cudaError_t launch_mla(const pks_mla_args& a, const MlaLayout& L, cudaStream_t s);
+// behind_topk: the kernel before it on the stream is the top-k of its step
+cudaError_t launch_mla(const pks_mla_args& a, const MlaLayout& L, bool behind_topk,
+                       cudaStream_t s);
 cudaError_t launch_residency(int32_t* state, int32_t num_pages, int32_t capacity, int32_t B,
                              int32_t k, int32_t page_size, int32_t max_pages,
                              const int32_t* topk_idx, const int32_t* block_table,

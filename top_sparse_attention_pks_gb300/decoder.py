@@ -197,8 +197,8 @@ class MlaAttention:
 
 
 class MlaDecodeStep:
-    """The DSA decode step with MLA attention: indexer scan and top-k
-    (``pks_decode_select``), then the sparse MLA over the selected tokens.
+    """The DSA decode step with MLA attention (``pks_mla_decode_step``): indexer
+    scan and top-k, then the sparse MLA over the selected tokens.
     ``tensors``: seq_lens, block_table, q_idx, w_idx, idx_k as for the GQA
     step, plus q [B, H, d + r] and kv [num_pages, P, d + r] (bf16)."""
 
@@ -245,8 +245,7 @@ class MlaDecodeStep:
         return self.topk_idx
 
     def __call__(self, stream=None):
-        pks.pks_decode_select(self.select_args, stream)
-        pks.pks_mla_sparse_attention(self.attention.args, stream)
+        pks.pks_mla_decode_step(self.select_args, self.attention.args, stream)
         return self.out, self.topk_idx
 
 

@@ -214,6 +214,8 @@ def _declare(L):
     L.pks_mla_workspace_size.restype = _ST
     L.pks_mla_sparse_attention.argtypes = [_PM, _P]
     L.pks_mla_sparse_attention.restype = _ST
+    L.pks_mla_decode_step.argtypes = [_PARGS, ctypes.POINTER(pks_mla_args), _P]
+    L.pks_mla_decode_step.restype = _ST
     L.pks_mla_device_error.argtypes = [_PM, ctypes.POINTER(ctypes.c_int32), _P]
     L.pks_mla_device_error.restype = _ST
 
@@ -648,6 +650,11 @@ def pks_mla_workspace_size(args: pks_mla_args) -> int:
 def pks_mla_sparse_attention(args: pks_mla_args, stream=None) -> None:
     _check(lib().pks_mla_sparse_attention(ctypes.byref(args), _stream(stream)),
            "pks_mla_sparse_attention")
+
+
+def pks_mla_decode_step(select: pks_decode_args, mla: pks_mla_args, stream=None) -> None:
+    _check(lib().pks_mla_decode_step(ctypes.byref(select), ctypes.byref(mla), _stream(stream)),
+           "pks_mla_decode_step")
 
 
 def pks_mla_device_error(args: pks_mla_args, stream=None) -> int:
