@@ -1451,12 +1451,15 @@ k_prefix_narrow(const int32_t* __restrict__ block_table, const __nv_bfloat16* __
     tc::mbar_init_fence();
     s_abort = 0;
   }
-  // after the wide kernel the plan is complete (its CTAs waited for it before
-  // they let this grid start), and this grid only waits for it at its end: the
-  // fence drops what the SM's L1 may hold from before (what is read ahead of it
-  // comes from L2, where the kernels before the wide one left it)
+  // Behind the wide kernel this grid runs beside that one and waits for it only at
+  // its end.  In place of a wait it relies on what it reads having been complete
+  // before it could start: every CTA of the wide kernel waited for the plan, and so
+  // for everything before the plan, before it let this grid start.  What the SM's L1
+  // may hold from before goes with a fence; the plan's numbers are read from L2, and
+  // table and queries through pointers that are named here (no non-coherent loads).
   if (wait_first) pdl_wait();
   else if (warp == HG * WPH) __threadfence();  // (for all, by the barrier below)
+  behind(block_table, q, pl.hdr, pl.npre);
   pdl_launch_dependents();
   const Pieces pieces(pl.hdr, ngroups);
   const int Treq = __ldcg(pl.hdr + kTiles);
