@@ -410,3 +410,32 @@ def test_free_flags_any_bad_entry(entry):
     assert pages.device_error() == 1
     assert lens.tolist() == [0, 0] and int(table.max()) == -1
     assert pages.refs.tolist() == [0, 1, 0, 0, 0, 0] and int(pages.n_free) == 5
+
+
+def _bitmap(pages):
+    off = pks.pks_pages_offsets(pages.refs.numel())["free_map"]
+    return pages.state[off: off + 4 * -(-pages.refs.numel() // 32)].clone()
+
+
+@pytest.mark.parametrize("num_pages,held", [(8, 3), (3000, 5), (140_000, 9)])
+def test_extend_with_fewer_free_pages_than_counted_takes_none(num_pages, held):
+    """The pages that are free stay so: growth that fits them is granted afterwards."""
+    B, width = 64, held + -(-num_pages // 64) + 2
+    table = np.full((B, width), -1)
+    table[0, :held] = np.random.default_rng(num_pages).permutation(num_pages)[:held]
+    lens, table = dev([16 * held] + [0] * (B - 1)), dev(table)
+    pages = PageTable(lens, table, num_pages, 16)
+    before = [x.clone() for x in (lens, table, pages.refs)] + [_bitmap(pages)]
+    pages.n_free.fill_(num_pages - 1)
+    need = np.full(B, (num_pages - held + 1) // B)
+    need[: (num_pages - held + 1) % B] += 1  # one page more than there are
+    pages.extend(dev(16 * need))
+    assert int(pages.granted) == 0 and pages.device_error() == 4
+    for was, x in zip(before, [lens, table, pages.refs, _bitmap(pages)]):
+        assert torch.equal(was, x)
+    pages.n_free.fill_(num_pages - held)
+    need[0] -= 1
+    pages.extend(dev(16 * need))
+    assert int(pages.granted) == 1 and pages.device_error() == 0
+    assert int(pages.n_free) == 0 and bool((pages.refs == 1).all())
+    assert not _bitmap(pages).any()

@@ -406,15 +406,19 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
     }
     rank0 += in_pass;
   }
-  if (rank0 < total) {  // the bitmap has fewer pages than the count of free ones
+  __syncthreads();
+  auto taken = [&](int r) { return r < kTakenShared ? s_taken[r] : st.taken[r]; };
+  if (rank0 < total) {  // the bitmap has fewer pages than the count of free ones:
+    for (int r = tid; r < rank0; r += kPlanThreads) {  // those found go back
+      const int page = taken(r);
+      atomicOr(&st.free_map[page >> 5], 1u << (page & 31));
+    }
     if (tid == 0) {
       flag_error(st.hdr, kErrState);
       st.hdr[kHdrGrant] = st.hdr[kHdrMoves] = 0;
     }
     return;
   }
-  __syncthreads();
-  auto taken = [&](int r) { return r < kTakenShared ? s_taken[r] : st.taken[r]; };
 #pragma unroll
   for (int u = 0; u < kPer; ++u) {
     const int b = tid + u * kPlanThreads;
