@@ -502,7 +502,8 @@ pks_status pks_prefix_device_error(const pks_prefix_args* args, int32_t* code,
  *   [0..63]                header: num_pages, page_size, n_free (index 2),
  *                          device error word, moves and grant (index 6) of
  *                          the last call, magic, n_used of the last
- *                          compaction (index 7), call counter
+ *                          compaction (index 7; -1: it was refused), call
+ *                          counter
  *   ref[num_pages]         holders of each page
  *   free_map               bit p of the uint32 words: page p is free
  *   scratch
@@ -589,9 +590,11 @@ pks_status pks_pages_compact(const pks_pages_args* args, int32_t* page_map, pks_
 
 /* Copy the state's device error word to *code (host) and clear it;
  * synchronises the stream.  0: none; 1 page id out of range; 3 length, token
- * count or growth out of range; 4 a page lost more holders than it had;
- * or the state is not one that pks_pages_init filled for these pages (then the
- * call changed nothing); 6 out of pages; 7 row index out of range, repeated,
+ * count or growth out of range; 4 a page lost more holders than it had; or the
+ * state is not one that pks_pages_init filled for these pages (then the call
+ * changed nothing), or its free pages are not as many as it counts (found by
+ * extend, where they do not suffice, and by compact, which then changed nothing);
+ * 6 out of pages; 7 row index out of range, repeated,
  * not empty or both source and destination.  Of several errors since the word
  * was last read one is kept. */
 pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks_stream stream);

@@ -439,3 +439,23 @@ def test_extend_with_fewer_free_pages_than_counted_takes_none(num_pages, held):
     assert int(pages.granted) == 1 and pages.device_error() == 0
     assert int(pages.n_free) == 0 and bool((pages.refs == 1).all())
     assert not _bitmap(pages).any()
+
+
+@pytest.mark.parametrize("counted", [7, 4, 8, 9, -1, 0, 2 ** 31 - 1, -2 ** 31])
+def test_compact_with_another_count_of_free_pages_changes_nothing(counted):
+    """Three of eight pages are held, two of them at or above the third."""
+    lens, table = dev([20, 0, 5]), dev([[0, 6, -1], [-1] * 3, [7, -1, -1]])
+    pool = torch.arange(8 * 16 * 3, dtype=torch.int32, device="cuda").view(8, 16, 3)
+    pages = PageTable(lens, table, 8, 16, pools=[pool])
+    mine = [lens, table, pages.refs, pool, pages.page_map]
+    pages.page_map.fill_(-9)
+    before = [x.clone() for x in mine] + [_bitmap(pages)]
+    pages.n_free.fill_(counted)
+    pages.compact()
+    assert pages.device_error() == 4 and int(pages.n_free) == counted
+    for was, x in zip(before, mine + [_bitmap(pages)]):
+        assert torch.equal(was, x)
+    pages.n_free.fill_(5)
+    assert pages.compact().tolist() == [0, -1, -1, -1, -1, -1, 1, 2]
+    assert pages.device_error() == 0 and table[[0, 2]].tolist() == [[0, 1, -1], [2, -1, -1]]
+    assert pages.refs.tolist() == [1, 1, 1, 0, 0, 0, 0, 0]

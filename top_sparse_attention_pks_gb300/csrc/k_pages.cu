@@ -348,7 +348,7 @@ k_pages_extend(PageState st, int32_t* seq_lens, int32_t* block_table, int num_pa
   unsigned long long all = s_need[tid & 31];
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) all += __shfl_xor_sync(0xffffffffu, all, o);
-  const bool enough = all <= (unsigned long long)n_free;
+  const bool enough = n_free >= 0 && all <= (unsigned long long)n_free;
   // prefix sums of needs and copies over the rows, 1024 rows at a time
   int at[kPer], c_at[kPer], total = 0, copies = 0;
 #pragma unroll
@@ -459,8 +459,10 @@ k_pages_pair(PageState st, int num_pages, int page_size) {
     if (tid == 0) flag_error(st.hdr, kErrState);
     return;
   }
-  const int n_used = num_pages - st.hdr[kHdrFree];
-  const int words = (num_pages + 31) / 32;
+  const int n_free = st.hdr[kHdrFree];
+  const bool in_range = n_free >= 0 && n_free <= num_pages;
+  const int n_used = in_range ? num_pages - n_free : 0;
+  const int words = in_range ? (num_pages + 31) / 32 : 0;
   const uint32_t call = (uint32_t)st.hdr[kHdrCalls] + 1;
   int holes = 0, high = 0;
   for (int w0 = 0; w0 < words; w0 += kPlanThreads) {
@@ -472,7 +474,7 @@ k_pages_pair(PageState st, int num_pages, int page_size) {
       const uint32_t lo = below >= 32 ? 0xffffffffu : below <= 0 ? 0u : (1u << below) - 1u;
       const int valid = num_pages - w * 32;
       const uint32_t in = valid >= 32 ? 0xffffffffu : (1u << valid) - 1u;
-      hole = m & lo;
+      hole = m & lo & in;
       held = ~m & ~lo & in;
     }
     int t0, t1;
@@ -484,18 +486,19 @@ k_pages_pair(PageState st, int num_pages, int page_size) {
     high += t1;
   }
   __syncthreads();
-  // both counts agree while the map and n_free do; the smaller one is safe
-  const int n = holes < high ? holes : high;
+  // both counts agree while the map and n_free do; else nothing moves
+  const bool agree = in_range && holes == high;
+  const int n = agree ? high : 0;
   for (int r = tid; r < n; r += kPlanThreads) {
     const int src = st.moves[r].x, dst = st.moves[r].y;
     st.stamp[src] = ((uint64_t)call << 32) | (uint32_t)dst;
     st.stamp[dst] = ((uint64_t)call << 32) | (uint32_t)src;
   }
   if (tid == 0) {
-    if (holes != high) flag_error(st.hdr, kErrState);
+    if (!agree) flag_error(st.hdr, kErrState);
     st.hdr[kHdrMoves] = n;
-    st.hdr[kHdrUsed] = n_used;
-    st.hdr[kHdrCalls] = (int32_t)call;
+    st.hdr[kHdrUsed] = agree ? n_used : -1;
+    if (agree) st.hdr[kHdrCalls] = (int32_t)call;
   }
 }
 
@@ -556,6 +559,7 @@ k_pages_move(PageState st, MovePools pools, const int32_t* __restrict__ seq_lens
   pdl_wait(seq_lens);
   if (!state_ok(st, num_pages, page_size)) return;
   const int n_used = st.hdr[kHdrUsed];
+  if (n_used < 0) return;  // refused
   const uint32_t call = (uint32_t)st.hdr[kHdrCalls];
   const int t0 = blockIdx.x * kMoveThreads + threadIdx.x, step = gridDim.x * kMoveThreads;
   // one thread a page; a pair's counts are written by its source's thread alone
