@@ -496,3 +496,26 @@ def test_attention_needs_a_plan_of_its_shapes(Nq, groups):
     torch.cuda.synchronize()
     assert att.device_error() == 0
     b.check(out, att.lse)
+
+
+def test_a_refused_layer_leaves_the_one_before_in_place(monkeypatch):
+    b = Batch([900, 1200], [0, 0], [768] * 2, seed=25)
+    att = b.attention()
+    out = att().clone()
+    q, k, v = (torch.randn_like(x) for x in (b.q, b.k, b.v))
+    odd = torch.empty(v.numel() + 4, dtype=torch.bfloat16, device="cuda")[4:].view(v.shape)
+    refused = [((q, k, v[1:]), ValueError), ((q, k[:, :, :1].contiguous(), v), ValueError),
+               ((q, k, v.float()), TypeError), ((q, k, odd), pks.PksError),
+               ((q, k, v.cpu()), ValueError)]
+    for tensors, error in refused:
+        with pytest.raises(error):
+            att.attend(*tensors)
+        att.out.fill_(float("nan"))
+        assert torch.equal(att.attend(), out) and torch.equal(att(), out)
+    with monkeypatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: 1)
+        with pytest.raises(ValueError):
+            att.attend(q, k, v)
+    assert torch.equal(att.attend(), out)
+    b.q, b.k, b.v = q, k, v
+    b.check(att.attend(q, k, v), att.lse)

@@ -262,7 +262,7 @@ class PrefixAttention:
     Calling the object plans and attends.  ``plan`` alone is needed whenever
     lengths, table or groups have changed; ``attend`` serves further layers,
     ``attend(q, kv_k, kv_v)`` with tensors of the same shapes, which later calls
-    keep to.  One object's calls run one after another: their workspace is one."""
+    keep to (a call that is refused leaves those before it in place).  One object's calls run one after another: their workspace is one."""
 
     def __init__(self, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
                  causal: bool = False, sm_scale: float = 0.0, lse: bool = False,
@@ -285,17 +285,26 @@ class PrefixAttention:
         pks.pks_prefix_plan(self.args, stream)
 
     def attend(self, q=None, kv_k=None, kv_v=None, stream=None):
-        for name, t in (("q", q), ("kv_k", kv_k), ("kv_v", kv_v)):
+        new = {}  # all of them are looked at before any is taken over
+        for at, (name, t) in enumerate((("q", q), ("kv_k", kv_k), ("kv_v", kv_v)), 3):
             if t is None:
                 continue
-            at = ("q", "kv_k", "kv_v").index(name) + 3
             was = self._keep[at]
             if t.shape != was.shape or t.device != was.device:
                 raise ValueError(f"{name} must have the shape and device it was planned with")
-            setattr(self.args, name, pks._dptr(t, torch.bfloat16, name))
-            self._keep[at] = t
+            new[name] = at, t, pks._dptr(t, torch.bfloat16, name)
         pks._on_current_device(self.out)
-        pks.pks_prefix_attention(self.args, stream)
+        old = {name: getattr(self.args, name) for name in new}
+        for name, (_, _, ptr) in new.items():
+            setattr(self.args, name, ptr)
+        try:
+            pks.pks_prefix_attention(self.args, stream)
+        except BaseException:
+            for name, ptr in old.items():
+                setattr(self.args, name, ptr)
+            raise
+        for at, t, _ in new.values():
+            self._keep[at] = t
         return self.out
 
     def __call__(self, stream=None):
