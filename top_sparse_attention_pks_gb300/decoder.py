@@ -256,8 +256,9 @@ class PrefixAttention:
     [B, Nq, Hq, D] (query tokens at the end of each request, ``causal`` among
     themselves), kv_k / kv_v [num_pages, P, Hkv, D] (bf16), prefix_group [B]
     (int32, negative: none) or None, min_shared: tokens from which on a prefix is
-    taken once (0: when that is expected to be faster).  Owns ``out``, ``lse`` (when asked for) and
-    the workspace.
+    taken once (0: when that is expected to be faster).  Owns ``out``, ``lse`` (when
+    asked for) and the workspace, allocated and cleared on ``stream`` (default: torch's
+    current stream): calls on another stream have to wait for that one.
 
     Calling the object plans and attends.  ``plan`` alone is needed whenever
     lengths, table or groups have changed; ``attend`` serves further layers,
@@ -266,17 +267,19 @@ class PrefixAttention:
 
     def __init__(self, seq_lens, block_table, q, kv_k, kv_v, prefix_group=None,
                  causal: bool = False, sm_scale: float = 0.0, lse: bool = False,
-                 wait_limit: int = 0, min_shared: int = 0):
+                 wait_limit: int = 0, min_shared: int = 0, stream=None):
         pks._on_current_device(seq_lens, block_table, q, kv_k, kv_v, prefix_group)
         dev = q.device
-        self.out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
-        self.lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
+        with pks._on_stream(stream):
+            self.out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            self.lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
         kw = dict(seq_lens=seq_lens, block_table=block_table, q=q, kv_k=kv_k, kv_v=kv_v,
                   prefix_group=prefix_group, causal=causal, sm_scale=sm_scale, out=self.out,
                   lse=self.lse, wait_limit=wait_limit, min_shared=min_shared)
         nbytes = pks.pks_prefix_workspace_size(pks.make_prefix_args(**kw))
-        self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        self.workspace[:256].zero_()
+        with pks._on_stream(stream):
+            self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+            self.workspace[:256].zero_()
         self.args = pks.make_prefix_args(workspace=self.workspace, **kw)
         self._keep = [seq_lens, block_table, prefix_group, q, kv_k, kv_v]
 
@@ -323,7 +326,8 @@ class PageTable:
     ``block_table`` [B, max_pages] (int32, e.g. from ``Pool.build_block_table``)
     stay the caller's tensors and are updated in place; ``pools`` are the paged
     tensors [num_pages, page_size, ...] whose rows move with the pages.  All
-    calls run on ``stream`` (default: torch's current stream), one after another.
+    calls run on ``stream`` (default: torch's current stream), one after another;
+    calls on another stream than the one it was built on have to wait for that one.
 
     ``refs`` [num_pages], ``n_free`` and ``granted`` (0-dim) are views of the
     state and ``page_map`` [num_pages] is what the last ``compact`` wrote."""
@@ -333,8 +337,10 @@ class PageTable:
         pks._on_current_device(seq_lens, block_table, state, *pools)
         dev = block_table.device
         nbytes = pks.pks_pages_state_bytes(num_pages)
-        if state is None:
-            state = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        with pks._on_stream(stream):
+            if state is None:
+                state = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+            self.page_map = torch.empty(int(num_pages), dtype=torch.int32, device=dev)
         self.state = state
         self.seq_lens, self.block_table, self.pools = seq_lens, block_table, list(pools)
         self.args = pks.make_pages_args(seq_lens=seq_lens, block_table=block_table,
@@ -344,7 +350,6 @@ class PageTable:
         header = state[:256].view(torch.int32)
         self.n_free, self.granted = header[2], header[6]
         self.refs = state[off: off + 4 * int(num_pages)].view(torch.int32)
-        self.page_map = torch.empty(int(num_pages), dtype=torch.int32, device=dev)
         pks.pks_pages_init(self.args, stream)
 
     def fork(self, src_rows, dst_rows, n_tokens=None, stream=None):

@@ -9,6 +9,7 @@ the first call raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from pathlib import Path
 from typing import Optional, Sequence
@@ -234,6 +235,15 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
+
+
+def _on_stream(stream):
+    """Context in which torch allocates and fills on ``stream`` (default: its current)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
 
 
 def _dptr(t: Optional[torch.Tensor], dtype, name: str) -> Optional[int]:
