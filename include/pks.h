@@ -432,13 +432,14 @@ pks_status pks_mla_device_error(const pks_mla_args* args, int32_t* code, pks_str
  * is each request's own attention whatever the groups are: prefix_group only
  * says between which requests aliased pages are looked for.  Within a group
  * the leading table entries equal to the longest member's are the shared
- * part; the group's common prefix (the least among the members that share at
- * least half of what the second longest shares) takes part once for all of
- * these members when that is worth it (min_shared), the rest of each request on
- * its own.  Rows of a tile beyond
- * a causal query's limit count with weight zero, so their V rows have to be
- * finite; rows at or beyond len_b are never read.  Calls that share a workspace
- * run one after another.
+ * part (members are compared with that one only: two that share nothing with
+ * it are read each on its own, whatever they share with one another); the
+ * group's common prefix (the least among the members that share at least half
+ * of what the second longest shares) takes part once for all of these members
+ * when that is worth it (min_shared), the rest of each request on its own.
+ * Rows of a tile beyond a causal query's limit count with weight zero, so their
+ * V rows have to be finite; rows at or beyond len_b are never read.  Calls that
+ * share a workspace run one after another.
  * ---------------------------------------------------------------------- */
 typedef struct pks_prefix_args {
   int32_t B;              /* requests; B * Nq <= 4096, B * max_pages * page_size <= 2^34 */
