@@ -600,6 +600,134 @@ pks_status pks_pages_compact(const pks_pages_args* args, int32_t* page_map, pks_
  * was last read one is kept. */
 pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks_stream stream);
 
+/* ------------------------------------------------------------------------
+ * A KV cache held in 4 bits ([SA] introduction: the selection and its attention
+ * need the whole context in HBM, whose bytes bound the step).  A cached row (K or
+ * V of one token and KV head, D values) is held in groups of 32 consecutive
+ * values; for the values x of a group
+ *   m = the largest fp16 <= min x,   s = the smallest fp16 >= (max x - m) / 15,
+ *   n = floor((x - m) / s + 1/2)     (0..15; all 0 where s = 0)
+ * and the row stands for m + s n.  A group for which m or s is not finite (an
+ * infinity or NaN among its values, or values outside fp16's range) has s = NaN
+ * and m = 0: all of it reads as NaN.
+ *
+ * A pool, uint8 [num_pages, page_size, token_bytes], holds K or V; its token rows
+ * move with the pages like those of any pool (pks_page_pool).  A token row holds
+ * the Hkv heads' records one after another, D/2 bytes of codes and then one
+ * (s, m) pair of fp16 a group (80 bytes for D = 128, 40 for D = 64), filled up to
+ * a multiple of 16 bytes.  With NB = D / 32 groups the codes of a record are
+ *   K: 32-bit word t * NB + b: values 32 b + 8 t + i in bits 4 i, i < 8 (t < 4)
+ *   V: 16-bit word g * NB + b: values 32 b + 4 g + i in bits 4 i, i < 4 (g < 8)
+ * the orders in which the attention's lanes take them.  Where token_bytes is a
+ * multiple of 128, byte o of the token row in slot i of its page stands at
+ * o ^ ((i & 7) << 4), which spreads a page's rows over the banks of shared memory.
+ * ---------------------------------------------------------------------- */
+
+/* Bytes of one token row of a pool, Hkv * (D/2 + D/8) filled up to a multiple of
+ * 16.  INVALID: Hkv < 1 or bytes NULL; UNSUPPORTED: D not 64 or 128, Hkv > 1024. */
+pks_status pks_q4_token_bytes(int32_t Hkv, int32_t D, size_t* bytes);
+
+/* Types of the rows that are written and read. */
+#define PKS_Q4_BF16 0
+#define PKS_Q4_FP16 1
+#define PKS_Q4_FP32 2
+
+/* Rows of a batch, packed: rows starts[b] .. starts[b + 1] are the last tokens of
+ * request b, row starts[b] + j standing at position
+ * len_b - (starts[b + 1] - starts[b]) + j.  Rows from starts[B] on are not used
+ * (a padded batch): they are neither written to the cache nor, by a read, changed. */
+typedef struct pks_q4_rows_args {
+  int32_t B;              /* requests, 0..4096 */
+  int32_t n_rows;         /* rows that k and v have room for, at least starts[B]; 0 allowed */
+  int32_t Hkv, D;         /* D: 64 or 128; Hkv <= 1024 */
+  int32_t page_size, max_pages, num_pages;
+  int32_t dtype;          /* of k and v: PKS_Q4_BF16, _FP16 or _FP32 */
+  const int32_t* seq_lens;     /* device int32 [B]: the new tokens counted in */
+  const int32_t* block_table;  /* device int32 [B, max_pages] */
+  const int32_t* starts;       /* device int32 [B + 1], not decreasing, starts[0] >= 0 */
+  void* k;                     /* device [n_rows, Hkv, D] (strides below), 16-byte aligned:
+                                  read by pks_q4_write, written by pks_q4_read */
+  void* v;
+  int64_t k_row, k_head;       /* values from one row, one head to the next; a multiple of */
+  int64_t v_row, v_head;       /* 16 bytes each */
+  void* pool_k;                /* device uint8 [num_pages, page_size, token_bytes], */
+  void* pool_v;                /* 16-byte aligned */
+  int32_t* error;              /* NULL, or a device int32: set to 1 (page id), 2 (starts) or 3
+                                  (length) when a row is skipped for it, else left as it is */
+} pks_q4_rows_args;
+
+/* Quantise rows into their pages.  A row without a place (its request's length
+ * or table entry out of range, more rows than the request has tokens) is skipped.
+ * No two rows of a call may have the same place: a page that requests share is
+ * written through one of them.  One launch.  INVALID for NULL or misaligned
+ * pointers, strides and shapes that are no shapes; UNSUPPORTED for shapes outside
+ * the ranges above. */
+pks_status pks_q4_write(const pks_q4_rows_args* args, pks_stream stream);
+
+/* The values that cached rows stand for, rounded once to the type of k and v.  A
+ * row without a place is left as it was.  One launch; errors as above. */
+pks_status pks_q4_read(const pks_q4_rows_args* args, pks_stream stream);
+
+/* Attention over a 4-bit cache.  For every request b, query token i and head h
+ *   out[b,i,h] = sum_t p_t V[t],  p = softmax over t of sm_scale * q[b,i,h] . K[t]
+ * with K and V the values the cache stands for (not rounded any further):
+ *  - pks_q4_attention: t < len_b, or with `causal` t < len_b - Nq + i + 1 (query
+ *    token i stands at position len_b - Nq + i).
+ *  - pks_q4_sparse_attention: the positions of topk_idx[b, i, :] holding a token
+ *    (>= 0, each < len_b), in any order; -1 entries are skipped.
+ * A query without tokens gets zeros.  Tokens that a query does not attend to are
+ * without influence on it, whatever they hold. */
+typedef struct pks_q4_attention_args {
+  int32_t B;              /* requests; B * Nq <= 4096 */
+  int32_t Hq, Hkv;        /* 1 <= Hq / Hkv <= 16; Hkv <= 16, or D = 128, or Hkv even */
+  int32_t D;              /* 64 or 128 */
+  int32_t page_size, max_pages, num_pages;  /* num_pages * page_size < 2^31 and
+                                               max_pages * page_size <= 2^24 */
+  int32_t n_queries;      /* Nq, 0 (one) to 64 */
+  int32_t causal;         /* 0 or 1; pks_q4_attention only */
+  int32_t k;              /* pks_q4_sparse_attention: entries a list, 1..65536; else 0 */
+  int32_t trim;           /* as in pks_mla_args; pks_q4_sparse_attention only */
+  int32_t wait_limit;     /* as in pks_mla_args */
+  float sm_scale;         /* 0 = 1 / sqrt(D) */
+  int32_t reserved;       /* must be 0 */
+  const int32_t* seq_lens;      /* device int32 [B] */
+  const int32_t* block_table;   /* device int32 [B, max_pages] */
+  const int32_t* topk_idx;      /* device int32 [B, Nq, k], or NULL where k is 0 */
+  const void* q;          /* device bf16 [B, Nq, Hq, D], 16-byte aligned */
+  const void* pool_k;     /* device uint8 [num_pages, page_size, token_bytes], 16-byte aligned */
+  const void* pool_v;     /* likewise */
+  void* out;              /* device bf16 [B, Nq, Hq, D], 16-byte aligned (written) */
+  float* lse;             /* NULL, or device float [B, Nq, Hq] (written): ln of the sum of
+                             exp(sm_scale * q . K), -inf for a query without tokens */
+  void* workspace;        /* device scratch owned by the caller, 256-byte aligned; its first
+                             256 bytes zeroed once by the caller.  Calls that share it run
+                             one after another */
+  size_t workspace_bytes;
+} pks_q4_attention_args;
+
+/* Workspace bytes for these shapes on the current device (pointers may be NULL). */
+pks_status pks_q4_workspace_size(const pks_q4_attention_args* args, size_t* bytes);
+
+/* Two launches each.  INVALID for NULL or misaligned pointers and shapes that are
+ * no shapes (a k other than 0 in the first, or 0 in the second, among them),
+ * UNSUPPORTED for shapes outside the ranges above, WORKSPACE for a missing,
+ * misaligned or too small workspace. */
+pks_status pks_q4_attention(const pks_q4_attention_args* args, pks_stream stream);
+pks_status pks_q4_sparse_attention(const pks_q4_attention_args* args, pks_stream stream);
+
+/* The decode step over a 4-bit cache: pks_decode_select(select), then
+ * pks_q4_sparse_attention(attention) over its selection.  INVALID also when B,
+ * n_queries, k or topk_idx of the two differ; nothing is launched unless both are
+ * valid. */
+pks_status pks_q4_decode_step(const pks_decode_args* select,
+                              const pks_q4_attention_args* attention, pks_stream stream);
+
+/* Copy the workspace's device error word to *code (host) and clear it;
+ * synchronises the stream (codes as for pks_decode_device_error; 5: a bounded wait
+ * inside the kernel gave up, the outputs are then undefined). */
+pks_status pks_q4_device_error(const pks_q4_attention_args* args, int32_t* code,
+                               pks_stream stream);
+
 /* ---- staging of a step's inputs and outputs --------------------------------
  * Not an operation of the pages: a serving convenience for moving a step's
  * small inputs (queries, lengths, block table) in and its outputs (attention

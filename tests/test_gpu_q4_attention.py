@@ -1,0 +1,254 @@
+"""Attention over a 4-bit cache, dense and over selected tokens, against the 64-bit
+restatement of q4_cases (which derives the tolerances)."""
+
+import numpy as np
+import pytest
+import torch
+
+from q4_cases import Batch, i32
+from top_sparse_attention_pks_gb300 import build
+from top_sparse_attention_pks_gb300.decoder import Q4Attention, Q4Cache, Q4SparseAttention
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    build.build_library()
+
+
+LENS = [0, 1, 2, 15, 16, 17, 31, 33, 64, 100, 257]
+
+
+@pytest.mark.parametrize("Hkv,G,D,page", [
+    (2, 4, 64, 16), (8, 4, 128, 64), (8, 8, 128, 16), (1, 1, 64, 1), (1, 8, 128, 5), (3, 7, 64, 17),
+    (4, 2, 128, 48), (5, 5, 128, 16), (6, 1, 64, 8), (7, 3, 128, 32), (16, 8, 128, 16),
+    (16, 2, 64, 64), (9, 4, 64, 3), (15, 1, 128, 16), (32, 4, 128, 16), (18, 2, 64, 16),
+    (8, 4, 128, 5), (3, 4, 64, 8), (2, 8, 128, 128), (13, 2, 64, 1)])
+def test_dense_one_query(Hkv, G, D, page):
+    Batch(LENS, page, Hkv, G, D, seed=Hkv).dense()
+
+
+@pytest.mark.parametrize("Hkv,G,D,page,Nq", [
+    (2, 4, 64, 16, 4), (8, 4, 128, 64, 4), (8, 16, 128, 16, 1), (1, 12, 64, 1, 1),
+    (1, 16, 128, 5, 3), (4, 8, 128, 16, 5), (8, 8, 128, 64, 8), (2, 1, 64, 16, 64),
+    (16, 16, 128, 16, 1), (12, 3, 128, 17, 3), (9, 16, 64, 16, 2), (3, 5, 64, 16, 2),
+    (5, 2, 128, 8, 7), (10, 9, 64, 16, 1)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_dense_several_queries(Hkv, G, D, page, Nq, causal):
+    Batch(LENS, page, Hkv, G, D, Nq, seed=Nq).dense(causal=causal)
+
+
+@pytest.mark.parametrize("Hkv,G,D,page,k", [
+    (2, 4, 64, 16, 64), (8, 8, 128, 64, 100), (1, 8, 128, 1, 7), (3, 16, 64, 17, 300),
+    (16, 4, 128, 16, 33), (8, 1, 64, 5, 1), (32, 2, 128, 16, 16), (7, 12, 128, 16, 50)])
+@pytest.mark.parametrize("holes", [False, True])
+@pytest.mark.parametrize("Nq", [1, 3])
+def test_selected_tokens(Hkv, G, D, page, k, holes, Nq):
+    Batch(LENS, page, Hkv, G, D, Nq, seed=k).sparse(k, holes)
+
+
+def test_long_requests_split_over_all_sms():
+    Batch([20000, 3, 0, 45011, 700], 64, 8, 8, 128, seed=1).dense()
+    Batch([70001], 16, 1, 4, 128, seed=2).dense()
+    Batch([50000, 9], 16, 2, 6, 64, 3, seed=3).dense(causal=True)
+    Batch([30000, 40000], 16, 8, 4, 128, seed=4).sparse(4096)
+
+
+def test_many_requests():
+    rng = np.random.default_rng(0)
+    lens = rng.integers(0, 40, 4096)
+    Batch(lens, 16, 1, 2, 64, seed=5).dense(rows=range(0, 4096, 37))
+    Batch(rng.integers(0, 90, 1000), 8, 2, 2, 64, 4, seed=6).sparse(20, rows=range(0, 1000, 31))
+
+
+def test_empty_batches():
+    Batch([0, 0, 0]).dense()
+    Batch([0, 0, 0], Nq=2).sparse(5)
+    b = Batch([0])
+    e = torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    q = torch.empty((0, 8, 64), dtype=torch.bfloat16, device="cuda")
+    att = Q4Attention(e[:, 0].contiguous(), e, q, b.cache)
+    att()
+    assert att.device_error() == 0
+
+
+@pytest.mark.parametrize("v_scale,q_scale", [
+    (1e-3, 1.0), (1e-6, 1.0), (100.0, 1.0), (1e4, 1.0), (3e4, 1.0), (1.0, 0.0), (1.0, 1e-30), (1.0, 8.0)])
+def test_sizes_of_values_and_queries(v_scale, q_scale):
+    """Scales from subnormal to near fp16's end, and scores from all equal to one token's."""
+    b = Batch([300, 40, 5], 16, 2, 4, 128, seed=7, q_scale=q_scale, v_scale=v_scale)
+    b.dense()
+    b.sparse(64)
+
+
+def test_scales_that_grow_along_a_request():
+    """A token's values a million times those before it, and the largest score late."""
+    b = Batch([2000], 16, 2, 4, 128, seed=8, v_scale=1e-2)
+    b.v[1500] *= 3e6
+    b.v[777] *= 1e3
+    b.k[1900] *= 4
+    b.write()
+    b.dense()
+
+
+def test_sm_scale():
+    b = Batch(LENS, 16, 2, 4, 64, 2, seed=9)
+    b.dense(sm_scale=0.5, causal=True)
+    b.sparse(20, sm_scale=0.01)
+
+
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+def test_tokens_that_a_query_does_not_see_are_without_influence(what):
+    """The last of four drafted tokens has no finite K and V: the three queries before it see
+    nothing of it, its own query gets NaN.  The same for a token that is not selected."""
+    b = Batch([37, 80, 4], 16, 2, 4, 128, 4, seed=10)
+    for e in b.starts[1:]:
+        b.k[e - 1, :, 3] = what
+        b.v[e - 1, :, 64:] = what
+    b.write()
+    att = Q4Attention(b.len_d, b.table, b.q, b.cache, causal=True, lse=True)
+    out = att()
+    assert bool(out[:, 3].isnan().all()) and bool(att.lse[:, 3].isnan().all())
+    b.Nq = 3
+    b.lens, lens = [n - 1 for n in b.lens], b.lens
+    starts = b.starts
+    k, v = b.k, b.v
+    # the restatement over the tokens that the first three queries see
+    keep = [i for s, e in zip(starts, starts[1:]) for i in range(s, e - 1)]
+    b.starts = np.concatenate([[0], np.cumsum(b.lens)]).tolist()
+    b.k, b.v = k[keep], v[keep]
+    b.check(out, att.lse, causal=True)
+    b.lens, b.starts, b.Nq = lens, starts, 4
+    lists = np.stack([np.stack([np.arange(3)] * 4)] * 3)
+    lists[2, 3] = [3, -1, 0]
+    att = Q4SparseAttention(b.len_d, b.table, i32(lists), b.q, b.cache, lse=True)
+    out = att()
+    assert bool(out[2, 3].isnan().all()) and bool(out[:2].isfinite().all())
+    assert bool(out[2, :3].isfinite().all())
+
+
+def test_queries_that_are_not_finite_stay_their_own():
+    b = Batch([50], 16, 2, 4, 64, seed=11)
+    q = b.q.clone()
+    b.q[0, 0, 3, 5] = float("nan")
+    b.q[0, 0, 6, 0] = float("inf")
+    att = Q4Attention(b.len_d, b.table, b.q, b.cache, lse=True)
+    out = att().clone()
+    assert bool(out[0, 0, [3, 6]].isnan().all())
+    b.q.copy_(q)
+    want = att()
+    keep = [0, 1, 2, 4, 5, 7]
+    assert torch.equal(out[0, 0, keep], want[0, 0, keep])
+
+
+def test_bad_entries_are_skipped_and_told():
+    b = Batch([64, 40, 33], 16, 2, 4, 64, seed=12)
+    table = b.tab.copy()
+    table[1, 1] = b.cache.k.shape[0]
+    att = Q4Attention(b.len_d, i32(table), b.q, b.cache, lse=True)
+    out = att()
+    assert att.device_error() == 1 and att.device_error() == 0
+    b.check(out, att.lse, rows=[0, 2])
+    lists = [[t] for t in (np.arange(64), np.r_[np.arange(16), np.arange(32, 40)], np.arange(33))]
+    b.check(out, att.lse, lists=lists)  # request 1 without the page's tokens
+    lists = np.array([[[0, 5, 64, 7]], [[-1, 39, 40, -2]], [[1, 2, 3, -1]]])
+    att = Q4SparseAttention(b.len_d, b.table, i32(lists), b.q, b.cache, lse=True)
+    out = att()
+    assert att.device_error() == 2
+    b.check(out, att.lse, lists=lists)
+    att = Q4Attention(i32([64, -3, 10 ** 6]), b.table, b.q, b.cache, lse=True)
+    out = att()
+    assert att.device_error() == 3
+    b.check(out, att.lse, rows=[0])
+    assert not out[1:].any()
+
+
+def test_runs_give_the_same_bits():
+    b = Batch([3000, 5000, 77], 16, 8, 8, 128, seed=13)
+    att = b.dense()
+    first, lse = att.out.clone(), att.lse.clone()
+    for _ in range(20):
+        att()
+        assert torch.equal(att.out, first) and torch.equal(att.lse, lse)
+
+
+def test_graphs_that_share_a_workspace_and_follow_lengths():
+    b = Batch([300, 500, 77], 16, 2, 4, 64, seed=14)
+    att = b.dense()
+    lists = b.lists(50)
+    sel = Q4SparseAttention(b.len_d, b.table, i32(lists), b.q, b.cache, trim=True, lse=True)
+    if sel.workspace.numel() <= att.workspace.numel():
+        sel.args.workspace, sel.args.workspace_bytes = att.args.workspace, att.args.workspace_bytes
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs = []
+    for a in (att, sel):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            a()
+        graphs.append(g)
+    lens = b.lens
+    for cut in (0, 1, 60, 76):
+        b.lens = [n - cut for n in lens]
+        b.len_d.copy_(i32(b.lens))
+        for g in graphs:
+            g.replay()
+        graphs[0].replay()
+        torch.cuda.synchronize()
+        full, b.lens = b.lens, lens
+        seen = [[np.arange(n)] for n in full]
+        b.check(att.out, att.lse, lists=seen)
+        short = []
+        for i, n in enumerate(full):  # trim: the first min(k, len) entries, those in reach
+            t = lists[i][0][:min(50, n)]
+            short.append([t[t < n]])
+        b.check(sel.out, sel.lse, lists=short)
+        b.lens = lens
+        if cut:
+            sel.device_error()
+
+
+def test_further_layers():
+    """One object over the queries and caches of several layers."""
+    b, c = (Batch([100, 30], 16, 2, 4, 64, seed=s) for s in (15, 15))
+    c.q = torch.randn_like(c.q.float()).to(torch.bfloat16)
+    c.k, c.v = c.k * 0.5, c.v * 2
+    c.write()
+    att = b.dense()
+    first = att.out.clone()
+    out = att.attend(c.q, c.cache)
+    c.check(out, att.lse)
+    with pytest.raises(ValueError):
+        att.attend(b.q[:, :, :4])
+    with pytest.raises(TypeError):
+        att.attend(b.q.float())
+    c.check(att(), att.lse)
+    assert torch.equal(att.attend(b.q, b.cache), first)
+
+
+def test_a_wait_that_runs_out_is_told():
+    """A limit far below what a first copy takes: the warps give up, the call ends with
+    device error 5 and the context stays usable."""
+    b = Batch([3000, 5000], 16, 8, 8, 128, seed=16)
+    for page_rows in (b, Batch([3000, 5000], 5, 8, 8, 128, seed=16)):
+        att = Q4Attention(page_rows.len_d, page_rows.table, page_rows.q, page_rows.cache,
+                          wait_limit=10)
+        att()
+        assert att.device_error() == 5
+        page_rows.dense()
+
+
+def test_long_tables_and_large_pools():
+    """Rows beyond 2^31 bytes of a pool."""
+    N, page, Hkv, D = 60000, 64, 8, 128
+    cache = Q4Cache(N, page, Hkv, D)
+    b = Batch([130], page, Hkv, 4, D, seed=17)
+    tab = np.array([[N - 1, 3, N - 2, -7]])
+    b.cache, b.tab, b.table = cache, tab, i32(tab)
+    b.write()
+    att = Q4Attention(b.len_d, b.table, b.q, cache, lse=True)
+    out = att()
+    small = Batch([130], page, Hkv, 4, D, seed=17)
+    want = small.dense()
+    assert torch.equal(out, want.out) and torch.equal(att.lse, want.lse)

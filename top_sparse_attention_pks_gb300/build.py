@@ -24,8 +24,8 @@ LIB = LIBDIR / "libpks.so"
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["pks_host.cpp", "k_indexer.cu", "k_topk.cu", "k_attention.cu", "k_residency.cu",
-           "k_mla.cu", "k_stage.cu", "k_pages.cu",
-           "k_prefix.cu"]
+           "k_mla.cu", "k_stage.cu", "k_pages.cu", "k_prefix.cu", "k_q4_rows.cu",
+           "k_q4_attention.cu"]
 
 
 def nvcc() -> str:
@@ -53,7 +53,8 @@ def _compile(src: Path, obj: Path, verbose: bool) -> str:
 def _stale(obj: Path, src: Path) -> bool:
     if not obj.exists():
         return True
-    deps = [src, CSRC / "pks_internal.h", CSRC / "tcgen05.cuh", INCLUDE / "pks.h"]
+    deps = [src, CSRC / "pks_internal.h", CSRC / "tcgen05.cuh", CSRC / "q4.cuh",
+            INCLUDE / "pks.h"]
     return obj.stat().st_mtime < max(d.stat().st_mtime for d in deps)
 
 

@@ -1,0 +1,1123 @@
+// Attention over a paged KV cache held in 4 bits, dense or over selected tokens.
+//
+// A cached value is m + s n (group of 32 values: s, m fp16; n 0..15), so with the
+// query's sums Q_b over the values of group b
+//   q . K = sum_b ( s_b sum_{d in b} q_d n_d  +  m_b Q_b )
+//   sum_t p_t V_t[d] = sum_t (p_t s_tb) n_td  +  sum_t p_t m_tb        (d in group b)
+// and both products run on the codes themselves (mma.sync, tokens or values as M,
+// the query rows of a KV head as N):
+//  - The bit pattern of n in a 16-bit word is the subnormal bf16 n 2^-133 (and fp16
+//    n 2^-24), one step up 16 n of it: eight codes become four operand registers
+//    with four ANDs and a shift, and no conversion.  Powers of two are put right in
+//    the queries (those at the odd places are a sixteenth) and at the end.
+//  - K: bf16, the queries scaled by a power of two, so that all products are exact.
+//    Each group's sum is scaled by s_b on its own (fp32); the m_b Q_b of all groups are
+//    one more MMA, Q_b cut into three fp16 pieces (33 bits).
+//  - V: fp16.  p s is rounded to fp16 once a group (2^-12 of it; p itself likewise);
+//    p is kept 2^11 to 2^15 times its size at the maximum so that small ones stay
+//    normal numbers, less where an s is large.  sum p m is one more MMA.
+// Maxima, sums, scores and accumulators are fp32.
+//
+// One persistent CTA an SM.  All (request, head group, row chunk) segments are cut into
+// stages of 16 tokens a consumer warp; the CTAs take equal runs of stages.  A
+// producer warp finds the tokens' rows (a batch of 256 tokens at a time, so that
+// its two dependent loads are rare) and fills a ring of stages; a consumer warp owns
+// one head and 16 tokens of every stage.  Segments that several CTAs hold parts of are
+// joined by k_q4_merge.
+
+#include <cuda_fp16.h>
+
+#include "pks_internal.h"
+#include "q4.cuh"
+#include "tcgen05.cuh"
+
+namespace pks {
+namespace {
+
+constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
+constexpr int kBatch = 256;    // tokens whose rows the producer finds at once
+constexpr int kMaxStages = 12;
+constexpr int kSmemMax = 227 * 1024 - 4096;  // dynamic; the rest is the static part
+constexpr int kBulkBytes = 2048;  // of a page, from which on its runs are copied whole
+constexpr int kFewRows = 4096;    // up to which a block joins a row, else a warp
+constexpr float kNone = -3e38f;  // reference of a row that has seen no token
+
+// Tokens of a warp's 16 as the rows of its MMA tiles, four bits each (lowest: row 0).
+// Lanes of one shared-memory access hold tokens whose records lie in different
+// banks: rows 2 i and 2 i + 1 must stand 64 bytes apart (mod 128), the rows 0, 2, 4, 6
+// and 1, 3, 5, 7 32 bytes.  By the distance between tokens: odd multiples of 16 bytes
+// (or permuted rows), odd multiples of 32, of 64 (every second access in two).
+constexpr uint64_t kOrderOdd = 0xbf9d7351ae8c6240ull;
+constexpr uint64_t kOrderTwo = 0xdfceb9a857463120ull;
+constexpr uint64_t kOrderFour = 0xefdcab9867542310ull;
+
+struct Q4Shape {
+  int Bv;            // requests; with selected tokens, requests times queries
+  int Hq, G, page_size, max_pages, num_pages;
+  int k, trim;       // entries a list, 0: dense
+  int lists;         // lists a request (1 when dense)
+  int Nq;            // query tokens a segment works on (1 with selected tokens)
+  int causal;
+  int R;             // query rows of a KV head: Nq * G
+  int HG, NHG, NRC;  // heads of a CTA, groups of them, chunks of rows
+  int WPH, TS;       // warps a head, tokens a stage
+  int row_bytes;     // of a token in the pool
+  int slice;         // of it what a head group takes: also the distance in shared memory
+  int swz_pool, swz_smem, bulk;
+  uint32_t chunk_magic;  // ceil(2^20 / chunks of a slice)
+  uint64_t order;
+  int stages, ring, scratch_at, nv_at;  // bytes of the ring; where scratch and lengths begin
+  int grid;
+};
+
+__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+      "{%8,%9}, {%0,%1,%2,%3};\n"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_bits(__half2 h) {
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ __half2 bits_half2(uint32_t u) {
+  return *reinterpret_cast<const __half2*>(&u);
+}
+__device__ __forceinline__ float low_half(uint32_t u) {
+  return __half2float(__low2half(bits_half2(u)));
+}
+
+// NW words from shared memory (8- or 16-byte aligned)
+template <int NW>
+__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[NW]) {
+  if constexpr (NW == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "r"(addr));
+  else if constexpr (NW == 2)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+  else
+    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(w[0]) : "r"(addr));
+}
+__device__ __forceinline__ void sts_zero8(uint32_t addr) {
+  asm volatile("st.shared.v2.b32 [%0], {%1, %1};\n" ::"r"(addr), "r"(0) : "memory");
+}
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n" ::"r"(
+          dst),
+      "l"(src), "r"(bytes), "r"(tc::smem_u32(bar))
+      : "memory");
+}
+
+// What a stage holds, from the producer to the consumers
+struct StageNote {
+  int v, c, p0, nv;     // segment (request or list, chunk), first position, positions in all
+  int flags, pad[3];
+  uint32_t mask[16];    // tokens present, of each 16
+};
+constexpr int kFirst = 1, kLast = 2, kWhole = 4, kSecond = 8;
+struct Desc {
+  int v, c, p0, nv, flags;
+};
+
+// First stage of CTA i when W stages go to n CTAs
+__device__ __forceinline__ int64_t first_stage(int64_t W, int n, int i) {
+  return W * i / n;
+}
+
+template <int D, int NT, int NW>
+__global__ void __launch_bounds__((NW + 1) * 32, 1)
+k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
+               const int32_t* __restrict__ lists, const __nv_bfloat16* __restrict__ q,
+               const uint8_t* __restrict__ pool_k, const uint8_t* __restrict__ pool_v,
+               __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
+               int64_t* __restrict__ prefix, float2* __restrict__ part_ml,
+               float* __restrict__ part_o, int32_t* __restrict__ err, const Q4Shape sh,
+               float scale_log2, long long wait_cycles) {
+  constexpr int NTHREADS = (NW + 1) * 32, NB = D / q4::kGroup, REC = q4::record_bytes(D);
+  constexpr int RC = 8 * NT;  // query rows a chunk
+  const float kNegInf = __int_as_float(0xff800000);
+  extern __shared__ __align__(1024) uint8_t smem[];
+  // bar_full: the producer's announcement (and its lanes' copies); bar_empty and
+  // bar_join: the consumer warps
+  __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
+  __shared__ StageNote s_note[kMaxStages];
+  __shared__ Desc s_desc[kBatch / 16];
+  __shared__ int s_row[kBatch], s_run[kBatch];
+  __shared__ int64_t s_warp[NW + 1], s_rest;
+  __shared__ int s_first, s_abort;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ring = tc::smem_u32(smem);
+  const int half = sh.TS * sh.slice;
+  int* s_nv = reinterpret_cast<int*>(smem + sh.nv_at);
+  const int consumers = sh.HG * sh.WPH;
+  if (tid == 0) {
+    for (int i = 0; i < sh.stages; ++i) {
+      tc::mbar_init(&bar_full[i], sh.bulk ? 1 : 33);
+      tc::mbar_init(&bar_empty[i], consumers);
+    }
+    tc::mbar_init(&bar_join, consumers);
+    tc::mbar_init_fence();
+    s_abort = 0;
+  }
+  pdl_wait(seq_lens, block_table, lists, q, pool_k, pool_v, out, lse, prefix, part_ml, part_o,
+           err);
+  pdl_launch_dependents();
+
+  // ---- the stages of every segment, and this CTA's run of them ----
+  const int per = (sh.Bv + NTHREADS - 1) / NTHREADS, v_lo = min(tid * per, sh.Bv),
+            v_hi = min(v_lo + per, sh.Bv);
+  const int chunks = sh.NHG * sh.NRC;
+  const int64_t cap = (int64_t)sh.max_pages * sh.page_size;
+  int64_t mine = 0;
+  for (int v = v_lo; v < v_hi; ++v) {
+    int n = seq_lens[v / sh.lists];
+    if (n < 0 || n > cap) {
+      *err = kErrLen;
+      n = 0;
+    }
+    if (sh.k) n = n == 0 ? 0 : sh.trim ? min(n, sh.k) : sh.k;
+    s_nv[v] = n;
+    mine += (int64_t)((n + sh.TS - 1) / sh.TS) * chunks;
+  }
+  int64_t upto = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+    if (lane >= d) upto += x;
+  }
+  if (lane == 31) s_warp[warp] = upto;
+  __syncthreads();
+  int64_t W = 0, before = 0;
+  for (int w = 0; w <= NW; ++w) {
+    if (w < warp) before += s_warp[w];
+    W += s_warp[w];
+  }
+  before += upto - mine;  // stages before this thread's first segment
+  const int n_ctas = (int)min((int64_t)sh.grid, W);
+  const int cta = blockIdx.x;
+  if (cta == 0) {
+    int64_t at = before;
+    for (int v = v_lo; v < v_hi; ++v) {
+      prefix[v] = at;
+      at += (int64_t)((s_nv[v] + sh.TS - 1) / sh.TS) * chunks;
+    }
+    if (tid == 0) prefix[sh.Bv] = W;
+  }
+  if (cta >= n_ctas) return;
+  const int64_t lo = first_stage(W, n_ctas, cta), hi = first_stage(W, n_ctas, cta + 1);
+  if (lo >= before && lo < before + mine) {
+    int64_t rest = lo - before;
+    int v = v_lo;
+    for (;; ++v) {
+      const int64_t units = (int64_t)((s_nv[v] + sh.TS - 1) / sh.TS) * chunks;
+      if (rest < units) break;
+      rest -= units;
+    }
+    s_first = v;
+    s_rest = rest;
+  }
+  __syncthreads();
+  const int64_t count = hi - lo;
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, wait_cycles)) != 0;
+  };
+  auto give_up = [&]() {
+    if (lane == 0) {
+      s_abort = 1;
+      *err = kErrTimeout;
+    }
+  };
+
+  if (warp == NW) {
+    // =========================== producer ===========================
+    int v = s_first;
+    int n = s_nv[v], T = (n + sh.TS - 1) / sh.TS;
+    int c = (int)(s_rest / T), tile = (int)(s_rest - (int64_t)c * T);
+    int64_t seg_at = lo - tile;  // first stage of the segment at hand
+    const int cpt = sh.slice / 16;
+    int stage = 0;
+    uint32_t phase = 0;  // of the ring's round
+    int64_t done = 0;
+    bool ok = true;
+    while (ok && done < count) {
+      const int nb = (int)min((int64_t)(kBatch / sh.TS), count - done);
+      // ---- which segments the next stages are of
+#pragma unroll 1
+      for (int j = 0; j < nb; ++j) {
+        const int64_t here = lo + done + j;
+        if (lane == 0) {
+          int f = 0;
+          if (tile == 0 || here == lo) f |= kFirst;
+          if (tile == T - 1 || here == hi - 1) f |= kLast;
+          if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
+          if (seg_at > lo) f |= kSecond;
+          s_desc[j] = {v, c, tile * sh.TS, n, f};
+        }
+        if (++tile == T) {
+          tile = 0;
+          seg_at += T;
+          if (++c == chunks) {
+            c = 0;
+            if (here + 1 < hi) {
+              do n = s_nv[++v];
+              while (n == 0);
+              T = (n + sh.TS - 1) / sh.TS;
+            }
+          }
+        }
+      }
+      __syncwarp();
+      // ---- the rows of their tokens
+      {
+        int t[kBatch / 32], b[kBatch / 32], pos[kBatch / 32];
+#pragma unroll
+        for (int i = 0; i < kBatch / 32; ++i) {
+          const int j = lane + 32 * i, st = j / sh.TS;
+          pos[i] = -1;
+          t[i] = -1;
+          b[i] = 0;
+          if (st < nb) {
+            const Desc d = s_desc[st];
+            const int p = d.p0 + j - st * sh.TS;
+            if (p < d.nv) {
+              pos[i] = p;
+              b[i] = d.v / sh.lists;
+              t[i] = sh.k ? lists[(int64_t)d.v * sh.k + p] : p;
+            }
+          }
+        }
+        if (sh.k) {
+#pragma unroll
+          for (int i = 0; i < kBatch / 32; ++i)
+            if (t[i] != -1) {
+              const int len = seq_lens[b[i]];
+              if (t[i] < 0 || t[i] >= len) {
+                *err = kErrToken;
+                t[i] = -1;
+              }
+            }
+        }
+        int page[kBatch / 32];
+#pragma unroll
+        for (int i = 0; i < kBatch / 32; ++i)
+          page[i] = t[i] < 0 ? -1
+                             : block_table[(int64_t)b[i] * sh.max_pages + t[i] / sh.page_size];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kBatch / 32; ++i) {
+          const int j = lane + 32 * i;
+          int row = -1, run = 0;
+          if (t[i] >= 0) {
+            if (page[i] < 0 || page[i] >= sh.num_pages) {
+              *err = kErrPage;
+            } else {
+              const int slot = t[i] % sh.page_size;
+              row = page[i] * sh.page_size + slot;
+              if (sh.bulk) {
+                // a copy from the first token of a page, or of the stage, on
+                const int st = j / sh.TS, at = j - st * sh.TS;
+                if (at == 0 || slot == 0)
+                  run = min(min(sh.page_size - slot, sh.TS - at), s_desc[st].nv - pos[i]);
+              } else {
+                run = slot & 7;
+              }
+            }
+          }
+          s_row[j] = row;
+          s_run[j] = run;
+        }
+        __syncwarp();
+      }
+      // ---- fill the stages
+#pragma unroll 1
+      for (int j = 0; j < nb; ++j) {
+        const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
+        if (done + j >= sh.stages) ok = wait(&bar_empty[stage], phase ^ 1);
+        if (!ok) break;
+        const Desc d = s_desc[j];
+        const int hg = d.c / sh.NRC;
+        StageNote* note = &s_note[stage];
+        int present = 0;
+        bool zeroed = false;
+        for (int i = 0; i * 32 < sh.TS; ++i) {
+          const int at = i * 32 + lane;
+          const bool here = at < sh.TS && s_row[j * sh.TS + at] >= 0;
+          const uint32_t m = __ballot_sync(0xffffffffu, here);
+          if (lane == 0) {
+            note->mask[2 * i] = m & 0xffffu;
+            note->mask[2 * i + 1] = m >> 16;
+          }
+          present += __popc(m);
+          if (at < sh.TS && !here) {
+            // no weight, but what the slot holds takes part in a product
+            zeroed = true;
+            const uint32_t x = sh.swz_smem ? q4::swizzle(at) : 0;
+            for (int h = 0; h < sh.HG; ++h)
+#pragma unroll
+              for (int o = 0; o < 4 * NB; o += 8)
+                sts_zero8(dst_v + at * sh.slice + ((h * REC + D / 2 + o) ^ x));
+          }
+        }
+        if (zeroed) tc::fence_async_smem();
+        if (lane == 0) {
+          note->v = d.v;
+          note->c = d.c;
+          note->p0 = d.p0;
+          note->nv = d.nv;
+          note->flags = d.flags;
+        }
+        __syncwarp();
+        if (sh.bulk) {
+          if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], 2u * present * sh.slice);
+          __syncwarp();
+          for (int at = lane; at < sh.TS; at += 32) {
+            const int run = s_run[j * sh.TS + at];
+            if (run > 0) {
+              const int64_t src = (int64_t)s_row[j * sh.TS + at] * sh.row_bytes;
+              const uint32_t o = at * sh.slice;
+              bulk_load(dst_k + o, pool_k + src, run * sh.slice, &bar_full[stage]);
+              bulk_load(dst_v + o, pool_v + src, run * sh.slice, &bar_full[stage]);
+            }
+          }
+        } else {
+          const int off = hg * sh.HG * REC, all = sh.TS * cpt;
+          for (int i = lane; i < all; i += 32) {
+            const int at = (int)((uint32_t)i * sh.chunk_magic >> 20), ch = i - at * cpt;
+            const int row = s_row[j * sh.TS + at];
+            if (row >= 0) {
+              const uint32_t xs = sh.swz_pool ? (uint32_t)s_run[j * sh.TS + at] << 4 : 0;
+              const uint32_t xd = sh.swz_smem ? q4::swizzle(at) : 0;
+              const int64_t src = (int64_t)row * sh.row_bytes + ((uint32_t)(off + 16 * ch) ^ xs);
+              const uint32_t o = at * sh.slice + ((uint32_t)(16 * ch) ^ xd);
+              tc::cp_async16(dst_k + o, pool_k + src, 16);
+              tc::cp_async16(dst_v + o, pool_v + src, 16);
+            }
+          }
+          tc::cp_async_arrive(&bar_full[stage]);
+          if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
+        }
+        if (++stage == sh.stages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      if (!ok) break;
+      done += nb;
+    }
+    if (!ok) {
+      give_up();
+      // the copies in flight land before the CTA gives its memory up: the last
+      // round's barriers complete by themselves
+      int s = stage;
+      uint32_t ph = phase;
+      for (int i = 0; i < sh.stages; ++i) {
+        if (s == 0) {
+          s = sh.stages;
+          ph ^= 1;
+        }
+        --s;
+        const long long t0 = clock64();
+        while (!tc::mbar_try_wait(&bar_full[s], ph) && clock64() - t0 < kWaitCycles) {
+        }
+      }
+    }
+    return;
+  }
+
+  // =========================== consumers ===========================
+  if (warp >= consumers) return;
+  const int h = warp / sh.WPH, sub = warp - h * sh.WPH;
+  const int g = lane >> 2, t = lane & 3;
+  auto token = [&](int r) { return sub * 16 + (int)(sh.order >> (4 * r) & 15); };
+  auto at = [&](int tok, int off) -> uint32_t {
+    return tok * sh.slice + ((uint32_t)(h * REC + off) ^ (sh.swz_smem ? q4::swizzle(tok) : 0));
+  };
+  // rows g and g + 8 of the tokens' tiles; K codes and pairs
+  const int tok0 = token(g), tok1 = token(g + 8);
+  const uint32_t k_code0 = at(tok0, 4 * NB * t), k_code1 = at(tok1, 4 * NB * t);
+  const uint32_t k_pair0 = at(tok0, D / 2), k_pair1 = at(tok1, D / 2);
+  // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile's order; V codes and pairs
+  uint32_t v_code[4], v_pair[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int tok = token(2 * t + (i & 1) + 8 * (i >> 1));
+    v_code[i] = at(tok, 2 * NB * g);
+    v_pair[i] = at(tok, D / 2);
+  }
+  const int m_word = 4 * (g & (NB - 1));
+
+  uint32_t qf[NT][NB][4], qs[NT][2];  // queries as B operands; the pieces of their sums
+  float cs[NT][2], ref[NT][2], sum[NT][2];  // of columns 2t, 2t + 1
+  int lim[NT][2], min_lim = 0;
+  float o[NT][NB][2][4], om[NT][4];
+  int sx = 0;  // log2 of the largest s, at least 0
+  int stage = 0;
+  uint32_t phase = 0, join_phase = 0;
+  bool ok = true;
+  auto join = [&]() {  // of the consumer warps
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bar_join);
+    ok = ok && wait(&bar_join, join_phase);
+    join_phase ^= 1;
+  };
+
+  for (int64_t done = 0; done < count; ++done) {
+    ok = wait(&bar_full[stage], phase);
+    if (!ok) break;
+    const StageNote* note = &s_note[stage];
+    const int flags = note->flags;
+    const uint32_t mask = note->mask[sub];
+    const int p0 = note->p0 + sub * 16;
+    if (flags & kFirst) {
+      // ---------------- the segment's queries ----------------
+      const int hg = note->c / sh.NRC, rc = note->c - hg * sh.NRC;
+      const int head = hg * sh.HG + h;
+      min_lim = note->nv;
+      if (sh.causal) min_lim -= sh.Nq - 1 - rc * RC / sh.G;
+      sx = 0;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = rc * RC + nt * 8 + g;
+        float x[NB][8];
+        if (r < sh.R) {
+          const int i = r / sh.G;
+          const int64_t row = ((int64_t)note->v * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint4 w = *reinterpret_cast<const uint4*>(q + row * D + 32 * b + 8 * t);
+            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[b][2 * e] = __uint_as_float(u[e] << 16);
+              x[b][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            }
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
+        }
+        float big = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[b][e]));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // the row times 2^p: its largest value in [2^120, 2^121)
+        const int e2 = max((int)(__float_as_uint(big) >> 23) - 127, -100);
+        const int p = 120 - e2;
+        const float f1 = __int_as_float((127 + (p >> 1)) << 23);
+        const float f2 = __int_as_float((127 + p - (p >> 1)) << 23);
+        float sums[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          sums[b] = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[b][e] = x[b][e] * f1 * f2;
+            sums[b] += x[b][e];
+          }
+          sums[b] += __shfl_xor_sync(0xffffffffu, sums[b], 1);
+          sums[b] += __shfl_xor_sync(0xffffffffu, sums[b], 2);
+          // values e and e + 4 of a word stand in one register; the odd ones come
+          // out of it 16 times too large
+          auto two = [&](int e, float f) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x[b][e] * f, x[b][e + 4] * f);
+            return *reinterpret_cast<const uint32_t*>(&y);
+          };
+          qf[nt][b][0] = two(0, 1.f);
+          qf[nt][b][1] = two(1, 0.0625f);
+          qf[nt][b][2] = two(2, 1.f);
+          qf[nt][b][3] = two(3, 0.0625f);
+        }
+        // the sums times 2^-112, below 2^14, in pieces: lanes with the same t & 1 (D =
+        // 128) hold two groups' pieces 0 to 3, for D = 64 all lanes
+        auto piece = [&](float y, int i) {
+          const __half h0 = __float2half_rn(y);
+          const float r1 = y - __half2float(h0);
+          const __half h1 = __float2half_rn(r1);
+          const __half h2 = __float2half_rn(r1 - __half2float(h1));
+          return i == 0 ? h0 : i == 1 ? h1 : i == 2 ? h2 : __ushort_as_half(0);
+        };
+        const float down = __int_as_float((127 - 112) << 23);
+        float y0 = sums[0] * down, y1 = sums[1] * down;
+        if constexpr (NB == 4) {
+          if (t & 1) {
+            y0 = sums[2] * down;
+            y1 = sums[3] * down;
+          }
+          qs[nt][0] = half2_bits(__halves2half2(piece(y0, t >> 1), piece(y1, t >> 1)));
+          qs[nt][1] = half2_bits(__halves2half2(piece(y0, 2 + (t >> 1)), piece(y1, 2 + (t >> 1))));
+        } else {
+          qs[nt][0] = half2_bits(__halves2half2(piece(y0, t), piece(y1, t)));
+          qs[nt][1] = 0;
+        }
+        // scores in powers of two: the accumulators' unit is 2^(133 - p)
+        const float mine_c = __int_as_float((127 + min(13 + e2, 128)) << 23) * scale_log2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          cs[nt][j] = __shfl_sync(0xffffffffu, mine_c, (2 * t + j) * 4);
+          ref[nt][j] = kNone;
+          sum[nt][j] = 0.f;
+          const int rr = rc * RC + nt * 8 + 2 * t + j;
+          lim[nt][j] = sh.causal ? note->nv - sh.Nq + min(rr / sh.G, sh.Nq - 1) + 1 : note->nv;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nt][b][m][e] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) om[nt][e] = 0.f;
+      }
+    }
+
+    if (mask) {
+      const uint32_t base_k = ring + (uint32_t)stage * 2 * half, base_v = base_k + half;
+      // ---------------- scores ----------------
+      float tot[NT][4];
+      {
+        uint32_t w0[NB], w1[NB], p0w[NB], p1w[NB];
+        lds(base_k + k_code0, w0);
+        lds(base_k + k_code1, w1);
+        lds(base_k + k_pair0, p0w);
+        lds(base_k + k_pair1, p1w);
+        uint32_t a0, a1;
+        if constexpr (NB == 4) {
+          a0 = __byte_perm(t & 1 ? p0w[2] : p0w[0], t & 1 ? p0w[3] : p0w[1], 0x7632);
+          a1 = __byte_perm(t & 1 ? p1w[2] : p1w[0], t & 1 ? p1w[3] : p1w[1], 0x7632);
+        } else {
+          a0 = __byte_perm(p0w[0], p0w[1], 0x7632);
+          a1 = __byte_perm(p1w[0], p1w[1], 0x7632);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          mma_f16(acc, a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
+          // units: 2^(p - 112) here, 2^(p - 133) below
+#pragma unroll
+          for (int e = 0; e < 4; ++e) tot[nt][e] = acc[e] * 4.76837158203125e-07f;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t x0 = w0[b], x1 = w1[b], y0 = x0 >> 8, y1 = x1 >> 8;
+          const float s0 = low_half(p0w[b]), s1 = low_half(p1w[b]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_bf16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
+                     qf[nt][b][0], qf[nt][b][1]);
+            mma_bf16(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
+                     qf[nt][b][2], qf[nt][b][3]);
+            tot[nt][0] = fmaf(acc[0], s0, tot[nt][0]);
+            tot[nt][1] = fmaf(acc[1], s0, tot[nt][1]);
+            tot[nt][2] = fmaf(acc[2], s1, tot[nt][2]);
+            tot[nt][3] = fmaf(acc[3], s1, tot[nt][3]);
+          }
+        }
+      }
+      const bool masked = mask != 0xffffu || p0 + 16 > min_lim;
+      if (masked) {
+        const bool on0 = mask >> (tok0 & 15) & 1, on1 = mask >> (tok1 & 15) & 1;
+        const int q0 = p0 + (tok0 & 15), q1 = p0 + (tok1 & 15);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (!on0 || q0 >= lim[nt][j]) tot[nt][j] = kNegInf;
+            if (!on1 || q1 >= lim[nt][j]) tot[nt][2 + j] = kNegInf;
+          }
+      }
+      // ---------------- V's scales ----------------
+      uint32_t s01[NB], s23[NB], ma0, ma2;
+      {
+        uint32_t w[4][NB], m[4][1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lds(base_v + v_pair[i], w[i]);
+          lds(base_v + v_pair[i] + m_word, m[i]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          s01[b] = __byte_perm(w[0][b], w[1][b], 0x5410);
+          s23[b] = __byte_perm(w[2][b], w[3][b], 0x5410);
+        }
+        ma0 = __byte_perm(m[0][0], m[1][0], 0x7632);
+        ma2 = __byte_perm(m[2][0], m[3][0], 0x7632);
+      }
+      __half2 s_max = __hmax2(bits_half2(s01[0]), bits_half2(s23[0]));
+#pragma unroll
+      for (int b = 1; b < NB; ++b)
+        s_max = __hmax2(s_max, __hmax2(bits_half2(s01[b]), bits_half2(s23[b])));
+      // p s must stay below 2^16, p being at most 2^(15 - sx)
+      if (__any_sync(0xffffffffu, fmaxf(__low2float(s_max), __high2float(s_max)) >
+                                      __int_as_float((127 + sx) << 23))) {
+        float top = fmaxf(__low2float(s_max), __high2float(s_max));
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1)
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int now = min((int)(__float_as_uint(top) >> 23) - 126, 16);
+        const float f = __int_as_float((127 - (now - sx)) << 23);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            ref[nt][j] += (float)(now - sx);
+            sum[nt][j] *= f;
+          }
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) o[nt][b][e >> 2][e & 3] *= f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) om[nt][e] *= f;
+        }
+        sx = now;
+      }
+      // ---------------- softmax ----------------
+      const float x_max = (float)(15 - sx);
+      float x[NT][4];
+      bool over = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          x[nt][e] = fmaf(tot[nt][e], cs[nt][e & 1], -ref[nt][e & 1]);
+          over |= x[nt][e] > x_max;
+        }
+      if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float top = fmaxf(tot[nt][j], tot[nt][2 + j]) * cs[nt][j];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1)
+              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float was = ref[nt][j];
+            if (top - was > x_max) {
+              ref[nt][j] = top - (x_max - 4.f);
+              const float f = ex2(was - ref[nt][j]);
+              sum[nt][j] *= f;
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                  o[nt][b][m][j] *= f;
+                  o[nt][b][m][2 + j] *= f;
+                }
+              om[nt][j] *= f;
+              om[nt][2 + j] *= f;
+            }
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(tot[nt][e], cs[nt][e & 1], -ref[nt][e & 1]);
+        }
+      }
+      uint32_t pt0[NT], pt1[NT], seen0[NT], seen1[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float p[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = ex2(x[nt][e]);
+        sum[nt][0] += p[0] + p[2];
+        sum[nt][1] += p[1] + p[3];
+        pt0[nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
+        pt1[nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
+        if (masked) {
+          auto seen = [&](int e) {
+            return (tot[nt][e] == kNegInf ? 0u : 0xffffu) |
+                   (tot[nt][e + 1] == kNegInf ? 0u : 0xffff0000u);
+          };
+          seen0[nt] = movmatrix_t(seen(0));
+          seen1[nt] = movmatrix_t(seen(2));
+        }
+      }
+      // ---------------- values ----------------
+      {
+        uint32_t w[4][NB / 2];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds(base_v + v_code[i], w[i]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(om[nt], ma0, 0u, ma2, 0u, pt0[nt], pt1[nt]);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
+          const uint32_t x01 = __byte_perm(w[0][b / 2], w[1][b / 2], sel);
+          const uint32_t x23 = __byte_perm(w[2][b / 2], w[3][b / 2], sel);
+          const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            uint32_t b0 = half2_bits(__hmul2(bits_half2(pt0[nt]), bits_half2(s01[b])));
+            uint32_t b1 = half2_bits(__hmul2(bits_half2(pt1[nt]), bits_half2(s23[b])));
+            if (masked) {  // (an s without a number must not reach rows that do not see it)
+              b0 &= seen0[nt];
+              b1 &= seen1[nt];
+            }
+            mma_f16(o[nt][b][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
+                    x23 & 0x00f000f0u, b0, b1);
+            mma_f16(o[nt][b][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
+                    y23 & 0x00f000f0u, b0, b1);
+          }
+        }
+      }
+    }
+    const int seg_v = note->v, seg_c = note->c;
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bar_empty[stage]);
+    if (++stage == sh.stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (!(flags & kLast)) continue;
+
+    // ---------------- end of the segment, or of the CTA's part of it ----------------
+    const int hg = seg_c / sh.NRC, rc = seg_c - hg * sh.NRC, head = hg * sh.HG + h;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1)
+          sum[nt][j] += __shfl_xor_sync(0xffffffffu, sum[nt][j], d);
+      }
+      // the codes' units, 2^-24 and (values 1 and 3 of four) 2^-20; plus sum p m
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const float m0 = __shfl_sync(0xffffffffu, om[nt][0], 4 * b + t);
+        const float m1 = __shfl_sync(0xffffffffu, om[nt][1], 4 * b + t);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          o[nt][b][m][0] = fmaf(o[nt][b][m][0], 16777216.f, m0);
+          o[nt][b][m][1] = fmaf(o[nt][b][m][1], 16777216.f, m1);
+          o[nt][b][m][2] = fmaf(o[nt][b][m][2], 1048576.f, m0);
+          o[nt][b][m][3] = fmaf(o[nt][b][m][3], 1048576.f, m1);
+        }
+      }
+    }
+    // the head's warps, pairwise through shared memory
+    constexpr int PER = NT * (8 * NB + 4);  // floats a lane: accumulators, sums, references
+    for (int d = 1; d < sh.WPH && ok; d <<= 1) {
+      const int pairs = sh.WPH / 2;
+      float* slot = reinterpret_cast<float*>(smem + sh.scratch_at) +
+                    (size_t)(h * pairs + sub / (2 * d)) * PER * 32 + lane;
+      if (sub % (2 * d) == d) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float* p = slot + nt * (8 * NB + 4) * 32;
+#pragma unroll
+          for (int i = 0; i < 8 * NB; ++i) p[i * 32] = o[nt][i >> 3][i >> 2 & 1][i & 3];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            p[(8 * NB + j) * 32] = sum[nt][j];
+            p[(8 * NB + 2 + j) * 32] = ref[nt][j];
+          }
+        }
+      }
+      join();
+      if (ok && sub % (2 * d) == 0 && sub + d < sh.WPH) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float* p = slot + nt * (8 * NB + 4) * 32;
+          float fa[2], fb[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float other = p[(8 * NB + 2 + j) * 32], top = fmaxf(ref[nt][j], other);
+            fa[j] = ex2(ref[nt][j] - top);
+            fb[j] = ex2(other - top);
+            ref[nt][j] = top;
+            sum[nt][j] = sum[nt][j] * fa[j] + p[(8 * NB + j) * 32] * fb[j];
+          }
+#pragma unroll
+          for (int i = 0; i < 8 * NB; ++i) {
+            float& a = o[nt][i >> 3][i >> 2 & 1][i & 3];
+            a = a * fa[i & 1] + p[i * 32] * fb[i & 1];
+          }
+        }
+      }
+      join();
+    }
+    if (!ok) break;
+    if (sub != 0) continue;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int col = nt * 8 + 2 * t + j, r = rc * RC + col;
+        if (r >= sh.R) continue;
+        if (flags & kWhole) {
+          const int i = r / sh.G;
+          const int64_t row = ((int64_t)seg_v * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
+          const float l = sum[nt][j];
+          const float f = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const __nv_bfloat162 a =
+                __floats2bfloat162_rn(o[nt][b][0][j] * f, o[nt][b][0][2 + j] * f);
+            const __nv_bfloat162 c =
+                __floats2bfloat162_rn(o[nt][b][1][j] * f, o[nt][b][1][2 + j] * f);
+            *reinterpret_cast<uint2*>(out + row * D + 32 * b + 4 * g) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                           *reinterpret_cast<const uint32_t*>(&c));
+          }
+          if (lse && g == 0)
+            lse[row] = l == 0.f ? kNegInf : (ref[nt][j] + log2f(l)) * 0.6931471805599453f;
+        } else {
+          const int64_t slot = ((int64_t)2 * cta + (flags & kSecond ? 1 : 0)) * sh.HG * RC +
+                               h * RC + col;
+          if (g == 0) part_ml[slot] = make_float2(ref[nt][j], sum[nt][j]);
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            *reinterpret_cast<float4*>(part_o + slot * D + 32 * b + 4 * g) =
+                make_float4(o[nt][b][0][j], o[nt][b][0][2 + j], o[nt][b][1][j],
+                            o[nt][b][1][2 + j]);
+        }
+      }
+  }
+  if (!ok) give_up();
+}
+
+// Rows whose segment several CTAs hold: sum the parts by the definition of the
+// softmax over a partition, w = 2^(reference - largest).  WARPS warps a row, each
+// taking every WARPS-th part.  Rows without tokens get zeros.
+template <int D, int WARPS>
+__global__ void __launch_bounds__(256)
+k_q4_merge(const int64_t* __restrict__ prefix, const float2* __restrict__ part_ml,
+           const float* __restrict__ part_o, __nv_bfloat16* __restrict__ out,
+           float* __restrict__ lse, const Q4Shape sh, int RC) {
+  constexpr int PL = D / 32;  // values a lane
+  __shared__ float s_o[WARPS > 1 ? 8 : 1][D];
+  __shared__ float2 s_ml[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int w = WARPS > 1 ? warp : 0;
+  pdl_wait(prefix, part_ml, part_o, out, lse);
+  pdl_launch_dependents();
+  const int64_t row = WARPS > 1 ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * 8 + warp;
+  if (row >= (int64_t)sh.Bv * sh.Nq * sh.Hq) return;  // (whole blocks where WARPS > 1)
+  const int64_t v = row / ((int64_t)sh.Nq * sh.Hq);
+  const int in = (int)(row - v * sh.Nq * sh.Hq), i = in / sh.Hq, hq = in - i * sh.Hq;
+  const int head = hq / sh.G, r = i * sh.G + hq - head * sh.G;
+  const int hg = head / sh.HG, h = head - hg * sh.HG, rc = r / RC, col = r - rc * RC;
+  const int64_t W = prefix[sh.Bv], p0 = prefix[v], units = prefix[v + 1] - p0;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float ref = kNone, l = 0.f;
+  bool write = units == 0;
+  if (units > 0) {
+    const int64_t T = units / (sh.NHG * sh.NRC), s0 = p0 + (hg * sh.NRC + rc) * T, s1 = s0 + T;
+    const int n = (int)min((int64_t)sh.grid, W);
+    const int first = (int)(((s0 + 1) * n - 1) / W), last = (int)((s1 * n - 1) / W);
+    write = first != last;
+    if (write) {
+      for (int c = first + w; c <= last; c += WARPS) {
+        const int second = c == first && first_stage(W, n, c) < s0 ? 1 : 0;
+        const int64_t slot = ((int64_t)2 * c + second) * sh.HG * RC + h * RC + col;
+        const float2 ml = part_ml[slot];
+        float4 x;
+        if constexpr (PL == 4) {
+          x = *reinterpret_cast<const float4*>(part_o + slot * D + 4 * lane);
+        } else {
+          const float2 y = *reinterpret_cast<const float2*>(part_o + slot * D + 2 * lane);
+          x = make_float4(y.x, y.y, 0.f, 0.f);
+        }
+        const float top = fmaxf(ref, ml.x), fa = ex2(ref - top), fb = ex2(ml.x - top);
+        ref = top;
+        l = l * fa + ml.y * fb;
+        acc.x = acc.x * fa + x.x * fb;
+        acc.y = acc.y * fa + x.y * fb;
+        acc.z = acc.z * fa + x.z * fb;
+        acc.w = acc.w * fa + x.w * fb;
+      }
+    }
+  }
+  if (!write) return;
+  if constexpr (WARPS > 1) {
+    if (lane == 0) s_ml[warp] = make_float2(ref, l);
+    if constexpr (PL == 4) *reinterpret_cast<float4*>(&s_o[warp][4 * lane]) = acc;
+    else *reinterpret_cast<float2*>(&s_o[warp][2 * lane]) = make_float2(acc.x, acc.y);
+    __syncthreads();
+    if (warp != 0) return;
+    acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    ref = kNone;
+    l = 0.f;
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) ref = fmaxf(ref, s_ml[u].x);
+#pragma unroll
+    for (int u = 0; u < WARPS; ++u) {
+      const float f = ex2(s_ml[u].x - ref);
+      l += s_ml[u].y * f;
+      acc.x += s_o[u][PL * lane] * f;
+      acc.y += s_o[u][PL * lane + 1] * f;
+      if constexpr (PL == 4) {
+        acc.z += s_o[u][PL * lane + 2] * f;
+        acc.w += s_o[u][PL * lane + 3] * f;
+      }
+    }
+  }
+  const float f = l == 0.f ? 0.f : 1.f / l;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x * f, acc.y * f);
+  __nv_bfloat16* to = out + row * D + PL * lane;
+  if constexpr (PL == 4) {
+    const __nv_bfloat162 c = __floats2bfloat162_rn(acc.z * f, acc.w * f);
+    *reinterpret_cast<uint2*>(to) = make_uint2(*reinterpret_cast<const uint32_t*>(&a),
+                                               *reinterpret_cast<const uint32_t*>(&c));
+  } else {
+    *reinterpret_cast<__nv_bfloat162*>(to) = a;
+  }
+  if (lse && lane == 0)
+    lse[row] = l == 0.f ? __int_as_float(0xff800000) : (ref + log2f(l)) * 0.6931471805599453f;
+}
+
+// Heads of a CTA: all of them, or the largest divisor whose records begin on 16 bytes
+int heads_of(int hkv, int D, int most) {
+  if (hkv <= most) return hkv;
+  for (int d = most; d > 0; --d)
+    if (hkv % d == 0 && d * q4::record_bytes(D) % 16 == 0) return d;
+  return 0;
+}
+
+struct Config {
+  Q4Shape sh;
+  int NT;
+  size_t smem;
+};
+
+Config configure(const pks_q4_attention_args& a) {
+  Config cf{};
+  Q4Shape& sh = cf.sh;
+  const int nq = a.n_queries > 1 ? a.n_queries : 1;
+  sh.lists = a.k ? nq : 1;
+  sh.Bv = a.B * sh.lists;
+  sh.Nq = a.k ? 1 : nq;
+  sh.Hq = a.Hq;
+  sh.G = a.Hq / a.Hkv;
+  sh.page_size = a.page_size;
+  sh.max_pages = a.max_pages;
+  sh.num_pages = a.num_pages;
+  sh.k = a.k;
+  sh.trim = a.trim;
+  sh.causal = a.k ? 0 : a.causal;
+  sh.R = sh.Nq * sh.G;
+  // Sixteen rows at a time on eight warps, or eight on sixteen; eight also where
+  // more heads than the eight warps can take would be read apart.
+  cf.NT = sh.R > 8 ? 2 : 1;
+  int hg = heads_of(a.Hkv, a.D, cf.NT == 2 ? 8 : 16);
+  if (cf.NT == 2 && a.Hkv > 8 && hg < 4) {
+    cf.NT = 1;
+    hg = heads_of(a.Hkv, a.D, 16);
+  }
+  if (hg == 0) return cf;  // (HG 0: no such shape)
+  const int warps = cf.NT == 2 ? 8 : 16;
+  sh.HG = hg;
+  sh.NHG = a.Hkv / hg;
+  sh.NRC = (sh.R + 8 * cf.NT - 1) / (8 * cf.NT);
+  sh.WPH = warps / hg;
+  sh.TS = 16 * sh.WPH;
+  sh.row_bytes = q4::token_bytes(a.Hkv, a.D);
+  sh.slice = sh.NHG == 1 ? sh.row_bytes : hg * q4::record_bytes(a.D);
+  sh.swz_pool = q4::swizzled(sh.row_bytes);
+  sh.swz_smem = q4::swizzled(sh.slice);
+  // whole runs of a page by one copy where its rows lie as the stage has them
+  sh.bulk = !a.k && sh.NHG == 1 && (!sh.swz_pool || a.page_size % 8 == 0) &&
+            (int64_t)a.page_size * sh.row_bytes >= kBulkBytes;
+  const int chunks = sh.slice / 16;
+  sh.chunk_magic = ((1u << 20) + chunks - 1) / chunks;
+  sh.order = sh.swz_smem || chunks % 2 ? kOrderOdd : chunks % 4 == 2 ? kOrderTwo : kOrderFour;
+  const int scratch = hg * (sh.WPH / 2) * cf.NT * (a.D / 4 + 4) * 32 * 4;
+  const int nv = (4 * sh.Bv + 15) / 16 * 16, stage = 2 * sh.TS * sh.slice;
+  int n = (kSmemMax - scratch - nv) / stage;
+  sh.stages = n > kMaxStages ? kMaxStages : n;
+  sh.ring = sh.stages * stage;
+  sh.scratch_at = sh.ring;
+  sh.nv_at = sh.ring + scratch;
+  cf.smem = (size_t)sh.nv_at + nv;
+  sh.grid = device_sm_count();
+  return cf;
+}
+
+template <int D, int NT, int NW>
+cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const Config& cf,
+                        cudaStream_t s) {
+  static bool done[64] = {false};
+  auto kern = k_q4_attention<D, NT, NW>;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!done[dev]) {
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
+    if (e != cudaSuccess) return e;
+    done[dev] = true;
+  }
+  const float scale = a.sm_scale > 0.f ? a.sm_scale : 1.f / sqrtf((float)a.D);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  int64_t* prefix = reinterpret_cast<int64_t*>(ws + L.prefix);
+  float2* ml = reinterpret_cast<float2*>(ws + L.part_ml);
+  float* po = reinterpret_cast<float*>(ws + L.part_o);
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
+  const Q4Shape& sh = cf.sh;
+  e = launch_ex(kern, dim3(sh.grid), dim3((NW + 1) * 32), cf.smem, s, /*pdl=*/true,
+                /*coop=*/false, a.seq_lens, a.block_table, a.topk_idx,
+                static_cast<const __nv_bfloat16*>(a.q), static_cast<const uint8_t*>(a.pool_k),
+                static_cast<const uint8_t*>(a.pool_v), out, a.lse, prefix, ml, po,
+                reinterpret_cast<int32_t*>(ws), sh, scale * 1.4426950408889634f,
+                a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles);
+  if (e != cudaSuccess) return e;
+  const int64_t rows = (int64_t)sh.Bv * sh.Nq * sh.Hq;
+  const bool few = rows <= kFewRows;
+  return launch_ex(few ? k_q4_merge<D, 8> : k_q4_merge<D, 1>,
+                   dim3((unsigned)(few ? rows : (rows + 7) / 8)), dim3(256), 0, s, /*pdl=*/true,
+                   /*coop=*/false, (const int64_t*)prefix, (const float2*)ml, (const float*)po,
+                   out, a.lse, sh, 8 * NT);
+}
+
+}  // namespace
+
+bool q4_supported(const pks_q4_attention_args& a) { return configure(a).sh.HG > 0; }
+
+Q4Layout q4_layout(const pks_q4_attention_args& a) {
+  const Config cf = configure(a);
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  Q4Layout L{};
+  L.prefix = 256;
+  L.part_ml = up(L.prefix + sizeof(int64_t) * (size_t)(cf.sh.Bv + 1));
+  // a CTA's first segment and its last
+  const size_t rows = (size_t)2 * cf.sh.grid * cf.sh.HG * 8 * cf.NT;
+  L.part_o = up(L.part_ml + sizeof(float2) * rows);
+  L.total = up(L.part_o + sizeof(float) * rows * (size_t)a.D);
+  return L;
+}
+
+cudaError_t launch_q4_attention(const pks_q4_attention_args& a, const Q4Layout& L,
+                                cudaStream_t s) {
+  const Config cf = configure(a);
+  if (a.D == 64)
+    return cf.NT == 2 ? launch_main<64, 2, 8>(a, L, cf, s) : launch_main<64, 1, 16>(a, L, cf, s);
+  return cf.NT == 2 ? launch_main<128, 2, 8>(a, L, cf, s) : launch_main<128, 1, 16>(a, L, cf, s);
+}
+
+}  // namespace pks

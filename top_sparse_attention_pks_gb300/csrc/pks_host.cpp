@@ -18,6 +18,7 @@
 #include <vector>
 
 #include "pks_internal.h"
+#include "q4.cuh"
 
 struct pks_pool {
   int32_t num_pages = 0;
@@ -787,6 +788,143 @@ pks_status pks_prefix_device_error(const pks_prefix_args* args, int32_t* code,
   pks_status st = prefix_check(args);
   if (st != PKS_OK) return st;
   if ((st = prefix_check_workspace(args, pks::prefix_layout(*args))) != PKS_OK) return st;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  int32_t* dev = static_cast<int32_t*>(args->workspace);
+  int32_t host = 0;
+  cudaError_t e = cudaMemcpyAsync(&host, dev, sizeof(int32_t), cudaMemcpyDeviceToHost, s);
+  if (e == cudaSuccess) e = cudaStreamSynchronize(s);
+  if (e == cudaSuccess) e = cudaMemsetAsync(dev, 0, sizeof(int32_t), s);
+  if (e != cudaSuccess) return PKS_ERR_CUDA;
+  *code = host;
+  return PKS_OK;
+}
+
+// ---------------------------------------------------------- 4-bit cache ---
+
+namespace {
+constexpr int kQ4MaxHeads = 1024;
+
+pks_status q4_check_pool(int B, int Hkv, int D, int page_size, int max_pages, int num_pages) {
+  if (B < 0 || Hkv < 1 || D < 1 || page_size < 1 || max_pages < 1 || num_pages < 1)
+    return PKS_ERR_INVALID;
+  if (D != 64 && D != 128) return PKS_ERR_UNSUPPORTED;
+  if (B > pks::kMaxB || Hkv > kQ4MaxHeads) return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)num_pages * page_size > INT32_MAX) return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)max_pages * page_size > pks::kMaxLen) return PKS_ERR_UNSUPPORTED;
+  return PKS_OK;
+}
+
+pks_status q4_rows(const pks_q4_rows_args* a, bool write, pks_stream stream) {
+  if (!a || a->n_rows < 0 || a->dtype < PKS_Q4_BF16 || a->dtype > PKS_Q4_FP32)
+    return PKS_ERR_INVALID;
+  pks_status st = q4_check_pool(a->B, a->Hkv, a->D, a->page_size, a->max_pages, a->num_pages);
+  if (st != PKS_OK) return st;
+  const int per16 = a->dtype == PKS_Q4_FP32 ? 4 : 8;
+  for (int64_t x : {a->k_row, a->k_head, a->v_row, a->v_head})
+    if (x < 0 || x % per16 != 0) return PKS_ERR_INVALID;
+  if (a->B == 0 || a->n_rows == 0) return PKS_OK;
+  if (!a->seq_lens || !a->block_table || !a->starts) return PKS_ERR_INVALID;
+  for (const void* p : {(const void*)a->k, (const void*)a->v, (const void*)a->pool_k,
+                        (const void*)a->pool_v})
+    if (!p || !pks::aligned16(p)) return PKS_ERR_INVALID;
+  return pks::from_cuda(
+      pks::launch_q4_rows(*a, write, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+pks_status q4_check(const pks_q4_attention_args* a) {
+  if (!a) return PKS_ERR_INVALID;
+  if (a->Hq < 1 || a->n_queries < 0 || a->causal < 0 || a->causal > 1 || a->k < 0 ||
+      a->trim < 0 || a->trim > 1 || a->wait_limit < 0 || a->reserved != 0 ||
+      !(a->sm_scale >= 0.f) || std::isinf(a->sm_scale))
+    return PKS_ERR_INVALID;
+  pks_status st = q4_check_pool(a->B, a->Hkv, a->D, a->page_size, a->max_pages, a->num_pages);
+  if (st != PKS_OK) return st;
+  if (a->Hq % a->Hkv != 0 || (a->k && a->causal) || (!a->k && a->trim)) return PKS_ERR_INVALID;
+  if (a->Hq / a->Hkv > 16 || a->n_queries > pks::kQ4MaxQueries || a->k > pks::kMaxK)
+    return PKS_ERR_UNSUPPORTED;
+  if ((int64_t)a->B * std::max(1, a->n_queries) > pks::kMaxB) return PKS_ERR_UNSUPPORTED;
+  return pks::q4_supported(*a) ? PKS_OK : PKS_ERR_UNSUPPORTED;
+}
+
+pks_status q4_check_workspace(const pks_q4_attention_args* a, const pks::Q4Layout& L) {
+  if (!a->workspace || (reinterpret_cast<uintptr_t>(a->workspace) & (pks::kAlign - 1)) != 0 ||
+      a->workspace_bytes < L.total)
+    return PKS_ERR_WORKSPACE;
+  return PKS_OK;
+}
+
+// all that a call checks before it launches
+pks_status q4_check_call(const pks_q4_attention_args* a, bool sparse) {
+  const pks_status st = q4_check(a);
+  if (st != PKS_OK) return st;
+  if (sparse != (a->k > 0)) return PKS_ERR_INVALID;
+  if (a->B > 0) {
+    if (!a->seq_lens || !a->block_table || (sparse && !a->topk_idx)) return PKS_ERR_INVALID;
+    for (const void* p : {a->q, a->pool_k, a->pool_v, (const void*)a->out})
+      if (!p || !pks::aligned16(p)) return PKS_ERR_INVALID;
+  }
+  return q4_check_workspace(a, pks::q4_layout(*a));
+}
+
+pks_status q4_launch(const pks_q4_attention_args* a, pks_stream stream) {
+  if (a->B == 0) return PKS_OK;
+  return pks::from_cuda(
+      pks::launch_q4_attention(*a, pks::q4_layout(*a), reinterpret_cast<cudaStream_t>(stream)));
+}
+}  // namespace
+
+pks_status pks_q4_token_bytes(int32_t Hkv, int32_t D, size_t* bytes) {
+  if (!bytes || Hkv < 1) return PKS_ERR_INVALID;
+  if ((D != 64 && D != 128) || Hkv > kQ4MaxHeads) return PKS_ERR_UNSUPPORTED;
+  *bytes = (size_t)pks::q4::token_bytes(Hkv, D);
+  return PKS_OK;
+}
+
+pks_status pks_q4_write(const pks_q4_rows_args* args, pks_stream stream) {
+  return q4_rows(args, /*write=*/true, stream);
+}
+
+pks_status pks_q4_read(const pks_q4_rows_args* args, pks_stream stream) {
+  return q4_rows(args, /*write=*/false, stream);
+}
+
+pks_status pks_q4_workspace_size(const pks_q4_attention_args* args, size_t* bytes) {
+  if (!bytes) return PKS_ERR_INVALID;
+  const pks_status st = q4_check(args);
+  if (st != PKS_OK) return st;
+  *bytes = pks::q4_layout(*args).total;
+  return PKS_OK;
+}
+
+pks_status pks_q4_attention(const pks_q4_attention_args* args, pks_stream stream) {
+  const pks_status st = q4_check_call(args, /*sparse=*/false);
+  return st != PKS_OK ? st : q4_launch(args, stream);
+}
+
+pks_status pks_q4_sparse_attention(const pks_q4_attention_args* args, pks_stream stream) {
+  const pks_status st = q4_check_call(args, /*sparse=*/true);
+  return st != PKS_OK ? st : q4_launch(args, stream);
+}
+
+pks_status pks_q4_decode_step(const pks_decode_args* select,
+                              const pks_q4_attention_args* attention, pks_stream stream) {
+  if (!select) return PKS_ERR_INVALID;
+  pks_status st = q4_check_call(attention, /*sparse=*/true);
+  if (st != PKS_OK) return st;
+  if (select->B != attention->B || select->k != attention->k ||
+      std::max(1, select->n_queries) != std::max(1, attention->n_queries) ||
+      select->topk_idx != attention->topk_idx)
+    return PKS_ERR_INVALID;
+  st = decode_impl(select, stream, nullptr, /*attention=*/false);
+  return st != PKS_OK ? st : q4_launch(attention, stream);
+}
+
+pks_status pks_q4_device_error(const pks_q4_attention_args* args, int32_t* code,
+                               pks_stream stream) {
+  if (!code) return PKS_ERR_INVALID;
+  pks_status st = q4_check(args);
+  if (st != PKS_OK) return st;
+  if ((st = q4_check_workspace(args, pks::q4_layout(*args))) != PKS_OK) return st;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   int32_t* dev = static_cast<int32_t*>(args->workspace);
   int32_t host = 0;

@@ -228,6 +228,18 @@ cudaError_t launch_pages_extend(const pks_pages_args& a, const PagesLayout& L, c
 cudaError_t launch_pages_compact(const pks_pages_args& a, const PagesLayout& L, int32_t* page_map,
                                  cudaStream_t s);
 
+// ---- 4-bit cache (k_q4_rows.cu, k_q4_attention.cu): byte offsets inside the
+// workspace; its first word is the device error word
+struct Q4Layout {
+  size_t prefix, part_ml, part_o, total;
+};
+constexpr int kQ4MaxQueries = 64;
+bool q4_supported(const pks_q4_attention_args& a);
+Q4Layout q4_layout(const pks_q4_attention_args& a);
+cudaError_t launch_q4_rows(const pks_q4_rows_args& a, bool write, cudaStream_t s);
+cudaError_t launch_q4_attention(const pks_q4_attention_args& a, const Q4Layout& L,
+                                cudaStream_t s);
+
 // Allocation-free attention (pks_sparse_attention_static): bytes of the
 // file-scope device scratch array, the least any call with these shapes
 // needs (one attention CTA; host only), the array's address on the current

@@ -196,6 +196,39 @@ class MlaAttention:
         return pks.pks_mla_device_error(self.args, stream)
 
 
+def _select_args(t: dict, topk_idx, num_pages: int, page_size: int, topk_mode: int):
+    """Selection arguments: the indexer and top-k fields of pks_decode_args (the GQA
+    attention fields stay unset; select does not read them)."""
+    a = pks.pks_decode_args()
+    B = t["seq_lens"].shape[0]
+    Hi, Di = t["q_idx"].shape[-2:]
+    a.B, a.Hq, a.Hkv, a.D, a.Hi, a.Di = int(B), 1, 1, 64, int(Hi), int(Di)
+    a.page_size, a.max_pages = int(page_size), int(t["block_table"].shape[1])
+    a.num_pages, a.k = int(num_pages), int(topk_idx.shape[-1])
+    a.seq_lens = pks._dptr(t["seq_lens"], torch.int32, "seq_lens")
+    a.block_table = pks._dptr(t["block_table"], torch.int32, "block_table")
+    a.q_idx = pks._dptr(t["q_idx"], torch.int8, "q_idx")
+    a.w_idx = pks._dptr(t.get("w_idx"), torch.int32, "w_idx")
+    a.idx_k = pks._dptr(t["idx_k"], torch.int8, "idx_k")
+    a.topk_idx = pks._dptr(topk_idx, torch.int32, "topk_idx")
+    a.topk_mode = int(topk_mode)
+    # real-valued head weights and FP8 e4m3 queries/keys (DSA's indexer)
+    if t.get("w_idx_f") is not None:
+        a.w_idx_f = pks._dptr(t["w_idx_f"], torch.float32, "w_idx_f")
+    a.idx_fp8 = 1 if t.get("idx_fp8") else 0
+    return a
+
+
+def _select_workspace(a, device, stream) -> torch.Tensor:
+    nbytes = pks.pks_decode_workspace_size(a)
+    with pks._on_stream(stream):
+        ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    a.workspace = ws.data_ptr()
+    a.workspace_bytes = ws.numel()
+    pks.pks_decode_workspace_init(a, stream)
+    return ws
+
+
 class MlaDecodeStep:
     """The DSA decode step with MLA attention (``pks_mla_decode_step``): indexer
     scan and top-k, then the sparse MLA over the selected tokens.
@@ -210,30 +243,9 @@ class MlaDecodeStep:
         B = q.shape[0]
         self.k = int(k)
         self.topk_idx = torch.empty((B, self.k), dtype=torch.int32, device=dev)
-        # selection arguments: the indexer and top-k fields of pks_decode_args
-        # (the GQA attention fields stay unset; select does not read them)
-        a = pks.pks_decode_args()
         npages, P, _ = kv.shape
-        _, Hi, Di = t["q_idx"].shape
-        a.B, a.Hq, a.Hkv, a.D, a.Hi, a.Di = int(B), 1, 1, 64, int(Hi), int(Di)
-        a.page_size, a.max_pages = int(P), int(t["block_table"].shape[1])
-        a.num_pages, a.k = int(npages), self.k
-        a.seq_lens = pks._dptr(t["seq_lens"], torch.int32, "seq_lens")
-        a.block_table = pks._dptr(t["block_table"], torch.int32, "block_table")
-        a.q_idx = pks._dptr(t["q_idx"], torch.int8, "q_idx")
-        a.w_idx = pks._dptr(t.get("w_idx"), torch.int32, "w_idx")
-        a.idx_k = pks._dptr(t["idx_k"], torch.int8, "idx_k")
-        a.topk_idx = pks._dptr(self.topk_idx, torch.int32, "topk_idx")
-        a.topk_mode = int(topk_mode)
-        # real-valued head weights and FP8 e4m3 queries/keys (DSA's indexer)
-        if t.get("w_idx_f") is not None:
-            a.w_idx_f = pks._dptr(t["w_idx_f"], torch.float32, "w_idx_f")
-        a.idx_fp8 = 1 if t.get("idx_fp8") else 0
-        nbytes = pks.pks_decode_workspace_size(a)
-        self.select_workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
-        a.workspace = self.select_workspace.data_ptr()
-        a.workspace_bytes = self.select_workspace.numel()
-        pks.pks_decode_workspace_init(a, stream)
+        a = _select_args(t, self.topk_idx, npages, P, topk_mode)
+        self.select_workspace = _select_workspace(a, dev, stream)
         self.select_args = a
         self.attention = MlaAttention(t["seq_lens"], t["block_table"], self.topk_idx, q, kv,
                                       sm_scale=sm_scale, trim=True, splits=splits)
@@ -375,3 +387,174 @@ class PageTable:
 
     def device_error(self, stream=None) -> int:
         return pks.pks_pages_device_error(self.args, stream)
+
+
+class Q4Cache:
+    """A paged K/V cache held in 4 bits (``pks_q4_write`` and ``pks_q4_read``): the pools
+    ``k`` and ``v``, uint8 [num_pages, page_size, token_bytes], which move with the pages of a
+    ``PageTable(pools=[cache.k, cache.v])``.  Allocated, with zeros, on ``stream`` (default:
+    torch's current stream): calls on another stream have to wait for that one.
+
+    Rows come packed: rows starts[b] .. starts[b + 1] of k and v [n, Hkv, D] (bfloat16,
+    float16 or float32, any row and head strides of 16 bytes) are the last tokens of request
+    b, whose length counts them.  Rows from starts[B] on are left alone."""
+
+    def __init__(self, num_pages: int, page_size: int, Hkv: int, D: int, device=None, stream=None):
+        row = pks.pks_q4_token_bytes(Hkv, D)
+        if device is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        with pks._on_stream(stream):
+            shape = (int(num_pages), int(page_size), row)
+            self.k = torch.zeros(shape, dtype=torch.uint8, device=device)
+            self.v = torch.zeros(shape, dtype=torch.uint8, device=device)
+            self.error = torch.zeros(1, dtype=torch.int32, device=device)
+        self.Hkv, self.D = int(Hkv), int(D)
+        pks._on_current_device(self.k)
+
+    def _args(self, k, v, seq_lens, block_table, starts):
+        pks._on_current_device(self.k, k, v, seq_lens, block_table, starts)
+        if tuple(k.shape[1:]) != (self.Hkv, self.D):
+            raise ValueError(f"rows must be [n, {self.Hkv}, {self.D}]")
+        return pks.make_q4_rows_args(k=k, v=v, seq_lens=seq_lens, block_table=block_table,
+                                     starts=starts, pool_k=self.k, pool_v=self.v,
+                                     error=self.error)
+
+    def write(self, k, v, seq_lens, block_table, starts, stream=None):
+        """Quantise the rows of k and v into their pages."""
+        pks.pks_q4_write(self._args(k, v, seq_lens, block_table, starts), stream)
+
+    def read(self, seq_lens, block_table, starts, k, v, stream=None):
+        """Fill k and v with the values that the cached rows stand for."""
+        pks.pks_q4_read(self._args(k, v, seq_lens, block_table, starts), stream)
+        return k, v
+
+    def device_error(self, stream=None) -> int:
+        """The last row's fault since this was last asked (1 page, 2 starts, 3 length), or 0;
+        synchronises the stream."""
+        with pks._on_stream(stream):
+            code = int(self.error.item())
+            if code:
+                self.error.zero_()
+        return code
+
+
+class Q4Attention:
+    """Dense decode attention over a ``Q4Cache`` (``pks_q4_attention``): q [B, Hq, D] or
+    [B, Nq, Hq, D] (query tokens at the end of each request, ``causal`` among themselves).
+    Owns ``out``, ``lse`` (when asked for) and the workspace, allocated and cleared on
+    ``stream`` (default: torch's current stream): calls on another stream have to wait for
+    that one.  ``attend(q, cache)`` serves further layers with tensors of the same shapes,
+    which later calls keep to (a call that is refused leaves those before it in place).  One
+    object's calls run one after another: their workspace is one."""
+
+    _entry = staticmethod(pks.pks_q4_attention)
+
+    def __init__(self, seq_lens, block_table, q, cache: Q4Cache, causal: bool = False,
+                 sm_scale: float = 0.0, lse: bool = False, wait_limit: int = 0, stream=None):
+        self._build(stream, lse, cache, q, seq_lens=seq_lens, block_table=block_table,
+                    causal=causal, sm_scale=sm_scale, wait_limit=wait_limit)
+
+    def _build(self, stream, lse, cache, q, **kw):
+        pks._on_current_device(q, cache.k, kw["seq_lens"], kw["block_table"], kw.get("topk_idx"))
+        if q.shape[-1] != cache.D:
+            raise ValueError("q and the cache differ in D")
+        dev = q.device
+        with pks._on_stream(stream):
+            self.out = torch.empty(q.shape, dtype=torch.bfloat16, device=dev)
+            self.lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if lse else None
+        kw.update(q=q, pool_k=cache.k, pool_v=cache.v, Hkv=cache.Hkv, out=self.out, lse=self.lse)
+        nbytes = pks.pks_q4_workspace_size(pks.make_q4_attention_args(**kw))
+        with pks._on_stream(stream):
+            self.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+            self.workspace[:256].zero_()
+        self.args = pks.make_q4_attention_args(workspace=self.workspace, **kw)
+        self._keep = [q, cache, kw["seq_lens"], kw["block_table"], kw.get("topk_idx")]
+
+    def attend(self, q=None, cache=None, stream=None):
+        was_q, was = self._keep[:2]
+        if q is not None and (q.shape != was_q.shape or q.device != was_q.device):
+            raise ValueError("q must have the shape and device it was built with")
+        if cache is not None and (cache.k.shape != was.k.shape or cache.k.device != was.k.device
+                                  or (cache.Hkv, cache.D) != (was.Hkv, was.D)):
+            raise ValueError("the cache must have the shape and device it was built with")
+        new = {}
+        if q is not None:
+            new["q"] = pks._dptr(q, torch.bfloat16, "q")
+        if cache is not None:
+            new["pool_k"] = pks._dptr(cache.k, torch.uint8, "pool_k")
+            new["pool_v"] = pks._dptr(cache.v, torch.uint8, "pool_v")
+        pks._on_current_device(self.out)
+        old = {name: getattr(self.args, name) for name in new}
+        for name, ptr in new.items():
+            setattr(self.args, name, ptr)
+        try:
+            self._entry(self.args, stream)
+        except BaseException:
+            for name, ptr in old.items():
+                setattr(self.args, name, ptr)
+            raise
+        if q is not None:
+            self._keep[0] = q
+        if cache is not None:
+            self._keep[1] = cache
+        return self.out
+
+    def __call__(self, stream=None):
+        pks._on_current_device(self.out)
+        self._entry(self.args, stream)
+        return self.out
+
+    def device_error(self, stream=None) -> int:
+        return pks.pks_q4_device_error(self.args, stream)
+
+
+class Q4SparseAttention(Q4Attention):
+    """Attention over selected tokens of a ``Q4Cache`` (``pks_q4_sparse_attention``): topk_idx
+    [B, k], or [B, Nq, k] with q [B, Nq, Hq, D] (int32 positions, -1: none).  ``trim``: every
+    list holds its entries first, and no more than its request has tokens."""
+
+    _entry = staticmethod(pks.pks_q4_sparse_attention)
+
+    def __init__(self, seq_lens, block_table, topk_idx, q, cache: Q4Cache, sm_scale: float = 0.0,
+                 trim: bool = False, lse: bool = False, wait_limit: int = 0, stream=None):
+        self._build(stream, lse, cache, q, seq_lens=seq_lens, block_table=block_table,
+                    topk_idx=topk_idx, trim=trim, sm_scale=sm_scale, wait_limit=wait_limit)
+
+
+class Q4DecodeStep:
+    """The sparse decode step over a ``Q4Cache`` (``pks_q4_decode_step``): indexer scan and
+    top-k, then attention over the selected tokens.  ``tensors``: seq_lens, block_table, q,
+    q_idx, w_idx (or w_idx_f), idx_k as for ``SparseDecodeStep``."""
+
+    def __init__(self, tensors: dict, cache: Q4Cache, k: int, topk_mode: int = 0,
+                 sm_scale: float = 0.0, lse: bool = False, stream=None):
+        t = dict(tensors)
+        q = t["q"]
+        self.k = int(k)
+        with pks._on_stream(stream):
+            self.topk_idx = torch.empty(tuple(q.shape[:-2]) + (self.k,), dtype=torch.int32,
+                                        device=q.device)
+        a = _select_args(t, self.topk_idx, int(cache.k.shape[0]), int(cache.k.shape[1]), topk_mode)
+        if q.dim() == 4:
+            a.n_queries = int(q.shape[1])
+        self.select_workspace = _select_workspace(a, q.device, stream)
+        self.select_args = a
+        self.attention = Q4SparseAttention(t["seq_lens"], t["block_table"], self.topk_idx, q,
+                                           cache, sm_scale=sm_scale, trim=True, lse=lse,
+                                           stream=stream)
+        self.out, self.lse = self.attention.out, self.attention.lse
+        self.tensors = t
+
+    def select(self, stream=None):
+        pks.pks_decode_select(self.select_args, stream)
+        return self.topk_idx
+
+    def __call__(self, stream=None):
+        pks._on_current_device(self.out)
+        pks.pks_q4_decode_step(self.select_args, self.attention.args, stream)
+        return self.out, self.topk_idx
+
+    def device_error(self, stream=None) -> int:
+        """Of the selection, else of the attention."""
+        return pks.pks_decode_device_error(self.select_args, stream) or \
+            self.attention.device_error(stream)

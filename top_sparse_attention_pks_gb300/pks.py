@@ -100,6 +100,37 @@ class pks_pages_args(ctypes.Structure):
     ]
 
 
+PKS_Q4_BF16, PKS_Q4_FP16, PKS_Q4_FP32 = 0, 1, 2
+_Q4_TYPES = {torch.bfloat16: PKS_Q4_BF16, torch.float16: PKS_Q4_FP16, torch.float32: PKS_Q4_FP32}
+
+
+class pks_q4_rows_args(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("n_rows", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("dtype", ctypes.c_int32), ("seq_lens", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("starts", ctypes.c_void_p), ("k", ctypes.c_void_p),
+        ("v", ctypes.c_void_p), ("k_row", ctypes.c_int64), ("k_head", ctypes.c_int64),
+        ("v_row", ctypes.c_int64), ("v_head", ctypes.c_int64), ("pool_k", ctypes.c_void_p),
+        ("pool_v", ctypes.c_void_p), ("error", ctypes.c_void_p),
+    ]
+
+
+class pks_q4_attention_args(ctypes.Structure):
+    _fields_ = [
+        ("B", ctypes.c_int32), ("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32),
+        ("D", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+        ("num_pages", ctypes.c_int32), ("n_queries", ctypes.c_int32),
+        ("causal", ctypes.c_int32), ("k", ctypes.c_int32), ("trim", ctypes.c_int32),
+        ("wait_limit", ctypes.c_int32), ("sm_scale", ctypes.c_float),
+        ("reserved", ctypes.c_int32), ("seq_lens", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("topk_idx", ctypes.c_void_p), ("q", ctypes.c_void_p),
+        ("pool_k", ctypes.c_void_p), ("pool_v", ctypes.c_void_p), ("out", ctypes.c_void_p),
+        ("lse", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+        ("workspace_bytes", ctypes.c_size_t),
+    ]
+
+
 def library_path() -> Path:
     return _LIB_PATH
 
@@ -207,6 +238,21 @@ def _declare(L):
     L.pks_pages_compact.restype = _ST
     L.pks_pages_device_error.argtypes = [_PG, ctypes.POINTER(ctypes.c_int32), _P]
     L.pks_pages_device_error.restype = _ST
+    L.pks_q4_token_bytes.argtypes = [_I32, _I32, ctypes.POINTER(ctypes.c_size_t)]
+    L.pks_q4_token_bytes.restype = _ST
+    for f in (L.pks_q4_write, L.pks_q4_read):
+        f.argtypes = [ctypes.POINTER(pks_q4_rows_args), _P]
+        f.restype = _ST
+    _PQ = ctypes.POINTER(pks_q4_attention_args)
+    L.pks_q4_workspace_size.argtypes = [_PQ, ctypes.POINTER(ctypes.c_size_t)]
+    L.pks_q4_workspace_size.restype = _ST
+    for f in (L.pks_q4_attention, L.pks_q4_sparse_attention):
+        f.argtypes = [_PQ, _P]
+        f.restype = _ST
+    L.pks_q4_decode_step.argtypes = [_PARGS, _PQ, _P]
+    L.pks_q4_decode_step.restype = _ST
+    L.pks_q4_device_error.argtypes = [_PQ, ctypes.POINTER(ctypes.c_int32), _P]
+    L.pks_q4_device_error.restype = _ST
     L.pks_stage_copy.argtypes = [ctypes.POINTER(pks_copy_range), _I32, _P]
     L.pks_stage_copy.restype = _ST
 
@@ -825,4 +871,133 @@ def pks_pages_device_error(args: pks_pages_args, stream=None) -> int:
     code = ctypes.c_int32()
     _check(lib().pks_pages_device_error(ctypes.byref(args), ctypes.byref(code), _stream(stream)),
            "pks_pages_device_error")
+    return code.value
+
+
+# ------------------------------------------------------- 4-bit cache
+
+def pks_q4_token_bytes(Hkv: int, D: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().pks_q4_token_bytes(int(Hkv), int(D), ctypes.byref(n)), "pks_q4_token_bytes")
+    return n.value
+
+
+def _q4_pools(a, pool_k, pool_v, Hkv: int, D: int) -> None:
+    row = pks_q4_token_bytes(Hkv, D)
+    if pool_k.dim() != 3 or pool_k.shape[2] != row or pool_v.shape != pool_k.shape:
+        raise ValueError(f"the pools must be [num_pages, page_size, {row}]")
+    a.num_pages, a.page_size = int(pool_k.shape[0]), int(pool_k.shape[1])
+    a.pool_k = _dptr(pool_k, torch.uint8, "pool_k")
+    a.pool_v = _dptr(pool_v, torch.uint8, "pool_v")
+
+
+def make_q4_rows_args(*, k, v, seq_lens, block_table, starts, pool_k, pool_v,
+                      error=None) -> pks_q4_rows_args:
+    """Fill a ``pks_q4_rows_args``: k, v [n_rows, Hkv, D] (any row and head strides, e.g.
+    slices of a fused projection), seq_lens [B], block_table [B, max_pages], starts [B + 1],
+    pools [num_pages, page_size, token_bytes] (uint8), error: int32 tensor or None."""
+    a = pks_q4_rows_args()
+    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype:
+        raise ValueError("k and v must be [n_rows, Hkv, D] of one type")
+    if k.dtype not in _Q4_TYPES:
+        raise TypeError(f"k and v must be bfloat16, float16 or float32, got {k.dtype}")
+    n, Hkv, D = k.shape
+    if n and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise ValueError("the values of a row's head must be contiguous")
+    B = block_table.shape[0]
+    if block_table.dim() != 2 or tuple(seq_lens.shape) != (B,) or tuple(starts.shape) != (B + 1,):
+        raise ValueError("block_table must be [B, max_pages], seq_lens [B] and starts [B + 1]")
+    a.B, a.n_rows, a.Hkv, a.D = int(B), int(n), int(Hkv), int(D)
+    a.max_pages = int(block_table.shape[1])
+    a.dtype = _Q4_TYPES[k.dtype]
+    _q4_pools(a, pool_k, pool_v, Hkv, D)
+    a.seq_lens = _dptr(seq_lens, torch.int32, "seq_lens")
+    a.block_table = _dptr(block_table, torch.int32, "block_table")
+    a.starts = _dptr(starts, torch.int32, "starts")
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    if n:
+        a.k_row, a.k_head, a.v_row, a.v_head = k.stride(0), k.stride(1), v.stride(0), v.stride(1)
+    a.error = _dptr(error, torch.int32, "error")
+    return a
+
+
+def pks_q4_write(args: pks_q4_rows_args, stream=None) -> None:
+    _check(lib().pks_q4_write(ctypes.byref(args), _stream(stream)), "pks_q4_write")
+
+
+def pks_q4_read(args: pks_q4_rows_args, stream=None) -> None:
+    _check(lib().pks_q4_read(ctypes.byref(args), _stream(stream)), "pks_q4_read")
+
+
+def make_q4_attention_args(*, seq_lens, block_table, q, pool_k, pool_v, Hkv: int, topk_idx=None,
+                           causal: bool = False, trim: bool = False, sm_scale: float = 0.0,
+                           out=None, lse=None, workspace=None,
+                           wait_limit: int = 0) -> pks_q4_attention_args:
+    """Fill a ``pks_q4_attention_args``: q [B, Hq, D] or [B, Nq, Hq, D] (``out`` alike,
+    ``lse`` without the last dimension), pools [num_pages, page_size, token_bytes] (uint8),
+    topk_idx None (every cached token) or q's leading dimensions and k."""
+    a = pks_q4_attention_args()
+    if q.dim() not in (3, 4):
+        raise ValueError("q must be [B, Hq, D] or [B, Nq, Hq, D]")
+    B, Hq, D = q.shape[0], q.shape[-2], q.shape[-1]
+    if q.dim() == 4:
+        if q.shape[1] < 1:
+            raise ValueError("q needs at least one query token")
+        a.n_queries = int(q.shape[1])
+    if block_table.dim() != 2 or block_table.shape[0] != B or tuple(seq_lens.shape) != (B,):
+        raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+    if topk_idx is not None:
+        if topk_idx.dim() != q.dim() - 1 or topk_idx.shape[:-1] != q.shape[:-2] or \
+                topk_idx.shape[-1] < 1:
+            raise ValueError("topk_idx must be [B, k], or [B, Nq, k], with k of 1 or more")
+        a.k = int(topk_idx.shape[-1])
+    if out is not None and tuple(out.shape) != tuple(q.shape):
+        raise ValueError("out must have q's shape")
+    if lse is not None and tuple(lse.shape) != tuple(q.shape[:-1]):
+        raise ValueError("lse must have q's shape without the last dimension")
+    a.B, a.Hq, a.Hkv, a.D = int(B), int(Hq), int(Hkv), int(D)
+    a.max_pages = int(block_table.shape[1])
+    _q4_pools(a, pool_k, pool_v, Hkv, D)
+    a.causal = 1 if causal else 0
+    a.trim = 1 if trim else 0
+    a.sm_scale = float(sm_scale)
+    a.wait_limit = int(wait_limit)
+    a.seq_lens = _dptr(seq_lens, torch.int32, "seq_lens")
+    a.block_table = _dptr(block_table, torch.int32, "block_table")
+    a.topk_idx = _dptr(topk_idx, torch.int32, "topk_idx")
+    a.q = _dptr(q, torch.bfloat16, "q")
+    a.out = _dptr(out, torch.bfloat16, "out")
+    a.lse = _dptr(lse, torch.float32, "lse")
+    if workspace is not None:
+        a.workspace = _dptr(workspace, torch.uint8, "workspace")
+        a.workspace_bytes = workspace.numel()
+    return a
+
+
+def pks_q4_workspace_size(args: pks_q4_attention_args) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().pks_q4_workspace_size(ctypes.byref(args), ctypes.byref(n)),
+           "pks_q4_workspace_size")
+    return n.value
+
+
+def pks_q4_attention(args: pks_q4_attention_args, stream=None) -> None:
+    _check(lib().pks_q4_attention(ctypes.byref(args), _stream(stream)), "pks_q4_attention")
+
+
+def pks_q4_sparse_attention(args: pks_q4_attention_args, stream=None) -> None:
+    _check(lib().pks_q4_sparse_attention(ctypes.byref(args), _stream(stream)),
+           "pks_q4_sparse_attention")
+
+
+def pks_q4_decode_step(select: pks_decode_args, attention: pks_q4_attention_args,
+                       stream=None) -> None:
+    _check(lib().pks_q4_decode_step(ctypes.byref(select), ctypes.byref(attention),
+                                    _stream(stream)), "pks_q4_decode_step")
+
+
+def pks_q4_device_error(args: pks_q4_attention_args, stream=None) -> int:
+    code = ctypes.c_int32()
+    _check(lib().pks_q4_device_error(ctypes.byref(args), ctypes.byref(code), _stream(stream)),
+           "pks_q4_device_error")
     return code.value
