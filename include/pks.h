@@ -679,7 +679,7 @@ pks_status pks_q4_read(const pks_q4_rows_args* args, pks_stream stream);
  * without influence on it, whatever they hold. */
 typedef struct pks_q4_attention_args {
   int32_t B;              /* requests; B * Nq <= 4096 */
-  int32_t Hq, Hkv;        /* 1 <= Hq / Hkv <= 16; Hkv <= 16, or D = 128, or Hkv even */
+  int32_t Hq, Hkv;        /* 1 <= Hq / Hkv <= 16; Hkv <= 1024 */
   int32_t D;              /* 64 or 128 */
   int32_t page_size, max_pages, num_pages;  /* num_pages * page_size < 2^31 and
                                                max_pages * page_size <= 2^24 */

@@ -24,7 +24,7 @@ LENS = [0, 1, 2, 15, 16, 17, 31, 33, 64, 100, 257]
     (2, 4, 64, 16), (8, 4, 128, 64), (8, 8, 128, 16), (1, 1, 64, 1), (1, 8, 128, 5), (3, 7, 64, 17),
     (4, 2, 128, 48), (5, 5, 128, 16), (6, 1, 64, 8), (7, 3, 128, 32), (16, 8, 128, 16),
     (16, 2, 64, 64), (9, 4, 64, 3), (15, 1, 128, 16), (32, 4, 128, 16), (18, 2, 64, 16),
-    (8, 4, 128, 5), (3, 4, 64, 8), (2, 8, 128, 128), (13, 2, 64, 1)])
+    (8, 4, 128, 5), (3, 4, 64, 8), (2, 8, 128, 128), (13, 2, 64, 1), (17, 4, 64, 16), (27, 1, 64, 5)])
 def test_dense_one_query(Hkv, G, D, page):
     Batch(LENS, page, Hkv, G, D, seed=Hkv).dense()
 
@@ -33,7 +33,7 @@ def test_dense_one_query(Hkv, G, D, page):
     (2, 4, 64, 16, 4), (8, 4, 128, 64, 4), (8, 16, 128, 16, 1), (1, 12, 64, 1, 1),
     (1, 16, 128, 5, 3), (4, 8, 128, 16, 5), (8, 8, 128, 64, 8), (2, 1, 64, 16, 64),
     (16, 16, 128, 16, 1), (12, 3, 128, 17, 3), (9, 16, 64, 16, 2), (3, 5, 64, 16, 2),
-    (5, 2, 128, 8, 7), (10, 9, 64, 16, 1)])
+    (5, 2, 128, 8, 7), (10, 9, 64, 16, 1), (11, 12, 64, 16, 1)])
 @pytest.mark.parametrize("causal", [False, True])
 def test_dense_several_queries(Hkv, G, D, page, Nq, causal):
     Batch(LENS, page, Hkv, G, D, Nq, seed=Nq).dense(causal=causal)

@@ -59,7 +59,7 @@ def test_token_bytes_refused(Hkv, D, want):
     (dict(trim=1), -1), (dict(k=4), -1), (dict(wait_limit=-1), -1), (dict(reserved=1), -1),
     (dict(sm_scale=-1.0), -1), (dict(sm_scale=float("nan")), -1),
     (dict(sm_scale=float("inf")), -1), (dict(Hq=34), -6), (dict(B=4097), -6),
-    (dict(B=2049, n_queries=2), -6), (dict(Hkv=17, Hq=17), -6), (dict(max_pages=1 << 21), -6),
+    (dict(B=2049, n_queries=2), -6), (dict(Hkv=1025, Hq=1025), -6), (dict(max_pages=1 << 21), -6),
     (dict(num_pages=1 << 28), -6), (dict(seq_lens=None), -1), (dict(block_table=None), -1),
     (dict(q=None), -1), (dict(q=4104), -1), (dict(pool_k=None), -1), (dict(pool_v=4100), -1),
     (dict(out=None), -1), (dict(out=4098), -1), (dict(workspace=None), -7),

@@ -13,16 +13,16 @@
 //  - K: bf16, the queries scaled by a power of two, so that all products are exact.
 //    Each group's sum is scaled by s_b on its own (fp32); the m_b Q_b of all groups are
 //    one more MMA, Q_b cut into three fp16 pieces (33 bits).
-//  - V: fp16.  p s is rounded to fp16 once a group (2^-12 of it; p itself likewise);
-//    p is kept 2^11 to 2^15 times its size at the maximum so that small ones stay
-//    normal numbers, less where an s is large.  sum p m is one more MMA.
+//  - V: fp16.  p s is rounded to fp16 once a group (by 2^-11 of it at most; p itself
+//    likewise); p is kept at 2^11 to 2^14 at the largest score so that small ones stay
+//    normal numbers, lower where an s is 2 or more.  sum p m is one more MMA.
 // Maxima, sums, scores and accumulators are fp32.
 //
 // One persistent CTA an SM.  All (request, head group, row chunk) segments are cut into
-// stages of 16 tokens a consumer warp; the CTAs take equal runs of stages.  A
-// producer warp finds the tokens' rows (a batch of 256 tokens at a time, so that
-// its two dependent loads are rare) and fills a ring of stages; a consumer warp owns
-// one head and 16 tokens of every stage.  Segments that several CTAs hold parts of are
+// stages of 16 tokens a consumer warp; the CTAs take equal runs of stages.  Four
+// producer warps, each for every fourth stage, find the tokens' rows (128 tokens at a
+// time, so that the two dependent loads are rare) and fill a ring of stages; a
+// consumer warp owns one head and 16 tokens of every stage.  Segments that several CTAs hold parts of are
 // joined by k_q4_merge.
 
 #include <cuda_fp16.h>
@@ -35,9 +35,13 @@ namespace pks {
 namespace {
 
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
-constexpr int kBatch = 256;    // tokens whose rows the producer finds at once
+constexpr int kConsumers = 8;  // warps, two a scheduler
+constexpr int kProducers = 4;  // warps, each filling every fourth stage
+constexpr uint32_t kProducerNs = 200, kConsumerNs = 20;  // between two looks at a barrier
+constexpr int kLookup = 128;   // tokens whose rows a producer finds at once
+constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 227 * 1024 - 4096;  // dynamic; the rest is the static part
+constexpr int kSmemMax = 227 * 1024 - 8192;  // dynamic; the rest is the static part
 constexpr int kBulkBytes = 2048;  // of a page, from which on its runs are copied whole
 constexpr int kFewRows = 4096;    // up to which a block joins a row, else a warp
 constexpr float kNone = -3e38f;  // reference of a row that has seen no token
@@ -62,30 +66,36 @@ struct Q4Shape {
   int HG, NHG, NRC;  // heads of a CTA, groups of them, chunks of rows
   int WPH, TS;       // warps a head, tokens a stage
   int row_bytes;     // of a token in the pool
-  int slice;         // of it what a head group takes: also the distance in shared memory
+  int taken;         // of it what a head group takes, copied in units of 8 or 16 bytes
+  int unit;
+  int slice;         // distance between tokens in shared memory
   int swz_pool, swz_smem, bulk;
-  uint32_t chunk_magic;  // ceil(2^20 / chunks of a slice)
+  uint32_t chunk_magic;  // ceil(2^20 / units a token)
   uint64_t order;
   int stages, ring, scratch_at, nv_at;  // bytes of the ring; where scratch and lengths begin
   int grid;
 };
 
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-      "{%8,%9}, {%0,%1,%2,%3};\n"
-      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// d = a b, and d += a b
+#define PKS_MMA(NAME, TYPE)                                                                      \
+  __device__ __forceinline__ void NAME(float(&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,      \
+                                       uint32_t a3, uint32_t b0, uint32_t b1) {                  \
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"              \
+                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                \
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));              \
+  }                                                                                              \
+  __device__ __forceinline__ void NAME##_add(float(&d)[4], uint32_t a0, uint32_t a1,             \
+                                             uint32_t a2, uint32_t a3, uint32_t b0,              \
+                                             uint32_t b1) {                                      \
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
+                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"                  \
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                \
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                        \
+  }
+PKS_MMA(mma_bf16, "bf16")
+PKS_MMA(mma_f16, "f16")
+#undef PKS_MMA
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
@@ -121,6 +131,9 @@ __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[NW]) {
 __device__ __forceinline__ void sts_zero8(uint32_t addr) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %1};\n" ::"r"(addr), "r"(0) : "memory");
 }
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;\n" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
                                           uint64_t* bar) {
   asm volatile(
@@ -130,24 +143,51 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// What a stage holds, from the producer to the consumers
+// What a stage holds, from its producer to the consumers.  mask: the tokens present,
+// of each 16, and the flags above them.
 struct StageNote {
-  int v, c, p0, nv;     // segment (request or list, chunk), first position, positions in all
-  int flags, pad[3];
-  uint32_t mask[16];    // tokens present, of each 16
+  int v, c, p0, nv;  // segment (request or list, chunk), first position, positions in all
+  uint32_t mask[16];
 };
-constexpr int kFirst = 1, kLast = 2, kWhole = 4, kSecond = 8;
+// kFirst, kLast: the CTA's first and last stage of the segment; kWhole: it has all of them;
+// kSecond: not the CTA's first segment; kEdge: some token lies beyond some query's limit
+constexpr uint32_t kFirst = 1u << 16, kLast = 2u << 16, kWhole = 4u << 16, kSecond = 8u << 16,
+                   kEdge = 16u << 16;
 struct Desc {
-  int v, c, p0, nv, flags;
+  int v, c, p0, nv;
+  uint32_t flags;
 };
+
+// Registers a thread of this warpgroup has from here on.  All of a CTA's together no
+// more than it was launched with.
+template <int N, bool MORE>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+// a += b, two at once
+__device__ __forceinline__ void add2(float& a0, float& a1, float b0, float b1) {
+  asm("{\n .reg .b64 x, y;\n mov.b64 x, {%0, %1};\n mov.b64 y, {%2, %3};\n"
+      " add.rn.f32x2 x, x, y;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "+f"(a0), "+f"(a1)
+      : "f"(b0), "f"(b1));
+}
+// d = a b + c, two at once
+__device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, float b0, float b1,
+                                     float c0, float c1) {
+  asm("{\n .reg .b64 x, y, z;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mov.b64 z, {%6, %7};\n fma.rn.f32x2 x, x, y, z;\n mov.b64 {%0, %1}, x;\n}\n"
+      : "=f"(d0), "=f"(d1)
+      : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
+}
 
 // First stage of CTA i when W stages go to n CTAs
 __device__ __forceinline__ int64_t first_stage(int64_t W, int n, int i) {
   return W * i / n;
 }
 
-template <int D, int NT, int NW>
-__global__ void __launch_bounds__((NW + 1) * 32, 1)
+template <int D, int NT, int TT>
+__global__ void __launch_bounds__((kConsumers + kProducers) * 32, 1)
 k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
                const int32_t* __restrict__ lists, const __nv_bfloat16* __restrict__ q,
                const uint8_t* __restrict__ pool_k, const uint8_t* __restrict__ pool_v,
@@ -155,7 +195,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                int64_t* __restrict__ prefix, float2* __restrict__ part_ml,
                float* __restrict__ part_o, int32_t* __restrict__ err, const Q4Shape sh,
                float scale_log2, long long wait_cycles) {
-  constexpr int NTHREADS = (NW + 1) * 32, NB = D / q4::kGroup, REC = q4::record_bytes(D);
+  constexpr int NW = kConsumers, NWARPS = NW + kProducers, NTHREADS = NWARPS * 32, NB = D / q4::kGroup, REC = q4::record_bytes(D);
   constexpr int RC = 8 * NT;  // query rows a chunk
   const float kNegInf = __int_as_float(0xff800000);
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -163,9 +203,10 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   // bar_join: the consumer warps
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
-  __shared__ Desc s_desc[kBatch / 16];
-  __shared__ int s_row[kBatch], s_run[kBatch];
-  __shared__ int64_t s_warp[NW + 1], s_rest;
+  __shared__ Desc s_desc_all[kProducers][kLookup / 16];
+  __shared__ int s_row_all[kProducers][kMaxTokens];
+  __shared__ uint16_t s_run_all[kProducers][kMaxTokens];
+  __shared__ int64_t s_warp[NWARPS], s_rest;
   __shared__ int s_first, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = tc::smem_u32(smem);
@@ -181,8 +222,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     tc::mbar_init_fence();
     s_abort = 0;
   }
-  pdl_wait(seq_lens, block_table, lists, q, pool_k, pool_v, out, lse, prefix, part_ml, part_o,
-           err);
+  // (table, lists and queries are renewed where they are read: kept in registers from
+  // here on, their addresses cost the consumers spills)
+  pdl_wait(seq_lens);
   pdl_launch_dependents();
 
   // ---- the stages of every segment, and this CTA's run of them ----
@@ -210,7 +252,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   if (lane == 31) s_warp[warp] = upto;
   __syncthreads();
   int64_t W = 0, before = 0;
-  for (int w = 0; w <= NW; ++w) {
+  for (int w = 0; w < NWARPS; ++w) {
     if (w < warp) before += s_warp[w];
     W += s_warp[w];
   }
@@ -239,9 +281,20 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     s_rest = rest;
   }
   __syncthreads();
-  const int64_t count = hi - lo;
-  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    return __all_sync(0xffffffffu, tc::mbar_wait(bar, parity, &s_abort, wait_cycles)) != 0;
+  const int count = (int)(hi - lo);  // (at most 2^33 stages over all SMs)
+  // Waits of a warp, which sleeps between two looks: polling takes issue slots from the
+  // warps that work (a third of them, when the four producers looked every 50 cycles).
+  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t ns) -> bool {
+    bool there = tc::mbar_test_wait(bar, parity);
+    if (!there) {
+      const long long t0 = clock64();
+      do {
+        if (*(volatile int*)&s_abort || clock64() - t0 > wait_cycles) break;
+        __nanosleep(ns);
+        there = tc::mbar_test_wait(bar, parity);
+      } while (!there);
+    }
+    return __all_sync(0xffffffffu, there) != 0;
   };
   auto give_up = [&]() {
     if (lane == 0) {
@@ -250,59 +303,70 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     }
   };
 
-  if (warp == NW) {
-    // =========================== producer ===========================
+  if (warp >= NW) {
+    // =========================== producers ===========================
+    set_registers<88, false>();
+    behind(seq_lens, block_table, lists);
+    const int me = warp - NW;
+    Desc* s_desc = s_desc_all[me];
+    int* s_row = s_row_all[me];
+    uint16_t* s_run = s_run_all[me];
     int v = s_first;
     int n = s_nv[v], T = (n + sh.TS - 1) / sh.TS;
     int c = (int)(s_rest / T), tile = (int)(s_rest - (int64_t)c * T);
     int64_t seg_at = lo - tile;  // first stage of the segment at hand
-    const int cpt = sh.slice / 16;
-    int stage = 0;
-    uint32_t phase = 0;  // of the ring's round
-    int64_t done = 0;
+    const int cpt = sh.taken / sh.unit, most = max(1, kLookup / sh.TS);
+    int at_stage = 0;  // of the CTA's run, the one that v, c, tile stand at
+    auto forward = [&](int to) {  // (not beyond the run's last stage)
+      int step = to - at_stage;
+      at_stage = to;
+      while (step >= T - tile) {
+        step -= T - tile;
+        tile = 0;
+        seg_at += T;
+        if (++c == chunks) {
+          c = 0;
+          do n = s_nv[++v];
+          while (n == 0);
+          T = (n + sh.TS - 1) / sh.TS;
+        }
+      }
+      tile += step;
+    };
+    int next = me;  // the next stage to fill
     bool ok = true;
-    while (ok && done < count) {
-      const int nb = (int)min((int64_t)(kBatch / sh.TS), count - done);
-      // ---- which segments the next stages are of
+    while (ok && next < count) {
+      const int nb = min(most, (count - next + kProducers - 1) / kProducers);
+      // ---- which segments the stages are of
 #pragma unroll 1
       for (int j = 0; j < nb; ++j) {
-        const int64_t here = lo + done + j;
+        const int i = next + j * kProducers;
+        forward(i);
         if (lane == 0) {
-          int f = 0;
-          if (tile == 0 || here == lo) f |= kFirst;
-          if (tile == T - 1 || here == hi - 1) f |= kLast;
+          uint32_t f = 0;
+          if (tile == 0 || i == 0) f |= kFirst;
+          if (tile == T - 1 || i == count - 1) f |= kLast;
           if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
           if (seg_at > lo) f |= kSecond;
+          if (sh.causal &&
+              (tile + 1) * sh.TS > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G)) f |= kEdge;
           s_desc[j] = {v, c, tile * sh.TS, n, f};
-        }
-        if (++tile == T) {
-          tile = 0;
-          seg_at += T;
-          if (++c == chunks) {
-            c = 0;
-            if (here + 1 < hi) {
-              do n = s_nv[++v];
-              while (n == 0);
-              T = (n + sh.TS - 1) / sh.TS;
-            }
-          }
         }
       }
       __syncwarp();
       // ---- the rows of their tokens
-      {
-        int t[kBatch / 32], b[kBatch / 32], pos[kBatch / 32];
+      for (int t0 = 0; t0 < nb * sh.TS; t0 += kLookup) {
+        int t[kLookup / 32], b[kLookup / 32], left[kLookup / 32];
 #pragma unroll
-        for (int i = 0; i < kBatch / 32; ++i) {
-          const int j = lane + 32 * i, st = j / sh.TS;
-          pos[i] = -1;
+        for (int i = 0; i < kLookup / 32; ++i) {
+          const int j = t0 + lane + 32 * i, st = j / sh.TS;
           t[i] = -1;
-          b[i] = 0;
+          b[i] = left[i] = 0;
           if (st < nb) {
             const Desc d = s_desc[st];
             const int p = d.p0 + j - st * sh.TS;
+            left[i] = d.nv - p;
             if (p < d.nv) {
-              pos[i] = p;
               b[i] = d.v / sh.lists;
               t[i] = sh.k ? lists[(int64_t)d.v * sh.k + p] : p;
             }
@@ -310,51 +374,49 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
         if (sh.k) {
 #pragma unroll
-          for (int i = 0; i < kBatch / 32; ++i)
-            if (t[i] != -1) {
-              const int len = seq_lens[b[i]];
-              if (t[i] < 0 || t[i] >= len) {
-                *err = kErrToken;
-                t[i] = -1;
-              }
+          for (int i = 0; i < kLookup / 32; ++i)
+            if (t[i] != -1 && (t[i] < 0 || t[i] >= seq_lens[b[i]])) {
+              *err = kErrToken;
+              t[i] = -1;
             }
         }
-        int page[kBatch / 32];
 #pragma unroll
-        for (int i = 0; i < kBatch / 32; ++i)
-          page[i] = t[i] < 0 ? -1
-                             : block_table[(int64_t)b[i] * sh.max_pages + t[i] / sh.page_size];
-        __syncwarp();
+        for (int i = 0; i < kLookup / 32; ++i) {
+          if (t[i] < 0) continue;
+          const int p = t[i] / sh.page_size;
+          b[i] = block_table[(int64_t)b[i] * sh.max_pages + p];  // its page
+          t[i] -= p * sh.page_size;                              // and slot
+        }
 #pragma unroll
-        for (int i = 0; i < kBatch / 32; ++i) {
-          const int j = lane + 32 * i;
+        for (int i = 0; i < kLookup / 32; ++i) {
+          const int j = t0 + lane + 32 * i;
+          if (j >= nb * sh.TS) break;
           int row = -1, run = 0;
           if (t[i] >= 0) {
-            if (page[i] < 0 || page[i] >= sh.num_pages) {
+            if (b[i] < 0 || b[i] >= sh.num_pages) {
               *err = kErrPage;
             } else {
-              const int slot = t[i] % sh.page_size;
-              row = page[i] * sh.page_size + slot;
+              row = b[i] * sh.page_size + t[i];
               if (sh.bulk) {
                 // a copy from the first token of a page, or of the stage, on
-                const int st = j / sh.TS, at = j - st * sh.TS;
-                if (at == 0 || slot == 0)
-                  run = min(min(sh.page_size - slot, sh.TS - at), s_desc[st].nv - pos[i]);
+                const int at = j % sh.TS;
+                if (at == 0 || t[i] == 0) run = min(min(sh.page_size - t[i], sh.TS - at), left[i]);
               } else {
-                run = slot & 7;
+                run = t[i] & 7;
               }
             }
           }
           s_row[j] = row;
-          s_run[j] = run;
+          s_run[j] = (uint16_t)run;
         }
-        __syncwarp();
       }
+      __syncwarp();
       // ---- fill the stages
 #pragma unroll 1
-      for (int j = 0; j < nb; ++j) {
+      for (int j = 0; j < nb; ++j, next += kProducers) {
+        const int round = next / sh.stages, stage = next - round * sh.stages;
         const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
-        if (done + j >= sh.stages) ok = wait(&bar_empty[stage], phase ^ 1);
+        if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1, kProducerNs);
         if (!ok) break;
         const Desc d = s_desc[j];
         const int hg = d.c / sh.NRC;
@@ -366,8 +428,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           const bool here = at < sh.TS && s_row[j * sh.TS + at] >= 0;
           const uint32_t m = __ballot_sync(0xffffffffu, here);
           if (lane == 0) {
-            note->mask[2 * i] = m & 0xffffu;
-            note->mask[2 * i + 1] = m >> 16;
+            note->mask[2 * i] = (m & 0xffffu) | d.flags;
+            note->mask[2 * i + 1] = m >> 16 | d.flags;
           }
           present += __popc(m);
           if (at < sh.TS && !here) {
@@ -386,7 +448,6 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           note->c = d.c;
           note->p0 = d.p0;
           note->nv = d.nv;
-          note->flags = d.flags;
         }
         __syncwarp();
         if (sh.bulk) {
@@ -409,37 +470,31 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             if (row >= 0) {
               const uint32_t xs = sh.swz_pool ? (uint32_t)s_run[j * sh.TS + at] << 4 : 0;
               const uint32_t xd = sh.swz_smem ? q4::swizzle(at) : 0;
-              const int64_t src = (int64_t)row * sh.row_bytes + ((uint32_t)(off + 16 * ch) ^ xs);
-              const uint32_t o = at * sh.slice + ((uint32_t)(16 * ch) ^ xd);
-              tc::cp_async16(dst_k + o, pool_k + src, 16);
-              tc::cp_async16(dst_v + o, pool_v + src, 16);
+              const int64_t src =
+                  (int64_t)row * sh.row_bytes + ((uint32_t)(off + sh.unit * ch) ^ xs);
+              const uint32_t o = at * sh.slice + ((uint32_t)(sh.unit * ch) ^ xd);
+              if (sh.unit == 16) {
+                tc::cp_async16(dst_k + o, pool_k + src, 16);
+                tc::cp_async16(dst_v + o, pool_v + src, 16);
+              } else {
+                cp_async8(dst_k + o, pool_k + src);
+                cp_async8(dst_v + o, pool_v + src);
+              }
             }
           }
           tc::cp_async_arrive(&bar_full[stage]);
           if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
         }
-        if (++stage == sh.stages) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
-      if (!ok) break;
-      done += nb;
     }
     if (!ok) {
       give_up();
-      // the copies in flight land before the CTA gives its memory up: the last
-      // round's barriers complete by themselves
-      int s = stage;
-      uint32_t ph = phase;
-      for (int i = 0; i < sh.stages; ++i) {
-        if (s == 0) {
-          s = sh.stages;
-          ph ^= 1;
-        }
-        --s;
+      // the copies in flight land before the CTA gives its memory up
+      for (int i = next - kProducers; i >= 0 && i >= next - sh.stages; i -= kProducers) {
+        const int round = i / sh.stages;
         const long long t0 = clock64();
-        while (!tc::mbar_try_wait(&bar_full[s], ph) && clock64() - t0 < kWaitCycles) {
+        while (!tc::mbar_try_wait(&bar_full[i - round * sh.stages], round & 1) &&
+               clock64() - t0 < kWaitCycles) {
         }
       }
     }
@@ -447,55 +502,62 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   }
 
   // =========================== consumers ===========================
+  set_registers<208, true>();
   if (warp >= consumers) return;
   const int h = warp / sh.WPH, sub = warp - h * sh.WPH;
   const int g = lane >> 2, t = lane & 3;
-  auto token = [&](int r) { return sub * 16 + (int)(sh.order >> (4 * r) & 15); };
-  auto at = [&](int tok, int off) -> uint32_t {
-    return tok * sh.slice + ((uint32_t)(h * REC + off) ^ (sh.swz_smem ? q4::swizzle(tok) : 0));
+  auto token = [&](int r) { return (int)(sh.order >> (4 * r) & 15); };
+  auto at = [&](int tok, int off) -> uint32_t {  // (16 tokens on, the same permutation)
+    return (sub * TT * 16 + tok) * sh.slice +
+           ((uint32_t)(h * REC + off) ^ (sh.swz_smem ? q4::swizzle(tok) : 0));
   };
   // rows g and g + 8 of the tokens' tiles; K codes and pairs
   const int tok0 = token(g), tok1 = token(g + 8);
-  const uint32_t k_code0 = at(tok0, 4 * NB * t), k_code1 = at(tok1, 4 * NB * t);
-  const uint32_t k_pair0 = at(tok0, D / 2), k_pair1 = at(tok1, D / 2);
+  uint32_t k_code0 = at(tok0, 4 * NB * t), k_code1 = at(tok1, 4 * NB * t);
+  uint32_t k_pair0 = at(tok0, D / 2), k_pair1 = at(tok1, D / 2);
   // tokens 2t, 2t + 1, 2t + 8, 2t + 9 of the tile's order; V codes and pairs
   uint32_t v_code[4], v_pair[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int tok = token(2 * t + (i & 1) + 8 * (i >> 1));
-    v_code[i] = at(tok, 2 * NB * g);
-    v_pair[i] = at(tok, D / 2);
+    v_code[i] = half + at(tok, 2 * NB * g);
+    v_pair[i] = half + at(tok, D / 2);
   }
+  // (kept, not worked out again for every tile)
+  asm volatile("" : "+r"(k_code0), "+r"(k_code1), "+r"(k_pair0), "+r"(k_pair1), "+r"(v_code[0]),
+               "+r"(v_code[1]), "+r"(v_code[2]), "+r"(v_code[3]));
+  asm volatile("" : "+r"(v_pair[0]), "+r"(v_pair[1]), "+r"(v_pair[2]), "+r"(v_pair[3]));
   const int m_word = 4 * (g & (NB - 1));
 
   uint32_t qf[NT][NB][4], qs[NT][2];  // queries as B operands; the pieces of their sums
-  float cs[NT][2], ref[NT][2], sum[NT][2];  // of columns 2t, 2t + 1
-  int lim[NT][2], min_lim = 0;
-  float o[NT][NB][2][4], om[NT][4];
-  int sx = 0;  // log2 of the largest s, at least 0
+  // of columns 2t, 2t + 1: scale of the scores, minus the reference, sum of weights
+  float cs[NT][2], nref[NT][2], sum[NT][2];
+  float o[NT][NB][2][4], om[NT][2];
+  int sx = 0;  // weights are at most 2^(14 - sx), scales below 2^(1 + sx)
   int stage = 0;
   uint32_t phase = 0, join_phase = 0;
   bool ok = true;
   auto join = [&]() {  // of the consumer warps
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&bar_join);
-    ok = ok && wait(&bar_join, join_phase);
+    ok = ok && wait(&bar_join, join_phase, kConsumerNs);
     join_phase ^= 1;
   };
 
-  for (int64_t done = 0; done < count; ++done) {
-    ok = wait(&bar_full[stage], phase);
+  for (int done = 0; done < count; ++done) {
+    ok = wait(&bar_full[stage], phase, kConsumerNs);
     if (!ok) break;
     const StageNote* note = &s_note[stage];
-    const int flags = note->flags;
-    const uint32_t mask = note->mask[sub];
-    const int p0 = note->p0 + sub * 16;
+    uint32_t mask[TT];
+#pragma unroll
+    for (int u = 0; u < TT; ++u) mask[u] = note->mask[sub * TT + u];
+    const uint32_t flags = mask[0];
     if (flags & kFirst) {
       // ---------------- the segment's queries ----------------
       const int hg = note->c / sh.NRC, rc = note->c - hg * sh.NRC;
       const int head = hg * sh.HG + h;
-      min_lim = note->nv;
-      if (sh.causal) min_lim -= sh.Nq - 1 - rc * RC / sh.G;
+      const __nv_bfloat16* from = q;
+      behind(from);
       sx = 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -506,7 +568,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           const int64_t row = ((int64_t)note->v * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            const uint4 w = *reinterpret_cast<const uint4*>(q + row * D + 32 * b + 8 * t);
+            const uint4 w = *reinterpret_cast<const uint4*>(from + row * D + 32 * b + 8 * t);
             const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -581,10 +643,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           cs[nt][j] = __shfl_sync(0xffffffffu, mine_c, (2 * t + j) * 4);
-          ref[nt][j] = kNone;
-          sum[nt][j] = 0.f;
-          const int rr = rc * RC + nt * 8 + 2 * t + j;
-          lim[nt][j] = sh.causal ? note->nv - sh.Nq + min(rr / sh.G, sh.Nq - 1) + 1 : note->nv;
+          nref[nt][j] = -kNone;
+          sum[nt][j] = om[nt][j] = 0.f;
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -592,21 +652,28 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           for (int m = 0; m < 2; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][b][m][e] = 0.f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) om[nt][e] = 0.f;
       }
     }
 
-    if (mask) {
-      const uint32_t base_k = ring + (uint32_t)stage * 2 * half, base_v = base_k + half;
+    uint32_t present = 0, absent = 0;
+#pragma unroll
+    for (int u = 0; u < TT; ++u) {
+      present |= mask[u];
+      absent |= ~mask[u];
+    }
+    if (present & 0xffffu) {
+      const uint32_t base = ring + (uint32_t)stage * 2 * half;
+      const uint32_t tile_bytes = 16 * sh.slice;
       // ---------------- scores ----------------
-      float tot[NT][4];
-      {
+      float tot[TT][NT][4];
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        const uint32_t from = base + u * tile_bytes;
         uint32_t w0[NB], w1[NB], p0w[NB], p1w[NB];
-        lds(base_k + k_code0, w0);
-        lds(base_k + k_code1, w1);
-        lds(base_k + k_pair0, p0w);
-        lds(base_k + k_pair1, p1w);
+        lds(from + k_code0, w0);
+        lds(from + k_code1, w1);
+        lds(from + k_pair0, p0w);
+        lds(from + k_pair1, p1w);
         uint32_t a0, a1;
         if constexpr (NB == 4) {
           a0 = __byte_perm(t & 1 ? p0w[2] : p0w[0], t & 1 ? p0w[3] : p0w[1], 0x7632);
@@ -617,11 +684,11 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          float acc[4];
           mma_f16(acc, a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
           // units: 2^(p - 112) here, 2^(p - 133) below
 #pragma unroll
-          for (int e = 0; e < 4; ++e) tot[nt][e] = acc[e] * 4.76837158203125e-07f;
+          for (int e = 0; e < 4; ++e) tot[u][nt][e] = acc[e] * 4.76837158203125e-07f;
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
@@ -629,101 +696,123 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           const float s0 = low_half(p0w[b]), s1 = low_half(p1w[b]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float acc[4];
             mma_bf16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
                      qf[nt][b][0], qf[nt][b][1]);
-            mma_bf16(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u, y1 & 0x00f000f0u,
-                     qf[nt][b][2], qf[nt][b][3]);
-            tot[nt][0] = fmaf(acc[0], s0, tot[nt][0]);
-            tot[nt][1] = fmaf(acc[1], s0, tot[nt][1]);
-            tot[nt][2] = fmaf(acc[2], s1, tot[nt][2]);
-            tot[nt][3] = fmaf(acc[3], s1, tot[nt][3]);
+            mma_bf16_add(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u,
+                         y1 & 0x00f000f0u, qf[nt][b][2], qf[nt][b][3]);
+            tot[u][nt][0] = fmaf(acc[0], s0, tot[u][nt][0]);
+            tot[u][nt][1] = fmaf(acc[1], s0, tot[u][nt][1]);
+            tot[u][nt][2] = fmaf(acc[2], s1, tot[u][nt][2]);
+            tot[u][nt][3] = fmaf(acc[3], s1, tot[u][nt][3]);
           }
         }
       }
-      const bool masked = mask != 0xffffu || p0 + 16 > min_lim;
+      const bool masked = (absent & 0xffffu) | (flags & kEdge);
       if (masked) {
-        const bool on0 = mask >> (tok0 & 15) & 1, on1 = mask >> (tok1 & 15) & 1;
-        const int q0 = p0 + (tok0 & 15), q1 = p0 + (tok1 & 15);
+        // of the first query's tokens, from this warp's first on
+        const int left = note->nv - sh.Nq + 1 - note->p0 - sub * TT * 16;
+        const int first = note->c % sh.NRC * RC + 2 * t;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int u = 0; u < TT; ++u) {
+          const bool on0 = mask[u] >> tok0 & 1, on1 = mask[u] >> tok1 & 1;
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            if (!on0 || q0 >= lim[nt][j]) tot[nt][j] = kNegInf;
-            if (!on1 || q1 >= lim[nt][j]) tot[nt][2 + j] = kNegInf;
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const int lim =
+                  (flags & kEdge ? left + min((first + nt * 8 + j) / sh.G, sh.Nq - 1) : 16 * TT) -
+                  16 * u;
+              if (!on0 || tok0 >= lim) tot[u][nt][j] = kNegInf;
+              if (!on1 || tok1 >= lim) tot[u][nt][2 + j] = kNegInf;
+            }
+        }
       }
       // ---------------- V's scales ----------------
-      uint32_t s01[NB], s23[NB], ma0, ma2;
-      {
+      uint32_t s01[TT][NB], s23[TT][NB], ma0[TT], ma2[TT];
+      uint32_t any = 0;
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
         uint32_t w[4][NB], m[4][1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          lds(base_v + v_pair[i], w[i]);
-          lds(base_v + v_pair[i] + m_word, m[i]);
+          const uint32_t from = base + u * tile_bytes + v_pair[i];
+          lds(from, w[i]);
+          lds(from + m_word, m[i]);
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          s01[b] = __byte_perm(w[0][b], w[1][b], 0x5410);
-          s23[b] = __byte_perm(w[2][b], w[3][b], 0x5410);
+          s01[u][b] = __byte_perm(w[0][b], w[1][b], 0x5410);
+          s23[u][b] = __byte_perm(w[2][b], w[3][b], 0x5410);
+          any |= s01[u][b] | s23[u][b];
         }
-        ma0 = __byte_perm(m[0][0], m[1][0], 0x7632);
-        ma2 = __byte_perm(m[2][0], m[3][0], 0x7632);
+        ma0[u] = __byte_perm(m[0][0], m[1][0], 0x7632);
+        ma2[u] = __byte_perm(m[2][0], m[3][0], 0x7632);
       }
-      __half2 s_max = __hmax2(bits_half2(s01[0]), bits_half2(s23[0]));
+      // p s stays below 2^16 while all s are below 2^(1 + sx)
+      if (__any_sync(0xffffffffu, any & 0x40004000u)) {  // some are 2 or more, or NaN
+        __half2 s_max = bits_half2(0);
 #pragma unroll
-      for (int b = 1; b < NB; ++b)
-        s_max = __hmax2(s_max, __hmax2(bits_half2(s01[b]), bits_half2(s23[b])));
-      // p s must stay below 2^16, p being at most 2^(15 - sx)
-      if (__any_sync(0xffffffffu, fmaxf(__low2float(s_max), __high2float(s_max)) >
-                                      __int_as_float((127 + sx) << 23))) {
+        for (int u = 0; u < TT; ++u)
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+            s_max = __hmax2(s_max, __hmax2(bits_half2(s01[u][b]), bits_half2(s23[u][b])));
         float top = fmaxf(__low2float(s_max), __high2float(s_max));
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const int now = min((int)(__float_as_uint(top) >> 23) - 126, 16);
-        const float f = __int_as_float((127 - (now - sx)) << 23);
+        const int now = min((int)(__float_as_uint(top) >> 23) - 127, 16);
+        if (now > sx) {
+          const float f = __int_as_float((127 - (now - sx)) << 23);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
+          for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            ref[nt][j] += (float)(now - sx);
-            sum[nt][j] *= f;
+            for (int j = 0; j < 2; ++j) {
+              nref[nt][j] -= (float)(now - sx);
+              sum[nt][j] *= f;
+              om[nt][j] *= f;
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+              for (int e = 0; e < 8; ++e) o[nt][b][e >> 2][e & 3] *= f;
           }
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) o[nt][b][e >> 2][e & 3] *= f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) om[nt][e] *= f;
+          sx = now;
         }
-        sx = now;
       }
       // ---------------- softmax ----------------
-      const float x_max = (float)(15 - sx);
-      float x[NT][4];
-      bool over = false;
+      const float x_max = (float)(14 - sx);
+      float x[TT][NT][4];
+      float x_top = kNegInf;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < TT; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[nt][e] = fmaf(tot[nt][e], cs[nt][e & 1], -ref[nt][e & 1]);
-          over |= x[nt][e] > x_max;
+        for (int nt = 0; nt < NT; ++nt) {
+          fma2(x[u][nt][0], x[u][nt][1], tot[u][nt][0], tot[u][nt][1], cs[nt][0], cs[nt][1],
+               nref[nt][0], nref[nt][1]);
+          fma2(x[u][nt][2], x[u][nt][3], tot[u][nt][2], tot[u][nt][3], cs[nt][0], cs[nt][1],
+               nref[nt][0], nref[nt][1]);
+          x_top = fmaxf(fmaxf(x_top, fmaxf(x[u][nt][0], x[u][nt][1])),
+                        fmaxf(x[u][nt][2], x[u][nt][3]));
         }
-      if (__any_sync(0xffffffffu, over)) {
+      if (__any_sync(0xffffffffu, x_top > x_max)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float top = fmaxf(tot[nt][j], tot[nt][2 + j]) * cs[nt][j];
+            float top = kNegInf;
+#pragma unroll
+            for (int u = 0; u < TT; ++u) top = fmaxf(top, fmaxf(tot[u][nt][j], tot[u][nt][2 + j]));
+            top *= cs[nt][j];
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1)
               top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float was = ref[nt][j];
-            if (top - was > x_max) {
-              ref[nt][j] = top - (x_max - 4.f);
-              const float f = ex2(was - ref[nt][j]);
+            const float was = nref[nt][j];
+            if (top + was > x_max) {
+              nref[nt][j] = x_max - 3.f - top;
+              const float f = ex2(nref[nt][j] - was);
               sum[nt][j] *= f;
+              om[nt][j] *= f;
 #pragma unroll
               for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -731,60 +820,92 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                   o[nt][b][m][j] *= f;
                   o[nt][b][m][2 + j] *= f;
                 }
-              om[nt][j] *= f;
-              om[nt][2 + j] *= f;
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) x[nt][e] = fmaf(tot[nt][e], cs[nt][e & 1], -ref[nt][e & 1]);
+          for (int u = 0; u < TT; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              x[u][nt][e] = fmaf(tot[u][nt][e], cs[nt][e & 1], nref[nt][e & 1]);
         }
       }
-      uint32_t pt0[NT], pt1[NT], seen0[NT], seen1[NT];
+      uint32_t pt0[TT][NT], pt1[TT][NT], seen0[TT][NT], seen1[TT][NT];
+#pragma unroll
+      for (int u = 0; u < TT; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = ex2(x[u][nt][e]);
+          add2(sum[nt][0], sum[nt][1], p[0], p[1]);
+          add2(sum[nt][0], sum[nt][1], p[2], p[3]);
+          pt0[u][nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
+          pt1[u][nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
+          if (masked) {
+            auto seen = [&](int e) {
+              return (tot[u][nt][e] == kNegInf ? 0u : 0xffffu) |
+                     (tot[u][nt][e + 1] == kNegInf ? 0u : 0xffff0000u);
+            };
+            seen0[u][nt] = movmatrix_t(seen(0));
+            seen1[u][nt] = movmatrix_t(seen(2));
+          }
+        }
+      // ---------------- values ----------------
+      // The products start from zero every time and are added on their own: the tensor
+      // core cuts off what lies below the accumulator's last place, and both sums grow
+      // to many times their difference (131,072 tokens: 0.017 of the result's norm
+      // instead of 0.0018).
+      uint32_t w[TT][4][NB / 2];
+#pragma unroll
+      for (int u = 0; u < TT; ++u)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lds(base + u * tile_bytes + v_code[i], w[u][i]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+        float acc[4];
+        mma_f16(acc, ma0[0], 0u, ma2[0], 0u, pt0[0][nt], pt1[0][nt]);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = ex2(x[nt][e]);
-        sum[nt][0] += p[0] + p[2];
-        sum[nt][1] += p[1] + p[3];
-        pt0[nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
-        pt1[nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
-        if (masked) {
-          auto seen = [&](int e) {
-            return (tot[nt][e] == kNegInf ? 0u : 0xffffu) |
-                   (tot[nt][e + 1] == kNegInf ? 0u : 0xffff0000u);
-          };
-          seen0[nt] = movmatrix_t(seen(0));
-          seen1[nt] = movmatrix_t(seen(2));
-        }
+        for (int u = 1; u < TT; ++u)
+          mma_f16_add(acc, ma0[u], 0u, ma2[u], 0u, pt0[u][nt], pt1[u][nt]);
+        add2(om[nt][0], om[nt][1], acc[0], acc[1]);
       }
-      // ---------------- values ----------------
-      {
-        uint32_t w[4][NB / 2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lds(base_v + v_code[i], w[i]);
+      for (int b = 0; b < NB; ++b) {
+        float acc[NT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(om[nt], ma0, 0u, ma2, 0u, pt0[nt], pt1[nt]);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
+        for (int u = 0; u < TT; ++u) {
           const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
-          const uint32_t x01 = __byte_perm(w[0][b / 2], w[1][b / 2], sel);
-          const uint32_t x23 = __byte_perm(w[2][b / 2], w[3][b / 2], sel);
+          const uint32_t x01 = __byte_perm(w[u][0][b / 2], w[u][1][b / 2], sel);
+          const uint32_t x23 = __byte_perm(w[u][2][b / 2], w[u][3][b / 2], sel);
           const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            uint32_t b0 = half2_bits(__hmul2(bits_half2(pt0[nt]), bits_half2(s01[b])));
-            uint32_t b1 = half2_bits(__hmul2(bits_half2(pt1[nt]), bits_half2(s23[b])));
+            uint32_t b0 = half2_bits(__hmul2(bits_half2(pt0[u][nt]), bits_half2(s01[u][b])));
+            uint32_t b1 = half2_bits(__hmul2(bits_half2(pt1[u][nt]), bits_half2(s23[u][b])));
             if (masked) {  // (an s without a number must not reach rows that do not see it)
-              b0 &= seen0[nt];
-              b1 &= seen1[nt];
+              b0 &= seen0[u][nt];
+              b1 &= seen1[u][nt];
             }
-            mma_f16(o[nt][b][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
-                    x23 & 0x00f000f0u, b0, b1);
-            mma_f16(o[nt][b][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
-                    y23 & 0x00f000f0u, b0, b1);
+            if (u == 0) {
+              mma_f16(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
+                      x23 & 0x00f000f0u, b0, b1);
+              mma_f16(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
+                      y23 & 0x00f000f0u, b0, b1);
+            } else {
+              mma_f16_add(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
+                          x23 & 0x00f000f0u, b0, b1);
+              mma_f16_add(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
+                          y23 & 0x00f000f0u, b0, b1);
+            }
           }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int m = 0; m < 2; ++m) {
+            add2(o[nt][b][m][0], o[nt][b][m][1], acc[nt][m][0], acc[nt][m][1]);
+            add2(o[nt][b][m][2], o[nt][b][m][3], acc[nt][m][2], acc[nt][m][3]);
+          }
       }
     }
     const int seg_v = note->v, seg_c = note->c;
@@ -835,7 +956,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             p[(8 * NB + j) * 32] = sum[nt][j];
-            p[(8 * NB + 2 + j) * 32] = ref[nt][j];
+            p[(8 * NB + 2 + j) * 32] = nref[nt][j];
           }
         }
       }
@@ -847,10 +968,10 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           float fa[2], fb[2];
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float other = p[(8 * NB + 2 + j) * 32], top = fmaxf(ref[nt][j], other);
-            fa[j] = ex2(ref[nt][j] - top);
-            fb[j] = ex2(other - top);
-            ref[nt][j] = top;
+            const float other = p[(8 * NB + 2 + j) * 32], low = fminf(nref[nt][j], other);
+            fa[j] = ex2(low - nref[nt][j]);
+            fb[j] = ex2(low - other);
+            nref[nt][j] = low;
             sum[nt][j] = sum[nt][j] * fa[j] + p[(8 * NB + j) * 32] * fb[j];
           }
 #pragma unroll
@@ -886,11 +1007,11 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                            *reinterpret_cast<const uint32_t*>(&c));
           }
           if (lse && g == 0)
-            lse[row] = l == 0.f ? kNegInf : (ref[nt][j] + log2f(l)) * 0.6931471805599453f;
+            lse[row] = l == 0.f ? kNegInf : (log2f(l) - nref[nt][j]) * 0.6931471805599453f;
         } else {
           const int64_t slot = ((int64_t)2 * cta + (flags & kSecond ? 1 : 0)) * sh.HG * RC +
                                h * RC + col;
-          if (g == 0) part_ml[slot] = make_float2(ref[nt][j], sum[nt][j]);
+          if (g == 0) part_ml[slot] = make_float2(-nref[nt][j], sum[nt][j]);
 #pragma unroll
           for (int b = 0; b < NB; ++b)
             *reinterpret_cast<float4*>(part_o + slot * D + 32 * b + 4 * g) =
@@ -992,12 +1113,12 @@ k_q4_merge(const int64_t* __restrict__ prefix, const float2* __restrict__ part_m
     lse[row] = l == 0.f ? __int_as_float(0xff800000) : (ref + log2f(l)) * 0.6931471805599453f;
 }
 
-// Heads of a CTA: all of them, or the largest divisor whose records begin on 16 bytes
-int heads_of(int hkv, int D, int most) {
-  if (hkv <= most) return hkv;
-  for (int d = most; d > 0; --d)
-    if (hkv % d == 0 && d * q4::record_bytes(D) % 16 == 0) return d;
-  return 0;
+// Heads of a CTA: all of them, or the largest divisor that the warps can take
+int heads_of(int hkv) {
+  if (hkv <= kConsumers) return hkv;
+  int d = kConsumers;
+  while (hkv % d) --d;
+  return d;
 }
 
 struct Config {
@@ -1022,35 +1143,33 @@ Config configure(const pks_q4_attention_args& a) {
   sh.trim = a.trim;
   sh.causal = a.k ? 0 : a.causal;
   sh.R = sh.Nq * sh.G;
-  // Sixteen rows at a time on eight warps, or eight on sixteen; eight also where
-  // more heads than the eight warps can take would be read apart.
+  // eight query rows at a time, or sixteen
   cf.NT = sh.R > 8 ? 2 : 1;
-  int hg = heads_of(a.Hkv, a.D, cf.NT == 2 ? 8 : 16);
-  if (cf.NT == 2 && a.Hkv > 8 && hg < 4) {
-    cf.NT = 1;
-    hg = heads_of(a.Hkv, a.D, 16);
-  }
-  if (hg == 0) return cf;  // (HG 0: no such shape)
-  const int warps = cf.NT == 2 ? 8 : 16;
+  const int hg = heads_of(a.Hkv);
+  const int tiles = cf.NT == 2 ? 1 : 2;
   sh.HG = hg;
   sh.NHG = a.Hkv / hg;
   sh.NRC = (sh.R + 8 * cf.NT - 1) / (8 * cf.NT);
-  sh.WPH = warps / hg;
-  sh.TS = 16 * sh.WPH;
+  sh.WPH = kConsumers / hg;
+  sh.TS = 16 * tiles * sh.WPH;
   sh.row_bytes = q4::token_bytes(a.Hkv, a.D);
-  sh.slice = sh.NHG == 1 ? sh.row_bytes : hg * q4::record_bytes(a.D);
+  sh.taken = sh.NHG == 1 ? sh.row_bytes : hg * q4::record_bytes(a.D);
+  sh.unit = sh.taken % 16 ? 8 : 16;
+  sh.slice = (sh.taken + 15) / 16 * 16;
   sh.swz_pool = q4::swizzled(sh.row_bytes);
   sh.swz_smem = q4::swizzled(sh.slice);
   // whole runs of a page by one copy where its rows lie as the stage has them
   sh.bulk = !a.k && sh.NHG == 1 && (!sh.swz_pool || a.page_size % 8 == 0) &&
             (int64_t)a.page_size * sh.row_bytes >= kBulkBytes;
-  const int chunks = sh.slice / 16;
-  sh.chunk_magic = ((1u << 20) + chunks - 1) / chunks;
+  const int units = sh.taken / sh.unit, chunks = sh.slice / 16;
+  sh.chunk_magic = ((1u << 20) + units - 1) / units;
   sh.order = sh.swz_smem || chunks % 2 ? kOrderOdd : chunks % 4 == 2 ? kOrderTwo : kOrderFour;
   const int scratch = hg * (sh.WPH / 2) * cf.NT * (a.D / 4 + 4) * 32 * 4;
   const int nv = (4 * sh.Bv + 15) / 16 * 16, stage = 2 * sh.TS * sh.slice;
   int n = (kSmemMax - scratch - nv) / stage;
   sh.stages = n > kMaxStages ? kMaxStages : n;
+  // (at least kProducers fit for every shape: a stage is 40 KiB at most.  With fewer a
+  // producer could pass the barrier of a stage that is a whole round behind)
   sh.ring = sh.stages * stage;
   sh.scratch_at = sh.ring;
   sh.nv_at = sh.ring + scratch;
@@ -1059,11 +1178,11 @@ Config configure(const pks_q4_attention_args& a) {
   return cf;
 }
 
-template <int D, int NT, int NW>
+template <int D, int NT, int TT>
 cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const Config& cf,
                         cudaStream_t s) {
   static bool done[64] = {false};
-  auto kern = k_q4_attention<D, NT, NW>;
+  auto kern = k_q4_attention<D, NT, TT>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1080,7 +1199,7 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
   float* po = reinterpret_cast<float*>(ws + L.part_o);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
   const Q4Shape& sh = cf.sh;
-  e = launch_ex(kern, dim3(sh.grid), dim3((NW + 1) * 32), cf.smem, s, /*pdl=*/true,
+  e = launch_ex(kern, dim3(sh.grid), dim3((kConsumers + kProducers) * 32), cf.smem, s, /*pdl=*/true,
                 /*coop=*/false, a.seq_lens, a.block_table, a.topk_idx,
                 static_cast<const __nv_bfloat16*>(a.q), static_cast<const uint8_t*>(a.pool_k),
                 static_cast<const uint8_t*>(a.pool_v), out, a.lse, prefix, ml, po,
@@ -1096,8 +1215,6 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
 }
 
 }  // namespace
-
-bool q4_supported(const pks_q4_attention_args& a) { return configure(a).sh.HG > 0; }
 
 Q4Layout q4_layout(const pks_q4_attention_args& a) {
   const Config cf = configure(a);
@@ -1116,8 +1233,8 @@ cudaError_t launch_q4_attention(const pks_q4_attention_args& a, const Q4Layout& 
                                 cudaStream_t s) {
   const Config cf = configure(a);
   if (a.D == 64)
-    return cf.NT == 2 ? launch_main<64, 2, 8>(a, L, cf, s) : launch_main<64, 1, 16>(a, L, cf, s);
-  return cf.NT == 2 ? launch_main<128, 2, 8>(a, L, cf, s) : launch_main<128, 1, 16>(a, L, cf, s);
+    return cf.NT == 2 ? launch_main<64, 2, 1>(a, L, cf, s) : launch_main<64, 1, 2>(a, L, cf, s);
+  return cf.NT == 2 ? launch_main<128, 2, 1>(a, L, cf, s) : launch_main<128, 1, 2>(a, L, cf, s);
 }
 
 }  // namespace pks
