@@ -27,6 +27,8 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "pks_internal.h"
 #include "q4.cuh"
 #include "tcgen05.cuh"
@@ -37,7 +39,6 @@ namespace {
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
 constexpr int kConsumers = 8;  // warps, two a scheduler
 constexpr int kProducers = 4;  // warps, each filling every fourth stage
-constexpr uint32_t kProducerNs = 200, kConsumerNs = 20;  // between two looks at a barrier
 constexpr int kLookup = 128;   // tokens whose rows a producer finds at once
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
@@ -80,7 +81,7 @@ struct Q4Shape {
 #define PKS_MMA(NAME, TYPE)                                                                      \
   __device__ __forceinline__ void NAME(float(&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,      \
                                        uint32_t a3, uint32_t b0, uint32_t b1) {                  \
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
                  ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"              \
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                \
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));              \
@@ -88,7 +89,7 @@ struct Q4Shape {
   __device__ __forceinline__ void NAME##_add(float(&d)[4], uint32_t a0, uint32_t a1,             \
                                              uint32_t a2, uint32_t a3, uint32_t b0,              \
                                              uint32_t b1) {                                      \
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
                  ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"                  \
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                \
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                        \
@@ -98,7 +99,7 @@ PKS_MMA(mma_f16, "f16")
 #undef PKS_MMA
 __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
   uint32_t y;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -116,17 +117,18 @@ __device__ __forceinline__ float low_half(uint32_t u) {
   return __half2float(__low2half(bits_half2(u)));
 }
 
-// NW words from shared memory (8- or 16-byte aligned)
-template <int NW>
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[NW]) {
-  if constexpr (NW == 4)
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                 : "r"(addr));
-  else if constexpr (NW == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-  else
-    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(w[0]) : "r"(addr));
+// N words from shared memory (8- or 16-byte aligned)
+template <int N>
+__device__ __forceinline__ void lds(const uint8_t* at, uint32_t (&w)[N]) {
+  if constexpr (N == 4) {
+    const uint4 x = *reinterpret_cast<const uint4*>(at);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else if constexpr (N == 2) {
+    const uint2 x = *reinterpret_cast<const uint2*>(at);
+    w[0] = x.x, w[1] = x.y;
+  } else {
+    w[0] = *reinterpret_cast<const uint32_t*>(at);
+  }
 }
 __device__ __forceinline__ void sts_zero8(uint32_t addr) {
   asm volatile("st.shared.v2.b32 [%0], {%1, %1};\n" ::"r"(addr), "r"(0) : "memory");
@@ -145,7 +147,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
 
 // What a stage holds, from its producer to the consumers.  mask: the tokens present,
 // of each 16, and the flags above them.
-struct StageNote {
+struct alignas(16) StageNote {
   int v, c, p0, nv;  // segment (request or list, chunk), first position, positions in all
   uint32_t mask[16];
 };
@@ -282,17 +284,16 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   }
   __syncthreads();
   const int count = (int)(hi - lo);  // (at most 2^33 stages over all SMs)
-  // Waits of a warp, which sleeps between two looks: polling takes issue slots from the
-  // warps that work (a third of them, when the four producers looked every 50 cycles).
-  auto wait = [&](uint64_t* bar, uint32_t parity, uint32_t ns) -> bool {
+  // Waits of a warp.  Looks at the clock and at the other warps once in many polls (each of
+  // which the hardware holds back): polling takes issue slots from the warps that work.
+  auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     bool there = tc::mbar_test_wait(bar, parity);
     if (!there) {
       const long long t0 = clock64();
-      do {
-        if (*(volatile int*)&s_abort || clock64() - t0 > wait_cycles) break;
-        __nanosleep(ns);
-        there = tc::mbar_test_wait(bar, parity);
-      } while (!there);
+      while (!there && !*(volatile int*)&s_abort && clock64() - t0 <= wait_cycles) {
+#pragma unroll 1
+        for (int i = 0; i < 32 && !there; ++i) there = tc::mbar_try_wait(bar, parity);
+      }
     }
     return __all_sync(0xffffffffu, there) != 0;
   };
@@ -416,7 +417,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       for (int j = 0; j < nb; ++j, next += kProducers) {
         const int round = next / sh.stages, stage = next - round * sh.stages;
         const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
-        if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1, kProducerNs);
+        if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
         if (!ok) break;
         const Desc d = s_desc[j];
         const int hg = d.c / sh.NRC;
@@ -540,21 +541,61 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   auto join = [&]() {  // of the consumer warps
     __syncwarp();
     if (lane == 0) tc::mbar_arrive(&bar_join);
-    ok = ok && wait(&bar_join, join_phase, kConsumerNs);
+    ok = ok && wait(&bar_join, join_phase);
     join_phase ^= 1;
   };
 
+  bool ready = false;  // the stage at hand has landed
   for (int done = 0; done < count; ++done) {
-    ok = wait(&bar_full[stage], phase, kConsumerNs);
+    if (!ready) ok = wait(&bar_full[stage], phase);
     if (!ok) break;
+    // ---------------- all of the stage that this warp needs, and on with the ring ----------
     const StageNote* note = &s_note[stage];
     uint32_t mask[TT];
 #pragma unroll
     for (int u = 0; u < TT; ++u) mask[u] = note->mask[sub * TT + u];
     const uint32_t flags = mask[0];
-    if (flags & kFirst) {
+    const int4 seg = *reinterpret_cast<const int4*>(note);  // v, c, p0, nv
+    uint32_t k0[TT][NB], k1[TT][NB], kp0[TT][NB], kp1[TT][NB];
+    uint32_t w[TT][4][NB / 2], s01[TT][NB], s23[TT][NB], ma0[TT], ma2[TT];
+    {
+      const uint8_t* base = smem + (uint32_t)stage * 2 * half;
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        const uint8_t* from = base + u * 16 * sh.slice;
+        lds(from + k_code0, k0[u]);
+        lds(from + k_code1, k1[u]);
+        lds(from + k_pair0, kp0[u]);
+        lds(from + k_pair1, kp1[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        const uint8_t* from = base + u * 16 * sh.slice;
+        uint32_t x[4][NB], m[4][1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          lds(from + v_pair[i], x[i]);
+          lds(from + v_pair[i] + m_word, m[i]);
+          lds(from + v_code[i], w[u][i]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          s01[u][b] = __byte_perm(x[0][b], x[1][b], 0x5410);
+          s23[u][b] = __byte_perm(x[2][b], x[3][b], 0x5410);
+        }
+        ma0[u] = __byte_perm(m[0][0], m[1][0], 0x7632);
+        ma2[u] = __byte_perm(m[2][0], m[3][0], 0x7632);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(&bar_empty[stage]);
+    if (++stage == sh.stages) {
+      stage = 0;
+      phase ^= 1;
+    }
+    if (__builtin_expect(flags & kFirst, 0)) {
       // ---------------- the segment's queries ----------------
-      const int hg = note->c / sh.NRC, rc = note->c - hg * sh.NRC;
+      const int hg = seg.y / sh.NRC, rc = seg.y - hg * sh.NRC;
       const int head = hg * sh.HG + h;
       const __nv_bfloat16* from = q;
       behind(from);
@@ -565,7 +606,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         float x[NB][8];
         if (r < sh.R) {
           const int i = r / sh.G;
-          const int64_t row = ((int64_t)note->v * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
+          const int64_t row = ((int64_t)seg.x * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
             const uint4 w = *reinterpret_cast<const uint4*>(from + row * D + 32 * b + 8 * t);
@@ -655,135 +696,50 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       }
     }
 
-    uint32_t present = 0, absent = 0;
+    // ---------------- scores ----------------
+    float tot[TT][NT][4];
 #pragma unroll
     for (int u = 0; u < TT; ++u) {
-      present |= mask[u];
-      absent |= ~mask[u];
-    }
-    if (present & 0xffffu) {
-      const uint32_t base = ring + (uint32_t)stage * 2 * half;
-      const uint32_t tile_bytes = 16 * sh.slice;
-      // ---------------- scores ----------------
-      float tot[TT][NT][4];
+      uint32_t a0, a1;
+      if constexpr (NB == 4) {
+        a0 = __byte_perm(t & 1 ? kp0[u][2] : kp0[u][0], t & 1 ? kp0[u][3] : kp0[u][1], 0x7632);
+        a1 = __byte_perm(t & 1 ? kp1[u][2] : kp1[u][0], t & 1 ? kp1[u][3] : kp1[u][1], 0x7632);
+      } else {
+        a0 = __byte_perm(kp0[u][0], kp0[u][1], 0x7632);
+        a1 = __byte_perm(kp1[u][0], kp1[u][1], 0x7632);
+      }
 #pragma unroll
-      for (int u = 0; u < TT; ++u) {
-        const uint32_t from = base + u * tile_bytes;
-        uint32_t w0[NB], w1[NB], p0w[NB], p1w[NB];
-        lds(from + k_code0, w0);
-        lds(from + k_code1, w1);
-        lds(from + k_pair0, p0w);
-        lds(from + k_pair1, p1w);
-        uint32_t a0, a1;
-        if constexpr (NB == 4) {
-          a0 = __byte_perm(t & 1 ? p0w[2] : p0w[0], t & 1 ? p0w[3] : p0w[1], 0x7632);
-          a1 = __byte_perm(t & 1 ? p1w[2] : p1w[0], t & 1 ? p1w[3] : p1w[1], 0x7632);
-        } else {
-          a0 = __byte_perm(p0w[0], p0w[1], 0x7632);
-          a1 = __byte_perm(p1w[0], p1w[1], 0x7632);
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        float acc[4];
+        mma_f16(acc, a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
+        // units: 2^(p - 112) here, 2^(p - 133) below
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tot[u][nt][e] = acc[e] * 4.76837158203125e-07f;
+      }
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        const uint32_t x0 = k0[u][b], x1 = k1[u][b], y0 = x0 >> 8, y1 = x1 >> 8;
+        const float s0 = low_half(kp0[u][b]), s1 = low_half(kp1[u][b]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float acc[4];
-          mma_f16(acc, a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
-          // units: 2^(p - 112) here, 2^(p - 133) below
-#pragma unroll
-          for (int e = 0; e < 4; ++e) tot[u][nt][e] = acc[e] * 4.76837158203125e-07f;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t x0 = w0[b], x1 = w1[b], y0 = x0 >> 8, y1 = x1 >> 8;
-          const float s0 = low_half(p0w[b]), s1 = low_half(p1w[b]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float acc[4];
-            mma_bf16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
-                     qf[nt][b][0], qf[nt][b][1]);
-            mma_bf16_add(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u,
-                         y1 & 0x00f000f0u, qf[nt][b][2], qf[nt][b][3]);
-            tot[u][nt][0] = fmaf(acc[0], s0, tot[u][nt][0]);
-            tot[u][nt][1] = fmaf(acc[1], s0, tot[u][nt][1]);
-            tot[u][nt][2] = fmaf(acc[2], s1, tot[u][nt][2]);
-            tot[u][nt][3] = fmaf(acc[3], s1, tot[u][nt][3]);
-          }
+          mma_bf16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
+                   qf[nt][b][0], qf[nt][b][1]);
+          mma_bf16_add(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u,
+                       y1 & 0x00f000f0u, qf[nt][b][2], qf[nt][b][3]);
+          tot[u][nt][0] = fmaf(acc[0], s0, tot[u][nt][0]);
+          tot[u][nt][1] = fmaf(acc[1], s0, tot[u][nt][1]);
+          tot[u][nt][2] = fmaf(acc[2], s1, tot[u][nt][2]);
+          tot[u][nt][3] = fmaf(acc[3], s1, tot[u][nt][3]);
         }
       }
-      const bool masked = (absent & 0xffffu) | (flags & kEdge);
-      if (masked) {
-        // of the first query's tokens, from this warp's first on
-        const int left = note->nv - sh.Nq + 1 - note->p0 - sub * TT * 16;
-        const int first = note->c % sh.NRC * RC + 2 * t;
-#pragma unroll
-        for (int u = 0; u < TT; ++u) {
-          const bool on0 = mask[u] >> tok0 & 1, on1 = mask[u] >> tok1 & 1;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int lim =
-                  (flags & kEdge ? left + min((first + nt * 8 + j) / sh.G, sh.Nq - 1) : 16 * TT) -
-                  16 * u;
-              if (!on0 || tok0 >= lim) tot[u][nt][j] = kNegInf;
-              if (!on1 || tok1 >= lim) tot[u][nt][2 + j] = kNegInf;
-            }
-        }
-      }
-      // ---------------- V's scales ----------------
-      uint32_t s01[TT][NB], s23[TT][NB], ma0[TT], ma2[TT];
-      uint32_t any = 0;
-#pragma unroll
-      for (int u = 0; u < TT; ++u) {
-        uint32_t w[4][NB], m[4][1];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t from = base + u * tile_bytes + v_pair[i];
-          lds(from, w[i]);
-          lds(from + m_word, m[i]);
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          s01[u][b] = __byte_perm(w[0][b], w[1][b], 0x5410);
-          s23[u][b] = __byte_perm(w[2][b], w[3][b], 0x5410);
-          any |= s01[u][b] | s23[u][b];
-        }
-        ma0[u] = __byte_perm(m[0][0], m[1][0], 0x7632);
-        ma2[u] = __byte_perm(m[2][0], m[3][0], 0x7632);
-      }
-      // p s stays below 2^16 while all s are below 2^(1 + sx)
-      if (__any_sync(0xffffffffu, any & 0x40004000u)) {  // some are 2 or more, or NaN
-        __half2 s_max = bits_half2(0);
-#pragma unroll
-        for (int u = 0; u < TT; ++u)
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-            s_max = __hmax2(s_max, __hmax2(bits_half2(s01[u][b]), bits_half2(s23[u][b])));
-        float top = fmaxf(__low2float(s_max), __high2float(s_max));
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1)
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-        const int now = min((int)(__float_as_uint(top) >> 23) - 127, 16);
-        if (now > sx) {
-          const float f = __int_as_float((127 - (now - sx)) << 23);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              nref[nt][j] -= (float)(now - sx);
-              sum[nt][j] *= f;
-              om[nt][j] *= f;
-            }
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-#pragma unroll
-              for (int e = 0; e < 8; ++e) o[nt][b][e >> 2][e & 3] *= f;
-          }
-          sx = now;
-        }
-      }
-      // ---------------- softmax ----------------
-      const float x_max = (float)(14 - sx);
-      float x[TT][NT][4];
-      float x_top = kNegInf;
+    }
+    // ---------------- weights ----------------
+    // As if all tokens counted, no reference had to move and all s were below 2^(1 + sx);
+    // when that is not so, which is rare, they are made anew.
+    float x[TT][NT][4], p[TT][NT][4];
+    uint32_t pt0[TT][NT], pt1[TT][NT];
+    auto exponents = [&]() {
 #pragma unroll
       for (int u = 0; u < TT; ++u)
 #pragma unroll
@@ -792,56 +748,124 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                nref[nt][0], nref[nt][1]);
           fma2(x[u][nt][2], x[u][nt][3], tot[u][nt][2], tot[u][nt][3], cs[nt][0], cs[nt][1],
                nref[nt][0], nref[nt][1]);
-          x_top = fmaxf(fmaxf(x_top, fmaxf(x[u][nt][0], x[u][nt][1])),
-                        fmaxf(x[u][nt][2], x[u][nt][3]));
         }
-      if (__any_sync(0xffffffffu, x_top > x_max)) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            float top = kNegInf;
-#pragma unroll
-            for (int u = 0; u < TT; ++u) top = fmaxf(top, fmaxf(tot[u][nt][j], tot[u][nt][2 + j]));
-            top *= cs[nt][j];
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1)
-              top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const float was = nref[nt][j];
-            if (top + was > x_max) {
-              nref[nt][j] = x_max - 3.f - top;
-              const float f = ex2(nref[nt][j] - was);
-              sum[nt][j] *= f;
-              om[nt][j] *= f;
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int m = 0; m < 2; ++m) {
-                  o[nt][b][m][j] *= f;
-                  o[nt][b][m][2 + j] *= f;
-                }
-            }
-          }
-#pragma unroll
-          for (int u = 0; u < TT; ++u)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              x[u][nt][e] = fmaf(tot[u][nt][e], cs[nt][e & 1], nref[nt][e & 1]);
-        }
-      }
-      uint32_t pt0[TT][NT], pt1[TT][NT], seen0[TT][NT], seen1[TT][NT];
+    };
+    auto weights = [&]() {
 #pragma unroll
       for (int u = 0; u < TT; ++u)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float p[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) p[e] = ex2(x[u][nt][e]);
-          add2(sum[nt][0], sum[nt][1], p[0], p[1]);
-          add2(sum[nt][0], sum[nt][1], p[2], p[3]);
-          pt0[u][nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[0], p[1])));
-          pt1[u][nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[2], p[3])));
-          if (masked) {
+          for (int e = 0; e < 4; ++e) p[u][nt][e] = ex2(x[u][nt][e]);
+          pt0[u][nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[u][nt][0], p[u][nt][1])));
+          pt1[u][nt] = movmatrix_t(half2_bits(__floats2half2_rn(p[u][nt][2], p[u][nt][3])));
+        }
+    };
+    exponents();
+    float x_top = kNegInf;
+    uint32_t any = 0, all = 0xffffu;
+#pragma unroll
+    for (int u = 0; u < TT; ++u) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        x_top = fmaxf(fmaxf(x_top, fmaxf(x[u][nt][0], x[u][nt][1])),
+                      fmaxf(x[u][nt][2], x[u][nt][3]));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) any |= s01[u][b] | s23[u][b];
+      all &= mask[u];
+    }
+    const bool redo = __any_sync(0xffffffffu, x_top > (float)(14 - sx) || (any & 0x40004000u) ||
+                                                  all != 0xffffu || (flags & kEdge));
+    weights();
+    if (__builtin_expect(redo, 0)) {
+      // tokens that are not there, or beyond a query's limit
+      const int left = seg.w - sh.Nq + 1 - seg.z - sub * TT * 16;  // of the first query's
+      const int first = seg.y % sh.NRC * RC + 2 * t;
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        const bool on0 = mask[u] >> tok0 & 1, on1 = mask[u] >> tok1 & 1;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const int lim =
+                (flags & kEdge ? left + min((first + nt * 8 + j) / sh.G, sh.Nq - 1) : 16 * TT) -
+                16 * u;
+            if (!on0 || tok0 >= lim) tot[u][nt][j] = kNegInf;
+            if (!on1 || tok1 >= lim) tot[u][nt][2 + j] = kNegInf;
+          }
+      }
+      // larger scales: p s stays below 2^16 while all are below 2^(1 + sx)
+      __half2 s_max = bits_half2(0);
+#pragma unroll
+      for (int u = 0; u < TT; ++u)
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          s_max = __hmax2(s_max, __hmax2(bits_half2(s01[u][b]), bits_half2(s23[u][b])));
+      float s_top = fmaxf(__low2float(s_max), __high2float(s_max));
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1)
+        s_top = fmaxf(s_top, __shfl_xor_sync(0xffffffffu, s_top, d));
+      const int now = max(sx, min((int)(__float_as_uint(s_top) >> 23) - 127, 16));
+      // the references, in reach of the largest score
+      const float x_max = (float)(14 - now);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float top = kNegInf;
+#pragma unroll
+          for (int u = 0; u < TT; ++u) top = fmaxf(top, fmaxf(tot[u][nt][j], tot[u][nt][2 + j]));
+          top *= cs[nt][j];
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const float was = nref[nt][j];
+          nref[nt][j] -= (float)(now - sx);
+          if (top + nref[nt][j] > x_max) nref[nt][j] = x_max - 3.f - top;
+          const float f = ex2(nref[nt][j] - was);
+          sum[nt][j] *= f;
+          om[nt][j] *= f;
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+              o[nt][b][m][j] *= f;
+              o[nt][b][m][2 + j] *= f;
+            }
+        }
+      sx = now;
+      exponents();
+      weights();
+    }
+    if (done + 1 < count) ready = tc::mbar_test_wait(&bar_full[stage], phase);
+    ready = __all_sync(0xffffffffu, ready) != 0;
+    // ---------------- values ----------------
+    // The products start from zero every time and are added on their own: the tensor
+    // core cuts off what lies below the accumulator's last place, and both sums grow
+    // to many times their difference (131,072 tokens: 0.017 of the result's norm
+    // instead of 0.0018).
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float acc[4];
+      mma_f16(acc, ma0[0], 0u, ma2[0], 0u, pt0[0][nt], pt1[0][nt]);
+#pragma unroll
+      for (int u = 1; u < TT; ++u)
+        mma_f16_add(acc, ma0[u], 0u, ma2[u], 0u, pt0[u][nt], pt1[u][nt]);
+      add2(om[nt][0], om[nt][1], acc[0], acc[1]);
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
+        add2(sum[nt][0], sum[nt][1], p[u][nt][0], p[u][nt][1]);
+        add2(sum[nt][0], sum[nt][1], p[u][nt][2], p[u][nt][3]);
+      }
+    }
+    auto values = [&](auto edge) {
+      // (at an edge, an s without a number must not reach the queries that do not see it)
+      uint32_t seen0[TT][NT], seen1[TT][NT];
+      if constexpr (decltype(edge)::value) {
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
             auto seen = [&](int e) {
               return (tot[u][nt][e] == kNegInf ? 0u : 0xffffu) |
                      (tot[u][nt][e + 1] == kNegInf ? 0u : 0xffff0000u);
@@ -849,25 +873,6 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             seen0[u][nt] = movmatrix_t(seen(0));
             seen1[u][nt] = movmatrix_t(seen(2));
           }
-        }
-      // ---------------- values ----------------
-      // The products start from zero every time and are added on their own: the tensor
-      // core cuts off what lies below the accumulator's last place, and both sums grow
-      // to many times their difference (131,072 tokens: 0.017 of the result's norm
-      // instead of 0.0018).
-      uint32_t w[TT][4][NB / 2];
-#pragma unroll
-      for (int u = 0; u < TT; ++u)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) lds(base + u * tile_bytes + v_code[i], w[u][i]);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float acc[4];
-        mma_f16(acc, ma0[0], 0u, ma2[0], 0u, pt0[0][nt], pt1[0][nt]);
-#pragma unroll
-        for (int u = 1; u < TT; ++u)
-          mma_f16_add(acc, ma0[u], 0u, ma2[u], 0u, pt0[u][nt], pt1[u][nt]);
-        add2(om[nt][0], om[nt][1], acc[0], acc[1]);
       }
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -882,7 +887,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           for (int nt = 0; nt < NT; ++nt) {
             uint32_t b0 = half2_bits(__hmul2(bits_half2(pt0[u][nt]), bits_half2(s01[u][b])));
             uint32_t b1 = half2_bits(__hmul2(bits_half2(pt1[u][nt]), bits_half2(s23[u][b])));
-            if (masked) {  // (an s without a number must not reach rows that do not see it)
+            if constexpr (decltype(edge)::value) {
               b0 &= seen0[u][nt];
               b1 &= seen1[u][nt];
             }
@@ -907,18 +912,13 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             add2(o[nt][b][m][2], o[nt][b][m][3], acc[nt][m][2], acc[nt][m][3]);
           }
       }
-    }
-    const int seg_v = note->v, seg_c = note->c;
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&bar_empty[stage]);
-    if (++stage == sh.stages) {
-      stage = 0;
-      phase ^= 1;
-    }
-    if (!(flags & kLast)) continue;
+    };
+    if (__builtin_expect(flags & kEdge, 0)) values(std::true_type{});
+    else values(std::false_type{});
+    if (__builtin_expect(!(flags & kLast), 1)) continue;
 
     // ---------------- end of the segment, or of the CTA's part of it ----------------
-    const int hg = seg_c / sh.NRC, rc = seg_c - hg * sh.NRC, head = hg * sh.HG + h;
+    const int hg = seg.y / sh.NRC, rc = seg.y - hg * sh.NRC, head = hg * sh.HG + h;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -993,7 +993,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         if (r >= sh.R) continue;
         if (flags & kWhole) {
           const int i = r / sh.G;
-          const int64_t row = ((int64_t)seg_v * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
+          const int64_t row = ((int64_t)seg.x * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
           const float l = sum[nt][j];
           const float f = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
