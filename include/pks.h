@@ -678,7 +678,9 @@ pks_status pks_q4_read(const pks_q4_rows_args* args, pks_stream stream);
  * A query without tokens gets zeros.  Tokens that a query does not attend to are
  * without influence on it, whatever they hold. */
 typedef struct pks_q4_attention_args {
-  int32_t B;              /* requests; B * Nq <= 4096 */
+  int32_t B;              /* requests; B * Nq <= 4096, and below 2^31 in all: 16-token
+                             pieces that a full batch has, times groups of eight KV heads and
+                             of eight query rows (Nq * Hq / Hkv) a KV head, rounded up */
   int32_t Hq, Hkv;        /* 1 <= Hq / Hkv <= 16; Hkv <= 1024 */
   int32_t D;              /* 64 or 128 */
   int32_t page_size, max_pages, num_pages;  /* num_pages * page_size < 2^31 and

@@ -20,9 +20,8 @@
 //
 // One persistent CTA an SM.  All (request, head group, row chunk) segments are cut into
 // stages of 16 tokens a consumer warp; the CTAs take equal runs of stages.  Four
-// producer warps, each for every fourth stage, find the tokens' rows (128 tokens at a
-// time, so that the two dependent loads are rare) and fill a ring of stages; a
-// consumer warp owns one head and 16 tokens of every stage.  Segments that several CTAs hold parts of are
+// producer warps, each for every fourth stage, find the tokens' rows and fill a ring of
+// stages; a consumer warp owns one head and some tokens of every stage.  Segments that several CTAs hold parts of are
 // joined by k_q4_merge.
 
 #include <cuda_fp16.h>
@@ -39,7 +38,6 @@ namespace {
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
 constexpr int kConsumers = 8;  // warps, two a scheduler
 constexpr int kProducers = 4;  // warps, each filling every fourth stage
-constexpr int kLookup = 128;   // tokens whose rows a producer finds at once
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
 constexpr int kSmemMax = 227 * 1024 - 8192;  // dynamic; the rest is the static part
@@ -65,7 +63,9 @@ struct Q4Shape {
   int causal;
   int R;             // query rows of a KV head: Nq * G
   int HG, NHG, NRC;  // heads of a CTA, groups of them, chunks of rows
-  int WPH, TS;       // warps a head, tokens a stage
+  int WPH, TS, ts_log2;  // warps a head, tokens a stage (a power of two)
+  int cap;           // tokens a request can have
+  uint32_t page_magic;   // ceil(2^32 / page_size), 0 for 1
   int row_bytes;     // of a token in the pool
   int taken;         // of it what a head group takes, copied in units of 8 or 16 bytes
   int unit;
@@ -155,11 +155,6 @@ struct alignas(16) StageNote {
 // kSecond: not the CTA's first segment; kEdge: some token lies beyond some query's limit
 constexpr uint32_t kFirst = 1u << 16, kLast = 2u << 16, kWhole = 4u << 16, kSecond = 8u << 16,
                    kEdge = 16u << 16;
-struct Desc {
-  int v, c, p0, nv;
-  uint32_t flags;
-};
-
 // Registers a thread of this warpgroup has from here on.  All of a CTA's together no
 // more than it was launched with.
 template <int N, bool MORE>
@@ -183,10 +178,16 @@ __device__ __forceinline__ void fma2(float& d0, float& d1, float a0, float a1, f
       : "f"(a0), "f"(a1), "f"(b0), "f"(b1), "f"(c0), "f"(c1));
 }
 
-// First stage of CTA i when W stages go to n CTAs
-__device__ __forceinline__ int64_t first_stage(int64_t W, int n, int i) {
-  return W * i / n;
-}
+// W stages over n CTAs: the first W % n of them take one more than the rest
+struct Shares {
+  int each, more;
+  __device__ __forceinline__ Shares(int W, int n) : each(W / n), more(W - W / n * n) {}
+  __device__ __forceinline__ int first(int cta) const { return each * cta + min(cta, more); }
+  __device__ __forceinline__ int holder(int stage) const {
+    const int big = more * (each + 1);
+    return stage < big ? stage / (each + 1) : more + (stage - big) / each;
+  }
+};
 
 template <int D, int NT, int TT>
 __global__ void __launch_bounds__((kConsumers + kProducers) * 32, 1)
@@ -194,7 +195,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                const int32_t* __restrict__ lists, const __nv_bfloat16* __restrict__ q,
                const uint8_t* __restrict__ pool_k, const uint8_t* __restrict__ pool_v,
                __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
-               int64_t* __restrict__ prefix, float2* __restrict__ part_ml,
+               int32_t* __restrict__ prefix, float2* __restrict__ part_ml,
                float* __restrict__ part_o, int32_t* __restrict__ err, const Q4Shape sh,
                float scale_log2, long long wait_cycles) {
   constexpr int NW = kConsumers, NWARPS = NW + kProducers, NTHREADS = NWARPS * 32, NB = D / q4::kGroup, REC = q4::record_bytes(D);
@@ -205,11 +206,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   // bar_join: the consumer warps
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
-  __shared__ Desc s_desc_all[kProducers][kLookup / 16];
   __shared__ int s_row_all[kProducers][kMaxTokens];
-  __shared__ uint16_t s_run_all[kProducers][kMaxTokens];
-  __shared__ int64_t s_warp[NWARPS], s_rest;
-  __shared__ int s_first, s_abort;
+  __shared__ int s_warp[NWARPS], s_first, s_rest, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = tc::smem_u32(smem);
   const int half = sh.TS * sh.slice;
@@ -233,49 +231,49 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   const int per = (sh.Bv + NTHREADS - 1) / NTHREADS, v_lo = min(tid * per, sh.Bv),
             v_hi = min(v_lo + per, sh.Bv);
   const int chunks = sh.NHG * sh.NRC;
-  const int64_t cap = (int64_t)sh.max_pages * sh.page_size;
-  int64_t mine = 0;
+  auto stages_of = [&](int n) { return (n + sh.TS - 1) >> sh.ts_log2; };
+  int mine = 0;
   for (int v = v_lo; v < v_hi; ++v) {
-    int n = seq_lens[v / sh.lists];
-    if (n < 0 || n > cap) {
+    int n = seq_lens[sh.lists == 1 ? v : v / sh.lists];
+    if (n < 0 || n > sh.cap) {
       *err = kErrLen;
       n = 0;
     }
     if (sh.k) n = n == 0 ? 0 : sh.trim ? min(n, sh.k) : sh.k;
     s_nv[v] = n;
-    mine += (int64_t)((n + sh.TS - 1) / sh.TS) * chunks;
+    mine += stages_of(n) * chunks;
   }
-  int64_t upto = mine;
+  int upto = mine;
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
+    const int x = __shfl_up_sync(0xffffffffu, upto, d);
     if (lane >= d) upto += x;
   }
   if (lane == 31) s_warp[warp] = upto;
   __syncthreads();
-  int64_t W = 0, before = 0;
+  int W = 0, before = upto - mine;  // (stages before this thread's first segment)
+#pragma unroll
   for (int w = 0; w < NWARPS; ++w) {
-    if (w < warp) before += s_warp[w];
-    W += s_warp[w];
+    const int x = s_warp[w];
+    if (w < warp) before += x;
+    W += x;
   }
-  before += upto - mine;  // stages before this thread's first segment
-  const int n_ctas = (int)min((int64_t)sh.grid, W);
-  const int cta = blockIdx.x;
+  const int n_ctas = min(sh.grid, W), cta = blockIdx.x;
   if (cta == 0) {
-    int64_t at = before;
+    int at = before;
     for (int v = v_lo; v < v_hi; ++v) {
       prefix[v] = at;
-      at += (int64_t)((s_nv[v] + sh.TS - 1) / sh.TS) * chunks;
+      at += stages_of(s_nv[v]) * chunks;
     }
     if (tid == 0) prefix[sh.Bv] = W;
   }
   if (cta >= n_ctas) return;
-  const int64_t lo = first_stage(W, n_ctas, cta), hi = first_stage(W, n_ctas, cta + 1);
+  const Shares shares(W, n_ctas);
+  const int lo = shares.first(cta), hi = shares.first(cta + 1), count = hi - lo;
   if (lo >= before && lo < before + mine) {
-    int64_t rest = lo - before;
-    int v = v_lo;
+    int rest = lo - before, v = v_lo;
     for (;; ++v) {
-      const int64_t units = (int64_t)((s_nv[v] + sh.TS - 1) / sh.TS) * chunks;
+      const int units = stages_of(s_nv[v]) * chunks;
       if (rest < units) break;
       rest -= units;
     }
@@ -283,7 +281,6 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     s_rest = rest;
   }
   __syncthreads();
-  const int count = (int)(hi - lo);  // (at most 2^33 stages over all SMs)
   // Waits of a warp.  Looks at the clock and at the other warps once in many polls (each of
   // which the hardware holds back): polling takes issue slots from the warps that work.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -309,18 +306,17 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     set_registers<88, false>();
     behind(seq_lens, block_table, lists);
     const int me = warp - NW;
-    Desc* s_desc = s_desc_all[me];
     int* s_row = s_row_all[me];
-    uint16_t* s_run = s_run_all[me];
-    int v = s_first;
-    int n = s_nv[v], T = (n + sh.TS - 1) / sh.TS;
-    int c = (int)(s_rest / T), tile = (int)(s_rest - (int64_t)c * T);
-    int64_t seg_at = lo - tile;  // first stage of the segment at hand
-    const int cpt = sh.taken / sh.unit, most = max(1, kLookup / sh.TS);
-    int at_stage = 0;  // of the CTA's run, the one that v, c, tile stand at
-    auto forward = [&](int to) {  // (not beyond the run's last stage)
-      int step = to - at_stage;
-      at_stage = to;
+    int v = s_first, n = s_nv[v], T = stages_of(n), c = 0, tile = s_rest;
+    if (chunks > 1) {
+      c = tile / T;
+      tile -= c * T;
+    }
+    int seg_at = lo - tile;  // first stage of the segment at hand
+    int request = sh.lists == 1 ? v : v / sh.lists;
+    int next = 0;            // of the CTA's run, the stage that these stand at
+    auto forward = [&](int step) {  // (not beyond the run's last stage)
+      next += step;
       while (step >= T - tile) {
         step -= T - tile;
         tile = 0;
@@ -329,172 +325,188 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           c = 0;
           do n = s_nv[++v];
           while (n == 0);
-          T = (n + sh.TS - 1) / sh.TS;
+          T = stages_of(n);
+          request = sh.lists == 1 ? v : v / sh.lists;
         }
       }
       tile += step;
     };
-    int next = me;  // the next stage to fill
+    // t / page_size by a rounded-up reciprocal, which is at most one too large
+    auto page_of = [&](int t, int& slot) {
+      int p = sh.page_magic ? (int)__umulhi((uint32_t)t, sh.page_magic) : t;
+      slot = t - p * sh.page_size;
+      if (slot < 0) {
+        --p;
+        slot += sh.page_size;
+      }
+      return p;
+    };
+    int stage = me, round = 0;  // (never more producers than stages)
     bool ok = true;
-    while (ok && next < count) {
-      const int nb = min(most, (count - next + kProducers - 1) / kProducers);
-      // ---- which segments the stages are of
-#pragma unroll 1
-      for (int j = 0; j < nb; ++j) {
-        const int i = next + j * kProducers;
-        forward(i);
-        if (lane == 0) {
-          uint32_t f = 0;
-          if (tile == 0 || i == 0) f |= kFirst;
-          if (tile == T - 1 || i == count - 1) f |= kLast;
-          if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
-          if (seg_at > lo) f |= kSecond;
-          if (sh.causal &&
-              (tile + 1) * sh.TS > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G)) f |= kEdge;
-          s_desc[j] = {v, c, tile * sh.TS, n, f};
-        }
-      }
-      __syncwarp();
-      // ---- the rows of their tokens
-      for (int t0 = 0; t0 < nb * sh.TS; t0 += kLookup) {
-        int t[kLookup / 32], b[kLookup / 32], left[kLookup / 32];
-#pragma unroll
-        for (int i = 0; i < kLookup / 32; ++i) {
-          const int j = t0 + lane + 32 * i, st = j / sh.TS;
-          t[i] = -1;
-          b[i] = left[i] = 0;
-          if (st < nb) {
-            const Desc d = s_desc[st];
-            const int p = d.p0 + j - st * sh.TS;
-            left[i] = d.nv - p;
-            if (p < d.nv) {
-              b[i] = d.v / sh.lists;
-              t[i] = sh.k ? lists[(int64_t)d.v * sh.k + p] : p;
-            }
+    if (me < count) forward(me);
+    for (int i = me; i < count; i += kProducers) {
+      if (i != next) forward(i - next);
+      const int p0 = tile << sh.ts_log2, here = min(n - p0, sh.TS);  // tokens in reach
+      const int* table = block_table + (int64_t)request * sh.max_pages;
+      // ---- where the stage's tokens lie
+      int run_at = 0, run = 0, run_row = -1;  // a run of tokens in one page, a lane each
+      bool whole = true;                      // all in reach are there
+      if (sh.bulk) {
+        int slot;
+        const int page0 = page_of(p0, slot);
+        run_at = lane == 0 ? 0 : lane * sh.page_size - slot;
+        if (run_at < here) {
+          const int page = table[page0 + lane];
+          if (page < 0 || page >= sh.num_pages) {
+            *err = kErrPage;
+          } else {
+            run = min((lane + 1) * sh.page_size - slot, here) - run_at;
+            run_row = page * sh.page_size + (lane == 0 ? slot : 0);
           }
         }
-        if (sh.k) {
+        whole = __all_sync(0xffffffffu, run_at >= here || run_row >= 0);
+        if (!whole) {  // token by token below
+          for (int at = lane; at < sh.TS; at += 32) s_row[at] = -1;
+          __syncwarp();
+          for (int r = 0; r < run; ++r) s_row[run_at + r] = run_row + r;
+          __syncwarp();
+        }
+      } else {
+        const int len = sh.k ? seq_lens[request] : 0;
+        for (int at0 = 0; at0 < sh.TS; at0 += 128) {  // (four tokens a lane at once)
+          int t[4], page[4], slot[4];
 #pragma unroll
-          for (int i = 0; i < kLookup / 32; ++i)
-            if (t[i] != -1 && (t[i] < 0 || t[i] >= seq_lens[b[i]])) {
+          for (int u = 0; u < 4; ++u) {
+            const int at = at0 + 32 * u + lane;
+            t[u] = at >= here ? -1 : sh.k ? lists[(int64_t)v * sh.k + p0 + at] : p0 + at;
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (sh.k && t[u] != -1 && (t[u] < 0 || t[u] >= len)) {
               *err = kErrToken;
-              t[i] = -1;
+              t[u] = -1;
             }
-        }
+            page[u] = t[u] < 0 ? -1 : table[page_of(t[u], slot[u])];
+          }
 #pragma unroll
-        for (int i = 0; i < kLookup / 32; ++i) {
-          if (t[i] < 0) continue;
-          const int p = t[i] / sh.page_size;
-          b[i] = block_table[(int64_t)b[i] * sh.max_pages + p];  // its page
-          t[i] -= p * sh.page_size;                              // and slot
-        }
-#pragma unroll
-        for (int i = 0; i < kLookup / 32; ++i) {
-          const int j = t0 + lane + 32 * i;
-          if (j >= nb * sh.TS) break;
-          int row = -1, run = 0;
-          if (t[i] >= 0) {
-            if (b[i] < 0 || b[i] >= sh.num_pages) {
-              *err = kErrPage;
-            } else {
-              row = b[i] * sh.page_size + t[i];
-              if (sh.bulk) {
-                // a copy from the first token of a page, or of the stage, on
-                const int at = j % sh.TS;
-                if (at == 0 || t[i] == 0) run = min(min(sh.page_size - t[i], sh.TS - at), left[i]);
-              } else {
-                run = t[i] & 7;
-              }
+          for (int u = 0; u < 4; ++u) {
+            const int at = at0 + 32 * u + lane;
+            int row = -1;
+            if (t[u] >= 0) {
+              if (page[u] < 0 || page[u] >= sh.num_pages) *err = kErrPage;
+              else row = page[u] * sh.page_size + slot[u];
             }
+            if (at < sh.TS) s_row[at] = row;
           }
-          s_row[j] = row;
-          s_run[j] = (uint16_t)run;
-        }
-      }
-      __syncwarp();
-      // ---- fill the stages
-#pragma unroll 1
-      for (int j = 0; j < nb; ++j, next += kProducers) {
-        const int round = next / sh.stages, stage = next - round * sh.stages;
-        const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
-        if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
-        if (!ok) break;
-        const Desc d = s_desc[j];
-        const int hg = d.c / sh.NRC;
-        StageNote* note = &s_note[stage];
-        int present = 0;
-        bool zeroed = false;
-        for (int i = 0; i * 32 < sh.TS; ++i) {
-          const int at = i * 32 + lane;
-          const bool here = at < sh.TS && s_row[j * sh.TS + at] >= 0;
-          const uint32_t m = __ballot_sync(0xffffffffu, here);
-          if (lane == 0) {
-            note->mask[2 * i] = (m & 0xffffu) | d.flags;
-            note->mask[2 * i + 1] = m >> 16 | d.flags;
-          }
-          present += __popc(m);
-          if (at < sh.TS && !here) {
-            // no weight, but what the slot holds takes part in a product
-            zeroed = true;
-            const uint32_t x = sh.swz_smem ? q4::swizzle(at) : 0;
-            for (int h = 0; h < sh.HG; ++h)
-#pragma unroll
-              for (int o = 0; o < 4 * NB; o += 8)
-                sts_zero8(dst_v + at * sh.slice + ((h * REC + D / 2 + o) ^ x));
-          }
-        }
-        if (zeroed) tc::fence_async_smem();
-        if (lane == 0) {
-          note->v = d.v;
-          note->c = d.c;
-          note->p0 = d.p0;
-          note->nv = d.nv;
         }
         __syncwarp();
-        if (sh.bulk) {
-          if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], 2u * present * sh.slice);
-          __syncwarp();
-          for (int at = lane; at < sh.TS; at += 32) {
-            const int run = s_run[j * sh.TS + at];
-            if (run > 0) {
-              const int64_t src = (int64_t)s_row[j * sh.TS + at] * sh.row_bytes;
-              const uint32_t o = at * sh.slice;
-              bulk_load(dst_k + o, pool_k + src, run * sh.slice, &bar_full[stage]);
-              bulk_load(dst_v + o, pool_v + src, run * sh.slice, &bar_full[stage]);
-            }
-          }
-        } else {
-          const int off = hg * sh.HG * REC, all = sh.TS * cpt;
-          for (int i = lane; i < all; i += 32) {
-            const int at = (int)((uint32_t)i * sh.chunk_magic >> 20), ch = i - at * cpt;
-            const int row = s_row[j * sh.TS + at];
-            if (row >= 0) {
-              const uint32_t xs = sh.swz_pool ? (uint32_t)s_run[j * sh.TS + at] << 4 : 0;
-              const uint32_t xd = sh.swz_smem ? q4::swizzle(at) : 0;
-              const int64_t src =
-                  (int64_t)row * sh.row_bytes + ((uint32_t)(off + sh.unit * ch) ^ xs);
-              const uint32_t o = at * sh.slice + ((uint32_t)(sh.unit * ch) ^ xd);
-              if (sh.unit == 16) {
-                tc::cp_async16(dst_k + o, pool_k + src, 16);
-                tc::cp_async16(dst_v + o, pool_v + src, 16);
-              } else {
-                cp_async8(dst_k + o, pool_k + src);
-                cp_async8(dst_v + o, pool_v + src);
-              }
-            }
-          }
-          tc::cp_async_arrive(&bar_full[stage]);
-          if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
+        whole = false;
+      }
+      // ---- fill it
+      if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
+      if (!ok) {
+        next = i;
+        break;
+      }
+      const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
+      StageNote* note = &s_note[stage];
+      uint32_t f = 0;
+      if (tile == 0 || i == 0) f |= kFirst;
+      if (tile == T - 1 || i == count - 1) f |= kLast;
+      if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
+      if (seg_at > lo) f |= kSecond;
+      if (sh.causal && p0 + sh.TS > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G)) f |= kEdge;
+      int present = here;
+      bool zeroed = false;
+      auto absent = [&](int at) {  // no weight, but what the slot holds takes part in a product
+        zeroed = true;
+        const uint32_t x = sh.swz_smem ? q4::swizzle(at) : 0;
+        for (int h = 0; h < sh.HG; ++h)
+#pragma unroll
+          for (int o = 0; o < 4 * NB; o += 8)
+            sts_zero8(dst_v + at * sh.slice + ((h * REC + D / 2 + o) ^ x));
+      };
+      if (whole) {
+        if (lane < 16) note->mask[lane] = (1u << min(max(here - 16 * lane, 0), 16)) - 1 | f;
+        for (int at = here + lane; at < sh.TS; at += 32) absent(at);
+      } else {
+        present = 0;
+        for (int at0 = 0; at0 < sh.TS; at0 += 32) {
+          const int at = at0 + lane;
+          const bool there = at < sh.TS && s_row[at] >= 0;
+          const uint32_t m = __ballot_sync(0xffffffffu, there);
+          if (lane < 2) note->mask[at0 / 16 + lane] = (m >> 16 * lane & 0xffffu) | f;
+          present += __popc(m);
+          if (at < sh.TS && !there) absent(at);
         }
+      }
+      if (zeroed) tc::fence_async_smem();
+      if (lane == 0) {
+        note->v = v;
+        note->c = c;
+        note->p0 = p0;
+        note->nv = n;
+      }
+      __syncwarp();
+      if (sh.bulk) {
+        if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], 2u * present * sh.slice);
+        __syncwarp();
+        if (run > 0) {
+          const int64_t src = (int64_t)run_row * sh.row_bytes;
+          const uint32_t o = run_at * sh.slice;
+          bulk_load(dst_k + o, pool_k + src, run * sh.slice, &bar_full[stage]);
+          bulk_load(dst_v + o, pool_v + src, run * sh.slice, &bar_full[stage]);
+        }
+      } else {
+        constexpr int U = 4;  // copies whose places are worked out together
+        const int cpt = sh.taken / sh.unit, all = sh.TS * cpt, off = c / sh.NRC * sh.HG * REC;
+        for (int i0 = lane; i0 < all; i0 += 32 * U) {
+          int row[U], at[U];
+          uint32_t o[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int id = i0 + 32 * u;
+            at[u] = (int)((uint32_t)id * sh.chunk_magic >> 20);
+            o[u] = (id - at[u] * cpt) * sh.unit;
+            row[u] = id < all ? s_row[at[u]] : -1;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            if (row[u] < 0) continue;
+            uint32_t xs = 0;
+            if (sh.swz_pool) {
+              int slot;
+              page_of(row[u], slot);
+              xs = q4::swizzle(slot);
+            }
+            const int64_t src = (int64_t)row[u] * sh.row_bytes + ((off + o[u]) ^ xs);
+            const uint32_t to =
+                at[u] * sh.slice + (o[u] ^ (sh.swz_smem ? q4::swizzle(at[u]) : 0));
+            if (sh.unit == 16) {
+              tc::cp_async16(dst_k + to, pool_k + src, 16);
+              tc::cp_async16(dst_v + to, pool_v + src, 16);
+            } else {
+              cp_async8(dst_k + to, pool_k + src);
+              cp_async8(dst_v + to, pool_v + src);
+            }
+          }
+        }
+        tc::cp_async_arrive(&bar_full[stage]);
+        if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
+      }
+      stage += kProducers;
+      if (stage >= sh.stages) {
+        stage -= sh.stages;
+        ++round;
       }
     }
     if (!ok) {
       give_up();
       // the copies in flight land before the CTA gives its memory up
       for (int i = next - kProducers; i >= 0 && i >= next - sh.stages; i -= kProducers) {
-        const int round = i / sh.stages;
+        const int r = i / sh.stages;
         const long long t0 = clock64();
-        while (!tc::mbar_try_wait(&bar_full[i - round * sh.stages], round & 1) &&
+        while (!tc::mbar_try_wait(&bar_full[i - r * sh.stages], r & 1) &&
                clock64() - t0 < kWaitCycles) {
         }
       }
@@ -1028,7 +1040,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 // taking every WARPS-th part.  Rows without tokens get zeros.
 template <int D, int WARPS>
 __global__ void __launch_bounds__(256)
-k_q4_merge(const int64_t* __restrict__ prefix, const float2* __restrict__ part_ml,
+k_q4_merge(const int32_t* __restrict__ prefix, const float2* __restrict__ part_ml,
            const float* __restrict__ part_o, __nv_bfloat16* __restrict__ out,
            float* __restrict__ lse, const Q4Shape sh, int RC) {
   constexpr int PL = D / 32;  // values a lane
@@ -1044,18 +1056,18 @@ k_q4_merge(const int64_t* __restrict__ prefix, const float2* __restrict__ part_m
   const int in = (int)(row - v * sh.Nq * sh.Hq), i = in / sh.Hq, hq = in - i * sh.Hq;
   const int head = hq / sh.G, r = i * sh.G + hq - head * sh.G;
   const int hg = head / sh.HG, h = head - hg * sh.HG, rc = r / RC, col = r - rc * RC;
-  const int64_t W = prefix[sh.Bv], p0 = prefix[v], units = prefix[v + 1] - p0;
+  const int W = prefix[sh.Bv], p0 = prefix[v], units = prefix[v + 1] - p0;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float ref = kNone, l = 0.f;
   bool write = units == 0;
   if (units > 0) {
-    const int64_t T = units / (sh.NHG * sh.NRC), s0 = p0 + (hg * sh.NRC + rc) * T, s1 = s0 + T;
-    const int n = (int)min((int64_t)sh.grid, W);
-    const int first = (int)(((s0 + 1) * n - 1) / W), last = (int)((s1 * n - 1) / W);
+    const int T = units / (sh.NHG * sh.NRC), s0 = p0 + (hg * sh.NRC + rc) * T, s1 = s0 + T;
+    const Shares shares(W, min(sh.grid, W));
+    const int first = shares.holder(s0), last = shares.holder(s1 - 1);
     write = first != last;
     if (write) {
       for (int c = first + w; c <= last; c += WARPS) {
-        const int second = c == first && first_stage(W, n, c) < s0 ? 1 : 0;
+        const int second = c == first && shares.first(c) < s0 ? 1 : 0;
         const int64_t slot = ((int64_t)2 * c + second) * sh.HG * RC + h * RC + col;
         const float2 ml = part_ml[slot];
         float4 x;
@@ -1152,6 +1164,10 @@ Config configure(const pks_q4_attention_args& a) {
   sh.NRC = (sh.R + 8 * cf.NT - 1) / (8 * cf.NT);
   sh.WPH = kConsumers / hg;
   sh.TS = 16 * tiles * sh.WPH;
+  sh.ts_log2 = 31 - __builtin_clz(sh.TS);
+  sh.cap = (int)((int64_t)a.max_pages * a.page_size);
+  sh.page_magic =
+      a.page_size > 1 ? (uint32_t)(((uint64_t(1) << 32) + a.page_size - 1) / a.page_size) : 0;
   sh.row_bytes = q4::token_bytes(a.Hkv, a.D);
   sh.taken = sh.NHG == 1 ? sh.row_bytes : hg * q4::record_bytes(a.D);
   sh.unit = sh.taken % 16 ? 8 : 16;
@@ -1194,7 +1210,7 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
   }
   const float scale = a.sm_scale > 0.f ? a.sm_scale : 1.f / sqrtf((float)a.D);
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
-  int64_t* prefix = reinterpret_cast<int64_t*>(ws + L.prefix);
+  int32_t* prefix = reinterpret_cast<int32_t*>(ws + L.prefix);
   float2* ml = reinterpret_cast<float2*>(ws + L.part_ml);
   float* po = reinterpret_cast<float*>(ws + L.part_o);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
@@ -1210,18 +1226,24 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
   const bool few = rows <= kFewRows;
   return launch_ex(few ? k_q4_merge<D, 8> : k_q4_merge<D, 1>,
                    dim3((unsigned)(few ? rows : (rows + 7) / 8)), dim3(256), 0, s, /*pdl=*/true,
-                   /*coop=*/false, (const int64_t*)prefix, (const float2*)ml, (const float*)po,
+                   /*coop=*/false, (const int32_t*)prefix, (const float2*)ml, (const float*)po,
                    out, a.lse, sh, 8 * NT);
 }
 
 }  // namespace
+
+bool q4_supported(const pks_q4_attention_args& a) {
+  const Q4Shape sh = configure(a).sh;  // the stages of a full batch are counted in 32 bits
+  const int64_t each = (sh.k ? sh.k : sh.cap) / sh.TS + 1;
+  return each * sh.NHG * sh.NRC * sh.Bv <= INT32_MAX;
+}
 
 Q4Layout q4_layout(const pks_q4_attention_args& a) {
   const Config cf = configure(a);
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   Q4Layout L{};
   L.prefix = 256;
-  L.part_ml = up(L.prefix + sizeof(int64_t) * (size_t)(cf.sh.Bv + 1));
+  L.part_ml = up(L.prefix + sizeof(int32_t) * (size_t)(cf.sh.Bv + 1));
   // a CTA's first segment and its last
   const size_t rows = (size_t)2 * cf.sh.grid * cf.sh.HG * 8 * cf.NT;
   L.part_o = up(L.part_ml + sizeof(float2) * rows);

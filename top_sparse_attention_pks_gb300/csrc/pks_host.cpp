@@ -843,7 +843,7 @@ pks_status q4_check(const pks_q4_attention_args* a) {
   if (a->Hq / a->Hkv > 16 || a->n_queries > pks::kQ4MaxQueries || a->k > pks::kMaxK)
     return PKS_ERR_UNSUPPORTED;
   if ((int64_t)a->B * std::max(1, a->n_queries) > pks::kMaxB) return PKS_ERR_UNSUPPORTED;
-  return PKS_OK;
+  return pks::q4_supported(*a) ? PKS_OK : PKS_ERR_UNSUPPORTED;
 }
 
 pks_status q4_check_workspace(const pks_q4_attention_args* a, const pks::Q4Layout& L) {

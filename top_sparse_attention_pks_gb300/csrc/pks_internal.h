@@ -234,6 +234,7 @@ struct Q4Layout {
   size_t prefix, part_ml, part_o, total;
 };
 constexpr int kQ4MaxQueries = 64;
+bool q4_supported(const pks_q4_attention_args& a);
 Q4Layout q4_layout(const pks_q4_attention_args& a);
 cudaError_t launch_q4_rows(const pks_q4_rows_args& a, bool write, cudaStream_t s);
 cudaError_t launch_q4_attention(const pks_q4_attention_args& a, const Q4Layout& L,
