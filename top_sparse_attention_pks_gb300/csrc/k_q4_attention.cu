@@ -40,7 +40,7 @@ constexpr int kConsumers = 8;  // warps, two a scheduler
 constexpr int kProducers = 4;  // warps, each filling every fourth stage
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 227 * 1024 - 8192;  // dynamic; the rest is the static part
+constexpr int kSmemMax = 227 * 1024 - 10240;  // dynamic; the rest is the static part
 constexpr int kBulkBytes = 2048;  // of a page, from which on its runs are copied whole
 constexpr int kFewRows = 4096;    // up to which a block joins a row, else a warp
 constexpr float kNone = -3e38f;  // reference of a row that has seen no token
@@ -71,7 +71,7 @@ struct Q4Shape {
   int unit;
   int slice;         // distance between tokens in shared memory
   int swz_pool, swz_smem, bulk;
-  uint32_t chunk_magic;  // ceil(2^20 / units a token)
+  int lanes;         // that copy a token, a unit or two each
   uint64_t order;
   int stages, ring, scratch_at, nv_at;  // bytes of the ring; where scratch and lengths begin
   int grid;
@@ -206,7 +206,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   // bar_join: the consumer warps
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
-  __shared__ int s_row_all[kProducers][kMaxTokens];
+  __shared__ int2 s_row_all[kProducers][kMaxTokens];  // a token's row (-1: none), its slot
   __shared__ int s_warp[NWARPS], s_first, s_rest, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = tc::smem_u32(smem);
@@ -306,7 +306,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     set_registers<88, false>();
     behind(seq_lens, block_table, lists);
     const int me = warp - NW;
-    int* s_row = s_row_all[me];
+    int2* s_row = s_row_all[me];
     int v = s_first, n = s_nv[v], T = stages_of(n), c = 0, tile = s_rest;
     if (chunks > 1) {
       c = tile / T;
@@ -366,9 +366,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
         whole = __all_sync(0xffffffffu, run_at >= here || run_row >= 0);
         if (!whole) {  // token by token below
-          for (int at = lane; at < sh.TS; at += 32) s_row[at] = -1;
+          for (int at = lane; at < sh.TS; at += 32) s_row[at] = make_int2(-1, 0);
           __syncwarp();
-          for (int r = 0; r < run; ++r) s_row[run_at + r] = run_row + r;
+          for (int r = 0; r < run; ++r) s_row[run_at + r] = make_int2(run_row + r, 0);
           __syncwarp();
         }
       } else {
@@ -396,7 +396,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
               if (page[u] < 0 || page[u] >= sh.num_pages) *err = kErrPage;
               else row = page[u] * sh.page_size + slot[u];
             }
-            if (at < sh.TS) s_row[at] = row;
+            if (at < sh.TS) s_row[at] = make_int2(row, slot[u]);
           }
         }
         __syncwarp();
@@ -433,7 +433,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         present = 0;
         for (int at0 = 0; at0 < sh.TS; at0 += 32) {
           const int at = at0 + lane;
-          const bool there = at < sh.TS && s_row[at] >= 0;
+          const bool there = at < sh.TS && s_row[at].x >= 0;
           const uint32_t m = __ballot_sync(0xffffffffu, there);
           if (lane < 2) note->mask[at0 / 16 + lane] = (m >> 16 * lane & 0xffffu) | f;
           present += __popc(m);
@@ -458,37 +458,42 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           bulk_load(dst_v + o, pool_v + src, run * sh.slice, &bar_full[stage]);
         }
       } else {
-        constexpr int U = 4;  // copies whose places are worked out together
-        const int cpt = sh.taken / sh.unit, all = sh.TS * cpt, off = c / sh.NRC * sh.HG * REC;
-        for (int i0 = lane; i0 < all; i0 += 32 * U) {
-          int row[U], at[U];
-          uint32_t o[U];
+        // `lanes` lanes a token, each with a unit or two of it; some tokens at once
+        constexpr int U = 4;
+        const int ln = sh.lanes, tok = lane / ln, unit = lane & (ln - 1), step = 32 / ln;
+        const int cpt = sh.taken / sh.unit, off = c / sh.NRC * sh.HG * REC;
+        const uint32_t o0 = unit * sh.unit, o1 = (unit + ln) * sh.unit;
+        const bool on0 = unit < cpt, on1 = unit + ln < cpt;
+        const int64_t to_v = pool_v - pool_k;
+#pragma unroll 1
+        for (int at0 = tok; at0 < sh.TS; at0 += step * U) {
+          int2 row[U];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const int id = i0 + 32 * u;
-            at[u] = (int)((uint32_t)id * sh.chunk_magic >> 20);
-            o[u] = (id - at[u] * cpt) * sh.unit;
-            row[u] = id < all ? s_row[at[u]] : -1;
+            const int at = at0 + u * step;
+            row[u] = at < sh.TS ? s_row[at] : make_int2(-1, 0);
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            if (row[u] < 0) continue;
-            uint32_t xs = 0;
-            if (sh.swz_pool) {
-              int slot;
-              page_of(row[u], slot);
-              xs = q4::swizzle(slot);
-            }
-            const int64_t src = (int64_t)row[u] * sh.row_bytes + ((off + o[u]) ^ xs);
-            const uint32_t to =
-                at[u] * sh.slice + (o[u] ^ (sh.swz_smem ? q4::swizzle(at[u]) : 0));
-            if (sh.unit == 16) {
-              tc::cp_async16(dst_k + to, pool_k + src, 16);
-              tc::cp_async16(dst_v + to, pool_v + src, 16);
-            } else {
-              cp_async8(dst_k + to, pool_k + src);
-              cp_async8(dst_v + to, pool_v + src);
-            }
+            if (row[u].x < 0) continue;
+            const int at = at0 + u * step;
+            const uint32_t xs = sh.swz_pool ? q4::swizzle(row[u].y) : 0;
+            const uint32_t xd = sh.swz_smem ? q4::swizzle(at) : 0;
+            const uint8_t* src = pool_k + (int64_t)row[u].x * sh.row_bytes;
+            const uint32_t to = dst_k + at * sh.slice;
+            auto copy = [&](uint32_t o) {
+              const uint8_t* a = src + ((off + o) ^ xs);
+              const uint32_t d = to + (o ^ xd);
+              if (sh.unit == 16) {
+                tc::cp_async16(d, a, 16);
+                tc::cp_async16(d + half, a + to_v, 16);
+              } else {
+                cp_async8(d, a);
+                cp_async8(d + half, a + to_v);
+              }
+            };
+            if (on0) copy(o0);
+            if (on1) copy(o1);
           }
         }
         tc::cp_async_arrive(&bar_full[stage]);
@@ -1178,7 +1183,7 @@ Config configure(const pks_q4_attention_args& a) {
   sh.bulk = !a.k && sh.NHG == 1 && (!sh.swz_pool || a.page_size % 8 == 0) &&
             (int64_t)a.page_size * sh.row_bytes >= kBulkBytes;
   const int units = sh.taken / sh.unit, chunks = sh.slice / 16;
-  sh.chunk_magic = ((1u << 20) + units - 1) / units;
+  for (sh.lanes = 1; sh.lanes < units && sh.lanes < 32;) sh.lanes *= 2;
   sh.order = sh.swz_smem || chunks % 2 ? kOrderOdd : chunks % 4 == 2 ? kOrderTwo : kOrderFour;
   const int scratch = hg * (sh.WPH / 2) * cf.NT * (a.D / 4 + 4) * 32 * 4;
   const int nv = (4 * sh.Bv + 15) / 16 * 16, stage = 2 * sh.TS * sh.slice;
