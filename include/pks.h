@@ -618,9 +618,7 @@ pks_status pks_pages_device_error(const pks_pages_args* args, int32_t* code, pks
  * a multiple of 16 bytes.  With NB = D / 32 groups the codes of a record are
  *   K: 32-bit word t * NB + b: values 32 b + 8 t + i in bits 4 i, i < 8 (t < 4)
  *   V: 16-bit word g * NB + b: values 32 b + 4 g + i in bits 4 i, i < 4 (g < 8)
- * the orders in which the attention's lanes take them.  Where token_bytes is a
- * multiple of 128, byte o of the token row in slot i of its page stands at
- * o ^ ((i & 7) << 4), which spreads a page's rows over the banks of shared memory.
+ * the orders in which the attention's lanes take them.
  * ---------------------------------------------------------------------- */
 
 /* Bytes of one token row of a pool, Hkv * (D/2 + D/8) filled up to a multiple of

@@ -35,20 +35,11 @@ def record_bytes(D):
     return D // 2 + D // 8
 
 
-def in_order(pool):
-    """A pool's token rows with their bytes put back in order."""
-    _, P, row = pool.shape
-    at = np.broadcast_to(np.arange(row), (P, row))
-    if row % 128 == 0:
-        at = at ^ ((np.arange(P)[:, None] & 7) << 4)
-    return np.take_along_axis(pool, np.broadcast_to(at, pool.shape), 2)
-
-
 def unpack(pool, Hkv, D, kind):
     """pool uint8 [num_pages, page_size, row] -> n [N, P, Hkv, D], s, m [N, P, Hkv, D / 32]."""
     N, P, row = pool.shape
     NB = D // GROUP
-    rec = in_order(pool)[:, :, :Hkv * record_bytes(D)].reshape(N, P, Hkv, record_bytes(D))
+    rec = pool[:, :, :Hkv * record_bytes(D)].reshape(N, P, Hkv, record_bytes(D))
     code = rec[..., :D // 2]
     nib = np.stack([code & 15, code >> 4], -1).reshape(N, P, Hkv, D)  # in order of the bits
     per = 8 if kind == "k" else 4  # values of a word, which are NB words apart

@@ -24,6 +24,8 @@
 // stages; a consumer warp owns one head and some tokens of every stage.  Segments that several CTAs hold parts of are
 // joined by k_q4_merge.
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -40,19 +42,32 @@ constexpr int kConsumers = 8;  // warps, two a scheduler
 constexpr int kProducers = 4;  // warps, each filling every fourth stage
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
-constexpr int kSmemMax = 227 * 1024 - 10240;  // dynamic; the rest is the static part
-constexpr int kBulkBytes = 2048;  // of a page, from which on its runs are copied whole
+constexpr int kSmemMax = 227 * 1024 - 6144;  // dynamic; the rest is the static part
+constexpr int kBulkBytes = 2048;   // of a page, from which on its runs are copied whole,
+constexpr int kTokenBytes = 512;   // rows smaller than this, that is
+constexpr int kTokenBytesLeast = 320;
 constexpr int kFewRows = 4096;    // up to which a block joins a row, else a warp
 constexpr float kNone = -3e38f;  // reference of a row that has seen no token
 
 // Tokens of a warp's 16 as the rows of its MMA tiles, four bits each (lowest: row 0).
 // Lanes of one shared-memory access hold tokens whose records lie in different
 // banks: rows 2 i and 2 i + 1 must stand 64 bytes apart (mod 128), the rows 0, 2, 4, 6
-// and 1, 3, 5, 7 32 bytes.  By the distance between tokens: odd multiples of 16 bytes
-// (or permuted rows), odd multiples of 32, of 64 (every second access in two).
+// and 1, 3, 5, 7 32 bytes.  By the distance between tokens: odd multiples of 16 bytes,
+// odd multiples of 32, of 64 (V's accesses in two).
 constexpr uint64_t kOrderOdd = 0xbf9d7351ae8c6240ull;
 constexpr uint64_t kOrderTwo = 0xdfceb9a857463120ull;
 constexpr uint64_t kOrderFour = 0xefdcab9867542310ull;
+
+// How a stage gets its tokens:
+//  kRuns   - dense, all heads of small rows: the tokens of one page by one bulk copy (a
+//            warp issues one in 63 cycles, so that pieces below 2 KiB do not keep up)
+//  kTokens - rows of 320 bytes or more: a bulk copy a token, at a distance in shared
+//            memory that suits the banks; two warps a stage, one for K and one for V
+//            (four warps: 7.3 TB/s of rows of 640 bytes, 6.3 of 320, 1.7 of 80)
+//  kBoxes  - dense, rows of 128-byte lines (D = 128 and Hkv a multiple of 8): TMA boxes of 16
+//            or 32 tokens, whose swizzle suits the banks; what fills no box as kLanes
+//  kLanes  - other small rows: 16 or 8 bytes a lane (cp.async)
+enum Copies { kRuns, kTokens, kBoxes, kLanes };
 
 struct Q4Shape {
   int Bv;            // requests; with selected tokens, requests times queries
@@ -70,8 +85,9 @@ struct Q4Shape {
   int taken;         // of it what a head group takes, copied in units of 8 or 16 bytes
   int unit;
   int slice;         // distance between tokens in shared memory
-  int swz_pool, swz_smem, bulk;
-  int lanes;         // that copy a token, a unit or two each
+  int copies;        // see above
+  int box;           // kBoxes: tokens of one
+  int lanes;         // kLanes: that copy a token, a unit or two each
   uint64_t order;
   int stages, ring, scratch_at, nv_at;  // bytes of the ring; where scratch and lengths begin
   int grid;
@@ -145,6 +161,11 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
+// Where byte o of a stage's K or V stands: boxes come with the 128-byte swizzle
+__device__ __forceinline__ uint32_t place(const Q4Shape& sh, uint32_t o) {
+  return sh.copies == kBoxes ? o ^ (o >> 7 & 7) << 4 : o;
+}
+
 // What a stage holds, from its producer to the consumers.  mask: the tokens present,
 // of each 16, and the flags above them.
 struct alignas(16) StageNote {
@@ -197,25 +218,27 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
                int32_t* __restrict__ prefix, float2* __restrict__ part_ml,
                float* __restrict__ part_o, int32_t* __restrict__ err, const Q4Shape sh,
-               float scale_log2, long long wait_cycles) {
+               float scale_log2, long long wait_cycles, const __grid_constant__ CUtensorMap map_k,
+               const __grid_constant__ CUtensorMap map_v) {
   constexpr int NW = kConsumers, NWARPS = NW + kProducers, NTHREADS = NWARPS * 32, NB = D / q4::kGroup, REC = q4::record_bytes(D);
   constexpr int RC = 8 * NT;  // query rows a chunk
   const float kNegInf = __int_as_float(0xff800000);
-  extern __shared__ __align__(1024) uint8_t smem[];
+  extern __shared__ uint8_t smem_raw[];
   // bar_full: the producer's announcement (and its lanes' copies); bar_empty and
   // bar_join: the consumer warps
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
-  __shared__ int2 s_row_all[kProducers][kMaxTokens];  // a token's row (-1: none), its slot
+  __shared__ int s_row_all[kProducers][kMaxTokens];  // tokens' rows in the pool (-1: none)
   __shared__ int s_warp[NWARPS], s_first, s_rest, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t ring = tc::smem_u32(smem);
+  const uint32_t ring = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* smem = smem_raw + (ring - tc::smem_u32(smem_raw));
   const int half = sh.TS * sh.slice;
   int* s_nv = reinterpret_cast<int*>(smem + sh.nv_at);
   const int consumers = sh.HG * sh.WPH;
   if (tid == 0) {
     for (int i = 0; i < sh.stages; ++i) {
-      tc::mbar_init(&bar_full[i], sh.bulk ? 1 : 33);
+      tc::mbar_init(&bar_full[i], sh.copies == kTokens ? 2 : sh.copies == kLanes ? 33 : 1);
       tc::mbar_init(&bar_empty[i], consumers);
     }
     tc::mbar_init(&bar_join, consumers);
@@ -306,7 +329,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     set_registers<88, false>();
     behind(seq_lens, block_table, lists);
     const int me = warp - NW;
-    int2* s_row = s_row_all[me];
+    int* s_row = s_row_all[me];
     int v = s_first, n = s_nv[v], T = stages_of(n), c = 0, tile = s_rest;
     if (chunks > 1) {
       c = tile / T;
@@ -341,174 +364,302 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       }
       return p;
     };
-    int stage = me, round = 0;  // (never more producers than stages)
-    bool ok = true;
-    if (me < count) forward(me);
-    for (int i = me; i < count; i += kProducers) {
-      if (i != next) forward(i - next);
-      const int p0 = tile << sh.ts_log2, here = min(n - p0, sh.TS);  // tokens in reach
-      const int* table = block_table + (int64_t)request * sh.max_pages;
-      // ---- where the stage's tokens lie
-      int run_at = 0, run = 0, run_row = -1;  // a run of tokens in one page, a lane each
-      bool whole = true;                      // all in reach are there
-      if (sh.bulk) {
-        int slot;
-        const int page0 = page_of(p0, slot);
-        run_at = lane == 0 ? 0 : lane * sh.page_size - slot;
-        if (run_at < here) {
-          const int page = table[page0 + lane];
-          if (page < 0 || page >= sh.num_pages) {
-            *err = kErrPage;
-          } else {
-            run = min((lane + 1) * sh.page_size - slot, here) - run_at;
-            run_row = page * sh.page_size + (lane == 0 ? slot : 0);
-          }
-        }
-        whole = __all_sync(0xffffffffu, run_at >= here || run_row >= 0);
-        if (!whole) {  // token by token below
-          for (int at = lane; at < sh.TS; at += 32) s_row[at] = make_int2(-1, 0);
-          __syncwarp();
-          for (int r = 0; r < run; ++r) s_row[run_at + r] = make_int2(run_row + r, 0);
-          __syncwarp();
-        }
-      } else {
-        const int len = sh.k ? seq_lens[request] : 0;
-        for (int at0 = 0; at0 < sh.TS; at0 += 128) {  // (four tokens a lane at once)
-          int t[4], page[4], slot[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int at = at0 + 32 * u + lane;
-            t[u] = at >= here ? -1 : sh.k ? lists[(int64_t)v * sh.k + p0 + at] : p0 + at;
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            if (sh.k && t[u] != -1 && (t[u] < 0 || t[u] >= len)) {
-              *err = kErrToken;
-              t[u] = -1;
-            }
-            page[u] = t[u] < 0 ? -1 : table[page_of(t[u], slot[u])];
-          }
-#pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int at = at0 + 32 * u + lane;
-            int row = -1;
-            if (t[u] >= 0) {
-              if (page[u] < 0 || page[u] >= sh.num_pages) *err = kErrPage;
-              else row = page[u] * sh.page_size + slot[u];
-            }
-            if (at < sh.TS) s_row[at] = make_int2(row, slot[u]);
-          }
-        }
-        __syncwarp();
-        whole = false;
-      }
-      // ---- fill it
-      if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
-      if (!ok) {
-        next = i;
-        break;
-      }
-      const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
-      StageNote* note = &s_note[stage];
+    auto flags_of = [&](int i) -> uint32_t {
       uint32_t f = 0;
       if (tile == 0 || i == 0) f |= kFirst;
       if (tile == T - 1 || i == count - 1) f |= kLast;
       if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
       if (seg_at > lo) f |= kSecond;
-      if (sh.causal && p0 + sh.TS > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G)) f |= kEdge;
-      int present = here;
-      bool zeroed = false;
-      auto absent = [&](int at) {  // no weight, but what the slot holds takes part in a product
-        zeroed = true;
-        const uint32_t x = sh.swz_smem ? q4::swizzle(at) : 0;
-        for (int h = 0; h < sh.HG; ++h)
+      if (sh.causal && ((tile + 1) << sh.ts_log2) > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G))
+        f |= kEdge;
+      return f;
+    };
+    // a token that is not there: no weight, but what its place holds takes part in a product
+    auto absent = [&](uint32_t dst_v, int at) {
+      for (int h = 0; h < sh.HG; ++h)
 #pragma unroll
-          for (int o = 0; o < 4 * NB; o += 8)
-            sts_zero8(dst_v + at * sh.slice + ((h * REC + D / 2 + o) ^ x));
+        for (int o = 0; o < 4 * NB; o += 8)
+          sts_zero8(dst_v + place(sh, at * sh.slice + h * REC + D / 2 + o));
+    };
+    // (the stages that one warp fills are never further apart than the ring is long)
+    const int stride = sh.copies == kTokens ? 2 : kProducers;
+    const int mine_from = sh.copies == kTokens ? me >> 1 : me;
+    int stage = mine_from, round = 0;
+    bool ok = true;
+    if (mine_from < count) forward(mine_from);
+    if (sh.copies == kTokens) {
+      // ---- a token a lane (or two), K or V ----
+      constexpr int PER = 2;
+      const bool is_v = me & 1;
+      const uint8_t* pool = is_v ? pool_v : pool_k;
+      int t[PER], page[PER], slot[PER], row[PER];
+      auto tokens = [&]() {  // of the stage at hand, as positions
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          const int at = 32 * u + lane, p = (tile << sh.ts_log2) + at;
+          t[u] = -1;
+          if (at < sh.TS && p < n) t[u] = sh.k ? lists[(int64_t)v * sh.k + p] : p;
+        }
       };
-      if (whole) {
-        if (lane < 16) note->mask[lane] = (1u << min(max(here - 16 * lane, 0), 16)) - 1 | f;
-        for (int at = here + lane; at < sh.TS; at += 32) absent(at);
-      } else {
-        present = 0;
-        for (int at0 = 0; at0 < sh.TS; at0 += 32) {
-          const int at = at0 + lane;
-          const bool there = at < sh.TS && s_row[at].x >= 0;
-          const uint32_t m = __ballot_sync(0xffffffffu, there);
-          if (lane < 2) note->mask[at0 / 16 + lane] = (m >> 16 * lane & 0xffffu) | f;
-          present += __popc(m);
-          if (at < sh.TS && !there) absent(at);
+      auto pages = [&]() {
+        const int* table = block_table + (int64_t)request * sh.max_pages;
+        const int len = sh.k ? seq_lens[request] : 0;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          if (sh.k && t[u] != -1 && (t[u] < 0 || t[u] >= len)) {
+            *err = kErrToken;
+            t[u] = -1;
+          }
+          page[u] = t[u] < 0 ? -1 : table[page_of(t[u], slot[u])];
         }
+      };
+      auto rows = [&]() {
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          row[u] = -1;
+          if (t[u] < 0) continue;
+          if (page[u] < 0 || page[u] >= sh.num_pages) *err = kErrPage;
+          else row[u] = page[u] * sh.page_size + slot[u];
+        }
+      };
+      if (mine_from < count) {
+        tokens();
+        pages();
+        rows();
       }
-      if (zeroed) tc::fence_async_smem();
-      if (lane == 0) {
-        note->v = v;
-        note->c = c;
-        note->p0 = p0;
-        note->nv = n;
-      }
-      __syncwarp();
-      if (sh.bulk) {
-        if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], 2u * present * sh.slice);
+      for (int i = mine_from; i < count; i += stride) {
+        const int4 seg = make_int4(v, c, tile << sh.ts_log2, n);
+        const uint32_t f = flags_of(i);
+        const bool more = i + stride < count;
+        // the next stage's places are looked up while this one waits and is filled
+        if (more) {
+          forward(stride);
+          tokens();
+        }
+        if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
+        if (!ok) {
+          next = i;
+          break;
+        }
+        if (more) pages();
+        const uint32_t dst = ring + (uint32_t)(2 * stage + is_v) * half;
+        StageNote* note = &s_note[stage];
+        uint32_t here[PER];
+        int present = 0;
+        bool gone = false;
+#pragma unroll
+        for (int u = 0; u < PER; ++u) {
+          here[u] = __ballot_sync(0xffffffffu, row[u] >= 0);
+          present += __popc(here[u]);
+          if (!is_v && lane < 2) note->mask[2 * u + lane] = (here[u] >> 16 * lane & 0xffffu) | f;
+          if (is_v && row[u] < 0 && 32 * u + lane < sh.TS) {
+            absent(dst, 32 * u + lane);
+            gone = true;
+          }
+        }
+        if (gone) tc::fence_async_smem();
+        if (!is_v && lane == 0) *reinterpret_cast<int4*>(note) = seg;
         __syncwarp();
-        if (run > 0) {
-          const int64_t src = (int64_t)run_row * sh.row_bytes;
-          const uint32_t o = run_at * sh.slice;
-          bulk_load(dst_k + o, pool_k + src, run * sh.slice, &bar_full[stage]);
-          bulk_load(dst_v + o, pool_v + src, run * sh.slice, &bar_full[stage]);
-        }
-      } else {
-        // `lanes` lanes a token, each with a unit or two of it; some tokens at once
-        constexpr int U = 4;
-        const int ln = sh.lanes, tok = lane / ln, unit = lane & (ln - 1), step = 32 / ln;
-        const int cpt = sh.taken / sh.unit, off = c / sh.NRC * sh.HG * REC;
-        const uint32_t o0 = unit * sh.unit, o1 = (unit + ln) * sh.unit;
-        const bool on0 = unit < cpt, on1 = unit + ln < cpt;
-        const int64_t to_v = pool_v - pool_k;
-#pragma unroll 1
-        for (int at0 = tok; at0 < sh.TS; at0 += step * U) {
-          int2 row[U];
+        if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], (uint32_t)present * sh.taken);
+        __syncwarp();
+        const int off = seg.y / sh.NRC * sh.HG * REC;
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int at = at0 + u * step;
-            row[u] = at < sh.TS ? s_row[at] : make_int2(-1, 0);
-          }
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            if (row[u].x < 0) continue;
-            const int at = at0 + u * step;
-            const uint32_t xs = sh.swz_pool ? q4::swizzle(row[u].y) : 0;
-            const uint32_t xd = sh.swz_smem ? q4::swizzle(at) : 0;
-            const uint8_t* src = pool_k + (int64_t)row[u].x * sh.row_bytes;
-            const uint32_t to = dst_k + at * sh.slice;
-            auto copy = [&](uint32_t o) {
-              const uint8_t* a = src + ((off + o) ^ xs);
-              const uint32_t d = to + (o ^ xd);
-              if (sh.unit == 16) {
-                tc::cp_async16(d, a, 16);
-                tc::cp_async16(d + half, a + to_v, 16);
-              } else {
-                cp_async8(d, a);
-                cp_async8(d + half, a + to_v);
-              }
-            };
-            if (on0) copy(o0);
-            if (on1) copy(o1);
-          }
+        for (int u = 0; u < PER; ++u)
+          if (row[u] >= 0)
+            bulk_load(dst + (32 * u + lane) * sh.slice,
+                      pool + (int64_t)row[u] * sh.row_bytes + off, sh.taken, &bar_full[stage]);
+        if (more) rows();
+        stage += stride;
+        if (stage >= sh.stages) {
+          stage -= sh.stages;
+          ++round;
         }
-        tc::cp_async_arrive(&bar_full[stage]);
-        if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
       }
-      stage += kProducers;
-      if (stage >= sh.stages) {
-        stage -= sh.stages;
-        ++round;
+    } else {
+      for (int i = mine_from; i < count; i += stride) {
+        if (i != next) forward(i - next);
+        const int p0 = tile << sh.ts_log2, here = min(n - p0, sh.TS);  // tokens in reach
+        const int* table = block_table + (int64_t)request * sh.max_pages;
+        // ---- where the stage's tokens lie
+        int run_at = 0, run = 0, run_row = -1;  // a run of tokens in one page, a lane each
+        bool whole = true;                      // all in reach are there
+        uint32_t full = 0;                      // boxes, and tokens in them
+        auto lone = [&](bool mine, int tokens) {  // tokens of a lane's page that go one by one
+          for (int at = lane; at < sh.TS; at += 32) s_row[at] = -1;
+          __syncwarp();
+          if (mine)
+            for (int r = 0; r < tokens; ++r) s_row[run_at + r] = run_row + r;
+          __syncwarp();
+        };
+        if (sh.copies == kBoxes) {
+          run_at = lane * sh.box;
+          const bool some = run_at < here;
+          if (some) {
+            int slot;
+            const int page = table[page_of(p0 + run_at, slot)];
+            if (page < 0 || page >= sh.num_pages) *err = kErrPage;
+            else run_row = page * sh.page_size + slot;
+          }
+          const bool boxed = run_row >= 0 && run_at + sh.box <= here;
+          full = __ballot_sync(0xffffffffu, boxed);
+          whole = __all_sync(0xffffffffu, boxed || run_at >= sh.TS);
+          if (!whole) lone(run_row >= 0 && !boxed, here - run_at);
+        } else if (sh.copies == kRuns) {
+          int slot;
+          const int page0 = page_of(p0, slot);
+          run_at = lane == 0 ? 0 : lane * sh.page_size - slot;
+          if (run_at < here) {
+            const int page = table[page0 + lane];
+            if (page < 0 || page >= sh.num_pages) {
+              *err = kErrPage;
+            } else {
+              run = min((lane + 1) * sh.page_size - slot, here) - run_at;
+              run_row = page * sh.page_size + (lane == 0 ? slot : 0);
+            }
+          }
+          whole = __all_sync(0xffffffffu, run_at >= here || run_row >= 0);
+          if (!whole) lone(true, run);  // (told apart below)
+        } else {
+          const int len = sh.k ? seq_lens[request] : 0;
+          for (int at0 = 0; at0 < sh.TS; at0 += 128) {  // (four tokens a lane at once)
+            int t[4], page[4], slot[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int at = at0 + 32 * u + lane;
+              t[u] = at >= here ? -1 : sh.k ? lists[(int64_t)v * sh.k + p0 + at] : p0 + at;
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              if (sh.k && t[u] != -1 && (t[u] < 0 || t[u] >= len)) {
+                *err = kErrToken;
+                t[u] = -1;
+              }
+              page[u] = t[u] < 0 ? -1 : table[page_of(t[u], slot[u])];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int at = at0 + 32 * u + lane;
+              int row = -1;
+              if (t[u] >= 0) {
+                if (page[u] < 0 || page[u] >= sh.num_pages) *err = kErrPage;
+                else row = page[u] * sh.page_size + slot[u];
+              }
+              if (at < sh.TS) s_row[at] = row;
+            }
+          }
+          __syncwarp();
+          whole = false;
+        }
+        // ---- fill it
+        if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
+        if (!ok) {
+          next = i;
+          break;
+        }
+        const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
+        StageNote* note = &s_note[stage];
+        const uint32_t f = flags_of(i);
+        int present = here;
+        bool gone = false;
+        if (whole) {
+          if (lane < 16) note->mask[lane] = ((1u << min(max(here - 16 * lane, 0), 16)) - 1) | f;
+          for (int at = here + lane; at < sh.TS; at += 32) {
+            absent(dst_v, at);
+            gone = true;
+          }
+        } else {
+          present = 0;
+          for (int at0 = 0; at0 < sh.TS; at0 += 32) {
+            const int at = at0 + lane;
+            const bool there =
+                at < sh.TS && (s_row[at] >= 0 || (sh.copies == kBoxes && full >> at / sh.box & 1));
+            const uint32_t m = __ballot_sync(0xffffffffu, there);
+            if (lane < 2) note->mask[at0 / 16 + lane] = (m >> 16 * lane & 0xffffu) | f;
+            present += __popc(m);
+            if (at < sh.TS && !there) {
+              absent(dst_v, at);
+              gone = true;
+            }
+          }
+        }
+        if (gone) tc::fence_async_smem();
+        if (lane == 0) *reinterpret_cast<int4*>(note) = make_int4(v, c, p0, n);
+        __syncwarp();
+        if (sh.copies == kRuns) {
+          if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], 2u * present * sh.slice);
+          __syncwarp();
+          if (run > 0) {
+            const int64_t src = (int64_t)run_row * sh.row_bytes;
+            const uint32_t o = run_at * sh.slice;
+            bulk_load(dst_k + o, pool_k + src, run * sh.slice, &bar_full[stage]);
+            bulk_load(dst_v + o, pool_v + src, run * sh.slice, &bar_full[stage]);
+          }
+        } else if (sh.copies == kLanes || !whole) {
+          // `lanes` lanes a token, each with a unit or two of it; some tokens at once
+          constexpr int U = 4;
+          const int ln = sh.lanes, tok = lane / ln, unit = lane & (ln - 1), step = 32 / ln;
+          const int cpt = sh.taken / sh.unit;
+          const uint32_t o0 = unit * sh.unit, o1 = (unit + ln) * sh.unit;
+          const bool on0 = unit < cpt, on1 = unit + ln < cpt;
+          const int64_t to_v = pool_v - pool_k;
+          const uint8_t* part = pool_k + c / sh.NRC * sh.HG * REC;
+#pragma unroll 1
+          for (int at0 = tok; at0 < sh.TS; at0 += step * U) {
+            int row[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              const int at = at0 + u * step;
+              row[u] = at < sh.TS ? s_row[at] : -1;
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              if (row[u] < 0) continue;
+              const uint8_t* src = part + (int64_t)row[u] * sh.row_bytes;
+              auto copy = [&](uint32_t o) {
+                const uint32_t to = dst_k + place(sh, (at0 + u * step) * sh.slice + o);
+                if (sh.unit == 16) {
+                  tc::cp_async16(to, src + o, 16);
+                  tc::cp_async16(to + half, src + to_v + o, 16);
+                } else {
+                  cp_async8(to, src + o);
+                  cp_async8(to + half, src + to_v + o);
+                }
+              };
+              if (on0) copy(o0);
+              if (on1) copy(o1);
+            }
+          }
+          if (sh.copies == kLanes) {
+            tc::cp_async_arrive(&bar_full[stage]);
+            if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
+          } else {  // (the end of a request: these copies land before the boxes are announced)
+            tc::cp_async_commit();
+            tc::cp_async_wait<0>();
+            __syncwarp();
+          }
+        }
+        if (sh.copies == kBoxes) {
+          if (lane == 0)
+            tc::mbar_arrive_expect(&bar_full[stage], 2u * __popc(full) * sh.box * sh.slice);
+          __syncwarp();
+          if (full >> lane & 1) {
+            const uint32_t o = run_at * sh.slice;
+            const int line = c / sh.NRC * (sh.slice / 128);
+            tc::tma_load_3d(dst_k + o, &map_k, 0, line, run_row, &bar_full[stage]);
+            tc::tma_load_3d(dst_v + o, &map_v, 0, line, run_row, &bar_full[stage]);
+          }
+        }
+        stage += stride;
+        if (stage >= sh.stages) {
+          stage -= sh.stages;
+          ++round;
+        }
       }
     }
     if (!ok) {
       give_up();
       // the copies in flight land before the CTA gives its memory up
-      for (int i = next - kProducers; i >= 0 && i >= next - sh.stages; i -= kProducers) {
+      for (int i = next - stride; i >= 0 && i >= next - sh.stages; i -= stride) {
         const int r = i / sh.stages;
         const long long t0 = clock64();
         while (!tc::mbar_try_wait(&bar_full[i - r * sh.stages], r & 1) &&
@@ -525,9 +676,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   const int h = warp / sh.WPH, sub = warp - h * sh.WPH;
   const int g = lane >> 2, t = lane & 3;
   auto token = [&](int r) { return (int)(sh.order >> (4 * r) & 15); };
-  auto at = [&](int tok, int off) -> uint32_t {  // (16 tokens on, the same permutation)
-    return (sub * TT * 16 + tok) * sh.slice +
-           ((uint32_t)(h * REC + off) ^ (sh.swz_smem ? q4::swizzle(tok) : 0));
+  auto at = [&](int tok, int off) -> uint32_t {  // (16 tokens on, a box is swizzled alike)
+    return sub * TT * 16 * sh.slice + place(sh, tok * sh.slice + h * REC + off);
   };
   // rows g and g + 8 of the tokens' tiles; K codes and pairs
   const int tok0 = token(g), tok1 = token(g + 8);
@@ -1176,27 +1326,57 @@ Config configure(const pks_q4_attention_args& a) {
   sh.row_bytes = q4::token_bytes(a.Hkv, a.D);
   sh.taken = sh.NHG == 1 ? sh.row_bytes : hg * q4::record_bytes(a.D);
   sh.unit = sh.taken % 16 ? 8 : 16;
+  const bool runs = !a.k && sh.NHG == 1 && sh.row_bytes % 128 != 0 && sh.row_bytes < kTokenBytes &&
+                    (int64_t)a.page_size * sh.row_bytes >= kBulkBytes;
+  for (sh.box = 32 < sh.TS ? 32 : sh.TS; a.page_size % sh.box;) sh.box /= 2;
+  const bool boxes = !a.k && sh.row_bytes % 128 == 0 && sh.taken % 128 == 0 && sh.box >= 16;
+  // (kTokens: two tokens a lane at most)
+  sh.copies = boxes                                                           ? kBoxes
+              : runs                                                          ? kRuns
+              : sh.unit == 16 && sh.taken >= kTokenBytesLeast && sh.TS <= 64 ? kTokens
+                                                                              : kLanes;
   sh.slice = (sh.taken + 15) / 16 * 16;
-  sh.swz_pool = q4::swizzled(sh.row_bytes);
-  sh.swz_smem = q4::swizzled(sh.slice);
-  // whole runs of a page by one copy where its rows lie as the stage has them
-  sh.bulk = !a.k && sh.NHG == 1 && (!sh.swz_pool || a.page_size % 8 == 0) &&
-            (int64_t)a.page_size * sh.row_bytes >= kBulkBytes;
+  if ((sh.copies == kTokens || sh.copies == kLanes) && sh.slice % 32 == 0) sh.slice += 16;
   const int units = sh.taken / sh.unit, chunks = sh.slice / 16;
   for (sh.lanes = 1; sh.lanes < units && sh.lanes < 32;) sh.lanes *= 2;
-  sh.order = sh.swz_smem || chunks % 2 ? kOrderOdd : chunks % 4 == 2 ? kOrderTwo : kOrderFour;
+  sh.order = chunks % 2 || sh.copies == kBoxes ? kOrderOdd : chunks % 4 == 2 ? kOrderTwo : kOrderFour;
   const int scratch = hg * (sh.WPH / 2) * cf.NT * (a.D / 4 + 4) * 32 * 4;
   const int nv = (4 * sh.Bv + 15) / 16 * 16, stage = 2 * sh.TS * sh.slice;
-  int n = (kSmemMax - scratch - nv) / stage;
+  int n = (kSmemMax - 1024 - scratch - nv) / stage;
   sh.stages = n > kMaxStages ? kMaxStages : n;
   // (at least kProducers fit for every shape: a stage is 40 KiB at most.  With fewer a
   // producer could pass the barrier of a stage that is a whole round behind)
   sh.ring = sh.stages * stage;
   sh.scratch_at = sh.ring;
   sh.nv_at = sh.ring + scratch;
-  cf.smem = (size_t)sh.nv_at + nv;
+  cf.smem = (size_t)sh.nv_at + nv + 1024;
   sh.grid = device_sm_count();
   return cf;
+}
+
+// Tensor map of a pool for kBoxes: 128-byte lines, a token row's lines, tokens; a box being
+// the lines of one head group of some tokens.
+cudaError_t pool_map(CUtensorMap* map, const void* pool, const Q4Shape& sh) {
+  static PFN_cuTensorMapEncodeTiled_v12000 encode = nullptr;
+  if (!encode) {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    const cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000,
+                                                           cudaEnableDefault, &found);
+    if (e != cudaSuccess) return e;
+    if (found != cudaDriverEntryPointSuccess || !fn) return cudaErrorNotSupported;
+    encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  }
+  const cuuint64_t dims[3] = {128, (cuuint64_t)sh.row_bytes / 128,
+                              (cuuint64_t)sh.num_pages * (cuuint64_t)sh.page_size};
+  const cuuint64_t strides[2] = {128, (cuuint64_t)sh.row_bytes};
+  const cuuint32_t box[3] = {128, (cuuint32_t)sh.slice / 128, (cuuint32_t)sh.box};
+  const cuuint32_t ones[3] = {1, 1, 1};
+  const CUresult r =
+      encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(pool), dims, strides, box,
+             ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <int D, int NT, int TT>
@@ -1220,12 +1400,17 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
   float* po = reinterpret_cast<float*>(ws + L.part_o);
   __nv_bfloat16* out = static_cast<__nv_bfloat16*>(a.out);
   const Q4Shape& sh = cf.sh;
+  CUtensorMap map_k{}, map_v{};
+  if (sh.copies == kBoxes) {
+    if ((e = pool_map(&map_k, a.pool_k, sh)) != cudaSuccess) return e;
+    if ((e = pool_map(&map_v, a.pool_v, sh)) != cudaSuccess) return e;
+  }
   e = launch_ex(kern, dim3(sh.grid), dim3((kConsumers + kProducers) * 32), cf.smem, s, /*pdl=*/true,
                 /*coop=*/false, a.seq_lens, a.block_table, a.topk_idx,
                 static_cast<const __nv_bfloat16*>(a.q), static_cast<const uint8_t*>(a.pool_k),
                 static_cast<const uint8_t*>(a.pool_v), out, a.lse, prefix, ml, po,
                 reinterpret_cast<int32_t*>(ws), sh, scale * 1.4426950408889634f,
-                a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles);
+                a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles, map_k, map_v);
   if (e != cudaSuccess) return e;
   const int64_t rows = (int64_t)sh.Bv * sh.Nq * sh.Hq;
   const bool few = rows <= kFewRows;

@@ -134,14 +134,11 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sm) 
 }
 
 // The place in the pool of row i of a call (page * page_size + slot), -1 for none.
-struct Place {
-  int row, slot;
-};
-__device__ __forceinline__ Place place_of(int i, const int32_t* starts, int B,
+__device__ __forceinline__ int place_of(int i, const int32_t* starts, int B,
                                           const int32_t* seq_lens, const int32_t* block_table,
                                           int page_size, int max_pages, int num_pages,
                                           int32_t* error) {
-  if (i < starts[0] || i >= starts[B]) return {-1, 0};
+  if (i < starts[0] || i >= starts[B]) return -1;
   int lo = 0, hi = B;  // starts[lo] <= i < starts[hi], whatever lies between
   while (hi - lo > 1) {
     const int mid = (lo + hi) >> 1;
@@ -150,7 +147,7 @@ __device__ __forceinline__ Place place_of(int i, const int32_t* starts, int B,
   }
   const int64_t len = seq_lens[lo];
   int bad = 0;
-  Place at{-1, 0};
+  int at = -1;
   if (len < 0 || len > (int64_t)max_pages * page_size) {
     bad = kErrLen;
   } else {
@@ -161,7 +158,7 @@ __device__ __forceinline__ Place place_of(int i, const int32_t* starts, int B,
       const int p = (int)pos / page_size, slot = (int)pos - p * page_size;
       const int page = block_table[(int64_t)lo * max_pages + p];
       if (page < 0 || page >= num_pages) bad = kErrPage;
-      else at = {page * page_size + slot, slot};
+      else at = page * page_size + slot;
     }
   }
   if (bad && error) *error = bad;
@@ -185,12 +182,11 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
   constexpr int NB = D / q4::kGroup, LANES = D / 8, AT_ONCE = kRowThreads / LANES;
   constexpr int REC = q4::record_bytes(D), UNROLL = 4;
   extern __shared__ int32_t s_starts[];
-  __shared__ Place s_place[kRowsMax];
+  __shared__ int s_place[kRowsMax];
   const int tid = threadIdx.x, lane = tid % LANES, b = lane >> 2, t = lane & 3;
   pdl_wait(seq_lens, block_table, starts, k, v, pool_k, pool_v);
   pdl_launch_dependents();
   for (int i = tid; i <= sh.B; i += kRowThreads) s_starts[i] = starts[i];
-  const bool swz = q4::swizzled(sh.row_bytes);
   const int records = sh.rows * 2 * sh.Hkv;
   for (int64_t r0 = (int64_t)blockIdx.x * sh.rows; r0 < sh.n_rows;
        r0 += (int64_t)gridDim.x * sh.rows) {
@@ -199,13 +195,13 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
       s_place[tid] = r0 + tid < sh.n_rows
                          ? place_of((int)r0 + tid, s_starts, sh.B, seq_lens, block_table,
                                     sh.page_size, sh.max_pages, sh.num_pages, error)
-                         : Place{-1, 0};
+                         : -1;
     __syncthreads();
     // (the shuffles need all lanes: lanes without a record go along)
     for (int it0 = tid / LANES; it0 < records + tid / LANES; it0 += AT_ONCE * UNROLL) {
       T* at[UNROLL];          // the lane's values
       uint8_t* rec[UNROLL];   // the token's row in the pool; nullptr: no place
-      uint32_t off[UNROLL], x16[UNROLL];
+      uint32_t off[UNROLL];
       bool is_v[UNROLL];
 #pragma unroll
       for (int u = 0; u < UNROLL; ++u) {
@@ -214,23 +210,22 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
         const int kv = it - r * 2 * sh.Hkv;
         is_v[u] = kv >= sh.Hkv;
         const int h = is_v[u] ? kv - sh.Hkv : kv;
-        const Place p = it < records ? s_place[r] : Place{-1, 0};
+        const int place = it < records ? s_place[r] : -1;
         const int64_t row = r0 + r;
         at[u] = is_v[u] ? v + row * sh.v_row + h * sh.v_head : k + row * sh.k_row + h * sh.k_head;
         at[u] += 8 * lane;
-        rec[u] = p.row < 0 ? nullptr
-                           : (is_v[u] ? pool_v : pool_k) + (int64_t)p.row * sh.row_bytes;
+        rec[u] = place < 0 ? nullptr
+                           : (is_v[u] ? pool_v : pool_k) + (int64_t)place * sh.row_bytes;
         off[u] = h * REC;
-        x16[u] = swz ? q4::swizzle(p.slot) : 0;
       }
       // the lane's word: K, word t NB + b; V, of chunk g = 2 t (even b) or 2 t + 1
       // (odd b) the halves of groups b & ~1 and b | 1
       auto code_at = [&](int u) {
         const int w = is_v[u] ? (2 * t + (b & 1)) * (NB / 2) + (b >> 1) : t * NB + b;
-        return reinterpret_cast<uint32_t*>(rec[u] + ((off[u] + 4 * w) ^ x16[u]));
+        return reinterpret_cast<uint32_t*>(rec[u] + off[u] + 4 * w);
       };
       auto pair_at = [&](int u) {
-        return reinterpret_cast<uint32_t*>(rec[u] + ((off[u] + D / 2 + 4 * b) ^ x16[u]));
+        return reinterpret_cast<uint32_t*>(rec[u] + off[u] + D / 2 + 4 * b);
       };
       if constexpr (WRITE) {
         Eight<T> in[UNROLL];

@@ -14,9 +14,6 @@ __host__ __device__ constexpr int record_bytes(int D) { return D / 2 + D / kGrou
 __host__ __device__ constexpr int token_bytes(int heads, int D) {
   return (heads * record_bytes(D) + 15) / 16 * 16;
 }
-// where the rows of a page are permuted: byte o of the row in slot i is at o ^ swizzle
-__host__ __device__ constexpr bool swizzled(int row_bytes) { return row_bytes % 128 == 0; }
-__host__ __device__ constexpr uint32_t swizzle(int slot) { return (uint32_t)(slot & 7) << 4; }
 
 }  // namespace q4
 }  // namespace pks
