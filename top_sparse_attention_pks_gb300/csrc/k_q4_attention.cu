@@ -28,8 +28,6 @@
 #include <cudaTypedefs.h>
 #include <cuda_fp16.h>
 
-#include <type_traits>
-
 #include "pks_internal.h"
 #include "q4.cuh"
 #include "tcgen05.cuh"
@@ -43,7 +41,7 @@ constexpr int kProducers = 4;  // warps, each filling every fourth stage
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
 constexpr int kSmemMax = 227 * 1024 - 6144;  // dynamic; the rest is the static part
-constexpr int kBulkBytes = 2048;   // of a page, from which on its runs are copied whole,
+constexpr int kBulkBytes = 512;    // of a page, from which on its runs are copied whole,
 constexpr int kTokenBytes = 512;   // rows smaller than this, that is
 constexpr int kTokenBytesLeast = 320;
 constexpr int kFewRows = 4096;    // up to which a block joins a row, else a warp
@@ -128,6 +126,10 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 h) {
 }
 __device__ __forceinline__ __half2 bits_half2(uint32_t u) {
   return *reinterpret_cast<const __half2*>(&u);
+}
+// all ones where a half is NaN
+__device__ __forceinline__ uint32_t no_number(uint32_t u) {
+  return ~__heq2_mask(bits_half2(u), bits_half2(u));
 }
 __device__ __forceinline__ float low_half(uint32_t u) {
   return __half2float(__low2half(bits_half2(u)));
@@ -307,9 +309,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   // Waits of a warp.  Looks at the clock and at the other warps once in many polls (each of
   // which the hardware holds back): polling takes issue slots from the warps that work.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+    const long long t0 = clock64();  // (before the first look: a tiny limit is over behind it)
     bool there = tc::mbar_test_wait(bar, parity);
     if (!there) {
-      const long long t0 = clock64();
       while (!there && !*(volatile int*)&s_abort && clock64() - t0 <= wait_cycles) {
 #pragma unroll 1
         for (int i = 0; i < 32 && !there; ++i) there = tc::mbar_try_wait(bar, parity);
@@ -713,7 +715,99 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   };
 
   bool ready = false;  // the stage at hand has landed
+  int q_v = s_first, q_c = 0;  // the segment whose queries are to be read next
+  if (chunks > 1) q_c = s_rest / stages_of(s_nv[q_v]);
+  bool fresh = true;
   for (int done = 0; done < count; ++done) {
+    if (__builtin_expect(fresh, 0)) {
+      // ---------------- the segment's queries (while its tokens are on their way) ------
+      fresh = false;
+      sx = 0;
+      const int hg = q_c / sh.NRC, rc = q_c - hg * sh.NRC;
+      const int head = hg * sh.HG + h;
+      const __nv_bfloat16* from = q;
+      behind(from);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int r = rc * RC + nt * 8 + g;
+        float x[NB][8];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
+        if (r < sh.R) {
+          const int qi = r / sh.G;
+          const int64_t row =
+              ((int64_t)q_v * sh.Nq + qi) * sh.Hq + head * sh.G + r - qi * sh.G;
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const uint4 y = *reinterpret_cast<const uint4*>(from + row * D + 32 * b + 8 * t);
+            const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              x[b][2 * e] = __uint_as_float(u[e] << 16);
+              x[b][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
+            }
+          }
+        }
+        float big = 0.f;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[b][e]));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        // the row times 2^p, here its largest value in [2^120, 2^121)
+        const int e2 = max((int)(__float_as_uint(big) >> 23) - 127, -100);
+        const int p = 120 - e2;
+        const float f1 = __int_as_float((127 + (p >> 1)) << 23);
+        const float f2 = __int_as_float((127 + p - (p >> 1)) << 23);
+        uint32_t piece[NB];  // of the sums: a lane's, by t
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float s = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            x[b][e] = x[b][e] * f1 * f2;
+            s += x[b][e];
+          }
+          s += __shfl_xor_sync(0xffffffffu, s, 1);
+          s += __shfl_xor_sync(0xffffffffu, s, 2);
+          // values i and i + 4 of a word stand in one register; the odd ones come out of it
+          // 16 times too large.  Up to [2^127, 2^128)
+          auto two = [&](int i, float f) {
+            const __nv_bfloat162 y = __floats2bfloat162_rn(x[b][i] * f, x[b][i + 4] * f);
+            return *reinterpret_cast<const uint32_t*>(&y);
+          };
+          qf[nt][b][0] = two(0, 128.f);
+          qf[nt][b][1] = two(1, 8.f);
+          qf[nt][b][2] = two(2, 128.f);
+          qf[nt][b][3] = two(3, 8.f);
+          // the sum in the unit of the codes' products, 2^(p + 7 - 133): at most 1, in
+          // pieces of 11 bits
+          const float y = s * __int_as_float(1 << 23);  // 2^-126
+          const __half h0 = __float2half_rn(y);
+          const float r1 = y - __half2float(h0);
+          const __half h1 = __float2half_rn(r1);
+          const __half h2 = __float2half_rn(r1 - __half2float(h1));
+          piece[b] = t == 3 ? 0 : __half_as_ushort(t == 0 ? h0 : t == 1 ? h1 : h2);
+        }
+        qs[nt][0] = piece[0] | piece[1] << 16;
+        qs[nt][1] = NB == 4 ? piece[NB - 2] | piece[NB - 1] << 16 : 0;
+        // scores in powers of two
+        const float mine_c = __int_as_float((127 + min(6 + e2, 128)) << 23) * scale_log2;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          cs[nt][j] = __shfl_sync(0xffffffffu, mine_c, (2 * t + j) * 4);
+          nref[nt][j] = -kNone;
+          sum[nt][j] = om[nt][j] = 0.f;
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) o[nt][b][e >> 2][e & 3] = 0.f;
+      }
+    }
     if (!ready) ok = wait(&bar_full[stage], phase);
     if (!ok) break;
     // ---------------- all of the stage that this warp needs, and on with the ring ----------
@@ -760,129 +854,18 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       stage = 0;
       phase ^= 1;
     }
-    if (__builtin_expect(flags & kFirst, 0)) {
-      // ---------------- the segment's queries ----------------
-      const int hg = seg.y / sh.NRC, rc = seg.y - hg * sh.NRC;
-      const int head = hg * sh.HG + h;
-      const __nv_bfloat16* from = q;
-      behind(from);
-      sx = 0;
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int r = rc * RC + nt * 8 + g;
-        float x[NB][8];
-        if (r < sh.R) {
-          const int i = r / sh.G;
-          const int64_t row = ((int64_t)seg.x * sh.Nq + i) * sh.Hq + head * sh.G + r - i * sh.G;
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const uint4 w = *reinterpret_cast<const uint4*>(from + row * D + 32 * b + 8 * t);
-            const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              x[b][2 * e] = __uint_as_float(u[e] << 16);
-              x[b][2 * e + 1] = __uint_as_float(u[e] & 0xffff0000u);
-            }
-          }
-        } else {
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[b][e] = 0.f;
-        }
-        float big = 0.f;
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[b][e]));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
-        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // the row times 2^p: its largest value in [2^120, 2^121)
-        const int e2 = max((int)(__float_as_uint(big) >> 23) - 127, -100);
-        const int p = 120 - e2;
-        const float f1 = __int_as_float((127 + (p >> 1)) << 23);
-        const float f2 = __int_as_float((127 + p - (p >> 1)) << 23);
-        float sums[NB];
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          sums[b] = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[b][e] = x[b][e] * f1 * f2;
-            sums[b] += x[b][e];
-          }
-          sums[b] += __shfl_xor_sync(0xffffffffu, sums[b], 1);
-          sums[b] += __shfl_xor_sync(0xffffffffu, sums[b], 2);
-          // values e and e + 4 of a word stand in one register; the odd ones come
-          // out of it 16 times too large
-          auto two = [&](int e, float f) {
-            const __nv_bfloat162 y = __floats2bfloat162_rn(x[b][e] * f, x[b][e + 4] * f);
-            return *reinterpret_cast<const uint32_t*>(&y);
-          };
-          qf[nt][b][0] = two(0, 1.f);
-          qf[nt][b][1] = two(1, 0.0625f);
-          qf[nt][b][2] = two(2, 1.f);
-          qf[nt][b][3] = two(3, 0.0625f);
-        }
-        // the sums times 2^-112, below 2^14, in pieces: lanes with the same t & 1 (D =
-        // 128) hold two groups' pieces 0 to 3, for D = 64 all lanes
-        auto piece = [&](float y, int i) {
-          const __half h0 = __float2half_rn(y);
-          const float r1 = y - __half2float(h0);
-          const __half h1 = __float2half_rn(r1);
-          const __half h2 = __float2half_rn(r1 - __half2float(h1));
-          return i == 0 ? h0 : i == 1 ? h1 : i == 2 ? h2 : __ushort_as_half(0);
-        };
-        const float down = __int_as_float((127 - 112) << 23);
-        float y0 = sums[0] * down, y1 = sums[1] * down;
-        if constexpr (NB == 4) {
-          if (t & 1) {
-            y0 = sums[2] * down;
-            y1 = sums[3] * down;
-          }
-          qs[nt][0] = half2_bits(__halves2half2(piece(y0, t >> 1), piece(y1, t >> 1)));
-          qs[nt][1] = half2_bits(__halves2half2(piece(y0, 2 + (t >> 1)), piece(y1, 2 + (t >> 1))));
-        } else {
-          qs[nt][0] = half2_bits(__halves2half2(piece(y0, t), piece(y1, t)));
-          qs[nt][1] = 0;
-        }
-        // scores in powers of two: the accumulators' unit is 2^(133 - p)
-        const float mine_c = __int_as_float((127 + min(13 + e2, 128)) << 23) * scale_log2;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          cs[nt][j] = __shfl_sync(0xffffffffu, mine_c, (2 * t + j) * 4);
-          nref[nt][j] = -kNone;
-          sum[nt][j] = om[nt][j] = 0.f;
-        }
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nt][b][m][e] = 0.f;
-      }
-    }
-
     // ---------------- scores ----------------
     float tot[TT][NT][4];
 #pragma unroll
     for (int u = 0; u < TT; ++u) {
-      uint32_t a0, a1;
-      if constexpr (NB == 4) {
-        a0 = __byte_perm(t & 1 ? kp0[u][2] : kp0[u][0], t & 1 ? kp0[u][3] : kp0[u][1], 0x7632);
-        a1 = __byte_perm(t & 1 ? kp1[u][2] : kp1[u][0], t & 1 ? kp1[u][3] : kp1[u][1], 0x7632);
-      } else {
-        a0 = __byte_perm(kp0[u][0], kp0[u][1], 0x7632);
-        a1 = __byte_perm(kp1[u][0], kp1[u][1], 0x7632);
-      }
+      // the minima: slots 2t, 2t + 1 groups 0 and 1, slots 2t + 8, 2t + 9 groups 2 and 3, the
+      // lanes' t telling the pieces apart
+      const uint32_t a0 = __byte_perm(kp0[u][0], kp0[u][1], 0x7632);
+      const uint32_t a1 = __byte_perm(kp1[u][0], kp1[u][1], 0x7632);
+      const uint32_t a2 = NB == 4 ? __byte_perm(kp0[u][NB - 2], kp0[u][NB - 1], 0x7632) : 0;
+      const uint32_t a3 = NB == 4 ? __byte_perm(kp1[u][NB - 2], kp1[u][NB - 1], 0x7632) : 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float acc[4];
-        mma_f16(acc, a0, a1, a0, a1, qs[nt][0], qs[nt][1]);
-        // units: 2^(p - 112) here, 2^(p - 133) below
-#pragma unroll
-        for (int e = 0; e < 4; ++e) tot[u][nt][e] = acc[e] * 4.76837158203125e-07f;
-      }
+      for (int nt = 0; nt < NT; ++nt) mma_f16(tot[u][nt], a0, a1, a2, a3, qs[nt][0], qs[nt][1]);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const uint32_t x0 = k0[u][b], x1 = k1[u][b], y0 = x0 >> 8, y1 = x1 >> 8;
@@ -962,6 +945,44 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             if (!on1 || tok1 >= lim) tot[u][nt][2 + j] = kNegInf;
           }
       }
+      // at an edge, an s without a number must not reach the queries that do not see it: it goes
+      // straight to the sums of those that do
+      if (flags & kEdge && __any_sync(0xffffffffu, any & 0x40004000u)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t hit = 0;  // by groups, for column g
+#pragma unroll
+          for (int u = 0; u < TT; ++u) {
+            auto seen = [&](int e) {
+              return movmatrix_t((tot[u][nt][e] == kNegInf ? 0u : 0xffffu) |
+                                 (tot[u][nt][e + 1] == kNegInf ? 0u : 0xffff0000u));
+            };
+            const uint32_t seen0 = seen(0), seen1 = seen(2);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              if ((seen0 & no_number(s01[u][b])) | (seen1 & no_number(s23[u][b]))) hit |= 1u << b;
+          }
+          hit |= __shfl_xor_sync(0xffffffffu, hit, 1);
+          hit |= __shfl_xor_sync(0xffffffffu, hit, 2);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const uint32_t mine = __shfl_sync(0xffffffffu, hit, (2 * t + j) * 4);
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+              if (mine >> b & 1)
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+                  o[nt][b][m][j] = o[nt][b][m][2 + j] = __int_as_float(0x7fc00000);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            s01[u][b] &= ~no_number(s01[u][b]);
+            s23[u][b] &= ~no_number(s23[u][b]);
+          }
+      }
       // larger scales: p s stays below 2^16 while all are below 2^(1 + sx)
       __half2 s_max = bits_half2(0);
 #pragma unroll
@@ -1025,64 +1046,52 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         add2(sum[nt][0], sum[nt][1], p[u][nt][2], p[u][nt][3]);
       }
     }
-    auto values = [&](auto edge) {
-      // (at an edge, an s without a number must not reach the queries that do not see it)
-      uint32_t seen0[TT][NT], seen1[TT][NT];
-      if constexpr (decltype(edge)::value) {
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
+    for (int b = 0; b < NB; ++b) {
+      float acc[NT][2][4];
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            auto seen = [&](int e) {
-              return (tot[u][nt][e] == kNegInf ? 0u : 0xffffu) |
-                     (tot[u][nt][e + 1] == kNegInf ? 0u : 0xffff0000u);
-            };
-            seen0[u][nt] = movmatrix_t(seen(0));
-            seen1[u][nt] = movmatrix_t(seen(2));
-          }
-      }
+      for (int u = 0; u < TT; ++u) {
+        const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
+        const uint32_t x01 = __byte_perm(w[u][0][b / 2], w[u][1][b / 2], sel);
+        const uint32_t x23 = __byte_perm(w[u][2][b / 2], w[u][3][b / 2], sel);
+        const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        float acc[NT][2][4];
-#pragma unroll
-        for (int u = 0; u < TT; ++u) {
-          const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
-          const uint32_t x01 = __byte_perm(w[u][0][b / 2], w[u][1][b / 2], sel);
-          const uint32_t x23 = __byte_perm(w[u][2][b / 2], w[u][3][b / 2], sel);
-          const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            uint32_t b0 = half2_bits(__hmul2(bits_half2(pt0[u][nt]), bits_half2(s01[u][b])));
-            uint32_t b1 = half2_bits(__hmul2(bits_half2(pt1[u][nt]), bits_half2(s23[u][b])));
-            if constexpr (decltype(edge)::value) {
-              b0 &= seen0[u][nt];
-              b1 &= seen1[u][nt];
-            }
-            if (u == 0) {
-              mma_f16(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
-                      x23 & 0x00f000f0u, b0, b1);
-              mma_f16(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
-                      y23 & 0x00f000f0u, b0, b1);
-            } else {
-              mma_f16_add(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
-                          x23 & 0x00f000f0u, b0, b1);
-              mma_f16_add(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
-                          y23 & 0x00f000f0u, b0, b1);
-            }
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint32_t b0 = half2_bits(__hmul2(bits_half2(pt0[u][nt]), bits_half2(s01[u][b])));
+          const uint32_t b1 = half2_bits(__hmul2(bits_half2(pt1[u][nt]), bits_half2(s23[u][b])));
+          if (u == 0) {
+            mma_f16(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
+                    x23 & 0x00f000f0u, b0, b1);
+            mma_f16(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
+                    y23 & 0x00f000f0u, b0, b1);
+          } else {
+            mma_f16_add(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
+                        x23 & 0x00f000f0u, b0, b1);
+            mma_f16_add(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
+                        y23 & 0x00f000f0u, b0, b1);
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int m = 0; m < 2; ++m) {
-            add2(o[nt][b][m][0], o[nt][b][m][1], acc[nt][m][0], acc[nt][m][1]);
-            add2(o[nt][b][m][2], o[nt][b][m][3], acc[nt][m][2], acc[nt][m][3]);
-          }
       }
-    };
-    if (__builtin_expect(flags & kEdge, 0)) values(std::true_type{});
-    else values(std::false_type{});
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+          add2(o[nt][b][m][0], o[nt][b][m][1], acc[nt][m][0], acc[nt][m][1]);
+          add2(o[nt][b][m][2], o[nt][b][m][3], acc[nt][m][2], acc[nt][m][3]);
+        }
+    }
     if (__builtin_expect(!(flags & kLast), 1)) continue;
+
+    fresh = done + 1 < count;
+    if (fresh) {
+      q_v = seg.x;
+      q_c = seg.y + 1;
+      if (q_c == chunks) {
+        q_c = 0;
+        do ++q_v;
+        while (s_nv[q_v] == 0);
+      }
+    }
 
     // ---------------- end of the segment, or of the CTA's part of it ----------------
     const int hg = seg.y / sh.NRC, rc = seg.y - hg * sh.NRC, head = hg * sh.HG + h;
