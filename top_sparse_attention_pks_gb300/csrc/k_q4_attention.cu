@@ -37,7 +37,10 @@ namespace {
 
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
 constexpr int kConsumers = 8;  // warps, two a scheduler
-constexpr int kProducers = 4;  // warps, each filling every fourth stage
+// Producer warps (PW): four, each filling every fourth stage; with kTokens teams of two, one
+// for K and one for V, of four warps or eight.  Eight keep up with long lists (256 x 1024
+// selected tokens 104 -> 90 us), four start sooner (16 x 2048 tokens 32 us, 34 with eight).
+constexpr int kLongRun = 12;   // stages a CTA from which on there are eight
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
 constexpr int kSmemMax = 227 * 1024 - 6144;  // dynamic; the rest is the static part
@@ -212,8 +215,8 @@ struct Shares {
   }
 };
 
-template <int D, int NT, int TT>
-__global__ void __launch_bounds__((kConsumers + kProducers) * 32, 1)
+template <int D, int NT, int TT, int PW>
+__global__ void __launch_bounds__((kConsumers + PW) * 32, 1)
 k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
                const int32_t* __restrict__ lists, const __nv_bfloat16* __restrict__ q,
                const uint8_t* __restrict__ pool_k, const uint8_t* __restrict__ pool_v,
@@ -222,7 +225,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                float* __restrict__ part_o, int32_t* __restrict__ err, const Q4Shape sh,
                float scale_log2, long long wait_cycles, const __grid_constant__ CUtensorMap map_k,
                const __grid_constant__ CUtensorMap map_v) {
-  constexpr int NW = kConsumers, NWARPS = NW + kProducers, NTHREADS = NWARPS * 32, NB = D / q4::kGroup, REC = q4::record_bytes(D);
+  constexpr int NW = kConsumers, NWARPS = NW + PW, NTHREADS = NWARPS * 32;
+  constexpr int NB = D / q4::kGroup, REC = q4::record_bytes(D);
   constexpr int RC = 8 * NT;  // query rows a chunk
   const float kNegInf = __int_as_float(0xff800000);
   extern __shared__ uint8_t smem_raw[];
@@ -230,7 +234,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   // bar_join: the consumer warps
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
-  __shared__ int s_row_all[kProducers][kMaxTokens];  // tokens' rows in the pool (-1: none)
+  __shared__ int s_row_all[4][kMaxTokens];  // tokens' rows in the pool (-1: none)
   __shared__ int s_warp[NWARPS], s_first, s_rest, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -328,10 +332,10 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 
   if (warp >= NW) {
     // =========================== producers ===========================
-    set_registers<88, false>();
+    set_registers<PW == 8 ? 48 : 88, false>();
     behind(seq_lens, block_table, lists);
     const int me = warp - NW;
-    int* s_row = s_row_all[me];
+    int* s_row = s_row_all[me & 3];
     int v = s_first, n = s_nv[v], T = stages_of(n), c = 0, tile = s_rest;
     if (chunks > 1) {
       c = tile / T;
@@ -384,8 +388,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           sts_zero8(dst_v + place(sh, at * sh.slice + h * REC + D / 2 + o));
     };
     // (the stages that one warp fills are never further apart than the ring is long)
-    const int stride = sh.copies == kTokens ? 2 : kProducers;
+    const int stride = sh.copies == kTokens ? PW / 2 : 4;
     const int mine_from = sh.copies == kTokens ? me >> 1 : me;
+    if (mine_from >= stride) return;
     int stage = mine_from, round = 0;
     bool ok = true;
     if (mine_from < count) forward(mine_from);
@@ -1299,7 +1304,7 @@ int heads_of(int hkv) {
 
 struct Config {
   Q4Shape sh;
-  int NT;
+  int NT, PW;
   size_t smem;
 };
 
@@ -1353,13 +1358,15 @@ Config configure(const pks_q4_attention_args& a) {
   const int nv = (4 * sh.Bv + 15) / 16 * 16, stage = 2 * sh.TS * sh.slice;
   int n = (kSmemMax - 1024 - scratch - nv) / stage;
   sh.stages = n > kMaxStages ? kMaxStages : n;
-  // (at least kProducers fit for every shape: a stage is 40 KiB at most.  With fewer a
+  // (at least four fit for every shape: a stage is 40 KiB at most.  With fewer a
   // producer could pass the barrier of a stage that is a whole round behind)
   sh.ring = sh.stages * stage;
   sh.scratch_at = sh.ring;
   sh.nv_at = sh.ring + scratch;
   cf.smem = (size_t)sh.nv_at + nv + 1024;
   sh.grid = device_sm_count();
+  const int64_t most = (int64_t)sh.Bv * sh.NHG * sh.NRC * ((sh.k ? sh.k : sh.cap) / sh.TS + 1);
+  cf.PW = sh.copies == kTokens && most > (int64_t)kLongRun * sh.grid ? 8 : 4;
   return cf;
 }
 
@@ -1388,11 +1395,11 @@ cudaError_t pool_map(CUtensorMap* map, const void* pool, const Q4Shape& sh) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int NT, int TT>
+template <int D, int NT, int TT, int PW>
 cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const Config& cf,
                         cudaStream_t s) {
   static bool done[64] = {false};
-  auto kern = k_q4_attention<D, NT, TT>;
+  auto kern = k_q4_attention<D, NT, TT, PW>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1414,7 +1421,7 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
     if ((e = pool_map(&map_k, a.pool_k, sh)) != cudaSuccess) return e;
     if ((e = pool_map(&map_v, a.pool_v, sh)) != cudaSuccess) return e;
   }
-  e = launch_ex(kern, dim3(sh.grid), dim3((kConsumers + kProducers) * 32), cf.smem, s, /*pdl=*/true,
+  e = launch_ex(kern, dim3(sh.grid), dim3((kConsumers + PW) * 32), cf.smem, s, /*pdl=*/true,
                 /*coop=*/false, a.seq_lens, a.block_table, a.topk_idx,
                 static_cast<const __nv_bfloat16*>(a.q), static_cast<const uint8_t*>(a.pool_k),
                 static_cast<const uint8_t*>(a.pool_v), out, a.lse, prefix, ml, po,
@@ -1427,6 +1434,14 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
                    dim3((unsigned)(few ? rows : (rows + 7) / 8)), dim3(256), 0, s, /*pdl=*/true,
                    /*coop=*/false, (const int32_t*)prefix, (const float2*)ml, (const float*)po,
                    out, a.lse, sh, 8 * NT);
+}
+
+template <int D>
+cudaError_t launch_rows(const pks_q4_attention_args& a, const Q4Layout& L, const Config& cf,
+                        cudaStream_t s) {
+  if (cf.PW == 8)
+    return cf.NT == 2 ? launch_main<D, 2, 1, 8>(a, L, cf, s) : launch_main<D, 1, 2, 8>(a, L, cf, s);
+  return cf.NT == 2 ? launch_main<D, 2, 1, 4>(a, L, cf, s) : launch_main<D, 1, 2, 4>(a, L, cf, s);
 }
 
 }  // namespace
@@ -1453,9 +1468,7 @@ Q4Layout q4_layout(const pks_q4_attention_args& a) {
 cudaError_t launch_q4_attention(const pks_q4_attention_args& a, const Q4Layout& L,
                                 cudaStream_t s) {
   const Config cf = configure(a);
-  if (a.D == 64)
-    return cf.NT == 2 ? launch_main<64, 2, 1>(a, L, cf, s) : launch_main<64, 1, 2>(a, L, cf, s);
-  return cf.NT == 2 ? launch_main<128, 2, 1>(a, L, cf, s) : launch_main<128, 1, 2>(a, L, cf, s);
+  return a.D == 64 ? launch_rows<64>(a, L, cf, s) : launch_rows<128>(a, L, cf, s);
 }
 
 }  // namespace pks
