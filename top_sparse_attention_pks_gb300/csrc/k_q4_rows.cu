@@ -1,14 +1,18 @@
 // Writing a 4-bit cache and reading it back.
 //
-// A row's head record is D/8 lanes' work, eight values a lane: lane 4 b + t has
-// values 32 b + 8 t .. + 7, so that the four lanes of a group find its minimum and
-// maximum with two shuffles and each lane's codes are one 32-bit word.  A block
-// takes some rows, finds their places in the pool once, and then all their K and V
-// records.
+// A block takes some rows, finds their places in the pool once, and then all their K and V
+// records, a warp (or several, when rows are few) a row.
+//  - Writing, a lane has a whole group of 32 values: what is worked out once a group
+//    (minimum, scale, reciprocal) is most of the work when four lanes share one.
+//  - Reading, a lane has eight values, 16 bytes of a row of two-byte values, so that stores
+//    are whole sectors.
 //
 // Bound by memory: a bf16 row of D = 128 is 256 bytes in and 80 out.
 
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
+
+#include <type_traits>
 
 #include "pks_internal.h"
 #include "q4.cuh"
@@ -16,8 +20,9 @@
 namespace pks {
 namespace {
 
-constexpr int kRowThreads = 256;
-constexpr int kRowsMax = 8;  // rows of a block at a time
+constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+// what eight magic numbers (1.5 2^23 as bits, shifted by 4 i) add up to beside the codes
+constexpr uint32_t kMagicSum = 0x4b400000u * 0x11111111u;
 
 __device__ __forceinline__ float min_nan(float a, float b) {
   float r;
@@ -83,27 +88,55 @@ __device__ __forceinline__ void pack(const float (&x)[8], Eight<float>& e) {
                       __float_as_uint(x[7]));
 }
 
-// Codes of eight values and (s in the low half, m in the high half) of their group,
-// whose other values are on the three lanes beside.  The numbers are those of the
-// definition in exact arithmetic, for any fp32 values:
+// Smallest and largest of a lane's 32 values (NaN when one is).  Two-byte types two at once.
+template <typename T>
+__device__ __forceinline__ void extent(const Eight<T> (&in)[4], float& lo, float& hi) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float x[8];
+      unpack(in[i], x);
+      if (i == 0) lo = hi = x[0];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        lo = min_nan(lo, x[e]);
+        hi = max_nan(hi, x[e]);
+      }
+    }
+  } else {
+    using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2,
+                                         __nv_bfloat162>::type;
+    T2 a{}, b{};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w[4] = {in[i].w[0].x, in[i].w[0].y, in[i].w[0].z, in[i].w[0].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const T2 x = *reinterpret_cast<const T2*>(&w[e]);
+        a = i + e == 0 ? x : __hmin2_nan(a, x);
+        b = i + e == 0 ? x : __hmax2_nan(b, x);
+      }
+    }
+    lo = min_nan((float)a.x, (float)a.y);
+    hi = max_nan((float)b.x, (float)b.y);
+  }
+}
+
+// (s in the low half, m in the high half) of a group, and what its codes are found with.
+// The numbers are those of the definition in exact arithmetic, for any fp32 values:
 //  - s: rounded up from the quotient, one step more where 15 s still falls short of
 //    max - m (whose own rounding error, err, is counted).
 //  - n: guessed from the reciprocal, at most one too low (the guess leans down by
 //    2^-9, more than its error of 2^-11), then compared with the border above it.
 //    Both sides of the comparison are exact: near m (15 s below 2^-7 |m|) as
 //    x - m >= (n + 1/2) s, else as x >= m + (n + 1/2) s, at most 24 bits long.
-__device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sm) {
-  float lo = x[0], hi = x[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) {
-    lo = min_nan(lo, x[i]);
-    hi = max_nan(hi, x[i]);
-  }
-#pragma unroll
-  for (int d = 1; d < 4; d <<= 1) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, d));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, d));
-  }
+struct Scale {
+  uint32_t pair;
+  float s, inv, from, guess, first;  // first: the border between 0 and 1
+  bool flat;                         // all codes are 0
+};
+__device__ __forceinline__ Scale scale_of(float lo, float hi) {
+  Scale g;
   const __half mh = __float2half_rd(lo);
   const float m = __half2float(mh);
   const float t = hi - m;
@@ -112,25 +145,31 @@ __device__ __forceinline__ uint32_t quantise(const float (&x)[8], uint32_t& sm) 
   __half sh = __float2half_ru(__fdiv_rn(t, 15.f));
   if (__fmaf_rn(-15.f, __half2float(sh), t) + err > 0.f)
     sh = __ushort_as_half(__half_as_ushort(sh) + 1);  // (s >= 0)
-  const float s = __half2float(sh);
-  const bool bad = !(fabsf(m) <= 65504.f && s <= 65504.f);
-  sm = bad ? 0x7e00u : (uint32_t)__half_as_ushort(mh) << 16 | __half_as_ushort(sh);
-  if (bad || s == 0.f) return 0;
-  const float inv = __frcp_rn(s);
-  const bool near = fabsf(m) > 2048.f * s;
-  const float from = near ? m : 0.f, base = near ? 0.f : m;
-  const float c = __fmaf_rn(-base, inv, -0.001953125f);
-  const float first = __fmaf_rn(0.5f, s, base);  // the border between 0 and 1
+  g.s = __half2float(sh);
+  const bool bad = !(fabsf(m) <= 65504.f && g.s <= 65504.f);
+  g.pair = bad ? 0x7e00u : (uint32_t)__half_as_ushort(mh) << 16 | __half_as_ushort(sh);
+  g.flat = bad || g.s == 0.f;
+  g.inv = g.flat ? 0.f : __frcp_rn(g.s);
+  const bool near = fabsf(m) > 2048.f * g.s;
+  g.from = near ? m : 0.f;
+  const float base = near ? 0.f : m;
+  g.guess = __fmaf_rn(-base, g.inv, -0.001953125f);
+  g.first = __fmaf_rn(0.5f, g.s, base);
+  return g;
+}
+// codes of eight values, the first in the lowest bits
+__device__ __forceinline__ uint32_t codes(const float (&x)[8], const Scale& g) {
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float xa = x[i] - from;
-    const float r = __fmaf_rn(xa, inv, c) + 12582912.f;  // to the nearest whole number
-    const float border = __fmaf_rn(r - 12582912.f, s, first);
-    const uint32_t n = (__float_as_uint(r) & 15u) + (xa >= border ? 1u : 0u);
-    w |= n << (4 * i);
+  for (int i = 7; i >= 0; --i) {
+    const float xa = x[i] - g.from;
+    const float r = __fmaf_rn(xa, g.inv, g.guess) + 12582912.f;  // to the nearest whole number
+    const float border = __fmaf_rn(r - 12582912.f, g.s, g.first);
+    uint32_t above;  // all ones from the border on
+    asm("set.ge.u32.f32 %0, %1, %2;" : "=r"(above) : "f"(xa), "f"(border));
+    w = w * 16 + (__float_as_uint(r) - above);
   }
-  return w;
+  return g.flat ? 0 : w - kMagicSum;
 }
 
 // The place in the pool of row i of a call (page * page_size + slot), -1 for none.
@@ -167,9 +206,8 @@ __device__ __forceinline__ int place_of(int i, const int32_t* starts, int B,
 
 struct RowShape {
   int B, n_rows, Hkv, page_size, max_pages, num_pages;
-  int rows;           // of a block at a time
+  int warps;          // a row: 1 to 8, a power of two
   int row_bytes;      // of a token in the pool
-  uint32_t magic;     // ceil(2^32 / (2 Hkv)): divides record numbers
   int64_t k_row, k_head, v_row, v_head;
 };
 
@@ -179,86 +217,100 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
           const int32_t* __restrict__ starts, T* __restrict__ k, T* __restrict__ v,
           uint8_t* __restrict__ pool_k, uint8_t* __restrict__ pool_v, int32_t* error,
           RowShape sh) {
-  constexpr int NB = D / q4::kGroup, LANES = D / 8, AT_ONCE = kRowThreads / LANES;
-  constexpr int REC = q4::record_bytes(D), UNROLL = 4;
+  constexpr int NB = D / q4::kGroup, REC = q4::record_bytes(D);
+  constexpr int LANES = WRITE ? NB : D / 8, AT_ONCE = 32 / LANES;  // records of a warp
+  constexpr int U = WRITE ? 1 : 4;                                // of a lane at once
   extern __shared__ int32_t s_starts[];
-  __shared__ int s_place[kRowsMax];
-  const int tid = threadIdx.x, lane = tid % LANES, b = lane >> 2, t = lane & 3;
+  __shared__ int s_place[kRowWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int part = warp & (sh.warps - 1), mine = warp / sh.warps, rows = kRowWarps / sh.warps;
   pdl_wait(seq_lens, block_table, starts, k, v, pool_k, pool_v);
   pdl_launch_dependents();
   for (int i = tid; i <= sh.B; i += kRowThreads) s_starts[i] = starts[i];
-  const int records = sh.rows * 2 * sh.Hkv;
-  for (int64_t r0 = (int64_t)blockIdx.x * sh.rows; r0 < sh.n_rows;
-       r0 += (int64_t)gridDim.x * sh.rows) {
+  for (int64_t r0 = (int64_t)blockIdx.x * rows; r0 < sh.n_rows; r0 += (int64_t)gridDim.x * rows) {
     __syncthreads();
-    if (tid < sh.rows)
+    if (tid < rows)
       s_place[tid] = r0 + tid < sh.n_rows
                          ? place_of((int)r0 + tid, s_starts, sh.B, seq_lens, block_table,
                                     sh.page_size, sh.max_pages, sh.num_pages, error)
                          : -1;
     __syncthreads();
-    // (the shuffles need all lanes: lanes without a record go along)
-    for (int it0 = tid / LANES; it0 < records + tid / LANES; it0 += AT_ONCE * UNROLL) {
-      T* at[UNROLL];          // the lane's values
-      uint8_t* rec[UNROLL];   // the token's row in the pool; nullptr: no place
-      uint32_t off[UNROLL];
-      bool is_v[UNROLL];
+    const int place = s_place[mine];
+    if (place < 0) continue;  // (a whole warp)
+    const int64_t row = r0 + mine, at = (int64_t)place * sh.row_bytes;
+    T* k_row = k + row * sh.k_row;
+    T* v_row = v + row * sh.v_row;
+    // K's records, then V's; the shuffles need all lanes: those without a record go along
+    for (int j0 = part * AT_ONCE * U; j0 < 2 * sh.Hkv; j0 += sh.warps * AT_ONCE * U) {
+      T* values[U];
+      uint8_t* rec[U];
+      bool is_v[U], on[U];
 #pragma unroll
-      for (int u = 0; u < UNROLL; ++u) {
-        const int it = it0 + u * AT_ONCE;
-        const int r = (int)__umulhi((uint32_t)it, sh.magic);
-        const int kv = it - r * 2 * sh.Hkv;
-        is_v[u] = kv >= sh.Hkv;
-        const int h = is_v[u] ? kv - sh.Hkv : kv;
-        const int place = it < records ? s_place[r] : -1;
-        const int64_t row = r0 + r;
-        at[u] = is_v[u] ? v + row * sh.v_row + h * sh.v_head : k + row * sh.k_row + h * sh.k_head;
-        at[u] += 8 * lane;
-        rec[u] = place < 0 ? nullptr
-                           : (is_v[u] ? pool_v : pool_k) + (int64_t)place * sh.row_bytes;
-        off[u] = h * REC;
+      for (int u = 0; u < U; ++u) {
+        const int j = j0 + u * AT_ONCE + lane / LANES;
+        on[u] = j < 2 * sh.Hkv;
+        is_v[u] = j >= sh.Hkv;
+        const int h = is_v[u] ? j - sh.Hkv : j;
+        values[u] = is_v[u] ? v_row + h * sh.v_head : k_row + h * sh.k_head;
+        rec[u] = (is_v[u] ? pool_v : pool_k) + at + h * REC;
       }
-      // the lane's word: K, word t NB + b; V, of chunk g = 2 t (even b) or 2 t + 1
-      // (odd b) the halves of groups b & ~1 and b | 1
-      auto code_at = [&](int u) {
-        const int w = is_v[u] ? (2 * t + (b & 1)) * (NB / 2) + (b >> 1) : t * NB + b;
-        return reinterpret_cast<uint32_t*>(rec[u] + off[u] + 4 * w);
-      };
-      auto pair_at = [&](int u) {
-        return reinterpret_cast<uint32_t*>(rec[u] + off[u] + D / 2 + 4 * b);
-      };
       if constexpr (WRITE) {
-        Eight<T> in[UNROLL];
+        const int b = lane & (NB - 1);
+        Eight<T> in[4];
+        const uint4* from = reinterpret_cast<const uint4*>(values[0] + 32 * b);
+        constexpr int W = sizeof(T) / 2;
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-            in[u].w[i] = rec[u] ? reinterpret_cast<const uint4*>(at[u])[i] : make_uint4(0, 0, 0, 0);
+          for (int i = 0; i < W; ++i)
+            in[t].w[i] = on[0] ? from[t * W + i] : make_uint4(0, 0, 0, 0);
+        float lo, hi;
+        extent(in, lo, hi);
+        const Scale g = scale_of(lo, hi);
+        uint32_t w[4];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
+        for (int t = 0; t < 4; ++t) {
           float x[8];
-          unpack(in[u], x);
-          uint32_t sm;
-          uint32_t w = quantise(x, sm);
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, b & 1 ? w & 0xffffu : w >> 16, 4);
-          if (is_v[u]) w = b & 1 ? got | (w & 0xffff0000u) : (w & 0xffffu) | got << 16;
-          if (rec[u]) {
-            *code_at(u) = w;
-            if (t == 0) *pair_at(u) = sm;
+          unpack(in[t], x);
+          w[t] = codes(x, g);
+        }
+        // V: the halves of groups b & ~1 and b | 1 stand in one word, those of chunks 0 to 3
+        // (values 0 to 15) with the even one's lane
+        const bool odd = b & 1;
+        const uint32_t got0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[2], 1);
+        const uint32_t got1 = __shfl_xor_sync(0xffffffffu, odd ? w[1] : w[3], 1);
+        uint32_t* to = reinterpret_cast<uint32_t*>(rec[0]);
+        if (on[0]) {
+          if (is_v[0]) {
+            const uint32_t low0 = odd ? got0 : w[0], low1 = odd ? got1 : w[1];
+            const uint32_t high0 = odd ? w[2] : got0, high1 = odd ? w[3] : got1;
+            to += (odd ? 4 : 0) * (NB / 2) + (b >> 1);
+            to[0] = __byte_perm(low0, high0, 0x5410);
+            to[NB / 2] = __byte_perm(low0, high0, 0x7632);
+            to[NB] = __byte_perm(low1, high1, 0x5410);
+            to[NB / 2 * 3] = __byte_perm(low1, high1, 0x7632);
+          } else {
+#pragma unroll
+            for (int t = 0; t < 4; ++t) to[t * NB + b] = w[t];
           }
+          reinterpret_cast<uint32_t*>(rec[0] + D / 2)[b] = g.pair;
         }
       } else {
-        uint32_t w[UNROLL], sm[UNROLL];
+        const int l = lane & (LANES - 1), b = l >> 2, t = l & 3;
+        const bool odd = b & 1;
+        uint32_t w[U], sm[U];
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-          w[u] = rec[u] ? *code_at(u) : 0;
-          sm[u] = rec[u] ? *pair_at(u) : 0;
+        for (int u = 0; u < U; ++u) {
+          // K: word t NB + b; V: of chunk 2 t (even b) or 2 t + 1 (odd b), the halves of
+          // groups b & ~1 and b | 1
+          const int at_word = is_v[u] ? (2 * t + odd) * (NB / 2) + (b >> 1) : t * NB + b;
+          w[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u])[at_word] : 0;
+          sm[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u] + D / 2)[b] : 0;
         }
 #pragma unroll
-        for (int u = 0; u < UNROLL; ++u) {
-          const uint32_t got =
-              __shfl_xor_sync(0xffffffffu, b & 1 ? w[u] & 0xffffu : w[u] >> 16, 4);
-          if (is_v[u]) w[u] = b & 1 ? got | (w[u] & 0xffff0000u) : (w[u] & 0xffffu) | got << 16;
+        for (int u = 0; u < U; ++u) {
+          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[u] & 0xffffu : w[u] >> 16, 4);
+          if (is_v[u]) w[u] = odd ? got | (w[u] & 0xffff0000u) : (w[u] & 0xffffu) | got << 16;
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sm[u]));
           float x[8];
 #pragma unroll
@@ -268,10 +320,10 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
           }
           Eight<T> o;
           pack(x, o);
-          if (rec[u])
+          if (on[u])
 #pragma unroll
             for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-              reinterpret_cast<uint4*>(at[u])[i] = o.w[i];
+              reinterpret_cast<uint4*>(values[u] + 8 * l)[i] = o.w[i];
         }
       }
     }
@@ -288,16 +340,19 @@ cudaError_t launch(const pks_q4_rows_args& a, cudaStream_t s) {
   sh.max_pages = a.max_pages;
   sh.num_pages = a.num_pages;
   sh.row_bytes = q4::token_bytes(a.Hkv, D);
-  sh.magic = (uint32_t)(((uint64_t(1) << 32) + 2 * a.Hkv - 1) / (2 * a.Hkv));
   sh.k_row = a.k_row;
   sh.k_head = a.k_head;
   sh.v_row = a.v_row;
   sh.v_head = a.v_head;
-  // few rows: a block each, so that they run side by side
-  const int per_sm = 8, most = device_sm_count() * per_sm;
-  sh.rows = 1;
-  while (sh.rows < kRowsMax && (int64_t)sh.rows * most < a.n_rows) sh.rows *= 2;
-  const int blocks = (int)(((int64_t)a.n_rows + sh.rows - 1) / sh.rows);
+  // few rows: as many warps a row as have work, so that they run side by side
+  const int most = device_sm_count() * (2048 / kRowThreads);
+  const int each = 32 / (WRITE ? D / q4::kGroup : D / 8) * (WRITE ? 1 : 4);
+  sh.warps = 1;
+  while (sh.warps < kRowWarps && sh.warps * each < 2 * a.Hkv &&
+         (int64_t)a.n_rows * sh.warps < (int64_t)most * kRowWarps / 2)
+    sh.warps *= 2;
+  const int rows = kRowWarps / sh.warps;
+  const int blocks = (int)(((int64_t)a.n_rows + rows - 1) / rows);
   return launch_ex(k_q4_rows<T, D, WRITE>, dim3(blocks < most ? blocks : most), dim3(kRowThreads),
                    sizeof(int32_t) * (size_t)(a.B + 1), s, /*pdl=*/true, /*coop=*/false,
                    a.seq_lens, a.block_table, a.starts, static_cast<T*>(a.k),
