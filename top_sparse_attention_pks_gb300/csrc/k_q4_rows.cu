@@ -21,6 +21,7 @@ namespace pks {
 namespace {
 
 constexpr int kRowThreads = 256, kRowWarps = kRowThreads / 32;
+constexpr int kRowsEach = 8;  // of a warp, at most, whose places a block finds at once
 // what eight magic numbers (1.5 2^23 as bits, shifted by 4 i) add up to beside the codes
 constexpr uint32_t kMagicSum = 0x4b400000u * 0x11111111u;
 
@@ -207,6 +208,7 @@ __device__ __forceinline__ int place_of(int i, const int32_t* starts, int B,
 struct RowShape {
   int B, n_rows, Hkv, page_size, max_pages, num_pages;
   int warps;          // a row: 1 to 8, a power of two
+  int each;           // rows that a block finds the places of at once, a warp's share of them
   int row_bytes;      // of a token in the pool
   int64_t k_row, k_head, v_row, v_head;
 };
@@ -221,9 +223,10 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
   constexpr int LANES = WRITE ? NB : D / 8, AT_ONCE = 32 / LANES;  // records of a warp
   constexpr int U = WRITE ? 1 : 4;                                // of a lane at once
   extern __shared__ int32_t s_starts[];
-  __shared__ int s_place[kRowWarps];
+  __shared__ int s_place[kRowWarps * kRowsEach];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int part = warp & (sh.warps - 1), mine = warp / sh.warps, rows = kRowWarps / sh.warps;
+  const int part = warp & (sh.warps - 1), mine = warp / sh.warps, side = kRowWarps / sh.warps;
+  const int rows = side * sh.each;
   pdl_wait(seq_lens, block_table, starts, k, v, pool_k, pool_v);
   pdl_launch_dependents();
   for (int i = tid; i <= sh.B; i += kRowThreads) s_starts[i] = starts[i];
@@ -235,95 +238,97 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
                                     sh.page_size, sh.max_pages, sh.num_pages, error)
                          : -1;
     __syncthreads();
-    const int place = s_place[mine];
-    if (place < 0) continue;  // (a whole warp)
-    const int64_t row = r0 + mine, at = (int64_t)place * sh.row_bytes;
-    T* k_row = k + row * sh.k_row;
-    T* v_row = v + row * sh.v_row;
-    // K's records, then V's; the shuffles need all lanes: those without a record go along
-    for (int j0 = part * AT_ONCE * U; j0 < 2 * sh.Hkv; j0 += sh.warps * AT_ONCE * U) {
-      T* values[U];
-      uint8_t* rec[U];
-      bool is_v[U], on[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int j = j0 + u * AT_ONCE + lane / LANES;
-        on[u] = j < 2 * sh.Hkv;
-        is_v[u] = j >= sh.Hkv;
-        const int h = is_v[u] ? j - sh.Hkv : j;
-        values[u] = is_v[u] ? v_row + h * sh.v_head : k_row + h * sh.k_head;
-        rec[u] = (is_v[u] ? pool_v : pool_k) + at + h * REC;
-      }
-      if constexpr (WRITE) {
-        const int b = lane & (NB - 1);
-        Eight<T> in[4];
-        const uint4* from = reinterpret_cast<const uint4*>(values[0] + 32 * b);
-        constexpr int W = sizeof(T) / 2;
-#pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-          for (int i = 0; i < W; ++i)
-            in[t].w[i] = on[0] ? from[t * W + i] : make_uint4(0, 0, 0, 0);
-        float lo, hi;
-        extent(in, lo, hi);
-        const Scale g = scale_of(lo, hi);
-        uint32_t w[4];
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          float x[8];
-          unpack(in[t], x);
-          w[t] = codes(x, g);
-        }
-        // V: the halves of groups b & ~1 and b | 1 stand in one word, those of chunks 0 to 3
-        // (values 0 to 15) with the even one's lane
-        const bool odd = b & 1;
-        const uint32_t got0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[2], 1);
-        const uint32_t got1 = __shfl_xor_sync(0xffffffffu, odd ? w[1] : w[3], 1);
-        uint32_t* to = reinterpret_cast<uint32_t*>(rec[0]);
-        if (on[0]) {
-          if (is_v[0]) {
-            const uint32_t low0 = odd ? got0 : w[0], low1 = odd ? got1 : w[1];
-            const uint32_t high0 = odd ? w[2] : got0, high1 = odd ? w[3] : got1;
-            to += (odd ? 4 : 0) * (NB / 2) + (b >> 1);
-            to[0] = __byte_perm(low0, high0, 0x5410);
-            to[NB / 2] = __byte_perm(low0, high0, 0x7632);
-            to[NB] = __byte_perm(low1, high1, 0x5410);
-            to[NB / 2 * 3] = __byte_perm(low1, high1, 0x7632);
-          } else {
-#pragma unroll
-            for (int t = 0; t < 4; ++t) to[t * NB + b] = w[t];
-          }
-          reinterpret_cast<uint32_t*>(rec[0] + D / 2)[b] = g.pair;
-        }
-      } else {
-        const int l = lane & (LANES - 1), b = l >> 2, t = l & 3;
-        const bool odd = b & 1;
-        uint32_t w[U], sm[U];
+    for (int r = mine; r < rows; r += side) {
+      const int place = s_place[r];
+      if (place < 0) continue;  // (a whole warp)
+      const int64_t row = r0 + r, at = (int64_t)place * sh.row_bytes;
+      T* k_row = k + row * sh.k_row;
+      T* v_row = v + row * sh.v_row;
+      // K's records, then V's; the shuffles need all lanes: those without a record go along
+      for (int j0 = part * AT_ONCE * U; j0 < 2 * sh.Hkv; j0 += sh.warps * AT_ONCE * U) {
+        T* values[U];
+        uint8_t* rec[U];
+        bool is_v[U], on[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-          // K: word t NB + b; V: of chunk 2 t (even b) or 2 t + 1 (odd b), the halves of
-          // groups b & ~1 and b | 1
-          const int at_word = is_v[u] ? (2 * t + odd) * (NB / 2) + (b >> 1) : t * NB + b;
-          w[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u])[at_word] : 0;
-          sm[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u] + D / 2)[b] : 0;
+          const int j = j0 + u * AT_ONCE + lane / LANES;
+          on[u] = j < 2 * sh.Hkv;
+          is_v[u] = j >= sh.Hkv;
+          const int h = is_v[u] ? j - sh.Hkv : j;
+          values[u] = is_v[u] ? v_row + h * sh.v_head : k_row + h * sh.k_head;
+          rec[u] = (is_v[u] ? pool_v : pool_k) + at + h * REC;
         }
+        if constexpr (WRITE) {
+          const int b = lane & (NB - 1);
+          Eight<T> in[4];
+          const uint4* from = reinterpret_cast<const uint4*>(values[0] + 32 * b);
+          constexpr int W = sizeof(T) / 2;
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[u] & 0xffffu : w[u] >> 16, 4);
-          if (is_v[u]) w[u] = odd ? got | (w[u] & 0xffff0000u) : (w[u] & 0xffffu) | got << 16;
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sm[u]));
-          float x[8];
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float n = __uint_as_float((w[u] >> (4 * i) & 15u) | 0x4b000000u) - 8388608.f;
-            x[i] = __fmaf_rn(n, f.x, f.y);
+            for (int i = 0; i < W; ++i)
+              in[t].w[i] = on[0] ? from[t * W + i] : make_uint4(0, 0, 0, 0);
+          float lo, hi;
+          extent(in, lo, hi);
+          const Scale g = scale_of(lo, hi);
+          uint32_t w[4];
+#pragma unroll
+          for (int t = 0; t < 4; ++t) {
+            float x[8];
+            unpack(in[t], x);
+            w[t] = codes(x, g);
           }
-          Eight<T> o;
-          pack(x, o);
-          if (on[u])
+          // V: the halves of groups b & ~1 and b | 1 stand in one word, those of chunks 0 to 3
+          // (values 0 to 15) with the even one's lane
+          const bool odd = b & 1;
+          const uint32_t got0 = __shfl_xor_sync(0xffffffffu, odd ? w[0] : w[2], 1);
+          const uint32_t got1 = __shfl_xor_sync(0xffffffffu, odd ? w[1] : w[3], 1);
+          uint32_t* to = reinterpret_cast<uint32_t*>(rec[0]);
+          if (on[0]) {
+            if (is_v[0]) {
+              const uint32_t low0 = odd ? got0 : w[0], low1 = odd ? got1 : w[1];
+              const uint32_t high0 = odd ? w[2] : got0, high1 = odd ? w[3] : got1;
+              to += (odd ? 4 : 0) * (NB / 2) + (b >> 1);
+              to[0] = __byte_perm(low0, high0, 0x5410);
+              to[NB / 2] = __byte_perm(low0, high0, 0x7632);
+              to[NB] = __byte_perm(low1, high1, 0x5410);
+              to[NB / 2 * 3] = __byte_perm(low1, high1, 0x7632);
+            } else {
 #pragma unroll
-            for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-              reinterpret_cast<uint4*>(values[u] + 8 * l)[i] = o.w[i];
+              for (int t = 0; t < 4; ++t) to[t * NB + b] = w[t];
+            }
+            reinterpret_cast<uint32_t*>(rec[0] + D / 2)[b] = g.pair;
+          }
+        } else {
+          const int l = lane & (LANES - 1), b = l >> 2, t = l & 3;
+          const bool odd = b & 1;
+          uint32_t w[U], sm[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            // K: word t NB + b; V: of chunk 2 t (even b) or 2 t + 1 (odd b), the halves of
+            // groups b & ~1 and b | 1
+            const int at_word = is_v[u] ? (2 * t + odd) * (NB / 2) + (b >> 1) : t * NB + b;
+            w[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u])[at_word] : 0;
+            sm[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u] + D / 2)[b] : 0;
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[u] & 0xffffu : w[u] >> 16, 4);
+            if (is_v[u]) w[u] = odd ? got | (w[u] & 0xffff0000u) : (w[u] & 0xffffu) | got << 16;
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sm[u]));
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float n = __uint_as_float((w[u] >> (4 * i) & 15u) | 0x4b000000u) - 8388608.f;
+              x[i] = __fmaf_rn(n, f.x, f.y);
+            }
+            Eight<T> o;
+            pack(x, o);
+            if (on[u])
+#pragma unroll
+              for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+                reinterpret_cast<uint4*>(values[u] + 8 * l)[i] = o.w[i];
+          }
         }
       }
     }
@@ -351,7 +356,11 @@ cudaError_t launch(const pks_q4_rows_args& a, cudaStream_t s) {
   while (sh.warps < kRowWarps && sh.warps * each < 2 * a.Hkv &&
          (int64_t)a.n_rows * sh.warps < (int64_t)most * kRowWarps / 2)
     sh.warps *= 2;
-  const int rows = kRowWarps / sh.warps;
+  sh.each = 1;
+  while (sh.each < kRowsEach &&
+         (int64_t)a.n_rows * sh.warps >= (int64_t)most * kRowWarps * 2 * sh.each)
+    sh.each *= 2;
+  const int rows = kRowWarps / sh.warps * sh.each;
   const int blocks = (int)(((int64_t)a.n_rows + rows - 1) / rows);
   return launch_ex(k_q4_rows<T, D, WRITE>, dim3(blocks < most ? blocks : most), dim3(kRowThreads),
                    sizeof(int32_t) * (size_t)(a.B + 1), s, /*pdl=*/true, /*coop=*/false,

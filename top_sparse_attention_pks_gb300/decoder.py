@@ -410,14 +410,12 @@ class Q4Cache:
             self.error = torch.zeros(1, dtype=torch.int32, device=device)
         self.Hkv, self.D = int(Hkv), int(D)
         pks._on_current_device(self.k)
+        self._base = pks._q4_rows_base(self.k, self.v, Hkv, D, self.error)
 
     def _args(self, k, v, seq_lens, block_table, starts):
         pks._on_current_device(self.k, k, v, seq_lens, block_table, starts)
-        if tuple(k.shape[1:]) != (self.Hkv, self.D):
-            raise ValueError(f"rows must be [n, {self.Hkv}, {self.D}]")
-        return pks.make_q4_rows_args(k=k, v=v, seq_lens=seq_lens, block_table=block_table,
-                                     starts=starts, pool_k=self.k, pool_v=self.v,
-                                     error=self.error)
+        a = pks.pks_q4_rows_args.from_buffer_copy(self._base)  # (calls may come from two threads)
+        return pks._q4_rows_fill(a, k, v, seq_lens, block_table, starts)
 
     def write(self, k, v, seq_lens, block_table, starts, stream=None):
         """Quantise the rows of k and v into their pages."""

@@ -891,34 +891,57 @@ def _q4_pools(a, pool_k, pool_v, Hkv: int, D: int) -> None:
     a.pool_v = _dptr(pool_v, torch.uint8, "pool_v")
 
 
+def _q4_rows_base(pool_k, pool_v, Hkv: int, D: int, error=None) -> pks_q4_rows_args:
+    """The fields of a cache, which its calls copy."""
+    a = pks_q4_rows_args()
+    a.Hkv, a.D = int(Hkv), int(D)
+    _q4_pools(a, pool_k, pool_v, Hkv, D)
+    a.error = _dptr(error, torch.int32, "error")
+    return a
+
+
+def _q4_rows_fill(a: pks_q4_rows_args, k, v, seq_lens, block_table, starts) -> pks_q4_rows_args:
+    """The fields of a call.  (One pass over what a decode step calls for every layer: each
+    tensor's attributes are looked up once.)"""
+    shape, dtype = k.shape, k.dtype
+    if len(shape) != 3 or v.shape != shape or v.dtype != dtype:
+        raise ValueError("k and v must be [n_rows, Hkv, D] of one type")
+    n, Hkv, D = shape
+    if Hkv != a.Hkv or D != a.D:
+        raise ValueError(f"rows must be [n_rows, {a.Hkv}, {a.D}]")
+    code = _Q4_TYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"k and v must be bfloat16, float16 or float32, got {dtype}")
+    if block_table.dim() != 2:
+        raise ValueError("block_table must be [B, max_pages]")
+    B, a.max_pages = block_table.shape
+    if seq_lens.shape != (B,) or starts.shape != (B + 1,):
+        raise ValueError("seq_lens must be [B] and starts [B + 1], block_table [B, max_pages]")
+    for name, t in (("seq_lens", seq_lens), ("block_table", block_table), ("starts", starts)):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be {torch.int32}, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        setattr(a, name, t.data_ptr())
+    a.B, a.n_rows, a.dtype = B, n, code
+    if n:
+        a.k_row, a.k_head, last = k.stride()
+        a.v_row, a.v_head, last_v = v.stride()
+        if last != 1 or last_v != 1:
+            raise ValueError("the values of a row's head must be contiguous")
+    a.k, a.v = k.data_ptr(), v.data_ptr()
+    return a
+
+
 def make_q4_rows_args(*, k, v, seq_lens, block_table, starts, pool_k, pool_v,
                       error=None) -> pks_q4_rows_args:
     """Fill a ``pks_q4_rows_args``: k, v [n_rows, Hkv, D] (any row and head strides, e.g.
     slices of a fused projection), seq_lens [B], block_table [B, max_pages], starts [B + 1],
     pools [num_pages, page_size, token_bytes] (uint8), error: int32 tensor or None."""
-    a = pks_q4_rows_args()
-    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype:
+    if k.dim() != 3:
         raise ValueError("k and v must be [n_rows, Hkv, D] of one type")
-    if k.dtype not in _Q4_TYPES:
-        raise TypeError(f"k and v must be bfloat16, float16 or float32, got {k.dtype}")
-    n, Hkv, D = k.shape
-    if n and (k.stride(2) != 1 or v.stride(2) != 1):
-        raise ValueError("the values of a row's head must be contiguous")
-    B = block_table.shape[0]
-    if block_table.dim() != 2 or tuple(seq_lens.shape) != (B,) or tuple(starts.shape) != (B + 1,):
-        raise ValueError("block_table must be [B, max_pages], seq_lens [B] and starts [B + 1]")
-    a.B, a.n_rows, a.Hkv, a.D = int(B), int(n), int(Hkv), int(D)
-    a.max_pages = int(block_table.shape[1])
-    a.dtype = _Q4_TYPES[k.dtype]
-    _q4_pools(a, pool_k, pool_v, Hkv, D)
-    a.seq_lens = _dptr(seq_lens, torch.int32, "seq_lens")
-    a.block_table = _dptr(block_table, torch.int32, "block_table")
-    a.starts = _dptr(starts, torch.int32, "starts")
-    a.k, a.v = k.data_ptr(), v.data_ptr()
-    if n:
-        a.k_row, a.k_head, a.v_row, a.v_head = k.stride(0), k.stride(1), v.stride(0), v.stride(1)
-    a.error = _dptr(error, torch.int32, "error")
-    return a
+    return _q4_rows_fill(_q4_rows_base(pool_k, pool_v, k.shape[1], k.shape[2], error), k, v,
+                         seq_lens, block_table, starts)
 
 
 def pks_q4_write(args: pks_q4_rows_args, stream=None) -> None:
