@@ -90,7 +90,7 @@ struct Q4Shape {
   int box;           // kBoxes: tokens of one
   int lanes;         // kLanes: that copy a token, a unit or two each
   uint64_t order;
-  int stages, ring, scratch_at, nv_at;  // bytes of the ring; where scratch and lengths begin
+  int stages, q_at, scratch_at, nv_at;  // of the ring; where what lies behind it begins
   int grid;
 };
 
@@ -166,11 +166,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_
       : "memory");
 }
 
-// Where byte o of a stage's K or V stands: boxes come with the 128-byte swizzle
-__device__ __forceinline__ uint32_t place(const Q4Shape& sh, uint32_t o) {
-  return sh.copies == kBoxes ? o ^ (o >> 7 & 7) << 4 : o;
-}
-
 // What a stage holds, from its producer to the consumers.  mask: the tokens present,
 // of each 16, and the flags above them.
 struct alignas(16) StageNote {
@@ -215,7 +210,10 @@ struct Shares {
   }
 };
 
-template <int D, int NT, int TT, int PW>
+// SLICE: 640 or 656 where a stage's rows are the records of eight heads of 128 values, by
+// boxes or by tokens: distances that the compiler knows save an address computation for
+// most loads from shared memory (16 x 131072 tokens 450 -> 441 us); 0: any others.
+template <int D, int NT, int TT, int PW, int SLICE>
 __global__ void __launch_bounds__((kConsumers + PW) * 32, 1)
 k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ block_table,
                const int32_t* __restrict__ lists, const __nv_bfloat16* __restrict__ q,
@@ -239,12 +237,20 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (ring - tc::smem_u32(smem_raw));
-  const int half = sh.TS * sh.slice;
+  constexpr bool FIXED = SLICE > 0;
+  const int slice = FIXED ? SLICE : sh.slice, TS = FIXED ? 16 * TT : sh.TS;
+  const int ts_log2 = FIXED ? (TT == 2 ? 5 : 4) : sh.ts_log2;
+  const int HG = FIXED ? 8 : sh.HG, WPH = FIXED ? 1 : sh.WPH;
+  const int copies = SLICE == 640 ? kBoxes : SLICE == 656 ? kTokens : sh.copies;
+  const int half = TS * slice;
+  auto place = [&](uint32_t o) {  // of byte o of a stage's K or V: boxes come swizzled
+    return copies == kBoxes ? o ^ (o >> 7 & 7) << 4 : o;
+  };
   int* s_nv = reinterpret_cast<int*>(smem + sh.nv_at);
-  const int consumers = sh.HG * sh.WPH;
+  const int consumers = HG * WPH;
   if (tid == 0) {
     for (int i = 0; i < sh.stages; ++i) {
-      tc::mbar_init(&bar_full[i], sh.copies == kTokens ? 2 : sh.copies == kLanes ? 33 : 1);
+      tc::mbar_init(&bar_full[i], copies == kTokens ? 2 : copies == kLanes ? 33 : 1);
       tc::mbar_init(&bar_empty[i], consumers);
     }
     tc::mbar_init(&bar_join, consumers);
@@ -260,7 +266,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   const int per = (sh.Bv + NTHREADS - 1) / NTHREADS, v_lo = min(tid * per, sh.Bv),
             v_hi = min(v_lo + per, sh.Bv);
   const int chunks = sh.NHG * sh.NRC;
-  auto stages_of = [&](int n) { return (n + sh.TS - 1) >> sh.ts_log2; };
+  auto stages_of = [&](int n) { return (n + TS - 1) >> ts_log2; };
   int mine = 0;
   for (int v = v_lo; v < v_hi; ++v) {
     int n = seq_lens[sh.lists == 1 ? v : v / sh.lists];
@@ -376,25 +382,25 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       if (tile == T - 1 || i == count - 1) f |= kLast;
       if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
       if (seg_at > lo) f |= kSecond;
-      if (sh.causal && ((tile + 1) << sh.ts_log2) > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G))
+      if (sh.causal && ((tile + 1) << ts_log2) > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G))
         f |= kEdge;
       return f;
     };
     // a token that is not there: no weight, but what its place holds takes part in a product
     auto absent = [&](uint32_t dst_v, int at) {
-      for (int h = 0; h < sh.HG; ++h)
+      for (int h = 0; h < HG; ++h)
 #pragma unroll
         for (int o = 0; o < 4 * NB; o += 8)
-          sts_zero8(dst_v + place(sh, at * sh.slice + h * REC + D / 2 + o));
+          sts_zero8(dst_v + place(at * slice + h * REC + D / 2 + o));
     };
     // (the stages that one warp fills are never further apart than the ring is long)
-    const int stride = sh.copies == kTokens ? PW / 2 : 4;
-    const int mine_from = sh.copies == kTokens ? me >> 1 : me;
+    const int stride = copies == kTokens ? PW / 2 : 4;
+    const int mine_from = copies == kTokens ? me >> 1 : me;
     if (mine_from >= stride) return;
     int stage = mine_from, round = 0;
     bool ok = true;
     if (mine_from < count) forward(mine_from);
-    if (sh.copies == kTokens) {
+    if (copies == kTokens) {
       // ---- a token a lane (or two), K or V ----
       constexpr int PER = 2;
       const bool is_v = me & 1;
@@ -403,9 +409,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       auto tokens = [&]() {  // of the stage at hand, as positions
 #pragma unroll
         for (int u = 0; u < PER; ++u) {
-          const int at = 32 * u + lane, p = (tile << sh.ts_log2) + at;
+          const int at = 32 * u + lane, p = (tile << ts_log2) + at;
           t[u] = -1;
-          if (at < sh.TS && p < n) t[u] = sh.k ? lists[(int64_t)v * sh.k + p] : p;
+          if (at < TS && p < n) t[u] = sh.k ? lists[(int64_t)v * sh.k + p] : p;
         }
       };
       auto pages = [&]() {
@@ -435,7 +441,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         rows();
       }
       for (int i = mine_from; i < count; i += stride) {
-        const int4 seg = make_int4(v, c, tile << sh.ts_log2, n);
+        const int4 seg = make_int4(v, c, tile << ts_log2, n);
         const uint32_t f = flags_of(i);
         const bool more = i + stride < count;
         // the next stage's places are looked up while this one waits and is filled
@@ -459,7 +465,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           here[u] = __ballot_sync(0xffffffffu, row[u] >= 0);
           present += __popc(here[u]);
           if (!is_v && lane < 2) note->mask[2 * u + lane] = (here[u] >> 16 * lane & 0xffffu) | f;
-          if (is_v && row[u] < 0 && 32 * u + lane < sh.TS) {
+          if (is_v && row[u] < 0 && 32 * u + lane < TS) {
             absent(dst, 32 * u + lane);
             gone = true;
           }
@@ -469,11 +475,11 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], (uint32_t)present * sh.taken);
         __syncwarp();
-        const int off = seg.y / sh.NRC * sh.HG * REC;
+        const int off = seg.y / sh.NRC * HG * REC;
 #pragma unroll
         for (int u = 0; u < PER; ++u)
           if (row[u] >= 0)
-            bulk_load(dst + (32 * u + lane) * sh.slice,
+            bulk_load(dst + (32 * u + lane) * slice,
                       pool + (int64_t)row[u] * sh.row_bytes + off, sh.taken, &bar_full[stage]);
         if (more) rows();
         stage += stride;
@@ -485,20 +491,20 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     } else {
       for (int i = mine_from; i < count; i += stride) {
         if (i != next) forward(i - next);
-        const int p0 = tile << sh.ts_log2, here = min(n - p0, sh.TS);  // tokens in reach
+        const int p0 = tile << ts_log2, here = min(n - p0, TS);  // tokens in reach
         const int* table = block_table + (int64_t)request * sh.max_pages;
         // ---- where the stage's tokens lie
         int run_at = 0, run = 0, run_row = -1;  // a run of tokens in one page, a lane each
         bool whole = true;                      // all in reach are there
         uint32_t full = 0;                      // boxes, and tokens in them
         auto lone = [&](bool mine, int tokens) {  // tokens of a lane's page that go one by one
-          for (int at = lane; at < sh.TS; at += 32) s_row[at] = -1;
+          for (int at = lane; at < TS; at += 32) s_row[at] = -1;
           __syncwarp();
           if (mine)
             for (int r = 0; r < tokens; ++r) s_row[run_at + r] = run_row + r;
           __syncwarp();
         };
-        if (sh.copies == kBoxes) {
+        if (copies == kBoxes) {
           run_at = lane * sh.box;
           const bool some = run_at < here;
           if (some) {
@@ -509,9 +515,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           }
           const bool boxed = run_row >= 0 && run_at + sh.box <= here;
           full = __ballot_sync(0xffffffffu, boxed);
-          whole = __all_sync(0xffffffffu, boxed || run_at >= sh.TS);
+          whole = __all_sync(0xffffffffu, boxed || run_at >= TS);
           if (!whole) lone(run_row >= 0 && !boxed, here - run_at);
-        } else if (sh.copies == kRuns) {
+        } else if (copies == kRuns) {
           int slot;
           const int page0 = page_of(p0, slot);
           run_at = lane == 0 ? 0 : lane * sh.page_size - slot;
@@ -528,7 +534,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           if (!whole) lone(true, run);  // (told apart below)
         } else {
           const int len = sh.k ? seq_lens[request] : 0;
-          for (int at0 = 0; at0 < sh.TS; at0 += 128) {  // (four tokens a lane at once)
+          for (int at0 = 0; at0 < TS; at0 += 128) {  // (four tokens a lane at once)
             int t[4], page[4], slot[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -551,7 +557,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                 if (page[u] < 0 || page[u] >= sh.num_pages) *err = kErrPage;
                 else row = page[u] * sh.page_size + slot[u];
               }
-              if (at < sh.TS) s_row[at] = row;
+              if (at < TS) s_row[at] = row;
             }
           }
           __syncwarp();
@@ -570,20 +576,20 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         bool gone = false;
         if (whole) {
           if (lane < 16) note->mask[lane] = ((1u << min(max(here - 16 * lane, 0), 16)) - 1) | f;
-          for (int at = here + lane; at < sh.TS; at += 32) {
+          for (int at = here + lane; at < TS; at += 32) {
             absent(dst_v, at);
             gone = true;
           }
         } else {
           present = 0;
-          for (int at0 = 0; at0 < sh.TS; at0 += 32) {
+          for (int at0 = 0; at0 < TS; at0 += 32) {
             const int at = at0 + lane;
             const bool there =
-                at < sh.TS && (s_row[at] >= 0 || (sh.copies == kBoxes && full >> at / sh.box & 1));
+                at < TS && (s_row[at] >= 0 || (copies == kBoxes && full >> at / sh.box & 1));
             const uint32_t m = __ballot_sync(0xffffffffu, there);
             if (lane < 2) note->mask[at0 / 16 + lane] = (m >> 16 * lane & 0xffffu) | f;
             present += __popc(m);
-            if (at < sh.TS && !there) {
+            if (at < TS && !there) {
               absent(dst_v, at);
               gone = true;
             }
@@ -592,16 +598,16 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         if (gone) tc::fence_async_smem();
         if (lane == 0) *reinterpret_cast<int4*>(note) = make_int4(v, c, p0, n);
         __syncwarp();
-        if (sh.copies == kRuns) {
-          if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], 2u * present * sh.slice);
+        if (copies == kRuns) {
+          if (lane == 0) tc::mbar_arrive_expect(&bar_full[stage], 2u * present * slice);
           __syncwarp();
           if (run > 0) {
             const int64_t src = (int64_t)run_row * sh.row_bytes;
-            const uint32_t o = run_at * sh.slice;
-            bulk_load(dst_k + o, pool_k + src, run * sh.slice, &bar_full[stage]);
-            bulk_load(dst_v + o, pool_v + src, run * sh.slice, &bar_full[stage]);
+            const uint32_t o = run_at * slice;
+            bulk_load(dst_k + o, pool_k + src, run * slice, &bar_full[stage]);
+            bulk_load(dst_v + o, pool_v + src, run * slice, &bar_full[stage]);
           }
-        } else if (sh.copies == kLanes || !whole) {
+        } else if (copies == kLanes || !whole) {
           // `lanes` lanes a token, each with a unit or two of it; some tokens at once
           constexpr int U = 4;
           const int ln = sh.lanes, tok = lane / ln, unit = lane & (ln - 1), step = 32 / ln;
@@ -609,21 +615,21 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           const uint32_t o0 = unit * sh.unit, o1 = (unit + ln) * sh.unit;
           const bool on0 = unit < cpt, on1 = unit + ln < cpt;
           const int64_t to_v = pool_v - pool_k;
-          const uint8_t* part = pool_k + c / sh.NRC * sh.HG * REC;
+          const uint8_t* part = pool_k + c / sh.NRC * HG * REC;
 #pragma unroll 1
-          for (int at0 = tok; at0 < sh.TS; at0 += step * U) {
+          for (int at0 = tok; at0 < TS; at0 += step * U) {
             int row[U];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               const int at = at0 + u * step;
-              row[u] = at < sh.TS ? s_row[at] : -1;
+              row[u] = at < TS ? s_row[at] : -1;
             }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
               if (row[u] < 0) continue;
               const uint8_t* src = part + (int64_t)row[u] * sh.row_bytes;
               auto copy = [&](uint32_t o) {
-                const uint32_t to = dst_k + place(sh, (at0 + u * step) * sh.slice + o);
+                const uint32_t to = dst_k + place((at0 + u * step) * slice + o);
                 if (sh.unit == 16) {
                   tc::cp_async16(to, src + o, 16);
                   tc::cp_async16(to + half, src + to_v + o, 16);
@@ -636,7 +642,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
               if (on1) copy(o1);
             }
           }
-          if (sh.copies == kLanes) {
+          if (copies == kLanes) {
             tc::cp_async_arrive(&bar_full[stage]);
             if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
           } else {  // (the end of a request: these copies land before the boxes are announced)
@@ -645,13 +651,13 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             __syncwarp();
           }
         }
-        if (sh.copies == kBoxes) {
+        if (copies == kBoxes) {
           if (lane == 0)
-            tc::mbar_arrive_expect(&bar_full[stage], 2u * __popc(full) * sh.box * sh.slice);
+            tc::mbar_arrive_expect(&bar_full[stage], 2u * __popc(full) * sh.box * slice);
           __syncwarp();
           if (full >> lane & 1) {
-            const uint32_t o = run_at * sh.slice;
-            const int line = c / sh.NRC * (sh.slice / 128);
+            const uint32_t o = run_at * slice;
+            const int line = c / sh.NRC * (slice / 128);
             tc::tma_load_3d(dst_k + o, &map_k, 0, line, run_row, &bar_full[stage]);
             tc::tma_load_3d(dst_v + o, &map_v, 0, line, run_row, &bar_full[stage]);
           }
@@ -680,11 +686,11 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   // =========================== consumers ===========================
   set_registers<208, true>();
   if (warp >= consumers) return;
-  const int h = warp / sh.WPH, sub = warp - h * sh.WPH;
+  const int h = warp / WPH, sub = warp - h * WPH;
   const int g = lane >> 2, t = lane & 3;
   auto token = [&](int r) { return (int)(sh.order >> (4 * r) & 15); };
   auto at = [&](int tok, int off) -> uint32_t {  // (16 tokens on, a box is swizzled alike)
-    return sub * TT * 16 * sh.slice + place(sh, tok * sh.slice + h * REC + off);
+    return sub * TT * 16 * slice + place(tok * slice + h * REC + off);
   };
   // rows g and g + 8 of the tokens' tiles; K codes and pairs
   const int tok0 = token(g), tok1 = token(g + 8);
@@ -704,7 +710,10 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   asm volatile("" : "+r"(v_pair[0]), "+r"(v_pair[1]), "+r"(v_pair[2]), "+r"(v_pair[3]));
   const int m_word = 4 * (g & (NB - 1));
 
-  uint32_t qf[NT][NB][4], qs[NT][2];  // queries as B operands; the pieces of their sums
+  // queries as B operands, in shared memory where registers are short; the pieces of their sums
+  constexpr bool QSHARED = NT * TT == 4;
+  uint32_t qf[QSHARED ? 1 : NT][NB][4], qs[NT][2];
+  uint4* q_shared = reinterpret_cast<uint4*>(smem + sh.q_at) + warp * NT * NB * 32 + lane;
   // of columns 2t, 2t + 1: scale of the scores, minus the reference, sum of weights
   float cs[NT][2], nref[NT][2], sum[NT][2];
   float o[NT][NB][2][4], om[NT][2];
@@ -729,7 +738,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       fresh = false;
       sx = 0;
       const int hg = q_c / sh.NRC, rc = q_c - hg * sh.NRC;
-      const int head = hg * sh.HG + h;
+      const int head = hg * HG + h;
       const __nv_bfloat16* from = q;
       behind(from);
 #pragma unroll
@@ -784,10 +793,12 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             const __nv_bfloat162 y = __floats2bfloat162_rn(x[b][i] * f, x[b][i + 4] * f);
             return *reinterpret_cast<const uint32_t*>(&y);
           };
-          qf[nt][b][0] = two(0, 128.f);
-          qf[nt][b][1] = two(1, 8.f);
-          qf[nt][b][2] = two(2, 128.f);
-          qf[nt][b][3] = two(3, 8.f);
+          const uint4 qb = make_uint4(two(0, 128.f), two(1, 8.f), two(2, 128.f), two(3, 8.f));
+          if constexpr (QSHARED) {
+            q_shared[(nt * NB + b) * 32] = qb;
+          } else {
+            qf[nt][b][0] = qb.x, qf[nt][b][1] = qb.y, qf[nt][b][2] = qb.z, qf[nt][b][3] = qb.w;
+          }
           // the sum in the unit of the codes' products, 2^(p + 7 - 133): at most 1, in
           // pieces of 11 bits
           const float y = s * __int_as_float(1 << 23);  // 2^-126
@@ -824,19 +835,19 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     const int4 seg = *reinterpret_cast<const int4*>(note);  // v, c, p0, nv
     uint32_t k0[TT][NB], k1[TT][NB], kp0[TT][NB], kp1[TT][NB];
     uint32_t w[TT][4][NB / 2], s01[TT][NB], s23[TT][NB], ma0[TT], ma2[TT];
-    {
-      const uint8_t* base = smem + (uint32_t)stage * 2 * half;
+    const uint8_t* base = smem + (uint32_t)stage * 2 * half;
+#pragma unroll
+    for (int u = 0; u < TT; ++u) {
+      const uint8_t* from = base + u * 16 * slice;
+      lds(from + k_code0, k0[u]);
+      lds(from + k_code1, k1[u]);
+      lds(from + k_pair0, kp0[u]);
+      lds(from + k_pair1, kp1[u]);
+    }
+    auto load_v = [&]() {
 #pragma unroll
       for (int u = 0; u < TT; ++u) {
-        const uint8_t* from = base + u * 16 * sh.slice;
-        lds(from + k_code0, k0[u]);
-        lds(from + k_code1, k1[u]);
-        lds(from + k_pair0, kp0[u]);
-        lds(from + k_pair1, kp1[u]);
-      }
-#pragma unroll
-      for (int u = 0; u < TT; ++u) {
-        const uint8_t* from = base + u * 16 * sh.slice;
+        const uint8_t* from = base + u * 16 * slice;
         uint32_t x[4][NB], m[4][1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -852,13 +863,14 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         ma0[u] = __byte_perm(m[0][0], m[1][0], 0x7632);
         ma2[u] = __byte_perm(m[2][0], m[3][0], 0x7632);
       }
-    }
-    __syncwarp();
-    if (lane == 0) tc::mbar_arrive(&bar_empty[stage]);
-    if (++stage == sh.stages) {
-      stage = 0;
-      phase ^= 1;
-    }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bar_empty[stage]);
+      if (++stage == sh.stages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    };
+    if constexpr (!QSHARED) load_v();  // (early, but where registers are short)
     // ---------------- scores ----------------
     float tot[TT][NT][4];
 #pragma unroll
@@ -871,17 +883,26 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       const uint32_t a3 = NB == 4 ? __byte_perm(kp1[u][NB - 2], kp1[u][NB - 1], 0x7632) : 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) mma_f16(tot[u][nt], a0, a1, a2, a3, qs[nt][0], qs[nt][1]);
+    }
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
+    for (int b = 0; b < NB; ++b) {
+      uint4 qb[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (QSHARED) qb[nt] = q_shared[(nt * NB + b) * 32];
+        else qb[nt] = make_uint4(qf[nt][b][0], qf[nt][b][1], qf[nt][b][2], qf[nt][b][3]);
+      }
+#pragma unroll
+      for (int u = 0; u < TT; ++u) {
         const uint32_t x0 = k0[u][b], x1 = k1[u][b], y0 = x0 >> 8, y1 = x1 >> 8;
         const float s0 = low_half(kp0[u][b]), s1 = low_half(kp1[u][b]);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float acc[4];
           mma_bf16(acc, x0 & 0x000f000fu, x1 & 0x000f000fu, x0 & 0x00f000f0u, x1 & 0x00f000f0u,
-                   qf[nt][b][0], qf[nt][b][1]);
+                   qb[nt].x, qb[nt].y);
           mma_bf16_add(acc, y0 & 0x000f000fu, y1 & 0x000f000fu, y0 & 0x00f000f0u,
-                       y1 & 0x00f000f0u, qf[nt][b][2], qf[nt][b][3]);
+                       y1 & 0x00f000f0u, qb[nt].z, qb[nt].w);
           tot[u][nt][0] = fmaf(acc[0], s0, tot[u][nt][0]);
           tot[u][nt][1] = fmaf(acc[1], s0, tot[u][nt][1]);
           tot[u][nt][2] = fmaf(acc[2], s1, tot[u][nt][2]);
@@ -889,6 +910,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
       }
     }
+    if constexpr (QSHARED) load_v();
     // ---------------- weights ----------------
     // As if all tokens counted, no reference had to move and all s were below 2^(1 + sx);
     // when that is not so, which is rare, they are made anew.
@@ -1099,7 +1121,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     }
 
     // ---------------- end of the segment, or of the CTA's part of it ----------------
-    const int hg = seg.y / sh.NRC, rc = seg.y - hg * sh.NRC, head = hg * sh.HG + h;
+    const int hg = seg.y / sh.NRC, rc = seg.y - hg * sh.NRC, head = hg * HG + h;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -1124,8 +1146,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     }
     // the head's warps, pairwise through shared memory
     constexpr int PER = NT * (8 * NB + 4);  // floats a lane: accumulators, sums, references
-    for (int d = 1; d < sh.WPH && ok; d <<= 1) {
-      const int pairs = sh.WPH / 2;
+    for (int d = 1; d < WPH && ok; d <<= 1) {
+      const int pairs = WPH / 2;
       float* slot = reinterpret_cast<float*>(smem + sh.scratch_at) +
                     (size_t)(h * pairs + sub / (2 * d)) * PER * 32 + lane;
       if (sub % (2 * d) == d) {
@@ -1142,7 +1164,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
       }
       join();
-      if (ok && sub % (2 * d) == 0 && sub + d < sh.WPH) {
+      if (ok && sub % (2 * d) == 0 && sub + d < WPH) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const float* p = slot + nt * (8 * NB + 4) * 32;
@@ -1190,7 +1212,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           if (lse && g == 0)
             lse[row] = l == 0.f ? kNegInf : (log2f(l) - nref[nt][j]) * 0.6931471805599453f;
         } else {
-          const int64_t slot = ((int64_t)2 * cta + (flags & kSecond ? 1 : 0)) * sh.HG * RC +
+          const int64_t slot = ((int64_t)2 * cta + (flags & kSecond ? 1 : 0)) * HG * RC +
                                h * RC + col;
           if (g == 0) part_ml[slot] = make_float2(-nref[nt][j], sum[nt][j]);
 #pragma unroll
@@ -1305,6 +1327,7 @@ int heads_of(int hkv) {
 struct Config {
   Q4Shape sh;
   int NT, PW;
+  bool fixed;  // SLICE is slice
   size_t smem;
 };
 
@@ -1327,7 +1350,8 @@ Config configure(const pks_q4_attention_args& a) {
   // eight query rows at a time, or sixteen
   cf.NT = sh.R > 8 ? 2 : 1;
   const int hg = heads_of(a.Hkv);
-  const int tiles = cf.NT == 2 ? 1 : 2;
+  const bool fixed = a.D == 128 && hg == 8;
+  const int tiles = cf.NT == 2 && !fixed ? 1 : 2;
   sh.HG = hg;
   sh.NHG = a.Hkv / hg;
   sh.NRC = (sh.R + 8 * cf.NT - 1) / (8 * cf.NT);
@@ -1356,17 +1380,19 @@ Config configure(const pks_q4_attention_args& a) {
   sh.order = chunks % 2 || sh.copies == kBoxes ? kOrderOdd : chunks % 4 == 2 ? kOrderTwo : kOrderFour;
   const int scratch = hg * (sh.WPH / 2) * cf.NT * (a.D / 4 + 4) * 32 * 4;
   const int nv = (4 * sh.Bv + 15) / 16 * 16, stage = 2 * sh.TS * sh.slice;
-  int n = (kSmemMax - 1024 - scratch - nv) / stage;
+  const int queries = cf.NT * tiles == 4 ? kConsumers * cf.NT * (a.D / 32) * 512 : 0;
+  const int n = (kSmemMax - 1024 - scratch - queries - nv) / stage;
   sh.stages = n > kMaxStages ? kMaxStages : n;
   // (at least four fit for every shape: a stage is 40 KiB at most.  With fewer a
   // producer could pass the barrier of a stage that is a whole round behind)
-  sh.ring = sh.stages * stage;
-  sh.scratch_at = sh.ring;
-  sh.nv_at = sh.ring + scratch;
+  sh.q_at = sh.stages * stage;
+  sh.scratch_at = sh.q_at + queries;
+  sh.nv_at = sh.scratch_at + scratch;
   cf.smem = (size_t)sh.nv_at + nv + 1024;
   sh.grid = device_sm_count();
   const int64_t most = (int64_t)sh.Bv * sh.NHG * sh.NRC * ((sh.k ? sh.k : sh.cap) / sh.TS + 1);
-  cf.PW = sh.copies == kTokens && most > (int64_t)kLongRun * sh.grid ? 8 : 4;
+  cf.PW = fixed && sh.copies == kTokens && most > (int64_t)kLongRun * sh.grid ? 8 : 4;
+  cf.fixed = fixed;
   return cf;
 }
 
@@ -1395,11 +1421,11 @@ cudaError_t pool_map(CUtensorMap* map, const void* pool, const Q4Shape& sh) {
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D, int NT, int TT, int PW>
+template <int D, int NT, int TT, int PW, int SLICE>
 cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const Config& cf,
                         cudaStream_t s) {
   static bool done[64] = {false};
-  auto kern = k_q4_attention<D, NT, TT, PW>;
+  auto kern = k_q4_attention<D, NT, TT, PW, SLICE>;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1436,12 +1462,17 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
                    out, a.lse, sh, 8 * NT);
 }
 
-template <int D>
+template <int NT>
 cudaError_t launch_rows(const pks_q4_attention_args& a, const Q4Layout& L, const Config& cf,
                         cudaStream_t s) {
-  if (cf.PW == 8)
-    return cf.NT == 2 ? launch_main<D, 2, 1, 8>(a, L, cf, s) : launch_main<D, 1, 2, 8>(a, L, cf, s);
-  return cf.NT == 2 ? launch_main<D, 2, 1, 4>(a, L, cf, s) : launch_main<D, 1, 2, 4>(a, L, cf, s);
+  constexpr int TT = NT == 2 ? 1 : 2;
+  if (cf.fixed) {
+    if (cf.sh.copies == kBoxes) return launch_main<128, NT, 2, 4, 640>(a, L, cf, s);
+    return cf.PW == 8 ? launch_main<128, NT, 2, 8, 656>(a, L, cf, s)
+                      : launch_main<128, NT, 2, 4, 656>(a, L, cf, s);
+  }
+  return a.D == 64 ? launch_main<64, NT, TT, 4, 0>(a, L, cf, s)
+                   : launch_main<128, NT, TT, 4, 0>(a, L, cf, s);
 }
 
 }  // namespace
@@ -1468,7 +1499,7 @@ Q4Layout q4_layout(const pks_q4_attention_args& a) {
 cudaError_t launch_q4_attention(const pks_q4_attention_args& a, const Q4Layout& L,
                                 cudaStream_t s) {
   const Config cf = configure(a);
-  return a.D == 64 ? launch_rows<64>(a, L, cf, s) : launch_rows<128>(a, L, cf, s);
+  return cf.NT == 2 ? launch_rows<2>(a, L, cf, s) : launch_rows<1>(a, L, cf, s);
 }
 
 }  // namespace pks
