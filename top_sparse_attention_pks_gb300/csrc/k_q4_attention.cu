@@ -1389,8 +1389,11 @@ Config configure(const pks_q4_attention_args& a) {
   sh.scratch_at = sh.q_at + queries;
   sh.nv_at = sh.scratch_at + scratch;
   cf.smem = (size_t)sh.nv_at + nv + 1024;
+  // no more CTAs than a full batch has stages
+  const int64_t most =
+      (int64_t)sh.Bv * sh.NHG * sh.NRC * (((sh.k ? sh.k : sh.cap) + sh.TS - 1) / sh.TS);
   sh.grid = device_sm_count();
-  const int64_t most = (int64_t)sh.Bv * sh.NHG * sh.NRC * ((sh.k ? sh.k : sh.cap) / sh.TS + 1);
+  if (most < sh.grid) sh.grid = most > 0 ? (int)most : 1;
   cf.PW = fixed && sh.copies == kTokens && most > (int64_t)kLongRun * sh.grid ? 8 : 4;
   cf.fixed = fixed;
   return cf;
@@ -1479,7 +1482,7 @@ cudaError_t launch_rows(const pks_q4_attention_args& a, const Q4Layout& L, const
 
 bool q4_supported(const pks_q4_attention_args& a) {
   const Q4Shape sh = configure(a).sh;  // the stages of a full batch are counted in 32 bits
-  const int64_t each = (sh.k ? sh.k : sh.cap) / sh.TS + 1;
+  const int64_t each = ((sh.k ? sh.k : sh.cap) + sh.TS - 1) / sh.TS;
   return each * sh.NHG * sh.NRC * sh.Bv <= INT32_MAX;
 }
 
