@@ -48,6 +48,15 @@ def test_selected_tokens(Hkv, G, D, page, k, holes, Nq):
     Batch(LENS, page, Hkv, G, D, Nq, seed=k).sparse(k, holes)
 
 
+@pytest.mark.parametrize("page", list(range(1, 20)) + [24, 40, 100])
+def test_pages_of_every_small_size(page):
+    """A stage of one head is 256 tokens: pages of 7 are 38 of them, more than a warp's lanes."""
+    lens = [255, 256, 257, 300, 511, 800]
+    Batch(lens, page, 1, 2, 128, seed=page).dense()
+    Batch(lens, page, 2, 2, 64, seed=page).dense()
+    Batch(lens, page, 4, 9, 128, 2, seed=page).dense(causal=True)
+
+
 def test_long_requests_split_over_all_sms():
     Batch([20000, 3, 0, 45011, 700], 64, 8, 8, 128, seed=1).dense()
     Batch([70001], 16, 1, 4, 128, seed=2).dense()

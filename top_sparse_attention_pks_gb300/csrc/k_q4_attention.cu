@@ -1364,8 +1364,12 @@ Config configure(const pks_q4_attention_args& a) {
   sh.row_bytes = q4::token_bytes(a.Hkv, a.D);
   sh.taken = sh.NHG == 1 ? sh.row_bytes : hg * q4::record_bytes(a.D);
   sh.unit = sh.taken % 16 ? 8 : 16;
+  // (kRuns: a lane a page of the stage, which begins in the middle of one unless it is
+  // whole pages long)
+  const int pages = sh.TS % a.page_size == 0 ? sh.TS / a.page_size
+                                             : (sh.TS - 2) / a.page_size + 2;
   const bool runs = !a.k && sh.NHG == 1 && sh.row_bytes % 128 != 0 && sh.row_bytes < kTokenBytes &&
-                    (int64_t)a.page_size * sh.row_bytes >= kBulkBytes;
+                    (int64_t)a.page_size * sh.row_bytes >= kBulkBytes && pages <= 32;
   for (sh.box = 32 < sh.TS ? 32 : sh.TS; a.page_size % sh.box;) sh.box /= 2;
   const bool boxes = !a.k && sh.row_bytes % 128 == 0 && sh.taken % 128 == 0 && sh.box >= 16;
   // (kTokens: two tokens a lane at most)
