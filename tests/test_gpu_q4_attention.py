@@ -1,6 +1,12 @@
 """Attention over a 4-bit cache, dense and over selected tokens, against the 64-bit
 restatement of q4_cases (which derives the tolerances)."""
 
+import os
+import subprocess
+import sys
+import threading
+from pathlib import Path
+
 import numpy as np
 import pytest
 import torch
@@ -180,6 +186,59 @@ def test_runs_give_the_same_bits():
     for _ in range(20):
         att()
         assert torch.equal(att.out, first) and torch.equal(att.lse, lse)
+
+
+def test_a_position_twice_counts_twice():
+    b = Batch([100, 40], 16, 2, 4, 64, seed=21)
+    lists = b.lists(30)
+    lists[0, 0, 10:20] = lists[0, 0, 5]
+    lists[1, 0, :] = 39
+    att = Q4SparseAttention(b.len_d, b.table, i32(lists), b.q, b.cache, lse=True)
+    b.check(att(), att.lse, lists=lists)
+
+
+def test_two_threads_and_streams():
+    """Objects of their own over one cache, each called from a thread on a stream of its own."""
+    b = Batch([3000, 700, 77], 16, 8, 4, 128, seed=22)
+    want = b.dense().out.clone()
+    atts = [Q4Attention(b.len_d, b.table, b.q, b.cache) for _ in range(2)]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def run(att, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(50):
+                    att.out.zero_()
+                    if not torch.equal(att(), want):
+                        wrong.append(att)
+        except BaseException as e:  # noqa: BLE001 (told below)
+            wrong.append(e)
+
+    threads = [threading.Thread(target=run, args=(a, torch.cuda.Stream())) for a in atts]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert all(a.device_error() == 0 for a in atts)
+
+
+def test_first_call_of_a_process_is_captured():
+    code = """
+import torch
+from q4_cases import Batch, Q4Attention
+b = Batch([300, 20], 16, 8, 4, 128, seed=23)
+att = Q4Attention(b.len_d, b.table, b.q, b.cache, lse=True)
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    att()
+g.replay()
+b.check(att.out, att.lse)
+"""
+    here = Path(__file__).parent
+    env = dict(os.environ, PYTHONPATH=os.pathsep.join([str(here), str(here.parent)]))
+    subprocess.run([sys.executable, "-c", code], env=env, check=True, timeout=300)
 
 
 def test_graphs_that_share_a_workspace_and_follow_lengths():

@@ -36,6 +36,7 @@ namespace pks {
 namespace {
 
 constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless wait_limit is set
+constexpr long long kLandCycles = 1LL << 26;  // for copies in flight to land, 30 ms
 constexpr int kConsumers = 8;  // warps, two a scheduler
 // Producer warps (PW): four, each filling every fourth stage; with kTokens teams of two, one
 // for K and one for V, of four warps or eight.  Eight keep up with long lists (256 x 1024
@@ -178,6 +179,9 @@ constexpr uint32_t kFirst = 1u << 16, kLast = 2u << 16, kWhole = 4u << 16, kSeco
                    kEdge = 16u << 16;
 // Registers a thread of this warpgroup has from here on.  All of a CTA's together no
 // more than it was launched with.
+constexpr int kConsumerRegisters = 208;
+template <int PW>
+constexpr int kProducerRegisters = PW == 8 ? 48 : 88;
 template <int N, bool MORE>
 __device__ __forceinline__ void set_registers() {
   if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -338,7 +342,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 
   if (warp >= NW) {
     // =========================== producers ===========================
-    set_registers<PW == 8 ? 48 : 88, false>();
+    set_registers<kProducerRegisters<PW>, false>();
     behind(seq_lens, block_table, lists);
     const int me = warp - NW;
     int* s_row = s_row_all[me & 3];
@@ -397,9 +401,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     const int stride = copies == kTokens ? PW / 2 : 4;
     const int mine_from = copies == kTokens ? me >> 1 : me;
     if (mine_from >= stride) return;
-    int stage = mine_from, round = 0;
+    int stage = mine_from, round = 0, i = mine_from;
     bool ok = true;
-    if (mine_from < count) forward(mine_from);
+    if (i < count) forward(i);
     if (copies == kTokens) {
       // ---- a token a lane (or two), K or V ----
       constexpr int PER = 2;
@@ -435,12 +439,12 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           else row[u] = page[u] * sh.page_size + slot[u];
         }
       };
-      if (mine_from < count) {
+      if (i < count) {
         tokens();
         pages();
         rows();
       }
-      for (int i = mine_from; i < count; i += stride) {
+      for (; i < count; i += stride) {
         const int4 seg = make_int4(v, c, tile << ts_log2, n);
         const uint32_t f = flags_of(i);
         const bool more = i + stride < count;
@@ -450,10 +454,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           tokens();
         }
         if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
-        if (!ok) {
-          next = i;
-          break;
-        }
+        if (!ok) break;
         if (more) pages();
         const uint32_t dst = ring + (uint32_t)(2 * stage + is_v) * half;
         StageNote* note = &s_note[stage];
@@ -489,7 +490,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
       }
     } else {
-      for (int i = mine_from; i < count; i += stride) {
+      for (; i < count; i += stride) {
         if (i != next) forward(i - next);
         const int p0 = tile << ts_log2, here = min(n - p0, TS);  // tokens in reach
         const int* table = block_table + (int64_t)request * sh.max_pages;
@@ -565,10 +566,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
         // ---- fill it
         if (round > 0) ok = wait(&bar_empty[stage], (round & 1) ^ 1);
-        if (!ok) {
-          next = i;
-          break;
-        }
+        if (!ok) break;
         const uint32_t dst_k = ring + (uint32_t)stage * 2 * half, dst_v = dst_k + half;
         StageNote* note = &s_note[stage];
         const uint32_t f = flags_of(i);
@@ -669,22 +667,20 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
       }
     }
-    if (!ok) {
-      give_up();
-      // the copies in flight land before the CTA gives its memory up
-      for (int i = next - stride; i >= 0 && i >= next - sh.stages; i -= stride) {
-        const int r = i / sh.stages;
-        const long long t0 = clock64();
-        while (!tc::mbar_try_wait(&bar_full[i - r * sh.stages], r & 1) &&
-               clock64() - t0 < kWaitCycles) {
-        }
+    if (!ok) give_up();
+    // this warp's copies in flight land before the CTA gives its memory up, whoever gave up
+    for (int j = i - stride; j >= 0 && j >= i - sh.stages; j -= stride) {
+      const int r = j / sh.stages;
+      const long long t0 = clock64();
+      while (!tc::mbar_try_wait(&bar_full[j - r * sh.stages], r & 1) &&
+             clock64() - t0 < kLandCycles) {
       }
     }
     return;
   }
 
   // =========================== consumers ===========================
-  set_registers<208, true>();
+  set_registers<kConsumerRegisters, true>();
   if (warp >= consumers) return;
   const int h = warp / WPH, sub = warp - h * WPH;
   const int g = lane >> 2, t = lane & 3;
@@ -1387,7 +1383,7 @@ Config configure(const pks_q4_attention_args& a) {
   const int queries = cf.NT * tiles == 4 ? kConsumers * cf.NT * (a.D / 32) * 512 : 0;
   const int n = (kSmemMax - 1024 - scratch - queries - nv) / stage;
   sh.stages = n > kMaxStages ? kMaxStages : n;
-  // (at least four fit for every shape: a stage is 40 KiB at most.  With fewer a
+  // (at least four fit for every shape: a stage is 44 KiB at most.  With fewer a
   // producer could pass the barrier of a stage that is a whole round behind)
   sh.q_at = sh.stages * stage;
   sh.scratch_at = sh.q_at + queries;
@@ -1438,6 +1434,12 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!done[dev]) {
+    // consumers wait for registers that the launch does not have
+    cudaFuncAttributes built;
+    if ((e = cudaFuncGetAttributes(&built, kern)) != cudaSuccess) return e;
+    if (kConsumers * kConsumerRegisters + PW * kProducerRegisters<PW> >
+        (kConsumers + PW) * built.numRegs)
+      return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
     if (e != cudaSuccess) return e;
     done[dev] = true;
