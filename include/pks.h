@@ -647,7 +647,8 @@ typedef struct pks_q4_rows_args {
                                   read by pks_q4_write, written by pks_q4_read */
   void* v;
   int64_t k_row, k_head;       /* values from one row, one head to the next; a multiple of */
-  int64_t v_row, v_head;       /* 16 bytes each */
+  int64_t v_row, v_head;       /* 16 bytes each, 0 or more; heads that pks_q4_read writes
+                                  share no values */
   void* pool_k;                /* device uint8 [num_pages, page_size, token_bytes], */
   void* pool_v;                /* 16-byte aligned */
   int32_t* error;              /* NULL, or a device int32: set to 1 (page id), 2 (starts) or 3
@@ -672,7 +673,8 @@ pks_status pks_q4_read(const pks_q4_rows_args* args, pks_stream stream);
  *  - pks_q4_attention: t < len_b, or with `causal` t < len_b - Nq + i + 1 (query
  *    token i stands at position len_b - Nq + i).
  *  - pks_q4_sparse_attention: the positions of topk_idx[b, i, :] holding a token
- *    (>= 0, each < len_b), in any order; -1 entries are skipped.
+ *    (>= 0, each < len_b), in any order; -1 entries are skipped, and a position
+ *    that stands there twice counts twice.
  * A query without tokens gets zeros.  Tokens that a query does not attend to are
  * without influence on it, whatever they hold. */
 typedef struct pks_q4_attention_args {

@@ -109,6 +109,26 @@ def test_write_and_read(dtype, Hkv, D, page, fused):
     assert cache.device_error() == 0
 
 
+def test_rows_of_any_strides():
+    """Heads before rows, one row for all, one head for all."""
+    lens, starts = [40, 3], [0, 40, 43]
+    table, N = layout(lens, 16, 9)
+    cache = Q4Cache(N, 16, 4, 64)
+    k, v = rows(43, 4, 64, torch.bfloat16, 10)
+    for a, b in ((k.transpose(0, 1).contiguous().transpose(0, 1), v), (k[:1].expand(43, 4, 64), v),
+                 (k, v[:, :1].expand(43, 4, 64))):
+        cache.write(a, b, i32(lens), i32(table), i32(starts))
+        check(cache, a, b, lens, table, starts)
+    out = torch.full((2, 4, 43, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    got = cache.read(i32(lens), i32(table), i32(starts), *out.transpose(1, 2))
+    same = torch.empty((2, 43, 4, 64), dtype=torch.bfloat16, device="cuda")
+    want = cache.read(i32(lens), i32(table), i32(starts), *same)
+    assert all(torch.equal(x, y) for x, y in zip(got, want))
+    with pytest.raises(pks.PksError):
+        cache.read(i32(lens), i32(table), i32(starts), k[:1].expand(43, 4, 64), v)
+    assert cache.device_error() == 0
+
+
 def test_prompts_of_many_rows():
     """More rows than blocks: blocks take eight rows at a time, more than once."""
     lens = [9000, 1, 4321, 0, 2777]

@@ -8,6 +8,7 @@ import torch
 
 import q4_reference as ref
 from top_sparse_attention_pks_gb300 import build, pks
+from top_sparse_attention_pks_gb300.decoder import Q4Cache
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -87,6 +88,19 @@ def test_rows_refused(change, want):
     for call in (pks.lib().pks_q4_write, pks.lib().pks_q4_read):
         assert call(ctypes.byref(rows(**change)), None) == want
         assert call(None, None) == -1
+
+
+@pytest.mark.parametrize("change", [
+    dict(k_row=0), dict(v_row=0), dict(k_head=0), dict(v_head=32), dict(k_row=64), dict(v_row=120),
+    dict(k_row=64, k_head=256), dict(v_row=32, v_head=1024)])
+def test_rows_to_read_into_share_no_values(change):
+    assert pks.lib().pks_q4_read(ctypes.byref(rows(**change)), None) == -1
+
+
+def test_cache_keeps_its_pools():
+    for name in ("k", "v", "error"):
+        with pytest.raises(AttributeError):
+            setattr(Q4Cache.__new__(Q4Cache), name, torch.zeros(1))
 
 
 def test_empty_calls_launch_nothing():

@@ -814,6 +814,18 @@ pks_status q4_check_pool(int B, int Hkv, int D, int page_size, int max_pages, in
   return PKS_OK;
 }
 
+// whether two heads of rows with these strides share values
+bool q4_overlaps(const pks_q4_rows_args& a, int64_t row, int64_t head) {
+  int64_t near = head, far = row, n = a.Hkv, m = a.n_rows;
+  if (m == 1 || (n > 1 && row < head)) {
+    std::swap(near, far);
+    std::swap(n, m);
+  }
+  // n of them `near` apart, m times
+  const int64_t reach = n > 1 ? (n - 1) * near + a.D : a.D;
+  return (n > 1 && near < a.D) || (m > 1 && far < reach);
+}
+
 pks_status q4_rows(const pks_q4_rows_args* a, bool write, pks_stream stream) {
   if (!a || a->n_rows < 0 || a->dtype < PKS_Q4_BF16 || a->dtype > PKS_Q4_FP32)
     return PKS_ERR_INVALID;
@@ -823,6 +835,8 @@ pks_status q4_rows(const pks_q4_rows_args* a, bool write, pks_stream stream) {
   for (int64_t x : {a->k_row, a->k_head, a->v_row, a->v_head})
     if (x < 0 || x % per16 != 0) return PKS_ERR_INVALID;
   if (a->B == 0 || a->n_rows == 0) return PKS_OK;
+  if (!write && (q4_overlaps(*a, a->k_row, a->k_head) || q4_overlaps(*a, a->v_row, a->v_head)))
+    return PKS_ERR_INVALID;
   if (!a->seq_lens || !a->block_table || !a->starts) return PKS_ERR_INVALID;
   for (const void* p : {(const void*)a->k, (const void*)a->v, (const void*)a->pool_k,
                         (const void*)a->pool_v})

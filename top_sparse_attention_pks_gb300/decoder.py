@@ -405,12 +405,17 @@ class Q4Cache:
             device = torch.device("cuda", torch.cuda.current_device())
         with pks._on_stream(stream):
             shape = (int(num_pages), int(page_size), row)
-            self.k = torch.zeros(shape, dtype=torch.uint8, device=device)
-            self.v = torch.zeros(shape, dtype=torch.uint8, device=device)
-            self.error = torch.zeros(1, dtype=torch.int32, device=device)
+            self._k = torch.zeros(shape, dtype=torch.uint8, device=device)
+            self._v = torch.zeros(shape, dtype=torch.uint8, device=device)
+            self._error = torch.zeros(1, dtype=torch.int32, device=device)
         self.Hkv, self.D = int(Hkv), int(D)
         pks._on_current_device(self.k)
         self._base = pks._q4_rows_base(self.k, self.v, Hkv, D, self.error)
+
+    # (read-only, as _base holds their addresses)
+    k = property(lambda self: self._k)
+    v = property(lambda self: self._v)
+    error = property(lambda self: self._error)
 
     def _args(self, k, v, seq_lens, block_table, starts):
         pks._on_current_device(self.k, k, v, seq_lens, block_table, starts)
