@@ -3,11 +3,17 @@
 // A block takes some rows, finds their places in the pool once, and then all their K and V
 // records, a warp (or several, when rows are few) a row.
 //  - Writing, a lane has a whole group of 32 values: what is worked out once a group
-//    (minimum, scale, reciprocal) is most of the work when four lanes share one.
-//  - Reading, a lane has eight values, 16 bytes of a row of two-byte values, so that stores
-//    are whole sectors.
+//    (minimum, scale, reciprocal) is most of the work when four lanes share one (131,072
+//    rows written and read back 492 -> 309 us).  The rest is two values at once where
+//    fp32 pairs allow it (a fifth fewer instructions, the same 253 -> 246 us).
+//  - Reading, a lane has a quarter of every group: one 16-byte load of codes, one of scales,
+//    and a store of 16 bytes (of a two-byte type) a group, four lanes 64 bytes side by side.
+//    Two records at once; one or four: 265 and 261 us for the same 253.
 //
-// Bound by memory: a bf16 row of D = 128 is 256 bytes in and 80 out.
+// Bound by memory: a bf16 row of D = 128 is 256 bytes in and 80 out, and four instructions in
+// five still are arithmetic.  Rows of eight heads of 128 in bf16: 131,072 written and read
+// back 239 us (6.0 TB/s), 154,000 read 138 us (6.0 TB/s).  More blocks an SM by fewer registers
+// are slower (48 registers: by 1%, 40: by 8%).
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -33,6 +39,31 @@ __device__ __forceinline__ float min_nan(float a, float b) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// two fp32 values in one register pair
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float first(uint64_t x) { return __uint_as_float((uint32_t)x); }
+__device__ __forceinline__ float second(uint64_t x) { return __uint_as_float((uint32_t)(x >> 32)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// 1 from the border on, else 0
+__device__ __forceinline__ float from_on(float x, float border) {
+  float r;
+  asm("set.ge.f32.f32 %0, %1, %2;" : "=f"(r) : "f"(x), "f"(border));
   return r;
 }
 
@@ -160,15 +191,18 @@ __device__ __forceinline__ Scale scale_of(float lo, float hi) {
 }
 // codes of eight values, the first in the lowest bits
 __device__ __forceinline__ uint32_t codes(const float (&x)[8], const Scale& g) {
+  const uint64_t from = two(-g.from, -g.from), inv = two(g.inv, g.inv),
+                 guess = two(g.guess, g.guess), scale = two(g.s, g.s), half = two(g.first, g.first),
+                 magic = two(12582912.f, 12582912.f), back = two(-12582912.f, -12582912.f);
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; --i) {
-    const float xa = x[i] - g.from;
-    const float r = __fmaf_rn(xa, g.inv, g.guess) + 12582912.f;  // to the nearest whole number
-    const float border = __fmaf_rn(r - 12582912.f, g.s, g.first);
-    uint32_t above;  // all ones from the border on
-    asm("set.ge.u32.f32 %0, %1, %2;" : "=r"(above) : "f"(xa), "f"(border));
-    w = w * 16 + (__float_as_uint(r) - above);
+  for (int i = 6; i >= 0; i -= 2) {
+    const uint64_t xa = add2(two(x[i], x[i + 1]), from);
+    const uint64_t r = add2(fma2(xa, inv, guess), magic);  // to the nearest whole number
+    const uint64_t border = fma2(add2(r, back), scale, half);
+    const uint64_t n = add2(r, two(from_on(first(xa), first(border)),
+                                   from_on(second(xa), second(border))));
+    w = (w * 16 + __float_as_uint(second(n))) * 16 + __float_as_uint(first(n));
   }
   return g.flat ? 0 : w - kMagicSum;
 }
@@ -205,6 +239,28 @@ __device__ __forceinline__ int place_of(int i, const int32_t* starts, int B,
   return at;
 }
 
+// d = a b + c, a and b halves, rounded once
+__device__ __forceinline__ float fma_mixed(uint16_t a, uint16_t b, float c) {
+  float d;
+  asm("fma.rn.f32.f16 %0, %1, %2, %3;" : "=f"(d) : "h"(a), "h"(b), "f"(c));
+  return d;
+}
+// a word a group
+__device__ __forceinline__ void group_words(const uint8_t* at, bool on, uint32_t (&w)[4]) {
+  const uint4 x = on ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+  w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+}
+__device__ __forceinline__ void group_words(const uint8_t* at, bool on, uint32_t (&w)[2]) {
+  const uint2 x = on ? *reinterpret_cast<const uint2*>(at) : make_uint2(0, 0);
+  w[0] = x.x, w[1] = x.y;
+}
+
+// Lanes of a record, and records of a lane at once
+template <int D, bool WRITE>
+constexpr int kLanes = WRITE ? D / q4::kGroup : 4;
+template <bool WRITE>
+constexpr int kAtOnce = WRITE ? 1 : 2;
+
 struct RowShape {
   int B, n_rows, Hkv, page_size, max_pages, num_pages;
   int warps;          // a row: 1 to 8, a power of two
@@ -220,8 +276,8 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
           uint8_t* __restrict__ pool_k, uint8_t* __restrict__ pool_v, int32_t* error,
           RowShape sh) {
   constexpr int NB = D / q4::kGroup, REC = q4::record_bytes(D);
-  constexpr int LANES = WRITE ? NB : D / 8, AT_ONCE = 32 / LANES;  // records of a warp
-  constexpr int U = WRITE ? 1 : 4;                                // of a lane at once
+  constexpr int LANES = kLanes<D, WRITE>, AT_ONCE = 32 / LANES;  // records of a warp
+  constexpr int U = kAtOnce<WRITE>;                                  // of a lane
   extern __shared__ int32_t s_starts[];
   __shared__ int s_place[kRowWarps * kRowsEach];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -300,34 +356,43 @@ k_q4_rows(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__ bloc
             reinterpret_cast<uint32_t*>(rec[0] + D / 2)[b] = g.pair;
           }
         } else {
-          const int l = lane & (LANES - 1), b = l >> 2, t = l & 3;
-          const bool odd = b & 1;
-          uint32_t w[U], sm[U];
+          const int t = lane & 3;
+          uint32_t code[U][NB], sm[U][NB];
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            // K: word t NB + b; V: of chunk 2 t (even b) or 2 t + 1 (odd b), the halves of
-            // groups b & ~1 and b | 1
-            const int at_word = is_v[u] ? (2 * t + odd) * (NB / 2) + (b >> 1) : t * NB + b;
-            w[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u])[at_word] : 0;
-            sm[u] = on[u] ? reinterpret_cast<const uint32_t*>(rec[u] + D / 2)[b] : 0;
+            group_words(rec[u] + 4 * NB * t, on[u], code[u]);
+            group_words(rec[u] + D / 2, on[u], sm[u]);
           }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
-            const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? w[u] & 0xffffu : w[u] >> 16, 4);
-            if (is_v[u]) w[u] = odd ? got | (w[u] & 0xffff0000u) : (w[u] & 0xffffu) | got << 16;
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&sm[u]));
-            float x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float n = __uint_as_float((w[u] >> (4 * i) & 15u) | 0x4b000000u) - 8388608.f;
-              x[i] = __fmaf_rn(n, f.x, f.y);
+            for (int b = 0; b < NB; ++b) {
+              // K: word t NB + b; V: 16-bit words (2 t) NB + b and (2 t + 1) NB + b
+              uint32_t w = code[u][b];
+              if (is_v[u])
+                w = __byte_perm(code[u][b / 2], code[u][(NB + b) / 2], b & 1 ? 0x7632 : 0x5410);
+              const uint16_t scale = (uint16_t)sm[u][b];
+              const float least = __half2float(__ushort_as_half((uint16_t)(sm[u][b] >> 16)));
+              // codes i and i + 4 as halves: 1024 + n or 1024 + 16 n, whose bits a mask gives
+              float x[8];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t y = ((i & 2 ? w >> 8 : w) & (i & 1 ? 0x00f000f0u : 0x000f000fu)) |
+                                   0x64006400u;
+                const __half2 h = *reinterpret_cast<const __half2*>(&y);
+                const __half2 n = i & 1 ? __hfma2(h, __float2half2_rn(0.0625f),
+                                                  __float2half2_rn(-64.f))
+                                        : __hadd2(h, __float2half2_rn(-1024.f));
+                x[i] = fma_mixed(__half_as_ushort(__low2half(n)), scale, least);
+                x[i + 4] = fma_mixed(__half_as_ushort(__high2half(n)), scale, least);
+              }
+              Eight<T> o;
+              pack(x, o);
+              if (on[u])
+#pragma unroll
+                for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+                  reinterpret_cast<uint4*>(values[u] + 32 * b + 8 * t)[i] = o.w[i];
             }
-            Eight<T> o;
-            pack(x, o);
-            if (on[u])
-#pragma unroll
-              for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-                reinterpret_cast<uint4*>(values[u] + 8 * l)[i] = o.w[i];
           }
         }
       }
@@ -351,7 +416,7 @@ cudaError_t launch(const pks_q4_rows_args& a, cudaStream_t s) {
   sh.v_head = a.v_head;
   // few rows: as many warps a row as have work, so that they run side by side
   const int most = device_sm_count() * (2048 / kRowThreads);
-  const int each = 32 / (WRITE ? D / q4::kGroup : D / 8) * (WRITE ? 1 : 4);
+  const int each = 32 / kLanes<D, WRITE> * kAtOnce<WRITE>;
   sh.warps = 1;
   while (sh.warps < kRowWarps && sh.warps * each < 2 * a.Hkv &&
          (int64_t)a.n_rows * sh.warps < (int64_t)most * kRowWarps / 2)
