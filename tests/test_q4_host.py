@@ -131,6 +131,18 @@ def test_step_refused(which, change, want):
     assert pks.lib().pks_q4_decode_step(ctypes.byref(s), None, None) == -1
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Nq", [(4096, 1), (64, 64), (1, 3)])
+def test_all_heads_fit(D, B, Nq):
+    """Every number of heads leaves the ring of stages its least length in shared memory."""
+    for Hkv in list(range(1, 34)) + [40, 64, 127, 1024]:
+        for G in (1, 3, 16) if Hkv <= 64 else (1,):
+            for k in (0, 9):
+                for page in (1, 7, 16, 64):
+                    a = attention(B=B, Hkv=Hkv, Hq=Hkv * G, D=D, n_queries=Nq, k=k, page_size=page)
+                    assert pks.pks_q4_workspace_size(a) > 0
+
+
 def test_workspace_grows_with_the_rows():
     sizes = [pks.pks_q4_workspace_size(attention(Hq=g * 2)) for g in (4, 8, 16)]
     assert 0 < sizes[0] == sizes[1] < sizes[2]

@@ -44,6 +44,7 @@ constexpr int kConsumers = 8;  // warps, two a scheduler
 constexpr int kLongRun = 12;   // stages a CTA from which on there are eight
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
+constexpr int kLeastStages = 4;  // with fewer a producer could pass a barrier a round behind
 constexpr int kSmemMax = 227 * 1024 - 6144;  // dynamic; the rest is the static part
 constexpr int kBulkBytes = 512;    // of a page, from which on its runs are copied whole,
 constexpr int kTokenBytes = 512;   // rows smaller than this, that is
@@ -1383,8 +1384,7 @@ Config configure(const pks_q4_attention_args& a) {
   const int queries = cf.NT * tiles == 4 ? kConsumers * cf.NT * (a.D / 32) * 512 : 0;
   const int n = (kSmemMax - 1024 - scratch - queries - nv) / stage;
   sh.stages = n > kMaxStages ? kMaxStages : n;
-  // (at least four fit for every shape: a stage is 44 KiB at most.  With fewer a
-  // producer could pass the barrier of a stage that is a whole round behind)
+  // (kLeastStages fit for every shape: a stage is 44 KiB at most)
   sh.q_at = sh.stages * stage;
   sh.scratch_at = sh.q_at + queries;
   sh.nv_at = sh.scratch_at + scratch;
@@ -1489,7 +1489,7 @@ cudaError_t launch_rows(const pks_q4_attention_args& a, const Q4Layout& L, const
 bool q4_supported(const pks_q4_attention_args& a) {
   const Q4Shape sh = configure(a).sh;  // the stages of a full batch are counted in 32 bits
   const int64_t each = ((sh.k ? sh.k : sh.cap) + sh.TS - 1) / sh.TS;
-  return each * sh.NHG * sh.NRC * sh.Bv <= INT32_MAX;
+  return each * sh.NHG * sh.NRC * sh.Bv <= INT32_MAX && sh.stages >= kLeastStages;
 }
 
 Q4Layout q4_layout(const pks_q4_attention_args& a) {
