@@ -19,10 +19,20 @@
 // Maxima, sums, scores and accumulators are fp32.
 //
 // One persistent CTA an SM.  All (request, head group, row chunk) segments are cut into
-// stages of 16 tokens a consumer warp; the CTAs take equal runs of stages.  Four
-// producer warps, each for every fourth stage, find the tokens' rows and fill a ring of
-// stages; a consumer warp owns one head and some tokens of every stage.  Segments that several CTAs hold parts of are
-// joined by k_q4_merge.
+// stages of 16 or 32 tokens a consumer warp; the CTAs take equal runs of stages.  Producer
+// warps find the tokens' rows and fill a ring of stages, each in its turn; a consumer
+// warp owns one head and some tokens of every stage and keeps the head's sums in registers.
+// Segments that several CTAs hold parts of are joined by k_q4_merge.
+//
+// Bound by memory where the tokens are many (16 x 131072 tokens of eight heads of 128, eight
+// queries a head: 416 us, 6.5 TB/s of codes), else by what the consumers issue: a head's 32
+// tokens take 1980 cycles from L2 (2970 with sixteen queries a head), of which the tensor
+// pipe is busy for a third and the integer pipe, which takes the codes apart, for half.
+// Measured against it:
+//  - sixteen consumer warps of half the registers, queries in shared memory: 468 us for 434;
+//  - one warp a head for scores and one for values: 569 for 456;
+//  - one tile of 16 tokens at a time: 593 for 468;
+//  - consumers of 200 registers: 462 for 450.
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -39,17 +49,20 @@ constexpr long long kWaitCycles = 4000000000LL;  // about 2 s at 2 GHz, unless w
 constexpr long long kLandCycles = 1LL << 26;  // for copies in flight to land, 30 ms
 constexpr int kConsumers = 8;  // warps, two a scheduler
 // Producer warps (PW): four, each filling every fourth stage; with kTokens teams of two, one
-// for K and one for V, of four warps or eight.  Eight keep up with long lists (256 x 1024
-// selected tokens 104 -> 90 us), four start sooner (16 x 2048 tokens 32 us, 34 with eight).
-constexpr int kLongRun = 12;   // stages a CTA from which on there are eight
+// for K and one for V, of four warps or eight.  Eight keep up with long lists, four start
+// sooner.  Selected tokens, four warps and eight: 7 stages a CTA 30 and 32 us, 13 40 and
+// 42, 20 50 both, 27 67 and 65, 54 95 and 89, 108 163 and 144.
+constexpr int kLongRun = 24;  // stages a CTA above which there are eight
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
 constexpr int kLeastStages = 4;  // with fewer a producer could pass a barrier a round behind
 constexpr int kSmemMax = 227 * 1024 - 6144;  // dynamic; the rest is the static part
-constexpr int kBulkBytes = 512;    // of a page, from which on its runs are copied whole,
-constexpr int kTokenBytes = 512;   // rows smaller than this, that is
+// Rows from here on may go by kTokens.  64 lists of 1024 tokens, by kTokens and by kLanes:
+// rows of 160 bytes 32 and 32 us, 240 38 and 36, 320 40 and 44, 480 42 and 46.
 constexpr int kTokenBytesLeast = 320;
-constexpr int kFewRows = 4096;    // up to which a block joins a row, else a warp
+// Output rows up to which a block of k_q4_merge joins one, else a warp: 64 rows 61 us and
+// 112, 1024 85 and 89, 2048 58.5 both, 3072 77 and 73, 16384 75 and 56.
+constexpr int kFewRows = 2048;
 constexpr float kNone = -3e38f;  // reference of a row that has seen no token
 
 // Tokens of a warp's 16 as the rows of its MMA tiles, four bits each (lowest: row 0).
@@ -62,8 +75,10 @@ constexpr uint64_t kOrderTwo = 0xdfceb9a857463120ull;
 constexpr uint64_t kOrderFour = 0xefdcab9867542310ull;
 
 // How a stage gets its tokens:
-//  kRuns   - dense, all heads of small rows: the tokens of one page by one bulk copy (a
-//            warp issues one in 63 cycles, so that pieces below 2 KiB do not keep up)
+//  kRuns   - dense, all heads: the tokens of one page by one bulk copy.  For any page that
+//            leaves a stage no more than 32 of them: 16 x 16384 tokens of 80 bytes 34 us, 42
+//            by kLanes, whatever the page; of 400 bytes 79 us, 87 by kTokens, and 81 and
+//            87 on pages of two
 //  kTokens - rows of 320 bytes or more: a bulk copy a token, at a distance in shared
 //            memory that suits the banks; two warps a stage, one for K and one for V
 //            (four warps: 7.3 TB/s of rows of 640 bytes, 6.3 of 320, 1.7 of 80)
@@ -100,18 +115,18 @@ struct Q4Shape {
 #define PKS_MMA(NAME, TYPE)                                                                      \
   __device__ __forceinline__ void NAME(float(&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,      \
                                        uint32_t a3, uint32_t b0, uint32_t b1) {                  \
-    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
-                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"              \
-                 : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                \
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));              \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                   \
+        ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"              \
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])                                         \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));                       \
   }                                                                                              \
   __device__ __forceinline__ void NAME##_add(float(&d)[4], uint32_t a0, uint32_t a1,             \
                                              uint32_t a2, uint32_t a3, uint32_t b0,              \
                                              uint32_t b1) {                                      \
-    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                          \
-                 ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"                  \
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                \
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                        \
+    asm("mma.sync.aligned.m16n8k16.row.col.f32." TYPE "." TYPE                                   \
+        ".f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"                  \
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])                                         \
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));                                 \
   }
 PKS_MMA(mma_bf16, "bf16")
 PKS_MMA(mma_f16, "f16")
@@ -174,10 +189,9 @@ struct alignas(16) StageNote {
   int v, c, p0, nv;  // segment (request or list, chunk), first position, positions in all
   uint32_t mask[16];
 };
-// kFirst, kLast: the CTA's first and last stage of the segment; kWhole: it has all of them;
-// kSecond: not the CTA's first segment; kEdge: some token lies beyond some query's limit
-constexpr uint32_t kFirst = 1u << 16, kLast = 2u << 16, kWhole = 4u << 16, kSecond = 8u << 16,
-                   kEdge = 16u << 16;
+// kLast: the CTA's last stage of the segment; kWhole: it has all of them; kSecond: not
+// the CTA's first segment; kEdge: some token lies beyond some query's limit
+constexpr uint32_t kLast = 1u << 16, kWhole = 2u << 16, kSecond = 4u << 16, kEdge = 8u << 16;
 // Registers a thread of this warpgroup has from here on.  All of a CTA's together no
 // more than it was launched with.
 constexpr int kConsumerRegisters = 208;
@@ -383,7 +397,6 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     };
     auto flags_of = [&](int i) -> uint32_t {
       uint32_t f = 0;
-      if (tile == 0 || i == 0) f |= kFirst;
       if (tile == T - 1 || i == count - 1) f |= kLast;
       if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
       if (seg_at > lo) f |= kSecond;
@@ -1348,6 +1361,8 @@ Config configure(const pks_q4_attention_args& a) {
   cf.NT = sh.R > 8 ? 2 : 1;
   const int hg = heads_of(a.Hkv);
   const bool fixed = a.D == 128 && hg == 8;
+  // tokens 32 at a time, or 16 where sixteen rows and unknown distances leave no registers
+  // (32 with queries in shared memory: four drafted tokens 124 -> 113 us)
   const int tiles = cf.NT == 2 && !fixed ? 1 : 2;
   sh.HG = hg;
   sh.NHG = a.Hkv / hg;
@@ -1365,8 +1380,7 @@ Config configure(const pks_q4_attention_args& a) {
   // whole pages long)
   const int pages = sh.TS % a.page_size == 0 ? sh.TS / a.page_size
                                              : (sh.TS - 2) / a.page_size + 2;
-  const bool runs = !a.k && sh.NHG == 1 && sh.row_bytes % 128 != 0 && sh.row_bytes < kTokenBytes &&
-                    (int64_t)a.page_size * sh.row_bytes >= kBulkBytes && pages <= 32;
+  const bool runs = !a.k && sh.NHG == 1 && sh.row_bytes % 128 != 0 && pages <= 32;
   for (sh.box = 32 < sh.TS ? 32 : sh.TS; a.page_size % sh.box;) sh.box /= 2;
   const bool boxes = !a.k && sh.row_bytes % 128 == 0 && sh.taken % 128 == 0 && sh.box >= 16;
   // (kTokens: two tokens a lane at most)
@@ -1378,7 +1392,9 @@ Config configure(const pks_q4_attention_args& a) {
   if ((sh.copies == kTokens || sh.copies == kLanes) && sh.slice % 32 == 0) sh.slice += 16;
   const int units = sh.taken / sh.unit, chunks = sh.slice / 16;
   for (sh.lanes = 1; sh.lanes < units && sh.lanes < 32;) sh.lanes *= 2;
-  sh.order = chunks % 2 || sh.copies == kBoxes ? kOrderOdd : chunks % 4 == 2 ? kOrderTwo : kOrderFour;
+  sh.order = chunks % 2 || sh.copies == kBoxes ? kOrderOdd
+             : chunks % 4 == 2                 ? kOrderTwo
+                                               : kOrderFour;
   const int scratch = hg * (sh.WPH / 2) * cf.NT * (a.D / 4 + 4) * 32 * 4;
   const int nv = (4 * sh.Bv + 15) / 16 * 16, stage = 2 * sh.TS * sh.slice;
   const int queries = cf.NT * tiles == 4 ? kConsumers * cf.NT * (a.D / 32) * 512 : 0;
