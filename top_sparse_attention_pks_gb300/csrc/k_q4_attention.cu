@@ -9,10 +9,13 @@
 //  - The bit pattern of n in a 16-bit word is the subnormal bf16 n 2^-133 (and fp16
 //    n 2^-24), one step up 16 n of it: eight codes become four operand registers
 //    with four ANDs and a shift, and no conversion.  Powers of two are put right in
-//    the queries (those at the odd places are a sixteenth) and at the end.
+//    the queries (those at the odd places are a sixteenth) and at the end.  Of V two
+//    registers in four even go without the AND: a byte of two codes is n + 16 n' of
+//    them, and n's sum is taken off at the end (integer pipe: 16 x 131072 tokens 433 -> 420 us).
 //  - K: bf16, the queries scaled by a power of two, so that all products are exact.
-//    Each group's sum is scaled by s_b on its own (fp32); the m_b Q_b of all groups are
-//    one more MMA, Q_b cut into three fp16 pieces (33 bits).
+//    Each group's sum is scaled by s_b on its own (fp32); the m_b Q_b of two groups are
+//    one more MMA, with the (s, m) pairs as they lie against 0 and Q_b, which is cut into
+//    three fp16 pieces (33 bits), one a lane (m taken out of the pairs: 420 us for 413).
 //  - V: fp16.  p s is rounded to fp16 once a group (by 2^-11 of it at most; p itself
 //    likewise); p is kept at 2^11 to 2^14 at the largest score so that small ones stay
 //    normal numbers, lower where an s is 2 or more.  sum p m is one more MMA.
@@ -25,8 +28,8 @@
 // Segments that several CTAs hold parts of are joined by k_q4_merge.
 //
 // Bound by memory where the tokens are many (16 x 131072 tokens of eight heads of 128, eight
-// queries a head: 416 us, 6.5 TB/s of codes), else by what the consumers issue: a head's 32
-// tokens take 1980 cycles from L2 (2970 with sixteen queries a head), of which the tensor
+// queries a head: 397 us, 6.8 TB/s of codes), else by what the consumers issue: a head's 32
+// tokens take 1870 cycles from L2 (2780 with sixteen queries a head), of which the tensor
 // pipe is busy for a third and the integer pipe, which takes the codes apart, for half.
 // Measured against it:
 //  - sixteen consumer warps of half the registers, queries in shared memory: 468 us for 434;
@@ -722,7 +725,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 
   // queries as B operands, in shared memory where registers are short; the pieces of their sums
   constexpr bool QSHARED = NT * TT == 4;
-  uint32_t qf[QSHARED ? 1 : NT][NB][4], qs[NT][2];
+  uint32_t qf[QSHARED ? 1 : NT][NB][4], qs[NT][NB];
   uint4* q_shared = reinterpret_cast<uint4*>(smem + sh.q_at) + warp * NT * NB * 32 + lane;
   // of columns 2t, 2t + 1: scale of the scores, minus the reference, sum of weights
   float cs[NT][2], nref[NT][2], sum[NT][2];
@@ -818,8 +821,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           const __half h2 = __float2half_rn(r1 - __half2float(h1));
           piece[b] = t == 3 ? 0 : __half_as_ushort(t == 0 ? h0 : t == 1 ? h1 : h2);
         }
-        qs[nt][0] = piece[0] | piece[1] << 16;
-        qs[nt][1] = NB == 4 ? piece[NB - 2] | piece[NB - 1] << 16 : 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) qs[nt][b] = piece[b] << 16;
         // scores in powers of two
         const float mine_c = __int_as_float((127 + min(6 + e2, 128)) << 23) * scale_log2;
 #pragma unroll
@@ -885,14 +888,12 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     float tot[TT][NT][4];
 #pragma unroll
     for (int u = 0; u < TT; ++u) {
-      // the minima: slots 2t, 2t + 1 groups 0 and 1, slots 2t + 8, 2t + 9 groups 2 and 3, the
-      // lanes' t telling the pieces apart
-      const uint32_t a0 = __byte_perm(kp0[u][0], kp0[u][1], 0x7632);
-      const uint32_t a1 = __byte_perm(kp1[u][0], kp1[u][1], 0x7632);
-      const uint32_t a2 = NB == 4 ? __byte_perm(kp0[u][NB - 2], kp0[u][NB - 1], 0x7632) : 0;
-      const uint32_t a3 = NB == 4 ? __byte_perm(kp1[u][NB - 2], kp1[u][NB - 1], 0x7632) : 0;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_f16(tot[u][nt], a0, a1, a2, a3, qs[nt][0], qs[nt][1]);
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_f16(tot[u][nt], kp0[u][0], kp1[u][0], kp0[u][1], kp1[u][1], qs[nt][0], qs[nt][1]);
+        if constexpr (NB == 4)
+          mma_f16_add(tot[u][nt], kp0[u][2], kp1[u][2], kp0[u][3], kp1[u][3], qs[nt][2], qs[nt][3]);
+      }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -1091,7 +1092,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         const uint32_t sel = b & 1 ? 0x7632 : 0x5410;
         const uint32_t x01 = __byte_perm(w[u][0][b / 2], w[u][1][b / 2], sel);
         const uint32_t x23 = __byte_perm(w[u][2][b / 2], w[u][3][b / 2], sel);
-        const uint32_t y01 = x01 >> 8, y23 = x23 >> 8;
+        const uint32_t y01 = __byte_perm(x01, 0, 0x4341), y23 = __byte_perm(x23, 0, 0x4341);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const uint32_t b0 = half2_bits(__hmul2(bits_half2(pt0[u][nt]), bits_half2(s01[u][b])));
@@ -1099,13 +1100,11 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           if (u == 0) {
             mma_f16(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
                     x23 & 0x00f000f0u, b0, b1);
-            mma_f16(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
-                    y23 & 0x00f000f0u, b0, b1);
+            mma_f16(acc[nt][1], y01 & 0x000f000fu, y01, y23 & 0x000f000fu, y23, b0, b1);
           } else {
             mma_f16_add(acc[nt][0], x01 & 0x000f000fu, x01 & 0x00f000f0u, x23 & 0x000f000fu,
                         x23 & 0x00f000f0u, b0, b1);
-            mma_f16_add(acc[nt][1], y01 & 0x000f000fu, y01 & 0x00f000f0u, y23 & 0x000f000fu,
-                        y23 & 0x00f000f0u, b0, b1);
+            mma_f16_add(acc[nt][1], y01 & 0x000f000fu, y01, y23 & 0x000f000fu, y23, b0, b1);
           }
         }
       }
@@ -1140,13 +1139,18 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         for (int d = 4; d < 32; d <<= 1)
           sum[nt][j] += __shfl_xor_sync(0xffffffffu, sum[nt][j], d);
       }
-      // the codes' units, 2^-24 and (values 1 and 3 of four) 2^-20; plus sum p m
+      // the codes' units, 2^-24 and (values 1 and 3 of four) 2^-20, value 3 without value 2,
+      // which its byte held too; plus sum p m
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         const float m0 = __shfl_sync(0xffffffffu, om[nt][0], 4 * b + t);
         const float m1 = __shfl_sync(0xffffffffu, om[nt][1], 4 * b + t);
 #pragma unroll
         for (int m = 0; m < 2; ++m) {
+          if (m) {
+            o[nt][b][m][2] -= o[nt][b][m][0];
+            o[nt][b][m][3] -= o[nt][b][m][1];
+          }
           o[nt][b][m][0] = fmaf(o[nt][b][m][0], 16777216.f, m0);
           o[nt][b][m][1] = fmaf(o[nt][b][m][1], 16777216.f, m1);
           o[nt][b][m][2] = fmaf(o[nt][b][m][2], 1048576.f, m0);
