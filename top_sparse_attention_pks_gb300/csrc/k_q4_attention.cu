@@ -56,6 +56,10 @@ constexpr int kConsumers = 8;  // warps, two a scheduler
 // sooner.  Selected tokens, four warps and eight: 7 stages a CTA 30 and 32 us, 13 40 and
 // 42, 20 50 both, 27 67 and 65, 54 95 and 89, 108 163 and 144.
 constexpr int kLongRun = 24;  // stages a CTA above which there are eight
+// Stages up to which a CTA has a segment to itself, without a plan and parts to join: four, and
+// one more for every sixteen segments.  5 requests of 2 stages 6.8 us and 8.5 split, of 4 8.9
+// and 8.6, of 6 10.6 and 8.6; 16 of 4 9.2 and 10.3, of 8 12.6 and 12.0; 64 lists of 8 14.0 and 19.3.
+constexpr int kWholeStages = 4, kWholeMore = 16;
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
 constexpr int kLeastStages = 4;  // with fewer a producer could pass a barrier a round behind
@@ -111,6 +115,7 @@ struct Q4Shape {
   int lanes;         // kLanes: that copy a token, a unit or two each
   uint64_t order;
   int stages, q_at, scratch_at, nv_at;  // of the ring; where what lies behind it begins
+  int whole;  // a CTA has a segment to itself (no parts to join)
   int grid;
 };
 
@@ -193,8 +198,10 @@ struct alignas(16) StageNote {
   uint32_t mask[16];
 };
 // kLast: the CTA's last stage of the segment; kWhole: it has all of them; kSecond: not
-// the CTA's first segment; kEdge: some token lies beyond some query's limit
-constexpr uint32_t kLast = 1u << 16, kWhole = 2u << 16, kSecond = 4u << 16, kEdge = 8u << 16;
+// the CTA's first segment; kEdge: some token lies beyond some query's limit; kEnd: the
+// CTA's last stage
+constexpr uint32_t kLast = 1u << 16, kWhole = 2u << 16, kSecond = 4u << 16, kEdge = 8u << 16,
+                   kEnd = 16u << 16;
 // Registers a thread of this warpgroup has from here on.  All of a CTA's together no
 // more than it was launched with.
 constexpr int kConsumerRegisters = 208;
@@ -255,7 +262,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
   __shared__ int s_row_all[4][kMaxTokens];  // tokens' rows in the pool (-1: none)
-  __shared__ int s_warp[NWARPS], s_first, s_rest, s_abort;
+  __shared__ int s_warp[NWARPS], s_first, s_rest, s_lo, s_count, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* smem = smem_raw + (ring - tc::smem_u32(smem_raw));
@@ -285,12 +292,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   pdl_launch_dependents();
 
   // ---- the stages of every segment, and this CTA's run of them ----
-  const int per = (sh.Bv + NTHREADS - 1) / NTHREADS, v_lo = min(tid * per, sh.Bv),
-            v_hi = min(v_lo + per, sh.Bv);
-  const int chunks = sh.NHG * sh.NRC;
+  const int chunks = sh.NHG * sh.NRC, cta = blockIdx.x;
   auto stages_of = [&](int n) { return (n + TS - 1) >> ts_log2; };
-  int mine = 0;
-  for (int v = v_lo; v < v_hi; ++v) {
+  auto tokens_of = [&](int v) {
     int n = seq_lens[sh.lists == 1 ? v : v / sh.lists];
     if (n < 0 || n > sh.cap) {
       *err = kErrLen;
@@ -298,46 +302,75 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     }
     if (sh.k) n = n == 0 ? 0 : sh.trim ? min(n, sh.k) : sh.k;
     s_nv[v] = n;
-    mine += stages_of(n) * chunks;
-  }
-  int upto = mine;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, upto, d);
-    if (lane >= d) upto += x;
-  }
-  if (lane == 31) s_warp[warp] = upto;
-  __syncthreads();
-  int W = 0, before = upto - mine;  // (stages before this thread's first segment)
-#pragma unroll
-  for (int w = 0; w < NWARPS; ++w) {
-    const int x = s_warp[w];
-    if (w < warp) before += x;
-    W += x;
-  }
-  const int n_ctas = min(sh.grid, W), cta = blockIdx.x;
-  if (cta == 0) {
-    int at = before;
-    for (int v = v_lo; v < v_hi; ++v) {
-      prefix[v] = at;
-      at += stages_of(s_nv[v]) * chunks;
+    return n;
+  };
+  if (sh.whole) {  // a CTA a segment
+    const int v = cta / chunks, c = cta - v * chunks;
+    if (tid == 0) {
+      s_first = v;
+      s_count = stages_of(tokens_of(v));
+      s_rest = c * s_count;
+      s_lo = 0;
     }
-    if (tid == 0) prefix[sh.Bv] = W;
-  }
-  if (cta >= n_ctas) return;
-  const Shares shares(W, n_ctas);
-  const int lo = shares.first(cta), hi = shares.first(cta + 1), count = hi - lo;
-  if (lo >= before && lo < before + mine) {
-    int rest = lo - before, v = v_lo;
-    for (;; ++v) {
-      const int units = stages_of(s_nv[v]) * chunks;
-      if (rest < units) break;
-      rest -= units;
+    __syncthreads();
+    if (s_count == 0) {
+      const int hg = c / sh.NRC, r0 = (c - hg * sh.NRC) * RC, rows = min(RC, sh.R - r0);
+      for (int i = tid; i < HG * rows * (D / 8); i += NTHREADS) {
+        const int x = i / (D / 8), h = x / rows, r = r0 + x - h * rows, qi = r / sh.G;
+        const int64_t row =
+            ((int64_t)v * sh.Nq + qi) * sh.Hq + (hg * HG + h) * sh.G + r - qi * sh.G;
+        const int at = i - x * (D / 8);
+        *reinterpret_cast<uint4*>(out + row * D + 8 * at) = make_uint4(0, 0, 0, 0);
+        if (lse && at == 0) lse[row] = kNegInf;
+      }
+      return;
     }
-    s_first = v;
-    s_rest = rest;
+  } else {
+    const int per = (sh.Bv + NTHREADS - 1) / NTHREADS, v_lo = min(tid * per, sh.Bv),
+              v_hi = min(v_lo + per, sh.Bv);
+    int mine = 0;
+    for (int v = v_lo; v < v_hi; ++v) mine += stages_of(tokens_of(v)) * chunks;
+    int upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, upto, d);
+      if (lane >= d) upto += x;
+    }
+    if (lane == 31) s_warp[warp] = upto;
+    __syncthreads();
+    int W = 0, before = upto - mine;  // (stages before this thread's first segment)
+#pragma unroll
+    for (int w = 0; w < NWARPS; ++w) {
+      const int x = s_warp[w];
+      if (w < warp) before += x;
+      W += x;
+    }
+    if (cta == 0) {
+      int at = before;
+      for (int v = v_lo; v < v_hi; ++v) {
+        prefix[v] = at;
+        at += stages_of(s_nv[v]) * chunks;
+      }
+      if (tid == 0) prefix[sh.Bv] = W;
+    }
+    const int n_ctas = min(sh.grid, W);
+    if (cta >= n_ctas) return;
+    const Shares shares(W, n_ctas);
+    const int lo = shares.first(cta);
+    if (lo >= before && lo < before + mine) {
+      int rest = lo - before, v = v_lo;
+      for (;; ++v) {
+        const int units = stages_of(s_nv[v]) * chunks;
+        if (rest < units) break;
+        rest -= units;
+      }
+      s_first = v;
+      s_rest = rest;
+      s_lo = lo;
+      s_count = shares.first(cta + 1) - lo;
+    }
+    __syncthreads();
   }
-  __syncthreads();
   // Waits of a warp.  Looks at the clock and at the other warps once in many polls (each of
   // which the hardware holds back): polling takes issue slots from the warps that work.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -362,7 +395,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     // =========================== producers ===========================
     set_registers<kProducerRegisters<PW>, false>();
     behind(seq_lens, block_table, lists);
-    const int me = warp - NW;
+    const int me = warp - NW, count = s_count, lo = s_lo, hi = lo + count;
     int* s_row = s_row_all[me & 3];
     int v = s_first, n = s_nv[v], T = stages_of(n), c = 0, tile = s_rest;
     if (chunks > 1) {
@@ -401,6 +434,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     auto flags_of = [&](int i) -> uint32_t {
       uint32_t f = 0;
       if (tile == T - 1 || i == count - 1) f |= kLast;
+      if (i == count - 1) f |= kEnd;
       if (seg_at >= lo && seg_at + T <= hi) f |= kWhole;
       if (seg_at > lo) f |= kSecond;
       if (sh.causal && ((tile + 1) << ts_log2) > n - (sh.Nq - 1 - c % sh.NRC * RC / sh.G))
@@ -745,7 +779,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   int q_v = s_first, q_c = 0;  // the segment whose queries are to be read next
   if (chunks > 1) q_c = s_rest / stages_of(s_nv[q_v]);
   bool fresh = true;
-  for (int done = 0; done < count; ++done) {
+  uint32_t flags = 0;
+  do {
     if (__builtin_expect(fresh, 0)) {
       // ---------------- the segment's queries (while its tokens are on their way) ------
       fresh = false;
@@ -844,7 +879,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     uint32_t mask[TT];
 #pragma unroll
     for (int u = 0; u < TT; ++u) mask[u] = note->mask[sub * TT + u];
-    const uint32_t flags = mask[0];
+    flags = mask[0];
     const int4 seg = *reinterpret_cast<const int4*>(note);  // v, c, p0, nv
     uint32_t k0[TT][NB], k1[TT][NB], kp0[TT][NB], kp1[TT][NB];
     uint32_t w[TT][4][NB / 2], s01[TT][NB], s23[TT][NB], ma0[TT], ma2[TT];
@@ -1063,8 +1098,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       exponents();
       weights();
     }
-    if (done + 1 < count) ready = tc::mbar_test_wait(&bar_full[stage], phase);
-    ready = __all_sync(0xffffffffu, ready) != 0;
+    ready = __all_sync(0xffffffffu, tc::mbar_test_wait(&bar_full[stage], phase)) != 0;
     // ---------------- values ----------------
     // The products start from zero every time and are added on their own: the tensor
     // core cuts off what lies below the accumulator's last place, and both sums grow
@@ -1118,7 +1152,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     }
     if (__builtin_expect(!(flags & kLast), 1)) continue;
 
-    fresh = done + 1 < count;
+    fresh = !(flags & kEnd);
     if (fresh) {
       q_v = seg.x;
       q_c = seg.y + 1;
@@ -1236,7 +1270,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                             o[nt][b][1][2 + j]);
         }
       }
-  }
+  } while (!(flags & kEnd));
   if (!ok) give_up();
 }
 
@@ -1409,11 +1443,13 @@ Config configure(const pks_q4_attention_args& a) {
   sh.scratch_at = sh.q_at + queries;
   sh.nv_at = sh.scratch_at + scratch;
   cf.smem = (size_t)sh.nv_at + nv + 1024;
-  // no more CTAs than a full batch has stages
-  const int64_t most =
-      (int64_t)sh.Bv * sh.NHG * sh.NRC * (((sh.k ? sh.k : sh.cap) + sh.TS - 1) / sh.TS);
+  // a CTA a segment where they are few and short, else no more than a full batch has stages
+  const int64_t each = ((sh.k ? sh.k : sh.cap) + sh.TS - 1) / sh.TS;
+  const int64_t segments = (int64_t)sh.Bv * sh.NHG * sh.NRC, most = segments * each;
   sh.grid = device_sm_count();
-  if (most < sh.grid) sh.grid = most > 0 ? (int)most : 1;
+  sh.whole = each <= kWholeStages + segments / kWholeMore && segments <= sh.grid;
+  const int64_t needed = sh.whole ? segments : most;
+  if (needed < sh.grid) sh.grid = needed > 0 ? (int)needed : 1;
   cf.PW = fixed && sh.copies == kTokens && most > (int64_t)kLongRun * sh.grid ? 8 : 4;
   cf.fixed = fixed;
   return cf;
@@ -1482,7 +1518,7 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
                 static_cast<const uint8_t*>(a.pool_v), out, a.lse, prefix, ml, po,
                 reinterpret_cast<int32_t*>(ws), sh, scale * 1.4426950408889634f,
                 a.wait_limit > 0 ? (long long)a.wait_limit : kWaitCycles, map_k, map_v);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || sh.whole) return e;
   const int64_t rows = (int64_t)sh.Bv * sh.Nq * sh.Hq;
   const bool few = rows <= kFewRows;
   return launch_ex(few ? k_q4_merge<D, 8> : k_q4_merge<D, 1>,
