@@ -63,6 +63,17 @@ def test_pages_of_every_small_size(page):
     Batch(lens, page, 4, 9, 128, 2, seed=page).dense(causal=True)
 
 
+@pytest.mark.parametrize("B,Hkv,longest", [(76, 16, 400), (77, 16, 400), (152, 8, 420), (153, 8, 90),
+                                           (8, 8, 128), (8, 8, 160), (8, 8, 190), (1, 2, 700)])
+def test_few_short_segments(B, Hkv, longest):
+    """On both sides of the limits up to which a CTA has a segment to itself, some of them empty."""
+    lens = np.random.default_rng(B).integers(0, longest + 1, B)
+    lens[::7] = 0
+    lens[-1] = longest
+    Batch(lens, 16, Hkv, 2, 128, seed=B).dense()
+    Batch(lens, 16, Hkv, 2, 128, 3, seed=B).sparse(70, holes=True)
+
+
 def test_long_requests_split_over_all_sms():
     Batch([20000, 3, 0, 45011, 700], 64, 8, 8, 128, seed=1).dense()
     Batch([70001], 16, 1, 4, 128, seed=2).dense()

@@ -22,14 +22,15 @@
 // Maxima, sums, scores and accumulators are fp32.
 //
 // One persistent CTA an SM.  All (request, head group, row chunk) segments are cut into
-// stages of 16 or 32 tokens a consumer warp; the CTAs take equal runs of stages.  Producer
+// stages of 16 or 32 tokens a consumer warp; the CTAs take equal runs of stages (or, where
+// segments are few and short, one segment each).  Producer
 // warps find the tokens' rows and fill a ring of stages, each in its turn; a consumer
 // warp owns one head and some tokens of every stage and keeps the head's sums in registers.
 // Segments that several CTAs hold parts of are joined by k_q4_merge.
 //
 // Bound by memory where the tokens are many (16 x 131072 tokens of eight heads of 128, eight
-// queries a head: 397 us, 6.8 TB/s of codes), else by what the consumers issue: a head's 32
-// tokens take 1870 cycles from L2 (2780 with sixteen queries a head), of which the tensor
+// queries a head: 388 us, 6.9 TB/s of codes), else by what the consumers issue: a head's 32
+// tokens take 1750 cycles from L2 (2640 with sixteen queries a head), of which the tensor
 // pipe is busy for a third and the integer pipe, which takes the codes apart, for half.
 // Measured against it:
 //  - sixteen consumer warps of half the registers, queries in shared memory: 468 us for 434;
@@ -199,7 +200,7 @@ struct alignas(16) StageNote {
 };
 // kLast: the CTA's last stage of the segment; kWhole: it has all of them; kSecond: not
 // the CTA's first segment; kEdge: some token lies beyond some query's limit; kEnd: the
-// CTA's last stage
+// CTA's last stage (counted by the producers: by the consumers, 1860 cycles a stage for 1750)
 constexpr uint32_t kLast = 1u << 16, kWhole = 2u << 16, kSecond = 4u << 16, kEdge = 8u << 16,
                    kEnd = 16u << 16;
 // Registers a thread of this warpgroup has from here on.  All of a CTA's together no
