@@ -59,7 +59,8 @@ constexpr int kConsumers = 8;  // warps, two a scheduler
 constexpr int kLongRun = 24;  // stages a CTA above which there are eight
 // Stages up to which a CTA has a segment to itself, without a plan and parts to join: four, and
 // one more for every sixteen segments.  5 requests of 2 stages 6.8 us and 8.5 split, of 4 8.9
-// and 8.6, of 6 10.6 and 8.6; 16 of 4 9.2 and 10.3, of 8 12.6 and 12.0; 64 lists of 8 14.0 and 19.3.
+// and 8.6, of 6 10.6 and 8.6; 16 of 4 9.2 and 10.3, of 8 12.6 and 12.0; 64 lists of 8 14.0 and
+// 19.3.
 constexpr int kWholeStages = 4, kWholeMore = 16;
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
@@ -69,7 +70,7 @@ constexpr int kSmemMax = 227 * 1024 - 6144;  // dynamic; the rest is the static 
 // rows of 160 bytes 32 and 32 us, 240 38 and 36, 320 40 and 44, 480 42 and 46.
 constexpr int kTokenBytesLeast = 320;
 // Output rows up to which a block of k_q4_merge joins one, else a warp: 64 rows 61 us and
-// 112, 1024 85 and 89, 2048 58.5 both, 3072 77 and 73, 16384 75 and 56.
+// 112, 1024 85 and 89, 2048 58.5 both, 4096 65 and 57, 8192 75 and 56.
 constexpr int kFewRows = 2048;
 constexpr float kNone = -3e38f;  // reference of a row that has seen no token
 
