@@ -549,6 +549,7 @@ class Q4DecodeStep:
         self.tensors = t
 
     def select(self, stream=None):
+        pks._on_current_device(self.topk_idx)
         pks.pks_decode_select(self.select_args, stream)
         return self.topk_idx
 
