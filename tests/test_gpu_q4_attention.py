@@ -199,6 +199,19 @@ def test_runs_give_the_same_bits():
         assert torch.equal(att.out, first) and torch.equal(att.lse, lse)
 
 
+@pytest.mark.parametrize("Hkv,G,D,Nq", [(1, 4, 64, 1), (1, 12, 128, 1), (2, 2, 64, 2), (3, 5, 64, 2),
+                                        (6, 3, 64, 1), (13, 2, 64, 1), (10, 9, 64, 1)])
+def test_small_rows_by_lanes(Hkv, G, D, Nq):
+    """Stage behind stage of tokens that lanes copy by rows which other lanes looked up, some of
+    them missing so that the lanes part: the same bits every time."""
+    b = Batch([5000, 40, 3100], 5, Hkv, G, D, Nq, seed=24)
+    att = b.sparse(3000, holes=True)
+    first, lse = att.out.clone(), att.lse.clone()
+    for _ in range(10):
+        att()
+        assert torch.equal(att.out, first) and torch.equal(att.lse, lse)
+
+
 def test_a_position_twice_counts_twice():
     b = Batch([100, 40], 16, 2, 4, 64, seed=21)
     lists = b.lists(30)

@@ -694,6 +694,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             }
           }
           if (copies == kLanes) {
+            __syncwarp();  // (all lanes have read the rows that the next stage overwrites)
             tc::cp_async_arrive(&bar_full[stage]);
             if (lane == 0) tc::mbar_arrive(&bar_full[stage]);
           } else {  // (the end of a request: these copies land before the boxes are announced)
