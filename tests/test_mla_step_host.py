@@ -4,8 +4,10 @@ GPU)."""
 import ctypes
 
 import pytest
+import torch
 
 from top_sparse_attention_pks_gb300 import build, pks
+from top_sparse_attention_pks_gb300.decoder import MlaDecodeStep
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -55,3 +57,15 @@ def test_nothing_and_an_empty_batch():
     s, m = pair()
     assert code(None, m) == -1 and code(s, None) == -1
     assert code(*pair(B=0)) == 0
+
+
+@pytest.mark.parametrize("shape", [(4, 128), (2, 3, 4, 64), (1, 2, 4, 64), (64,)])
+def test_queries_of_the_indexer_have_their_three_dimensions(shape):
+    i = torch.int32
+    t = dict(seq_lens=torch.zeros(2, dtype=i), block_table=torch.zeros((2, 3), dtype=i),
+             q=torch.zeros((2, 128, 576), dtype=torch.bfloat16),
+             kv=torch.zeros((4, 16, 576), dtype=torch.bfloat16),
+             idx_k=torch.zeros((4, 16, 64), dtype=torch.int8), w_idx=torch.ones(4, dtype=i),
+             q_idx=torch.zeros(shape, dtype=torch.int8))
+    with pytest.raises(ValueError):
+        MlaDecodeStep(t, 8)

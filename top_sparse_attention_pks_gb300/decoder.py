@@ -201,13 +201,16 @@ def _select_args(t: dict, topk_idx, num_pages: int, page_size: int, topk_mode: i
     attention fields stay unset; select does not read them)."""
     a = pks.pks_decode_args()
     B = t["seq_lens"].shape[0]
-    Hi, Di = t["q_idx"].shape[-2:]
+    q_idx = t["q_idx"]
+    if q_idx.dim() != topk_idx.dim() + 1:
+        raise ValueError("q_idx must be [B, Hi, Di], or [B, Nq, Hi, Di] where q has Nq")
+    Hi, Di = q_idx.shape[-2:]
     a.B, a.Hq, a.Hkv, a.D, a.Hi, a.Di = int(B), 1, 1, 64, int(Hi), int(Di)
     a.page_size, a.max_pages = int(page_size), int(t["block_table"].shape[1])
     a.num_pages, a.k = int(num_pages), int(topk_idx.shape[-1])
     a.seq_lens = pks._dptr(t["seq_lens"], torch.int32, "seq_lens")
     a.block_table = pks._dptr(t["block_table"], torch.int32, "block_table")
-    a.q_idx = pks._dptr(t["q_idx"], torch.int8, "q_idx")
+    a.q_idx = pks._dptr(q_idx, torch.int8, "q_idx")
     a.w_idx = pks._dptr(t.get("w_idx"), torch.int32, "w_idx")
     a.idx_k = pks._dptr(t["idx_k"], torch.int8, "idx_k")
     a.topk_idx = pks._dptr(topk_idx, torch.int32, "topk_idx")
