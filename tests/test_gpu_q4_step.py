@@ -61,6 +61,14 @@ def test_step(nq, hi, mode):
     assert torch.equal(att(), first)
 
 
+@pytest.mark.parametrize("name", ["q_idx", "idx_k", "w_idx", "block_table"])
+def test_step_refuses_tensors_on_the_host(name):
+    wl = WORKLOADS["paging_example"]
+    c = Case(wl)
+    with pytest.raises(ValueError):
+        Q4DecodeStep(dict(c.t, **{name: c.t[name].cpu()}), c.cache, wl.k)
+
+
 def test_step_against_the_oracle():
     wl = WORKLOADS["b32_4k"].replace(B=4, seq_lens=(4096, 700, 0, 1500))
     t, _, _ = prepare(wl)

@@ -8,7 +8,7 @@ import torch
 
 import q4_reference as ref
 from top_sparse_attention_pks_gb300 import build, pks
-from top_sparse_attention_pks_gb300.decoder import Q4Cache
+from top_sparse_attention_pks_gb300.decoder import Q4Cache, Q4DecodeStep
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -129,6 +129,35 @@ def test_step_refused(which, change, want):
     assert pks.lib().pks_q4_decode_step(ctypes.byref(s), ctypes.byref(a), None) == want
     assert pks.lib().pks_q4_decode_step(None, ctypes.byref(a), None) == -1
     assert pks.lib().pks_q4_decode_step(ctypes.byref(s), None, None) == -1
+
+
+def host_step(nq, **change):
+    """Tensors of a step and its cache, on the host."""
+    i = torch.int32
+    cache = Q4Cache.__new__(Q4Cache)
+    cache.Hkv, cache.D = 2, 64
+    cache._k = cache._v = torch.zeros((4, 16, pks.pks_q4_token_bytes(2, 64)), dtype=torch.uint8)
+    lead = (2, nq) if nq else (2,)
+    t = dict(seq_lens=torch.zeros(2, dtype=i), block_table=torch.zeros((2, 3), dtype=i),
+             q=torch.zeros(lead + (8, 64), dtype=torch.bfloat16),
+             q_idx=torch.zeros(lead + (4, 64), dtype=torch.int8), w_idx=torch.ones(4, dtype=i),
+             idx_k=torch.zeros((4, 16, 64), dtype=torch.int8))
+    t.update({name: (x if isinstance(x, torch.Tensor) else torch.zeros(x, dtype=t[name].dtype))
+              for name, x in change.items()})
+    return t, cache
+
+
+@pytest.mark.parametrize("nq,change", [
+    (0, dict(q_idx=(2, 3, 4, 64))), (0, dict(q_idx=(1, 4, 64))), (0, dict(q_idx=(4, 64))),
+    (3, dict(q_idx=(2, 4, 64))), (3, dict(q_idx=(2, 2, 4, 64))), (3, dict(q_idx=(1, 3, 4, 64))),
+    (0, dict(idx_k=(3, 16, 64))), (0, dict(idx_k=(4, 8, 64))), (0, dict(idx_k=(4, 16, 128))),
+    (0, dict(idx_k=(8, 8, 64))), (3, dict(seq_lens=(3,))), (0, dict(block_table=(3, 3))),
+    (0, dict(block_table=(6,))), (0, dict(w_idx=(3,))), (0, dict(w_idx_f=torch.zeros(4))),
+    (3, dict(w_idx_f=torch.zeros(2, 4)))])
+def test_step_refuses_shapes_that_disagree(nq, change):
+    t, cache = host_step(nq, **change)
+    with pytest.raises(ValueError):
+        Q4DecodeStep(t, cache, 8)
 
 
 @pytest.mark.parametrize("D", [64, 128])

@@ -540,9 +540,25 @@ class Q4DecodeStep:
         with pks._on_stream(stream):
             self.topk_idx = torch.empty(tuple(q.shape[:-2]) + (self.k,), dtype=torch.int32,
                                         device=q.device)
-        a = _select_args(t, self.topk_idx, int(cache.k.shape[0]), int(cache.k.shape[1]), topk_mode)
+        num_pages, page_size = cache.k.shape[:2]
+        if t["q_idx"].shape[:-2] != q.shape[:-2]:
+            raise ValueError("q_idx must be [B, Hi, Di] or [B, Nq, Hi, Di] like q")
+        Hi, Di = t["q_idx"].shape[-2:]
+        if tuple(t["idx_k"].shape) != (num_pages, page_size, Di):
+            raise ValueError("idx_k must be [num_pages, page_size, Di] of the cache's pages")
+        if t["seq_lens"].shape != q.shape[:1] or t["block_table"].dim() != 2 or \
+                t["block_table"].shape[0] != q.shape[0]:
+            raise ValueError("block_table must be [B, max_pages] and seq_lens [B]")
+        if t.get("w_idx") is not None and t["w_idx"].numel() != Hi:
+            raise ValueError("w_idx must be [Hi]")
+        if t.get("w_idx_f") is not None and \
+                t["w_idx_f"].numel() != t["q_idx"].shape[:-1].numel():
+            raise ValueError("w_idx_f must be [B, Hi]")
+        a = _select_args(t, self.topk_idx, num_pages, page_size, topk_mode)
         if q.dim() == 4:
             a.n_queries = int(q.shape[1])
+        pks._on_current_device(q, cache.k, *(t.get(x) for x in (
+            "seq_lens", "block_table", "q_idx", "idx_k", "w_idx", "w_idx_f")))
         self.select_workspace = _select_workspace(a, q.device, stream)
         self.select_args = a
         self.attention = Q4SparseAttention(t["seq_lens"], t["block_table"], self.topk_idx, q,
