@@ -10,7 +10,7 @@ from q4_cases import Batch, i32
 from top_sparse_attention_pks_gb300 import build
 from top_sparse_attention_pks_gb300.decoder import (PageTable, Q4Attention, Q4Cache, Q4DecodeStep,
                                                     Q4SparseAttention, SparseDecodeStep)
-from top_sparse_attention_pks_gb300.workloads import WORKLOADS
+from top_sparse_attention_pks_gb300.workloads import WORKLOADS, draw_float_weights, draw_fp8_indexer
 
 pytestmark = pytest.mark.gpu
 
@@ -59,6 +59,29 @@ def test_step(nq, hi, mode):
     assert torch.equal(step.select(), want)
     att = Q4SparseAttention(c.len_d, c.t["block_table"], idx, c.t["q"], c.cache, trim=True)
     assert torch.equal(att(), first)
+
+
+@pytest.mark.parametrize("fp8", [None, torch.int8, torch.float8_e4m3fn])
+def test_step_with_real_weights_and_fp8(fp8):
+    wl = WORKLOADS["b32_4k"].replace(B=4, seq_lens=(4096, 700, 0, 1500))
+    t, _, _ = prepare(wl)
+    t["w_idx_f"] = draw_float_weights(wl, "cuda", signed=True)
+    if fp8 is not None:
+        t["q_idx"], t["idx_k"] = (x.view(fp8) for x in draw_fp8_indexer(wl, "cuda"))
+        t["idx_fp8"] = True
+    _, want = SparseDecodeStep(t, wl.k)()
+    cache = Q4Cache(wl.num_pages, wl.page_size, wl.Hkv, wl.D)
+    lens = [int(n) for n in wl.seq_lens]
+    starts = i32(np.concatenate([[0], np.cumsum(lens)]))
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn((sum(lens), wl.Hkv, wl.D), generator=g, device="cuda") for _ in range(2))
+    cache.write(k, v, t["seq_lens"], t["block_table"], starts)
+    del t["kv_k"], t["kv_v"]
+    step = Q4DecodeStep(t, cache, wl.k)
+    out, idx = step()
+    assert torch.equal(idx, want) and step.device_error() == 0
+    att = Q4SparseAttention(t["seq_lens"], t["block_table"], want, t["q"], cache, trim=True)
+    assert torch.equal(att(), out) and bool(out[0].any()) and not out[2].any()
 
 
 @pytest.mark.parametrize("name", ["q_idx", "idx_k", "w_idx", "block_table"])

@@ -8,7 +8,7 @@ import torch
 
 import q4_reference as ref
 from top_sparse_attention_pks_gb300 import build, pks
-from top_sparse_attention_pks_gb300.decoder import Q4Cache, Q4DecodeStep
+from top_sparse_attention_pks_gb300.decoder import Q4Cache, Q4DecodeStep, _select_args
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -158,6 +158,16 @@ def test_step_refuses_shapes_that_disagree(nq, change):
     t, cache = host_step(nq, **change)
     with pytest.raises(ValueError):
         Q4DecodeStep(t, cache, 8)
+
+
+def test_step_takes_fp8_tensors_as_their_bits():
+    t, _ = host_step(0)
+    top = torch.zeros((2, 8), dtype=torch.int32)
+    for name in ("q_idx", "idx_k"):
+        f8 = dict(t, **{name: t[name].view(torch.float8_e4m3fn)})
+        assert getattr(_select_args(f8, top, 4, 16, 0), name) == t[name].data_ptr()
+        with pytest.raises(TypeError):
+            _select_args(dict(t, **{name: t[name].view(torch.uint8)}), top, 4, 16, 0)
 
 
 @pytest.mark.parametrize("D", [64, 128])

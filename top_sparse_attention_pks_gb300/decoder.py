@@ -210,9 +210,11 @@ def _select_args(t: dict, topk_idx, num_pages: int, page_size: int, topk_mode: i
     a.num_pages, a.k = int(num_pages), int(topk_idx.shape[-1])
     a.seq_lens = pks._dptr(t["seq_lens"], torch.int32, "seq_lens")
     a.block_table = pks._dptr(t["block_table"], torch.int32, "block_table")
+    f8 = torch.float8_e4m3fn  # (taken by their bit patterns, as in make_args)
+    q_idx, idx_k = (x.view(torch.int8) if x.dtype == f8 else x for x in (q_idx, t["idx_k"]))
     a.q_idx = pks._dptr(q_idx, torch.int8, "q_idx")
     a.w_idx = pks._dptr(t.get("w_idx"), torch.int32, "w_idx")
-    a.idx_k = pks._dptr(t["idx_k"], torch.int8, "idx_k")
+    a.idx_k = pks._dptr(idx_k, torch.int8, "idx_k")
     a.topk_idx = pks._dptr(topk_idx, torch.int32, "topk_idx")
     a.topk_mode = int(topk_mode)
     # real-valued head weights and FP8 e4m3 queries/keys (DSA's indexer)
@@ -530,7 +532,7 @@ class Q4SparseAttention(Q4Attention):
 class Q4DecodeStep:
     """The sparse decode step over a ``Q4Cache`` (``pks_q4_decode_step``): indexer scan and
     top-k, then attention over the selected tokens.  ``tensors``: seq_lens, block_table, q,
-    q_idx, w_idx (or w_idx_f), idx_k as for ``SparseDecodeStep``."""
+    q_idx, w_idx (or w_idx_f), idx_k, idx_fp8 as for ``SparseDecodeStep``."""
 
     def __init__(self, tensors: dict, cache: Q4Cache, k: int, topk_mode: int = 0,
                  sm_scale: float = 0.0, lse: bool = False, stream=None):
