@@ -170,6 +170,49 @@ def test_groups_that_are_hard_to_round(dtype):
     check_read(cache, lens, table, starts, torch.float32)
 
 
+def border_rows(dtype, seed, n=600):
+    """Rows of a group each whose minimum is small beside its scale, and whose values stand at
+    the borders between two codes, rounded to the type, or next to them."""
+    rng = np.random.default_rng(seed)
+    m = (rng.integers(1024, 2048, n) * 2.0 ** rng.integers(-28, -12, n)).astype(np.float16)
+    m[: n // 8] = rng.integers(1, 1024, n // 8) * 2.0 ** -24  # subnormal ones
+    m[n // 8: n // 4] *= -1
+    m = m.astype(np.float64)
+    s = (rng.integers(1024, 2048, n) * 2.0 ** rng.integers(-14, -8, n)).astype(np.float64)
+    top = m + 15 * s
+    x = np.empty((n, 32))
+    x[:, 0], x[:, 1] = m, top
+    x[:, 2:] = (m[:, None] + (np.arange(30) // 2 + 0.5) * s[:, None])
+    x = torch.from_numpy(x).to(torch.float32).to(dtype)
+    bits = x.view(torch.int32 if dtype == torch.float32 else torch.int16)
+    off = torch.from_numpy(rng.integers(-1, 2, (n, 32)))
+    off[:, :2] = 0
+    off[:, 2::2] = 0
+    bits += off.to(bits.dtype)
+    return x
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_values_at_the_borders_between_codes(dtype):
+    """Minima whose last bits lie below the place of a border m + (n + 1/2) s in fp32."""
+    t = TYPES[dtype]
+    x = border_rows(t, 5)
+    odd = torch.zeros((4, 32))
+    odd[0, :30], odd[0, 30], odd[0, 31] = 2.0 ** -14 * (1 + 2.0 ** -10), 7.5 + 2.0 ** -14, 15.0
+    odd[1, :30], odd[1, 30], odd[1, 31] = 0.0004887580871582031, 8.3984375, 19.375
+    odd[2, :30], odd[2, 30], odd[2, 31] = 2.0 ** -24, 7.5, 15.0
+    odd[3, :30], odd[3, 30], odd[3, 31] = -2.0 ** -24, 7.5, 15.0
+    x = torch.cat([odd.to(t), x])
+    x = x[: len(x) // 2 * 2].reshape(-1, 1, 64).cuda()
+    n = x.shape[0]
+    table, N = layout([n], 16)
+    cache = Q4Cache(N, 16, 1, 64)
+    y = x.flip(2).contiguous()
+    cache.write(x, y, i32([n]), i32(table), i32([0, n]))
+    check(cache, x, y, [n], table, [0, n])
+    check_read(cache, [n], table, [0, n], torch.float32)
+
+
 def test_padded_rows_and_rows_without_a_place():
     """Rows behind the last request, a page out of range, a length out of range and more rows
     than tokens: those rows are skipped, all others written; a read leaves theirs alone."""

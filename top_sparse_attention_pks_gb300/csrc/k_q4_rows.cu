@@ -55,6 +55,11 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t add2_down(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rm.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
@@ -159,13 +164,14 @@ __device__ __forceinline__ void extent(const Eight<T> (&in)[4], float& lo, float
 //  - s: rounded up from the quotient, one step more where 15 s still falls short of
 //    max - m (whose own rounding error, err, is counted).
 //  - n: guessed from the reciprocal, at most one too low (the guess leans down by
-//    2^-9, more than its error of 2^-11), then compared with the border above it.
-//    Both sides of the comparison are exact: near m (15 s below 2^-7 |m|) as
-//    x - m >= (n + 1/2) s, else as x >= m + (n + 1/2) s, at most 24 bits long.
+//    2^-9, more than its error of 2^-17), then compared with the border above it,
+//    (n + 1/2) s, which is at most 16 bits long.  x - m may need more than fp32 has (a
+//    small m below a large s), so it is rounded down: then it is at or above a number
+//    of fp32 exactly when x - m is.
 struct Scale {
   uint32_t pair;
-  float s, inv, from, guess, first;  // first: the border between 0 and 1
-  bool flat;                         // all codes are 0
+  float s, inv, m;
+  bool flat;  // all codes are 0
 };
 __device__ __forceinline__ Scale scale_of(float lo, float hi) {
   Scale g;
@@ -182,23 +188,20 @@ __device__ __forceinline__ Scale scale_of(float lo, float hi) {
   g.pair = bad ? 0x7e00u : (uint32_t)__half_as_ushort(mh) << 16 | __half_as_ushort(sh);
   g.flat = bad || g.s == 0.f;
   g.inv = g.flat ? 0.f : __frcp_rn(g.s);
-  const bool near = fabsf(m) > 2048.f * g.s;
-  g.from = near ? m : 0.f;
-  const float base = near ? 0.f : m;
-  g.guess = __fmaf_rn(-base, g.inv, -0.001953125f);
-  g.first = __fmaf_rn(0.5f, g.s, base);
+  g.m = m;
   return g;
 }
 // codes of eight values, the first in the lowest bits
 __device__ __forceinline__ uint32_t codes(const float (&x)[8], const Scale& g) {
-  const uint64_t from = two(-g.from, -g.from), inv = two(g.inv, g.inv),
-                 guess = two(g.guess, g.guess), scale = two(g.s, g.s), half = two(g.first, g.first),
-                 magic = two(12582912.f, 12582912.f), back = two(-12582912.f, -12582912.f);
+  const uint64_t least = two(-g.m, -g.m), inv = two(g.inv, g.inv),
+                 lean = two(-0.001953125f, -0.001953125f), scale = two(g.s, g.s),
+                 half = two(0.5f * g.s, 0.5f * g.s), magic = two(12582912.f, 12582912.f),
+                 back = two(-12582912.f, -12582912.f);
   uint32_t w = 0;
 #pragma unroll
   for (int i = 6; i >= 0; i -= 2) {
-    const uint64_t xa = add2(two(x[i], x[i + 1]), from);
-    const uint64_t r = add2(fma2(xa, inv, guess), magic);  // to the nearest whole number
+    const uint64_t xa = add2_down(two(x[i], x[i + 1]), least);
+    const uint64_t r = add2(fma2(xa, inv, lean), magic);  // to the nearest whole number
     const uint64_t border = fma2(add2(r, back), scale, half);
     const uint64_t n = add2(r, two(from_on(first(xa), first(border)),
                                    from_on(second(xa), second(border))));
