@@ -16,9 +16,8 @@
 //    Each group's sum is scaled by s_b on its own (fp32); the m_b Q_b of two groups are
 //    one more MMA, with the (s, m) pairs as they lie against 0 and Q_b, which is cut into
 //    three fp16 pieces (33 bits), one a lane (m taken out of the pairs: 420 us for 413).
-//  - V: fp16.  p s is rounded to fp16 once a group (by 2^-11 of it at most; p itself
-//    likewise); p is kept at 2^11 to 2^14 at the largest score so that small ones stay
-//    normal numbers, lower where an s is 2 or more.  sum p m is one more MMA.
+//  - V: fp16.  p is rounded to fp16, and p s once a group (by 2^-11 of it at most while
+//    they are normal numbers: kTop and what follows there).  sum p m is one more MMA.
 // Maxima, sums, scores and accumulators are fp32.
 //
 // One persistent CTA an SM.  All (request, head group, row chunk) segments are cut into
@@ -73,6 +72,21 @@ constexpr int kTokenBytesLeast = 320;
 // 112, 1024 85 and 89, 2048 58.5 both, 4096 65 and 57, 8192 75 and 56.
 constexpr int kFewRows = 2048;
 constexpr float kNone = -3e38f;  // reference of a row that has seen no token
+// Weights p are kept at 2^(kTop - 3) to 2^kTop at the largest score, 2^11 to 2^14, so that those of
+// 2^-25 of the largest are normal numbers of fp16 still, and those above 2^-36 are not 0.  The
+// same has to hold for p s, whatever V's size.  So the sums of a group are in a unit 2^sx, by
+// which its scales are divided:
+//  - 1 while they have their usual size, the largest of a stage in [2^-kSmall, 2).  That none is
+//    2 is seen to at every stage, that some are large enough at one stage in two rounds of the
+//    ring (at every stage, in a few operations: 16 x 131072 tokens 407 us for 389);
+//  - else what brings the stage's largest scale into [1, 2), or, so that it seldom changes,
+//    within 2^-kKeep below.
+// What is lost of a token is so 15 2^-29 of the largest s that was looked at, 2^-9 of 15 s over
+// kLongSegment tokens; longer segments have a unit of their own at every stage.
+constexpr float kTop = 14.f;
+constexpr int kSmall = 7, kKeep = 3, kLongSegment = 1 << 20;
+// What a warp keeps of it in shared memory: 32 + sx a byte, and kLong for such a segment
+constexpr uint32_t kUsual = 0x20202020u, kLong = 0x80000000u;
 
 // Tokens of a warp's 16 as the rows of its MMA tiles, four bits each (lowest: row 0).
 // Lanes of one shared-memory access hold tokens whose records lie in different
@@ -160,6 +174,11 @@ __device__ __forceinline__ __half2 bits_half2(uint32_t u) {
 // all ones where a half is NaN
 __device__ __forceinline__ uint32_t no_number(uint32_t u) {
   return ~__heq2_mask(bits_half2(u), bits_half2(u));
+}
+// the halves' sizes, 0 for those that are not finite
+__device__ __forceinline__ uint32_t finite(uint32_t u) {
+  u &= 0x7fff7fffu;
+  return u & __vcmpltu2(u, 0x7c007c00u);
 }
 __device__ __forceinline__ float low_half(uint32_t u) {
   return __half2float(__low2half(bits_half2(u)));
@@ -257,13 +276,14 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   constexpr int NW = kConsumers, NWARPS = NW + PW, NTHREADS = NWARPS * 32;
   constexpr int NB = D / q4::kGroup, REC = q4::record_bytes(D);
   constexpr int RC = 8 * NT;  // query rows a chunk
-  const float kNegInf = __int_as_float(0xff800000);
+  const float kNegInf = __int_as_float(0xff800000), kAlways = __int_as_float(0x7fc00000);
   extern __shared__ uint8_t smem_raw[];
   // bar_full: the producer's announcement (and its lanes' copies); bar_empty and
   // bar_join: the consumer warps
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
   __shared__ int s_row_all[4][kMaxTokens];  // tokens' rows in the pool (-1: none)
+  __shared__ uint32_t s_units[NW];
   __shared__ int s_warp[NWARPS], s_first, s_rest, s_lo, s_count, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t ring = (tc::smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -767,7 +787,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   // of columns 2t, 2t + 1: scale of the scores, minus the reference, sum of weights
   float cs[NT][2], nref[NT][2], sum[NT][2];
   float o[NT][NB][2][4], om[NT][2];
-  int sx = 0;  // weights are at most 2^(14 - sx), scales below 2^(1 + sx)
+  float limit = kAlways;  // of the scores, above which a stage is looked at more closely
   int stage = 0;
   uint32_t phase = 0, join_phase = 0;
   bool ok = true;
@@ -787,7 +807,10 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     if (__builtin_expect(fresh, 0)) {
       // ---------------- the segment's queries (while its tokens are on their way) ------
       fresh = false;
-      sx = 0;
+      limit = kAlways;
+      __syncwarp();
+      if (lane == 0) s_units[warp] = kUsual | (s_nv[q_v] > kLongSegment ? kLong : 0);
+      __syncwarp();
       const int hg = q_c / sh.NRC, rc = q_c - hg * sh.NRC;
       const int head = hg * HG + h;
       const __nv_bfloat16* from = q;
@@ -919,6 +942,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       if (++stage == sh.stages) {
         stage = 0;
         phase ^= 1;
+        if (phase) limit = kAlways;
       }
     };
     if constexpr (!QSHARED) load_v();  // (early, but where registers are short)
@@ -961,8 +985,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
     }
     if constexpr (QSHARED) load_v();
     // ---------------- weights ----------------
-    // As if all tokens counted, no reference had to move and all s were below 2^(1 + sx);
-    // when that is not so, which is rare, they are made anew.
+    // As if all tokens counted, no reference had to move and all scales had their usual size,
+    // unless a closer look says otherwise, which is rare.
     float x[TT][NT][4], p[TT][NT][4];
     uint32_t pt0[TT][NT], pt1[TT][NT];
     auto exponents = [&]() {
@@ -996,13 +1020,72 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       for (int nt = 0; nt < NT; ++nt)
         x_top = fmaxf(fmaxf(x_top, fmaxf(x[u][nt][0], x[u][nt][1])),
                       fmaxf(x[u][nt][2], x[u][nt][3]));
-#pragma unroll
-      for (int b = 0; b < NB; ++b) any |= s01[u][b] | s23[u][b];
       all &= mask[u];
     }
-    const bool redo = __any_sync(0xffffffffu, x_top > (float)(14 - sx) || (any & 0x40004000u) ||
-                                                  all != 0xffffu || (flags & kEdge));
-    weights();
+#pragma unroll
+    for (int u = 0; u < TT; ++u)
+#pragma unroll
+      for (int b = 0; b < NB; ++b) any |= s01[u][b] | s23[u][b];
+    const bool look = __any_sync(0xffffffffu, !(x_top <= limit) || (any & 0x40004000u)) ||
+                      all != 0xffffu || (flags & kEdge);
+    bool redo = false, rescale = false;
+    if (__builtin_expect(look, 0)) {
+      const uint32_t units = s_units[warp];
+      redo = __any_sync(0xffffffffu, x_top > kTop) || all != 0xffffu || (flags & kEdge);
+      bool unusual = any & 0x40004000u, none = false;
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t y = 0;
+#pragma unroll
+        for (int u = 0; u < TT; ++u) y |= s01[u][b] | s23[u][b];
+        unusual |= y && !(y & 0x60006000u);  // (2^-kSmall and more have one of these bits)
+        none |= y == 0;
+      }
+      rescale = __any_sync(0xffffffffu, unusual) || units != kUsual;
+      limit = __any_sync(0xffffffffu, none) ? kAlways : kTop;
+    }
+    if (__builtin_expect(rescale, 0)) {
+      // A unit for each group of this stage, 2^sx, so that its largest s is in [1, 2) of it (or
+      // within kKeep below, if the unit was good before; 1 for usual sizes).
+      const uint32_t units = s_units[warp];
+      uint32_t now = (units & kLong) | (kUsual & (NB == 2 ? 0xffff0000u : 0));
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        uint32_t top = 0;
+#pragma unroll
+        for (int u = 0; u < TT; ++u)
+          top = __vmaxu2(top, __vmaxu2(finite(s01[u][b]), finite(s23[u][b])));
+        top = max(top >> 16, top & 0xffffu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int was = (int)(units >> 8 * b & 63) - 32;
+        const int e = (int)(__float_as_uint(low_half(top)) >> 23) - 127;
+        int sx = e;
+        if (top == 0 || (e <= was && e >= was - kKeep)) sx = was;
+        else if (e <= 0 && e >= -kSmall && !(units & kLong)) sx = 0;
+        if (sx != was) {
+          const float f = __int_as_float((127 + was - sx) << 23);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) o[nt][b][i >> 2][i & 3] *= f;
+        }
+        // times 2^-sx, in two steps as 2^24 is no fp16
+        const int f0 = min(max(-sx, -14), 15), f1 = -sx - f0;
+        const __half2 h0 = bits_half2((uint32_t)(f0 + 15) * 0x04000400u);
+        const __half2 h1 = bits_half2((uint32_t)(f1 + 15) * 0x04000400u);
+#pragma unroll
+        for (int u = 0; u < TT; ++u) {
+          s01[u][b] = half2_bits(__hmul2(__hmul2(bits_half2(s01[u][b]), h0), h1));
+          s23[u][b] = half2_bits(__hmul2(__hmul2(bits_half2(s23[u][b]), h0), h1));
+        }
+        now |= (uint32_t)(32 + sx) << 8 * b;
+      }
+      __syncwarp();
+      if (lane == 0) s_units[warp] = now;
+      __syncwarp();
+      if (now != kUsual) limit = kAlways;
+    }
     if (__builtin_expect(redo, 0)) {
       // tokens that are not there, or beyond a query's limit
       const int left = seg.w - sh.Nq + 1 - seg.z - sub * TT * 16;  // of the first query's
@@ -1059,20 +1142,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             s23[u][b] &= ~no_number(s23[u][b]);
           }
       }
-      // larger scales: p s stays below 2^16 while all are below 2^(1 + sx)
-      __half2 s_max = bits_half2(0);
-#pragma unroll
-      for (int u = 0; u < TT; ++u)
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          s_max = __hmax2(s_max, __hmax2(bits_half2(s01[u][b]), bits_half2(s23[u][b])));
-      float s_top = fmaxf(__low2float(s_max), __high2float(s_max));
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1)
-        s_top = fmaxf(s_top, __shfl_xor_sync(0xffffffffu, s_top, d));
-      const int now = max(sx, min((int)(__float_as_uint(s_top) >> 23) - 127, 16));
       // the references, in reach of the largest score
-      const float x_max = (float)(14 - now);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -1084,8 +1154,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 #pragma unroll
           for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
           const float was = nref[nt][j];
-          nref[nt][j] -= (float)(now - sx);
-          if (top + nref[nt][j] > x_max) nref[nt][j] = x_max - 3.f - top;
+          if (top + nref[nt][j] > kTop) nref[nt][j] = kTop - 3.f - top;
           const float f = ex2(nref[nt][j] - was);
           sum[nt][j] *= f;
           om[nt][j] *= f;
@@ -1097,10 +1166,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
               o[nt][b][m][2 + j] *= f;
             }
         }
-      sx = now;
       exponents();
-      weights();
     }
+    weights();
     ready = __all_sync(0xffffffffu, tc::mbar_test_wait(&bar_full[stage], phase)) != 0;
     // ---------------- values ----------------
     // The products start from zero every time and are added on their own: the tensor
@@ -1168,6 +1236,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 
     // ---------------- end of the segment, or of the CTA's part of it ----------------
     const int hg = seg.y / sh.NRC, rc = seg.y - hg * sh.NRC, head = hg * HG + h;
+    const uint32_t units = s_units[warp];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -1180,6 +1249,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       // which its byte held too; plus sum p m
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
+        const float unit = __int_as_float((127 + 24 - 32 + (int)(units >> 8 * b & 63)) << 23);
         const float m0 = __shfl_sync(0xffffffffu, om[nt][0], 4 * b + t);
         const float m1 = __shfl_sync(0xffffffffu, om[nt][1], 4 * b + t);
 #pragma unroll
@@ -1188,10 +1258,10 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             o[nt][b][m][2] -= o[nt][b][m][0];
             o[nt][b][m][3] -= o[nt][b][m][1];
           }
-          o[nt][b][m][0] = fmaf(o[nt][b][m][0], 16777216.f, m0);
-          o[nt][b][m][1] = fmaf(o[nt][b][m][1], 16777216.f, m1);
-          o[nt][b][m][2] = fmaf(o[nt][b][m][2], 1048576.f, m0);
-          o[nt][b][m][3] = fmaf(o[nt][b][m][3], 1048576.f, m1);
+          o[nt][b][m][0] = fmaf(o[nt][b][m][0], unit, m0);
+          o[nt][b][m][1] = fmaf(o[nt][b][m][1], unit, m1);
+          o[nt][b][m][2] = fmaf(o[nt][b][m][2], 0.0625f * unit, m0);
+          o[nt][b][m][3] = fmaf(o[nt][b][m][3], 0.0625f * unit, m1);
         }
       }
     }
