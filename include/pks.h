@@ -690,7 +690,8 @@ typedef struct pks_q4_attention_args {
   int32_t k;              /* pks_q4_sparse_attention: entries a list, 1..65536; else 0 */
   int32_t trim;           /* as in pks_mla_args; pks_q4_sparse_attention only */
   int32_t wait_limit;     /* as in pks_mla_args */
-  float sm_scale;         /* 0 = 1 / sqrt(D) */
+  float sm_scale;         /* 0 = 1 / sqrt(D).  sm_scale times the largest value of a query
+                             row is below 2^121: else its scores may be too small */
   int32_t reserved;       /* must be 0 */
   const int32_t* seq_lens;      /* device int32 [B] */
   const int32_t* block_table;   /* device int32 [B, max_pages] */

@@ -124,6 +124,28 @@ def test_sm_scale():
     b.sparse(20, sm_scale=0.01)
 
 
+@pytest.mark.parametrize("sm_scale", [1e-12, 1e-17, 1e-20, 1e-30, 1e-38, 1e-44])
+@pytest.mark.parametrize("q_scale", [0.0, 1e-30, 1.0])
+def test_small_sm_scale(sm_scale, q_scale):
+    """Scores that are all but 0: the mean of the tokens that are there."""
+    b = Batch(LENS, 16, 2, 4, 64, 2, seed=25, q_scale=q_scale)
+    b.dense(sm_scale=sm_scale, causal=True)
+    b.sparse(20, holes=True, sm_scale=sm_scale)
+
+
+@pytest.mark.parametrize("q_scale,sm_scale", [(1e37, 0.0), (3e38, 0.0), (1e37, 1e-37), (1e38, 1e-38),
+                                              (1.0, 1e38), (1e-30, 1e30), (1.0, 3e38)])
+def test_large_queries_and_sm_scale(q_scale, sm_scale):
+    """Keys of 0 have scores of 0, and sizes of queries and sm_scale may cancel."""
+    b = Batch([37, 300], 16, 2, 4, 64, 2, seed=26)
+    b.q = (b.q.float().clamp(-1, 1) * q_scale).to(torch.bfloat16)
+    cancel = 0 < q_scale * sm_scale < 10
+    if not cancel:
+        b.k.zero_()
+        b.write()
+    b.dense(sm_scale=sm_scale, causal=True)
+
+
 @pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
 def test_tokens_that_a_query_does_not_see_are_without_influence(what):
     """The last of four drafted tokens has no finite K and V: the three queries before it see

@@ -884,8 +884,13 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         }
 #pragma unroll
         for (int b = 0; b < NB; ++b) qs[nt][b] = piece[b] << 16;
-        // scores in powers of two
-        const float mine_c = __int_as_float((127 + min(6 + e2, 128)) << 23) * scale_log2;
+        // scores in powers of two; never 0 or infinite, so that a product with it is a number
+        // where a score is 0 and minus infinity where a token does not count (a score times
+        // 2^-126 is nothing beside the others)
+        const int c2 = 6 + e2;
+        const float c = scale_log2 * __int_as_float((127 + (c2 >> 1)) << 23) *
+                        __int_as_float((127 + c2 - (c2 >> 1)) << 23);
+        const float mine_c = fminf(fmaxf(c, 1.17549435e-38f), 3.40282347e38f);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           cs[nt][j] = __shfl_sync(0xffffffffu, mine_c, (2 * t + j) * 4);
