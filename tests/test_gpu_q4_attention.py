@@ -176,6 +176,35 @@ def test_tokens_that_a_query_does_not_see_are_without_influence(what):
     assert bool(out[2, :3].isfinite().all())
 
 
+@pytest.mark.parametrize("s", [0xffff, 0x7c00, 0xfc00, 0x3800])
+@pytest.mark.parametrize("m", [0xffff, 0x7c00, 0xfc00, 0x3800])
+@pytest.mark.parametrize("Hkv,G,D", [(2, 2, 64), (8, 4, 128), (5, 4, 128), (1, 1, 128)])
+def test_bytes_that_a_query_does_not_see_are_without_influence(s, m, Hkv, G, D):
+    """The pairs of the last of four drafted tokens, raw in its pages: scales and minima that a
+    write never stores, in all groups or in one."""
+    lens = [37, 80, 4, 33]
+    b = Batch(lens, 16, Hkv, G, D, 4, seed=27)
+    att = Q4Attention(b.len_d, b.table, b.q, b.cache, causal=True, lse=True)
+    want, want_lse = att().clone(), att.lse.clone()
+    pair = torch.tensor([s & 255, s >> 8, m & 255, m >> 8], dtype=torch.uint8, device="cuda")
+    rec = D // 2 + D // 8
+    for r, n in enumerate(lens):
+        at = b.tab[r, (n - 1) // 16], (n - 1) % 16
+        for pool in (b.cache.k, b.cache.v):
+            row = pool[at]
+            for i in range(D // 32 if r % 2 == 0 else 1):
+                o = (Hkv - 1) * rec + D // 2 + 4 * i
+                row[o:o + 4] = pair
+    out = att()
+    assert torch.equal(out[:, :3], want[:, :3]) and torch.equal(att.lse[:, :3], want_lse[:, :3])
+    heads = (Hkv - 1) * G
+    assert torch.equal(out[:, 3, :heads], want[:, 3, :heads])
+    if s != 0x3800 or m != 0x3800:
+        assert not out[:, 3, heads:, :32].isfinite().any()
+    else:
+        assert bool(out.isfinite().all())
+
+
 def test_queries_that_are_not_finite_stay_their_own():
     b = Batch([50], 16, 2, 4, 64, seed=11)
     q = b.q.clone()

@@ -171,14 +171,13 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 h) {
 __device__ __forceinline__ __half2 bits_half2(uint32_t u) {
   return *reinterpret_cast<const __half2*>(&u);
 }
-// all ones where a half is NaN
-__device__ __forceinline__ uint32_t no_number(uint32_t u) {
-  return ~__heq2_mask(bits_half2(u), bits_half2(u));
+// all ones where a half is NaN or infinite
+__device__ __forceinline__ uint32_t infinite(uint32_t u) {
+  return __vcmpgeu2(u & 0x7fff7fffu, 0x7c007c00u);
 }
 // the halves' sizes, 0 for those that are not finite
 __device__ __forceinline__ uint32_t finite(uint32_t u) {
-  u &= 0x7fff7fffu;
-  return u & __vcmpltu2(u, 0x7c007c00u);
+  return u & 0x7fff7fffu & ~infinite(u);
 }
 __device__ __forceinline__ float low_half(uint32_t u) {
   return __half2float(__low2half(bits_half2(u)));
@@ -1109,28 +1108,43 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
             if (!on1 || tok1 >= lim) tot[u][nt][2 + j] = kNegInf;
           }
       }
-      // at an edge, an s without a number must not reach the queries that do not see it: it goes
-      // straight to the sums of those that do
-      if (flags & kEdge && __any_sync(0xffffffffu, any & 0x40004000u)) {
+      // at an edge, an s or m that is not finite must not reach the queries that do not see its
+      // token: it goes straight to the sums of those that do
+      uint32_t bad_m = 0;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          uint32_t hit = 0;  // by groups, for column g
+      for (int u = 0; u < TT; ++u) bad_m |= infinite(ma0[u]) | infinite(ma2[u]);
+      if (flags & kEdge && __any_sync(0xffffffffu, (any & 0x40004000u) | bad_m)) {
+        uint32_t hit[NT] = {};  // by groups, for column g
 #pragma unroll
-          for (int u = 0; u < TT; ++u) {
+        for (int u = 0; u < TT; ++u) {
+          uint32_t seen0[NT], seen1[NT];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
             auto seen = [&](int e) {
               return movmatrix_t((tot[u][nt][e] == kNegInf ? 0u : 0xffffu) |
                                  (tot[u][nt][e + 1] == kNegInf ? 0u : 0xffff0000u));
             };
-            const uint32_t seen0 = seen(0), seen1 = seen(2);
-#pragma unroll
-            for (int b = 0; b < NB; ++b)
-              if ((seen0 & no_number(s01[u][b])) | (seen1 & no_number(s23[u][b]))) hit |= 1u << b;
+            seen0[nt] = seen(0);
+            seen1[nt] = seen(2);
           }
-          hit |= __shfl_xor_sync(0xffffffffu, hit, 1);
-          hit |= __shfl_xor_sync(0xffffffffu, hit, 2);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {  // (the lanes of row b have its m)
+            const uint32_t bad0 = infinite(s01[u][b]) |
+                                  infinite(__shfl_sync(0xffffffffu, ma0[u], 4 * b + t));
+            const uint32_t bad1 = infinite(s23[u][b]) |
+                                  infinite(__shfl_sync(0xffffffffu, ma2[u], 4 * b + t));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              if ((seen0[nt] & bad0) | (seen1[nt] & bad1)) hit[nt] |= 1u << b;
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          hit[nt] |= __shfl_xor_sync(0xffffffffu, hit[nt], 1);
+          hit[nt] |= __shfl_xor_sync(0xffffffffu, hit[nt], 2);
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const uint32_t mine = __shfl_sync(0xffffffffu, hit, (2 * t + j) * 4);
+            const uint32_t mine = __shfl_sync(0xffffffffu, hit[nt], (2 * t + j) * 4);
 #pragma unroll
             for (int b = 0; b < NB; ++b)
               if (mine >> b & 1)
@@ -1140,12 +1154,15 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           }
         }
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
+        for (int u = 0; u < TT; ++u) {
+          ma0[u] &= ~infinite(ma0[u]);
+          ma2[u] &= ~infinite(ma2[u]);
 #pragma unroll
           for (int b = 0; b < NB; ++b) {
-            s01[u][b] &= ~no_number(s01[u][b]);
-            s23[u][b] &= ~no_number(s23[u][b]);
+            s01[u][b] &= ~infinite(s01[u][b]);
+            s23[u][b] &= ~infinite(s23[u][b]);
           }
+        }
       }
       // the references, in reach of the largest score
 #pragma unroll
