@@ -663,8 +663,9 @@ typedef struct pks_q4_rows_args {
  * the ranges above. */
 pks_status pks_q4_write(const pks_q4_rows_args* args, pks_stream stream);
 
-/* The values that cached rows stand for, rounded once to the type of k and v.  A
- * row without a place is left as it was.  One launch; errors as above. */
+/* The values that cached rows stand for, m + s n rounded to fp32 and from there to
+ * the type of k and v.  A row without a place is left as it was.  One launch; errors
+ * as above. */
 pks_status pks_q4_read(const pks_q4_rows_args* args, pks_stream stream);
 
 /* Attention over a 4-bit cache.  For every request b, query token i and head h
@@ -676,7 +677,9 @@ pks_status pks_q4_read(const pks_q4_rows_args* args, pks_stream stream);
  *    (>= 0, each < len_b), in any order; -1 entries are skipped, and a position
  *    that stands there twice counts twice.
  * A query without tokens gets zeros.  Tokens that a query does not attend to are
- * without influence on it, whatever they hold. */
+ * without influence on it, whatever they hold; a drafted token with scales s of 2 and
+ * more can only move what the queries before it make of the 32 tokens around it, by
+ * 2^-18 of its largest s. */
 typedef struct pks_q4_attention_args {
   int32_t B;              /* requests; B * Nq <= 4096, and below 2^31 in all: 16-token
                              pieces that a full batch has, times groups of eight KV heads and
@@ -711,7 +714,9 @@ typedef struct pks_q4_attention_args {
 /* Workspace bytes for these shapes on the current device (pointers may be NULL). */
 pks_status pks_q4_workspace_size(const pks_q4_attention_args* args, size_t* bytes);
 
-/* Two launches each.  INVALID for NULL or misaligned pointers and shapes that are
+/* Two launches each, one where the shapes allow few and short segments only (a
+ * segment: a request, or one of its lists, with up to eight KV heads and sixteen
+ * query rows a head).  INVALID for NULL or misaligned pointers and shapes that are
  * no shapes (a k other than 0 in the first, or 0 in the second, among them),
  * UNSUPPORTED for shapes outside the ranges above, WORKSPACE for a missing,
  * misaligned or too small workspace. */

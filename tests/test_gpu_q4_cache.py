@@ -170,6 +170,22 @@ def test_groups_that_are_hard_to_round(dtype):
     check_read(cache, lens, table, starts, torch.float32)
 
 
+def test_a_value_is_rounded_to_fp32_and_from_there():
+    """m + s n = 1.00390625 + 2^-24, which lies above the middle of two bf16 numbers: fp32 rounds
+    it to that middle."""
+    cache = Q4Cache(1, 16, 1, 64)
+    x = torch.full((1, 1, 64), 2.0 ** -24, device="cuda")
+    x[0, 0, 0], x[0, 0, 32] = 15 * 1.00390625, 1.00390625
+    x[0, 0, 1] = x[0, 0, 33] = 1.00390625
+    cache.write(x, x, i32([1]), i32([[0]]), i32([0, 1]))
+    _, s, m = ref.unpack(cache.k.cpu().numpy(), 1, 64, "k")
+    assert s[0, 0, 0, 0] == 1.00390625 and m[0, 0, 0, 0] == 2.0 ** -24
+    for dtype, want in (("fp32", 1.00390625), ("fp16", 1.00390625), ("bf16", 1.0)):
+        out = torch.empty((2, 1, 1, 64), dtype=TYPES[dtype], device="cuda")
+        cache.read(i32([1]), i32([[0]]), i32([0, 1]), out[0], out[1])
+        assert float(out[0, 0, 0, 1]) == float(out[1, 0, 0, 1]) == want
+
+
 def border_rows(dtype, seed, n=600):
     """Rows of a group each whose minimum is small beside its scale, and whose values stand at
     the borders between two codes, rounded to the type, or next to them."""

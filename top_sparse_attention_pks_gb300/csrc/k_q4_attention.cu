@@ -15,7 +15,8 @@
 //  - K: bf16, the queries scaled by a power of two, so that all products are exact.
 //    Each group's sum is scaled by s_b on its own (fp32); the m_b Q_b of two groups are
 //    one more MMA, with the (s, m) pairs as they lie against 0 and Q_b, which is cut into
-//    three fp16 pieces (33 bits), one a lane (m taken out of the pairs: 420 us for 413).
+//    fp16 pieces, one a lane: two of them to 2^-24 of what 32 queries of the largest size
+//    sum up to, the third what is left of large sums (m taken out of the pairs: 420 us for 413).
 //  - V: fp16.  p is rounded to fp16, and p s once a group (by 2^-11 of it at most while
 //    they are normal numbers: kTop and what follows there).  sum p m is one more MMA.
 // Maxima, sums, scores and accumulators are fp32.
