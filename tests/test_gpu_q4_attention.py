@@ -352,6 +352,49 @@ def test_graphs_that_share_a_workspace_and_follow_lengths():
             sel.device_error()
 
 
+def test_graphs_that_share_a_workspace_and_join_parts():
+    """Two objects whose segments several CTAs hold, so that both write the plan and the parts of
+    the one workspace, replayed in turn with lengths that change in between."""
+    b = Batch([9000, 5001, 77, 0, 3000], 16, 8, 4, 128, 2, seed=28)
+    lists = b.lists(2500, seed=28)
+    att = Q4Attention(b.len_d, b.table, b.q, b.cache, causal=True, lse=True)
+    sel = Q4SparseAttention(b.len_d, b.table, i32(lists), b.q, b.cache, trim=True, lse=True)
+    ws = torch.zeros(max(a.workspace.numel() for a in (att, sel)), dtype=torch.uint8, device="cuda")
+    for a in (att, sel):
+        a.workspace = ws
+        a.args.workspace, a.args.workspace_bytes = ws.data_ptr(), ws.numel()
+    graphs = []
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for a in (att, sel):
+        a()
+        assert bool((ws[256:] != 0).any())  # (the plan and the parts, not the error word alone)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            a()
+        graphs.append(g)
+    full = b.lens
+    for cut in (0, 1, 2500, 4000, 0):
+        b.lens = [max(0, n - cut) for n in full]
+        b.len_d.copy_(i32(b.lens))
+        short = [[t[:min(2500, n)] for t in rows] for rows, n in zip(lists, b.lens)]
+        for order in ((0, 1), (1, 0)):
+            for a in (att, sel):
+                a.out.fill_(float("nan"))
+                a.lse.fill_(float("nan"))
+            for i in order:
+                graphs[i].replay()
+            torch.cuda.synchronize()
+            now, b.lens = b.lens, full
+            dense = [[np.arange(max(0, n - 1 + i)) for i in range(2)] for n in now]
+            b.check(att.out, att.lse, lists=dense)
+            b.check(sel.out, sel.lse, lists=[[t[t < n] for t in rows]
+                                             for rows, n in zip(short, now)])
+            b.lens = now
+        sel.device_error()
+        b.lens = full
+
+
 def test_further_layers():
     """One object over the queries and caches of several layers."""
     b, c = (Batch([100, 30], 16, 2, 4, 64, seed=s) for s in (15, 15))
