@@ -134,7 +134,8 @@ def test_small_sm_scale(sm_scale, q_scale):
 
 
 @pytest.mark.parametrize("q_scale,sm_scale", [(1e37, 0.0), (3e38, 0.0), (1e37, 1e-37), (1e38, 1e-38),
-                                              (1.0, 1e38), (1e-30, 1e30), (1.0, 3e38)])
+                                              (1.0, 1e38), (1e-30, 1e30), (1.0, 3e38),
+                                              (1e-32, 1e32), (1e-37, 1e37), (3e-39, 1e38)])
 def test_large_queries_and_sm_scale(q_scale, sm_scale):
     """Keys of 0 have scores of 0, and sizes of queries and sm_scale may cancel."""
     b = Batch([37, 300], 16, 2, 4, 64, 2, seed=26)

@@ -845,8 +845,8 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           for (int e = 0; e < 8; ++e) big = fmaxf(big, fabsf(x[b][e]));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 1));
         big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        // the row times 2^p, here its largest value in [2^120, 2^121)
-        const int e2 = max((int)(__float_as_uint(big) >> 23) - 127, -100);
+        // the row times 2^p, here its largest value in [2^120, 2^121) (or below, from 2^-126 on)
+        const int e2 = max((int)(__float_as_uint(big) >> 23) - 127, -126);
         const int p = 120 - e2;
         const float f1 = __int_as_float((127 + (p >> 1)) << 23);
         const float f2 = __int_as_float((127 + p - (p >> 1)) << 23);
