@@ -7,11 +7,11 @@ looked at once in two rounds.
  - p is rounded to fp16 and p s again: 2^-11 of each, so 2^-10 size.  p is at least 2^11 at the
    largest score, so what is lost below fp16's normal numbers is 2^-36 of the largest weight, which
    is 1 at most: 2^-36 (|m| + 15 s) a token.
- - p s likewise, in the unit of its stage: 2^-36 15 units a token.  The unit is 8 times the stage's
-   largest s at most; or it is 1, and then some s where they were last looked at is 2^-7 or more,
-   which is within 6144 tokens before the stage's end.
- - s in that unit, when it is 2 or more: 2^-25 2^3 of the stage's largest s, times 15 and the
-   stage's weight.
+ - p s likewise, in the unit of its stage: 2^-36 15 units a token.  The unit is 8 times the
+   largest s at most of where they were last looked at, which is within 6144 tokens before the
+   stage's end; or it is 1, and then some s there is 2^-7 or more, 2^-11 where the
+   request has up to 65536 tokens; or it is 2^-15.
+ - s in that unit, when it is 2 or more: 2^-25 of it, times 15 and the stage's weight.
  - the result is rounded to bf16: 2^-8 of itself; fp32 sums and exponentials: 2^-12 size.
  - scores off by 2^-20 of mag = sum |q| (|m| + s n) move every weight by as much: 2 size times that.
 """
@@ -75,11 +75,12 @@ def check(b, out, lse, lists=None, causal=False, sm_scale=0.0):
             # (of all tokens there, also those that this query does not see)
             all_s = s[b.starts[r]:b.starts[r] + n] if lists is None else s[at]
             all_i = torch.arange(n, device="cuda") if lists is None else index
-            top = largest(all_s, all_i // 32)[index // 32]  # of the token's stage
             near = largest(all_s, all_i // 6144)
             near[1:] = torch.maximum(near[1:], near[:-1].clone())
-            unit = torch.maximum(8 * top, (2.0 ** 7 * near[index // 6144]).clamp_max(1.0))
-            w = torch.einsum("hgt,thb->hgb", p, top) * (15 * 2.0 ** -22)
+            near = near[index // 6144]
+            small = 2.0 ** (7 if (n if lists is None else len(lists[r][i])) > 65536 else 11)
+            unit = torch.maximum(8 * near, (small * near).clamp(2.0 ** -15, 1.0))
+            w = torch.einsum("hgt,thb->hgb", p, unit * (unit > 1)) * (15 * 2.0 ** -25)
             lost = ((m[at] + 15 * s[at] + 15 * unit) * 2.0 ** -36).sum(0)
             tol = (2.0 ** -10 + 2.0 ** -12 + 2 * 2.0 ** -20 * mag[..., None]) * size
             tol = tol + 2.0 ** -8 * want.abs()

@@ -77,17 +77,22 @@ constexpr float kNone = -3e38f;  // reference of a row that has seen no token
 // 2^-25 of the largest are normal numbers of fp16 still, and those above 2^-36 are not 0.  The
 // same has to hold for p s, whatever V's size.  So the sums of a group are in a unit 2^sx, by
 // which its scales are divided:
-//  - 1 while they have their usual size, the largest of a stage in [2^-kSmall, 2).  That none is
-//    2 is seen to at every stage, that some are large enough at one stage in two rounds of the
-//    ring (at every stage, in a few operations: 16 x 131072 tokens 407 us for 389);
-//  - else what brings the stage's largest scale into [1, 2), or, so that it seldom changes,
-//    within 2^-kKeep below.
-// What is lost of a token is so 15 2^-29 of the largest s that was looked at, 2^-9 of 15 s over
-// kLongSegment tokens; longer segments have a unit of their own at every stage.
+//  - 1 while they have their usual size, the largest of a stage below 2 and not below 2^-kSmall
+//    (2^-kSmallShort in segments of up to kShortSegment tokens).  That none is 2 is seen to at
+//    every stage, that some are large enough at one stage in two rounds of the ring (at every
+//    stage, in a few operations: 16 x 131072 tokens 407 us for 389);
+//  - else what brings the largest of such a stage into [1, 2), or, so that it seldom changes,
+//    within 2^-kKeep below, 2^-15 at the least; a larger one than 2 units moves it at once.
+// 16 x 131072 tokens with a unit other than 1 take 481 us for 394; worked out anew at every stage
+// 632 us; by a branch that scales before the scores 504.
+// What is lost of a token is so 15 2^-36 units at most, 2^-9 of 15 s over as many tokens as the
+// limits say; segments of more than kLongSegment tokens always have a unit of their own.
 constexpr float kTop = 14.f;
-constexpr int kSmall = 7, kKeep = 3, kLongSegment = 1 << 20;
-// What a warp keeps of it in shared memory: 32 + sx a byte, and kLong for such a segment
-constexpr uint32_t kUsual = 0x20202020u, kLong = 0x80000000u;
+constexpr int kSmall = 7, kSmallShort = 11, kKeep = 3;
+constexpr int kShortSegment = 1 << 16, kLongSegment = 1 << 20;
+// What a warp keeps of it in shared memory: 32 + sx a byte, kLong for such a segment, kAgain where
+// the next stage is looked at too
+constexpr uint32_t kUsual = 0x20202020u, kLong = 0x80000000u, kAgain = 0x40000000u;
 
 // Tokens of a warp's 16 as the rows of its MMA tiles, four bits each (lowest: row 0).
 // Lanes of one shared-memory access hold tokens whose records lie in different
@@ -171,6 +176,9 @@ __device__ __forceinline__ uint32_t half2_bits(__half2 h) {
 }
 __device__ __forceinline__ __half2 bits_half2(uint32_t u) {
   return *reinterpret_cast<const __half2*>(&u);
+}
+__device__ __forceinline__ int unit_of(uint32_t units, int b) {  // sx of group b
+  return (int)(units >> 8 * b & 63) - 32;
 }
 // all ones where a half is NaN or infinite
 __device__ __forceinline__ uint32_t infinite(uint32_t u) {
@@ -283,6 +291,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   __shared__ __align__(8) uint64_t bar_full[kMaxStages], bar_empty[kMaxStages], bar_join;
   __shared__ StageNote s_note[kMaxStages];
   __shared__ int s_row_all[4][kMaxTokens];  // tokens' rows in the pool (-1: none)
+  __shared__ __align__(16) uint32_t s_by_unit[NW][NB];
   __shared__ uint32_t s_units[NW];
   __shared__ int s_warp[NWARPS], s_first, s_rest, s_lo, s_count, s_abort;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -809,7 +818,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       fresh = false;
       limit = kAlways;
       __syncwarp();
-      if (lane == 0) s_units[warp] = kUsual | (s_nv[q_v] > kLongSegment ? kLong : 0);
+      if (lane == 0) s_units[warp] = kUsual | (s_nv[q_v] > kLongSegment ? kLong | kAgain : 0);
       __syncwarp();
       const int hg = q_c / sh.NRC, rc = q_c - hg * sh.NRC;
       const int head = hg * HG + h;
@@ -1035,25 +1044,50 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
                       all != 0xffffu || (flags & kEdge);
     bool redo = false, rescale = false;
     if (__builtin_expect(look, 0)) {
-      const uint32_t units = s_units[warp];
       redo = __any_sync(0xffffffffu, x_top > kTop) || all != 0xffffu || (flags & kEdge);
-      bool unusual = any & 0x40004000u, none = false;
+      const uint32_t units = s_units[warp];
+      limit = kTop;
+      if (units == kUsual || (units & kAgain) || (stage == 0 && phase)) {
+        // (one of these bits is set from 2^-kSmall on, or 2^-kSmallShort)
+        const uint32_t least = seg.w > kShortSegment ? 0x60006000u : 0x70007000u;
+        bool unusual = any & 0x40004000u;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t y = 0;
+        for (int b = 0; b < NB; ++b) {
+          uint32_t y = 0;
 #pragma unroll
-        for (int u = 0; u < TT; ++u) y |= s01[u][b] | s23[u][b];
-        unusual |= y && !(y & 0x60006000u);  // (2^-kSmall and more have one of these bits)
-        none |= y == 0;
+          for (int u = 0; u < TT; ++u) y |= s01[u][b] | s23[u][b];
+          unusual |= !(y & least) && (y || all == 0xffffu);  // (0: of tokens that are not there)
+        }
+        rescale = __any_sync(0xffffffffu, unusual) || units != kUsual;
+      } else {  // in the units at hand, if nothing is too large for them
+        uint32_t f[NB];
+        lds(reinterpret_cast<const uint8_t*>(s_by_unit[warp]), f);
+        bool over = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          uint32_t top = 0;
+#pragma unroll
+          for (int u = 0; u < TT; ++u) top = __vmaxu2(top, __vmaxu2(s01[u][b], s23[u][b]));
+          over |= __vcmpgeu2(top, 0x7c007c00u - f[b]) != 0;
+        }
+        rescale = __any_sync(0xffffffffu, over);
+        if (!rescale) {
+#pragma unroll
+          for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int u = 0; u < TT; ++u) {
+              s01[u][b] = half2_bits(__hmul2(bits_half2(s01[u][b]), bits_half2(f[b])));
+              s23[u][b] = half2_bits(__hmul2(bits_half2(s23[u][b]), bits_half2(f[b])));
+            }
+          limit = kAlways;
+        }
       }
-      rescale = __any_sync(0xffffffffu, unusual) || units != kUsual;
-      limit = __any_sync(0xffffffffu, none) ? kAlways : kTop;
     }
     if (__builtin_expect(rescale, 0)) {
-      // A unit for each group of this stage, 2^sx, so that its largest s is in [1, 2) of it (or
-      // within kKeep below, if the unit was good before; 1 for usual sizes).
       const uint32_t units = s_units[warp];
-      uint32_t now = (units & kLong) | (kUsual & (NB == 2 ? 0xffff0000u : 0));
+      const int least = seg.w > kShortSegment ? -kSmall : -kSmallShort;
+      uint32_t now = units & kLong;
+      if constexpr (NB == 2) now |= kUsual & 0xffff0000u;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         uint32_t top = 0;
@@ -1063,28 +1097,27 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
         top = max(top >> 16, top & 0xffffu);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int was = (int)(units >> 8 * b & 63) - 32;
-        const int e = (int)(__float_as_uint(low_half(top)) >> 23) - 127;
+        const int was = unit_of(units, b);
+        const int e = max((int)(__float_as_uint(low_half(top)) >> 23) - 127, -15);
         int sx = e;
-        if (top == 0 || (e <= was && e >= was - kKeep)) sx = was;
-        else if (e <= 0 && e >= -kSmall && !(units & kLong)) sx = 0;
+        if (e <= was && e >= was - kKeep) sx = was;
+        else if (e <= 0 && e >= least && !(units & kLong)) sx = 0;
+        now |= (uint32_t)(32 + sx) << 8 * b;
         if (sx != was) {
           const float f = __int_as_float((127 + was - sx) << 23);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 8; ++i) o[nt][b][i >> 2][i & 3] *= f;
+          if (sx > was) now |= kAgain;  // (a single large one does not set the unit for long)
         }
-        // times 2^-sx, in two steps as 2^24 is no fp16
-        const int f0 = min(max(-sx, -14), 15), f1 = -sx - f0;
-        const __half2 h0 = bits_half2((uint32_t)(f0 + 15) * 0x04000400u);
-        const __half2 h1 = bits_half2((uint32_t)(f1 + 15) * 0x04000400u);
+        const uint32_t f = sx == 15 ? 0x02000200u : (uint32_t)(15 - sx) * 0x04000400u;
+        if (lane == 0) s_by_unit[warp][b] = f;
 #pragma unroll
         for (int u = 0; u < TT; ++u) {
-          s01[u][b] = half2_bits(__hmul2(__hmul2(bits_half2(s01[u][b]), h0), h1));
-          s23[u][b] = half2_bits(__hmul2(__hmul2(bits_half2(s23[u][b]), h0), h1));
+          s01[u][b] = half2_bits(__hmul2(bits_half2(s01[u][b]), bits_half2(f)));
+          s23[u][b] = half2_bits(__hmul2(bits_half2(s23[u][b]), bits_half2(f)));
         }
-        now |= (uint32_t)(32 + sx) << 8 * b;
       }
       __syncwarp();
       if (lane == 0) s_units[warp] = now;
@@ -1272,7 +1305,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       // which its byte held too; plus sum p m
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        const float unit = __int_as_float((127 + 24 - 32 + (int)(units >> 8 * b & 63)) << 23);
+        const float unit = __int_as_float((127 + 24 + unit_of(units, b)) << 23);
         const float m0 = __shfl_sync(0xffffffffu, om[nt][0], 4 * b + t);
         const float m1 = __shfl_sync(0xffffffffu, om[nt][1], 4 * b + t);
 #pragma unroll
