@@ -30,7 +30,7 @@
 //
 // Bound by memory where the tokens are many (16 x 131072 tokens of eight heads of 128, eight
 // queries a head: 388 us, 6.9 TB/s of codes), else by what the consumers issue: a head's 32
-// tokens take 1750 cycles from L2 (2640 with sixteen queries a head), of which the tensor
+// tokens take 1750 cycles from L2 (2780 with sixteen queries a head), of which the tensor
 // pipe is busy for a third and the integer pipe, which takes the codes apart, for half.
 // Measured against it:
 //  - sixteen consumer warps of half the registers, queries in shared memory: 468 us for 434;
@@ -58,9 +58,9 @@ constexpr int kConsumers = 8;  // warps, two a scheduler
 // 42, 20 50 both, 27 67 and 65, 54 95 and 89, 108 163 and 144.
 constexpr int kLongRun = 24;  // stages a CTA above which there are eight
 // Stages up to which a CTA has a segment to itself, without a plan and parts to join: four, and
-// one more for every sixteen segments.  5 requests of 2 stages 6.8 us and 8.5 split, of 4 8.9
-// and 8.6, of 6 10.6 and 8.6; 16 of 4 9.2 and 10.3, of 8 12.6 and 12.0; 64 lists of 8 14.0 and
-// 19.3.
+// one more for every sixteen segments.  5 requests of 2 stages 6.9 us and 8.6 split, of 4 8.9
+// and 8.8, of 5 10.4 and 8.9; 16 of 5 10.6 and 11.7, of 8 13.7 and 12.2; 64 lists of 8 13.9 and
+// 19.1.
 constexpr int kWholeStages = 4, kWholeMore = 16;
 constexpr int kMaxTokens = 256;  // of a stage
 constexpr int kMaxStages = 12;
@@ -83,7 +83,7 @@ constexpr float kNone = -3e38f;  // reference of a row that has seen no token
 //    stage, in a few operations: 16 x 131072 tokens 407 us for 389);
 //  - else what brings the largest of such a stage into [1, 2), or, so that it seldom changes,
 //    within 2^-kKeep below, 2^-15 at the least; a larger one than 2 units moves it at once.
-// 16 x 131072 tokens with a unit other than 1 take 481 us for 394; worked out anew at every stage
+// 16 x 131072 tokens with a unit other than 1 take 485 us for 388; worked out anew at every stage
 // 632 us; by a branch that scales before the scores 504.
 // What is lost of a token is so 15 2^-36 units at most, 2^-9 of 15 s over as many tokens as the
 // limits say; segments of more than kLongSegment tokens always have a unit of their own.
@@ -1042,9 +1042,9 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
       for (int b = 0; b < NB; ++b) any |= s01[u][b] | s23[u][b];
     const bool look = __any_sync(0xffffffffu, !(x_top <= limit) || (any & 0x40004000u)) ||
                       all != 0xffffu || (flags & kEdge);
-    bool redo = false, rescale = false;
     if (__builtin_expect(look, 0)) {
-      redo = __any_sync(0xffffffffu, x_top > kTop) || all != 0xffffu || (flags & kEdge);
+      bool rescale;
+      const bool redo = __any_sync(0xffffffffu, x_top > kTop) || all != 0xffffu || (flags & kEdge);
       const uint32_t units = s_units[warp];
       limit = kTop;
       if (units == kUsual || (units & kAgain) || (stage == 0 && phase)) {
@@ -1082,149 +1082,154 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           limit = kAlways;
         }
       }
-    }
-    if (__builtin_expect(rescale, 0)) {
-      const uint32_t units = s_units[warp];
-      const int least = seg.w > kShortSegment ? -kSmall : -kSmallShort;
-      uint32_t now = units & kLong;
-      if constexpr (NB == 2) now |= kUsual & 0xffff0000u;
+      if (rescale) {
+        const uint32_t units = s_units[warp];
+        const int least = seg.w > kShortSegment ? -kSmall : -kSmallShort;
+        uint32_t now = units & kLong;
+        if constexpr (NB == 2) now |= kUsual & 0xffff0000u;
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        uint32_t top = 0;
+        for (int b = 0; b < NB; ++b) {
+          uint32_t top = 0;
 #pragma unroll
-        for (int u = 0; u < TT; ++u)
-          top = __vmaxu2(top, __vmaxu2(finite(s01[u][b]), finite(s23[u][b])));
-        top = max(top >> 16, top & 0xffffu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int was = unit_of(units, b);
-        const int e = max((int)(__float_as_uint(low_half(top)) >> 23) - 127, -15);
-        int sx = e;
-        if (e <= was && e >= was - kKeep) sx = was;
-        else if (e <= 0 && e >= least && !(units & kLong)) sx = 0;
-        now |= (uint32_t)(32 + sx) << 8 * b;
-        if (sx != was) {
-          const float f = __int_as_float((127 + was - sx) << 23);
+          for (int u = 0; u < TT; ++u)
+            top = __vmaxu2(top, __vmaxu2(finite(s01[u][b]), finite(s23[u][b])));
+          top = max(top >> 16, top & 0xffffu);
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+          top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+          const int was = unit_of(units, b);
+          const int e = max((int)(__float_as_uint(low_half(top)) >> 23) - 127, -15);
+          int sx = e;
+          if (e <= was && e >= was - kKeep) sx = was;
+          else if (e <= 0 && e >= least && !(units & kLong)) sx = 0;
+          now |= (uint32_t)(32 + sx) << 8 * b;
+          if (sx != was) {
+            const float f = __int_as_float((127 + was - sx) << 23);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) o[nt][b][i >> 2][i & 3] *= f;
+            if (sx > was) now |= kAgain;  // (a single large one does not set the unit for long)
+          }
+          const uint32_t f = sx == 15 ? 0x02000200u : (uint32_t)(15 - sx) * 0x04000400u;
+          if (lane == 0) s_by_unit[warp][b] = f;
+#pragma unroll
+          for (int u = 0; u < TT; ++u) {
+            s01[u][b] = half2_bits(__hmul2(bits_half2(s01[u][b]), bits_half2(f)));
+            s23[u][b] = half2_bits(__hmul2(bits_half2(s23[u][b]), bits_half2(f)));
+          }
+        }
+        __syncwarp();
+        if (lane == 0) s_units[warp] = now;
+        __syncwarp();
+        if (now != kUsual) limit = kAlways;
+      }
+      if (redo) {
+        // tokens that are not there, or beyond a query's limit
+        const int left = seg.w - sh.Nq + 1 - seg.z - sub * TT * 16;  // of the first query's
+        const int first = seg.y % sh.NRC * RC + 2 * t;
+#pragma unroll
+        for (int u = 0; u < TT; ++u) {
+          const bool on0 = mask[u] >> tok0 & 1, on1 = mask[u] >> tok1 & 1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) o[nt][b][i >> 2][i & 3] *= f;
-          if (sx > was) now |= kAgain;  // (a single large one does not set the unit for long)
+            for (int j = 0; j < 2; ++j) {
+              const int lim =
+                  (flags & kEdge ? left + min((first + nt * 8 + j) / sh.G, sh.Nq - 1) : 16 * TT) -
+                  16 * u;
+              if (!on0 || tok0 >= lim) tot[u][nt][j] = kNegInf;
+              if (!on1 || tok1 >= lim) tot[u][nt][2 + j] = kNegInf;
+            }
         }
-        const uint32_t f = sx == 15 ? 0x02000200u : (uint32_t)(15 - sx) * 0x04000400u;
-        if (lane == 0) s_by_unit[warp][b] = f;
+        // at an edge, an s or m that is not finite must not reach the queries that do not see its
+        // token: it goes straight to the sums of those that do
+        uint32_t bad_m = 0;
 #pragma unroll
-        for (int u = 0; u < TT; ++u) {
-          s01[u][b] = half2_bits(__hmul2(bits_half2(s01[u][b]), bits_half2(f)));
-          s23[u][b] = half2_bits(__hmul2(bits_half2(s23[u][b]), bits_half2(f)));
+        for (int u = 0; u < TT; ++u) bad_m |= infinite(ma0[u]) | infinite(ma2[u]);
+        if (flags & kEdge && __any_sync(0xffffffffu, (any & 0x40004000u) | bad_m)) {
+          uint32_t hit[NT] = {};  // by groups, for column g
+#pragma unroll
+          for (int u = 0; u < TT; ++u) {
+            uint32_t seen0[NT], seen1[NT];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              auto seen = [&](int e) {
+                return movmatrix_t((tot[u][nt][e] == kNegInf ? 0u : 0xffffu) |
+                                   (tot[u][nt][e + 1] == kNegInf ? 0u : 0xffff0000u));
+              };
+              seen0[nt] = seen(0);
+              seen1[nt] = seen(2);
+            }
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {  // (the lanes of row b have its m)
+              const uint32_t bad0 = infinite(s01[u][b]) |
+                                    infinite(__shfl_sync(0xffffffffu, ma0[u], 4 * b + t));
+              const uint32_t bad1 = infinite(s23[u][b]) |
+                                    infinite(__shfl_sync(0xffffffffu, ma2[u], 4 * b + t));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                if ((seen0[nt] & bad0) | (seen1[nt] & bad1)) hit[nt] |= 1u << b;
+            }
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            hit[nt] |= __shfl_xor_sync(0xffffffffu, hit[nt], 1);
+            hit[nt] |= __shfl_xor_sync(0xffffffffu, hit[nt], 2);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t mine = __shfl_sync(0xffffffffu, hit[nt], (2 * t + j) * 4);
+#pragma unroll
+              for (int b = 0; b < NB; ++b)
+                if (mine >> b & 1)
+#pragma unroll
+                  for (int m = 0; m < 2; ++m)
+                    o[nt][b][m][j] = o[nt][b][m][2 + j] = __int_as_float(0x7fc00000);
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < TT; ++u) {
+            ma0[u] &= ~infinite(ma0[u]);
+            ma2[u] &= ~infinite(ma2[u]);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+              s01[u][b] &= ~infinite(s01[u][b]);
+              s23[u][b] &= ~infinite(s23[u][b]);
+            }
+          }
         }
-      }
-      __syncwarp();
-      if (lane == 0) s_units[warp] = now;
-      __syncwarp();
-      if (now != kUsual) limit = kAlways;
-    }
-    if (__builtin_expect(redo, 0)) {
-      // tokens that are not there, or beyond a query's limit
-      const int left = seg.w - sh.Nq + 1 - seg.z - sub * TT * 16;  // of the first query's
-      const int first = seg.y % sh.NRC * RC + 2 * t;
-#pragma unroll
-      for (int u = 0; u < TT; ++u) {
-        const bool on0 = mask[u] >> tok0 & 1, on1 = mask[u] >> tok1 & 1;
+        // the references, in reach of the largest score
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const int lim =
-                (flags & kEdge ? left + min((first + nt * 8 + j) / sh.G, sh.Nq - 1) : 16 * TT) -
-                16 * u;
-            if (!on0 || tok0 >= lim) tot[u][nt][j] = kNegInf;
-            if (!on1 || tok1 >= lim) tot[u][nt][2 + j] = kNegInf;
-          }
-      }
-      // at an edge, an s or m that is not finite must not reach the queries that do not see its
-      // token: it goes straight to the sums of those that do
-      uint32_t bad_m = 0;
+            float top = kNegInf;
 #pragma unroll
-      for (int u = 0; u < TT; ++u) bad_m |= infinite(ma0[u]) | infinite(ma2[u]);
-      if (flags & kEdge && __any_sync(0xffffffffu, (any & 0x40004000u) | bad_m)) {
-        uint32_t hit[NT] = {};  // by groups, for column g
+            for (int u = 0; u < TT; ++u) top = fmaxf(top, fmaxf(tot[u][nt][j], tot[u][nt][2 + j]));
+            top *= cs[nt][j];
 #pragma unroll
-        for (int u = 0; u < TT; ++u) {
-          uint32_t seen0[NT], seen1[NT];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            auto seen = [&](int e) {
-              return movmatrix_t((tot[u][nt][e] == kNegInf ? 0u : 0xffffu) |
-                                 (tot[u][nt][e + 1] == kNegInf ? 0u : 0xffff0000u));
-            };
-            seen0[nt] = seen(0);
-            seen1[nt] = seen(2);
-          }
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {  // (the lanes of row b have its m)
-            const uint32_t bad0 = infinite(s01[u][b]) |
-                                  infinite(__shfl_sync(0xffffffffu, ma0[u], 4 * b + t));
-            const uint32_t bad1 = infinite(s23[u][b]) |
-                                  infinite(__shfl_sync(0xffffffffu, ma2[u], 4 * b + t));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              if ((seen0[nt] & bad0) | (seen1[nt] & bad1)) hit[nt] |= 1u << b;
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          hit[nt] |= __shfl_xor_sync(0xffffffffu, hit[nt], 1);
-          hit[nt] |= __shfl_xor_sync(0xffffffffu, hit[nt], 2);
-#pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const uint32_t mine = __shfl_sync(0xffffffffu, hit[nt], (2 * t + j) * 4);
+            for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const float was = nref[nt][j];
+            if (top + nref[nt][j] > kTop) nref[nt][j] = kTop - 3.f - top;
+            const float f = ex2(nref[nt][j] - was);
+            sum[nt][j] *= f;
+            om[nt][j] *= f;
 #pragma unroll
             for (int b = 0; b < NB; ++b)
-              if (mine >> b & 1)
 #pragma unroll
-                for (int m = 0; m < 2; ++m)
-                  o[nt][b][m][j] = o[nt][b][m][2 + j] = __int_as_float(0x7fc00000);
+              for (int m = 0; m < 2; ++m) {
+                o[nt][b][m][j] *= f;
+                o[nt][b][m][2 + j] *= f;
+              }
           }
-        }
-#pragma unroll
-        for (int u = 0; u < TT; ++u) {
-          ma0[u] &= ~infinite(ma0[u]);
-          ma2[u] &= ~infinite(ma2[u]);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            s01[u][b] &= ~infinite(s01[u][b]);
-            s23[u][b] &= ~infinite(s23[u][b]);
-          }
-        }
+        exponents();
       }
-      // the references, in reach of the largest score
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float top = kNegInf;
-#pragma unroll
-          for (int u = 0; u < TT; ++u) top = fmaxf(top, fmaxf(tot[u][nt][j], tot[u][nt][2 + j]));
-          top *= cs[nt][j];
-#pragma unroll
-          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-          const float was = nref[nt][j];
-          if (top + nref[nt][j] > kTop) nref[nt][j] = kTop - 3.f - top;
-          const float f = ex2(nref[nt][j] - was);
-          sum[nt][j] *= f;
-          om[nt][j] *= f;
-#pragma unroll
-          for (int b = 0; b < NB; ++b)
-#pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              o[nt][b][m][j] *= f;
-              o[nt][b][m][2 + j] *= f;
-            }
-        }
-      exponents();
+      if constexpr (!QSHARED) weights();
+    } else {
+      // (a second copy: one for both 1860 cycles a stage instead of 1750; where registers are
+      // short two cost more, 2900 for 2780)
+      if constexpr (!QSHARED) weights();
     }
-    weights();
+    if constexpr (QSHARED) weights();
     ready = __all_sync(0xffffffffu, tc::mbar_test_wait(&bar_full[stage], phase)) != 0;
     // ---------------- values ----------------
     // The products start from zero every time and are added on their own: the tensor
