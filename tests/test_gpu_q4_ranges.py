@@ -114,10 +114,10 @@ def dominated(n, share, v_scale, Hkv=1, G=2, D=128, Nq=1, page=64, at=10, seed=0
     return b
 
 
-def run(b, lists=None, causal=False):
+def run(b, lists=None, causal=False, copies=None):
     """Attention over a request for every SM, all over the same pages, so that a CTA has it whole
-    and what comes behind the dominant token is weighed against it."""
-    n = torch.cuda.get_device_properties(0).multi_processor_count
+    and what comes behind the dominant token is weighed against it; or over ``copies``."""
+    n = copies or torch.cuda.get_device_properties(0).multi_processor_count
     lens, table, q = (x.repeat_interleave(n, 0) for x in (b.len_d, b.table, b.q))
     if lists is None:
         att = Q4Attention(lens, table, q, b.cache, causal=causal, lse=True)
@@ -139,7 +139,7 @@ def test_a_dominant_token_beside_many(v_scale, share):
 
 @pytest.mark.parametrize("Hkv,G,D,page,Nq", [
     (8, 1, 128, 64, 1), (8, 4, 128, 16, 4), (2, 4, 64, 5, 1), (1, 16, 64, 16, 1),
-    (5, 12, 128, 16, 1), (16, 1, 64, 16, 1)])
+    (5, 12, 128, 16, 1), (16, 1, 64, 16, 1), (8, 16, 128, 64, 1)])
 @pytest.mark.parametrize("v_scale", [1e-4, 1e-6])
 def test_small_values_by_every_way_of_copying(Hkv, G, D, page, Nq, v_scale):
     b = dominated(20000, 0.9, v_scale, Hkv, G, D, Nq, page, seed=1)
@@ -154,7 +154,11 @@ def test_small_values_by_every_way_of_copying(Hkv, G, D, page, Nq, v_scale):
 @pytest.mark.parametrize("sizes", [(1.0, 1e-4, 1e-2, 1e-6), (1e4, 1.0, 1e-3, 1e-5),
                                    (1e-5, 1e-5, 1e4, 0.0), (2.0 ** -24, 1e-6, 1.0, 100.0)])
 def test_groups_of_different_sizes(sizes):
-    run(dominated(131072, 0.9, sizes, seed=3))
+    b = dominated(131072, 0.9, sizes, seed=3)
+    run(b)
+    run(b, copies=1)  # (every CTA a part of it, in units of its own)
+    b = dominated(9000, 0.5, sizes, G=16, at=5000, seed=3)
+    run(b, copies=1)
 
 
 @pytest.mark.parametrize("small,large", [(1e-4, 1.0), (1.0, 1e4), (1e-5, 1e4), (0.0, 1.0)])

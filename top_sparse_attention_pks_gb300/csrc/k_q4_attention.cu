@@ -30,7 +30,7 @@
 //
 // Bound by memory where the tokens are many (16 x 131072 tokens of eight heads of 128, eight
 // queries a head: 388 us, 6.9 TB/s of codes), else by what the consumers issue: a head's 32
-// tokens take 1750 cycles from L2 (2780 with sixteen queries a head), of which the tensor
+// tokens take 1750 cycles from L2 (2640 with sixteen queries a head), of which the tensor
 // pipe is busy for a third and the integer pipe, which takes the codes apart, for half.
 // Measured against it:
 //  - sixteen consumer warps of half the registers, queries in shared memory: 468 us for 434;
@@ -232,10 +232,15 @@ struct alignas(16) StageNote {
 constexpr uint32_t kLast = 1u << 16, kWhole = 2u << 16, kSecond = 4u << 16, kEdge = 8u << 16,
                    kEnd = 16u << 16;
 // Registers a thread of this warpgroup has from here on.  All of a CTA's together no
-// more than it was launched with.
-constexpr int kConsumerRegisters = 208;
-template <int PW>
-constexpr int kProducerRegisters = PW == 8 ? 48 : 88;
+// more than it was launched with.  Consumers have 216 where 208 are too few (sixteen rows of eight
+// heads of 128 by boxes 2636 cycles a stage for 2784) and the producers can do with 72; eight
+// rows by boxes are slower with them (1845 for 1750).
+template <int NT, int PW, int SLICE>
+constexpr bool kMoreRegisters = PW == 4 && (SLICE == 0 || (NT == 2 && SLICE == 640));
+template <int NT, int PW, int SLICE>
+constexpr int kConsumerRegisters = kMoreRegisters<NT, PW, SLICE> ? 216 : 208;
+template <int NT, int PW, int SLICE>
+constexpr int kProducerRegisters = kMoreRegisters<NT, PW, SLICE> ? 72 : PW == 8 ? 48 : 88;
 template <int N, bool MORE>
 __device__ __forceinline__ void set_registers() {
   if constexpr (MORE) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -424,7 +429,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
 
   if (warp >= NW) {
     // =========================== producers ===========================
-    set_registers<kProducerRegisters<PW>, false>();
+    set_registers<kProducerRegisters<NT, PW, SLICE>, false>();
     behind(seq_lens, block_table, lists);
     const int me = warp - NW, count = s_count, lo = s_lo, hi = lo + count;
     int* s_row = s_row_all[me & 3];
@@ -763,7 +768,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   }
 
   // =========================== consumers ===========================
-  set_registers<kConsumerRegisters, true>();
+  set_registers<kConsumerRegisters<NT, PW, SLICE>, true>();
   if (warp >= consumers) return;
   const int h = warp / WPH, sub = warp - h * WPH;
   const int g = lane >> 2, t = lane & 3;
@@ -790,7 +795,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
   const int m_word = 4 * (g & (NB - 1));
 
   // queries as B operands, in shared memory where registers are short; the pieces of their sums
-  constexpr bool QSHARED = NT * TT == 4;
+  constexpr bool QSHARED = NT * TT == 4, TWICE = FIXED && !QSHARED;
   uint32_t qf[QSHARED ? 1 : NT][NB][4], qs[NT][NB];
   uint4* q_shared = reinterpret_cast<uint4*>(smem + sh.q_at) + warp * NT * NB * 32 + lane;
   // of columns 2t, 2t + 1: scale of the scores, minus the reference, sum of weights
@@ -1223,13 +1228,13 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           }
         exponents();
       }
-      if constexpr (!QSHARED) weights();
+      if constexpr (TWICE) weights();
     } else {
-      // (a second copy: one for both 1860 cycles a stage instead of 1750; where registers are
-      // short two cost more, 2900 for 2780)
-      if constexpr (!QSHARED) weights();
+      // (a second copy: one for both 1860 cycles a stage instead of 1750; with sixteen rows, and
+      // with distances that are not known, two cost more, 2900 for 2780)
+      if constexpr (TWICE) weights();
     }
-    if constexpr (QSHARED) weights();
+    if constexpr (!TWICE) weights();
     ready = __all_sync(0xffffffffu, tc::mbar_test_wait(&bar_full[stage], phase)) != 0;
     // ---------------- values ----------------
     // The products start from zero every time and are added on their own: the tensor
@@ -1627,7 +1632,7 @@ cudaError_t launch_main(const pks_q4_attention_args& a, const Q4Layout& L, const
     // consumers wait for registers that the launch does not have
     cudaFuncAttributes built;
     if ((e = cudaFuncGetAttributes(&built, kern)) != cudaSuccess) return e;
-    if (kConsumers * kConsumerRegisters + PW * kProducerRegisters<PW> >
+    if (kConsumers * kConsumerRegisters<NT, PW, SLICE> + PW * kProducerRegisters<NT, PW, SLICE> >
         (kConsumers + PW) * built.numRegs)
       return cudaErrorInvalidConfiguration;
     e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMax);
