@@ -175,6 +175,17 @@ def test_sizes_that_change_along_a_request(small, large):
     run(b)
 
 
+def test_few_tokens_without_scales_before_many_small_ones():
+    """Lists whose first stage has few tokens, and these no scales."""
+    b = dominated(20000, 0.9, 1e-6, seed=8)
+    b.v[:40] = 1e-6
+    b.write()
+    lists = np.full((1, 1, 19000), -1)
+    lists[0, 0, [3, 40, 77, 100, 130, 170, 200, 230]] = np.arange(5, 13)
+    lists[0, 0, 256:] = np.arange(1000, 1000 + 19000 - 256)
+    run(b, lists=lists)
+
+
 def test_values_without_any_scale():
     """All values of a group alike: s is 0 and everything is in m."""
     b = dominated(5000, 0.9, 1.0, seed=5)

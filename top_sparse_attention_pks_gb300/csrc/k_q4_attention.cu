@@ -1064,6 +1064,7 @@ k_q4_attention(const int32_t* __restrict__ seq_lens, const int32_t* __restrict__
           unusual |= !(y & least) && (y || all == 0xffffu);  // (0: of tokens that are not there)
         }
         rescale = __any_sync(0xffffffffu, unusual) || units != kUsual;
+        if (all != 0xffffu) limit = kAlways;  // (few tokens say little about those to come)
       } else {  // in the units at hand, if nothing is too large for them
         uint32_t f[NB];
         lds(reinterpret_cast<const uint8_t*>(s_by_unit[warp]), f);
